@@ -92,7 +92,7 @@ def _load(p: str) -> ctypes.CDLL:
             raise RuntimeError(f"MoL CUDA library not built ({p} missing): run "
                                "moe_lora_virtual_gb300.build.build_library() first")
         lib = ctypes.CDLL(p)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in (*_SIGS.items(), *BLOCK_SIGS.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -390,3 +390,9 @@ def decode_check_record(first: int, count: int) -> CheckRecord:
     if value >= 1 << 47:
         value -= 1 << 48
     return CheckRecord(count, first >> 48, value)
+
+
+# The MoE block around the LoRA path (include/mol_block.h).
+from .block import (BLOCK_EXPORTS, BLOCK_SIGS, W4, mol_block_norm, mol_moe_down,  # noqa: E402
+                    mol_moe_forward, mol_moe_gate_up, mol_moe_route, mol_w4_linear, w4_pack,
+                    w4_quantize, w4_unpack)

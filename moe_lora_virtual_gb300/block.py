@@ -1,0 +1,317 @@
+"""Binding of the MoE block around the LoRA path (``include/mol_block.h``).
+
+Norms between blocks, the router's choice, the experts for a few tokens and the
+4-bit linear. As in the package itself the functions keep the C names, marshal
+arguments and raise ``MolError`` on a status; outputs that are not passed in are
+allocated. ``w4_pack``, ``w4_quantize`` and ``w4_unpack`` lay 4-bit weights out once,
+with torch operations on the tensors' own device.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Union
+
+import torch
+
+import moe_lora_virtual_gb300 as _mol
+
+BLOCK_EXPORTS = ("mol_block_norm", "mol_moe_route", "mol_moe_gate_up", "mol_moe_down",
+                 "mol_moe_forward", "mol_w4_linear")
+MOL_NORM_MAX_H = 16384
+MOL_ROUTE_MAX_EXPERTS = 1024
+MOL_ROUTE_MAX_TOPK = 32
+MOL_MOE_MAX_TOKENS = 128
+MOL_MOE_MAX_PAIRS = 1024
+MOL_MOE_MAX_EXPERTS = 1024
+MOL_MOE_MAX_WIDTH = 65536
+MOL_W4_MAX_TOKENS = 64
+MOL_F32, MOL_BF16 = 0, 1
+
+_P, _I32, _I64, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+BLOCK_SIGS = {
+    "mol_block_norm": (_I32, [_P, _I64, _P, _I64, _P, _P, _I64, _F32, _P, _F32, _I64, _I32, _P,
+                              _I64, _P, _I64, _P]),
+    "mol_moe_route": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _F32, _P, _P, _P]),
+    "mol_moe_gate_up": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64,
+                               _P, _P]),
+    "mol_moe_down": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
+                            _I64, _P]),
+    "mol_moe_forward": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I32,
+                               _P, _P, _I64, _P]),
+    "mol_w4_linear": (_I32, [_P, _I64, _I64, _I32, _I32, _P, _P, _I32, _P, _I64, _P]),
+}
+
+
+class W4(NamedTuple):
+    """4-bit weight rows: value[..., k] = scales[..., k // group] * (q - 8).
+
+    The byte layout is that of ``include/mol_block.h``; ``w4_pack`` makes it."""
+    qweight: torch.Tensor   # uint8 [..., N, Kp // 2], Kp = in_features rounded up to 256
+    scales: torch.Tensor    # bf16 [..., N, Kp // group]
+    in_features: int
+    group: int
+
+
+Weights = Union[torch.Tensor, W4]
+GROUPS = (32, 64, 128)
+# Input j of a word's eight sits at bit _SHIFTS[j].
+_SHIFTS = (0, 16, 4, 20, 8, 24, 12, 28)
+
+
+def _padded(k: int) -> int:
+    return (k + 255) // 256 * 256
+
+
+def w4_pack(q: torch.Tensor, scales: torch.Tensor, group: int) -> W4:
+    """Packs q (integers 0..15, [..., N, K]) and scales ([..., N, ceil(K / group)])."""
+    if group not in GROUPS:
+        raise ValueError(f"group: expected one of {GROUPS}, got {group}")
+    K = q.shape[-1]
+    groups = -(-K // group)
+    if scales.shape != q.shape[:-1] + (groups,):
+        raise ValueError(f"scales: expected {tuple(q.shape[:-1]) + (groups,)}, "
+                         f"got {tuple(scales.shape)}")
+    if q.numel() and (int(q.min()) < 0 or int(q.max()) > 15):
+        raise ValueError("q: expected integers 0..15")
+    Kp, lead = _padded(K), q.shape[:-1]
+    padded = torch.full((*lead, Kp), 8, dtype=torch.uint8, device=q.device)
+    padded[..., :K] = q
+    # inputs [block, i, t, j] -> words [block, t, i], byte b = inputs at bits 8b and 8b + 4
+    v = padded.view(*lead, Kp // 128, 4, 4, 8).transpose(-3, -2)
+    order = sorted(range(8), key=lambda j: _SHIFTS[j])
+    v = v[..., order]
+    qweight = (v[..., 0::2] | (v[..., 1::2] << 4)).reshape(*lead, Kp // 2).contiguous()
+    s = torch.zeros(*lead, Kp // group, dtype=torch.bfloat16, device=q.device)
+    s[..., :groups] = scales.to(torch.bfloat16)
+    return W4(qweight, s, K, group)
+
+
+def w4_quantize(w: torch.Tensor, group: int = 128) -> W4:
+    """Rounds weight rows [..., N, K] to 4 bits: each group's largest magnitude maps to 7 (or to
+    -8 where a negative value is the largest), its scale is rounded to bf16 first."""
+    if group not in GROUPS:
+        raise ValueError(f"group: expected one of {GROUPS}, got {group}")
+    K = w.shape[-1]
+    groups = -(-K // group)
+    f = torch.zeros(*w.shape[:-1], groups * group, dtype=torch.float32, device=w.device)
+    f[..., :K] = w
+    f = f.view(*w.shape[:-1], groups, group)
+    s = torch.maximum(f.amax(-1) / 7, -f.amin(-1) / 8).to(torch.bfloat16)
+    step = torch.where(s > 0, s, torch.ones_like(s)).to(torch.float32).unsqueeze(-1)
+    q = torch.clamp(torch.round(f / step), -8, 7).add_(8).to(torch.uint8)
+    return w4_pack(q.view(*w.shape[:-1], groups * group)[..., :K], s, group)
+
+
+def w4_unpack(w: W4) -> torch.Tensor:
+    """fp32 weight rows [..., N, K] of packed ones."""
+    lead = w.qweight.shape[:-1]
+    v = torch.stack([w.qweight & 15, w.qweight >> 4], -1).view(*lead, -1, 4, 4, 8)
+    order = sorted(range(8), key=lambda j: _SHIFTS[j])
+    back = [order.index(j) for j in range(8)]
+    v = v[..., back].transpose(-3, -2).reshape(*lead, -1, w.group).to(torch.float32) - 8
+    v = v * w.scales.to(torch.float32).unsqueeze(-1)
+    return v.reshape(*lead, -1)[..., :w.in_features]
+
+
+def _rows(t: torch.Tensor, dtype, name: str) -> int:
+    """Row stride of a 2-D CUDA operand with unit column stride."""
+    if t.dtype != dtype or not t.is_cuda:
+        _mol._need(t, dtype, name)
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name}: expected a 2-D tensor with unit column stride")
+    # a single row (or none) has no stride that matters
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8 * -(-t.shape[1] // 8))
+
+
+def _flat(t: torch.Tensor, dtype, name: str, shape) -> int:
+    if t.dtype != dtype or not t.is_cuda:
+        _mol._need(t, dtype, name)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int):
+    return None if t is None else _flat(t, torch.bfloat16, name, (n,))
+
+
+def _weights(w: Weights, name: str, lead, K: int):
+    """(data, scales, group) of bf16 rows or packed 4-bit rows [*lead, K]."""
+    if isinstance(w, W4):
+        if w.in_features != K:
+            raise ValueError(f"{name}: expected {K} inputs, got {w.in_features}")
+        if w.group not in GROUPS:
+            raise ValueError(f"{name}: group is one of {GROUPS}, got {w.group}")
+        Kp = _padded(K)
+        return (_flat(w.qweight, torch.uint8, name, (*lead, Kp // 2)),
+                _flat(w.scales, torch.bfloat16, name + " scales", (*lead, Kp // w.group)), w.group)
+    return _flat(w, torch.bfloat16, name, (*lead, K)), None, 0
+
+
+def _lead(w: Weights) -> torch.Size:
+    return (w.qweight if isinstance(w, W4) else w).shape[:-1]
+
+
+def _delta(delta: Optional[torch.Tensor], pairs: int, width: int):
+    if delta is None:
+        return None, 0
+    stride = _rows(delta, torch.bfloat16, "delta")
+    if delta.shape != (pairs, width):
+        raise ValueError(f"delta: expected shape {(pairs, width)}, got {tuple(delta.shape)}")
+    return delta.data_ptr(), stride
+
+
+def _out(out: Optional[torch.Tensor], shape, like: torch.Tensor, name: str = "out"):
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device), shape[1]
+    stride = _rows(out, torch.bfloat16, name)
+    if out.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out, stride
+
+
+def _call(name: str, *args) -> None:
+    status = getattr(_mol._lib or _mol.library(), name)(*args)
+    if status != 0:
+        raise _mol.MolError(name, status)
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def mol_block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: Optional[torch.Tensor], *,
+                   post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                   residual_scale: float = 1.0, eps: float = 1e-6,
+                   residual_out: Optional[torch.Tensor] = None,
+                   normed: Optional[torch.Tensor] = None, stream=None):
+    """residual + residual_scale * gate * rms(y; post_weight), and its rms(.; pre_weight).
+
+    y, residual bf16 [T, H]; post_weight, pre_weight bf16 [H] or None; gate bf16 [H], [T, H] or
+    None. Returns (residual_out, normed); normed is None without pre_weight. residual_out may be
+    `residual`, normed may be `y`."""
+    T, H = y.shape
+    ys = _rows(y, torch.bfloat16, "y")
+    rs = _rows(residual, torch.bfloat16, "residual")
+    if residual.shape != y.shape:
+        raise ValueError(f"residual: expected shape {tuple(y.shape)}, got {tuple(residual.shape)}")
+    gp, gs = None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _flat(gate, torch.bfloat16, "gate", (H,))
+        else:
+            gp, gs = gate.data_ptr(), _rows(gate, torch.bfloat16, "gate")
+            if gate.shape != y.shape:
+                raise ValueError(f"gate: expected shape {(H,)} or {tuple(y.shape)}, got "
+                                 f"{tuple(gate.shape)}")
+    post, pre = _vector(post_weight, "post_weight", H), _vector(pre_weight, "pre_weight", H)
+    residual_out, ros = _out(residual_out, y.shape, y, "residual_out")
+    ns = 0
+    if pre is not None:
+        normed, ns = _out(normed, y.shape, y, "normed")
+    elif normed is not None:
+        raise ValueError("normed: needs pre_weight")
+    _call("mol_block_norm", y.data_ptr(), ys, residual.data_ptr(), rs, post, gp, gs, residual_scale,
+          pre, eps, T, H, residual_out.data_ptr(), ros,
+          None if normed is None else normed.data_ptr(), ns, _stream(stream))
+    return residual_out, normed
+
+
+def mol_moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True, scale: float = 1.0,
+                  topk_ids: Optional[torch.Tensor] = None,
+                  topk_weights: Optional[torch.Tensor] = None, stream=None):
+    """(topk_ids int32, topk_weights fp32), [T, topk] each, of router logits fp32 or bf16 [T, E]."""
+    bf16 = logits.dtype == torch.bfloat16
+    stride = _rows(logits, torch.bfloat16 if bf16 else torch.float32, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    _call("mol_moe_route", logits.data_ptr(), MOL_BF16 if bf16 else MOL_F32, stride, T, E, topk,
+          int(renormalize), scale, _flat(topk_ids, torch.int32, "topk_ids", (T, topk)),
+          _flat(topk_weights, torch.float32, "topk_weights", (T, topk)), _stream(stream))
+    return topk_ids, topk_weights
+
+
+def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
+                    act: Optional[torch.Tensor] = None, delta: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """act [T * topk, I] = silu(gate) * up of each pair's expert; rows without one are not written.
+
+    x bf16 [T, H]; topk_ids int32 [T, topk]; w_gate_up bf16 [E, 2I, H] or W4; delta bf16
+    [T * topk, 2I]: rows a LoRA gate_up stage added into zeros."""
+    (T, H), k = x.shape, topk_ids.shape[1]
+    E, I2 = _lead(w_gate_up)
+    wp, sp, group = _weights(w_gate_up, "w_gate_up", (E, I2), H)
+    dp, ds = _delta(delta, T * k, I2)
+    if act is None:
+        act = torch.empty((T * k, I2 // 2), dtype=torch.bfloat16, device=x.device)
+    _call("mol_moe_gate_up", x.data_ptr(), _rows(x, torch.bfloat16, "x"),
+          _flat(topk_ids, torch.int32, "topk_ids", (T, k)), T, k, E, H, I2 // 2, wp, sp, group, dp,
+          ds, _flat(act, torch.bfloat16, "act", (T * k, I2 // 2)), _stream(stream))
+    return act
+
+
+def mol_moe_down(act: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                 w_down: Weights, out: Optional[torch.Tensor] = None,
+                 delta: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [T, H] = sum over a token's pairs of topk_weights * (w_down[e] . act + delta).
+
+    act bf16 [T * topk, I]; w_down bf16 [E, H, I] or W4; delta bf16 [T * topk, H]: rows a LoRA down
+    stage added into zeros."""
+    T, k = topk_ids.shape
+    E, H = _lead(w_down)
+    I = act.shape[1]
+    wp, sp, group = _weights(w_down, "w_down", (E, H), I)
+    dp, ds = _delta(delta, T * k, H)
+    out, os = _out(out, (T, H), act)
+    _call("mol_moe_down", _flat(act, torch.bfloat16, "act", (T * k, I)),
+          _flat(topk_ids, torch.int32, "topk_ids", (T, k)),
+          _flat(topk_weights, torch.float32, "topk_weights", (T, k)), T, k, E, H, I, wp, sp, group,
+          dp, ds, out.data_ptr(), os, _stream(stream))
+    return out
+
+
+def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                    w_gate_up: Weights, w_down: Weights, out: Optional[torch.Tensor] = None,
+                    act: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts of a MoE layer for a few tokens: mol_moe_gate_up, then mol_moe_down.
+
+    x bf16 [T, H]; topk_ids int32 and topk_weights fp32 [T, topk]; weights bf16 [E, 2I, H] and
+    [E, H, I], or both W4 of one group; act: scratch bf16 [T * topk, I]."""
+    (T, H), k = x.shape, topk_ids.shape[1]
+    E, I2 = _lead(w_gate_up)
+    I = I2 // 2
+    gp, gsp, group = _weights(w_gate_up, "w_gate_up", (E, 2 * I), H)
+    wp, wsp, group_down = _weights(w_down, "w_down", (E, H), I)
+    if group != group_down:
+        raise ValueError("w_gate_up, w_down: expected the same type and group")
+    if act is None:
+        act = torch.empty((T * k, I), dtype=torch.bfloat16, device=x.device)
+    out, os = _out(out, (T, H), x)
+    _call("mol_moe_forward", x.data_ptr(), _rows(x, torch.bfloat16, "x"),
+          _flat(topk_ids, torch.int32, "topk_ids", (T, k)),
+          _flat(topk_weights, torch.float32, "topk_weights", (T, k)), T, k, E, H, I, gp, gsp, wp,
+          wsp, group, _flat(act, torch.bfloat16, "act", (T * k, I)), out.data_ptr(), os,
+          _stream(stream))
+    return out
+
+
+def mol_w4_linear(x: torch.Tensor, w: W4, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """out [T, N] = x [T, K] . w^T with 4-bit weight rows [N, K]."""
+    if not isinstance(w, W4):
+        raise TypeError("w: expected W4")
+    T, K = x.shape
+    (N,) = _lead(w)
+    wp, sp, group = _weights(w, "w", (N,), K)
+    out, os = _out(out, (T, N), x)
+    _call("mol_w4_linear", x.data_ptr(), _rows(x, torch.bfloat16, "x"), T, K, N, wp, sp, group,
+          out.data_ptr(), os, _stream(stream))
+    return out

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmol.so")
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libmol_checked.so")
 
 SOURCES = ["mol_abi.cu", "mol_align.cu", "mol_lora.cu", "mol_umma.cu", "mol_stage.cu",
-           "mol_expand_tc.cu"]
+           "mol_expand_tc.cu", "mol_block_abi.cu", "mol_block.cu", "mol_moe.cu"]
 HEADERS = ["mol_device.cuh", "mol_internal.h", "mol_tc.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -31,8 +31,9 @@ def _stale(path: str) -> bool:
     if not os.path.exists(path):
         return True
     t = os.path.getmtime(path)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "mol.h"),
-                                                                 os.path.abspath(__file__)]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
+        os.path.join(INCLUDE, "mol.h"), os.path.join(INCLUDE, "mol_block.h"),
+        os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -16,13 +16,18 @@ std::atomic<int64_t> g_launches{0};
 void mol::count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 namespace {
-
 thread_local int32_t g_last_cuda_error = 0;
+}  // namespace
 
-int32_t cuda_fail(cudaError_t e) {
+int32_t mol::cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int32_t)e;
   return MOL_ERR_CUDA;
 }
+
+namespace {
+
+using mol::cuda_fail;
+using mol::ensure_device;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_block_m(int32_t bm) { return bm == 16 || bm == 32 || bm == 64 || bm == 128; }
@@ -33,9 +38,11 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_state[kMaxDevices] = {};
 std::mutex g_device_mutex;
 
+}  // namespace
+
 // Checks the current device is an sm_103 part and prepares kernel attributes
 // once per device. Returns MOL_OK, MOL_ERR_UNSUPPORTED or MOL_ERR_CUDA.
-int32_t ensure_device() {
+int32_t mol::ensure_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -57,6 +64,8 @@ int32_t ensure_device() {
   }
   return g_device_state[dev].load(std::memory_order_relaxed) == 1 ? MOL_OK : MOL_ERR_UNSUPPORTED;
 }
+
+namespace {
 
 int32_t check_align_args(int64_t numel, int32_t num_vexperts, int32_t block_m) {
   if (numel < 0 || num_vexperts < 1) return MOL_ERR_INVALID_ARG;
@@ -205,10 +214,11 @@ int32_t mol_take_check_record(uint64_t* first, uint64_t* count) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
   // in the path's order: align, item shrink and expands, tcgen05 shrink, fused stage,
-  // tcgen05 expand
-  cudaError_t (*const take[5])(unsigned long long*, unsigned long long*) = {
-      mol::take_align_checks, mol::take_lora_checks, mol::take_tc_checks,
-      mol::take_stage_checks, mol::take_expand_tc_checks};
+  // tcgen05 expand, norm and router, experts and 4-bit linear
+  cudaError_t (*const take[7])(unsigned long long*, unsigned long long*) = {
+      mol::take_align_checks, mol::take_lora_checks,      mol::take_tc_checks,
+      mol::take_stage_checks, mol::take_expand_tc_checks, mol::take_block_checks,
+      mol::take_moe_checks};
   unsigned long long f = 0, n = 0;
   for (auto fn : take) {
     unsigned long long fi = 0, ni = 0;

@@ -9,6 +9,10 @@ namespace mol {
 
 // Kernels this library has enqueued in this process (read by mol_launch_count).
 void count_launch();
+// Records a failed CUDA call for mol_last_cuda_error and returns MOL_ERR_CUDA.
+int32_t cuda_fail(cudaError_t e);
+// MOL_OK once the current device is a prepared sm_103 part (see mol_abi.cu).
+int32_t ensure_device();
 
 // Geometry of the align step for given sizes (host arithmetic).
 struct AlignPlan {
@@ -215,6 +219,58 @@ cudaError_t take_expand_tc_checks(unsigned long long* first, unsigned long long*
 // the tcgen05 expand's producers.
 cudaError_t set_wait_test(unsigned stall, unsigned long long limit_ns);
 cudaError_t set_expand_tc_wait_test(unsigned stall, unsigned long long limit_ns);
+
+// --- the MoE block around the LoRA path (include/mol_block.h) ---
+
+// Norms before and after a block, its gate and the residual add (rows of H bf16
+// elements, 16-byte aligned; post_weight, gate, pre_weight / normed may be NULL).
+struct NormArgs {
+  const void* y;
+  const void* residual;
+  const void* post_weight;
+  const void* gate;
+  const void* pre_weight;
+  void* residual_out;
+  void* normed;
+  int64_t y_stride, residual_stride, gate_stride, residual_out_stride, normed_stride, rows;
+  int H;
+  float residual_scale, eps;
+};
+cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream);
+
+// The router's choice: topk largest logits of each row, softmax weights.
+cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t row_stride, int64_t rows,
+                             int num_experts, int topk, bool renormalize, float scale,
+                             int32_t* ids, float* weights, cudaStream_t stream);
+cudaError_t take_block_checks(unsigned long long* first, unsigned long long* count);
+
+// Weight rows of the experts (or of one linear): bf16 (group 0) or 4-bit with one
+// bf16 scale per `group` inputs, in the layout of include/mol_block.h.
+struct WeightRows {
+  const void* data;
+  const void* scales;
+  int K;
+  int group;
+};
+// Bytes between 4-bit rows: the inputs are padded to a multiple of 256.
+__host__ __device__ constexpr int w4_padded(int K) { return (K + 255) / 256 * 256; }
+
+struct MoeShape {
+  int num_tokens, topk, num_experts, hidden, inter;
+};
+cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_stride,
+                               const int32_t* topk_ids, const WeightRows& w, const void* delta,
+                               int64_t delta_stride, void* act, cudaStream_t stream);
+// chained: the kernel before is launch_moe_gate_up of the same call.
+cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* topk_ids,
+                            const float* topk_weights, const WeightRows& w, const void* delta,
+                            int64_t delta_stride, void* out, int64_t out_stride, bool chained,
+                            cudaStream_t stream);
+cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, int N,
+                             const WeightRows& w, void* out, int64_t out_stride,
+                             cudaStream_t stream);
+cudaError_t prepare_moe_kernels();
+cudaError_t take_moe_checks(unsigned long long* first, unsigned long long* count);
 
 // Largest contraction width accepted by the shrink (it streams K in chunks).
 constexpr int kShrinkMaxK = 1 << 16;
