@@ -143,7 +143,7 @@ int32_t mol_moe_forward(const void* x, int64_t x_row_stride, const int32_t* topk
  *   w    w4 rows [N, Kp / 2 bytes], scales bf16 [N, Kp / group]
  *   out  bf16 rows of N at out + t * out_row_stride (2-byte aligned, any stride >= N)
  * Contract: num_tokens <= MOL_W4_MAX_TOKENS, K % 8 == 0, K <= MOL_MOE_MAX_WIDTH,
- * N >= 1, group in {32, 64, 128}.
+ * 1 <= N <= 2^30, group in {32, 64, 128}.
  */
 int32_t mol_w4_linear(const void* x, int64_t x_row_stride, int64_t num_tokens, int32_t K, int32_t N,
                       const void* w, const void* scales, int32_t group, void* out,

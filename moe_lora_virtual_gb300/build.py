@@ -15,8 +15,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libmol.so")
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libmol_checked.so")
 
 SOURCES = ["mol_abi.cu", "mol_align.cu", "mol_lora.cu", "mol_umma.cu", "mol_stage.cu",
-           "mol_expand_tc.cu", "mol_block_abi.cu", "mol_block.cu", "mol_moe.cu"]
-HEADERS = ["mol_device.cuh", "mol_internal.h", "mol_tc.cuh"]
+           "mol_expand_tc.cu", "mol_block_abi.cu", "mol_block.cu", "mol_moe.cu",
+           "mol_moe_bf16.cu", "mol_moe_w4_32.cu", "mol_moe_w4_64.cu", "mol_moe_w4_128.cu"]
+HEADERS = ["mol_device.cuh", "mol_internal.h", "mol_tc.cuh", "mol_moe.h", "mol_moe.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

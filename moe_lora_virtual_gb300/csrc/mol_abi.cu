@@ -181,13 +181,14 @@ int32_t mol_take_fault_flags(uint32_t* flags) {
   if (st != MOL_OK) return st;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
-  unsigned a = 0, b = 0, c = 0, d = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0;
   e = mol::take_lora_faults(&a);
   if (e == cudaSuccess) e = mol::take_tc_faults(&b);
   if (e == cudaSuccess) e = mol::take_stage_faults(&c);
   if (e == cudaSuccess) e = mol::take_expand_tc_faults(&d);
+  if (e == cudaSuccess) e = mol::take_moe_faults(&f);
   if (e != cudaSuccess) return cuda_fail(e);
-  *flags = a | b | c | d;
+  *flags = a | b | c | d | f;
   return MOL_OK;
 }
 
@@ -197,6 +198,7 @@ int32_t mol_debug_wait_test(uint32_t stall_producer, uint64_t wait_limit_ns) {
   if (st != MOL_OK) return st;
   const unsigned long long lim = wait_limit_ns == 0 ? 1000000000ull : wait_limit_ns;
   cudaError_t e = mol::set_wait_test(stall_producer, lim);
+  if (e == cudaSuccess) e = mol::set_moe_wait_test(stall_producer, lim);
   return e == cudaSuccess ? MOL_OK : cuda_fail(e);
 }
 

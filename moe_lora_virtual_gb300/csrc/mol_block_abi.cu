@@ -177,7 +177,7 @@ int32_t mol_w4_linear(const void* x, int64_t x_row_stride, int64_t num_tokens, i
                       const void* w, const void* scales, int32_t group, void* out,
                       int64_t out_row_stride, void* stream) {
   if (num_tokens < 0 || K < 1 || N < 1 || out_row_stride < N) return MOL_ERR_INVALID_ARG;
-  if (num_tokens > MOL_W4_MAX_TOKENS || K % 8 != 0 || K > MOL_MOE_MAX_WIDTH)
+  if (num_tokens > MOL_W4_MAX_TOKENS || K % 8 != 0 || K > MOL_MOE_MAX_WIDTH || N > 1 << 30)
     return MOL_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MOL_OK;
   if (!out) return MOL_ERR_INVALID_ARG;

@@ -270,6 +270,8 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
                              const WeightRows& w, void* out, int64_t out_stride,
                              cudaStream_t stream);
 cudaError_t prepare_moe_kernels();
+cudaError_t take_moe_faults(unsigned* out);
+cudaError_t set_moe_wait_test(unsigned stall, unsigned long long limit_ns);
 cudaError_t take_moe_checks(unsigned long long* first, unsigned long long* count);
 
 // Largest contraction width accepted by the shrink (it streams K in chunks).

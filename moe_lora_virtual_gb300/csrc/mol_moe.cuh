@@ -1,0 +1,920 @@
+// The experts of a MoE layer for a few tokens and the 4-bit linear (include/mol_block.h): the
+// streaming kernel. One translation unit per weight format instantiates it (mol_moe_*.cu).
+//
+// Mathematics. Both halves of the experts and the linear are products w . x of weight rows with a
+// few activation rows, every weight used by the tokens of its expert only (a few), so the time is
+// that of reading the taken experts' weights once: 2 bytes (or about half a byte) for 2 n
+// operations at n tokens an expert. One streaming loop serves all three:
+//
+// - A block owns tiles of 16 (or 8) whole weight rows. A tile belongs to a team of one to four
+//   consumer warps, which bring it themselves: each team has a small ring of stages of its own (a
+//   tile, or a piece of it along K where rows or tokens are too long for shared memory), and its
+//   first warp asks for the next stage by bulk copy as soon as the team is through with one. Rows of
+//   a tile are neighbours in memory, so a copy is kilobytes long. No team waits for another, and no
+//   single warp issues a block's copies (one warp that did held the stream at 2 to 4 TB/s).
+// - The tokens' rows of an expert come the same way into slots that all teams read, from a warp of
+//   its own, once for all the block's tiles of that expert.
+// - The warps of a team split the tile's inputs; the first adds the others' fp32 sums, in their
+//   order, to its own.
+// - The product is mma.sync m16n8k16: weight rows are the M side, tokens the N side (8 a tile), so
+//   a single token wastes tensor work and no bandwidth. The contraction's order is free as long as
+//   both sides agree: each lane takes 8 neighbouring inputs of its row in one 16-byte shared-memory
+//   read, for two mma steps. Tokens of a tile are independent columns; lanes of columns past the
+//   last token read that token's row again (a broadcast), their products are dropped.
+// - 4-bit words become bf16 pairs with a mask and a subtraction that are exact ((128 + q) - 136);
+//   a group's products are summed in fp32 first and multiplied by its scale after, so nothing is
+//   rounded that fp32 arithmetic would not round.
+// - Work is dealt by weight bytes: the gate_up rows of all taken experts form one list that the
+//   blocks share evenly, whatever the routing; the down rows are dealt to clusters, whose blocks
+//   split the experts. A row tile always goes to the same teams, which add their products into
+//   sums of their own in the order of the experts; the teams' and the blocks' sums are added in a
+//   fixed order at the end, through distributed shared memory. No atomics on results.
+// - Each block groups the (token, slot) pairs by expert itself (at most 1024 of them: match masks,
+//   counts in shared memory, one scan), so the layer is two launches, and the down kernel groups
+//   the pairs and asks for its first weights while the gate_up kernel's last blocks still run.
+#pragma once
+
+#include <type_traits>
+
+#include "mol_block.h"
+#include "mol_device.cuh"
+#include "mol_internal.h"
+#include "mol_moe.h"
+
+namespace mol {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kExpertsPerThread = 4;
+constexpr int kListThreads = MOL_MOE_MAX_EXPERTS / kExpertsPerThread;  // of the block's first warps
+constexpr int kListWarps = kListThreads / 32;
+constexpr int kPairsPerThread = MOL_MOE_MAX_PAIRS / kListThreads;
+constexpr uint32_t kWaitPolls = 1u << 22;
+
+__device__ unsigned int g_moe_fault_flags;
+// Test controls of the bounded waits, set only through mol_debug_wait_test.
+__device__ unsigned int g_moe_test_stall;
+__device__ unsigned long long g_moe_wait_limit_ns = kWaitLimitNs;
+
+// Tokens of one expert: a tile's columns.
+struct Entry {
+  int e, off, n;
+};
+
+// The pairs grouped by expert, in shared memory.
+struct Lists {
+  uint32_t* order;  // [numel] pair | token << 16, by entry
+  float* weight;    // [numel] of the same pairs (down)
+  int2* entry;      // x: expert, y: first pair | pairs << 16
+  int count;        // entries
+  bool repeated;    // some token lists an expert twice
+};
+
+// Groups the pairs by expert, in the order of their index: every block finds the same entries, so
+// blocks that hold different rows of one expert agree on which entry has which pair. Each warp
+// ranks a contiguous run of pairs with match masks and per-warp counts; the counts are then summed
+// over the warps, one thread to four experts. `scratch`: 16 E + 4 numel bytes, free again after.
+MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weights) {
+  __shared__ int scan[kListWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, numel = a.num_tokens * a.topk;
+  const int rounds = (numel + kListThreads - 1) / kListThreads;
+  const int used = (numel + rounds * 32 - 1) / (rounds * 32);  // warps that hold pairs
+  int* ids = reinterpret_cast<int*>(scratch);
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(ids + numel);  // [warp][expert]
+  int mine[kPairsPerThread], pos[kPairsPerThread];
+  const int first = warp * rounds * 32 + lane;
+#pragma unroll
+  for (int j = 0; j < kPairsPerThread; ++j) {
+    const int i = first + j * 32;
+    mine[j] = warp < used && j < rounds && i < numel ? ld_cg_i32(a.ids + i) : -1;
+    if (mine[j] >= a.E) mine[j] = -1;
+  }
+  for (int e = tid; e < (a.E * used + 1) / 2; e += blockDim.x) reinterpret_cast<uint32_t*>(cnt)[e] = 0;
+  __syncthreads();
+  if (warp < used) {
+#pragma unroll
+    for (int j = 0; j < kPairsPerThread; ++j) {
+      if (j >= rounds) break;
+      const int i = first + j * 32;
+      if (i < numel) ids[i] = mine[j];
+      const unsigned same = __match_any_sync(0xffffffffu, mine[j]);
+      const int before = __popc(same & lanemask_lt());
+      if (mine[j] >= 0) pos[j] = cnt[warp * a.E + mine[j]] + before;
+      __syncwarp();
+      if (mine[j] >= 0 && before == 0) cnt[warp * a.E + mine[j]] += (uint16_t)__popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  bool again = false;
+  if (weights) {
+#pragma unroll
+    for (int j = 0; j < kPairsPerThread; ++j) {
+      const int i = first + j * 32;
+      if (mine[j] >= 0)
+        for (int q = i - i % a.topk; q < i; ++q) again |= ids[q] == mine[j];
+    }
+  }
+  // Counts before each warp's pairs, then (count, entries) offsets of the experts in 16 bits each.
+  int c[kExpertsPerThread], sum = 0;
+#pragma unroll
+  for (int j = 0; j < kExpertsPerThread; ++j) {
+    const int e = tid * kExpertsPerThread + j;  // (threads past the lists' have none)
+    c[j] = 0;
+    if (e >= a.E) continue;
+    for (int w = 0; w < used; ++w) {
+      const int n = cnt[w * a.E + e];
+      cnt[w * a.E + e] = (uint16_t)c[j];
+      c[j] += n;
+    }
+    if (c[j] > 0) sum += c[j] | ((c[j] + a.xrows - 1) / a.xrows) << 16;
+  }
+  int at = sum;  // exclusive sums over the first warps' threads
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += n;
+  }
+  if (warp < kListWarps && lane == 31) scan[warp] = at;
+  l.repeated = __syncthreads_or(again);
+  at -= sum;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kListWarps; ++w) {
+    if (w < warp) at += scan[w];
+    total += scan[w];
+  }
+#pragma unroll
+  for (int j = 0; j < kExpertsPerThread; ++j) {
+    const int e = tid * kExpertsPerThread + j;
+    if (c[j] == 0) continue;
+    const int off = at & 0xFFFF;
+    int idx = at >> 16;
+    for (int w = 0; w < used; ++w) cnt[w * a.E + e] += (uint16_t)off;
+    for (int o = 0; o < c[j]; o += a.xrows) {
+      if (MOL_CHECK(idx < numel, MOL_CHECK_SMEM, idx))
+        l.entry[idx] = make_int2(e, (off + o) | (min(a.xrows, c[j] - o) << 16));
+      ++idx;
+    }
+    at = idx << 16 | (off + c[j]);
+  }
+  l.count = total >> 16;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPairsPerThread; ++j) {
+    const int i = first + j * 32;
+    if (mine[j] >= 0) {
+      const int s = cnt[warp * a.E + mine[j]] + pos[j];
+      if (!MOL_CHECK(s < numel, MOL_CHECK_SMEM, s)) continue;
+      l.order[s] = (uint32_t)i | (uint32_t)(i / a.topk) << 16;
+      if (weights) l.weight[s] = a.weights[i];
+    }
+  }
+  __syncthreads();
+}
+
+// A team's place in its work, stage after stage: its tiles, each with all its k steps.
+// gate_up, linear: the block's share [lo, hi) of the list of output rows (row pairs), in which every
+// entry takes `per_entry` tiles; the team has every teams-th tile, from a tile boundary on.
+// down: the block's share [lo, hi) of (entry, k step) units for one row tile; the team has every
+// copies-th unit.
+template <int MODE>
+struct Cursor {
+  int pos, hi, lo;      // first position of the tile in the list (of the share's end), or units
+  int entry, row, ks;   // row: first row of the tile
+  bool valid;
+
+  MOL_DEV void next(const StreamArgs& a) {
+    if (MODE == kDown) {
+      pos += a.sum_copies;
+      ks += a.sum_copies;  // (more copies than one only with one k step)
+      while (ks >= a.ksteps) {
+        ks -= a.ksteps;
+        ++entry;
+      }
+    } else {
+      if (++ks < a.ksteps) return;
+      ks = 0;
+      pos += a.teams * a.tile_rows;
+      row += a.teams * a.tile_rows;
+      while (row >= a.entry_rows) {
+        row -= a.entry_rows;
+        ++entry;
+      }
+    }
+    valid = pos < hi;
+  }
+  // gate_up, linear: the share's rows in the tile: [skip, skip + rows) of its tile_rows
+  MOL_DEV int skip() const { return max(0, lo - pos); }
+  MOL_DEV int rows(const StreamArgs& a) const {
+    return max(0, min(min(a.tile_rows, a.N - row), hi - pos) - skip());
+  }
+};
+
+MOL_DEV uint32_t w4_pair(uint32_t v) {  // two nibbles at bits 0 and 16 -> bf16 pair q - 8, exact
+  const uint32_t b = (v & 0x000F000Fu) | 0x43004300u;  // 128 + q
+  const uint32_t c = 0x43084308u;                      // 136
+  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b),
+                             *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Products of a warp's weight rows with NTC tiles of 8 tokens over its share (every parts-th block)
+// of the stage's `len` inputs. r0, r1: the lane's rows g and g + 8 (TWO: there is a second set); x:
+// its token's row in each tile.
+template <bool TWO, int NTC, int NT>
+MOL_DEV void multiply_bf16(float (&acc)[NT][4], const char* r0, const char* r1,
+                           const char* const (&x)[NT], int len, int t, int part, int parts) {
+  const int full = len >> 5;
+  const int o = t * 16;
+#pragma unroll 4
+  for (int b = part; b < full; b += parts) {
+    const uint4 a0 = lds16(r0 + o + b * 64);
+    const uint4 a1 = TWO ? lds16(r1 + o + b * 64) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt) {
+      const uint4 v = lds16(x[nt] + o + b * 64);
+      mma_16816(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+      mma_16816(acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+    }
+  }
+  if ((len & 31) && (full & (parts - 1)) == part) {  // a partial block: inputs past len are zeros
+    const bool in = t * 8 < (len & 31);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 a0 = in ? lds16(r0 + o + full * 64) : zero;
+    const uint4 a1 = TWO && in ? lds16(r1 + o + full * 64) : zero;
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt) {
+      const uint4 v = in ? lds16(x[nt] + o + full * 64) : zero;
+      mma_16816(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+      mma_16816(acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+    }
+  }
+}
+
+// One block of 128 inputs of 4-bit rows; FULL: all of them below len.
+template <int G, bool TWO, int NTC, int NT, bool FULL>
+MOL_DEV void block_w4(float (&acc)[NT][4], const char* r0, const char* r1, const char* s0,
+                      const char* s1, const char* const (&x)[NT], int b, int len, int t) {
+  const uint4 a0 = lds16(r0 + t * 16 + b * 64);
+  const uint4 a1 = TWO ? lds16(r1 + t * 16 + b * 64) : make_uint4(0, 0, 0, 0);
+  const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
+  float sum[NTC][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i * 32 % G == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NTC; ++nt) sum[nt][0] = sum[nt][1] = sum[nt][2] = sum[nt][3] = 0.f;
+    }
+    uint32_t p0[4], p1[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p0[j] = w4_pair(w0[i] >> (4 * j));
+      p1[j] = TWO ? w4_pair(w1[i] >> (4 * j)) : 0u;
+    }
+    const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt) {
+      const uint4 v = in ? lds16(x[nt] + t * 16 + b * 256 + i * 64) : make_uint4(0, 0, 0, 0);
+      mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v.x, v.y);
+      mma_16816(sum[nt], p0[2], p1[2], p0[3], p1[3], v.z, v.w);
+    }
+    if ((i + 1) * 32 % G == 0) {
+      // a group wholly past len holds no weights: its scale may be anything
+      const int grp = (b * 128 + i * 32) / G;
+      const bool has = FULL || grp * G < len;
+      const float f0 = has ? __bfloat162float(reinterpret_cast<const bf16*>(s0)[grp]) : 0.f;
+      const float f1 = TWO && has ? __bfloat162float(reinterpret_cast<const bf16*>(s1)[grp]) : 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NTC; ++nt) {
+        acc[nt][0] = fmaf(f0, sum[nt][0], acc[nt][0]);
+        acc[nt][1] = fmaf(f0, sum[nt][1], acc[nt][1]);
+        if (TWO) {
+          acc[nt][2] = fmaf(f1, sum[nt][2], acc[nt][2]);
+          acc[nt][3] = fmaf(f1, sum[nt][3], acc[nt][3]);
+        }
+      }
+    }
+  }
+}
+
+template <int G, bool TWO, int NTC, int NT>
+MOL_DEV void multiply_w4(float (&acc)[NT][4], const char* r0, const char* r1, const char* s0,
+                         const char* s1, const char* const (&x)[NT], int len, int t, int part,
+                         int parts) {
+  const int full = len >> 7;
+#pragma unroll 1
+  for (int b = part; b < full; b += parts)
+    block_w4<G, TWO, NTC, NT, true>(acc, r0, r1, s0, s1, x, b, len, t);
+  if ((len & 127) && (full & (parts - 1)) == part)
+    block_w4<G, TWO, NTC, NT, false>(acc, r0, r1, s0, s1, x, full, len, t);
+}
+
+MOL_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MOL_DEV void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+MOL_DEV float remote_f32(uint32_t addr, uint32_t rank) {
+  uint32_t p;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
+
+// Adds column `col` of a tile (value h of rows g and g + 8) times its pair's weight into the sums.
+MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, float* sums, const Entry& en,
+                      const float (&acc)[4], int h, int col, int row, int rows, int g) {
+  if (col >= en.n) return;
+  const int tok = l.order[en.off + col] >> 16;
+  const float w = l.weight[en.off + col];
+  if (!MOL_CHECK(tok < a.num_tokens && row >= 0 && row + rows <= a.acc_stride, MOL_CHECK_SMEM, row))
+    return;
+  float* s = sums + tok * a.acc_stride + row + g;
+  if (g < rows) s[0] = fmaf(w, h ? acc[1] : acc[0], s[0]);
+  if (g + 8 < rows) s[8] = fmaf(w, h ? acc[3] : acc[2], s[8]);
+}
+
+// v + the deltas of token tok's pairs at output column n, in the order of the slots.
+MOL_DEV float add_deltas(const StreamArgs& a, float v, int tok, int n) {
+  for (int k = 0; k < a.topk; ++k) {
+    const int64_t pair = tok * a.topk + k;
+    const int e = a.ids[pair];
+    if (e >= 0 && e < a.E)
+      v = fmaf(a.weights[pair], __bfloat162float(a.delta[pair * a.delta_stride + n]), v);
+  }
+  return v;
+}
+
+// The byte range [at, at + len) of the scales (4-byte aligned) into shared memory at dst + (at &
+// 15): bulk copies move whole 16-byte units, so the range is widened to them; at the end of the
+// tensor the last bytes that a unit would overrun are copied word by word.
+struct ScaleRange {
+  int64_t from, to;  // bulk part, multiples of 16
+  MOL_DEV ScaleRange(int64_t at, int len, int64_t total) {
+    from = at & ~(int64_t)15;
+    to = min((at + len + 15) & ~(int64_t)15, total & ~(int64_t)15);
+    if (to < from) to = from;
+  }
+  MOL_DEV uint32_t bytes() const { return (uint32_t)(to - from); }
+};
+
+template <int G, int MODE, int NT>
+__global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
+    stream_kernel(const __grid_constant__ StreamArgs a) {
+  constexpr bool kW4 = G != 0;
+  constexpr int GG = kW4 ? G : 32;  // (a group for code that bf16 does not reach)
+  extern __shared__ __align__(128) char smem[];
+  // a stage has landed; its other warps are through with it; a token slot has landed, is free
+  __shared__ uint64_t wfull[kMaxStages], pfull[kMaxStages], xfull[kMaxSlots], xempty[kMaxSlots];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int numel = a.num_tokens * a.topk;
+  const int consumers = a.teams * a.parts;
+  const int rows_per_expert = MODE == kGateUp ? 2 * a.N : a.N;
+
+  // shared memory: stages | token slots | output sums (down) | lists
+  char* ring = smem;
+  char* xslots = ring + a.stages * a.stage_bytes;
+  float* sums = reinterpret_cast<float*>(xslots + a.xstages * a.xslot_bytes);
+  Lists lists;
+  lists.entry = reinterpret_cast<int2*>(sums + a.sum_copies * a.num_tokens * a.acc_stride);
+  lists.order = reinterpret_cast<uint32_t*>(lists.entry + (MODE == kLinear ? 0 : numel));
+  lists.weight = reinterpret_cast<float*>(lists.order + numel);
+  lists.count = 1;
+  lists.repeated = false;
+
+  if (warp == kListWarps) {  // (a warp without pairs to rank)
+    for (int s = lane; s < a.stages; s += 32) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&pfull[s], max(1, a.parts - 1));
+    }
+    for (int s = lane; s < a.xstages; s += 32) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], consumers);
+    }
+    fence_mbar_init();
+  }
+  if (!a.chained) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  if (MODE != kLinear) {
+    build_lists(a, lists, ring, MODE == kDown);
+    // the lists' scratch becomes the ring: ordinary accesses before the copies
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  auto entry_of = [&](int i) {
+    if (MODE == kLinear) return Entry{0, 0, a.num_tokens};
+    const int2 v = lists.entry[i];
+    return Entry{v.x, v.y & 0xFFFF, v.y >> 16};
+  };
+
+  // this block's share
+  const int ranks = MODE == kDown ? a.cluster : 1;
+  const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+  int first_row = 0, end_row = 0;  // down: the output rows of this block (of its cluster)
+  int lo, hi;
+  if (MODE == kDown) {
+    const int clusters = gridDim.x / ranks, cl = blockIdx.x / ranks;
+    first_row = (int)((int64_t)a.N * cl / clusters);
+    end_row = (int)((int64_t)a.N * (cl + 1) / clusters);
+    const int units = lists.count * a.ksteps;
+    lo = units * rank / ranks;
+    hi = units * (rank + 1) / ranks;
+    for (int i = tid; i < a.sum_copies * a.num_tokens * a.acc_stride; i += blockDim.x) sums[i] = 0.f;
+  } else {
+    const int64_t all = (int64_t)lists.count * a.entry_rows;
+    lo = (int)(all * blockIdx.x / gridDim.x);
+    hi = (int)(all * (blockIdx.x + 1) / gridDim.x);
+    if (a.ksteps > 1) {  // whole groups of a tile for each team: they share the tokens' pieces
+      const int group = a.teams * a.tile_rows, groups = (int)(all / group);
+      lo = (int)((int64_t)groups * blockIdx.x / gridDim.x) * group;
+      hi = (int)((int64_t)groups * (blockIdx.x + 1) / gridDim.x) * group;
+    }
+  }
+  // Token slots in the order of their use: whole rows: one for each entry of the share; pieces: one
+  // for each k step of each group of tiles (gate_up, linear) or each unit (down).
+  const bool whole = a.ksteps == 1;
+  const int tile0 = lo / a.tile_rows * a.tile_rows;  // gate_up, linear: the first tile's position
+  const int entry0 = MODE == kDown ? lo / a.ksteps : tile0 / a.entry_rows;
+  int slots;
+  if (lo >= hi) slots = 0;
+  else if (MODE == kDown) slots = hi - lo;
+  else if (whole) slots = (hi - 1) / a.entry_rows - entry0 + 1;
+  else slots = (hi - lo) / (a.teams * a.tile_rows) * a.ksteps;
+  if (MODE == kDown && first_row == end_row) slots = 0;
+  __syncthreads();
+  const unsigned long long limit = g_moe_wait_limit_ns;
+  bool fault = false;
+
+  if (warp >= consumers) {
+    // ---- the tokens' rows ----
+    if (a.chained) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
+    if (warp == consumers && !(g_moe_test_stall & 1)) {
+      int entry = entry0, ks = MODE == kDown ? lo - entry0 * a.ksteps : 0;
+      int left = MODE == kDown || whole ? 0 : a.entry_rows - (lo - entry0 * a.entry_rows);
+      int i = 0;
+      for (; i < slots; ++i) {
+        const int s = i % a.xstages, use = i / a.xstages;
+        if (use > 0 && !mbar_wait(&xempty[s], (use - 1) & 1, kWaitPolls, limit)) {
+          fault = true;
+          break;
+        }
+        const Entry en = entry_of(entry);
+        const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
+        if (lane == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)en.n * len * 2);
+        __syncwarp();
+        for (int j = lane; j < en.n; j += 32) {
+          int row = j;
+          if (MODE != kLinear) {
+            const uint32_t p = lists.order[en.off + j];
+            row = MODE == kGateUp ? p >> 16 : p & 0xFFFF;
+          }
+          if (!MOL_CHECK(row < (MODE == kDown ? numel : a.num_tokens), MOL_CHECK_ROW, row)) row = 0;
+          bulk_g2s(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
+                   &xfull[s]);
+        }
+        // the next slot's entry and k step
+        if (++ks == a.ksteps) {
+          ks = 0;
+          if (MODE == kDown || whole) {
+            ++entry;
+          } else {
+            left -= a.teams * a.tile_rows;
+            if (left == 0) {
+              left = a.entry_rows;
+              ++entry;
+            }
+          }
+        }
+      }
+      // no copy may be in flight when the block leaves
+      if (fault)
+        for (int q = max(0, i - a.xstages); q < i; ++q)
+          (void)mbar_wait(&xfull[q % a.xstages], (q / a.xstages) & 1, kWaitPolls, limit);
+    }
+  } else if (slots > 0) {
+    // ---- consumers ----
+    const int g = lane >> 2, t = lane & 3;
+    const int part = warp / a.teams, team = warp - part * a.teams, parts = a.parts;
+    const int depth = a.stages / a.teams;  // stages of the team's ring
+    char* my_ring = ring + team * depth * a.stage_bytes;
+    uint64_t* my_full = wfull + team * depth;
+    uint64_t* my_pfull = pfull + team * depth;
+    Cursor<MODE> cur;
+    cur.hi = hi;
+    cur.lo = lo;
+    int down_rows = 0;  // down: rows of the team's tile
+    if (MODE == kDown) {
+      const int copy = team / a.group, tile = team - copy * a.group;
+      cur.pos = lo + copy;
+      cur.entry = cur.pos / a.ksteps;
+      cur.ks = cur.pos - cur.entry * a.ksteps;
+      cur.row = first_row + tile * a.tile_rows;
+      down_rows = max(0, min(a.tile_rows, end_row - cur.row));
+      cur.valid = cur.pos < hi && down_rows > 0;
+      sums += copy * a.num_tokens * a.acc_stride;
+    } else {
+      cur.pos = tile0 + team * a.tile_rows;
+      cur.entry = cur.pos / a.entry_rows;
+      cur.row = cur.pos - cur.entry * a.entry_rows;
+      cur.ks = 0;
+      cur.valid = cur.pos < hi;
+    }
+    const bool go = !(g_moe_test_stall & 1);
+    const int spitch = kW4 ? w4_padded(a.K) / GG * 2 : 0;
+    const int pitch = kW4 ? w4_padded(a.K) / 2 : a.K * 2;
+    const int64_t stotal = kW4 ? (int64_t)a.E * rows_per_expert * spitch : 0;
+
+    // Asks for the stage at c: the first warp of the team.
+    auto put = [&](const Cursor<MODE>& c, int slot) {
+      char* dst = my_ring + slot * a.stage_bytes;
+      uint64_t* bar = &my_full[slot];
+      const int rows = MODE == kDown ? down_rows : c.rows(a);
+      const int k0 = c.ks * a.Kc, len = min(a.Kc, a.K - k0);
+      const int bytes = kW4 ? (len + 127) / 128 * 64 : len * 2;  // of a row
+      const int copies = a.row_copies ? rows : min(rows, 1);      // of a half
+      const int per = a.row_copies ? 1 : rows;                    // rows of a copy
+      const int total = MODE == kGateUp ? 2 * copies : copies;
+      const uint32_t size = a.row_copies ? bytes : per * pitch;   // contiguous: the rows are whole
+      // lanes take the copies in turn (at most 16 of them); lane 0 announces all their bytes first
+      const int h = lane >= copies;
+      const int r = (h ? lane - copies : lane) * per;
+      const int row = entry_of(c.entry).e * rows_per_expert + c.row +
+                      (MODE == kDown ? 0 : c.skip()) + (h ? a.N : 0) + r;
+      const bool has = lane < total && MOL_CHECK(row + per <= a.E * rows_per_expert,
+                                                 MOL_CHECK_WEIGHT_ROW, row);
+      uint32_t mine = has ? size : 0;
+      int64_t from = 0;
+      uint32_t sbytes = 0;
+      char* sd = dst + a.scale_off + (h * a.half_rows + r) * a.scale_pitch + h * 16;
+      if (kW4 && has) {
+        const int64_t at = (int64_t)row * spitch + k0 / GG * 2;
+        const int slen = a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
+        const ScaleRange sr(at, slen, stotal);
+        from = sr.from;
+        sbytes = sr.bytes();
+        mine += sbytes;
+        // what the bulk copy leaves at the end of the tensor
+        for (int64_t b = max(sr.to, at); b < at + slen; b += 4)
+          *reinterpret_cast<uint32_t*>(sd + (b - sr.from)) =
+              *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b);
+      }
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar, mine);
+      __syncwarp();
+      if (has) {
+        bulk_g2s(dst + (h * a.half_rows + r) * a.row_pitch,
+                 a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size, bar);
+        if (kW4 && sbytes)
+          bulk_g2s(sd, reinterpret_cast<const char*>(a.scales) + from, sbytes, bar);
+      }
+    };
+    Cursor<MODE> ahead = cur;
+    int filled = 0;  // first warp: stages asked for beyond those consumed
+    if (part == 0)
+      for (; go && filled < depth && ahead.valid; ++filled, ahead.next(a)) put(ahead, filled);
+
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    int slot = 0, phase = 0, xi = -1, have = -1;
+    Entry en{0, 0, 0};
+    for (; cur.valid; cur.next(a)) {
+      // the token slot of this stage; those passed over are seen full and released in their order
+      const int want = MODE == kDown ? cur.pos - lo
+                       : whole       ? cur.entry - entry0
+                                     : (cur.pos - lo) / (a.teams * a.tile_rows) * a.ksteps + cur.ks;
+      while (xi < want) {
+        if (xi >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&xempty[xi % a.xstages]);
+        }
+        ++xi;
+        fault = fault || !mbar_wait(&xfull[xi % a.xstages], (xi / a.xstages) & 1, kWaitPolls, limit);
+      }
+      if (cur.entry != have) {
+        have = cur.entry;
+        en = entry_of(have);
+      }
+      fault = fault || !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+      if (fault) break;
+      const int rows = MODE == kDown ? down_rows : cur.rows(a);
+      const int row0 = cur.row + (MODE == kDown ? 0 : cur.skip());  // of the expert
+      const char* st = my_ring + slot * a.stage_bytes;
+      if (rows > 0) {
+        const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
+        // the lane's rows; rows past the tile's last read that row again, their products are dropped
+        int i0, i1;
+        if (MODE == kGateUp) {
+          i0 = min(a.half_rows == 8 ? g : g & 3, rows - 1);
+          i1 = a.half_rows + i0;
+          if (a.half_rows != 8 && g >= 4) i0 = i1;  // 4 gate rows, then 4 up rows
+        } else {
+          i0 = min(g, rows - 1);
+          i1 = min(g + 8, rows - 1);
+        }
+        const char* x[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          x[nt] = xslots + xi % a.xstages * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch;
+        const char *r0 = st + i0 * a.row_pitch, *r1 = st + i1 * a.row_pitch;
+        if constexpr (kW4) {
+          const int first = en.e * rows_per_expert + row0;
+          // the copy that brought a row's scales began at 16 bytes' boundary at or before them, or
+          // before those of its half's first row
+          auto scales_of = [&](int i) {
+            const int h = MODE == kGateUp && i >= a.half_rows;
+            const int row = first + (h ? a.N : 0) + (a.row_copies ? i - h * a.half_rows : 0);
+            return st + a.scale_off + i * a.scale_pitch + h * 16 +
+                   (((uint32_t)row * spitch + k0 / GG * 2) & 15u);
+          };
+          const char *s0 = scales_of(i0), *s1 = scales_of(i1);
+          if (a.stage_rows == 8) {
+            if (NT > 1 && en.n <= 8)
+              multiply_w4<GG, false, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+            else multiply_w4<GG, false, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+          } else {
+            if (NT > 1 && en.n <= 8)
+              multiply_w4<GG, true, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+            else multiply_w4<GG, true, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+          }
+        } else if (a.stage_rows == 8) {
+          if (NT > 1 && en.n <= 8) multiply_bf16<false, 1, NT>(acc, r0, r1, x, len, t, part, parts);
+          else multiply_bf16<false, NT, NT>(acc, r0, r1, x, len, t, part, parts);
+        } else {
+          if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, part, parts);
+          else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, part, parts);
+        }
+      }
+      const bool ends =
+          cur.ks == a.ksteps - 1 || (MODE == kDown && cur.pos + a.sum_copies >= hi);
+      if (parts > 1) {
+        // the others' sums lie in the stage's own buffer until the first warp refills the stage
+        float4* sums_of = reinterpret_cast<float4*>(my_ring + slot * a.stage_bytes + a.parts_off);
+        if (part > 0) {
+          if (ends) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              sums_of[((part - 1) * NT + nt) * 32 + lane] =
+                  make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+              acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&my_pfull[slot]);
+        } else {
+          fault = !mbar_wait(&my_pfull[slot], phase, kWaitPolls, limit);
+          if (fault) break;
+          if (ends) {
+            for (int p = 0; p < parts - 1; ++p) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float4 v = sums_of[(p * NT + nt) * 32 + lane];
+                acc[nt][0] += v.x;
+                acc[nt][1] += v.y;
+                acc[nt][2] += v.z;
+                acc[nt][3] += v.w;
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (part == 0) {  // the team is through with the stage: the next one into its place
+        if (ahead.valid) {
+          put(ahead, slot);
+          ahead.next(a);
+        } else {
+          --filled;
+        }
+      }
+      if (++slot == depth) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if (!ends || part > 0 || rows == 0) continue;
+
+      // the tile's values: column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h)
+      if (MODE == kDown && lists.repeated) {
+        // columns of one step may hold the same token: they take turns
+        for (int turn = 0; turn < 4; ++turn) {
+          if (t == turn) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              add_sums(a, lists, sums, en, acc[nt], 0, nt * 8 + 2 * t, row0 - first_row, rows, g);
+              add_sums(a, lists, sums, en, acc[nt], 1, nt * 8 + 2 * t + 1, row0 - first_row, rows, g);
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = nt * 8 + 2 * t + h;
+            float v0 = acc[nt][h], v1 = acc[nt][2 + h];
+            if (MODE == kGateUp) {
+              if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
+              if (col >= en.n || g >= rows) continue;
+              const int64_t pair = lists.order[en.off + col] & 0xFFFF;
+              const int n = row0 + g;
+              if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
+              if (a.delta) {
+                const bf16* dl = a.delta + pair * a.delta_stride + n;
+                v0 += __bfloat162float(dl[0]);
+                v1 += __bfloat162float(dl[a.N]);
+              }
+              a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
+            } else if (MODE == kDown) {
+              add_sums(a, lists, sums, en, acc[nt], h, col, row0 - first_row, rows, g);
+            } else if (col < en.n) {
+              bf16* o = a.out + col * a.out_stride + row0;
+              if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
+              if (g < rows) o[g] = __float2bfloat16(v0);
+              if (g + 8 < rows) o[g + 8] = __float2bfloat16(v1);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    }
+    // the token slots that are left, for the teams that still need them to be refilled
+    while (!fault && xi < slots) {
+      if (xi >= 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xempty[xi % a.xstages]);
+      }
+      if (++xi < slots)
+        fault = !mbar_wait(&xfull[xi % a.xstages], (xi / a.xstages) & 1, kWaitPolls, limit);
+    }
+    // no copy may be in flight when the block leaves
+    if (fault && part == 0)
+      for (int q = 0; q < filled; ++q) {
+        (void)mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+        if (++slot == depth) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    if (a.chained) pdl_wait();
+  } else if (a.chained) {
+    pdl_wait();
+  }
+  if (fault && lane == 0) atomicOr(&g_moe_fault_flags, kFaultBulkTimeout);
+
+  if (MODE == kDown) {
+    // the ranks' sums in their order, each rank's copies in theirs, the deltas, one rounding
+    __syncthreads();
+    if (ranks > 1) cluster_barrier();
+    sums = reinterpret_cast<float*>(xslots + a.xstages * a.xslot_bytes);
+    const int rows = end_row - first_row, total = rows * a.num_tokens;
+    for (int i = tid + rank * (int)blockDim.x; i < total; i += blockDim.x * ranks) {
+      const int tok = i / rows, row = i - tok * rows;
+      const float* at = sums + tok * a.acc_stride + row;
+      float v = 0.f;
+      for (int q = 0; q < ranks; ++q)
+        for (int c = 0; c < a.sum_copies; ++c) {
+          const float* p = at + c * a.num_tokens * a.acc_stride;
+          v += ranks > 1 ? remote_f32(smem_u32(p), q) : *p;
+        }
+      if (a.delta) v = add_deltas(a, v, tok, first_row + row);
+      if (MOL_CHECK(first_row + row < a.N, MOL_CHECK_COLUMN, first_row + row))
+        a.out[tok * a.out_stride + first_row + row] = __float2bfloat16(v);
+    }
+    if (ranks > 1) cluster_barrier();
+  }
+}
+
+// The launches of one weight format.
+template <int G>
+struct StreamLaunch {
+  template <int MODE, int NT>
+  static cudaError_t one(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((a.consumers + 1) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, stream_kernel<G, MODE, NT>, a);
+  }
+  template <int MODE>
+  static cudaError_t by_tiles(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
+    if (a.xrows <= 8) return one<MODE, 1>(a, grid, smem, stream);
+    if (a.xrows <= 16) return one<MODE, 2>(a, grid, smem, stream);
+    if (a.xrows <= 32) return one<MODE, 4>(a, grid, smem, stream);
+    return one<MODE, 8>(a, grid, smem, stream);
+  }
+  static cudaError_t launch(const StreamArgs& a, int mode, int grid, size_t smem,
+                            cudaStream_t stream) {
+    if (mode == kGateUp) return by_tiles<kGateUp>(a, grid, smem, stream);
+    if constexpr (G != 0) {
+      if (mode == kLinear) return by_tiles<kLinear>(a, grid, smem, stream);
+    }
+    return by_tiles<kDown>(a, grid, smem, stream);
+  }
+  template <int MODE, int NT>
+  static cudaError_t prepare_one() {
+    cudaError_t e = cudaFuncSetAttribute(stream_kernel<G, MODE, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLarge);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(stream_kernel<G, MODE, NT>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    return e;
+  }
+  template <int MODE>
+  static cudaError_t prepare_mode() {
+    cudaError_t e = prepare_one<MODE, 1>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 2>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 4>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 8>();
+    return e;
+  }
+  // clusters: how many clusters of kCluster blocks of `smem` bytes fit the device
+  static cudaError_t prepare(int smem, int* clusters) {
+    cudaError_t e = prepare_mode<kGateUp>();
+    if (e == cudaSuccess) e = prepare_mode<kDown>();
+    if constexpr (G != 0) {
+      if (e == cudaSuccess) e = prepare_mode<kLinear>();
+    }
+    if (e != cudaSuccess || !clusters) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3((kMostConsumers + 1) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(clusters, stream_kernel<G, kDown, 1>, &cfg);
+  }
+  static cudaError_t take_faults(unsigned* out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_moe_fault_flags, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_moe_fault_flags, &zero, sizeof(unsigned));
+  }
+  static cudaError_t wait_test(unsigned stall, unsigned long long limit_ns) {
+    cudaError_t e = cudaMemcpyToSymbol(g_moe_test_stall, &stall, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_moe_wait_limit_ns, &limit_ns, sizeof(unsigned long long));
+  }
+  static cudaError_t take_checks(CheckRecord* r) { return take_check_record_here(r); }
+};
+
+}  // namespace
+
+// What mol_moe.cu calls, one set for each weight format.
+#define MOL_MOE_FORMAT(G)                                                                     \
+  template <>                                                                                 \
+  cudaError_t stream_launch<G>(const StreamArgs& a, int mode, int grid, size_t smem,          \
+                               cudaStream_t stream) {                                         \
+    return StreamLaunch<G>::launch(a, mode, grid, smem, stream);                              \
+  }                                                                                           \
+  template <>                                                                                 \
+  cudaError_t stream_prepare<G>(int smem, int* clusters) {                                    \
+    return StreamLaunch<G>::prepare(smem, clusters);                                          \
+  }                                                                                           \
+  template <>                                                                                 \
+  cudaError_t stream_take_faults<G>(unsigned* out) {                                          \
+    return StreamLaunch<G>::take_faults(out);                                                 \
+  }                                                                                           \
+  template <>                                                                                 \
+  cudaError_t stream_wait_test<G>(unsigned stall, unsigned long long limit_ns) {              \
+    return StreamLaunch<G>::wait_test(stall, limit_ns);                                       \
+  }                                                                                           \
+  template <>                                                                                 \
+  cudaError_t stream_take_checks<G>(unsigned long long* first, unsigned long long* count) {   \
+    CheckRecord r;                                                                            \
+    const cudaError_t e = StreamLaunch<G>::take_checks(&r);                                   \
+    *first = r.first;                                                                         \
+    *count = r.count;                                                                         \
+    return e;                                                                                 \
+  }
+
+}  // namespace mol

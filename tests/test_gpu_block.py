@@ -177,7 +177,9 @@ SHAPES = [
     (17, 16, 4, 1000, 200, "plain"), (23, 128, 8, 256, 48, "plain"), (33, 8, 2, 136, 768, "outside"),
     (64, 6, 3, 520, 104, "hot"), (65, 4, 4, 72, 88, "hot"), (128, 16, 8, 256, 40, "plain"),
     (128, 2, 2, 64, 64, "repeated"), (12, 8, 2, 2048, 32, "none"), (3, 300, 8, 128, 16, "plain"),
-    (1, 1024, 16, 64, 32, "plain"), (31, 24, 32, 64, 16, "plain"), (128, 8, 8, 1288, 8, "hot")]
+    (1, 1024, 16, 64, 32, "plain"), (31, 24, 32, 64, 16, "plain"), (128, 8, 8, 1288, 8, "hot"),
+    (2, 3, 2, 10248, 16, "plain"), (40, 3, 2, 4104, 520, "plain"), (100, 2, 1, 2600, 1032, "plain"),
+    (1, 2, 1, 32, 20000, "plain"), (64, 12, 4, 6152, 40, "dropped")]
 
 
 def run_experts(env, shape, group, delta, seed=0):
@@ -398,3 +400,29 @@ def test_checked_build_records_nothing(env, group):
         rec = mol.mol_take_check_record()
         assert rec.count == 0, f"{rec.count} failed checks, first {rec.site_name} value {rec.value}"
         assert mol.mol_take_fault_flags() == 0
+
+
+# ---------------------------------------------------------------------------------- bounded waits
+@pytest.mark.parametrize("group", [0, 64])
+def test_wait_runs_out_sets_flag_then_device_recovers(env, group):
+    """With the producer warps issuing nothing every wait gives up: the calls return, bit 0 is
+    reported, no activation was written; the same call right after is right, with no bit set."""
+    torch, mol = env
+    g = torch.Generator().manual_seed(11)
+    T, E, k, H, I = 9, 8, 2, 512, 128
+    x, ids = randn(torch, g, T, H).cuda(), make_ids(torch, g, T, E, k, "plain").cuda()
+    weights = torch.rand(T, k, generator=g).cuda()
+    gu, _ = make_weights(torch, mol, g, (E, 2 * I), H, group)
+    dn, _ = make_weights(torch, mol, g, (E, H), I, group)
+    want = mol.mol_moe_forward(x, ids, weights, gu, dn)
+    assert mol.mol_take_fault_flags() == 0
+    act = torch.full((T * k, I), 7.0, dtype=torch.bfloat16, device="cuda")
+    try:
+        mol.mol_debug_wait_test(True, 2_000_000)  # waits give up after 2 ms
+        mol.mol_moe_forward(x, ids, weights, gu, dn, act=act)
+        flags = mol.mol_take_fault_flags()
+    finally:
+        mol.mol_debug_wait_test(False, 0)
+    assert flags == 1 and bool((act == 7.0).all())
+    assert torch.equal(mol.mol_moe_forward(x, ids, weights, gu, dn), want)
+    assert mol.mol_take_fault_flags() == 0
