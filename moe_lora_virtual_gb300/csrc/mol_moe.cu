@@ -25,12 +25,12 @@ cudaError_t launch_by_group(int group, const StreamArgs& a, int mode, int grid, 
   }
 }
 
-// Tokens of an entry: twice the mean of an expert's pairs, so that few experts need a second entry
-// (which reads their weights again), and no more room than the tokens need.
-int entry_rows(int num_tokens, int pairs, int experts) {
-  int n = 4;
+// Tokens of an entry, a power of two: twice the mean of an expert's pairs, so that few experts need
+// a second entry (which reads their weights again), and no more room than the tokens need.
+int entry_tokens(int num_tokens, int pairs, int experts) {
+  int n = num_tokens == 1 ? 1 : num_tokens == 2 ? 2 : 4;
   while (n < 64 && n < num_tokens && n * experts < 2 * pairs) n *= 2;
-  return std::min(n, num_tokens);
+  return n;
 }
 
 // A team's partial sums cost 512 bytes a stage for each further warp and tile of 8 tokens.
@@ -110,7 +110,7 @@ StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const
   a.E = s.num_experts;
   a.K = w.K;
   a.cluster = 1;
-  a.xrows = entry_rows(s.num_tokens, s.num_tokens * s.topk, s.num_experts);
+  a.xrows = entry_tokens(s.num_tokens, s.num_tokens * s.topk, s.num_experts);
   return a;
 }
 
@@ -130,7 +130,7 @@ cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_strid
   a.N = s.inter;
   for (bool small = small_step(s);; small = false) {
     const int room = (small ? kSmemSmall : kSmemLarge) - (int)list_bytes(s);
-    a.consumers = small ? kMostConsumers / 2 : kMostConsumers;
+    a.consumers = small ? kFewConsumers : kMostConsumers;
     if (plan(a, w.group, kGateUp, room, 2)) break;
     if (!small) return cudaErrorInvalidConfiguration;
   }
@@ -155,7 +155,7 @@ cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* t
   const int at_once = split ? g_clusters : g_sm_count;
   for (bool small = small_step(s);; small = false) {
     const int budget = (small ? kSmemSmall : kSmemLarge) - (int)list_bytes(s);
-    a.consumers = small ? kMostConsumers / 2 : kMostConsumers;
+    a.consumers = small ? kFewConsumers : kMostConsumers;
     for (int most = 128; most >= 8; most /= 2) {
       const int waves = (s.hidden + at_once * most - 1) / (at_once * most);
       const int blocks = std::min(at_once * waves, (s.hidden + 7) / 8);

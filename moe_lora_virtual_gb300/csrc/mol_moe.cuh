@@ -57,6 +57,47 @@ __device__ unsigned int g_moe_fault_flags;
 __device__ unsigned int g_moe_test_stall;
 __device__ unsigned long long g_moe_wait_limit_ns = kWaitLimitNs;
 
+// Shared memory by 32-bit address: the loads are then shared loads whatever the compiler can see of
+// the pointers, and addresses take one register. Volatile: they stay behind the waits before them.
+MOL_DEV uint4 ld_s16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
+  return v;
+}
+MOL_DEV uint2 ld_s8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+MOL_DEV uint32_t ld_s4(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+MOL_DEV uint32_t ld_s2(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+MOL_DEV float ld_sf(uint32_t at) { return __uint_as_float(ld_s4(at)); }
+MOL_DEV void st_s4(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+MOL_DEV void st_sf(uint32_t at, float v) { st_s4(at, __float_as_uint(v)); }
+MOL_DEV void st_s16(uint32_t at, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+MOL_DEV void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Tokens of one expert: a tile's columns.
 struct Entry {
   int e, off, n;
@@ -64,31 +105,90 @@ struct Entry {
 
 // The pairs grouped by expert, in shared memory.
 struct Lists {
-  uint32_t* order;  // [numel] pair | token << 16, by entry
-  float* weight;    // [numel] of the same pairs (down)
-  int2* entry;      // x: expert, y: first pair | pairs << 16
+  uint32_t order;   // [numel] pair | token << 16, by entry
+  uint32_t weight;  // [numel] fp32, of the same pairs (down)
+  uint32_t entry;   // pairs of words: expert, first pair | pairs << 16
   int count;        // entries
   bool repeated;    // some token lists an expert twice
+  MOL_DEV Entry get(int i) const {
+    const uint2 v = ld_s8(entry + 8 * i);
+    return Entry{(int)v.x, (int)(v.y & 0xFFFF), (int)(v.y >> 16)};
+  }
+  MOL_DEV uint32_t pair(int i) const { return ld_s4(order + 4 * i); }
 };
 
 // Groups the pairs by expert, in the order of their index: every block finds the same entries, so
-// blocks that hold different rows of one expert agree on which entry has which pair. Each warp
-// ranks a contiguous run of pairs with match masks and per-warp counts; the counts are then summed
-// over the warps, one thread to four experts. `scratch`: 16 E + 4 numel bytes, free again after.
+// blocks that hold different rows of one expert agree on which entry has which pair. An expert with
+// more than xrows pairs (a power of two) takes several entries. `scratch`: 16 E + 4 numel bytes,
+// free again afterwards. The block waits for nothing but its own ids, and the code is kept short: it
+// runs once a launch, from cold instruction caches.
 MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weights) {
   __shared__ int scan[kListWarps];
+  __shared__ int total_shared;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, numel = a.num_tokens * a.topk;
+  const int xlog = 31 - __clz(a.xrows);
+  if (numel <= 32) {
+    // one warp: a lane for each pair, entries in the order of their first pair
+    bool again = false;
+    if (warp == 0) {
+      int e = -1;
+      float w = 0.f;
+      if (lane < numel) {
+        e = ld_cg_i32(a.ids + lane);
+        if (weights) w = a.weights[lane];
+      }
+      if (e >= a.E) e = -1;
+      const int tok = lane / a.topk;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int n = __popc(same), before = __popc(same & lanemask_lt());
+      const bool first = e >= 0 && before == 0;
+      const int chunks = (n + a.xrows - 1) >> xlog;
+      int at = first ? n | chunks << 16 : 0;
+      const int own = at;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      const int total = __shfl_sync(0xffffffffu, at, 31);
+      at -= own;
+      const int off = __shfl_sync(0xffffffffu, at, __ffs(same) - 1) & 0xFFFF;
+      if (e >= 0) {
+        st_s4(l.order + 4 * (off + before), (uint32_t)lane | (uint32_t)tok << 16);
+        if (weights) st_sf(l.weight + 4 * (off + before), w);
+      }
+      if (first)
+        for (int c = 0; c < chunks; ++c) {
+          st_s4(l.entry + 8 * ((at >> 16) + c), e);
+          st_s4(l.entry + 8 * ((at >> 16) + c) + 4,
+                (off + (c << xlog)) | min(a.xrows, n - (c << xlog)) << 16);
+        }
+      // an expert twice at one token: some later lane of the same token and expert
+      if (weights) {
+        const unsigned mates = __match_any_sync(0xffffffffu, e < 0 ? -1 - lane : e << 8 | tok);
+        again = __popc(mates) > 1;
+      }
+      if (lane == 0) total_shared = total >> 16;
+    }
+    l.repeated = __syncthreads_or(again);
+    l.count = total_shared;
+    return;
+  }
+  // Each warp ranks a contiguous run of pairs with match masks and per-warp counts; the counts are
+  // then summed over the warps, one thread to four experts.
   const int rounds = (numel + kListThreads - 1) / kListThreads;
   const int used = (numel + rounds * 32 - 1) / (rounds * 32);  // warps that hold pairs
   int* ids = reinterpret_cast<int*>(scratch);
   uint16_t* cnt = reinterpret_cast<uint16_t*>(ids + numel);  // [warp][expert]
   int mine[kPairsPerThread], pos[kPairsPerThread];
+  float wt[kPairsPerThread];
   const int first = warp * rounds * 32 + lane;
 #pragma unroll
   for (int j = 0; j < kPairsPerThread; ++j) {
     const int i = first + j * 32;
-    mine[j] = warp < used && j < rounds && i < numel ? ld_cg_i32(a.ids + i) : -1;
-    if (mine[j] >= a.E) mine[j] = -1;
+    const bool in = warp < used && j < rounds && i < numel;
+    mine[j] = in ? ld_cg_i32(a.ids + i) : -1;
+    wt[j] = in && weights ? a.weights[i] : 0.f;
   }
   for (int e = tid; e < (a.E * used + 1) / 2; e += blockDim.x) reinterpret_cast<uint32_t*>(cnt)[e] = 0;
   __syncthreads();
@@ -97,6 +197,7 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     for (int j = 0; j < kPairsPerThread; ++j) {
       if (j >= rounds) break;
       const int i = first + j * 32;
+      if (mine[j] >= a.E) mine[j] = -1;
       if (i < numel) ids[i] = mine[j];
       const unsigned same = __match_any_sync(0xffffffffu, mine[j]);
       const int before = __popc(same & lanemask_lt());
@@ -107,15 +208,6 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     }
   }
   __syncthreads();
-  bool again = false;
-  if (weights) {
-#pragma unroll
-    for (int j = 0; j < kPairsPerThread; ++j) {
-      const int i = first + j * 32;
-      if (mine[j] >= 0)
-        for (int q = i - i % a.topk; q < i; ++q) again |= ids[q] == mine[j];
-    }
-  }
   // Counts before each warp's pairs, then (count, entries) offsets of the experts in 16 bits each.
   int c[kExpertsPerThread], sum = 0;
 #pragma unroll
@@ -123,12 +215,13 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     const int e = tid * kExpertsPerThread + j;  // (threads past the lists' have none)
     c[j] = 0;
     if (e >= a.E) continue;
+#pragma unroll 1
     for (int w = 0; w < used; ++w) {
       const int n = cnt[w * a.E + e];
       cnt[w * a.E + e] = (uint16_t)c[j];
       c[j] += n;
     }
-    if (c[j] > 0) sum += c[j] | ((c[j] + a.xrows - 1) / a.xrows) << 16;
+    sum += c[j] | ((c[j] + a.xrows - 1) >> xlog) << 16;
   }
   int at = sum;  // exclusive sums over the first warps' threads
 #pragma unroll
@@ -137,6 +230,16 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     if (lane >= o) at += n;
   }
   if (warp < kListWarps && lane == 31) scan[warp] = at;
+  bool again = false;
+  if (weights) {
+#pragma unroll
+    for (int j = 0; j < kPairsPerThread; ++j) {
+      const int i = first + j * 32;
+      if (mine[j] >= 0)
+#pragma unroll 1
+        for (int q = i - i % a.topk; q < i; ++q) again |= ids[q] == mine[j];
+    }
+  }
   l.repeated = __syncthreads_or(again);
   at -= sum;
   int total = 0;
@@ -151,11 +254,13 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     if (c[j] == 0) continue;
     const int off = at & 0xFFFF;
     int idx = at >> 16;
+#pragma unroll 1
     for (int w = 0; w < used; ++w) cnt[w * a.E + e] += (uint16_t)off;
-    for (int o = 0; o < c[j]; o += a.xrows) {
-      if (MOL_CHECK(idx < numel, MOL_CHECK_SMEM, idx))
-        l.entry[idx] = make_int2(e, (off + o) | (min(a.xrows, c[j] - o) << 16));
-      ++idx;
+#pragma unroll 1
+    for (int o = 0; o < c[j]; o += a.xrows, ++idx) {
+      if (!MOL_CHECK(idx < numel, MOL_CHECK_SMEM, idx)) continue;
+      st_s4(l.entry + 8 * idx, e);
+      st_s4(l.entry + 8 * idx + 4, (off + o) | min(a.xrows, c[j] - o) << 16);
     }
     at = idx << 16 | (off + c[j]);
   }
@@ -167,8 +272,8 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     if (mine[j] >= 0) {
       const int s = cnt[warp * a.E + mine[j]] + pos[j];
       if (!MOL_CHECK(s < numel, MOL_CHECK_SMEM, s)) continue;
-      l.order[s] = (uint32_t)i | (uint32_t)(i / a.topk) << 16;
-      if (weights) l.weight[s] = a.weights[i];
+      st_s4(l.order + 4 * s, (uint32_t)i | (uint32_t)(i / a.topk) << 16);
+      if (weights) st_sf(l.weight + 4 * s, wt[j]);
     }
   }
   __syncthreads();
@@ -222,77 +327,133 @@ MOL_DEV uint32_t w4_pair(uint32_t v) {  // two nibbles at bits 0 and 16 -> bf16 
 
 // Products of a warp's weight rows with NTC tiles of 8 tokens over its share (every parts-th block)
 // of the stage's `len` inputs. r0, r1: the lane's rows g and g + 8 (TWO: there is a second set); x:
-// its token's row in each tile.
+// its token's row in each tile (all at the lane's 16 bytes). mma.sync has 21 cycles of latency and
+// issues every 8 a sub-partition, and a shared load takes 40: blocks are taken U at a time, loads
+// first, and one tile's two steps of a block go to two accumulators.
 template <bool TWO, int NTC, int NT>
-MOL_DEV void multiply_bf16(float (&acc)[NT][4], const char* r0, const char* r1,
-                           const char* const (&x)[NT], int len, int t, int part, int parts) {
+MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const uint32_t (&x)[NT],
+                           int len, int t, int part, int parts) {
+  constexpr int U = NTC == 1 ? 4 : NTC <= 4 ? 2 : 1;
+  constexpr bool kTwo = NTC <= 2;  // (more tiles are independent chains enough)
   const int full = len >> 5;
-  const int o = t * 16;
-#pragma unroll 4
-  for (int b = part; b < full; b += parts) {
-    const uint4 a0 = lds16(r0 + o + b * 64);
-    const uint4 a1 = TWO ? lds16(r1 + o + b * 64) : make_uint4(0, 0, 0, 0);
+  float two[kTwo ? NTC : 1][4];
 #pragma unroll
-    for (int nt = 0; nt < NTC; ++nt) {
-      const uint4 v = lds16(x[nt] + o + b * 64);
-      mma_16816(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-      mma_16816(acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+  for (int nt = 0; nt < (kTwo ? NTC : 1); ++nt) two[nt][0] = two[nt][1] = two[nt][2] = two[nt][3] = 0.f;
+  int b = part;
+  for (; b + (U - 1) * parts < full; b += U * parts) {
+    uint4 a0[U], a1[U], v[U][NTC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t o = (b + u * parts) * 64;
+      a0[u] = ld_s16(r0 + o);
+      a1[u] = TWO ? ld_s16(r1 + o) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int nt = 0; nt < NTC; ++nt) v[u][nt] = ld_s16(x[nt] + o);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int nt = 0; nt < NTC; ++nt)
+        mma_16816(acc[nt], a0[u].x, a1[u].x, a0[u].y, a1[u].y, v[u][nt].x, v[u][nt].y);
+#pragma unroll
+      for (int nt = 0; nt < NTC; ++nt)
+        mma_16816(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0[u].z, a1[u].z, a0[u].w, a1[u].w, v[u][nt].z, v[u][nt].w);
     }
   }
-  if ((len & 31) && (full & (parts - 1)) == part) {  // a partial block: inputs past len are zeros
-    const bool in = t * 8 < (len & 31);
+  // what is left of the share, the last, partial block with it: inputs past len are zeros
+#pragma unroll 1
+  for (; b * 32 < len; b += parts) {
+    const bool in = b * 32 + t * 8 < len;
+    const uint32_t o = b * 64;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a0 = in ? lds16(r0 + o + full * 64) : zero;
-    const uint4 a1 = TWO && in ? lds16(r1 + o + full * 64) : zero;
+    const uint4 a0 = in ? ld_s16(r0 + o) : zero, a1 = TWO && in ? ld_s16(r1 + o) : zero;
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt) {
-      const uint4 v = in ? lds16(x[nt] + o + full * 64) : zero;
+      const uint4 v = in ? ld_s16(x[nt] + o) : zero;
       mma_16816(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-      mma_16816(acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+      mma_16816(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
     }
+  }
+  if (kTwo) {
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] += two[nt][i];
   }
 }
 
-// One block of 128 inputs of 4-bit rows; FULL: all of them below len.
+// The scales of one row for a block of 128 inputs, as fp32.
+template <int G>
+MOL_DEV void load_scales(float (&f)[128 / G], uint32_t at) {
+  if constexpr (G == 128) {
+    f[0] = __uint_as_float(ld_s2(at) << 16);
+  } else if constexpr (G == 64) {
+    const uint32_t v = ld_s4(at);
+    f[0] = bf16_lo(v);
+    f[1] = bf16_hi(v);
+  } else {
+    const uint2 v = ld_s8(at);
+    f[0] = bf16_lo(v.x);
+    f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y);
+    f[3] = bf16_hi(v.y);
+  }
+}
+
+// One block of 128 inputs of 4-bit rows (s0, s1: their scales of this block); FULL: all of them
+// below len.
 template <int G, bool TWO, int NTC, int NT, bool FULL>
-MOL_DEV void block_w4(float (&acc)[NT][4], const char* r0, const char* r1, const char* s0,
-                      const char* s1, const char* const (&x)[NT], int b, int len, int t) {
-  const uint4 a0 = lds16(r0 + t * 16 + b * 64);
-  const uint4 a1 = TWO ? lds16(r1 + t * 16 + b * 64) : make_uint4(0, 0, 0, 0);
+MOL_DEV void block_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
+                      const uint32_t (&x)[NT], int b, int len, int t) {
+  const uint4 a0 = ld_s16(r0 + b * 64);
+  const uint4 a1 = TWO ? ld_s16(r1 + b * 64) : make_uint4(0, 0, 0, 0);
+  float f0[128 / G], f1[128 / G];
+  load_scales<G>(f0, s0 + b * (256 / G));
+  if (TWO) load_scales<G>(f1, s1 + b * (256 / G));
   const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
-  float sum[NTC][4];
+  float sum[NTC][4], two[4];  // (a single tile's two steps: two accumulators)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (i * 32 % G == 0) {
 #pragma unroll
-      for (int nt = 0; nt < NTC; ++nt) sum[nt][0] = sum[nt][1] = sum[nt][2] = sum[nt][3] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        two[j] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NTC; ++nt) sum[nt][j] = 0.f;
+      }
     }
+    const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
+    uint4 v[NTC];
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt)
+      v[nt] = in ? ld_s16(x[nt] + b * 256 + i * 64) : make_uint4(0, 0, 0, 0);
     uint32_t p0[4], p1[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       p0[j] = w4_pair(w0[i] >> (4 * j));
       p1[j] = TWO ? w4_pair(w1[i] >> (4 * j)) : 0u;
     }
-    const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
 #pragma unroll
-    for (int nt = 0; nt < NTC; ++nt) {
-      const uint4 v = in ? lds16(x[nt] + t * 16 + b * 256 + i * 64) : make_uint4(0, 0, 0, 0);
-      mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v.x, v.y);
-      mma_16816(sum[nt], p0[2], p1[2], p0[3], p1[3], v.z, v.w);
-    }
+    for (int nt = 0; nt < NTC; ++nt)
+      mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt)
+      mma_16816(NTC == 1 ? two : sum[nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
     if ((i + 1) * 32 % G == 0) {
       // a group wholly past len holds no weights: its scale may be anything
-      const int grp = (b * 128 + i * 32) / G;
-      const bool has = FULL || grp * G < len;
-      const float f0 = has ? __bfloat162float(reinterpret_cast<const bf16*>(s0)[grp]) : 0.f;
-      const float f1 = TWO && has ? __bfloat162float(reinterpret_cast<const bf16*>(s1)[grp]) : 0.f;
+      const int grp = i * 32 / G;
+      const bool has = FULL || b * 128 + grp * G < len;
+      const float g0 = has ? f0[grp] : 0.f, g1 = TWO && has ? f1[grp] : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt) {
-        acc[nt][0] = fmaf(f0, sum[nt][0], acc[nt][0]);
-        acc[nt][1] = fmaf(f0, sum[nt][1], acc[nt][1]);
+        if (NTC == 1)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[nt][j] += two[j];
+        acc[nt][0] = fmaf(g0, sum[nt][0], acc[nt][0]);
+        acc[nt][1] = fmaf(g0, sum[nt][1], acc[nt][1]);
         if (TWO) {
-          acc[nt][2] = fmaf(f1, sum[nt][2], acc[nt][2]);
-          acc[nt][3] = fmaf(f1, sum[nt][3], acc[nt][3]);
+          acc[nt][2] = fmaf(g1, sum[nt][2], acc[nt][2]);
+          acc[nt][3] = fmaf(g1, sum[nt][3], acc[nt][3]);
         }
       }
     }
@@ -300,9 +461,8 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const char* r0, const char* r1, const
 }
 
 template <int G, bool TWO, int NTC, int NT>
-MOL_DEV void multiply_w4(float (&acc)[NT][4], const char* r0, const char* r1, const char* s0,
-                         const char* s1, const char* const (&x)[NT], int len, int t, int part,
-                         int parts) {
+MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
+                         const uint32_t (&x)[NT], int len, int t, int part, int parts) {
   const int full = len >> 7;
 #pragma unroll 1
   for (int b = part; b < full; b += parts)
@@ -328,16 +488,23 @@ MOL_DEV float remote_f32(uint32_t addr, uint32_t rank) {
 }
 
 // Adds column `col` of a tile (value h of rows g and g + 8) times its pair's weight into the sums.
-MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, float* sums, const Entry& en,
+MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, uint32_t sums, const Entry& en,
                       const float (&acc)[4], int h, int col, int row, int rows, int g) {
   if (col >= en.n) return;
-  const int tok = l.order[en.off + col] >> 16;
-  const float w = l.weight[en.off + col];
+  const int tok = l.pair(en.off + col) >> 16;
+  const float w = ld_sf(l.weight + 4 * (en.off + col));
   if (!MOL_CHECK(tok < a.num_tokens && row >= 0 && row + rows <= a.acc_stride, MOL_CHECK_SMEM, row))
     return;
-  float* s = sums + tok * a.acc_stride + row + g;
-  if (g < rows) s[0] = fmaf(w, h ? acc[1] : acc[0], s[0]);
-  if (g + 8 < rows) s[8] = fmaf(w, h ? acc[3] : acc[2], s[8]);
+  const uint32_t s = sums + 4 * (tok * a.acc_stride + row + g);
+  if (g < rows) st_sf(s, fmaf(w, h ? acc[1] : acc[0], ld_sf(s)));
+  if (g + 8 < rows) st_sf(s + 32, fmaf(w, h ? acc[3] : acc[2], ld_sf(s + 32)));
+}
+
+// The part'th of `parts` nearly equal shares of [0, all).
+MOL_DEV void share(int all, int parts, int part, int& from, int& to) {
+  const int q = all / parts, r = all - q * parts;
+  from = q * part + min(part, r);
+  to = from + q + (part < r);
 }
 
 // v + the deltas of token tok's pairs at output column n, in the order of the slots.
@@ -378,17 +545,18 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
   const int rows_per_expert = MODE == kGateUp ? 2 * a.N : a.N;
 
   // shared memory: stages | token slots | output sums (down) | lists
-  char* ring = smem;
-  char* xslots = ring + a.stages * a.stage_bytes;
-  float* sums = reinterpret_cast<float*>(xslots + a.xstages * a.xslot_bytes);
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t xslots = ring + a.stages * a.stage_bytes;
+  const uint32_t all_sums = xslots + a.xstages * a.xslot_bytes;
+  const uint32_t copy_bytes = a.num_tokens * a.acc_stride * 4;
   Lists lists;
-  lists.entry = reinterpret_cast<int2*>(sums + a.sum_copies * a.num_tokens * a.acc_stride);
-  lists.order = reinterpret_cast<uint32_t*>(lists.entry + (MODE == kLinear ? 0 : numel));
-  lists.weight = reinterpret_cast<float*>(lists.order + numel);
+  lists.entry = all_sums + a.sum_copies * copy_bytes;
+  lists.order = lists.entry + (MODE == kLinear ? 0 : numel * 8);
+  lists.weight = lists.order + numel * 4;
   lists.count = 1;
   lists.repeated = false;
 
-  if (warp == kListWarps) {  // (a warp without pairs to rank)
+  if (warp == (int)(blockDim.x >> 5) - 1) {
     for (int s = lane; s < a.stages; s += 32) {
       mbar_init(&wfull[s], 1);
       mbar_init(&pfull[s], max(1, a.parts - 1));
@@ -404,14 +572,13 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     pdl_launch_dependents();
   }
   if (MODE != kLinear) {
-    build_lists(a, lists, ring, MODE == kDown);
+    build_lists(a, lists, smem, MODE == kDown);
     // the lists' scratch becomes the ring: ordinary accesses before the copies
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   auto entry_of = [&](int i) {
     if (MODE == kLinear) return Entry{0, 0, a.num_tokens};
-    const int2 v = lists.entry[i];
-    return Entry{v.x, v.y & 0xFFFF, v.y >> 16};
+    return lists.get(i);
   };
 
   // this block's share
@@ -420,22 +587,19 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
   int first_row = 0, end_row = 0;  // down: the output rows of this block (of its cluster)
   int lo, hi;
   if (MODE == kDown) {
-    const int clusters = gridDim.x / ranks, cl = blockIdx.x / ranks;
-    first_row = (int)((int64_t)a.N * cl / clusters);
-    end_row = (int)((int64_t)a.N * (cl + 1) / clusters);
+    const int cl = ranks > 1 ? blockIdx.x / kCluster : blockIdx.x;
+    share(a.N, ranks > 1 ? gridDim.x / kCluster : gridDim.x, cl, first_row, end_row);
     const int units = lists.count * a.ksteps;
-    lo = units * rank / ranks;
-    hi = units * (rank + 1) / ranks;
-    for (int i = tid; i < a.sum_copies * a.num_tokens * a.acc_stride; i += blockDim.x) sums[i] = 0.f;
+    lo = ranks > 1 ? units * rank / kCluster : 0;
+    hi = ranks > 1 ? units * (rank + 1) / kCluster : units;
+    for (int i = tid; i < a.sum_copies * (int)copy_bytes / 4; i += blockDim.x)
+      st_s4(all_sums + 4 * i, 0u);
   } else {
-    const int64_t all = (int64_t)lists.count * a.entry_rows;
-    lo = (int)(all * blockIdx.x / gridDim.x);
-    hi = (int)(all * (blockIdx.x + 1) / gridDim.x);
-    if (a.ksteps > 1) {  // whole groups of a tile for each team: they share the tokens' pieces
-      const int group = a.teams * a.tile_rows, groups = (int)(all / group);
-      lo = (int)((int64_t)groups * blockIdx.x / gridDim.x) * group;
-      hi = (int)((int64_t)groups * (blockIdx.x + 1) / gridDim.x) * group;
-    }
+    // whole tiles' pieces: groups of a tile for each team, which share the tokens' pieces
+    const int step = a.ksteps > 1 ? a.teams * a.tile_rows : 1;
+    share(lists.count * (a.entry_rows / step), gridDim.x, blockIdx.x, lo, hi);
+    lo *= step;
+    hi *= step;
   }
   // Token slots in the order of their use: whole rows: one for each entry of the share; pieces: one
   // for each k step of each group of tiles (gate_up, linear) or each unit (down).
@@ -461,9 +625,8 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     if (warp == consumers && !(g_moe_test_stall & 1)) {
       int entry = entry0, ks = MODE == kDown ? lo - entry0 * a.ksteps : 0;
       int left = MODE == kDown || whole ? 0 : a.entry_rows - (lo - entry0 * a.entry_rows);
-      int i = 0;
+      int i = 0, s = 0, use = 0;
       for (; i < slots; ++i) {
-        const int s = i % a.xstages, use = i / a.xstages;
         if (use > 0 && !mbar_wait(&xempty[s], (use - 1) & 1, kWaitPolls, limit)) {
           fault = true;
           break;
@@ -475,14 +638,18 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
         for (int j = lane; j < en.n; j += 32) {
           int row = j;
           if (MODE != kLinear) {
-            const uint32_t p = lists.order[en.off + j];
+            const uint32_t p = lists.pair(en.off + j);
             row = MODE == kGateUp ? p >> 16 : p & 0xFFFF;
           }
           if (!MOL_CHECK(row < (MODE == kDown ? numel : a.num_tokens), MOL_CHECK_ROW, row)) row = 0;
-          bulk_g2s(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
-                   &xfull[s]);
+          bulk_copy(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
+                    &xfull[s]);
         }
-        // the next slot's entry and k step
+        // the next slot, its entry and k step
+        if (++s == a.xstages) {
+          s = 0;
+          ++use;
+        }
         if (++ks == a.ksteps) {
           ks = 0;
           if (MODE == kDown || whole) {
@@ -506,13 +673,14 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     const int g = lane >> 2, t = lane & 3;
     const int part = warp / a.teams, team = warp - part * a.teams, parts = a.parts;
     const int depth = a.stages / a.teams;  // stages of the team's ring
-    char* my_ring = ring + team * depth * a.stage_bytes;
+    const uint32_t my_ring = ring + team * depth * a.stage_bytes;
     uint64_t* my_full = wfull + team * depth;
     uint64_t* my_pfull = pfull + team * depth;
     Cursor<MODE> cur;
     cur.hi = hi;
     cur.lo = lo;
-    int down_rows = 0;  // down: rows of the team's tile
+    int down_rows = 0;  // down: rows of the team's tile, its sums
+    uint32_t sums = 0;
     if (MODE == kDown) {
       const int copy = team / a.group, tile = team - copy * a.group;
       cur.pos = lo + copy;
@@ -521,11 +689,15 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       cur.row = first_row + tile * a.tile_rows;
       down_rows = max(0, min(a.tile_rows, end_row - cur.row));
       cur.valid = cur.pos < hi && down_rows > 0;
-      sums += copy * a.num_tokens * a.acc_stride;
+      sums = all_sums + copy * copy_bytes;
     } else {
       cur.pos = tile0 + team * a.tile_rows;
-      cur.entry = cur.pos / a.entry_rows;
-      cur.row = cur.pos - cur.entry * a.entry_rows;
+      cur.entry = entry0;
+      cur.row = cur.pos - entry0 * a.entry_rows;
+      while (cur.row >= a.entry_rows) {
+        cur.row -= a.entry_rows;
+        ++cur.entry;
+      }
       cur.ks = 0;
       cur.valid = cur.pos < hi;
     }
@@ -536,7 +708,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
 
     // Asks for the stage at c: the first warp of the team.
     auto put = [&](const Cursor<MODE>& c, int slot) {
-      char* dst = my_ring + slot * a.stage_bytes;
+      const uint32_t dst = my_ring + slot * a.stage_bytes;
       uint64_t* bar = &my_full[slot];
       const int rows = MODE == kDown ? down_rows : c.rows(a);
       const int k0 = c.ks * a.Kc, len = min(a.Kc, a.K - k0);
@@ -555,7 +727,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       uint32_t mine = has ? size : 0;
       int64_t from = 0;
       uint32_t sbytes = 0;
-      char* sd = dst + a.scale_off + (h * a.half_rows + r) * a.scale_pitch + h * 16;
+      const uint32_t sd = dst + a.scale_off + (h * a.half_rows + r) * a.scale_pitch + h * 16;
       if (kW4 && has) {
         const int64_t at = (int64_t)row * spitch + k0 / GG * 2;
         const int slen = a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
@@ -565,18 +737,18 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
         mine += sbytes;
         // what the bulk copy leaves at the end of the tensor
         for (int64_t b = max(sr.to, at); b < at + slen; b += 4)
-          *reinterpret_cast<uint32_t*>(sd + (b - sr.from)) =
-              *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b);
+          st_s4(sd + (uint32_t)(b - sr.from),
+                *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b));
       }
       mine = __reduce_add_sync(0xffffffffu, mine);
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(bar, mine);
       __syncwarp();
       if (has) {
-        bulk_g2s(dst + (h * a.half_rows + r) * a.row_pitch,
-                 a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size, bar);
+        bulk_copy(dst + (h * a.half_rows + r) * a.row_pitch,
+                  a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size, bar);
         if (kW4 && sbytes)
-          bulk_g2s(sd, reinterpret_cast<const char*>(a.scales) + from, sbytes, bar);
+          bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + from, sbytes, bar);
       }
     };
     Cursor<MODE> ahead = cur;
@@ -587,21 +759,24 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     float acc[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    int slot = 0, phase = 0, xi = -1, have = -1;
+    int slot = 0, phase = 0, have = -1;
+    int xi = -1, xs = -1, xphase = 0;  // token slots so far, the newest one's place and phase
+    auto next_tokens = [&]() {         // releases the token slot in use and waits for the next
+      if (xi >= 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xempty[xs]);
+      }
+      if (++xs == a.xstages) {
+        xs = 0;
+        xphase ^= 1;
+      }
+      if (++xi < slots) fault = !mbar_wait(&xfull[xs], xphase, kWaitPolls, limit);
+    };
+    int want = MODE == kDown ? cur.pos - lo : 0;  // the token slot of this stage
     Entry en{0, 0, 0};
     for (; cur.valid; cur.next(a)) {
-      // the token slot of this stage; those passed over are seen full and released in their order
-      const int want = MODE == kDown ? cur.pos - lo
-                       : whole       ? cur.entry - entry0
-                                     : (cur.pos - lo) / (a.teams * a.tile_rows) * a.ksteps + cur.ks;
-      while (xi < want) {
-        if (xi >= 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&xempty[xi % a.xstages]);
-        }
-        ++xi;
-        fault = fault || !mbar_wait(&xfull[xi % a.xstages], (xi / a.xstages) & 1, kWaitPolls, limit);
-      }
+      if (MODE != kDown && whole) want = cur.entry - entry0;
+      while (xi < want && !fault) next_tokens();  // (those passed over are released in their order)
       if (cur.entry != have) {
         have = cur.entry;
         en = entry_of(have);
@@ -610,7 +785,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       if (fault) break;
       const int rows = MODE == kDown ? down_rows : cur.rows(a);
       const int row0 = cur.row + (MODE == kDown ? 0 : cur.skip());  // of the expert
-      const char* st = my_ring + slot * a.stage_bytes;
+      const uint32_t st = my_ring + slot * a.stage_bytes;
       if (rows > 0) {
         const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
         // the lane's rows; rows past the tile's last read that row again, their products are dropped
@@ -623,11 +798,11 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           i0 = min(g, rows - 1);
           i1 = min(g + 8, rows - 1);
         }
-        const char* x[NT];
+        uint32_t x[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          x[nt] = xslots + xi % a.xstages * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch;
-        const char *r0 = st + i0 * a.row_pitch, *r1 = st + i1 * a.row_pitch;
+          x[nt] = xslots + xs * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
+        const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
         if constexpr (kW4) {
           const int first = en.e * rows_per_expert + row0;
           // the copy that brought a row's scales began at 16 bytes' boundary at or before them, or
@@ -638,7 +813,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
             return st + a.scale_off + i * a.scale_pitch + h * 16 +
                    (((uint32_t)row * spitch + k0 / GG * 2) & 15u);
           };
-          const char *s0 = scales_of(i0), *s1 = scales_of(i1);
+          const uint32_t s0 = scales_of(i0), s1 = scales_of(i1);
           if (a.stage_rows == 8) {
             if (NT > 1 && en.n <= 8)
               multiply_w4<GG, false, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
@@ -660,13 +835,13 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           cur.ks == a.ksteps - 1 || (MODE == kDown && cur.pos + a.sum_copies >= hi);
       if (parts > 1) {
         // the others' sums lie in the stage's own buffer until the first warp refills the stage
-        float4* sums_of = reinterpret_cast<float4*>(my_ring + slot * a.stage_bytes + a.parts_off);
+        const uint32_t sums_of = st + a.parts_off + lane * 16;
         if (part > 0) {
           if (ends) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              sums_of[((part - 1) * NT + nt) * 32 + lane] =
-                  make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+              st_s16(sums_of + ((part - 1) * NT + nt) * 512, acc[nt][0], acc[nt][1], acc[nt][2],
+                     acc[nt][3]);
               acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
             }
           }
@@ -679,11 +854,11 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
             for (int p = 0; p < parts - 1; ++p) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const float4 v = sums_of[(p * NT + nt) * 32 + lane];
-                acc[nt][0] += v.x;
-                acc[nt][1] += v.y;
-                acc[nt][2] += v.z;
-                acc[nt][3] += v.w;
+                const uint4 v = ld_s16(sums_of + (p * NT + nt) * 512);
+                acc[nt][0] += __uint_as_float(v.x);
+                acc[nt][1] += __uint_as_float(v.y);
+                acc[nt][2] += __uint_as_float(v.z);
+                acc[nt][3] += __uint_as_float(v.w);
               }
             }
           }
@@ -702,6 +877,8 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
         slot = 0;
         phase ^= 1;
       }
+      // (pieces of rows: the team's stages and the token slots go together, one by one)
+      want += MODE == kDown ? a.sum_copies : 1;
       if (!ends || part > 0 || rows == 0) continue;
 
       // the tile's values: column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h)
@@ -727,7 +904,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
             if (MODE == kGateUp) {
               if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
               if (col >= en.n || g >= rows) continue;
-              const int64_t pair = lists.order[en.off + col] & 0xFFFF;
+              const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
               const int n = row0 + g;
               if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
               if (a.delta) {
@@ -751,14 +928,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
     // the token slots that are left, for the teams that still need them to be refilled
-    while (!fault && xi < slots) {
-      if (xi >= 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&xempty[xi % a.xstages]);
-      }
-      if (++xi < slots)
-        fault = !mbar_wait(&xfull[xi % a.xstages], (xi / a.xstages) & 1, kWaitPolls, limit);
-    }
+    while (!fault && xi < slots) next_tokens();
     // no copy may be in flight when the block leaves
     if (fault && part == 0)
       for (int q = 0; q < filled; ++q) {
@@ -778,17 +948,14 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     // the ranks' sums in their order, each rank's copies in theirs, the deltas, one rounding
     __syncthreads();
     if (ranks > 1) cluster_barrier();
-    sums = reinterpret_cast<float*>(xslots + a.xstages * a.xslot_bytes);
     const int rows = end_row - first_row, total = rows * a.num_tokens;
     for (int i = tid + rank * (int)blockDim.x; i < total; i += blockDim.x * ranks) {
       const int tok = i / rows, row = i - tok * rows;
-      const float* at = sums + tok * a.acc_stride + row;
+      const uint32_t at = all_sums + 4 * (tok * a.acc_stride + row);
       float v = 0.f;
       for (int q = 0; q < ranks; ++q)
-        for (int c = 0; c < a.sum_copies; ++c) {
-          const float* p = at + c * a.num_tokens * a.acc_stride;
-          v += ranks > 1 ? remote_f32(smem_u32(p), q) : *p;
-        }
+        for (int c = 0; c < a.sum_copies; ++c)
+          v += ranks > 1 ? remote_f32(at + c * copy_bytes, q) : ld_sf(at + c * copy_bytes);
       if (a.delta) v = add_deltas(a, v, tok, first_row + row);
       if (MOL_CHECK(first_row + row < a.N, MOL_CHECK_COLUMN, first_row + row))
         a.out[tok * a.out_stride + first_row + row] = __float2bfloat16(v);

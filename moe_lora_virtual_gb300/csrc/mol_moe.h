@@ -9,7 +9,9 @@ namespace mol {
 
 enum StreamMode { kGateUp = 0, kDown = 1, kLinear = 2 };
 
-constexpr int kMostConsumers = 16;  // consumer warps of a block
+// Consumer warps of a block: with the tokens' warp sixteen, so a thread may have 128 registers.
+constexpr int kMostConsumers = 15;
+constexpr int kFewConsumers = 7;
 constexpr int kMaxStages = 32;  // of all teams of a block
 constexpr int kMaxSlots = 8;    // token slots
 // Blocks of a cluster that share output rows (down).
