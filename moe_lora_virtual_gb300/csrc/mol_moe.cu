@@ -11,7 +11,7 @@ namespace mol {
 namespace {
 
 int g_sm_count = 0;
-int g_clusters = 0;  // clusters of kCluster large blocks that fit the device
+int g_clusters[kClusterSizes] = {};  // clusters of 1 << i blocks that the device holds at once
 
 constexpr int align_up(int v, int m) { return (v + m - 1) / m * m; }
 
@@ -25,11 +25,12 @@ cudaError_t launch_by_group(int group, const StreamArgs& a, int mode, int grid, 
   }
 }
 
-// Tokens of an entry, a power of two: twice the mean of an expert's pairs, so that few experts need
-// a second entry (which reads their weights again), and no more room than the tokens need.
+// Tokens of an entry, a power of two: half as many again as the mean of an expert's pairs, so that few
+// experts need a second entry (which reads their weights again), and no more room than the tokens
+// need.
 int entry_tokens(int num_tokens, int pairs, int experts) {
   int n = num_tokens == 1 ? 1 : num_tokens == 2 ? 2 : 4;
-  while (n < 64 && n < num_tokens && n * experts < 2 * pairs) n *= 2;
+  while (n < 64 && n < num_tokens && 2 * n * experts < 3 * pairs) n *= 2;
   return n;
 }
 
@@ -37,59 +38,87 @@ int entry_tokens(int num_tokens, int pairs, int experts) {
 int parts_most(int xrows) { return xrows <= 16 ? 4 : 2; }
 int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : xrows <= 32 ? 4 : 8; }
 
-// Chooses the stage and the rings for a block that has `room` bytes for them. xstages_most: token
-// slots of use when they hold whole rows. False when nothing fits.
+// The ring is the lists' scratch first, 20 KB at most: sixteen stages of this size hold it, and rings
+// of fewer are larger.
+constexpr int kLeastStage = 1280;
+
+// Rows of Kc inputs in a stage.
+void row_layout(StreamArgs& a, int group, int rows, int Kc, int copy_rows_from) {
+  const int bytes = group ? align_up(Kc, 256) / 2 : Kc * 2;  // of a row
+  const int scale_bytes = group ? align_up(Kc, 256) / group * 2 : 0;
+  a.Kc = Kc;
+  a.ksteps = (a.K + Kc - 1) / Kc;
+  // a copy for each row: pieces of rows, and rows so long that shorter copies gain nothing (padding
+  // then keeps the lanes' reads off the same banks)
+  a.row_copies = a.ksteps > 1 || bytes >= copy_rows_from;
+  a.row_pitch = a.row_copies ? align_up(bytes, 128) + 64 : bytes;
+  a.scale_pitch = !group ? 0 : a.row_copies ? align_up(scale_bytes, 16) + 16 : scale_bytes;
+  a.scale_off = align_up(rows * a.row_pitch, 16);
+  a.x_pitch = align_up(Kc * 2, 128) + 64;
+}
+
+// gate_up, linear: chooses the stage and the rings for a block that has `room` bytes for them.
+// xstages_most: token slots of use when they hold whole rows. False when nothing fits.
 bool plan(StreamArgs& a, int group, int mode, int room, int xstages_most) {
   auto stage = [&](int rows, int Kc, int xstages) {
-    const int bytes = group ? align_up(Kc, 256) / 2 : Kc * 2;  // of a row
-    const int scale_bytes = group ? align_up(Kc, 256) / group * 2 : 0;
-    a.Kc = Kc;
-    a.ksteps = (a.K + Kc - 1) / Kc;
+    row_layout(a, group, rows, Kc, 4096);
     a.stage_rows = rows;
     a.half_rows = rows / 2;
     a.tile_rows = mode == kGateUp ? rows / 2 : rows;
-    // rows of 4 KB and more by a copy each (shorter copies are slower): padding keeps the lanes'
-    // reads off the same banks
-    a.row_copies = a.ksteps > 1 || bytes >= 4096;
-    a.row_pitch = a.row_copies ? align_up(bytes, 128) + 64 : bytes;
-    a.scale_pitch = !group ? 0 : a.row_copies ? align_up(scale_bytes, 16) + 16 : scale_bytes;
-    a.scale_off = align_up(rows * a.row_pitch, 16);
     a.parts_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
-    a.stage_bytes = a.parts_off + (parts_most(a.xrows) - 1) * 512 * token_tiles(a.xrows);
-    a.x_pitch = align_up(Kc * 2, 128) + 64;
+    a.stage_bytes = std::max(
+        kLeastStage, a.parts_off + (parts_most(a.xrows) - 1) * 512 * token_tiles(a.xrows));
     a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
     a.xstages = xstages;
     a.stages = std::min(kMaxStages, (room - xstages * a.xslot_bytes) / a.stage_bytes);
     return a.stages;
   };
-  // Whole rows. 16 rows a tile use the tensor instruction's M side fully; tiles of 8 leave room for
-  // more stages where rows are long. A second token slot lets the producer go on to the next
-  // expert while the last one's stages are consumed.
-  for (int x = xstages_most; x >= 1; --x) {
-    if (stage(16, a.K, x) >= (x > 2 ? 12 : 6)) return true;
-    if (stage(8, a.K, x) >= (x > 2 ? 12 : 4)) return true;
-  }
-  if (stage(8, a.K, 1) >= 3) return true;
+  // Whole rows. 16 rows a tile use the tensor instruction's M side, and each read of the tokens,
+  // fully; tiles of 8 leave room for more stages where rows are long. A second token slot lets the
+  // next expert's tokens come while the last one's stages are consumed.
+  for (int x = xstages_most; x >= 1; --x)
+    if (stage(16, a.K, x) >= (x > 1 ? 6 : 4)) return true;
+  for (int x = xstages_most; x >= 1; --x)
+    if (stage(8, a.K, x) >= (x > 1 ? 4 : 3)) return true;
   // pieces of rows, the longest that leave four stages
   for (int Kc = 2048; Kc > 256; Kc -= 256)
     if (Kc < a.K && stage(group || Kc <= 1024 ? 16 : 8, Kc, 2) >= 4) return true;
   return stage(8, std::min(256, a.K), 2) >= 2;
 }
 
-void fit_parts(StreamArgs& a) {
-  a.parts = 1;
-  while (2 * a.parts <= parts_most(a.xrows) && 2 * a.parts * a.teams <= a.consumers) a.parts *= 2;
-}
-
-// As many teams as there are stages, or fewer that share them evenly without leaving more unused.
+// gate_up, linear: as many teams as there are stages, or fewer that share them evenly without leaving
+// more unused; the warps that are left join them.
 void fit_teams(StreamArgs& a) {
-  const int most = std::min(a.consumers, a.stages);
+  const int most = std::min(kBlockWarps - 1, a.stages);
   a.teams = most;
   for (int w = most; w > most / 2; --w)
     if (a.stages / w * w > a.stages / a.teams * a.teams) a.teams = w;
   a.stages = a.stages / a.teams * a.teams;
-  fit_parts(a);
+  a.parts = 1;
+  while (2 * a.parts <= parts_most(a.xrows) && 2 * a.parts * a.teams <= kBlockWarps - 1) a.parts *= 2;
   a.entry_rows = align_up(a.N, a.tile_rows * (a.ksteps > 1 ? a.teams : 1));
+}
+
+// down: the stage and the teams of a block of `rows` output rows, with `fixed` bytes of lists and
+// sums besides each team's `copy` of them. False when fewer than two stages fit.
+bool plan_down(StreamArgs& a, int group, int rows, int fixed, int copy) {
+  a.parts = (rows + 15) / 16;
+  auto stage = [&](int Kc) {
+    row_layout(a, group, rows, Kc, 1 << 30);
+    a.x_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
+    a.stage_bytes = std::max(kLeastStage, a.x_off + align_up(a.xrows * a.x_pitch, 128));
+    // as many teams as have a stage each, beside their sums
+    for (a.teams = kBlockWarps / a.parts; a.teams >= 1; --a.teams) {
+      a.stages = std::min(kMaxStages, (kSmem - fixed - a.teams * copy) / a.stage_bytes);
+      if (a.stages >= a.teams) break;
+    }
+    a.stages = a.teams ? a.stages / a.teams * a.teams : 0;
+    return a.stages;
+  };
+  if (stage(a.K) >= 3) return true;
+  for (int Kc = 2048; Kc > 256; Kc -= 256)
+    if (Kc < a.K && stage(Kc) >= 3) return true;
+  return stage(std::min(256, a.K)) >= 2;
 }
 
 StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const int32_t* ids,
@@ -114,12 +143,7 @@ StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const
   return a;
 }
 
-size_t list_bytes(const MoeShape& s) { return (size_t)s.num_tokens * s.topk * 16; }
-
-// A step of a token or two: blocks of half an SM's shared memory and registers, so that the down
-// kernel's blocks are resident, and their first weights on the way, while the gate_up kernel
-// streams. Elsewhere the ring takes the whole SM.
-bool small_step(const MoeShape& s) { return s.num_tokens * s.topk <= 16; }
+int list_bytes(const MoeShape& s) { return s.num_tokens * s.topk * 16; }
 
 }  // namespace
 
@@ -128,12 +152,7 @@ cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_strid
                                int64_t delta_stride, void* act, cudaStream_t stream) {
   StreamArgs a = common_args(s, x, x_stride, topk_ids, w, delta, delta_stride, act, s.inter);
   a.N = s.inter;
-  for (bool small = small_step(s);; small = false) {
-    const int room = (small ? kSmemSmall : kSmemLarge) - (int)list_bytes(s);
-    a.consumers = small ? kFewConsumers : kMostConsumers;
-    if (plan(a, w.group, kGateUp, room, 2)) break;
-    if (!small) return cudaErrorInvalidConfiguration;
-  }
+  if (!plan(a, w.group, kGateUp, kSmem - list_bytes(s), 2)) return cudaErrorInvalidConfiguration;
   fit_teams(a);
   const size_t smem = (size_t)a.stages * a.stage_bytes + a.xstages * a.xslot_bytes + list_bytes(s);
   return launch_by_group(w.group, a, kGateUp, g_sm_count, smem, stream);
@@ -147,39 +166,39 @@ cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* t
   a.weights = topk_weights;
   a.N = s.hidden;
   a.chained = chained;
-  // Rows over clusters (whose blocks read each activation row once instead of four times), or over
-  // blocks when there are too few pairs to split. A block has at most `most` rows, so many rows
-  // take several waves of blocks.
-  const bool split = s.num_tokens * s.topk >= 2 * kCluster;
-  a.cluster = split ? kCluster : 1;
-  const int at_once = split ? g_clusters : g_sm_count;
-  for (bool small = small_step(s);; small = false) {
-    const int budget = (small ? kSmemSmall : kSmemLarge) - (int)list_bytes(s);
-    a.consumers = small ? kFewConsumers : kMostConsumers;
-    for (int most = 128; most >= 8; most /= 2) {
-      const int waves = (s.hidden + at_once * most - 1) / (at_once * most);
-      const int blocks = std::min(at_once * waves, (s.hidden + 7) / 8);
-      const int rows = (s.hidden + blocks - 1) / blocks;
-      a.acc_stride = align_up(rows, 4) + 4;
-      // as many copies of the sums (each for `group` teams of its own) as there are teams
-      const int copy = s.num_tokens * a.acc_stride * 4;
-      for (a.sum_copies = a.consumers; a.sum_copies >= 1; --a.sum_copies) {
-        if (a.sum_copies * copy > (a.sum_copies > 1 ? budget / 4 : budget / 3)) continue;
-        if (!plan(a, w.group, kDown, budget - a.sum_copies * copy, 4)) continue;
-        a.group = (rows + a.tile_rows - 1) / a.tile_rows;
-        a.teams = a.group * a.sum_copies;
-        // (a team keeps its row tile from one k step to the next only if it is the tile's only one)
-        if (a.teams > std::min(a.consumers, a.stages) || (a.ksteps > 1 && a.sum_copies > 1))
-          continue;
-        a.stages = a.stages / a.teams * a.teams;
-        fit_parts(a);
-        const size_t smem = (size_t)a.stages * a.stage_bytes + a.xstages * a.xslot_bytes +
-                            (size_t)a.sum_copies * copy + list_bytes(s);
-        return launch_by_group(w.group, a, kDown, blocks * a.cluster, smem, stream);
-      }
+  // Blocks alone or clusters that split the experts: the fewer rows a block has, the more often each
+  // activation row is read. Taken is what brings the fewest bytes into one block, a cluster's
+  // exchange counted as the 64 KB that arrive meanwhile. Many rows take several waves of blocks.
+  const int pairs = s.num_tokens * s.topk, units = std::min(pairs, s.num_experts);
+  const int64_t x_bytes = (int64_t)s.inter * 2 * ((pairs + units - 1) / units);
+  const int64_t row_bytes = w.group ? w4_padded(s.inter) / 2 : s.inter * 2;
+  int64_t least = INT64_MAX;
+  int blocks = 0;
+  for (int i = 0; i < kClusterSizes; ++i) {
+    if (g_clusters[i] < 1) continue;
+    const int waves = (s.hidden + g_clusters[i] * kDownRows - 1) / (g_clusters[i] * kDownRows);
+    const int n = std::min(g_clusters[i] * waves, (s.hidden + 7) / 8);
+    const int rows = (s.hidden + n - 1) / n;
+    const int64_t bytes = waves * (((units + (1 << i) - 1) >> i) * (rows * row_bytes + x_bytes)) +
+                          (i > 0 ? 65536 : 0);
+    if (bytes < least) {
+      least = bytes;
+      a.cluster = 1 << i;
+      blocks = n;
     }
-    if (!small) return cudaErrorInvalidConfiguration;
   }
+  // fewer rows a block where the sums or a stage of so many do not fit
+  for (; blocks < s.hidden; blocks *= 2) {
+    const int n = std::min(blocks, s.hidden), rows = (s.hidden + n - 1) / n;
+    a.acc_stride = align_up(rows, 4) + 4;
+    const int copy = s.num_tokens * a.acc_stride * 4;
+    const int fixed =
+        list_bytes(s) + (a.cluster > 1 ? align_up(s.num_tokens, a.cluster) * a.acc_stride * 4 : 0);
+    if (fixed + copy > kSmem / 2 || !plan_down(a, w.group, rows, fixed, copy)) continue;
+    const size_t smem = (size_t)a.stages * a.stage_bytes + a.teams * copy + fixed;
+    return launch_by_group(w.group, a, kDown, n * a.cluster, smem, stream);
+  }
+  return cudaErrorInvalidConfiguration;
 }
 
 cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, int N,
@@ -189,8 +208,7 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   StreamArgs a = common_args(s, x, x_stride, nullptr, w, nullptr, 0, out, out_stride);
   a.N = N;
   a.xrows = num_tokens;
-  a.consumers = kMostConsumers;
-  if (!plan(a, w.group, kLinear, kSmemLarge, 1)) return cudaErrorInvalidConfiguration;
+  if (!plan(a, w.group, kLinear, kSmem, 1)) return cudaErrorInvalidConfiguration;
   fit_teams(a);
   const size_t smem = (size_t)a.stages * a.stage_bytes + a.xstages * a.xslot_bytes;
   return launch_by_group(w.group, a, kLinear, std::min((N + 7) / 8, g_sm_count), smem, stream);
@@ -200,11 +218,11 @@ cudaError_t prepare_moe_kernels() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&g_sm_count, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = stream_prepare<0>(kSmemLarge, &g_clusters);
-  if (e == cudaSuccess) e = stream_prepare<32>(0, nullptr);
-  if (e == cudaSuccess) e = stream_prepare<64>(0, nullptr);
-  if (e == cudaSuccess) e = stream_prepare<128>(0, nullptr);
-  if (e == cudaSuccess && g_clusters < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) e = stream_prepare<0>(g_clusters);
+  if (e == cudaSuccess) e = stream_prepare<32>(nullptr);
+  if (e == cudaSuccess) e = stream_prepare<64>(nullptr);
+  if (e == cudaSuccess) e = stream_prepare<128>(nullptr);
+  if (e == cudaSuccess && g_clusters[0] < 1) e = cudaErrorInvalidConfiguration;
   return e;
 }
 

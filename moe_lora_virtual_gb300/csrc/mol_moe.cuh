@@ -12,10 +12,11 @@
 //   first warp asks for the next stage by bulk copy as soon as the team is through with one. Rows of
 //   a tile are neighbours in memory, so a copy is kilobytes long. No team waits for another, and no
 //   single warp issues a block's copies (one warp that did held the stream at 2 to 4 TB/s).
-// - The tokens' rows of an expert come the same way into slots that all teams read, from a warp of
-//   its own, once for all the block's tiles of that expert.
-// - The warps of a team split the tile's inputs; the first adds the others' fp32 sums, in their
-//   order, to its own.
+// - The tokens' rows of an expert come the same way: gate_up and linear: into slots that all teams
+//   read, from a warp of its own, once for all the block's tiles of that expert; down: with the
+//   weights, into the stage.
+// - The warps of a team split the tile: its inputs (gate_up, linear; the first adds the others' fp32
+//   sums, in their order, to its own) or its rows (down).
 // - The product is mma.sync m16n8k16: weight rows are the M side, tokens the N side (8 a tile), so
 //   a single token wastes tensor work and no bandwidth. The contraction's order is free as long as
 //   both sides agree: each lane takes 8 neighbouring inputs of its row in one 16-byte shared-memory
@@ -25,10 +26,10 @@
 //   a group's products are summed in fp32 first and multiplied by its scale after, so nothing is
 //   rounded that fp32 arithmetic would not round.
 // - Work is dealt by weight bytes: the gate_up rows of all taken experts form one list that the
-//   blocks share evenly, whatever the routing; the down rows are dealt to clusters, whose blocks
-//   split the experts. A row tile always goes to the same teams, which add their products into
-//   sums of their own in the order of the experts; the teams' and the blocks' sums are added in a
-//   fixed order at the end, through distributed shared memory. No atomics on results.
+//   blocks share evenly, whatever the routing; the down rows are dealt to blocks or clusters, whose
+//   blocks split the experts. A team adds its products into sums of its own in the order of the
+//   experts; the teams' and the blocks' sums are added in a fixed order at the end, through
+//   distributed shared memory. No atomics on results.
 // - Each block groups the (token, slot) pairs by expert itself (at most 1024 of them: match masks,
 //   counts in shared memory, one scan), so the layer is two launches, and the down kernel groups
 //   the pairs and asks for its first weights while the gate_up kernel's last blocks still run.
@@ -279,38 +280,26 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
   __syncthreads();
 }
 
-// A team's place in its work, stage after stage: its tiles, each with all its k steps.
-// gate_up, linear: the block's share [lo, hi) of the list of output rows (row pairs), in which every
-// entry takes `per_entry` tiles; the team has every teams-th tile, from a tile boundary on.
-// down: the block's share [lo, hi) of (entry, k step) units for one row tile; the team has every
-// copies-th unit.
-template <int MODE>
+// A team's place in its work, stage after stage: its tiles, each with all its k steps. The block's
+// share [lo, hi) of the list of output rows (row pairs), in which every entry takes whole tiles; the
+// team has every teams-th tile.
 struct Cursor {
-  int pos, hi, lo;      // first position of the tile in the list (of the share's end), or units
-  int entry, row, ks;   // row: first row of the tile
+  int pos, hi, lo;     // first position of the tile in the list, of the share's end and start
+  int entry, row, ks;  // row: first row of the tile
   bool valid;
 
   MOL_DEV void next(const StreamArgs& a) {
-    if (MODE == kDown) {
-      pos += a.sum_copies;
-      ks += a.sum_copies;  // (more copies than one only with one k step)
-      while (ks >= a.ksteps) {
-        ks -= a.ksteps;
-        ++entry;
-      }
-    } else {
-      if (++ks < a.ksteps) return;
-      ks = 0;
-      pos += a.teams * a.tile_rows;
-      row += a.teams * a.tile_rows;
-      while (row >= a.entry_rows) {
-        row -= a.entry_rows;
-        ++entry;
-      }
+    if (++ks < a.ksteps) return;
+    ks = 0;
+    pos += a.teams * a.tile_rows;
+    row += a.teams * a.tile_rows;
+    while (row >= a.entry_rows) {
+      row -= a.entry_rows;
+      ++entry;
     }
     valid = pos < hi;
   }
-  // gate_up, linear: the share's rows in the tile: [skip, skip + rows) of its tile_rows
+  // the share's rows in the tile: [skip, skip + rows) of its tile_rows
   MOL_DEV int skip() const { return max(0, lo - pos); }
   MOL_DEV int rows(const StreamArgs& a) const {
     return max(0, min(min(a.tile_rows, a.N - row), hi - pos) - skip());
@@ -476,15 +465,13 @@ MOL_DEV uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-MOL_DEV void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-MOL_DEV float remote_f32(uint32_t addr, uint32_t rank) {
+MOL_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+MOL_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// A float into the same shared-memory address of another block of the cluster.
+MOL_DEV void remote_store(uint32_t at, uint32_t rank, float v) {
   uint32_t p;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
-  return v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p), "f"(v) : "memory");
 }
 
 // Adds column `col` of a tile (value h of rows g and g + 8) times its pair's weight into the sums.
@@ -532,7 +519,7 @@ struct ScaleRange {
 };
 
 template <int G, int MODE, int NT>
-__global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
+__global__ void __launch_bounds__(kBlockWarps * 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs a) {
   constexpr bool kW4 = G != 0;
   constexpr int GG = kW4 ? G : 32;  // (a group for code that bf16 does not reach)
@@ -544,15 +531,13 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
   const int consumers = a.teams * a.parts;
   const int rows_per_expert = MODE == kGateUp ? 2 * a.N : a.N;
 
-  // shared memory: stages | token slots | output sums (down) | lists
+  // shared memory: stages | token slots | lists
   const uint32_t ring = smem_u32(smem);
   const uint32_t xslots = ring + a.stages * a.stage_bytes;
-  const uint32_t all_sums = xslots + a.xstages * a.xslot_bytes;
-  const uint32_t copy_bytes = a.num_tokens * a.acc_stride * 4;
   Lists lists;
-  lists.entry = all_sums + a.sum_copies * copy_bytes;
+  lists.entry = xslots + a.xstages * a.xslot_bytes;
   lists.order = lists.entry + (MODE == kLinear ? 0 : numel * 8);
-  lists.weight = lists.order + numel * 4;
+  lists.weight = 0;
   lists.count = 1;
   lists.repeated = false;
 
@@ -567,12 +552,10 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     }
     fence_mbar_init();
   }
-  if (!a.chained) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   if (MODE != kLinear) {
-    build_lists(a, lists, smem, MODE == kDown);
+    build_lists(a, lists, smem, false);
     // the lists' scratch becomes the ring: ordinary accesses before the copies
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -582,49 +565,29 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
   };
 
   // this block's share
-  const int ranks = MODE == kDown ? a.cluster : 1;
-  const int rank = ranks > 1 ? (int)cluster_rank() : 0;
-  int first_row = 0, end_row = 0;  // down: the output rows of this block (of its cluster)
+  // whole tiles' pieces: groups of a tile for each team, which share the tokens' pieces
+  const int step = a.ksteps > 1 ? a.teams * a.tile_rows : 1;
   int lo, hi;
-  if (MODE == kDown) {
-    const int cl = ranks > 1 ? blockIdx.x / kCluster : blockIdx.x;
-    share(a.N, ranks > 1 ? gridDim.x / kCluster : gridDim.x, cl, first_row, end_row);
-    const int units = lists.count * a.ksteps;
-    lo = ranks > 1 ? units * rank / kCluster : 0;
-    hi = ranks > 1 ? units * (rank + 1) / kCluster : units;
-    for (int i = tid; i < a.sum_copies * (int)copy_bytes / 4; i += blockDim.x)
-      st_s4(all_sums + 4 * i, 0u);
-  } else {
-    // whole tiles' pieces: groups of a tile for each team, which share the tokens' pieces
-    const int step = a.ksteps > 1 ? a.teams * a.tile_rows : 1;
-    share(lists.count * (a.entry_rows / step), gridDim.x, blockIdx.x, lo, hi);
-    lo *= step;
-    hi *= step;
-  }
+  share(lists.count * (a.entry_rows / step), gridDim.x, blockIdx.x, lo, hi);
+  lo *= step;
+  hi *= step;
   // Token slots in the order of their use: whole rows: one for each entry of the share; pieces: one
-  // for each k step of each group of tiles (gate_up, linear) or each unit (down).
+  // for each k step of each group of tiles.
   const bool whole = a.ksteps == 1;
-  const int tile0 = lo / a.tile_rows * a.tile_rows;  // gate_up, linear: the first tile's position
-  const int entry0 = MODE == kDown ? lo / a.ksteps : tile0 / a.entry_rows;
-  int slots;
-  if (lo >= hi) slots = 0;
-  else if (MODE == kDown) slots = hi - lo;
-  else if (whole) slots = (hi - 1) / a.entry_rows - entry0 + 1;
-  else slots = (hi - lo) / (a.teams * a.tile_rows) * a.ksteps;
-  if (MODE == kDown && first_row == end_row) slots = 0;
+  const int tile0 = lo / a.tile_rows * a.tile_rows;  // the first tile's position
+  const int entry0 = tile0 / a.entry_rows;
+  const int slots = lo >= hi ? 0
+                    : whole  ? (hi - 1) / a.entry_rows - entry0 + 1
+                             : (hi - lo) / (a.teams * a.tile_rows) * a.ksteps;
   __syncthreads();
   const unsigned long long limit = g_moe_wait_limit_ns;
   bool fault = false;
 
   if (warp >= consumers) {
     // ---- the tokens' rows ----
-    if (a.chained) {
-      pdl_wait();
-      pdl_launch_dependents();
-    }
     if (warp == consumers && !(g_moe_test_stall & 1)) {
-      int entry = entry0, ks = MODE == kDown ? lo - entry0 * a.ksteps : 0;
-      int left = MODE == kDown || whole ? 0 : a.entry_rows - (lo - entry0 * a.entry_rows);
+      int entry = entry0, ks = 0;
+      int left = a.entry_rows - (lo - entry0 * a.entry_rows);  // pieces: rows of the entry to come
       int i = 0, s = 0, use = 0;
       for (; i < slots; ++i) {
         if (use > 0 && !mbar_wait(&xempty[s], (use - 1) & 1, kWaitPolls, limit)) {
@@ -639,9 +602,9 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           int row = j;
           if (MODE != kLinear) {
             const uint32_t p = lists.pair(en.off + j);
-            row = MODE == kGateUp ? p >> 16 : p & 0xFFFF;
+            row = p >> 16;
           }
-          if (!MOL_CHECK(row < (MODE == kDown ? numel : a.num_tokens), MOL_CHECK_ROW, row)) row = 0;
+          if (!MOL_CHECK(row < a.num_tokens, MOL_CHECK_ROW, row)) row = 0;
           bulk_copy(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
                     &xfull[s]);
         }
@@ -652,14 +615,10 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
         }
         if (++ks == a.ksteps) {
           ks = 0;
-          if (MODE == kDown || whole) {
+          if (!whole) left -= a.teams * a.tile_rows;
+          if (whole || left == 0) {
+            left = a.entry_rows;
             ++entry;
-          } else {
-            left -= a.teams * a.tile_rows;
-            if (left == 0) {
-              left = a.entry_rows;
-              ++entry;
-            }
           }
         }
       }
@@ -676,41 +635,28 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
     const uint32_t my_ring = ring + team * depth * a.stage_bytes;
     uint64_t* my_full = wfull + team * depth;
     uint64_t* my_pfull = pfull + team * depth;
-    Cursor<MODE> cur;
+    Cursor cur;
     cur.hi = hi;
     cur.lo = lo;
-    int down_rows = 0;  // down: rows of the team's tile, its sums
-    uint32_t sums = 0;
-    if (MODE == kDown) {
-      const int copy = team / a.group, tile = team - copy * a.group;
-      cur.pos = lo + copy;
-      cur.entry = cur.pos / a.ksteps;
-      cur.ks = cur.pos - cur.entry * a.ksteps;
-      cur.row = first_row + tile * a.tile_rows;
-      down_rows = max(0, min(a.tile_rows, end_row - cur.row));
-      cur.valid = cur.pos < hi && down_rows > 0;
-      sums = all_sums + copy * copy_bytes;
-    } else {
-      cur.pos = tile0 + team * a.tile_rows;
-      cur.entry = entry0;
-      cur.row = cur.pos - entry0 * a.entry_rows;
-      while (cur.row >= a.entry_rows) {
-        cur.row -= a.entry_rows;
-        ++cur.entry;
-      }
-      cur.ks = 0;
-      cur.valid = cur.pos < hi;
+    cur.pos = tile0 + team * a.tile_rows;
+    cur.entry = entry0;
+    cur.row = cur.pos - entry0 * a.entry_rows;
+    while (cur.row >= a.entry_rows) {
+      cur.row -= a.entry_rows;
+      ++cur.entry;
     }
+    cur.ks = 0;
+    cur.valid = cur.pos < hi;
     const bool go = !(g_moe_test_stall & 1);
     const int spitch = kW4 ? w4_padded(a.K) / GG * 2 : 0;
     const int pitch = kW4 ? w4_padded(a.K) / 2 : a.K * 2;
     const int64_t stotal = kW4 ? (int64_t)a.E * rows_per_expert * spitch : 0;
 
     // Asks for the stage at c: the first warp of the team.
-    auto put = [&](const Cursor<MODE>& c, int slot) {
+    auto put = [&](const Cursor& c, int slot) {
       const uint32_t dst = my_ring + slot * a.stage_bytes;
       uint64_t* bar = &my_full[slot];
-      const int rows = MODE == kDown ? down_rows : c.rows(a);
+      const int rows = c.rows(a);
       const int k0 = c.ks * a.Kc, len = min(a.Kc, a.K - k0);
       const int bytes = kW4 ? (len + 127) / 128 * 64 : len * 2;  // of a row
       const int copies = a.row_copies ? rows : min(rows, 1);      // of a half
@@ -720,8 +666,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       // lanes take the copies in turn (at most 16 of them); lane 0 announces all their bytes first
       const int h = lane >= copies;
       const int r = (h ? lane - copies : lane) * per;
-      const int row = entry_of(c.entry).e * rows_per_expert + c.row +
-                      (MODE == kDown ? 0 : c.skip()) + (h ? a.N : 0) + r;
+      const int row = entry_of(c.entry).e * rows_per_expert + c.row + c.skip() + (h ? a.N : 0) + r;
       const bool has = lane < total && MOL_CHECK(row + per <= a.E * rows_per_expert,
                                                  MOL_CHECK_WEIGHT_ROW, row);
       uint32_t mine = has ? size : 0;
@@ -751,7 +696,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + from, sbytes, bar);
       }
     };
-    Cursor<MODE> ahead = cur;
+    Cursor ahead = cur;
     int filled = 0;  // first warp: stages asked for beyond those consumed
     if (part == 0)
       for (; go && filled < depth && ahead.valid; ++filled, ahead.next(a)) put(ahead, filled);
@@ -772,10 +717,10 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       }
       if (++xi < slots) fault = !mbar_wait(&xfull[xs], xphase, kWaitPolls, limit);
     };
-    int want = MODE == kDown ? cur.pos - lo : 0;  // the token slot of this stage
+    int want = 0;  // the token slot of this stage
     Entry en{0, 0, 0};
     for (; cur.valid; cur.next(a)) {
-      if (MODE != kDown && whole) want = cur.entry - entry0;
+      if (whole) want = cur.entry - entry0;
       while (xi < want && !fault) next_tokens();  // (those passed over are released in their order)
       if (cur.entry != have) {
         have = cur.entry;
@@ -783,8 +728,8 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
       }
       fault = fault || !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
       if (fault) break;
-      const int rows = MODE == kDown ? down_rows : cur.rows(a);
-      const int row0 = cur.row + (MODE == kDown ? 0 : cur.skip());  // of the expert
+      const int rows = cur.rows(a);
+      const int row0 = cur.row + cur.skip();  // of the expert
       const uint32_t st = my_ring + slot * a.stage_bytes;
       if (rows > 0) {
         const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
@@ -831,8 +776,7 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, part, parts);
         }
       }
-      const bool ends =
-          cur.ks == a.ksteps - 1 || (MODE == kDown && cur.pos + a.sum_copies >= hi);
+      const bool ends = cur.ks == a.ksteps - 1;
       if (parts > 1) {
         // the others' sums lie in the stage's own buffer until the first warp refills the stage
         const uint32_t sums_of = st + a.parts_off + lane * 16;
@@ -878,49 +822,33 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
         phase ^= 1;
       }
       // (pieces of rows: the team's stages and the token slots go together, one by one)
-      want += MODE == kDown ? a.sum_copies : 1;
+      ++want;
       if (!ends || part > 0 || rows == 0) continue;
 
       // the tile's values: column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h)
-      if (MODE == kDown && lists.repeated) {
-        // columns of one step may hold the same token: they take turns
-        for (int turn = 0; turn < 4; ++turn) {
-          if (t == turn) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              add_sums(a, lists, sums, en, acc[nt], 0, nt * 8 + 2 * t, row0 - first_row, rows, g);
-              add_sums(a, lists, sums, en, acc[nt], 1, nt * 8 + 2 * t + 1, row0 - first_row, rows, g);
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = nt * 8 + 2 * t + h;
+          float v0 = acc[nt][h], v1 = acc[nt][2 + h];
+          if (MODE == kGateUp) {
+            if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
+            if (col >= en.n || g >= rows) continue;
+            const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
+            const int n = row0 + g;
+            if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
+            if (a.delta) {
+              const bf16* dl = a.delta + pair * a.delta_stride + n;
+              v0 += __bfloat162float(dl[0]);
+              v1 += __bfloat162float(dl[a.N]);
             }
-          }
-          __syncwarp();
-        }
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = nt * 8 + 2 * t + h;
-            float v0 = acc[nt][h], v1 = acc[nt][2 + h];
-            if (MODE == kGateUp) {
-              if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
-              if (col >= en.n || g >= rows) continue;
-              const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
-              const int n = row0 + g;
-              if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
-              if (a.delta) {
-                const bf16* dl = a.delta + pair * a.delta_stride + n;
-                v0 += __bfloat162float(dl[0]);
-                v1 += __bfloat162float(dl[a.N]);
-              }
-              a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
-            } else if (MODE == kDown) {
-              add_sums(a, lists, sums, en, acc[nt], h, col, row0 - first_row, rows, g);
-            } else if (col < en.n) {
-              bf16* o = a.out + col * a.out_stride + row0;
-              if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
-              if (g < rows) o[g] = __float2bfloat16(v0);
-              if (g + 8 < rows) o[g + 8] = __float2bfloat16(v1);
-            }
+            a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
+          } else if (col < en.n) {
+            bf16* o = a.out + col * a.out_stride + row0;
+            if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
+            if (g < rows) o[g] = __float2bfloat16(v0);
+            if (g + 8 < rows) o[g + 8] = __float2bfloat16(v1);
           }
         }
       }
@@ -938,29 +866,246 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
           phase ^= 1;
         }
       }
-    if (a.chained) pdl_wait();
-  } else if (a.chained) {
+  }
+  if (fault && lane == 0) atomicOr(&g_moe_fault_flags, kFaultBulkTimeout);
+}
+
+// out[t] = sum of weight * (w[e] . act[pair]) over t's pairs. A cluster (or one block) has up to 64
+// output rows of every expert; its blocks split the (entry, k step) units. A unit is one stage of a
+// team: the rows' weights, contiguous in memory, and the entry's activation rows. The warps of a team
+// have 16 rows each. A team adds its products into sums of its own, unit after unit; the teams' and
+// then the blocks' sums are added in their order.
+template <int G, int NT>
+__global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_constant__ StreamArgs a) {
+  constexpr bool kW4 = G != 0;
+  constexpr int GG = kW4 ? G : 32;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint64_t wfull[kMaxStages], pfull[kMaxStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int numel = a.num_tokens * a.topk;
+  const int parts = a.parts, team = warp / parts, part = warp - team * parts;
+
+  // shared memory: stages | sums of each team | sums from the cluster's blocks | lists
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t all_sums = ring + a.stages * a.stage_bytes;
+  const uint32_t copy_bytes = a.num_tokens * a.acc_stride * 4;
+  const uint32_t received = all_sums + a.teams * copy_bytes;
+  Lists lists;
+  const int each = (a.num_tokens + a.cluster - 1) / a.cluster;  // tokens a block adds at most
+  lists.entry = received + (a.cluster > 1 ? each * a.cluster * a.acc_stride * 4 : 0);
+  lists.order = lists.entry + numel * 8;
+  lists.weight = lists.order + numel * 4;
+
+  if (warp == (int)(blockDim.x >> 5) - 1) {
+    for (int s = lane; s < a.stages; s += 32) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&pfull[s], max(1, parts - 1));
+    }
+    fence_mbar_init();
+  }
+  if (!a.chained) {
     pdl_wait();
+    pdl_launch_dependents();
+  }
+  const int ranks = a.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
+  if (ranks > 1) cluster_arrive();  // (waited for before the first access to another block)
+  build_lists(a, lists, smem, true);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scratch becomes the ring
+  int first_row, end_row, lo, hi;
+  share(a.N, gridDim.x / ranks, blockIdx.x / ranks, first_row, end_row);
+  share(lists.count * a.ksteps, ranks, rank, lo, hi);
+  const int rows = end_row - first_row;
+  for (int i = tid; i < a.teams * (int)copy_bytes / 4; i += blockDim.x) st_s4(all_sums + 4 * i, 0u);
+  __syncthreads();
+  const unsigned long long limit = g_moe_wait_limit_ns;
+  bool fault = false;
+
+  if (team < a.teams && rows > 0) {
+    const int g = lane >> 2, t = lane & 3;
+    const int depth = a.stages / a.teams;
+    const uint32_t my_ring = ring + team * depth * a.stage_bytes;
+    uint64_t* my_full = wfull + team * depth;
+    uint64_t* my_pfull = pfull + team * depth;
+    const int spitch = kW4 ? w4_padded(a.K) / GG * 2 : 0;
+    const int pitch = kW4 ? w4_padded(a.K) / 2 : a.K * 2;
+    const int64_t stotal = kW4 ? (int64_t)a.E * a.N * spitch : 0;
+
+    // Asks for a unit's weights and announces its activation rows as well: the team's first warp.
+    auto put_weights = [&](int unit, int slot) {
+      const int entry = unit / a.ksteps, ks = unit - entry * a.ksteps;
+      const Entry en = lists.get(entry);
+      const uint32_t dst = my_ring + slot * a.stage_bytes;
+      uint64_t* bar = &my_full[slot];
+      const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
+      const int row0 = en.e * a.N + first_row;
+      const int copies = a.row_copies ? rows : 1, per = a.row_copies ? 1 : rows;
+      const uint32_t size = a.row_copies ? (kW4 ? (len + 127) / 128 * 64 : len * 2) : per * pitch;
+      const int slen = kW4 ? (a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch) : 0;
+      uint32_t bytes = 0;
+      for (int r = lane; r < copies; r += 32) {
+        bytes += size;
+        if (kW4) {
+          const int64_t at = (int64_t)(row0 + r) * spitch + k0 / GG * 2;
+          const ScaleRange sr(at, slen, stotal);
+          bytes += sr.bytes();
+          // what the bulk copy leaves at the end of the tensor
+          for (int64_t b = max(sr.to, at); b < at + slen; b += 4)
+            st_s4(dst + a.scale_off + r * a.scale_pitch + (uint32_t)(b - sr.from),
+                  *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b));
+        }
+      }
+      bytes = __reduce_add_sync(0xffffffffu, bytes);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes + en.n * len * 2);
+      __syncwarp();
+      for (int r = lane; r < copies; r += 32) {
+        const int row = row0 + r;
+        if (!MOL_CHECK(row + per <= a.E * a.N, MOL_CHECK_WEIGHT_ROW, row)) continue;
+        bulk_copy(dst + r * a.row_pitch, a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size,
+                  bar);
+        if (kW4) {
+          const ScaleRange sr((int64_t)row * spitch + k0 / GG * 2, slen, stotal);
+          if (sr.bytes())
+            bulk_copy(dst + a.scale_off + r * a.scale_pitch,
+                      reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes(), bar);
+        }
+      }
+    };
+    auto put_x = [&](int unit, int slot) {
+      const int entry = unit / a.ksteps, ks = unit - entry * a.ksteps;
+      const Entry en = lists.get(entry);
+      const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
+      for (int j = lane; j < en.n; j += 32) {
+        int pair = lists.pair(en.off + j) & 0xFFFF;
+        if (!MOL_CHECK(pair < numel, MOL_CHECK_ROW, pair)) pair = 0;
+        bulk_copy(my_ring + slot * a.stage_bytes + a.x_off + j * a.x_pitch,
+                  a.x + pair * a.x_stride + k0, len * 2, &my_full[slot]);
+      }
+    };
+    int filled = 0;  // first warp: stages asked for and not consumed
+    if (part == 0 && !(g_moe_test_stall & 1)) {
+      for (int u = lo + team; u < hi && filled < depth; u += a.teams) put_weights(u, filled++);
+      if (a.chained) {  // the rows that the kernel before writes
+        pdl_wait();
+        pdl_launch_dependents();
+      }
+      for (int i = 0; i < filled; ++i) put_x(lo + team + i * a.teams, i);
+    }
+    const uint32_t sums = all_sums + team * copy_bytes;
+    int slot = 0, phase = 0;
+    for (int unit = lo + team; unit < hi; unit += a.teams) {
+      fault = !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+      if (fault) break;
+      const int entry = unit / a.ksteps, ks = unit - entry * a.ksteps;
+      const Entry en = lists.get(entry);
+      const uint32_t st = my_ring + slot * a.stage_bytes;
+      const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
+      float acc[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      // the lane's rows; rows past the block's last read that row again, their products are dropped
+      const int i0 = min(part * 16 + g, rows - 1), i1 = min(part * 16 + g + 8, rows - 1);
+      uint32_t x[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        x[nt] = st + a.x_off + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
+      const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
+      if constexpr (kW4) {
+        const int first = en.e * a.N + first_row;
+        // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
+        // before those of the first row
+        auto scales_of = [&](int i) {
+          const uint32_t row = first + (a.row_copies ? i : 0);
+          return st + a.scale_off + i * a.scale_pitch + ((row * spitch + k0 / GG * 2) & 15u);
+        };
+        if (NT > 1 && en.n <= 8)
+          multiply_w4<GG, true, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+        else
+          multiply_w4<GG, true, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+      } else {
+        if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, 0, 1);
+        else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, 0, 1);
+      }
+      __syncwarp();
+      if (parts > 1) {
+        if (part > 0) {
+          if (lane == 0) mbar_arrive(&my_pfull[slot]);
+        } else {
+          fault = !mbar_wait(&my_pfull[slot], phase, kWaitPolls, limit);
+          if (fault) break;
+        }
+      }
+      if (part == 0) {  // the team is through with the stage: the next one into its place
+        const int next = unit + depth * a.teams;
+        if (next < hi) {
+          put_weights(next, slot);
+          put_x(next, slot);
+        } else {
+          --filled;
+        }
+      }
+      if (++slot == depth) {
+        slot = 0;
+        phase ^= 1;
+      }
+      // column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h); columns of one step
+      // may hold the same token where a token lists its expert twice: they take turns
+      for (int turn = 0; turn < (lists.repeated ? 4 : 1); ++turn) {
+        if (!lists.repeated || t == turn) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            add_sums(a, lists, sums, en, acc[nt], 0, nt * 8 + 2 * t, part * 16, rows - part * 16, g);
+            add_sums(a, lists, sums, en, acc[nt], 1, nt * 8 + 2 * t + 1, part * 16, rows - part * 16,
+                     g);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // no copy may be in flight when the block leaves
+    if (fault && part == 0)
+      for (int q = 0; q < filled; ++q) {
+        (void)mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+        if (++slot == depth) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
   }
   if (fault && lane == 0) atomicOr(&g_moe_fault_flags, kFaultBulkTimeout);
 
-  if (MODE == kDown) {
-    // the ranks' sums in their order, each rank's copies in theirs, the deltas, one rounding
-    __syncthreads();
-    if (ranks > 1) cluster_barrier();
-    const int rows = end_row - first_row, total = rows * a.num_tokens;
-    for (int i = tid + rank * (int)blockDim.x; i < total; i += blockDim.x * ranks) {
-      const int tok = i / rows, row = i - tok * rows;
-      const uint32_t at = all_sums + 4 * (tok * a.acc_stride + row);
-      float v = 0.f;
-      for (int q = 0; q < ranks; ++q)
-        for (int c = 0; c < a.sum_copies; ++c)
-          v += ranks > 1 ? remote_f32(at + c * copy_bytes, q) : ld_sf(at + c * copy_bytes);
-      if (a.delta) v = add_deltas(a, v, tok, first_row + row);
-      if (MOL_CHECK(first_row + row < a.N, MOL_CHECK_COLUMN, first_row + row))
-        a.out[tok * a.out_stride + first_row + row] = __float2bfloat16(v);
+  // The teams' sums in their order; with a cluster each block adds the blocks' sums of its share of
+  // the tokens, sent to it, in the order of their ranks. Then the deltas and one rounding.
+  if (a.chained) pdl_wait();
+  __syncthreads();
+  auto finish = [&](int tok, int row, float v) {
+    if (a.delta) v = add_deltas(a, v, tok, first_row + row);
+    if (MOL_CHECK(first_row + row < a.N, MOL_CHECK_COLUMN, first_row + row))
+      a.out[tok * a.out_stride + first_row + row] = __float2bfloat16(v);
+  };
+  const int total = rows * a.num_tokens;
+  if (ranks > 1) cluster_wait();
+  for (int i = tid; i < total; i += blockDim.x) {
+    const int tok = i / rows, row = i - tok * rows;
+    const uint32_t at = 4 * (tok * a.acc_stride + row);
+    float v = 0.f;
+    for (int c = 0; c < a.teams; ++c) v += ld_sf(all_sums + c * copy_bytes + at);
+    if (ranks == 1) {
+      finish(tok, row, v);
+    } else {  // to the block that adds the token
+      remote_store(received + 4 * ((rank * each + tok / ranks) * rows + row), tok % ranks, v);
     }
-    if (ranks > 1) cluster_barrier();
+  }
+  if (ranks > 1) {
+    cluster_arrive();
+    cluster_wait();
+    const int mine = (a.num_tokens - rank + ranks - 1) / ranks;  // tokens rank, rank + ranks, ...
+    for (int i = tid; i < mine * rows; i += blockDim.x) {
+      const int slot_tok = i / rows, row = i - slot_tok * rows;
+      float v = 0.f;
+      for (int q = 0; q < ranks; ++q) v += ld_sf(received + 4 * ((q * each + slot_tok) * rows + row));
+      finish(slot_tok * ranks + rank, row, v);
+    }
   }
 }
 
@@ -968,10 +1113,15 @@ __global__ void __launch_bounds__((kMostConsumers + 1) * 32, 1)
 template <int G>
 struct StreamLaunch {
   template <int MODE, int NT>
+  static auto kernel() {
+    if constexpr (MODE == kDown) return down_kernel<G, NT>;
+    else return stream_kernel<G, MODE, NT>;
+  }
+  template <int MODE, int NT>
   static cudaError_t one(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((a.consumers + 1) * 32);
+    cfg.blockDim = dim3(kBlockWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -984,7 +1134,7 @@ struct StreamLaunch {
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, stream_kernel<G, MODE, NT>, a);
+    return cudaLaunchKernelEx(&cfg, kernel<MODE, NT>(), a);
   }
   template <int MODE>
   static cudaError_t by_tiles(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
@@ -1003,11 +1153,10 @@ struct StreamLaunch {
   }
   template <int MODE, int NT>
   static cudaError_t prepare_one() {
-    cudaError_t e = cudaFuncSetAttribute(stream_kernel<G, MODE, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLarge);
+    cudaError_t e = cudaFuncSetAttribute(kernel<MODE, NT>(),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(stream_kernel<G, MODE, NT>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(kernel<MODE, NT>(), cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     return e;
   }
@@ -1019,26 +1168,29 @@ struct StreamLaunch {
     if (e == cudaSuccess) e = prepare_one<MODE, 8>();
     return e;
   }
-  // clusters: how many clusters of kCluster blocks of `smem` bytes fit the device
-  static cudaError_t prepare(int smem, int* clusters) {
+  // clusters[i] (may be NULL): how many clusters of 1 << i blocks the device holds at once
+  static cudaError_t prepare(int* clusters) {
     cudaError_t e = prepare_mode<kGateUp>();
     if (e == cudaSuccess) e = prepare_mode<kDown>();
     if constexpr (G != 0) {
       if (e == cudaSuccess) e = prepare_mode<kLinear>();
     }
-    if (e != cudaSuccess || !clusters) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3((kMostConsumers + 1) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(clusters, stream_kernel<G, kDown, 1>, &cfg);
+    if (!clusters) return e;
+    for (int i = 0; i < kClusterSizes && e == cudaSuccess; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1 << i);
+      cfg.blockDim = dim3(kBlockWarps * 32);
+      cfg.dynamicSmemBytes = kSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1 << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&clusters[i], kernel<kDown, 1>(), &cfg);
+    }
+    return e;
   }
   static cudaError_t take_faults(unsigned* out) {
     cudaError_t e = cudaMemcpyFromSymbol(out, g_moe_fault_flags, sizeof(unsigned));
@@ -1064,8 +1216,8 @@ struct StreamLaunch {
     return StreamLaunch<G>::launch(a, mode, grid, smem, stream);                              \
   }                                                                                           \
   template <>                                                                                 \
-  cudaError_t stream_prepare<G>(int smem, int* clusters) {                                    \
-    return StreamLaunch<G>::prepare(smem, clusters);                                          \
+  cudaError_t stream_prepare<G>(int* clusters) {                                              \
+    return StreamLaunch<G>::prepare(clusters);                                                \
   }                                                                                           \
   template <>                                                                                 \
   cudaError_t stream_take_faults<G>(unsigned* out) {                                          \

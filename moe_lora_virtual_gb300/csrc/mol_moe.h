@@ -9,16 +9,15 @@ namespace mol {
 
 enum StreamMode { kGateUp = 0, kDown = 1, kLinear = 2 };
 
-// Consumer warps of a block: with the tokens' warp sixteen, so a thread may have 128 registers.
-constexpr int kMostConsumers = 15;
-constexpr int kFewConsumers = 7;
+// Sixteen warps a block, so a thread may have 128 registers: gate_up and linear: one of them brings
+// the tokens' rows.
+constexpr int kBlockWarps = 16;
 constexpr int kMaxStages = 32;  // of all teams of a block
 constexpr int kMaxSlots = 8;    // token slots
-// Blocks of a cluster that share output rows (down).
-constexpr int kCluster = 4;
-// Shared memory of a block: the small one leaves room for a block of the next kernel beside it.
-constexpr int kSmemSmall = 112 * 1024;
-constexpr int kSmemLarge = 222 * 1024;
+constexpr int kClusterSizes = 3;  // down: clusters of 1, 2 or 4 blocks
+constexpr int kSmem = 222 * 1024;
+constexpr int kDownRows = 64;     // output rows of a block of the down kernel at most
+
 struct StreamArgs {
   const __nv_bfloat16* x;  // activation rows: tokens (gate_up, linear) or pairs (down)
   const int32_t* ids;      // [num_tokens * topk], not for the linear
@@ -40,21 +39,18 @@ struct StreamArgs {
                            // where rows come in pieces)
   int row_copies;          // a copy for each row, row_pitch apart; else rows lie as in memory
   int row_pitch, scale_off, scale_pitch, stage_bytes, stages;
-  // a token slot: `xrows` activation rows of Kc inputs
-  int xrows, x_pitch, xslot_bytes, xstages;
-  int group;               // down: row tiles of the block
-  int consumers;           // consumer warps that the block has room for, besides the tokens' warp
+  // `xrows` activation rows of Kc inputs: a token slot, or at x_off of a stage (down)
+  int xrows, x_pitch, xslot_bytes, xstages, x_off;
   int teams, parts;        // teams of `parts` warps in use; the teams divide the stages
-  int parts_off;           // of the partial sums inside a stage
-  // output sums (down): one copy for each team of a row tile, [num_tokens][acc_stride] floats
-  int sum_copies, acc_stride;
+  int parts_off;           // gate_up, linear: of the partial sums inside a stage
+  int acc_stride;          // down: floats between tokens of a team's sums
 };
 
 // One set for each weight format, each in a translation unit of its own (mol_moe_*.cu).
 template <int G>
 cudaError_t stream_launch(const StreamArgs& a, int mode, int grid, size_t smem, cudaStream_t stream);
 template <int G>
-cudaError_t stream_prepare(int smem, int* clusters);
+cudaError_t stream_prepare(int* clusters);
 template <int G>
 cudaError_t stream_take_faults(unsigned* out);
 template <int G>
@@ -66,7 +62,7 @@ cudaError_t stream_take_checks(unsigned long long* first, unsigned long long* co
   template <>                                                                                 \
   cudaError_t stream_launch<G>(const StreamArgs&, int, int, size_t, cudaStream_t);            \
   template <>                                                                                 \
-  cudaError_t stream_prepare<G>(int, int*);                                                   \
+  cudaError_t stream_prepare<G>(int*);                                                        \
   template <>                                                                                 \
   cudaError_t stream_take_faults<G>(unsigned*);                                               \
   template <>                                                                                 \
