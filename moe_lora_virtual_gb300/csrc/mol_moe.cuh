@@ -306,9 +306,21 @@ struct Cursor {
   }
 };
 
-MOL_DEV uint32_t w4_pair(uint32_t v) {  // two nibbles at bits 0 and 16 -> bf16 pair q - 8, exact
-  const uint32_t b = (v & 0x000F000Fu) | 0x43004300u;  // 128 + q
-  const uint32_t c = 0x43084308u;                      // 136
+// mma_16816 with a zero accumulator: d = a . b.
+MOL_DEV void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Two nibbles at bits 0 and 16 -> bf16 pair q - 8, exact: (v & mask) | 128 as one instruction (the
+// compiler makes two of the expression, and the ALU's rate is what 4-bit weights are bound by).
+MOL_DEV uint32_t w4_pair(uint32_t v) {
+  uint32_t b;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(b) : "r"(v), "r"(0x43004300u));
+  const uint32_t c = 0x43084308u;  // 136
   __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b),
                              *reinterpret_cast<const __nv_bfloat162*>(&c));
   return *reinterpret_cast<uint32_t*>(&r);
@@ -389,28 +401,29 @@ MOL_DEV void load_scales(float (&f)[128 / G], uint32_t at) {
   }
 }
 
-// One block of 128 inputs of 4-bit rows (s0, s1: their scales of this block); FULL: all of them
-// below len.
-template <int G, bool TWO, int NTC, int NT, bool FULL>
-MOL_DEV void block_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
-                      const uint32_t (&x)[NT], int b, int len, int t) {
-  const uint4 a0 = ld_s16(r0 + b * 64);
-  const uint4 a1 = TWO ? ld_s16(r1 + b * 64) : make_uint4(0, 0, 0, 0);
+// One block of 128 inputs of 4-bit rows, as loaded.
+template <int G>
+struct BlockW4 {
+  uint4 a0, a1;  // rows g and g + 8
   float f0[128 / G], f1[128 / G];
-  load_scales<G>(f0, s0 + b * (256 / G));
-  if (TWO) load_scales<G>(f1, s1 + b * (256 / G));
-  const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
-  float sum[NTC][4], two[4];  // (a single tile's two steps: two accumulators)
+  template <bool TWO>
+  MOL_DEV void load(uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1, int b) {
+    a0 = ld_s16(r0 + b * 64);
+    a1 = TWO ? ld_s16(r1 + b * 64) : make_uint4(0, 0, 0, 0);
+    load_scales<G>(f0, s0 + b * (256 / G));
+    if (TWO) load_scales<G>(f1, s1 + b * (256 / G));
+  }
+};
+
+// Its products; FULL: all of its inputs are below len.
+template <int G, bool TWO, int NTC, int NT, bool FULL>
+MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (&x)[NT], int b,
+                      int len, int t) {
+  const uint32_t w0[4] = {w.a0.x, w.a0.y, w.a0.z, w.a0.w};
+  const uint32_t w1[4] = {w.a1.x, w.a1.y, w.a1.z, w.a1.w};
+  float sum[NTC][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (i * 32 % G == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        two[j] = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NTC; ++nt) sum[nt][j] = 0.f;
-      }
-    }
     const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
     uint4 v[NTC];
 #pragma unroll
@@ -423,21 +436,22 @@ MOL_DEV void block_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0
       p1[j] = TWO ? w4_pair(w1[i] >> (4 * j)) : 0u;
     }
 #pragma unroll
-    for (int nt = 0; nt < NTC; ++nt)
-      mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+    for (int nt = 0; nt < NTC; ++nt) {
+      if (i * 32 % G == 0)
+        mma_16816_zero(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+      else
+        mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+    }
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt)
-      mma_16816(NTC == 1 ? two : sum[nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
+      mma_16816(sum[nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
     if ((i + 1) * 32 % G == 0) {
       // a group wholly past len holds no weights: its scale may be anything
       const int grp = i * 32 / G;
       const bool has = FULL || b * 128 + grp * G < len;
-      const float g0 = has ? f0[grp] : 0.f, g1 = TWO && has ? f1[grp] : 0.f;
+      const float g0 = has ? w.f0[grp] : 0.f, g1 = TWO && has ? w.f1[grp] : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt) {
-        if (NTC == 1)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[nt][j] += two[j];
         acc[nt][0] = fmaf(g0, sum[nt][0], acc[nt][0]);
         acc[nt][1] = fmaf(g0, sum[nt][1], acc[nt][1]);
         if (TWO) {
@@ -453,11 +467,22 @@ template <int G, bool TWO, int NTC, int NT>
 MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
                          const uint32_t (&x)[NT], int len, int t, int part, int parts) {
   const int full = len >> 7;
+  BlockW4<G> w;
+  int b = part;
+  if (b < full) w.template load<TWO>(r0, r1, s0, s1, b);
 #pragma unroll 1
-  for (int b = part; b < full; b += parts)
-    block_w4<G, TWO, NTC, NT, true>(acc, r0, r1, s0, s1, x, b, len, t);
-  if ((len & 127) && (full & (parts - 1)) == part)
-    block_w4<G, TWO, NTC, NT, false>(acc, r0, r1, s0, s1, x, full, len, t);
+  for (; b + parts < full; b += 2 * parts) {  // a block's weights come while the other is multiplied
+    BlockW4<G> v;
+    v.template load<TWO>(r0, r1, s0, s1, b + parts);
+    block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
+    if (b + 2 * parts < full) w.template load<TWO>(r0, r1, s0, s1, b + 2 * parts);
+    block_w4<G, TWO, NTC, NT, true>(acc, v, x, b + parts, len, t);
+  }
+  if (b < full) block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
+  if ((len & 127) && (full & (parts - 1)) == part) {
+    w.template load<TWO>(r0, r1, s0, s1, full);
+    block_w4<G, TWO, NTC, NT, false>(acc, w, x, full, len, t);
+  }
 }
 
 MOL_DEV uint32_t cluster_rank() {
@@ -505,17 +530,25 @@ MOL_DEV float add_deltas(const StreamArgs& a, float v, int tok, int n) {
   return v;
 }
 
-// The byte range [at, at + len) of the scales (4-byte aligned) into shared memory at dst + (at &
-// 15): bulk copies move whole 16-byte units, so the range is widened to them; at the end of the
-// tensor the last bytes that a unit would overrun are copied word by word.
+// The bytes of some rows' scales, [at, at + len) of the tensor (4-byte aligned), for a bulk copy to a
+// 16-byte aligned place: whole 16-byte units from `from` on. At the end of the tensor the last unit
+// may not be there in full: its words are then copied one by one (`tail`).
 struct ScaleRange {
-  int64_t from, to;  // bulk part, multiples of 16
-  MOL_DEV ScaleRange(int64_t at, int len, int64_t total) {
-    from = at & ~(int64_t)15;
-    to = min((at + len + 15) & ~(int64_t)15, total & ~(int64_t)15);
-    if (to < from) to = from;
+  int64_t from;
+  uint32_t bytes;
+  bool tail;
+  MOL_DEV ScaleRange(int64_t at, uint32_t len, int64_t total) {
+    const uint32_t mis = (uint32_t)at & 15u;
+    from = at - mis;
+    bytes = (mis + len + 15u) & ~15u;
+    tail = from + bytes > total;
+    if (tail) bytes = (uint32_t)(max(from, total & ~(int64_t)15) - from);
   }
-  MOL_DEV uint32_t bytes() const { return (uint32_t)(to - from); }
+  MOL_DEV void copy_tail(const void* scales, uint32_t dst, int64_t at, uint32_t len) const {
+    for (int64_t b = max(from + bytes, at); b < at + len; b += 4)
+      st_s4(dst + (uint32_t)(b - from),
+            *reinterpret_cast<const uint32_t*>(static_cast<const char*>(scales) + b));
+  }
 };
 
 template <int G, int MODE, int NT>
@@ -670,20 +703,13 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       const bool has = lane < total && MOL_CHECK(row + per <= a.E * rows_per_expert,
                                                  MOL_CHECK_WEIGHT_ROW, row);
       uint32_t mine = has ? size : 0;
-      int64_t from = 0;
-      uint32_t sbytes = 0;
       const uint32_t sd = dst + a.scale_off + (h * a.half_rows + r) * a.scale_pitch + h * 16;
+      const int slen = !kW4 ? 0 : a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
+      const int64_t at = kW4 ? (int64_t)row * spitch + k0 / GG * 2 : 0;
+      const ScaleRange sr(at, slen, stotal);
       if (kW4 && has) {
-        const int64_t at = (int64_t)row * spitch + k0 / GG * 2;
-        const int slen = a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
-        const ScaleRange sr(at, slen, stotal);
-        from = sr.from;
-        sbytes = sr.bytes();
-        mine += sbytes;
-        // what the bulk copy leaves at the end of the tensor
-        for (int64_t b = max(sr.to, at); b < at + slen; b += 4)
-          st_s4(sd + (uint32_t)(b - sr.from),
-                *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b));
+        mine += sr.bytes;
+        if (sr.tail) sr.copy_tail(a.scales, sd, at, slen);
       }
       mine = __reduce_add_sync(0xffffffffu, mine);
       __syncwarp();
@@ -692,8 +718,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       if (has) {
         bulk_copy(dst + (h * a.half_rows + r) * a.row_pitch,
                   a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size, bar);
-        if (kW4 && sbytes)
-          bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + from, sbytes, bar);
+        if (kW4 && sr.bytes)
+          bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes, bar);
       }
     };
     Cursor ahead = cur;
@@ -719,12 +745,16 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
     };
     int want = 0;  // the token slot of this stage
     Entry en{0, 0, 0};
+    uint32_t x[NT];  // the lane's token row of each tile
     for (; cur.valid; cur.next(a)) {
       if (whole) want = cur.entry - entry0;
-      while (xi < want && !fault) next_tokens();  // (those passed over are released in their order)
-      if (cur.entry != have) {
+      if (xi < want || cur.entry != have) {
+        while (xi < want && !fault) next_tokens();  // (those passed over are released in their order)
         have = cur.entry;
         en = entry_of(have);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          x[nt] = xslots + xs * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
       }
       fault = fault || !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
       if (fault) break;
@@ -743,10 +773,6 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
           i0 = min(g, rows - 1);
           i1 = min(g + 8, rows - 1);
         }
-        uint32_t x[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          x[nt] = xslots + xs * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
         const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
         if constexpr (kW4) {
           const int first = en.e * rows_per_expert + row0;
@@ -947,11 +973,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
         if (kW4) {
           const int64_t at = (int64_t)(row0 + r) * spitch + k0 / GG * 2;
           const ScaleRange sr(at, slen, stotal);
-          bytes += sr.bytes();
-          // what the bulk copy leaves at the end of the tensor
-          for (int64_t b = max(sr.to, at); b < at + slen; b += 4)
-            st_s4(dst + a.scale_off + r * a.scale_pitch + (uint32_t)(b - sr.from),
-                  *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(a.scales) + b));
+          bytes += sr.bytes;
+          if (sr.tail) sr.copy_tail(a.scales, dst + a.scale_off + r * a.scale_pitch, at, slen);
         }
       }
       bytes = __reduce_add_sync(0xffffffffu, bytes);
@@ -965,9 +988,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
                   bar);
         if (kW4) {
           const ScaleRange sr((int64_t)row * spitch + k0 / GG * 2, slen, stotal);
-          if (sr.bytes())
+          if (sr.bytes)
             bulk_copy(dst + a.scale_off + r * a.scale_pitch,
-                      reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes(), bar);
+                      reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes, bar);
         }
       }
     };
