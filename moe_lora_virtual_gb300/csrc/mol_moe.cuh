@@ -383,46 +383,45 @@ MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const 
   }
 }
 
-// The scales of one row for a block of 128 inputs: bf16 pairs as they lie.
+// The scales of one row for a block of 128 inputs, as fp32.
 template <int G>
-struct Scales {
-  uint32_t v[G == 32 ? 2 : 1];
-  MOL_DEV void load(uint32_t at) {
-    if constexpr (G == 128) {
-      v[0] = ld_s2(at);
-    } else if constexpr (G == 64) {
-      v[0] = ld_s4(at);
-    } else {
-      const uint2 w = ld_s8(at);
-      v[0] = w.x;
-      v[1] = w.y;
-    }
+MOL_DEV void load_scales(float (&f)[128 / G], uint32_t at) {
+  if constexpr (G == 128) {
+    f[0] = __uint_as_float(ld_s2(at) << 16);
+  } else if constexpr (G == 64) {
+    const uint32_t v = ld_s4(at);
+    f[0] = bf16_lo(v);
+    f[1] = bf16_hi(v);
+  } else {
+    const uint2 v = ld_s8(at);
+    f[0] = bf16_lo(v.x);
+    f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y);
+    f[3] = bf16_hi(v.y);
   }
-  MOL_DEV float get(int i) const { return i & 1 ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }
-};
+}
 
-// One block of 128 inputs of 16 * MT 4-bit rows, as loaded: the lane's rows g, g + 8 of each 16.
-template <int G, int MT>
+// One block of 128 inputs of 4-bit rows, as loaded.
+template <int G>
 struct BlockW4 {
-  uint4 a[2 * MT];
-  Scales<G> f[2 * MT];
-  MOL_DEV void load(const uint32_t (&r)[2 * MT], const uint32_t (&s)[2 * MT], int b) {
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      a[i] = ld_s16(r[i] + b * 64);
-      f[i].load(s[i] + b * (256 / G));
-    }
-  }
-  MOL_DEV uint32_t word(int row, int i) const {
-    return i == 0 ? a[row].x : i == 1 ? a[row].y : i == 2 ? a[row].z : a[row].w;
+  uint4 a0, a1;  // rows g and g + 8
+  float f0[128 / G], f1[128 / G];
+  template <bool TWO>
+  MOL_DEV void load(uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1, int b) {
+    a0 = ld_s16(r0 + b * 64);
+    a1 = TWO ? ld_s16(r1 + b * 64) : make_uint4(0, 0, 0, 0);
+    load_scales<G>(f0, s0 + b * (256 / G));
+    if (TWO) load_scales<G>(f1, s1 + b * (256 / G));
   }
 };
 
-// Its products; FULL: all of its inputs are below len. Each read of the tokens serves 16 * MT rows.
-template <int G, int MT, int NTC, int NT, bool FULL>
-MOL_DEV void block_w4(float (&acc)[MT][NT][4], const BlockW4<G, MT>& w, const uint32_t (&x)[NT],
-                      int b, int len, int t) {
-  float sum[MT][NTC][4];
+// Its products; FULL: all of its inputs are below len.
+template <int G, bool TWO, int NTC, int NT, bool FULL>
+MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (&x)[NT], int b,
+                      int len, int t) {
+  const uint32_t w0[4] = {w.a0.x, w.a0.y, w.a0.z, w.a0.w};
+  const uint32_t w1[4] = {w.a1.x, w.a1.y, w.a1.z, w.a1.w};
+  float sum[NTC][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
@@ -430,65 +429,59 @@ MOL_DEV void block_w4(float (&acc)[MT][NT][4], const BlockW4<G, MT>& w, const ui
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt)
       v[nt] = in ? ld_s16(x[nt] + b * 256 + i * 64) : make_uint4(0, 0, 0, 0);
+    uint32_t p0[4], p1[4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint32_t p0[4], p1[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p0[j] = w4_pair(w.word(2 * m, i) >> (4 * j));
-        p1[j] = w4_pair(w.word(2 * m + 1, i) >> (4 * j));
-      }
-#pragma unroll
-      for (int nt = 0; nt < NTC; ++nt) {
-        if (i * 32 % G == 0)
-          mma_16816_zero(sum[m][nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
-        else
-          mma_16816(sum[m][nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NTC; ++nt)
-        mma_16816(sum[m][nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
+    for (int j = 0; j < 4; ++j) {
+      p0[j] = w4_pair(w0[i] >> (4 * j));
+      p1[j] = TWO ? w4_pair(w1[i] >> (4 * j)) : 0u;
     }
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt) {
+      if (i * 32 % G == 0)
+        mma_16816_zero(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+      else
+        mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NTC; ++nt)
+      mma_16816(sum[nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
     if ((i + 1) * 32 % G == 0) {
       // a group wholly past len holds no weights: its scale may be anything
       const int grp = i * 32 / G;
       const bool has = FULL || b * 128 + grp * G < len;
+      const float g0 = has ? w.f0[grp] : 0.f, g1 = TWO && has ? w.f1[grp] : 0.f;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float g0 = has ? w.f[2 * m].get(grp) : 0.f;
-        const float g1 = has ? w.f[2 * m + 1].get(grp) : 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NTC; ++nt) {
-          acc[m][nt][0] = fmaf(g0, sum[m][nt][0], acc[m][nt][0]);
-          acc[m][nt][1] = fmaf(g0, sum[m][nt][1], acc[m][nt][1]);
-          acc[m][nt][2] = fmaf(g1, sum[m][nt][2], acc[m][nt][2]);
-          acc[m][nt][3] = fmaf(g1, sum[m][nt][3], acc[m][nt][3]);
+      for (int nt = 0; nt < NTC; ++nt) {
+        acc[nt][0] = fmaf(g0, sum[nt][0], acc[nt][0]);
+        acc[nt][1] = fmaf(g0, sum[nt][1], acc[nt][1]);
+        if (TWO) {
+          acc[nt][2] = fmaf(g1, sum[nt][2], acc[nt][2]);
+          acc[nt][3] = fmaf(g1, sum[nt][3], acc[nt][3]);
         }
       }
     }
   }
 }
 
-template <int G, int MT, int NTC, int NT>
-MOL_DEV void multiply_w4(float (&acc)[MT][NT][4], const uint32_t (&r)[2 * MT],
-                         const uint32_t (&s)[2 * MT], const uint32_t (&x)[NT], int len, int t,
-                         int part, int parts) {
+template <int G, bool TWO, int NTC, int NT>
+MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
+                         const uint32_t (&x)[NT], int len, int t, int part, int parts) {
   const int full = len >> 7;
-  BlockW4<G, MT> w;
+  BlockW4<G> w;
   int b = part;
-  if (b < full) w.load(r, s, b);
+  if (b < full) w.template load<TWO>(r0, r1, s0, s1, b);
 #pragma unroll 1
   for (; b + parts < full; b += 2 * parts) {  // a block's weights come while the other is multiplied
-    BlockW4<G, MT> v;
-    v.load(r, s, b + parts);
-    block_w4<G, MT, NTC, NT, true>(acc, w, x, b, len, t);
-    if (b + 2 * parts < full) w.load(r, s, b + 2 * parts);
-    block_w4<G, MT, NTC, NT, true>(acc, v, x, b + parts, len, t);
+    BlockW4<G> v;
+    v.template load<TWO>(r0, r1, s0, s1, b + parts);
+    block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
+    if (b + 2 * parts < full) w.template load<TWO>(r0, r1, s0, s1, b + 2 * parts);
+    block_w4<G, TWO, NTC, NT, true>(acc, v, x, b + parts, len, t);
   }
-  if (b < full) block_w4<G, MT, NTC, NT, true>(acc, w, x, b, len, t);
+  if (b < full) block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
   if ((len & 127) && (full & (parts - 1)) == part) {
-    w.load(r, s, full);
-    block_w4<G, MT, NTC, NT, false>(acc, w, x, full, len, t);
+    w.template load<TWO>(r0, r1, s0, s1, full);
+    block_w4<G, TWO, NTC, NT, false>(acc, w, x, full, len, t);
   }
 }
 
@@ -506,21 +499,14 @@ MOL_DEV void remote_store(uint32_t at, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p), "f"(v) : "memory");
 }
 
-template <int MT, int NT>
-MOL_DEV void clear(float (&acc)[MT][NT][4]) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-}
-
 // Adds column `col` of a tile (value h of rows g and g + 8) times its pair's weight into the sums.
 MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, uint32_t sums, const Entry& en,
                       const float (&acc)[4], int h, int col, int row, int rows, int g) {
   if (col >= en.n) return;
   const int tok = l.pair(en.off + col) >> 16;
   const float w = ld_sf(l.weight + 4 * (en.off + col));
-  if (!MOL_CHECK(tok < a.num_tokens && row + rows <= a.acc_stride, MOL_CHECK_SMEM, row)) return;
+  if (!MOL_CHECK(tok < a.num_tokens && row >= 0 && row + rows <= a.acc_stride, MOL_CHECK_SMEM, row))
+    return;
   const uint32_t s = sums + 4 * (tok * a.acc_stride + row + g);
   if (g < rows) st_sf(s, fmaf(w, h ? acc[1] : acc[0], ld_sf(s)));
   if (g + 8 < rows) st_sf(s + 32, fmaf(w, h ? acc[3] : acc[2], ld_sf(s + 32)));
@@ -565,7 +551,7 @@ struct ScaleRange {
   }
 };
 
-template <int G, int MODE, int MT, int NT>
+template <int G, int MODE, int NT>
 __global__ void __launch_bounds__(kBlockWarps * 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs a) {
   constexpr bool kW4 = G != 0;
@@ -741,8 +727,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
     if (part == 0)
       for (; go && filled < depth && ahead.valid; ++filled, ahead.next(a)) put(ahead, filled);
 
-    float acc[MT][NT][4];
-    clear(acc);
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     int slot = 0, phase = 0, have = -1;
     int xi = -1, xs = -1, xphase = 0;  // token slots so far, the newest one's place and phase
     auto next_tokens = [&]() {         // releases the token slot in use and waits for the next
@@ -776,46 +763,43 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       const uint32_t st = my_ring + slot * a.stage_bytes;
       if (rows > 0) {
         const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
-        // the lane's rows g, g + 8 of each 16 (a gate and an up row of one output; with tiles of 8
-        // rows 4 gate rows, then 4 up rows); rows past the tile's last read that row again, their
-        // products are dropped
-        int row[2 * MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (MODE == kGateUp) {
-            row[2 * m] = min(m * 8 + (a.half_rows == 4 ? g & 3 : g), rows - 1);
-            row[2 * m + 1] = a.half_rows + row[2 * m];
-            if (a.half_rows == 4 && g >= 4) row[2 * m] = row[2 * m + 1];
-          } else {
-            row[2 * m] = min(m * 16 + g, rows - 1);
-            row[2 * m + 1] = min(m * 16 + g + 8, rows - 1);
-          }
+        // the lane's rows; rows past the tile's last read that row again, their products are dropped
+        int i0, i1;
+        if (MODE == kGateUp) {
+          i0 = min(a.half_rows == 8 ? g : g & 3, rows - 1);
+          i1 = a.half_rows + i0;
+          if (a.half_rows != 8 && g >= 4) i0 = i1;  // 4 gate rows, then 4 up rows
+        } else {
+          i0 = min(g, rows - 1);
+          i1 = min(g + 8, rows - 1);
         }
+        const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
         if constexpr (kW4) {
           const int first = en.e * rows_per_expert + row0;
-          uint32_t r[2 * MT], s[2 * MT];
-#pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) {
-            r[i] = st + row[i] * a.row_pitch + t * 16;
-            // the copy that brought a row's scales began at the 16 bytes' boundary at or before them,
-            // or before those of its half's first row
-            const int h = MODE == kGateUp && row[i] >= a.half_rows;
-            const uint32_t from = first + (h ? a.N : 0) + (a.row_copies ? row[i] - h * a.half_rows : 0);
-            s[i] = st + a.scale_off + row[i] * a.scale_pitch + h * 16 +
-                   ((from * spitch + k0 / GG * 2) & 15u);
-          }
-          if (NT > 1 && en.n <= 8) multiply_w4<GG, MT, 1, NT>(acc, r, s, x, len, t, part, parts);
-          else multiply_w4<GG, MT, NT, NT>(acc, r, s, x, len, t, part, parts);
-        } else {
-          const uint32_t r0 = st + row[0] * a.row_pitch + t * 16, r1 = st + row[1] * a.row_pitch + t * 16;
+          // the copy that brought a row's scales began at 16 bytes' boundary at or before them, or
+          // before those of its half's first row
+          auto scales_of = [&](int i) {
+            const int h = MODE == kGateUp && i >= a.half_rows;
+            const int row = first + (h ? a.N : 0) + (a.row_copies ? i - h * a.half_rows : 0);
+            return st + a.scale_off + i * a.scale_pitch + h * 16 +
+                   (((uint32_t)row * spitch + k0 / GG * 2) & 15u);
+          };
+          const uint32_t s0 = scales_of(i0), s1 = scales_of(i1);
           if (a.stage_rows == 8) {
             if (NT > 1 && en.n <= 8)
-              multiply_bf16<false, 1, NT>(acc[0], r0, r1, x, len, t, part, parts);
-            else multiply_bf16<false, NT, NT>(acc[0], r0, r1, x, len, t, part, parts);
+              multiply_w4<GG, false, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+            else multiply_w4<GG, false, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
           } else {
-            if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc[0], r0, r1, x, len, t, part, parts);
-            else multiply_bf16<true, NT, NT>(acc[0], r0, r1, x, len, t, part, parts);
+            if (NT > 1 && en.n <= 8)
+              multiply_w4<GG, true, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+            else multiply_w4<GG, true, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
           }
+        } else if (a.stage_rows == 8) {
+          if (NT > 1 && en.n <= 8) multiply_bf16<false, 1, NT>(acc, r0, r1, x, len, t, part, parts);
+          else multiply_bf16<false, NT, NT>(acc, r0, r1, x, len, t, part, parts);
+        } else {
+          if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, part, parts);
+          else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, part, parts);
         }
       }
       const bool ends = cur.ks == a.ksteps - 1;
@@ -825,12 +809,11 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         if (part > 0) {
           if (ends) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                st_s16(sums_of + (((part - 1) * MT + m) * NT + nt) * 512, acc[m][nt][0],
-                       acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]);
-            clear(acc);
+            for (int nt = 0; nt < NT; ++nt) {
+              st_s16(sums_of + ((part - 1) * NT + nt) * 512, acc[nt][0], acc[nt][1], acc[nt][2],
+                     acc[nt][3]);
+              acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&my_pfull[slot]);
@@ -840,15 +823,13 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
           if (ends) {
             for (int p = 0; p < parts - 1; ++p) {
 #pragma unroll
-              for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint4 v = ld_s16(sums_of + ((p * MT + m) * NT + nt) * 512);
-                  acc[m][nt][0] += __uint_as_float(v.x);
-                  acc[m][nt][1] += __uint_as_float(v.y);
-                  acc[m][nt][2] += __uint_as_float(v.z);
-                  acc[m][nt][3] += __uint_as_float(v.w);
-                }
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint4 v = ld_s16(sums_of + (p * NT + nt) * 512);
+                acc[nt][0] += __uint_as_float(v.x);
+                acc[nt][1] += __uint_as_float(v.y);
+                acc[nt][2] += __uint_as_float(v.z);
+                acc[nt][3] += __uint_as_float(v.w);
+              }
             }
           }
         }
@@ -872,37 +853,33 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
 
       // the tile's values: column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = nt * 8 + 2 * t + h;
-            float v0 = acc[m][nt][h], v1 = acc[m][nt][2 + h];
-            if (MODE == kGateUp) {
-              if (a.half_rows == 4) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
-              const int r = m * 8 + g;
-              if (col >= en.n || r >= rows) continue;
-              const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
-              const int n = row0 + r;
-              if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
-              if (a.delta) {
-                const bf16* dl = a.delta + pair * a.delta_stride + n;
-                v0 += __bfloat162float(dl[0]);
-                v1 += __bfloat162float(dl[a.N]);
-              }
-              a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
-            } else if (col < en.n) {
-              bf16* o = a.out + col * a.out_stride + row0;
-              const int r = m * 16 + g;
-              if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
-              if (r < rows) o[r] = __float2bfloat16(v0);
-              if (r + 8 < rows) o[r + 8] = __float2bfloat16(v1);
+        for (int h = 0; h < 2; ++h) {
+          const int col = nt * 8 + 2 * t + h;
+          float v0 = acc[nt][h], v1 = acc[nt][2 + h];
+          if (MODE == kGateUp) {
+            if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
+            if (col >= en.n || g >= rows) continue;
+            const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
+            const int n = row0 + g;
+            if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
+            if (a.delta) {
+              const bf16* dl = a.delta + pair * a.delta_stride + n;
+              v0 += __bfloat162float(dl[0]);
+              v1 += __bfloat162float(dl[a.N]);
             }
+            a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
+          } else if (col < en.n) {
+            bf16* o = a.out + col * a.out_stride + row0;
+            if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
+            if (g < rows) o[g] = __float2bfloat16(v0);
+            if (g + 8 < rows) o[g + 8] = __float2bfloat16(v1);
           }
         }
       }
-      clear(acc);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
     // the token slots that are left, for the teams that still need them to be refilled
     while (!fault && xi < slots) next_tokens();
@@ -922,9 +899,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
 // out[t] = sum of weight * (w[e] . act[pair]) over t's pairs. A cluster (or one block) has up to 64
 // output rows of every expert; its blocks split the (entry, k step) units. A unit is one stage of a
 // team: the rows' weights, contiguous in memory, and the entry's activation rows. The warps of a team
-// have 16 * MT rows each. A team adds its products into sums of its own, unit after unit; the teams' and
+// have 16 rows each. A team adds its products into sums of its own, unit after unit; the teams' and
 // then the blocks' sums are added in their order.
-template <int G, int MT, int NT>
+template <int G, int NT>
 __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_constant__ StreamArgs a) {
   constexpr bool kW4 = G != 0;
   constexpr int GG = kW4 ? G : 32;
@@ -1038,7 +1015,6 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       for (int i = 0; i < filled; ++i) put_x(lo + team + i * a.teams, i);
     }
     const uint32_t sums = all_sums + team * copy_bytes;
-    const int my_row = part * 16 * MT;
     int slot = 0, phase = 0;
     for (int unit = lo + team; unit < hi; unit += a.teams) {
       fault = !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
@@ -1047,33 +1023,31 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       const Entry en = lists.get(entry);
       const uint32_t st = my_ring + slot * a.stage_bytes;
       const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
-      float acc[MT][NT][4];
-      clear(acc);
-      // the lane's rows; rows past the block's last read that row again, their products are dropped
-      int row[2 * MT];
+      float acc[NT][4];
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) row[i] = min(my_row + i * 8 + g, rows - 1);
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      // the lane's rows; rows past the block's last read that row again, their products are dropped
+      const int i0 = min(part * 16 + g, rows - 1), i1 = min(part * 16 + g + 8, rows - 1);
       uint32_t x[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         x[nt] = st + a.x_off + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
+      const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
       if constexpr (kW4) {
         const int first = en.e * a.N + first_row;
-        uint32_t r[2 * MT], s[2 * MT];
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          r[i] = st + row[i] * a.row_pitch + t * 16;
-          // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
-          // before those of the first row
-          const uint32_t from = first + (a.row_copies ? row[i] : 0);
-          s[i] = st + a.scale_off + row[i] * a.scale_pitch + ((from * spitch + k0 / GG * 2) & 15u);
-        }
-        if (NT > 1 && en.n <= 8) multiply_w4<GG, MT, 1, NT>(acc, r, s, x, len, t, 0, 1);
-        else multiply_w4<GG, MT, NT, NT>(acc, r, s, x, len, t, 0, 1);
+        // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
+        // before those of the first row
+        auto scales_of = [&](int i) {
+          const uint32_t row = first + (a.row_copies ? i : 0);
+          return st + a.scale_off + i * a.scale_pitch + ((row * spitch + k0 / GG * 2) & 15u);
+        };
+        if (NT > 1 && en.n <= 8)
+          multiply_w4<GG, true, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+        else
+          multiply_w4<GG, true, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
       } else {
-        const uint32_t r0 = st + row[0] * a.row_pitch + t * 16, r1 = st + row[1] * a.row_pitch + t * 16;
-        if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc[0], r0, r1, x, len, t, 0, 1);
-        else multiply_bf16<true, NT, NT>(acc[0], r0, r1, x, len, t, 0, 1);
+        if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, 0, 1);
+        else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, 0, 1);
       }
       __syncwarp();
       if (parts > 1) {
@@ -1102,13 +1076,11 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       for (int turn = 0; turn < (lists.repeated ? 4 : 1); ++turn) {
         if (!lists.repeated || t == turn) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                add_sums(a, lists, sums, en, acc[m][nt], h, nt * 8 + 2 * t + h, my_row + m * 16,
-                         rows - my_row - m * 16, g);
+          for (int nt = 0; nt < NT; ++nt) {
+            add_sums(a, lists, sums, en, acc[nt], 0, nt * 8 + 2 * t, part * 16, rows - part * 16, g);
+            add_sums(a, lists, sums, en, acc[nt], 1, nt * 8 + 2 * t + 1, part * 16, rows - part * 16,
+                     g);
+          }
         }
         __syncwarp();
       }
@@ -1163,12 +1135,12 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
 // The launches of one weight format.
 template <int G>
 struct StreamLaunch {
-  template <int MODE, int MT, int NT>
+  template <int MODE, int NT>
   static auto kernel() {
-    if constexpr (MODE == kDown) return down_kernel<G, MT, NT>;
-    else return stream_kernel<G, MODE, MT, NT>;
+    if constexpr (MODE == kDown) return down_kernel<G, NT>;
+    else return stream_kernel<G, MODE, NT>;
   }
-  template <int MODE, int MT, int NT>
+  template <int MODE, int NT>
   static cudaError_t one(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1185,17 +1157,14 @@ struct StreamLaunch {
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kernel<MODE, MT, NT>(), a);
+    return cudaLaunchKernelEx(&cfg, kernel<MODE, NT>(), a);
   }
   template <int MODE>
   static cudaError_t by_tiles(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
-    if constexpr (G != 0) {
-      if (a.mtiles == 2) return one<MODE, 2, 1>(a, grid, smem, stream);
-    }
-    if (a.xrows <= 8) return one<MODE, 1, 1>(a, grid, smem, stream);
-    if (a.xrows <= 16) return one<MODE, 1, 2>(a, grid, smem, stream);
-    if (a.xrows <= 32) return one<MODE, 1, 4>(a, grid, smem, stream);
-    return one<MODE, 1, 8>(a, grid, smem, stream);
+    if (a.xrows <= 8) return one<MODE, 1>(a, grid, smem, stream);
+    if (a.xrows <= 16) return one<MODE, 2>(a, grid, smem, stream);
+    if (a.xrows <= 32) return one<MODE, 4>(a, grid, smem, stream);
+    return one<MODE, 8>(a, grid, smem, stream);
   }
   static cudaError_t launch(const StreamArgs& a, int mode, int grid, size_t smem,
                             cudaStream_t stream) {
@@ -1205,24 +1174,21 @@ struct StreamLaunch {
     }
     return by_tiles<kDown>(a, grid, smem, stream);
   }
-  template <int MODE, int MT, int NT>
+  template <int MODE, int NT>
   static cudaError_t prepare_one() {
-    cudaError_t e = cudaFuncSetAttribute(kernel<MODE, MT, NT>(),
+    cudaError_t e = cudaFuncSetAttribute(kernel<MODE, NT>(),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kernel<MODE, MT, NT>(), cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(kernel<MODE, NT>(), cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     return e;
   }
   template <int MODE>
   static cudaError_t prepare_mode() {
-    cudaError_t e = prepare_one<MODE, 1, 1>();
-    if (e == cudaSuccess) e = prepare_one<MODE, 1, 2>();
-    if (e == cudaSuccess) e = prepare_one<MODE, 1, 4>();
-    if (e == cudaSuccess) e = prepare_one<MODE, 1, 8>();
-    if constexpr (G != 0) {
-      if (e == cudaSuccess) e = prepare_one<MODE, 2, 1>();
-    }
+    cudaError_t e = prepare_one<MODE, 1>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 2>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 4>();
+    if (e == cudaSuccess) e = prepare_one<MODE, 8>();
     return e;
   }
   // clusters[i] (may be NULL): how many clusters of 1 << i blocks the device holds at once
@@ -1245,7 +1211,7 @@ struct StreamLaunch {
       attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&clusters[i], kernel<kDown, 1, 1>(), &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters[i], kernel<kDown, 1>(), &cfg);
     }
     return e;
   }

@@ -32,8 +32,7 @@ struct StreamArgs {
   int N;                   // outputs of one expert: I, H, or the linear's N
   int chained;             // the kernel before is this call's gate_up
   int cluster;             // blocks that share output rows (down), 1 otherwise
-  int mtiles;              // 16-row tiles of a warp: 2 with 4-bit weights where rows are many
-  // A stage: `stage_rows` (8, or 16 * mtiles) weight rows of Kc inputs, gate rows and from half_rows on up
+  // A stage: `stage_rows` (8 or 16) weight rows of Kc inputs, gate rows and from half_rows on up
   // rows (gate_up); tile_rows outputs.
   int stage_rows, half_rows, tile_rows, Kc, ksteps;
   int entry_rows;          // gate_up, linear: N rounded up to whole tiles (to a tile for each team
