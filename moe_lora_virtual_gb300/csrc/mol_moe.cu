@@ -42,15 +42,13 @@ int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : xrows <= 
 // of fewer are larger.
 constexpr int kLeastStage = 1280;
 
-// Rows of Kc inputs in a stage.
-void row_layout(StreamArgs& a, int group, int rows, int Kc, int copy_rows_from) {
+// Rows of Kc inputs in a stage: as they lie in memory (one copy), or pieces of them (a copy each).
+void row_layout(StreamArgs& a, int group, int rows, int Kc) {
   const int bytes = group ? align_up(Kc, 256) / 2 : Kc * 2;  // of a row
   const int scale_bytes = group ? align_up(Kc, 256) / group * 2 : 0;
   a.Kc = Kc;
   a.ksteps = (a.K + Kc - 1) / Kc;
-  // a copy for each row: pieces of rows, and rows so long that shorter copies gain nothing (padding
-  // then keeps the lanes' reads off the same banks)
-  a.row_copies = a.ksteps > 1 || bytes >= copy_rows_from;
+  a.row_copies = a.ksteps > 1;
   a.row_pitch = a.row_copies ? align_up(bytes, 128) + 64 : bytes;
   a.scale_pitch = !group ? 0 : a.row_copies ? align_up(scale_bytes, 16) + 16 : scale_bytes;
   a.scale_off = align_up(rows * a.row_pitch, 16);
@@ -60,12 +58,12 @@ void row_layout(StreamArgs& a, int group, int rows, int Kc, int copy_rows_from) 
 // gate_up, linear: chooses the stage and the rings for a block that has `room` bytes for them.
 // xstages_most: token slots of use when they hold whole rows. False when nothing fits.
 bool plan(StreamArgs& a, int group, int mode, int room, int xstages_most) {
-  auto stage = [&](int rows, int Kc, int xstages) {
-    row_layout(a, group, rows, Kc, 4096);
-    a.stage_rows = rows;
-    a.half_rows = rows / 2;
-    a.tile_rows = mode == kGateUp ? rows / 2 : rows;
-    a.parts_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
+  auto stage = [&](int stage_rows, int Kc, int xstages) {
+    row_layout(a, group, stage_rows, Kc);
+    a.stage_rows = stage_rows;
+    a.half_rows = stage_rows / 2;
+    a.tile_rows = mode == kGateUp ? stage_rows / 2 : stage_rows;
+    a.parts_off = align_up(a.scale_off + stage_rows * a.scale_pitch + (group ? 32 : 0), 128);
     a.stage_bytes = std::max(
         kLeastStage, a.parts_off + (parts_most(a.xrows) - 1) * 512 * token_tiles(a.xrows));
     a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
@@ -74,16 +72,17 @@ bool plan(StreamArgs& a, int group, int mode, int room, int xstages_most) {
     return a.stages;
   };
   // Whole rows. 16 rows a tile use the tensor instruction's M side, and each read of the tokens,
-  // fully; tiles of 8 leave room for more stages where rows are long. A second token slot lets the
-  // next expert's tokens come while the last one's stages are consumed.
+  // fully; tiles of 8 (bf16) leave room for more stages where rows are long. A second token slot lets
+  // the next expert's tokens come while the last one's stages are consumed.
   for (int x = xstages_most; x >= 1; --x)
     if (stage(16, a.K, x) >= (x > 1 ? 6 : 4)) return true;
-  for (int x = xstages_most; x >= 1; --x)
+  for (int x = xstages_most; x >= 1 && !group; --x)
     if (stage(8, a.K, x) >= (x > 1 ? 4 : 3)) return true;
+  if (stage(16, a.K, 1) >= 2) return true;
   // pieces of rows, the longest that leave four stages
   for (int Kc = 2048; Kc > 256; Kc -= 256)
     if (Kc < a.K && stage(group || Kc <= 1024 ? 16 : 8, Kc, 2) >= 4) return true;
-  return stage(8, std::min(256, a.K), 2) >= 2;
+  return stage(group ? 16 : 8, std::min(256, a.K), 2) >= 2;
 }
 
 // gate_up, linear: as many teams as there are stages, or fewer that share them evenly without leaving
@@ -100,25 +99,19 @@ void fit_teams(StreamArgs& a) {
 }
 
 // down: the stage and the teams of a block of `rows` output rows, with `fixed` bytes of lists and
-// sums besides each team's `copy` of them. False when fewer than two stages fit.
-bool plan_down(StreamArgs& a, int group, int rows, int fixed, int copy) {
+// sums besides each team's `copy` of them. False when the stages that fit are fewer than `least`.
+bool plan_down(StreamArgs& a, int group, int rows, int Kc, int fixed, int copy, int least) {
   a.parts = (rows + 15) / 16;
-  auto stage = [&](int Kc) {
-    row_layout(a, group, rows, Kc, 1 << 30);
-    a.x_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
-    a.stage_bytes = std::max(kLeastStage, a.x_off + align_up(a.xrows * a.x_pitch, 128));
-    // as many teams as have a stage each, beside their sums
-    for (a.teams = kBlockWarps / a.parts; a.teams >= 1; --a.teams) {
-      a.stages = std::min(kMaxStages, (kSmem - fixed - a.teams * copy) / a.stage_bytes);
-      if (a.stages >= a.teams) break;
-    }
-    a.stages = a.teams ? a.stages / a.teams * a.teams : 0;
-    return a.stages;
-  };
-  if (stage(a.K) >= 3) return true;
-  for (int Kc = 2048; Kc > 256; Kc -= 256)
-    if (Kc < a.K && stage(Kc) >= 3) return true;
-  return stage(std::min(256, a.K)) >= 2;
+  row_layout(a, group, rows, Kc);
+  a.x_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
+  a.stage_bytes = std::max(kLeastStage, a.x_off + align_up(a.xrows * a.x_pitch, 128));
+  // as many teams as have a stage each, beside their sums
+  for (a.teams = kBlockWarps / a.parts; a.teams >= 1; --a.teams) {
+    a.stages = std::min(kMaxStages, (kSmem - fixed - a.teams * copy) / a.stage_bytes);
+    if (a.stages >= a.teams) break;
+  }
+  a.stages = a.teams ? a.stages / a.teams * a.teams : 0;
+  return a.stages >= least;
 }
 
 StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const int32_t* ids,
@@ -168,37 +161,50 @@ cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* t
   a.chained = chained;
   // Blocks alone or clusters that split the experts: the fewer rows a block has, the more often each
   // activation row is read. Taken is what brings the fewest bytes into one block, a cluster's
-  // exchange counted as the 64 KB that arrive meanwhile. Many rows take several waves of blocks.
+  // exchange counted as the 64 KB that arrive meanwhile, among those whose stages hold whole rows.
+  // Many rows take several waves of blocks.
   const int pairs = s.num_tokens * s.topk, units = std::min(pairs, s.num_experts);
   const int64_t x_bytes = (int64_t)s.inter * 2 * ((pairs + units - 1) / units);
   const int64_t row_bytes = w.group ? w4_padded(s.inter) / 2 : s.inter * 2;
+  StreamArgs best = {};
   int64_t least = INT64_MAX;
-  int blocks = 0;
-  for (int i = 0; i < kClusterSizes; ++i) {
-    if (g_clusters[i] < 1) continue;
-    const int waves = (s.hidden + g_clusters[i] * kDownRows - 1) / (g_clusters[i] * kDownRows);
-    const int n = std::min(g_clusters[i] * waves, (s.hidden + 7) / 8);
-    const int rows = (s.hidden + n - 1) / n;
-    const int64_t bytes = waves * (((units + (1 << i) - 1) >> i) * (rows * row_bytes + x_bytes)) +
-                          (i > 0 ? 65536 : 0);
-    if (bytes < least) {
-      least = bytes;
-      a.cluster = 1 << i;
-      blocks = n;
-    }
-  }
-  // fewer rows a block where the sums or a stage of so many do not fit
-  for (; blocks < s.hidden; blocks *= 2) {
-    const int n = std::min(blocks, s.hidden), rows = (s.hidden + n - 1) / n;
+  int grid = 0;
+  size_t smem = 0;
+  auto consider = [&](int cluster, int blocks, int waves, int Kc, int stages) {
+    const int rows = (s.hidden + blocks - 1) / blocks;
+    a.cluster = cluster;
     a.acc_stride = align_up(rows, 4) + 4;
     const int copy = s.num_tokens * a.acc_stride * 4;
     const int fixed =
-        list_bytes(s) + (a.cluster > 1 ? align_up(s.num_tokens, a.cluster) * a.acc_stride * 4 : 0);
-    if (fixed + copy > kSmem / 2 || !plan_down(a, w.group, rows, fixed, copy)) continue;
-    const size_t smem = (size_t)a.stages * a.stage_bytes + a.teams * copy + fixed;
-    return launch_by_group(w.group, a, kDown, n * a.cluster, smem, stream);
+        list_bytes(s) + (cluster > 1 ? align_up(s.num_tokens, cluster) * a.acc_stride * 4 : 0);
+    if (fixed + copy > kSmem / 2 || !plan_down(a, w.group, rows, Kc, fixed, copy, stages)) return;
+    const int64_t bytes =
+        waves * ((units + cluster - 1) / cluster) * (rows * row_bytes + x_bytes) +
+        (cluster > 1 ? 65536 : 0);
+    if (bytes >= least) return;
+    least = bytes;
+    best = a;
+    grid = blocks * cluster;
+    smem = (size_t)a.stages * a.stage_bytes + a.teams * copy + fixed;
+  };
+  for (int i = 0; i < kClusterSizes; ++i) {
+    const int at_once = g_clusters[i];
+    if (at_once < 1) continue;
+    const int waves = (s.hidden + at_once * kDownRows - 1) / (at_once * kDownRows);
+    consider(1 << i, std::min(at_once * waves, (s.hidden + 7) / 8), waves, s.inter, 3);
   }
-  return cudaErrorInvalidConfiguration;
+  // else pieces of rows, or fewer rows a block
+  for (int blocks = g_clusters[0]; grid == 0; blocks *= 2) {
+    const int n = std::min(blocks, s.hidden), rows = (s.hidden + n - 1) / n;
+    if (rows <= kDownRows) {
+      for (int Kc = 2048; Kc > 256 && grid == 0; Kc -= 256)
+        if (Kc < s.inter) consider(1, n, 1, Kc, 3);
+      if (grid == 0) consider(1, n, 1, std::min(256, s.inter), 2);
+    }
+    if (n == s.hidden) break;
+  }
+  if (grid == 0) return cudaErrorInvalidConfiguration;
+  return launch_by_group(w.group, best, kDown, grid, smem, stream);
 }
 
 cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, int N,

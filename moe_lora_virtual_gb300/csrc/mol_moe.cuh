@@ -383,40 +383,39 @@ MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const 
   }
 }
 
-// The scales of one row for a block of 128 inputs, as fp32.
+// The scales of one row for a block of 128 inputs: bf16 pairs as they lie.
 template <int G>
-MOL_DEV void load_scales(float (&f)[128 / G], uint32_t at) {
-  if constexpr (G == 128) {
-    f[0] = __uint_as_float(ld_s2(at) << 16);
-  } else if constexpr (G == 64) {
-    const uint32_t v = ld_s4(at);
-    f[0] = bf16_lo(v);
-    f[1] = bf16_hi(v);
-  } else {
-    const uint2 v = ld_s8(at);
-    f[0] = bf16_lo(v.x);
-    f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y);
-    f[3] = bf16_hi(v.y);
+struct Scales {
+  uint32_t v[G == 32 ? 2 : 1];
+  MOL_DEV void load(uint32_t at) {
+    if constexpr (G == 128) {
+      v[0] = ld_s2(at);
+    } else if constexpr (G == 64) {
+      v[0] = ld_s4(at);
+    } else {
+      const uint2 w = ld_s8(at);
+      v[0] = w.x;
+      v[1] = w.y;
+    }
   }
-}
+  MOL_DEV float get(int i) const { return i & 1 ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }
+};
 
 // One block of 128 inputs of 4-bit rows, as loaded.
 template <int G>
 struct BlockW4 {
   uint4 a0, a1;  // rows g and g + 8
-  float f0[128 / G], f1[128 / G];
-  template <bool TWO>
+  Scales<G> f0, f1;
   MOL_DEV void load(uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1, int b) {
     a0 = ld_s16(r0 + b * 64);
-    a1 = TWO ? ld_s16(r1 + b * 64) : make_uint4(0, 0, 0, 0);
-    load_scales<G>(f0, s0 + b * (256 / G));
-    if (TWO) load_scales<G>(f1, s1 + b * (256 / G));
+    a1 = ld_s16(r1 + b * 64);
+    f0.load(s0 + b * (256 / G));
+    f1.load(s1 + b * (256 / G));
   }
 };
 
 // Its products; FULL: all of its inputs are below len.
-template <int G, bool TWO, int NTC, int NT, bool FULL>
+template <int G, int NTC, int NT, bool FULL>
 MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (&x)[NT], int b,
                       int len, int t) {
   const uint32_t w0[4] = {w.a0.x, w.a0.y, w.a0.z, w.a0.w};
@@ -433,7 +432,7 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       p0[j] = w4_pair(w0[i] >> (4 * j));
-      p1[j] = TWO ? w4_pair(w1[i] >> (4 * j)) : 0u;
+      p1[j] = w4_pair(w1[i] >> (4 * j));
     }
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt) {
@@ -449,39 +448,37 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
       // a group wholly past len holds no weights: its scale may be anything
       const int grp = i * 32 / G;
       const bool has = FULL || b * 128 + grp * G < len;
-      const float g0 = has ? w.f0[grp] : 0.f, g1 = TWO && has ? w.f1[grp] : 0.f;
+      const float g0 = has ? w.f0.get(grp) : 0.f, g1 = has ? w.f1.get(grp) : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt) {
         acc[nt][0] = fmaf(g0, sum[nt][0], acc[nt][0]);
         acc[nt][1] = fmaf(g0, sum[nt][1], acc[nt][1]);
-        if (TWO) {
-          acc[nt][2] = fmaf(g1, sum[nt][2], acc[nt][2]);
-          acc[nt][3] = fmaf(g1, sum[nt][3], acc[nt][3]);
-        }
+        acc[nt][2] = fmaf(g1, sum[nt][2], acc[nt][2]);
+        acc[nt][3] = fmaf(g1, sum[nt][3], acc[nt][3]);
       }
     }
   }
 }
 
-template <int G, bool TWO, int NTC, int NT>
+template <int G, int NTC, int NT>
 MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
                          const uint32_t (&x)[NT], int len, int t, int part, int parts) {
   const int full = len >> 7;
   BlockW4<G> w;
   int b = part;
-  if (b < full) w.template load<TWO>(r0, r1, s0, s1, b);
+  if (b < full) w.load(r0, r1, s0, s1, b);
 #pragma unroll 1
   for (; b + parts < full; b += 2 * parts) {  // a block's weights come while the other is multiplied
     BlockW4<G> v;
-    v.template load<TWO>(r0, r1, s0, s1, b + parts);
-    block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
-    if (b + 2 * parts < full) w.template load<TWO>(r0, r1, s0, s1, b + 2 * parts);
-    block_w4<G, TWO, NTC, NT, true>(acc, v, x, b + parts, len, t);
+    v.load(r0, r1, s0, s1, b + parts);
+    block_w4<G, NTC, NT, true>(acc, w, x, b, len, t);
+    if (b + 2 * parts < full) w.load(r0, r1, s0, s1, b + 2 * parts);
+    block_w4<G, NTC, NT, true>(acc, v, x, b + parts, len, t);
   }
-  if (b < full) block_w4<G, TWO, NTC, NT, true>(acc, w, x, b, len, t);
+  if (b < full) block_w4<G, NTC, NT, true>(acc, w, x, b, len, t);
   if ((len & 127) && (full & (parts - 1)) == part) {
-    w.template load<TWO>(r0, r1, s0, s1, full);
-    block_w4<G, TWO, NTC, NT, false>(acc, w, x, full, len, t);
+    w.load(r0, r1, s0, s1, full);
+    block_w4<G, NTC, NT, false>(acc, w, x, full, len, t);
   }
 }
 
@@ -785,15 +782,10 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
                    (((uint32_t)row * spitch + k0 / GG * 2) & 15u);
           };
           const uint32_t s0 = scales_of(i0), s1 = scales_of(i1);
-          if (a.stage_rows == 8) {
-            if (NT > 1 && en.n <= 8)
-              multiply_w4<GG, false, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-            else multiply_w4<GG, false, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-          } else {
-            if (NT > 1 && en.n <= 8)
-              multiply_w4<GG, true, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-            else multiply_w4<GG, true, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-          }
+          if (NT > 1 && en.n <= 8)
+            multiply_w4<GG, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
+          else
+            multiply_w4<GG, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
         } else if (a.stage_rows == 8) {
           if (NT > 1 && en.n <= 8) multiply_bf16<false, 1, NT>(acc, r0, r1, x, len, t, part, parts);
           else multiply_bf16<false, NT, NT>(acc, r0, r1, x, len, t, part, parts);
@@ -1042,9 +1034,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
           return st + a.scale_off + i * a.scale_pitch + ((row * spitch + k0 / GG * 2) & 15u);
         };
         if (NT > 1 && en.n <= 8)
-          multiply_w4<GG, true, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+          multiply_w4<GG, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
         else
-          multiply_w4<GG, true, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+          multiply_w4<GG, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
       } else {
         if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, 0, 1);
         else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, 0, 1);
