@@ -50,8 +50,10 @@ void row_layout(StreamArgs& a, int group, int rows, int Kc) {
   a.ksteps = (a.K + Kc - 1) / Kc;
   a.row_copies = a.ksteps > 1;
   a.row_pitch = a.row_copies ? align_up(bytes, 128) + 64 : bytes;
+  a.span = 8;
+  a.span_shift = a.row_copies ? 0 : 64;  // (the pieces' pitch has the shift)
   a.scale_pitch = !group ? 0 : a.row_copies ? align_up(scale_bytes, 16) + 16 : scale_bytes;
-  a.scale_off = align_up(rows * a.row_pitch, 16);
+  a.scale_off = align_up(rows * a.row_pitch + (rows + 7) / 8 * a.span_shift, 16);
   a.x_pitch = align_up(Kc * 2, 128) + 64;
 }
 
@@ -61,9 +63,9 @@ bool plan(StreamArgs& a, int group, int mode, int room, int xstages_most) {
   auto stage = [&](int stage_rows, int Kc, int xstages) {
     row_layout(a, group, stage_rows, Kc);
     a.stage_rows = stage_rows;
-    a.half_rows = stage_rows / 2;
+    a.span = std::min(8, stage_rows / 2);
     a.tile_rows = mode == kGateUp ? stage_rows / 2 : stage_rows;
-    a.parts_off = align_up(a.scale_off + stage_rows * a.scale_pitch + (group ? 32 : 0), 128);
+    a.parts_off = align_up(a.scale_off + stage_rows * a.scale_pitch + (group ? 16 * ((stage_rows + 7) / 8) + 16 : 0), 128);
     a.stage_bytes = std::max(
         kLeastStage, a.parts_off + (parts_most(a.xrows) - 1) * 512 * token_tiles(a.xrows));
     a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
@@ -103,7 +105,7 @@ void fit_teams(StreamArgs& a) {
 bool plan_down(StreamArgs& a, int group, int rows, int Kc, int fixed, int copy, int least) {
   a.parts = (rows + 15) / 16;
   row_layout(a, group, rows, Kc);
-  a.x_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 32 : 0), 128);
+  a.x_off = align_up(a.scale_off + rows * a.scale_pitch + (group ? 16 * ((rows + 7) / 8) + 16 : 0), 128);
   a.stage_bytes = std::max(kLeastStage, a.x_off + align_up(a.xrows * a.x_pitch, 128));
   // as many teams as have a stage each, beside their sums
   for (a.teams = kBlockWarps / a.parts; a.teams >= 1; --a.teams) {

@@ -306,11 +306,17 @@ struct Cursor {
   }
 };
 
-// mma_16816 with a zero accumulator: d = a . b.
-MOL_DEV void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                            uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+// d += a . b as mma_16816, free to be scheduled among the loads around it; d = a . b.
+MOL_DEV void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+MOL_DEV void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -355,10 +361,10 @@ MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const 
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt)
-        mma_16816(acc[nt], a0[u].x, a1[u].x, a0[u].y, a1[u].y, v[u][nt].x, v[u][nt].y);
+        mma_add(acc[nt], a0[u].x, a1[u].x, a0[u].y, a1[u].y, v[u][nt].x, v[u][nt].y);
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt)
-        mma_16816(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0[u].z, a1[u].z, a0[u].w, a1[u].w, v[u][nt].z, v[u][nt].w);
+        mma_add(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0[u].z, a1[u].z, a0[u].w, a1[u].w, v[u][nt].z, v[u][nt].w);
     }
   }
   // what is left of the share, the last, partial block with it: inputs past len are zeros
@@ -371,8 +377,8 @@ MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const 
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt) {
       const uint4 v = in ? ld_s16(x[nt] + o) : zero;
-      mma_16816(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-      mma_16816(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+      mma_add(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+      mma_add(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
     }
   }
   if (kTwo) {
@@ -420,14 +426,22 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
                       int len, int t) {
   const uint32_t w0[4] = {w.a0.x, w.a0.y, w.a0.z, w.a0.w};
   const uint32_t w1[4] = {w.a1.x, w.a1.y, w.a1.z, w.a1.w};
-  float sum[NTC][4];
+  // the tokens' inputs of two words (64 inputs) at a time, all four with one tile: loads first
+  constexpr int kAhead = NTC == 1 ? 4 : NTC == 2 ? 2 : 1;
+  uint4 v[kAhead][NTC];
+  float sum[NTC][4], odd[4];  // one tile and one group: two accumulators, for shorter chains
+  constexpr bool kOdd = NTC == 1 && G == 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool in = FULL || b * 128 + i * 32 + t * 8 < len;  // inputs past len are zeros
-    uint4 v[NTC];
+    if (i % kAhead == 0) {
 #pragma unroll
-    for (int nt = 0; nt < NTC; ++nt)
-      v[nt] = in ? ld_s16(x[nt] + b * 256 + i * 64) : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < kAhead; ++u) {
+        const bool in = FULL || b * 128 + (i + u) * 32 + t * 8 < len;  // inputs past len are zeros
+#pragma unroll
+        for (int nt = 0; nt < NTC; ++nt)
+          v[u][nt] = in ? ld_s16(x[nt] + b * 256 + (i + u) * 64) : make_uint4(0, 0, 0, 0);
+      }
+    }
     uint32_t p0[4], p1[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -436,14 +450,19 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
     }
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt) {
-      if (i * 32 % G == 0)
-        mma_16816_zero(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
-      else
-        mma_16816(sum[nt], p0[0], p1[0], p0[1], p1[1], v[nt].x, v[nt].y);
+      const uint4& y = v[i % kAhead][nt];
+      if (kOdd && i == 1) {
+        mma_set(odd, p0[0], p1[0], p0[1], p1[1], y.x, y.y);
+        mma_add(odd, p0[2], p1[2], p0[3], p1[3], y.z, y.w);
+      } else if (kOdd && i == 3) {
+        mma_add(odd, p0[0], p1[0], p0[1], p1[1], y.x, y.y);
+        mma_add(odd, p0[2], p1[2], p0[3], p1[3], y.z, y.w);
+      } else {
+        if (i * 32 % G == 0) mma_set(sum[nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
+        else mma_add(sum[nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
+        mma_add(sum[nt], p0[2], p1[2], p0[3], p1[3], y.z, y.w);
+      }
     }
-#pragma unroll
-    for (int nt = 0; nt < NTC; ++nt)
-      mma_16816(sum[nt], p0[2], p1[2], p0[3], p1[3], v[nt].z, v[nt].w);
     if ((i + 1) * 32 % G == 0) {
       // a group wholly past len holds no weights: its scale may be anything
       const int grp = i * 32 / G;
@@ -451,6 +470,9 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
       const float g0 = has ? w.f0.get(grp) : 0.f, g1 = has ? w.f1.get(grp) : 0.f;
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt) {
+        if (kOdd)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[nt][j] += odd[j];
         acc[nt][0] = fmaf(g0, sum[nt][0], acc[nt][0]);
         acc[nt][1] = fmaf(g0, sum[nt][1], acc[nt][1]);
         acc[nt][2] = fmaf(g1, sum[nt][2], acc[nt][2]);
@@ -464,19 +486,14 @@ template <int G, int NTC, int NT>
 MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
                          const uint32_t (&x)[NT], int len, int t, int part, int parts) {
   const int full = len >> 7;
-  BlockW4<G> w;
-  int b = part;
-  if (b < full) w.load(r0, r1, s0, s1, b);
 #pragma unroll 1
-  for (; b + parts < full; b += 2 * parts) {  // a block's weights come while the other is multiplied
-    BlockW4<G> v;
-    v.load(r0, r1, s0, s1, b + parts);
+  for (int b = part; b < full; b += parts) {
+    BlockW4<G> w;
+    w.load(r0, r1, s0, s1, b);
     block_w4<G, NTC, NT, true>(acc, w, x, b, len, t);
-    if (b + 2 * parts < full) w.load(r0, r1, s0, s1, b + 2 * parts);
-    block_w4<G, NTC, NT, true>(acc, v, x, b + parts, len, t);
   }
-  if (b < full) block_w4<G, NTC, NT, true>(acc, w, x, b, len, t);
   if ((len & 127) && (full & (parts - 1)) == part) {
+    BlockW4<G> w;
     w.load(r0, r1, s0, s1, full);
     block_w4<G, NTC, NT, false>(acc, w, x, full, len, t);
   }
@@ -496,17 +513,27 @@ MOL_DEV void remote_store(uint32_t at, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p), "f"(v) : "memory");
 }
 
-// Adds column `col` of a tile (value h of rows g and g + 8) times its pair's weight into the sums.
-MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, uint32_t sums, const Entry& en,
-                      const float (&acc)[4], int h, int col, int row, int rows, int g) {
+// Adds column `col`'s values of rows `row` and row + 8 times its pair's weight into the sums.
+MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, uint32_t sums, const Entry& en, int col,
+                      int row, int rows, float v0, float v1) {
   if (col >= en.n) return;
   const int tok = l.pair(en.off + col) >> 16;
   const float w = ld_sf(l.weight + 4 * (en.off + col));
-  if (!MOL_CHECK(tok < a.num_tokens && row >= 0 && row + rows <= a.acc_stride, MOL_CHECK_SMEM, row))
-    return;
-  const uint32_t s = sums + 4 * (tok * a.acc_stride + row + g);
-  if (g < rows) st_sf(s, fmaf(w, h ? acc[1] : acc[0], ld_sf(s)));
-  if (g + 8 < rows) st_sf(s + 32, fmaf(w, h ? acc[3] : acc[2], ld_sf(s + 32)));
+  if (!MOL_CHECK(tok < a.num_tokens && rows <= a.acc_stride, MOL_CHECK_SMEM, tok)) return;
+  const uint32_t s = sums + 4 * (tok * a.acc_stride + row);
+  if (row < rows) st_sf(s, fmaf(w, v0, ld_sf(s)));
+  if (row + 8 < rows) st_sf(s + 32, fmaf(w, v1, ld_sf(s + 32)));
+}
+
+// Where row j of span q lies in a stage, and its scales. Spans of 8 rows (a half of 4 in tiles of 8)
+// are brought by a copy each, 64 bytes apart, and the lanes of odd g take the row of the odd span
+// first: the eight lanes of a shared-memory phase then read two rows that lie an odd multiple of 64
+// bytes apart (rows of a multiple of 128 bytes) and no bank twice.
+MOL_DEV uint32_t row_at(const StreamArgs& a, int q, int j) {
+  return (q * a.span + j) * a.row_pitch + q * a.span_shift;
+}
+MOL_DEV uint32_t scale_at(const StreamArgs& a, int q, int j) {
+  return a.scale_off + (q * a.span + j) * a.scale_pitch + q * 16;
 }
 
 // The part'th of `parts` nearly equal shares of [0, all).
@@ -688,19 +715,28 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       uint64_t* bar = &my_full[slot];
       const int rows = c.rows(a);
       const int k0 = c.ks * a.Kc, len = min(a.Kc, a.K - k0);
-      const int bytes = kW4 ? (len + 127) / 128 * 64 : len * 2;  // of a row
-      const int copies = a.row_copies ? rows : min(rows, 1);      // of a half
-      const int per = a.row_copies ? 1 : rows;                    // rows of a copy
-      const int total = MODE == kGateUp ? 2 * copies : copies;
-      const uint32_t size = a.row_copies ? bytes : per * pitch;   // contiguous: the rows are whole
-      // lanes take the copies in turn (at most 16 of them); lane 0 announces all their bytes first
-      const int h = lane >= copies;
-      const int r = (h ? lane - copies : lane) * per;
-      const int row = entry_of(c.entry).e * rows_per_expert + c.row + c.skip() + (h ? a.N : 0) + r;
-      const bool has = lane < total && MOL_CHECK(row + per <= a.E * rows_per_expert,
-                                                 MOL_CHECK_WEIGHT_ROW, row);
+      // a copy for each span (whole rows), or for each row (pieces); lanes take them in turn (at most
+      // 16), lane 0 announces all their bytes first
+      int q, j, per;
+      bool has;
+      if (MODE == kGateUp) {  // span 0: gate rows, span 1: up rows
+        per = a.row_copies ? 1 : rows;
+        const int copies = a.row_copies ? rows : min(rows, 1);
+        q = lane >= copies;
+        j = lane - q * copies;
+        has = lane < 2 * copies;
+      } else {
+        q = a.row_copies ? lane >> 3 : lane;
+        j = a.row_copies ? lane & 7 : 0;
+        per = a.row_copies ? 1 : min(8, rows - 8 * q);
+        has = a.row_copies ? lane < rows : 8 * lane < rows;
+      }
+      const int row = entry_of(c.entry).e * rows_per_expert + c.row + c.skip() +
+                      (MODE == kGateUp ? q * a.N : q * 8) + j;
+      has = has && MOL_CHECK(row + per <= a.E * rows_per_expert, MOL_CHECK_WEIGHT_ROW, row);
+      const uint32_t size = a.row_copies ? (kW4 ? (len + 127) / 128 * 64 : len * 2) : per * pitch;
       uint32_t mine = has ? size : 0;
-      const uint32_t sd = dst + a.scale_off + (h * a.half_rows + r) * a.scale_pitch + h * 16;
+      const uint32_t sd = dst + scale_at(a, q, j);
       const int slen = !kW4 ? 0 : a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
       const int64_t at = kW4 ? (int64_t)row * spitch + k0 / GG * 2 : 0;
       const ScaleRange sr(at, slen, stotal);
@@ -713,8 +749,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       if (lane == 0) mbar_arrive_expect_tx(bar, mine);
       __syncwarp();
       if (has) {
-        bulk_copy(dst + (h * a.half_rows + r) * a.row_pitch,
-                  a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size, bar);
+        bulk_copy(dst + row_at(a, q, j), a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size,
+                  bar);
         if (kW4 && sr.bytes)
           bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes, bar);
       }
@@ -760,28 +796,30 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       const uint32_t st = my_ring + slot * a.stage_bytes;
       if (rows > 0) {
         const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
-        // the lane's rows; rows past the tile's last read that row again, their products are dropped
-        int i0, i1;
-        if (MODE == kGateUp) {
-          i0 = min(a.half_rows == 8 ? g : g & 3, rows - 1);
-          i1 = a.half_rows + i0;
-          if (a.half_rows != 8 && g >= 4) i0 = i1;  // 4 gate rows, then 4 up rows
+        // the lane's rows, of span 0 and 1 (gate and up row of one output; gate_up tiles of 8 rows:
+        // one row, of span g & 1); rows past the tile's last read that row again, their products are
+        // dropped
+        const int n0 = MODE == kGateUp ? rows : min(rows, 8), n1 = MODE == kGateUp ? rows : rows - 8;
+        const int q0 = !kW4 && a.stage_rows == 8 ? 0 : g & 1;  // span of the first row
+        int j0 = min(g, (q0 ? n1 : n0) - 1), j1 = min(g, (q0 ? n0 : n1) - 1);
+        uint32_t r0, r1;
+        if (!kW4 && a.stage_rows == 8) {
+          r0 = r1 = st + row_at(a, g & 1, min(g >> 1, rows - 1)) + t * 16;
         } else {
-          i0 = min(g, rows - 1);
-          i1 = min(g + 8, rows - 1);
+          if (j0 < 0) j0 = 0;  // (a tile of at most 8 rows has no second span: anything that is there)
+          if (j1 < 0) j1 = 0;
+          r0 = st + row_at(a, q0, j0) + t * 16;
+          r1 = st + row_at(a, q0 ^ 1, j1) + t * 16;
         }
-        const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
         if constexpr (kW4) {
           const int first = en.e * rows_per_expert + row0;
-          // the copy that brought a row's scales began at 16 bytes' boundary at or before them, or
-          // before those of its half's first row
-          auto scales_of = [&](int i) {
-            const int h = MODE == kGateUp && i >= a.half_rows;
-            const int row = first + (h ? a.N : 0) + (a.row_copies ? i - h * a.half_rows : 0);
-            return st + a.scale_off + i * a.scale_pitch + h * 16 +
-                   (((uint32_t)row * spitch + k0 / GG * 2) & 15u);
+          // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
+          // before those of its span's first row
+          auto scales_of = [&](int q, int j) {
+            const uint32_t from = first + (MODE == kGateUp ? q * a.N : q * 8) + (a.row_copies ? j : 0);
+            return st + scale_at(a, q, j) + ((from * spitch + k0 / GG * 2) & 15u);
           };
-          const uint32_t s0 = scales_of(i0), s1 = scales_of(i1);
+          const uint32_t s0 = scales_of(q0, j0), s1 = scales_of(q0 ^ 1, j1);
           if (NT > 1 && en.n <= 8)
             multiply_w4<GG, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
           else
@@ -843,18 +881,24 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
       ++want;
       if (!ends || part > 0 || rows == 0) continue;
 
-      // the tile's values: column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h)
+      // the tile's values: column 2t + h of each token tile; the lane's row of span 0 in values h and
+      // that of span 1 in values 2 + h, the other way round where g is odd
+      const bool eight = !kW4 && a.stage_rows == 8;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = nt * 8 + 2 * t + h;
-          float v0 = acc[nt][h], v1 = acc[nt][2 + h];
+          float v0 = g & 1 ? acc[nt][2 + h] : acc[nt][h], v1 = g & 1 ? acc[nt][h] : acc[nt][2 + h];
           if (MODE == kGateUp) {
-            if (a.half_rows != 8) v1 = __shfl_down_sync(0xffffffffu, v0, 16);
-            if (col >= en.n || g >= rows) continue;
+            if (eight) {
+              v0 = acc[nt][h];
+              v1 = __shfl_down_sync(0xffffffffu, v0, 4);
+            }
+            const int j = eight ? g >> 1 : g;
+            if (col >= en.n || j >= rows || (eight && (g & 1))) continue;
             const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
-            const int n = row0 + g;
+            const int n = row0 + j;
             if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
             if (a.delta) {
               const bf16* dl = a.delta + pair * a.delta_stride + n;
@@ -956,35 +1000,42 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       uint64_t* bar = &my_full[slot];
       const int k0 = ks * a.Kc, len = min(a.Kc, a.K - k0);
       const int row0 = en.e * a.N + first_row;
-      const int copies = a.row_copies ? rows : 1, per = a.row_copies ? 1 : rows;
-      const uint32_t size = a.row_copies ? (kW4 ? (len + 127) / 128 * 64 : len * 2) : per * pitch;
-      const int slen = kW4 ? (a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch) : 0;
+      // a copy for each span of 8 rows, or for each row
+      const int copies = a.row_copies ? rows : (rows + 7) / 8;
+      auto each = [&](auto f) {
+        for (int c = lane; c < copies; c += 32) {
+          const int q = a.row_copies ? c >> 3 : c, j = a.row_copies ? c & 7 : 0;
+          const int per = a.row_copies ? 1 : min(8, rows - 8 * q);
+          const int row = row0 + 8 * q + j;
+          if (!MOL_CHECK(row + per <= a.E * a.N, MOL_CHECK_WEIGHT_ROW, row)) continue;
+          const uint32_t size = a.row_copies ? (kW4 ? (len + 127) / 128 * 64 : len * 2) : per * pitch;
+          const uint32_t slen = !kW4 ? 0 : a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
+          f(q, j, row, size, slen, kW4 ? (int64_t)row * spitch + k0 / GG * 2 : 0);
+        }
+      };
       uint32_t bytes = 0;
-      for (int r = lane; r < copies; r += 32) {
+      each([&](int q, int j, int row, uint32_t size, uint32_t slen, int64_t at) {
         bytes += size;
         if (kW4) {
-          const int64_t at = (int64_t)(row0 + r) * spitch + k0 / GG * 2;
           const ScaleRange sr(at, slen, stotal);
           bytes += sr.bytes;
-          if (sr.tail) sr.copy_tail(a.scales, dst + a.scale_off + r * a.scale_pitch, at, slen);
+          if (sr.tail) sr.copy_tail(a.scales, dst + scale_at(a, q, j), at, slen);
         }
-      }
+      });
       bytes = __reduce_add_sync(0xffffffffu, bytes);
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes + en.n * len * 2);
       __syncwarp();
-      for (int r = lane; r < copies; r += 32) {
-        const int row = row0 + r;
-        if (!MOL_CHECK(row + per <= a.E * a.N, MOL_CHECK_WEIGHT_ROW, row)) continue;
-        bulk_copy(dst + r * a.row_pitch, a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size,
+      each([&](int q, int j, int row, uint32_t size, uint32_t slen, int64_t at) {
+        bulk_copy(dst + row_at(a, q, j), a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size,
                   bar);
         if (kW4) {
-          const ScaleRange sr((int64_t)row * spitch + k0 / GG * 2, slen, stotal);
+          const ScaleRange sr(at, slen, stotal);
           if (sr.bytes)
-            bulk_copy(dst + a.scale_off + r * a.scale_pitch,
-                      reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes, bar);
+            bulk_copy(dst + scale_at(a, q, j), reinterpret_cast<const char*>(a.scales) + sr.from,
+                      sr.bytes, bar);
         }
-      }
+      });
     };
     auto put_x = [&](int unit, int slot) {
       const int entry = unit / a.ksteps, ks = unit - entry * a.ksteps;
@@ -1007,6 +1058,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       for (int i = 0; i < filled; ++i) put_x(lo + team + i * a.teams, i);
     }
     const uint32_t sums = all_sums + team * copy_bytes;
+    const int my_row = part * 16;
     int slot = 0, phase = 0;
     for (int unit = lo + team; unit < hi; unit += a.teams) {
       fault = !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
@@ -1018,20 +1070,22 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
       float acc[NT][4];
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-      // the lane's rows; rows past the block's last read that row again, their products are dropped
-      const int i0 = min(part * 16 + g, rows - 1), i1 = min(part * 16 + g + 8, rows - 1);
+      // the lane's rows of the warp's two spans, that of the odd span first where g is odd; rows past
+      // the block's last read that row again, their products are dropped
+      const int i0 = min(my_row + (g & 1) * 8 + g, rows - 1);
+      const int i1 = min(my_row + (g & 1 ? 0 : 8) + g, rows - 1);
       uint32_t x[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         x[nt] = st + a.x_off + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
-      const uint32_t r0 = st + i0 * a.row_pitch + t * 16, r1 = st + i1 * a.row_pitch + t * 16;
+      const uint32_t r0 = st + row_at(a, i0 >> 3, i0 & 7) + t * 16;
+      const uint32_t r1 = st + row_at(a, i1 >> 3, i1 & 7) + t * 16;
       if constexpr (kW4) {
-        const int first = en.e * a.N + first_row;
         // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
-        // before those of the first row
+        // before those of its span's first row
         auto scales_of = [&](int i) {
-          const uint32_t row = first + (a.row_copies ? i : 0);
-          return st + a.scale_off + i * a.scale_pitch + ((row * spitch + k0 / GG * 2) & 15u);
+          const uint32_t from = en.e * a.N + first_row + (a.row_copies ? i : i & ~7);
+          return st + scale_at(a, i >> 3, i & 7) + ((from * spitch + k0 / GG * 2) & 15u);
         };
         if (NT > 1 && en.n <= 8)
           multiply_w4<GG, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
@@ -1063,16 +1117,17 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
         slot = 0;
         phase ^= 1;
       }
-      // column 2t + h of each token tile, rows g (values h) and g + 8 (2 + h); columns of one step
-      // may hold the same token where a token lists its expert twice: they take turns
+      // column 2t + h of each token tile: rows my_row + g and + 8 + g, in values h and 2 + h, the
+      // other way round where g is odd. Columns of one step may hold the same token where a token
+      // lists its expert twice: they take turns.
       for (int turn = 0; turn < (lists.repeated ? 4 : 1); ++turn) {
         if (!lists.repeated || t == turn) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            add_sums(a, lists, sums, en, acc[nt], 0, nt * 8 + 2 * t, part * 16, rows - part * 16, g);
-            add_sums(a, lists, sums, en, acc[nt], 1, nt * 8 + 2 * t + 1, part * 16, rows - part * 16,
-                     g);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              add_sums(a, lists, sums, en, nt * 8 + 2 * t + h, my_row + g, rows,
+                       g & 1 ? acc[nt][2 + h] : acc[nt][h], g & 1 ? acc[nt][h] : acc[nt][2 + h]);
         }
         __syncwarp();
       }
