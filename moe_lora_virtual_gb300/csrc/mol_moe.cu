@@ -2,6 +2,7 @@
 // kernel).
 
 #include <algorithm>
+#include <cmath>
 
 #include "mol_block.h"
 #include "mol_internal.h"
@@ -34,8 +35,6 @@ int entry_tokens(int num_tokens, int pairs, int experts) {
   return n;
 }
 
-// A team's partial sums cost 512 bytes a stage for each further warp and tile of 8 tokens.
-int parts_most(int xrows) { return xrows <= 16 ? 4 : 2; }
 int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : xrows <= 32 ? 4 : 8; }
 
 // The ring is the lists' scratch first, 20 KB at most: sixteen stages of this size hold it, and rings
@@ -57,47 +56,56 @@ void row_layout(StreamArgs& a, int group, int rows, int Kc) {
   a.x_pitch = align_up(Kc * 2, 128) + 64;
 }
 
-// gate_up, linear: chooses the stage and the rings for a block that has `room` bytes for them.
-// xstages_most: token slots of use when they hold whole rows. False when nothing fits.
-bool plan(StreamArgs& a, int group, int mode, int room, int xstages_most) {
-  auto stage = [&](int stage_rows, int Kc, int xstages) {
-    row_layout(a, group, stage_rows, Kc);
-    a.stage_rows = stage_rows;
-    a.span = std::min(8, stage_rows / 2);
-    a.tile_rows = mode == kGateUp ? stage_rows / 2 : stage_rows;
-    a.parts_off = align_up(a.scale_off + stage_rows * a.scale_pitch + (group ? 16 * ((stage_rows + 7) / 8) + 16 : 0), 128);
-    a.stage_bytes = std::max(
-        kLeastStage, a.parts_off + (parts_most(a.xrows) - 1) * 512 * token_tiles(a.xrows));
-    a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
-    a.xstages = xstages;
-    a.stages = std::min(kMaxStages, (room - xstages * a.xslot_bytes) / a.stage_bytes);
-    return a.stages;
-  };
-  // Whole rows. 16 rows a tile use the tensor instruction's M side, and each read of the tokens,
-  // fully; tiles of 8 (bf16) leave room for more stages where rows are long. A second token slot lets
-  // the next expert's tokens come while the last one's stages are consumed.
-  for (int x = xstages_most; x >= 1; --x)
-    if (stage(16, a.K, x) >= (x > 1 ? 6 : 4)) return true;
-  for (int x = xstages_most; x >= 1 && !group; --x)
-    if (stage(8, a.K, x) >= (x > 1 ? 4 : 3)) return true;
-  if (stage(16, a.K, 1) >= 2) return true;
-  // pieces of rows, the longest that leave four stages
-  for (int Kc = 2048; Kc > 256; Kc -= 256)
-    if (Kc < a.K && stage(group || Kc <= 1024 ? 16 : 8, Kc, 2) >= 4) return true;
-  return stage(group ? 16 : 8, std::min(256, a.K), 2) >= 2;
+// gate_up, linear: the token slots and the teams of a block that has `room` bytes beside its rings,
+// when the blocks share `entries` entries. False when nothing fits.
+// Teams: the warps of a team split the inputs of a tile, so more parts fill all warps where a block has
+// few tiles, and leave less to wait for at the end; against that each tile costs its warps half a
+// chunk's time, or two for each token tile where their sums are to be added. Taken is the
+// least of that model, with one more tile a warp for the end: measured, an output head of 49 tiles a
+// block takes 29.5 us with one part and 36 with four, a linear of one tile a block 5.5 us with one
+// and 4.1 with four.
+bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
+  const int inputs = group ? 256 : 64, nt = token_tiles(a.xrows);
+  a.tile_rows = mode == kGateUp ? 8 : 16;
+  const int64_t tiles = (int64_t)entries * ((a.N + a.tile_rows - 1) / a.tile_rows);
+  const double block_tiles = (double)tiles / grid;
+  StreamArgs best = {};
+  double least = 0;
+  for (int parts = 1; parts <= consumer_warps(nt); ++parts) {
+    a.parts = parts;
+    a.teams = consumer_warps(nt) / parts;
+    const int left = room - a.teams * (parts - 1) * nt * 512;
+    auto slots = [&](int Kc, int n) {
+      a.Kc = Kc;
+      a.ksteps = (a.K + Kc - 1) / Kc;
+      a.x_pitch = align_up(Kc * 2, 128) + 64;
+      a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
+      a.xstages = n;
+      return n * a.xslot_bytes <= left;
+    };
+    // whole rows; a second token slot lets the next expert's tokens come while the last one's weights
+    // are consumed. Else pieces.
+    bool fits = (entries > 1 && slots(a.K, 2)) || slots(a.K, 1);
+    for (int Kc = 2048; Kc >= 256 && !fits; Kc -= 256) fits = Kc < a.K && slots(Kc, 2);
+    fits = fits || slots(std::min(256, a.K), 1);
+    if (!fits) continue;
+    const int per = (std::min(a.Kc, a.K) + inputs - 1) / inputs;
+    const double one = a.ksteps * ((per + parts - 1) / parts) + (parts > 1 ? 2 * nt - 0.5 : 0.5);
+    const double rounds = block_tiles / a.teams;
+    const double cost = (std::max(1.0, (rounds + std::ceil(rounds)) / 2) + 1) * one;
+    if (best.parts && cost > least) continue;
+    least = cost;
+    best = a;
+  }
+  if (!best.parts) return false;
+  a = best;
+  a.entry_rows = align_up(a.N, a.tile_rows * (a.ksteps > 1 ? a.teams : 1));
+  return true;
 }
 
-// gate_up, linear: as many teams as there are stages, or fewer that share them evenly without leaving
-// more unused; the warps that are left join them.
-void fit_teams(StreamArgs& a) {
-  const int most = std::min(kBlockWarps - 1, a.stages);
-  a.teams = most;
-  for (int w = most; w > most / 2; --w)
-    if (a.stages / w * w > a.stages / a.teams * a.teams) a.teams = w;
-  a.stages = a.stages / a.teams * a.teams;
-  a.parts = 1;
-  while (2 * a.parts <= parts_most(a.xrows) && 2 * a.parts * a.teams <= kBlockWarps - 1) a.parts *= 2;
-  a.entry_rows = align_up(a.N, a.tile_rows * (a.ksteps > 1 ? a.teams : 1));
+int stream_smem(const StreamArgs& a, int group) {
+  return consumer_warps(token_tiles(a.xrows)) * kChunks * chunk_bytes(group) + a.xstages * a.xslot_bytes +
+         a.teams * (a.parts - 1) * token_tiles(a.xrows) * 512;
 }
 
 // down: the stage and the teams of a block of `rows` output rows, with `fixed` bytes of lists and
@@ -147,9 +155,10 @@ cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_strid
                                int64_t delta_stride, void* act, cudaStream_t stream) {
   StreamArgs a = common_args(s, x, x_stride, topk_ids, w, delta, delta_stride, act, s.inter);
   a.N = s.inter;
-  if (!plan(a, w.group, kGateUp, kSmem - list_bytes(s), 2)) return cudaErrorInvalidConfiguration;
-  fit_teams(a);
-  const size_t smem = (size_t)a.stages * a.stage_bytes + a.xstages * a.xslot_bytes + list_bytes(s);
+  const int entries = std::min(s.num_tokens * s.topk, s.num_experts);
+  if (!plan(a, w.group, kGateUp, kSmem - list_bytes(s) - stream_smem(a, w.group), entries, g_sm_count))
+    return cudaErrorInvalidConfiguration;
+  const size_t smem = stream_smem(a, w.group) + list_bytes(s);
   return launch_by_group(w.group, a, kGateUp, g_sm_count, smem, stream);
 }
 
@@ -216,10 +225,10 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   StreamArgs a = common_args(s, x, x_stride, nullptr, w, nullptr, 0, out, out_stride);
   a.N = N;
   a.xrows = num_tokens;
-  if (!plan(a, w.group, kLinear, kSmem, 1)) return cudaErrorInvalidConfiguration;
-  fit_teams(a);
-  const size_t smem = (size_t)a.stages * a.stage_bytes + a.xstages * a.xslot_bytes;
-  return launch_by_group(w.group, a, kLinear, std::min((N + 7) / 8, g_sm_count), smem, stream);
+  const int grid = std::min((N + 15) / 16, g_sm_count);
+  if (!plan(a, w.group, kLinear, kSmem - stream_smem(a, w.group), 1, grid))
+    return cudaErrorInvalidConfiguration;
+  return launch_by_group(w.group, a, kLinear, grid, stream_smem(a, w.group), stream);
 }
 
 cudaError_t prepare_moe_kernels() {

@@ -4,19 +4,20 @@
 // Mathematics. Both halves of the experts and the linear are products w . x of weight rows with a
 // few activation rows, every weight used by the tokens of its expert only (a few), so the time is
 // that of reading the taken experts' weights once: 2 bytes (or about half a byte) for 2 n
-// operations at n tokens an expert. One streaming loop serves all three:
+// operations at n tokens an expert; 4-bit weights take about 120 instructions a KB to become bf16,
+// which costs more than to read them. Two streaming loops:
 //
-// - A block owns tiles of 16 (or 8) whole weight rows. A tile belongs to a team of one to four
-//   consumer warps, which bring it themselves: each team has a small ring of stages of its own (a
-//   tile, or a piece of it along K where rows or tokens are too long for shared memory), and its
-//   first warp asks for the next stage by bulk copy as soon as the team is through with one. Rows of
-//   a tile are neighbours in memory, so a copy is kilobytes long. No team waits for another, and no
-//   single warp issues a block's copies (one warp that did held the stream at 2 to 4 TB/s).
-// - The tokens' rows of an expert come the same way: gate_up and linear: into slots that all teams
-//   read, from a warp of its own, once for all the block's tiles of that expert; down: with the
-//   weights, into the stage.
-// - The warps of a team split the tile: its inputs (gate_up, linear; the first adds the others' fp32
-//   sums, in their order, to its own) or its rows (down).
+// - gate_up and linear: a block owns tiles of 16 whole weight rows (8 gate and 8 up rows) and a tile
+//   belongs to a team of warps, which split its inputs; each warp streams its share of tile after
+//   tile through a ring of its own. A lane copies (cp.async) the very 16 bytes that it will read, so
+//   nobody signals anybody: a chunk of 2 KB has landed when the lane's own copies have, and three are
+//   in flight a warp, 96 KB a block. (Stages of whole tiles, brought by bulk copies, kept shared
+//   memory full of tiles that were being multiplied: an output head took 35 us instead of 29.5.) The
+//   tokens' rows come by bulk copies into slots that all warps read, from a warp of its own, once for
+//   all the block's tiles of an expert.
+// - down: a block or cluster owns rows of every expert, and a stage holds a unit's weights and
+//   activation rows (bulk copies; rows of a tile are neighbours in memory). A team's first warp asks
+//   for the next stage as soon as the team is through with one; its warps have 16 rows each.
 // - The product is mma.sync m16n8k16: weight rows are the M side, tokens the N side (8 a tile), so
 //   a single token wastes tensor work and no bandwidth. The contraction's order is free as long as
 //   both sides agree: each lane takes 8 neighbouring inputs of its row in one 16-byte shared-memory
@@ -284,7 +285,7 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
 // share [lo, hi) of the list of output rows (row pairs), in which every entry takes whole tiles; the
 // team has every teams-th tile.
 struct Cursor {
-  int pos, hi, lo;     // first position of the tile in the list, of the share's end and start
+  int pos, hi;         // first position of the tile in the list, end of the share
   int entry, row, ks;  // row: first row of the tile
   bool valid;
 
@@ -298,11 +299,6 @@ struct Cursor {
       ++entry;
     }
     valid = pos < hi;
-  }
-  // the share's rows in the tile: [skip, skip + rows) of its tile_rows
-  MOL_DEV int skip() const { return max(0, lo - pos); }
-  MOL_DEV int rows(const StreamArgs& a) const {
-    return max(0, min(min(a.tile_rows, a.N - row), hi - pos) - skip());
   }
 };
 
@@ -575,34 +571,47 @@ struct ScaleRange {
   }
 };
 
+// Asynchronous copies of a lane, complete in the order of its groups. The first reads `bytes` of the 16
+// (0 or 16) and fills the rest with zeros.
+MOL_DEV void copy16(uint32_t dst, const char* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+template <int BYTES>
+MOL_DEV void copy_small(uint32_t dst, const char* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+
 template <int G, int MODE, int NT>
-__global__ void __launch_bounds__(kBlockWarps * 32, 1)
+__global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs a) {
   constexpr bool kW4 = G != 0;
   constexpr int GG = kW4 ? G : 32;  // (a group for code that bf16 does not reach)
+  constexpr int kInputs = kW4 ? 256 : 64;  // of a chunk
+  constexpr int kChunk = chunk_bytes(G);
   extern __shared__ __align__(128) char smem[];
-  // a stage has landed; its other warps are through with it; a token slot has landed, is free
-  __shared__ uint64_t wfull[kMaxStages], pfull[kMaxStages], xfull[kMaxSlots], xempty[kMaxSlots];
+  __shared__ uint64_t xfull[2], xempty[2];  // a token slot has landed, is free
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int numel = a.num_tokens * a.topk;
   const int consumers = a.teams * a.parts;
   const int rows_per_expert = MODE == kGateUp ? 2 * a.N : a.N;
 
-  // shared memory: stages | token slots | lists
-  const uint32_t ring = smem_u32(smem);
-  const uint32_t xslots = ring + a.stages * a.stage_bytes;
+  // shared memory: rings | token slots | sums of a team's warps | lists
+  const uint32_t rings = smem_u32(smem);
+  const uint32_t xslots = rings + consumer_warps(NT) * kChunks * kChunk;
+  const uint32_t sums = xslots + a.xstages * a.xslot_bytes;
   Lists lists;
-  lists.entry = xslots + a.xstages * a.xslot_bytes;
+  lists.entry = sums + a.teams * (a.parts - 1) * NT * 512;
   lists.order = lists.entry + (MODE == kLinear ? 0 : numel * 8);
   lists.weight = 0;
   lists.count = 1;
   lists.repeated = false;
 
-  if (warp == (int)(blockDim.x >> 5) - 1) {
-    for (int s = lane; s < a.stages; s += 32) {
-      mbar_init(&wfull[s], 1);
-      mbar_init(&pfull[s], max(1, a.parts - 1));
-    }
+  if (warp == consumer_warps(NT)) {
     for (int s = lane; s < a.xstages; s += 32) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], consumers);
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
   pdl_launch_dependents();
   if (MODE != kLinear) {
     build_lists(a, lists, smem, false);
-    // the lists' scratch becomes the ring: ordinary accesses before the copies
+    // the lists' scratch becomes rings and token slots: ordinary accesses before the copies
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   auto entry_of = [&](int i) {
@@ -621,28 +630,27 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
     return lists.get(i);
   };
 
-  // this block's share
-  // whole tiles' pieces: groups of a tile for each team, which share the tokens' pieces
-  const int step = a.ksteps > 1 ? a.teams * a.tile_rows : 1;
+  // this block's share: whole tiles, in pieces: groups of a tile for each team, which share the
+  // tokens' pieces
+  const bool whole = a.ksteps == 1;
+  const int step = a.tile_rows * (whole ? 1 : a.teams);
   int lo, hi;
   share(lists.count * (a.entry_rows / step), gridDim.x, blockIdx.x, lo, hi);
   lo *= step;
   hi *= step;
   // Token slots in the order of their use: whole rows: one for each entry of the share; pieces: one
   // for each k step of each group of tiles.
-  const bool whole = a.ksteps == 1;
-  const int tile0 = lo / a.tile_rows * a.tile_rows;  // the first tile's position
-  const int entry0 = tile0 / a.entry_rows;
+  const int entry0 = lo / a.entry_rows;
   const int slots = lo >= hi ? 0
                     : whole  ? (hi - 1) / a.entry_rows - entry0 + 1
-                             : (hi - lo) / (a.teams * a.tile_rows) * a.ksteps;
+                             : (hi - lo) / step * a.ksteps;
   __syncthreads();
   const unsigned long long limit = g_moe_wait_limit_ns;
   bool fault = false;
 
-  if (warp >= consumers) {
+  if (warp == consumer_warps(NT)) {
     // ---- the tokens' rows ----
-    if (warp == consumers && !(g_moe_test_stall & 1)) {
+    if (!(g_moe_test_stall & 1)) {
       int entry = entry0, ks = 0;
       int left = a.entry_rows - (lo - entry0 * a.entry_rows);  // pieces: rows of the entry to come
       int i = 0, s = 0, use = 0;
@@ -657,10 +665,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         __syncwarp();
         for (int j = lane; j < en.n; j += 32) {
           int row = j;
-          if (MODE != kLinear) {
-            const uint32_t p = lists.pair(en.off + j);
-            row = p >> 16;
-          }
+          if (MODE != kLinear) row = lists.pair(en.off + j) >> 16;
           if (!MOL_CHECK(row < a.num_tokens, MOL_CHECK_ROW, row)) row = 0;
           bulk_copy(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
                     &xfull[s]);
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         }
         if (++ks == a.ksteps) {
           ks = 0;
-          if (!whole) left -= a.teams * a.tile_rows;
+          if (!whole) left -= step;
           if (whole || left == 0) {
             left = a.entry_rows;
             ++entry;
@@ -684,18 +689,16 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         for (int q = max(0, i - a.xstages); q < i; ++q)
           (void)mbar_wait(&xfull[q % a.xstages], (q / a.xstages) & 1, kWaitPolls, limit);
     }
-  } else if (slots > 0) {
+  } else if (slots > 0 && warp < consumers) {
     // ---- consumers ----
     const int g = lane >> 2, t = lane & 3;
-    const int part = warp / a.teams, team = warp - part * a.teams, parts = a.parts;
-    const int depth = a.stages / a.teams;  // stages of the team's ring
-    const uint32_t my_ring = ring + team * depth * a.stage_bytes;
-    uint64_t* my_full = wfull + team * depth;
-    uint64_t* my_pfull = pfull + team * depth;
+    // (a team's warps are neighbours, so that they run on different sub-partitions)
+    const int parts = a.parts, team = warp / parts, part = warp - team * parts;
+    const int64_t spitch = kW4 ? w4_padded(a.K) / GG * 2 : 0;
+    const int64_t pitch = kW4 ? w4_padded(a.K) / 2 : a.K * 2;
     Cursor cur;
     cur.hi = hi;
-    cur.lo = lo;
-    cur.pos = tile0 + team * a.tile_rows;
+    cur.pos = lo + team * a.tile_rows;
     cur.entry = entry0;
     cur.row = cur.pos - entry0 * a.entry_rows;
     while (cur.row >= a.entry_rows) {
@@ -704,66 +707,85 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
     }
     cur.ks = 0;
     cur.valid = cur.pos < hi;
-    const bool go = !(g_moe_test_stall & 1);
-    const int spitch = kW4 ? w4_padded(a.K) / GG * 2 : 0;
-    const int pitch = kW4 ? w4_padded(a.K) / 2 : a.K * 2;
-    const int64_t stotal = kW4 ? (int64_t)a.E * rows_per_expert * spitch : 0;
+    // chunks of a tile's step; none in a tile that only fills up a group
+    auto chunks_of = [&](const Cursor& c) {
+      return c.row >= a.N ? 0 : (min(a.Kc, a.K - c.ks * a.Kc) + kInputs - 1) / kInputs;
+    };
 
-    // Asks for the stage at c: the first warp of the team.
-    auto put = [&](const Cursor& c, int slot) {
-      const uint32_t dst = my_ring + slot * a.stage_bytes;
-      uint64_t* bar = &my_full[slot];
-      const int rows = c.rows(a);
-      const int k0 = c.ks * a.Kc, len = min(a.Kc, a.K - k0);
-      // a copy for each span (whole rows), or for each row (pieces); lanes take them in turn (at most
-      // 16), lane 0 announces all their bytes first
-      int q, j, per;
-      bool has;
-      if (MODE == kGateUp) {  // span 0: gate rows, span 1: up rows
-        per = a.row_copies ? 1 : rows;
-        const int copies = a.row_copies ? rows : min(rows, 1);
-        q = lane >= copies;
-        j = lane - q * copies;
-        has = lane < 2 * copies;
+    // The warp's weights, chunk after chunk of its tiles, asked for kChunks - 1 ahead of their use.
+    // Every lane copies what it reads itself (its rows' 16 bytes of each block), so a chunk has
+    // landed when the lane's own copies have; scales: a lane for each row.
+    const uint32_t ring = rings + warp * kChunks * kChunk;
+    Cursor ahead = cur;
+    int next = part, count = 0;  // chunk of ahead's step, how many it has
+    const char *w0 = nullptr, *w1 = nullptr, *ws = nullptr;
+    int left = 0;  // bytes of the step's row from the lane's place on (bf16)
+    const int64_t tile_bytes = a.teams * a.tile_rows * pitch;
+    const int tile_scales = a.teams * a.tile_rows * (int)spitch;
+    auto aim = [&]() {
+      const int rows = min(a.tile_rows, a.N - ahead.row), k0 = ahead.ks * a.Kc;
+      const int64_t first = (int64_t)entry_of(ahead.entry).e * rows_per_expert + ahead.row;
+      // rows past the tile's last: that row again
+      int64_t r0 = first + min(g, rows - 1);
+      int64_t r1 = MODE == kGateUp ? r0 + a.N : first + min(g + 8, rows - 1);
+      if (!MOL_CHECK(r1 < (int64_t)a.E * rows_per_expert, MOL_CHECK_WEIGHT_ROW, r1)) r0 = r1 = 0;
+      const int64_t o = (kW4 ? k0 / 2 : k0 * 2) + t * 16;
+      w0 = a.w + r0 * pitch + o;
+      w1 = a.w + r1 * pitch + o;
+      if (kW4) ws = reinterpret_cast<const char*>(a.scales) + (t & 1 ? r1 : r0) * spitch + k0 / GG * 2;
+      else left = min(a.Kc, a.K - k0) * 2 - t * 16;
+    };
+    // the next step that has chunks for this warp
+    auto advance = [&]() {
+      const int entry = ahead.entry, ks = ahead.ks, pos = ahead.pos;
+      do {
+        ahead.next(a);
+        next = part;
+      } while (ahead.valid && next >= (count = chunks_of(ahead)));
+      if (!ahead.valid) return;
+      if (whole && ahead.entry == entry && ahead.row + a.tile_rows <= a.N) {
+        w0 += tile_bytes;
+        w1 += tile_bytes;
+        if (kW4) ws += tile_scales;
+      } else if (ahead.pos == pos) {
+        const int k = (ahead.ks - ks) * a.Kc;
+        w0 += kW4 ? k / 2 : k * 2;
+        w1 += kW4 ? k / 2 : k * 2;
+        if (kW4) ws += k / GG * 2;
+        else left = min(a.Kc, a.K - ahead.ks * a.Kc) * 2 - t * 16;
       } else {
-        q = a.row_copies ? lane >> 3 : lane;
-        j = a.row_copies ? lane & 7 : 0;
-        per = a.row_copies ? 1 : min(8, rows - 8 * q);
-        has = a.row_copies ? lane < rows : 8 * lane < rows;
-      }
-      const int row = entry_of(c.entry).e * rows_per_expert + c.row + c.skip() +
-                      (MODE == kGateUp ? q * a.N : q * 8) + j;
-      has = has && MOL_CHECK(row + per <= a.E * rows_per_expert, MOL_CHECK_WEIGHT_ROW, row);
-      const uint32_t size = a.row_copies ? (kW4 ? (len + 127) / 128 * 64 : len * 2) : per * pitch;
-      uint32_t mine = has ? size : 0;
-      const uint32_t sd = dst + scale_at(a, q, j);
-      const int slen = !kW4 ? 0 : a.row_copies ? (len + GG - 1) / GG * 2 : per * spitch;
-      const int64_t at = kW4 ? (int64_t)row * spitch + k0 / GG * 2 : 0;
-      const ScaleRange sr(at, slen, stotal);
-      if (kW4 && has) {
-        mine += sr.bytes;
-        if (sr.tail) sr.copy_tail(a.scales, sd, at, slen);
-      }
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar, mine);
-      __syncwarp();
-      if (has) {
-        bulk_copy(dst + row_at(a, q, j), a.w + (int64_t)row * pitch + (kW4 ? k0 / 2 : k0 * 2), size,
-                  bar);
-        if (kW4 && sr.bytes)
-          bulk_copy(sd, reinterpret_cast<const char*>(a.scales) + sr.from, sr.bytes, bar);
+        aim();
       }
     };
-    Cursor ahead = cur;
-    int filled = 0;  // first warp: stages asked for beyond those consumed
-    if (part == 0)
-      for (; go && filled < depth && ahead.valid; ++filled, ahead.next(a)) put(ahead, filled);
+    auto fetch = [&](int slot) {
+      if (ahead.valid) {
+        const uint32_t dst = ring + slot * kChunk + lane * 16;
+        const int o = next * 128;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const bool in = kW4 || o + u * 64 < left;  // past the row: zeros
+          copy16(dst + u * 512, in ? w0 + o + u * 64 : a.w, in ? 16 : 0);
+          copy16(dst + 1024 + u * 512, in ? w1 + o + u * 64 : a.w, in ? 16 : 0);
+        }
+        if (kW4 && t < 2)
+          copy_small<512 / GG>(ring + slot * kChunk + 2048 + (t * 8 + g) * (512 / GG),
+                               ws + next * (512 / GG));
+        next += parts;
+        if (next >= count) advance();
+      }
+      cp_async_commit();
+    };
+    if (ahead.valid) {
+      if (next < (count = chunks_of(ahead))) aim();
+      else advance();
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks - 1; ++i) fetch(i);
 
     float acc[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    int slot = 0, phase = 0, have = -1;
+    int slot = 0, have = -1, finisher = 0;
     int xi = -1, xs = -1, xphase = 0;  // token slots so far, the newest one's place and phase
     auto next_tokens = [&]() {         // releases the token slot in use and waits for the next
       if (xi >= 0) {
@@ -774,14 +796,16 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         xs = 0;
         xphase ^= 1;
       }
-      if (++xi < slots) fault = !mbar_wait(&xfull[xs], xphase, kWaitPolls, limit);
+      if (++xi < slots)
+        fault = __any_sync(0xffffffffu, !mbar_wait(&xfull[xs], xphase, kWaitPolls, limit));
     };
-    int want = 0;  // the token slot of this stage
+    int want = 0;  // the token slot of this step
     Entry en{0, 0, 0};
     uint32_t x[NT];  // the lane's token row of each tile
+    // After a fault nothing is read or written any more, but the team's warps still meet.
     for (; cur.valid; cur.next(a)) {
       if (whole) want = cur.entry - entry0;
-      if (xi < want || cur.entry != have) {
+      if (!fault && (xi < want || cur.entry != have)) {
         while (xi < want && !fault) next_tokens();  // (those passed over are released in their order)
         have = cur.entry;
         en = entry_of(have);
@@ -789,116 +813,99 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
         for (int nt = 0; nt < NT; ++nt)
           x[nt] = xslots + xs * a.xslot_bytes + min(g + 8 * nt, en.n - 1) * a.x_pitch + t * 16;
       }
-      fault = fault || !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
-      if (fault) break;
-      const int rows = cur.rows(a);
-      const int row0 = cur.row + cur.skip();  // of the expert
-      const uint32_t st = my_ring + slot * a.stage_bytes;
-      if (rows > 0) {
-        const int k0 = cur.ks * a.Kc, len = min(a.Kc, a.K - k0);
-        // the lane's rows, of span 0 and 1 (gate and up row of one output; gate_up tiles of 8 rows:
-        // one row, of span g & 1); rows past the tile's last read that row again, their products are
-        // dropped
-        const int n0 = MODE == kGateUp ? rows : min(rows, 8), n1 = MODE == kGateUp ? rows : rows - 8;
-        const int q0 = !kW4 && a.stage_rows == 8 ? 0 : g & 1;  // span of the first row
-        int j0 = min(g, (q0 ? n1 : n0) - 1), j1 = min(g, (q0 ? n0 : n1) - 1);
-        uint32_t r0, r1;
-        if (!kW4 && a.stage_rows == 8) {
-          r0 = r1 = st + row_at(a, g & 1, min(g >> 1, rows - 1)) + t * 16;
-        } else {
-          if (j0 < 0) j0 = 0;  // (a tile of at most 8 rows has no second span: anything that is there)
-          if (j1 < 0) j1 = 0;
-          r0 = st + row_at(a, q0, j0) + t * 16;
-          r1 = st + row_at(a, q0 ^ 1, j1) + t * 16;
-        }
-        if constexpr (kW4) {
-          const int first = en.e * rows_per_expert + row0;
-          // the copy that brought a row's scales began at the 16 bytes' boundary at or before them, or
-          // before those of its span's first row
-          auto scales_of = [&](int q, int j) {
-            const uint32_t from = first + (MODE == kGateUp ? q * a.N : q * 8) + (a.row_copies ? j : 0);
-            return st + scale_at(a, q, j) + ((from * spitch + k0 / GG * 2) & 15u);
-          };
-          const uint32_t s0 = scales_of(q0, j0), s1 = scales_of(q0 ^ 1, j1);
-          if (NT > 1 && en.n <= 8)
-            multiply_w4<GG, 1, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-          else
-            multiply_w4<GG, NT, NT>(acc, r0, r1, s0, s1, x, len, t, part, parts);
-        } else if (a.stage_rows == 8) {
-          if (NT > 1 && en.n <= 8) multiply_bf16<false, 1, NT>(acc, r0, r1, x, len, t, part, parts);
-          else multiply_bf16<false, NT, NT>(acc, r0, r1, x, len, t, part, parts);
-        } else {
-          if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, part, parts);
-          else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, part, parts);
-        }
-      }
-      const bool ends = cur.ks == a.ksteps - 1;
-      if (parts > 1) {
-        // the others' sums lie in the stage's own buffer until the first warp refills the stage
-        const uint32_t sums_of = st + a.parts_off + lane * 16;
-        if (part > 0) {
-          if (ends) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              st_s16(sums_of + ((part - 1) * NT + nt) * 512, acc[nt][0], acc[nt][1], acc[nt][2],
-                     acc[nt][3]);
-              acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+      ++want;
+      const int chunks = fault ? 0 : chunks_of(cur), len = min(a.Kc, a.K - cur.ks * a.Kc);
+#pragma unroll 1
+      for (int c = part; c < chunks; c += parts) {
+        cp_async_wait_group<kChunks - 2>();
+        __syncwarp();  // the row's scales have landed too; the chunk before has been read by all
+        fetch((slot + kChunks - 1) % kChunks);
+        const uint32_t st = ring + slot * kChunk;
+        slot = (slot + 1) % kChunks;
+        auto multiply = [&](auto tiles) {
+          constexpr int NTC = decltype(tiles)::value;
+          if constexpr (kW4) {
+            auto block = [&](int u, auto full) {
+              BlockW4<GG> w;
+              w.a0 = ld_s16(st + u * 512 + lane * 16);
+              w.a1 = ld_s16(st + 1024 + u * 512 + lane * 16);
+              w.f0.load(st + 2048 + g * (512 / GG) + u * (256 / GG));
+              w.f1.load(st + 2048 + (8 + g) * (512 / GG) + u * (256 / GG));
+              block_w4<GG, NTC, NT, decltype(full)::value>(acc, w, x, c * 2 + u, len, t);
+            };
+            if ((c + 1) * 256 <= len) {
+              block(0, std::true_type{});
+              block(1, std::true_type{});
+            } else {
+#pragma unroll 1
+              for (int u = 0; u < 2; ++u) block(u, std::false_type{});
             }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&my_pfull[slot]);
-        } else {
-          fault = !mbar_wait(&my_pfull[slot], phase, kWaitPolls, limit);
-          if (fault) break;
-          if (ends) {
-            for (int p = 0; p < parts - 1; ++p) {
+          } else {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint4 v = ld_s16(sums_of + (p * NT + nt) * 512);
-                acc[nt][0] += __uint_as_float(v.x);
-                acc[nt][1] += __uint_as_float(v.y);
-                acc[nt][2] += __uint_as_float(v.z);
-                acc[nt][3] += __uint_as_float(v.w);
+            for (int u = 0; u < 2; ++u) {
+              const int b = c * 2 + u;
+              const uint4 a0 = ld_s16(st + u * 512 + lane * 16);
+              const uint4 a1 = ld_s16(st + 1024 + u * 512 + lane * 16);
+              const bool in = b * 32 + t * 8 < len;  // inputs past len are zeros
+#pragma unroll
+              for (int nt = 0; nt < NTC; ++nt) {
+                const uint4 v = in ? ld_s16(x[nt] + b * 64) : make_uint4(0, 0, 0, 0);
+                mma_add(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+                mma_add(acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
               }
             }
           }
-        }
+        };
+        if (NT > 1 && en.n <= 8) multiply(std::integral_constant<int, 1>{});
+        else multiply(std::integral_constant<int, NT>{});
       }
-      __syncwarp();
-      if (part == 0) {  // the team is through with the stage: the next one into its place
-        if (ahead.valid) {
-          put(ahead, slot);
-          ahead.next(a);
-        } else {
-          --filled;
-        }
-      }
-      if (++slot == depth) {
-        slot = 0;
-        phase ^= 1;
-      }
-      // (pieces of rows: the team's stages and the token slots go together, one by one)
-      ++want;
-      if (!ends || part > 0 || rows == 0) continue;
+      if (cur.ks < a.ksteps - 1) continue;
 
-      // the tile's values: column 2t + h of each token tile; the lane's row of span 0 in values h and
-      // that of span 1 in values 2 + h, the other way round where g is odd
-      const bool eight = !kW4 && a.stage_rows == 8;
+      // The warps of a team take turns in adding the others' sums and finishing.
+      if (parts > 1) {
+        const bool mine = part == finisher;
+        auto place = [&](int p) {
+          return sums + (team * (parts - 1) + p - (p > finisher)) * NT * 512 + lane * 16;
+        };
+        named_sync(1 + team, parts * 32);  // (the tile before has been added)
+        if (!mine) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            st_s16(place(part) + nt * 512, acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+        }
+        named_sync(1 + team, parts * 32);
+        if (mine) {
+          for (int p = 0; p < parts; ++p) {
+            if (p == part) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 v = ld_s16(place(p) + nt * 512);
+              acc[nt][0] += __uint_as_float(v.x);
+              acc[nt][1] += __uint_as_float(v.y);
+              acc[nt][2] += __uint_as_float(v.z);
+              acc[nt][3] += __uint_as_float(v.w);
+            }
+          }
+        }
+        finisher = finisher + 1 == parts ? 0 : finisher + 1;
+        if (!mine) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+          continue;
+        }
+      }
+      // the tile's values: column 2t + h of each token tile; row g of the first eight in values h, of
+      // the second (gate_up: the up row) in values 2 + h
+      const int rows = fault ? 0 : min(a.tile_rows, a.N - cur.row);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int col = nt * 8 + 2 * t + h;
-          float v0 = g & 1 ? acc[nt][2 + h] : acc[nt][h], v1 = g & 1 ? acc[nt][h] : acc[nt][2 + h];
+          const int col = nt * 8 + 2 * t + h, n = cur.row + g;
+          float v0 = acc[nt][h], v1 = acc[nt][2 + h];
+          if (col >= en.n || g >= rows) continue;
           if (MODE == kGateUp) {
-            if (eight) {
-              v0 = acc[nt][h];
-              v1 = __shfl_down_sync(0xffffffffu, v0, 4);
-            }
-            const int j = eight ? g >> 1 : g;
-            if (col >= en.n || j >= rows || (eight && (g & 1))) continue;
             const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
-            const int n = row0 + j;
             if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
             if (a.delta) {
               const bf16* dl = a.delta + pair * a.delta_stride + n;
@@ -906,28 +913,20 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1)
               v1 += __bfloat162float(dl[a.N]);
             }
             a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
-          } else if (col < en.n) {
-            bf16* o = a.out + col * a.out_stride + row0;
-            if (!MOL_CHECK(row0 + rows <= a.N, MOL_CHECK_COLUMN, row0)) continue;
-            if (g < rows) o[g] = __float2bfloat16(v0);
-            if (g + 8 < rows) o[g + 8] = __float2bfloat16(v1);
+          } else {
+            if (!MOL_CHECK(cur.row + rows <= a.N, MOL_CHECK_COLUMN, cur.row)) continue;
+            bf16* o = a.out + col * a.out_stride + n;
+            o[0] = __float2bfloat16(v0);
+            if (g + 8 < rows) o[8] = __float2bfloat16(v1);
           }
         }
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
-    // the token slots that are left, for the teams that still need them to be refilled
+    // the token slots that are left, for the warps that still need them to be refilled
     while (!fault && xi < slots) next_tokens();
-    // no copy may be in flight when the block leaves
-    if (fault && part == 0)
-      for (int q = 0; q < filled; ++q) {
-        (void)mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
-        if (++slot == depth) {
-          slot = 0;
-          phase ^= 1;
-        }
-      }
+    if (fault) cp_async_wait_all();  // no copy may be in flight when the block leaves
   }
   if (fault && lane == 0) atomicOr(&g_moe_fault_flags, kFaultBulkTimeout);
 }
@@ -1191,7 +1190,7 @@ struct StreamLaunch {
   static cudaError_t one(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kBlockWarps * 32);
+    cfg.blockDim = dim3((MODE == kDown ? kBlockWarps : consumer_warps(NT) + 1) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -9,9 +9,15 @@ namespace mol {
 
 enum StreamMode { kGateUp = 0, kDown = 1, kLinear = 2 };
 
-// Sixteen warps a block, so a thread may have 128 registers (24 of 80 measured 5 % slower where one
-// token tile suffices); gate_up and linear: one of them brings the tokens' rows.
+// Warps of a block of down; at 16 a thread may have 128 registers.
 constexpr int kBlockWarps = 16;
+// gate_up, linear: consumer warps of a block, by its token tiles. One more brings the tokens' rows; a
+// seventeenth warp lowers the registers of a thread to 96, too few for many tokens' sums.
+__host__ __device__ constexpr int consumer_warps(int token_tiles) { return token_tiles <= 2 ? 16 : 15; }
+// gate_up, linear: a warp's ring of chunks. A chunk is 128 bytes of each of a tile's 16 weight rows, and
+// their scales.
+constexpr int kChunks = 4;
+__host__ __device__ constexpr int chunk_bytes(int group) { return 2048 + (group ? 16 * 512 / group : 0); }
 constexpr int kMaxStages = 32;  // of all teams of a block
 constexpr int kMaxSlots = 8;    // token slots
 constexpr int kClusterSizes = 3;  // down: clusters of 1, 2 or 4 blocks
