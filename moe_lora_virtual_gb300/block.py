@@ -114,14 +114,20 @@ def w4_unpack(w: W4) -> torch.Tensor:
     return v.reshape(*lead, -1)[..., :w.in_features]
 
 
+# The checks below read each property of a tensor once and allocate like their input: what a call
+# costs on the host is what the smallest calls take.
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _rows(t: torch.Tensor, dtype, name: str) -> int:
     """Row stride of a 2-D CUDA operand with unit column stride."""
     if t.dtype != dtype or not t.is_cuda:
         _mol._need(t, dtype, name)
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    stride, shape = t.stride(), t.shape
+    if len(stride) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: expected a 2-D tensor with unit column stride")
     # a single row (or none) has no stride that matters
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8 * -(-t.shape[1] // 8))
+    return stride[0] if shape[0] > 1 else max(shape[1], 8 * -(-shape[1] // 8))
 
 
 def _flat(t: torch.Tensor, dtype, name: str, shape) -> int:
@@ -134,7 +140,7 @@ def _flat(t: torch.Tensor, dtype, name: str, shape) -> int:
 
 
 def _vector(t: Optional[torch.Tensor], name: str, n: int):
-    return None if t is None else _flat(t, torch.bfloat16, name, (n,))
+    return None if t is None else _flat(t, _bf16, name, (n,))
 
 
 def _weights(w: Weights, name: str, lead, K: int):
@@ -146,8 +152,8 @@ def _weights(w: Weights, name: str, lead, K: int):
             raise ValueError(f"{name}: group is one of {GROUPS}, got {w.group}")
         Kp = _padded(K)
         return (_flat(w.qweight, torch.uint8, name, (*lead, Kp // 2)),
-                _flat(w.scales, torch.bfloat16, name + " scales", (*lead, Kp // w.group)), w.group)
-    return _flat(w, torch.bfloat16, name, (*lead, K)), None, 0
+                _flat(w.scales, _bf16, name + " scales", (*lead, Kp // w.group)), w.group)
+    return _flat(w, _bf16, name, (*lead, K)), None, 0
 
 
 def _lead(w: Weights) -> torch.Size:
@@ -157,7 +163,7 @@ def _lead(w: Weights) -> torch.Size:
 def _delta(delta: Optional[torch.Tensor], pairs: int, width: int):
     if delta is None:
         return None, 0
-    stride = _rows(delta, torch.bfloat16, "delta")
+    stride = _rows(delta, _bf16, "delta")
     if delta.shape != (pairs, width):
         raise ValueError(f"delta: expected shape {(pairs, width)}, got {tuple(delta.shape)}")
     return delta.data_ptr(), stride
@@ -165,8 +171,8 @@ def _delta(delta: Optional[torch.Tensor], pairs: int, width: int):
 
 def _out(out: Optional[torch.Tensor], shape, like: torch.Tensor, name: str = "out"):
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device), shape[1]
-    stride = _rows(out, torch.bfloat16, name)
+        return torch.empty(shape, dtype=_bf16, device=like.device), shape[1]
+    stride = _rows(out, _bf16, name)
     if out.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
     return out, stride
@@ -178,9 +184,10 @@ def _call(name: str, *args) -> None:
         raise _mol.MolError(name, status)
 
 
-def _stream(stream) -> int:
+def _stream(stream, t: torch.Tensor) -> int:
+    """The stream given, or the current one of the tensor's device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -194,30 +201,36 @@ def mol_block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: Optional
     y, residual bf16 [T, H]; post_weight, pre_weight bf16 [H] or None; gate bf16 [H], [T, H] or
     None. Returns (residual_out, normed); normed is None without pre_weight. residual_out may be
     `residual`, normed may be `y`."""
-    T, H = y.shape
-    ys = _rows(y, torch.bfloat16, "y")
-    rs = _rows(residual, torch.bfloat16, "residual")
-    if residual.shape != y.shape:
+    shape = T, H = y.shape
+    ys = _rows(y, _bf16, "y")
+    rs = _rows(residual, _bf16, "residual")
+    if residual.shape != shape:
         raise ValueError(f"residual: expected shape {tuple(y.shape)}, got {tuple(residual.shape)}")
     gp, gs = None, 0
     if gate is not None:
         if gate.dim() == 1:
-            gp = _flat(gate, torch.bfloat16, "gate", (H,))
+            gp = _flat(gate, _bf16, "gate", (H,))
         else:
-            gp, gs = gate.data_ptr(), _rows(gate, torch.bfloat16, "gate")
+            gp, gs = gate.data_ptr(), _rows(gate, _bf16, "gate")
             if gate.shape != y.shape:
                 raise ValueError(f"gate: expected shape {(H,)} or {tuple(y.shape)}, got "
                                  f"{tuple(gate.shape)}")
     post, pre = _vector(post_weight, "post_weight", H), _vector(pre_weight, "pre_weight", H)
-    residual_out, ros = _out(residual_out, y.shape, y, "residual_out")
+    if residual_out is None:
+        residual_out, ros = torch.empty_like(y, memory_format=torch.contiguous_format), H
+    else:
+        residual_out, ros = _out(residual_out, shape, y, "residual_out")
     ns = 0
     if pre is not None:
-        normed, ns = _out(normed, y.shape, y, "normed")
+        if normed is None:
+            normed, ns = torch.empty_like(y, memory_format=torch.contiguous_format), H
+        else:
+            normed, ns = _out(normed, shape, y, "normed")
     elif normed is not None:
         raise ValueError("normed: needs pre_weight")
     _call("mol_block_norm", y.data_ptr(), ys, residual.data_ptr(), rs, post, gp, gs, residual_scale,
           pre, eps, T, H, residual_out.data_ptr(), ros,
-          None if normed is None else normed.data_ptr(), ns, _stream(stream))
+          None if normed is None else normed.data_ptr(), ns, _stream(stream, y))
     return residual_out, normed
 
 
@@ -225,17 +238,16 @@ def mol_moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True, sca
                   topk_ids: Optional[torch.Tensor] = None,
                   topk_weights: Optional[torch.Tensor] = None, stream=None):
     """(topk_ids int32, topk_weights fp32), [T, topk] each, of router logits fp32 or bf16 [T, E]."""
-    bf16 = logits.dtype == torch.bfloat16
-    stride = _rows(logits, torch.bfloat16 if bf16 else torch.float32, "logits")
+    bf16 = logits.dtype == _bf16
+    stride = _rows(logits, _bf16 if bf16 else _f32, "logits")
     T, E = logits.shape
-    dev = logits.device
     if topk_ids is None:
-        topk_ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        topk_ids = torch.empty((T, topk), dtype=_i32, device=logits.device)
     if topk_weights is None:
-        topk_weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        topk_weights = torch.empty((T, topk), dtype=_f32, device=logits.device)
     _call("mol_moe_route", logits.data_ptr(), MOL_BF16 if bf16 else MOL_F32, stride, T, E, topk,
-          int(renormalize), scale, _flat(topk_ids, torch.int32, "topk_ids", (T, topk)),
-          _flat(topk_weights, torch.float32, "topk_weights", (T, topk)), _stream(stream))
+          int(renormalize), scale, _flat(topk_ids, _i32, "topk_ids", (T, topk)),
+          _flat(topk_weights, _f32, "topk_weights", (T, topk)), _stream(stream, logits))
     return topk_ids, topk_weights
 
 
@@ -251,10 +263,10 @@ def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
     wp, sp, group = _weights(w_gate_up, "w_gate_up", (E, I2), H)
     dp, ds = _delta(delta, T * k, I2)
     if act is None:
-        act = torch.empty((T * k, I2 // 2), dtype=torch.bfloat16, device=x.device)
-    _call("mol_moe_gate_up", x.data_ptr(), _rows(x, torch.bfloat16, "x"),
-          _flat(topk_ids, torch.int32, "topk_ids", (T, k)), T, k, E, H, I2 // 2, wp, sp, group, dp,
-          ds, _flat(act, torch.bfloat16, "act", (T * k, I2 // 2)), _stream(stream))
+        act = torch.empty((T * k, I2 // 2), dtype=_bf16, device=x.device)
+    _call("mol_moe_gate_up", x.data_ptr(), _rows(x, _bf16, "x"),
+          _flat(topk_ids, _i32, "topk_ids", (T, k)), T, k, E, H, I2 // 2, wp, sp, group, dp,
+          ds, _flat(act, _bf16, "act", (T * k, I2 // 2)), _stream(stream, x))
     return act
 
 
@@ -271,10 +283,10 @@ def mol_moe_down(act: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
     wp, sp, group = _weights(w_down, "w_down", (E, H), I)
     dp, ds = _delta(delta, T * k, H)
     out, os = _out(out, (T, H), act)
-    _call("mol_moe_down", _flat(act, torch.bfloat16, "act", (T * k, I)),
-          _flat(topk_ids, torch.int32, "topk_ids", (T, k)),
-          _flat(topk_weights, torch.float32, "topk_weights", (T, k)), T, k, E, H, I, wp, sp, group,
-          dp, ds, out.data_ptr(), os, _stream(stream))
+    _call("mol_moe_down", _flat(act, _bf16, "act", (T * k, I)),
+          _flat(topk_ids, _i32, "topk_ids", (T, k)),
+          _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, wp, sp, group,
+          dp, ds, out.data_ptr(), os, _stream(stream, act))
     return out
 
 
@@ -293,13 +305,13 @@ def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
     if group != group_down:
         raise ValueError("w_gate_up, w_down: expected the same type and group")
     if act is None:
-        act = torch.empty((T * k, I), dtype=torch.bfloat16, device=x.device)
+        act = torch.empty((T * k, I), dtype=_bf16, device=x.device)
     out, os = _out(out, (T, H), x)
-    _call("mol_moe_forward", x.data_ptr(), _rows(x, torch.bfloat16, "x"),
-          _flat(topk_ids, torch.int32, "topk_ids", (T, k)),
-          _flat(topk_weights, torch.float32, "topk_weights", (T, k)), T, k, E, H, I, gp, gsp, wp,
-          wsp, group, _flat(act, torch.bfloat16, "act", (T * k, I)), out.data_ptr(), os,
-          _stream(stream))
+    _call("mol_moe_forward", x.data_ptr(), _rows(x, _bf16, "x"),
+          _flat(topk_ids, _i32, "topk_ids", (T, k)),
+          _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, gp, gsp, wp,
+          wsp, group, _flat(act, _bf16, "act", (T * k, I)), out.data_ptr(), os,
+          _stream(stream, x))
     return out
 
 
@@ -312,6 +324,6 @@ def mol_w4_linear(x: torch.Tensor, w: W4, out: Optional[torch.Tensor] = None,
     (N,) = _lead(w)
     wp, sp, group = _weights(w, "w", (N,), K)
     out, os = _out(out, (T, N), x)
-    _call("mol_w4_linear", x.data_ptr(), _rows(x, torch.bfloat16, "x"), T, K, N, wp, sp, group,
-          out.data_ptr(), os, _stream(stream))
+    _call("mol_w4_linear", x.data_ptr(), _rows(x, _bf16, "x"), T, K, N, wp, sp, group,
+          out.data_ptr(), os, _stream(stream, x))
     return out
