@@ -138,6 +138,29 @@ int32_t mol_moe_forward(const void* x, int64_t x_row_stride, const int32_t* topk
                         int32_t group, void* act, void* out, int64_t out_row_stride, void* stream);
 
 /*
+ * mol_moe_down and mol_moe_forward with a workspace, where they take one step more
+ * for many pairs: the products of each pair in fp32, then their weighted sums.
+ * Same contract and result (the fp32 sums are in the order of the slots then).
+ *   workspace  device, >= mol_moe_workspace_bytes of the sizes, 16-byte aligned
+ *              (may be NULL when that is 0); contents are scratch
+ */
+size_t mol_moe_workspace_bytes(int64_t num_tokens, int32_t topk, int32_t num_experts,
+                               int32_t hidden, int32_t inter, int32_t group);
+int32_t mol_moe_down_split(const void* act, const int32_t* topk_ids, const float* topk_weights,
+                           int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t hidden,
+                           int32_t inter, const void* w, const void* w_scales, int32_t group,
+                           const void* delta, int64_t delta_row_stride, void* workspace,
+                           size_t workspace_bytes, void* out, int64_t out_row_stride,
+                           void* stream);
+int32_t mol_moe_forward_split(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
+                              const float* topk_weights, int64_t num_tokens, int32_t topk,
+                              int32_t num_experts, int32_t hidden, int32_t inter,
+                              const void* w_gate_up, const void* gate_up_scales,
+                              const void* w_down, const void* down_scales, int32_t group,
+                              void* act, void* workspace, size_t workspace_bytes, void* out,
+                              int64_t out_row_stride, void* stream);
+
+/*
  * out[t, n] = sum_k w[n, k] * x[t, k] in fp32, rounded to bf16 once.
  *   x    bf16 rows of K at x + t * x_row_stride
  *   w    w4 rows [N, Kp / 2 bytes], scales bf16 [N, Kp / group]

@@ -394,5 +394,5 @@ def decode_check_record(first: int, count: int) -> CheckRecord:
 
 # The MoE block around the LoRA path (include/mol_block.h).
 from .block import (BLOCK_EXPORTS, BLOCK_SIGS, W4, mol_block_norm, mol_moe_down,  # noqa: E402
-                    mol_moe_forward, mol_moe_gate_up, mol_moe_route, mol_w4_linear, w4_pack,
-                    w4_quantize, w4_unpack)
+                    mol_moe_forward, mol_moe_gate_up, mol_moe_route, mol_moe_workspace_bytes,
+                    mol_w4_linear, w4_pack, w4_quantize, w4_unpack)

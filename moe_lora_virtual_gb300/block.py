@@ -17,7 +17,8 @@ import torch
 import moe_lora_virtual_gb300 as _mol
 
 BLOCK_EXPORTS = ("mol_block_norm", "mol_moe_route", "mol_moe_gate_up", "mol_moe_down",
-                 "mol_moe_forward", "mol_w4_linear")
+                 "mol_moe_forward", "mol_moe_workspace_bytes", "mol_moe_down_split",
+                 "mol_moe_forward_split", "mol_w4_linear")
 MOL_NORM_MAX_H = 16384
 MOL_ROUTE_MAX_EXPERTS = 1024
 MOL_ROUTE_MAX_TOPK = 32
@@ -29,6 +30,7 @@ MOL_W4_MAX_TOKENS = 64
 MOL_F32, MOL_BF16 = 0, 1
 
 _P, _I32, _I64, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_SZ = ctypes.c_size_t
 BLOCK_SIGS = {
     "mol_block_norm": (_I32, [_P, _I64, _P, _I64, _P, _P, _I64, _F32, _P, _F32, _I64, _I32, _P,
                               _I64, _P, _I64, _P]),
@@ -39,6 +41,11 @@ BLOCK_SIGS = {
                             _I64, _P]),
     "mol_moe_forward": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I32,
                                _P, _P, _I64, _P]),
+    "mol_moe_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I32]),
+    "mol_moe_down_split": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64,
+                                  _P, _SZ, _P, _I64, _P]),
+    "mol_moe_forward_split": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                     _I32, _P, _P, _SZ, _P, _I64, _P]),
     "mol_w4_linear": (_I32, [_P, _I64, _I64, _I32, _I32, _P, _P, _I32, _P, _I64, _P]),
 }
 
@@ -270,33 +277,56 @@ def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
     return act
 
 
+def mol_moe_workspace_bytes(num_tokens: int, topk: int, num_experts: int, hidden: int, inter: int,
+                            group: int = 0) -> int:
+    """Bytes of workspace mol_moe_down and mol_moe_forward use for these sizes (often 0)."""
+    return (_mol._lib or _mol.library()).mol_moe_workspace_bytes(num_tokens, topk, num_experts,
+                                                                 hidden, inter, group)
+
+
+def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, *shape):
+    """(pointer, bytes, tensor) of the workspace for these sizes: the one given, or a new one."""
+    need = mol_moe_workspace_bytes(*shape)
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace: expected a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def mol_moe_down(act: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
                  w_down: Weights, out: Optional[torch.Tensor] = None,
-                 delta: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 delta: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
     """out [T, H] = sum over a token's pairs of topk_weights * (w_down[e] . act + delta).
 
     act bf16 [T * topk, I]; w_down bf16 [E, H, I] or W4; delta bf16 [T * topk, H]: rows a LoRA down
-    stage added into zeros."""
+    stage added into zeros; workspace: mol_moe_workspace_bytes of scratch."""
     T, k = topk_ids.shape
     E, H = _lead(w_down)
     I = act.shape[1]
     wp, sp, group = _weights(w_down, "w_down", (E, H), I)
     dp, ds = _delta(delta, T * k, H)
     out, os = _out(out, (T, H), act)
-    _call("mol_moe_down", _flat(act, _bf16, "act", (T * k, I)),
+    ws, wsb, workspace = _workspace(workspace, act, T, k, E, H, I, group)
+    _call("mol_moe_down_split", _flat(act, _bf16, "act", (T * k, I)),
           _flat(topk_ids, _i32, "topk_ids", (T, k)),
           _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, wp, sp, group,
-          dp, ds, out.data_ptr(), os, _stream(stream, act))
+          dp, ds, ws, wsb, out.data_ptr(), os, _stream(stream, act))
     return out
 
 
 def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
                     w_gate_up: Weights, w_down: Weights, out: Optional[torch.Tensor] = None,
-                    act: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                    act: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
     """The experts of a MoE layer for a few tokens: mol_moe_gate_up, then mol_moe_down.
 
     x bf16 [T, H]; topk_ids int32 and topk_weights fp32 [T, topk]; weights bf16 [E, 2I, H] and
-    [E, H, I], or both W4 of one group; act: scratch bf16 [T * topk, I]."""
+    [E, H, I], or both W4 of one group; scratch: act bf16 [T * topk, I], workspace of
+    mol_moe_workspace_bytes."""
     (T, H), k = x.shape, topk_ids.shape[1]
     E, I2 = _lead(w_gate_up)
     I = I2 // 2
@@ -307,10 +337,11 @@ def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
     if act is None:
         act = torch.empty((T * k, I), dtype=_bf16, device=x.device)
     out, os = _out(out, (T, H), x)
-    _call("mol_moe_forward", x.data_ptr(), _rows(x, _bf16, "x"),
+    ws, wsb, workspace = _workspace(workspace, x, T, k, E, H, I, group)
+    _call("mol_moe_forward_split", x.data_ptr(), _rows(x, _bf16, "x"),
           _flat(topk_ids, _i32, "topk_ids", (T, k)),
           _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, gp, gsp, wp,
-          wsp, group, _flat(act, _bf16, "act", (T * k, I)), out.data_ptr(), os,
+          wsp, group, _flat(act, _bf16, "act", (T * k, I)), ws, wsb, out.data_ptr(), os,
           _stream(stream, x))
     return out
 

@@ -42,13 +42,67 @@ int32_t check_delta(const void* delta, int64_t stride, int64_t width) {
 
 int32_t done(cudaError_t e) { return e == cudaSuccess ? MOL_OK : mol::cuda_fail(e); }
 
-}  // namespace
-
 #define MOL_TRY(call)              \
   do {                             \
     const int32_t st_ = (call);    \
     if (st_ != MOL_OK) return st_; \
   } while (0)
+
+int32_t check_down(const void* act, const int32_t* topk_ids, const float* topk_weights,
+                   int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t hidden,
+                   int32_t inter, const void* w, const void* w_scales, int32_t group,
+                   const void* delta, int64_t delta_row_stride, const void* out,
+                   int64_t out_row_stride) {
+  MOL_TRY(check_moe_shape(num_tokens, topk, num_experts, hidden, inter));
+  if (num_tokens == 0) return MOL_OK;
+  if (!topk_ids || !topk_weights) return MOL_ERR_INVALID_ARG;
+  MOL_TRY(check_rows(act, inter, inter));
+  MOL_TRY(check_weights(w, w_scales, group, false));
+  MOL_TRY(check_delta(delta, delta_row_stride, hidden));
+  return check_rows(out, out_row_stride, hidden);
+}
+
+// Whether the split form is taken, for which the workspace has to do.
+int32_t check_workspace(const mol::MoeShape& s, int32_t group, const void* workspace, size_t bytes,
+                        bool& split) {
+  const size_t need = mol::moe_split_bytes(s, group);
+  split = need > 0;
+  if (!split) return MOL_OK;
+  if (!workspace || bytes < need) return MOL_ERR_CAPACITY;
+  return aligned16(workspace) ? MOL_OK : MOL_ERR_UNSUPPORTED;
+}
+
+int32_t forward(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
+                const float* topk_weights, int64_t num_tokens, int32_t topk, int32_t num_experts,
+                int32_t hidden, int32_t inter, const void* w_gate_up, const void* gate_up_scales,
+                const void* w_down, const void* down_scales, int32_t group, void* act,
+                void* workspace, size_t workspace_bytes, bool may_split, void* out,
+                int64_t out_row_stride, void* stream) {
+  MOL_TRY(check_moe_shape(num_tokens, topk, num_experts, hidden, inter));
+  if (num_tokens == 0) return MOL_OK;
+  if (!topk_ids || !topk_weights) return MOL_ERR_INVALID_ARG;
+  MOL_TRY(check_rows(x, x_row_stride, hidden));
+  MOL_TRY(check_weights(w_gate_up, gate_up_scales, group, false));
+  MOL_TRY(check_weights(w_down, down_scales, group, false));
+  MOL_TRY(check_rows(act, inter, inter));
+  MOL_TRY(check_rows(out, out_row_stride, hidden));
+  const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
+  bool split = false;
+  if (may_split) MOL_TRY(check_workspace(s, group, workspace, workspace_bytes, split));
+  MOL_TRY(mol::ensure_device());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = mol::launch_moe_gate_up(
+      s, x, x_row_stride, topk_ids, mol::WeightRows{w_gate_up, gate_up_scales, hidden, group},
+      nullptr, 0, act, st);
+  if (e != cudaSuccess) return mol::cuda_fail(e);
+  const mol::WeightRows rows{w_down, down_scales, inter, group};
+  return done(split ? mol::launch_moe_down_split(s, act, topk_ids, topk_weights, rows, nullptr, 0,
+                                                 workspace, out, out_row_stride, true, st)
+                    : mol::launch_moe_down(s, act, topk_ids, topk_weights, rows, nullptr, 0, out,
+                                           out_row_stride, true, st));
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -133,13 +187,9 @@ int32_t mol_moe_down(const void* act, const int32_t* topk_ids, const float* topk
                      int32_t inter, const void* w, const void* w_scales, int32_t group,
                      const void* delta, int64_t delta_row_stride, void* out,
                      int64_t out_row_stride, void* stream) {
-  MOL_TRY(check_moe_shape(num_tokens, topk, num_experts, hidden, inter));
+  MOL_TRY(check_down(act, topk_ids, topk_weights, num_tokens, topk, num_experts, hidden, inter, w,
+                     w_scales, group, delta, delta_row_stride, out, out_row_stride));
   if (num_tokens == 0) return MOL_OK;
-  if (!topk_ids || !topk_weights) return MOL_ERR_INVALID_ARG;
-  MOL_TRY(check_rows(act, inter, inter));
-  MOL_TRY(check_weights(w, w_scales, group, false));
-  MOL_TRY(check_delta(delta, delta_row_stride, hidden));
-  MOL_TRY(check_rows(out, out_row_stride, hidden));
   MOL_TRY(mol::ensure_device());
   const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
   return done(mol::launch_moe_down(s, act, topk_ids, topk_weights,
@@ -148,29 +198,56 @@ int32_t mol_moe_down(const void* act, const int32_t* topk_ids, const float* topk
                                    static_cast<cudaStream_t>(stream)));
 }
 
+size_t mol_moe_workspace_bytes(int64_t num_tokens, int32_t topk, int32_t num_experts,
+                               int32_t hidden, int32_t inter, int32_t group) {
+  if (check_moe_shape(num_tokens, topk, num_experts, hidden, inter) != MOL_OK || num_tokens == 0)
+    return 0;
+  return mol::moe_split_bytes(mol::MoeShape{(int)num_tokens, topk, num_experts, hidden, inter},
+                              group);
+}
+
+int32_t mol_moe_down_split(const void* act, const int32_t* topk_ids, const float* topk_weights,
+                           int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t hidden,
+                           int32_t inter, const void* w, const void* w_scales, int32_t group,
+                           const void* delta, int64_t delta_row_stride, void* workspace,
+                           size_t workspace_bytes, void* out, int64_t out_row_stride,
+                           void* stream) {
+  MOL_TRY(check_down(act, topk_ids, topk_weights, num_tokens, topk, num_experts, hidden, inter, w,
+                     w_scales, group, delta, delta_row_stride, out, out_row_stride));
+  if (num_tokens == 0) return MOL_OK;
+  const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
+  bool split = false;
+  MOL_TRY(check_workspace(s, group, workspace, workspace_bytes, split));
+  MOL_TRY(mol::ensure_device());
+  const mol::WeightRows rows{w, w_scales, inter, group};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return done(split ? mol::launch_moe_down_split(s, act, topk_ids, topk_weights, rows, delta,
+                                                 delta_row_stride, workspace, out, out_row_stride,
+                                                 false, st)
+                    : mol::launch_moe_down(s, act, topk_ids, topk_weights, rows, delta,
+                                           delta_row_stride, out, out_row_stride, false, st));
+}
+
 int32_t mol_moe_forward(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
                         const float* topk_weights, int64_t num_tokens, int32_t topk,
                         int32_t num_experts, int32_t hidden, int32_t inter, const void* w_gate_up,
                         const void* gate_up_scales, const void* w_down, const void* down_scales,
                         int32_t group, void* act, void* out, int64_t out_row_stride, void* stream) {
-  MOL_TRY(check_moe_shape(num_tokens, topk, num_experts, hidden, inter));
-  if (num_tokens == 0) return MOL_OK;
-  if (!topk_ids || !topk_weights) return MOL_ERR_INVALID_ARG;
-  MOL_TRY(check_rows(x, x_row_stride, hidden));
-  MOL_TRY(check_weights(w_gate_up, gate_up_scales, group, false));
-  MOL_TRY(check_weights(w_down, down_scales, group, false));
-  MOL_TRY(check_rows(act, inter, inter));
-  MOL_TRY(check_rows(out, out_row_stride, hidden));
-  MOL_TRY(mol::ensure_device());
-  const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = mol::launch_moe_gate_up(
-      s, x, x_row_stride, topk_ids, mol::WeightRows{w_gate_up, gate_up_scales, hidden, group},
-      nullptr, 0, act, st);
-  if (e != cudaSuccess) return mol::cuda_fail(e);
-  return done(mol::launch_moe_down(s, act, topk_ids, topk_weights,
-                                   mol::WeightRows{w_down, down_scales, inter, group}, nullptr, 0,
-                                   out, out_row_stride, true, st));
+  return forward(x, x_row_stride, topk_ids, topk_weights, num_tokens, topk, num_experts, hidden,
+                 inter, w_gate_up, gate_up_scales, w_down, down_scales, group, act, nullptr, 0,
+                 false, out, out_row_stride, stream);
+}
+
+int32_t mol_moe_forward_split(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
+                              const float* topk_weights, int64_t num_tokens, int32_t topk,
+                              int32_t num_experts, int32_t hidden, int32_t inter,
+                              const void* w_gate_up, const void* gate_up_scales,
+                              const void* w_down, const void* down_scales, int32_t group,
+                              void* act, void* workspace, size_t workspace_bytes, void* out,
+                              int64_t out_row_stride, void* stream) {
+  return forward(x, x_row_stride, topk_ids, topk_weights, num_tokens, topk, num_experts, hidden,
+                 inter, w_gate_up, gate_up_scales, w_down, down_scales, group, act, workspace,
+                 workspace_bytes, true, out, out_row_stride, stream);
 }
 
 int32_t mol_w4_linear(const void* x, int64_t x_row_stride, int64_t num_tokens, int32_t K, int32_t N,

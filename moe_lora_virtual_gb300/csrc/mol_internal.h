@@ -266,6 +266,12 @@ cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* t
                             const float* topk_weights, const WeightRows& w, const void* delta,
                             int64_t delta_stride, void* out, int64_t out_stride, bool chained,
                             cudaStream_t stream);
+// Bytes of the split form's partial products, 0 where the form above is the faster.
+size_t moe_split_bytes(const MoeShape& s, int group);
+cudaError_t launch_moe_down_split(const MoeShape& s, const void* act, const int32_t* topk_ids,
+                                  const float* topk_weights, const WeightRows& w, const void* delta,
+                                  int64_t delta_stride, void* workspace, void* out,
+                                  int64_t out_stride, bool chained, cudaStream_t stream);
 cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, int N,
                              const WeightRows& w, void* out, int64_t out_stride,
                              cudaStream_t stream);

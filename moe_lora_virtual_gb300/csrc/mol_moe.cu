@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "mol_block.h"
+#include "mol_device.cuh"
 #include "mol_internal.h"
 #include "mol_moe.h"
 
@@ -28,10 +29,14 @@ cudaError_t launch_by_group(int group, const StreamArgs& a, int mode, int grid, 
 
 // Tokens of an entry, a power of two: half as many again as the mean of an expert's pairs, so that few
 // experts need a second entry (which reads their weights again), and no more room than the tokens
-// need.
+// need. From 8 on, where twice as many cost a second token tile, a tenth more than the mean suffices
+// (128 experts, 4 bits: 96 tokens 120 us at 8 and 131 at 16, 127 tokens 148 and 165; bf16: 110 tokens
+// 224 and 237, 127 tokens 273 and 243).
 int entry_tokens(int num_tokens, int pairs, int experts) {
   int n = num_tokens == 1 ? 1 : num_tokens == 2 ? 2 : 4;
-  while (n < 64 && n < num_tokens && 2 * n * experts < 3 * pairs) n *= 2;
+  while (n < 64 && n < num_tokens &&
+         (n < 8 ? 2 * n * experts < 3 * pairs : 10 * n * experts < 11 * pairs))
+    n *= 2;
   return n;
 }
 
@@ -148,7 +153,77 @@ StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const
 
 int list_bytes(const MoeShape& s) { return s.num_tokens * s.topk * 16; }
 
+constexpr int kCombineThreads = 128;
+
+// The split form's second step, out[t] = sum over t's pairs of weight * partial, in the order of the
+// slots, then the deltas in that order. Four columns a thread; bound by reading the fp32 partials
+// back from L2.
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const StreamArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t = blockIdx.y, n = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
+  if (n >= a.N) return;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, float v0, float v1, float v2, float v3) {
+    sum.x = fmaf(w, v0, sum.x);
+    sum.y = fmaf(w, v1, sum.y);
+    sum.z = fmaf(w, v2, sum.z);
+    sum.w = fmaf(w, v3, sum.w);
+  };
+#pragma unroll 4
+  for (int k = 0; k < a.topk; ++k) {
+    const int64_t pair = t * a.topk + k;
+    const int e = a.ids[pair];
+    if (e < 0 || e >= a.E) continue;
+    const float4 v = *reinterpret_cast<const float4*>(a.partial + pair * a.N + n);
+    add(a.weights[pair], v.x, v.y, v.z, v.w);
+  }
+  if (a.delta) {
+    for (int k = 0; k < a.topk; ++k) {
+      const int64_t pair = t * a.topk + k;
+      const int e = a.ids[pair];
+      if (e < 0 || e >= a.E) continue;
+      const __nv_bfloat16* d = a.delta + pair * a.delta_stride + n;
+      add(a.weights[pair], __bfloat162float(d[0]), __bfloat162float(d[1]), __bfloat162float(d[2]),
+          __bfloat162float(d[3]));
+    }
+  }
+  __nv_bfloat162 o[2] = {__floats2bfloat162_rn(sum.x, sum.y), __floats2bfloat162_rn(sum.z, sum.w)};
+  *reinterpret_cast<uint2*>(a.out + t * a.out_stride + n) = *reinterpret_cast<uint2*>(o);
+}
+
 }  // namespace
+
+// The split form reads each activation row once and shares all weights evenly, for a second kernel
+// and the partials' way through L2. It pays for 4-bit weights from a few pairs on, as theirs is the
+// work of the warps (128 experts of 2048 x 768, top 8, layer: 32 pairs 29.7 us against 28.8, 64 pairs
+// 44.3 against 48.9, 768 pairs 97 against 121), for bf16 where experts have many tokens (496 pairs
+// 202 us against 194, 1016 pairs 217 against 250).
+size_t moe_split_bytes(const MoeShape& s, int group) {
+  const int pairs = s.num_tokens * s.topk;
+  if (pairs <= 32 || (group == 0 && pairs < 6 * s.num_experts)) return 0;
+  return (size_t)pairs * s.hidden * sizeof(float);
+}
+
+cudaError_t launch_moe_down_split(const MoeShape& s, const void* act, const int32_t* topk_ids,
+                                  const float* topk_weights, const WeightRows& w, const void* delta,
+                                  int64_t delta_stride, void* workspace, void* out,
+                                  int64_t out_stride, bool chained, cudaStream_t stream) {
+  StreamArgs a = common_args(s, act, s.inter, topk_ids, w, delta, delta_stride, out, out_stride);
+  a.weights = topk_weights;
+  a.partial = static_cast<float*>(workspace);
+  a.N = s.hidden;
+  a.chained = chained;
+  const int entries = std::min(s.num_tokens * s.topk, s.num_experts);
+  if (!plan(a, w.group, kPairs, kSmem - list_bytes(s) - stream_smem(a, w.group), entries, g_sm_count))
+    return cudaErrorInvalidConfiguration;
+  const size_t smem = stream_smem(a, w.group) + list_bytes(s);
+  const cudaError_t e = launch_by_group(w.group, a, kPairs, g_sm_count, smem, stream);
+  if (e != cudaSuccess) return e;
+  const int columns = kCombineThreads * 4;
+  return launch_pdl(moe_combine_kernel, dim3((s.hidden + columns - 1) / columns, s.num_tokens),
+                    dim3(kCombineThreads), 0, stream, a);
+}
 
 cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_stride,
                                const int32_t* topk_ids, const WeightRows& w, const void* delta,

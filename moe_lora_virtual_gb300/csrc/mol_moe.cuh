@@ -618,7 +618,10 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
     }
     fence_mbar_init();
   }
-  pdl_wait();
+  // kPairs after this call's gate_up: only the tokens' rows are its work, the lists and the weights
+  // need not wait for it
+  const bool late = MODE == kPairs && a.chained;
+  if (!late) pdl_wait();
   pdl_launch_dependents();
   if (MODE != kLinear) {
     build_lists(a, lists, smem, false);
@@ -650,6 +653,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
 
   if (warp == consumer_warps(NT)) {
     // ---- the tokens' rows ----
+    if (late) pdl_wait();
     if (!(g_moe_test_stall & 1)) {
       int entry = entry0, ks = 0;
       int left = a.entry_rows - (lo - entry0 * a.entry_rows);  // pieces: rows of the entry to come
@@ -665,8 +669,9 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
         __syncwarp();
         for (int j = lane; j < en.n; j += 32) {
           int row = j;
-          if (MODE != kLinear) row = lists.pair(en.off + j) >> 16;
-          if (!MOL_CHECK(row < a.num_tokens, MOL_CHECK_ROW, row)) row = 0;
+          if (MODE == kGateUp) row = lists.pair(en.off + j) >> 16;
+          if (MODE == kPairs) row = lists.pair(en.off + j) & 0xFFFF;
+          if (!MOL_CHECK(row < (MODE == kPairs ? numel : a.num_tokens), MOL_CHECK_ROW, row)) row = 0;
           bulk_copy(xslots + s * a.xslot_bytes + j * a.x_pitch, a.x + row * a.x_stride + k0, len * 2,
                     &xfull[s]);
         }
@@ -913,6 +918,12 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
               v1 += __bfloat162float(dl[a.N]);
             }
             a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
+          } else if (MODE == kPairs) {
+            const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
+            if (!MOL_CHECK(pair < numel && cur.row + rows <= a.N, MOL_CHECK_ROW, pair)) continue;
+            float* o = a.partial + pair * a.N + n;
+            o[0] = v0;
+            if (g + 8 < rows) o[8] = v1;
           } else {
             if (!MOL_CHECK(cur.row + rows <= a.N, MOL_CHECK_COLUMN, cur.row)) continue;
             bf16* o = a.out + col * a.out_stride + n;
@@ -1215,6 +1226,7 @@ struct StreamLaunch {
   static cudaError_t launch(const StreamArgs& a, int mode, int grid, size_t smem,
                             cudaStream_t stream) {
     if (mode == kGateUp) return by_tiles<kGateUp>(a, grid, smem, stream);
+    if (mode == kPairs) return by_tiles<kPairs>(a, grid, smem, stream);
     if constexpr (G != 0) {
       if (mode == kLinear) return by_tiles<kLinear>(a, grid, smem, stream);
     }
@@ -1240,6 +1252,7 @@ struct StreamLaunch {
   // clusters[i] (may be NULL): how many clusters of 1 << i blocks the device holds at once
   static cudaError_t prepare(int* clusters) {
     cudaError_t e = prepare_mode<kGateUp>();
+    if (e == cudaSuccess) e = prepare_mode<kPairs>();
     if (e == cudaSuccess) e = prepare_mode<kDown>();
     if constexpr (G != 0) {
       if (e == cudaSuccess) e = prepare_mode<kLinear>();

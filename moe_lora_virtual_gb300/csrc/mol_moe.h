@@ -7,7 +7,7 @@
 
 namespace mol {
 
-enum StreamMode { kGateUp = 0, kDown = 1, kLinear = 2 };
+enum StreamMode { kGateUp = 0, kDown = 1, kLinear = 2, kPairs = 3 };  // kPairs: down's split form
 
 // Warps of a block of down; at 16 a thread may have 128 registers.
 constexpr int kBlockWarps = 16;
@@ -32,6 +32,7 @@ struct StreamArgs {
   const __nv_bfloat16* scales;
   const __nv_bfloat16* delta;
   __nv_bfloat16* out;      // act, or the output rows
+  float* partial;          // kPairs: [num_tokens * topk, N]
   int64_t x_stride, delta_stride, out_stride;
   int num_tokens, topk, E;
   int K;                   // contraction width

@@ -226,3 +226,29 @@ def test_oracle_norm_hand_worked():
     assert np.allclose(ro, [[1 + 3 / m, 1.0]])
     q = np.sqrt(((1 + 3 / m) ** 2 + 1) / 2)
     assert np.allclose(n, [[(1 + 3 / m) / q, 2 / q]])
+
+
+@needs_nvcc
+@pytest.mark.parametrize("kw,status", [
+    (dict(ws=None), -2), (dict(wsb=40 * 64 * 4 - 1), -2), (dict(ws=P(20)), UNSUPPORTED),
+    (dict(tw=None), INVALID), (dict(act=None), INVALID), (dict(T=129), UNSUPPORTED)])
+def test_split_refusals(mol, kw, status):
+    """40 pairs of 4-bit experts take the workspace of one fp32 row for each."""
+    assert mol.mol_moe_workspace_bytes(20, 2, 4, 64, 64, 32) == 40 * 64 * 4
+    a = dict(act=P(16), ids=P(16), tw=P(16), T=20, k=2, E=4, H=64, I=64, w=P(16), s=P(16), G=32,
+             d=None, ds=0, ws=P(16), wsb=40 * 64 * 4, out=P(16), os=64)
+    a.update(kw)
+    assert mol.library().mol_moe_down_split(*a.values(), None) == status
+    f = dict(x=P(16), xs=64, ids=P(16), tw=P(16), T=20, k=2, E=4, H=64, I=64, w=P(16), s=P(16),
+             w2=P(16), s2=P(16), G=32, act=P(16), ws=P(16), wsb=40 * 64 * 4, out=P(16), os=64)
+    f.update(kw)
+    assert mol.library().mol_moe_forward_split(*f.values(), None) == status
+
+
+@needs_nvcc
+def test_workspace_sizes(mol):
+    """Few pairs, and bf16 experts of few tokens, need none; nor do sizes that are refused."""
+    for shape in [(0, 8, 16, 64, 64, 32), (4, 8, 16, 64, 64, 32), (40, 8, 128, 64, 64, 0),
+                  (129, 1, 4, 64, 64, 32), (20, 2, 4, 60, 64, 32)]:
+        assert mol.mol_moe_workspace_bytes(*shape) == 0, shape
+    assert mol.mol_moe_workspace_bytes(40, 8, 16, 64, 64, 0) == 320 * 64 * 4

@@ -426,3 +426,41 @@ def test_wait_runs_out_sets_flag_then_device_recovers(env, group):
     assert flags == 1 and bool((act == 7.0).all())
     assert torch.equal(mol.mol_moe_forward(x, ids, weights, gu, dn), want)
     assert mol.mol_take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("group", FORMATS)
+@pytest.mark.parametrize("shape", [
+    (17, 4, 2, 200, 72, "plain"), (64, 6, 3, 520, 104, "hot"), (128, 3, 8, 264, 40, "dropped"),
+    (40, 5, 4, 2056, 264, "repeated"), (65, 1, 1, 72, 1032, "plain"), (33, 7, 2, 8, 8, "outside")],
+    ids=lambda s: "-".join(map(str, s)))
+def test_down_in_both_forms(env, shape, group, delta):
+    """The second half in one kernel and, with a workspace, as fp32 products and their sums."""
+    torch, mol = env
+    T, E, k, H, I, kind = shape
+    g = torch.Generator().manual_seed(11 + T + H + group)
+    ids, w = make_ids(torch, g, T, E, k, kind), torch.rand(T, k, generator=g) * 2 - 0.5
+    a = randn(torch, g, T * k, I)
+    a[(ids.flatten() < 0) | (ids.flatten() >= E)] = float("nan")
+    dn, dn64 = make_weights(torch, mol, g, (E, H), I, group)
+    d = randn(torch, g, T * k, H) if delta else None
+    want, mag = bo.moe_down(f64(a), ids.numpy(), f64(w), dn64, None if d is None else f64(d))
+    a, ids, w, d = a.cuda(), ids.cuda(), w.cuda(), None if d is None else d.cuda()
+    data, scales = (dn.qweight, dn.scales) if group else (dn, None)
+    out = torch.full((T, H), 5.0, dtype=torch.bfloat16, device="cuda")
+    args = [a.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, E, H, I, data.data_ptr(),
+            None if scales is None else scales.data_ptr(), group,
+            None if d is None else d.data_ptr(), 0 if d is None else H]
+    assert mol.library().mol_moe_down(*args, out.data_ptr(), H, None) == 0
+    close(out, want, ROUND * np.abs(want) + ACC * mag, "one kernel")
+    need = mol.mol_moe_workspace_bytes(T, k, E, H, I, group)
+    ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device="cuda")  # (fp32 NaN)
+    before = mol.mol_launch_count()
+    got = mol.mol_moe_down(a, ids, w, dn, delta=d, workspace=ws)
+    assert mol.mol_launch_count() - before == (2 if need else 1)
+    close(got, want, ROUND * np.abs(want) + ACC * mag, "with a workspace")
+    if need:
+        with pytest.raises(mol.MolError):
+            mol.mol_moe_down(a, ids, w, dn, delta=d, workspace=ws[:-4])
+        with pytest.raises(TypeError):
+            mol.mol_moe_down(a, ids, w, dn, delta=d, workspace=ws.cpu())
