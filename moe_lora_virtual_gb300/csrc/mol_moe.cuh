@@ -572,10 +572,17 @@ struct ScaleRange {
 };
 
 // Asynchronous copies of a lane, complete in the order of its groups. The first reads `bytes` of the 16
-// (0 or 16) and fills the rest with zeros.
+// (0 or 16) and fills the rest with zeros; WIDE: L2 brings the 256 bytes around (bf16 rows: 1 % of the
+// time of a memory-bound layer less, 4-bit rows 1 % more).
+template <bool WIDE>
 MOL_DEV void copy16(uint32_t dst, const char* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+  if constexpr (WIDE)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
 }
 template <int BYTES>
 MOL_DEV void copy_small(uint32_t dst, const char* src) {
@@ -769,8 +776,8 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const bool in = kW4 || o + u * 64 < left;  // past the row: zeros
-          copy16(dst + u * 512, in ? w0 + o + u * 64 : a.w, in ? 16 : 0);
-          copy16(dst + 1024 + u * 512, in ? w1 + o + u * 64 : a.w, in ? 16 : 0);
+          copy16<!kW4>(dst + u * 512, in ? w0 + o + u * 64 : a.w, in ? 16 : 0);
+          copy16<!kW4>(dst + 1024 + u * 512, in ? w1 + o + u * 64 : a.w, in ? 16 : 0);
         }
         if (kW4 && t < 2)
           copy_small<512 / GG>(ring + slot * kChunk + 2048 + (t * 8 + g) * (512 / GG),
