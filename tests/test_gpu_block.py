@@ -464,3 +464,66 @@ def test_down_in_both_forms(env, shape, group, delta):
             mol.mol_moe_down(a, ids, w, dn, delta=d, workspace=ws[:-4])
         with pytest.raises(TypeError):
             mol.mol_moe_down(a, ids, w, dn, delta=d, workspace=ws.cpu())
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_example_model_step(env, group):
+    """A step of the example model: a graph's replay equals the calls, and the logits those of the
+    same step in float64 with bf16 rounding where the model holds bf16. Each such rounding is at
+    most ROUND / 2 of its value; a layer has fewer than ten in a row and the norms keep magnitudes
+    near one, so 2 layers and the head stay below 32 roundings, taken in the mean square."""
+    import importlib.util
+    import os
+    torch, mol = env
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decode_layers.py")
+    spec = importlib.util.spec_from_file_location("decode_layers", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    T, k, E, L = 13, 4, 32, 4
+    model = example.Model(tokens=T, group=group, seed=3)
+    g = torch.Generator().manual_seed(4)
+    tokens = torch.randint(0, 5000, (T,), generator=g).cuda()
+    lora = torch.randint(-1, L, (T,), generator=g).to(torch.int32).cuda()
+    got = model(tokens, lora)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = model(tokens, lora)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, got)
+
+    def dense(w):
+        return mol.w4_unpack(w).double() if isinstance(w, mol.W4) else w.double()
+
+    def rms(v, w):
+        return (v * w.double() * torch.rsqrt((v * v).mean(-1, keepdim=True) + 1e-6))
+
+    residual, y = model.embed[tokens].double(), 0.0
+    for lay in model.layers:
+        residual = (residual + y).bfloat16().double()
+        x = rms(residual, lay.norm).bfloat16().double()
+        # the choice is the device's: it is exact for its own logits, and ties within a rounding
+        ids, w = mol.mol_moe_route(x.bfloat16() @ lay.router.T, k)
+        gu, dn = dense(lay.gate_up), dense(lay.down)
+        y = torch.zeros_like(x)
+        for t in range(T):
+            for j in range(k):
+                e, l = int(ids[t, j]), int(lora[t])
+                h, v = gu[e] @ x[t], e + l * E
+                if l >= 0:
+                    r = lay.b_gu.shape[-1]
+                    a = (lay.a_gu[v].double() @ x[t]).view(2, r)
+                    h = h + lay.scale * torch.cat([lay.b_gu[v, s * (len(h) // 2):][:len(h) // 2].double() @ a[s]
+                                                   for s in range(2)])
+                gate, up = h.chunk(2)
+                act = (gate * torch.sigmoid(gate) * up).bfloat16().double()
+                o = dn[e] @ act
+                if l >= 0:
+                    o = o + lay.scale * (lay.b_dn[v].double() @ (lay.a_dn[v].double() @ act))
+                y[t] += w[t, j].double() * o
+        y = y.bfloat16().double()
+    residual = (residual + y).bfloat16().double()
+    want = rms(residual, model.norm).bfloat16().double() @ dense(model.head).T
+    err = ((got.double() - want).square().mean() / want.square().mean()).sqrt().item()
+    assert err < 32 ** 0.5 * ROUND / 2, err
