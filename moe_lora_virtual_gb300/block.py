@@ -16,6 +16,11 @@ import torch
 
 import moe_lora_virtual_gb300 as _mol
 
+try:  # the common case of each call in one native step; None from it: the Python path below
+    from . import _block_native as _native
+except ImportError:
+    _native = None
+
 BLOCK_EXPORTS = ("mol_block_norm", "mol_moe_route", "mol_moe_gate_up", "mol_moe_down",
                  "mol_moe_forward", "mol_moe_workspace_bytes", "mol_moe_down_split",
                  "mol_moe_forward_split", "mol_w4_linear")
@@ -163,6 +168,10 @@ def _weights(w: Weights, name: str, lead, K: int):
     return _flat(w, _bf16, name, (*lead, K)), None, 0
 
 
+def _native_weights(w: Weights):
+    return w if isinstance(w, W4) else (w, None, w.shape[-1], 0)
+
+
 def _lead(w: Weights) -> torch.Size:
     return (w.qweight if isinstance(w, W4) else w).shape[:-1]
 
@@ -191,6 +200,15 @@ def _call(name: str, *args) -> None:
         raise _mol.MolError(name, status)
 
 
+def _entry(name: str) -> int:
+    """Address of a C entry point of the library in use."""
+    lib = _mol._lib or _mol.library()
+    addresses = lib.__dict__.setdefault("_block_entries", {})
+    if name not in addresses:
+        addresses[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    return addresses[name]
+
+
 def _stream(stream, t: torch.Tensor) -> int:
     """The stream given, or the current one of the tensor's device."""
     if stream is None:
@@ -208,6 +226,11 @@ def mol_block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: Optional
     y, residual bf16 [T, H]; post_weight, pre_weight bf16 [H] or None; gate bf16 [H], [T, H] or
     None. Returns (residual_out, normed); normed is None without pre_weight. residual_out may be
     `residual`, normed may be `y`."""
+    if _native is not None and residual_out is None and normed is None and stream is None:
+        done = _native.block_norm(_entry("mol_block_norm"), y, residual, pre_weight, post_weight,
+                                  gate, residual_scale, eps)
+        if done is not None:
+            return done
     shape = T, H = y.shape
     ys = _rows(y, _bf16, "y")
     rs = _rows(residual, _bf16, "residual")
@@ -245,6 +268,10 @@ def mol_moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True, sca
                   topk_ids: Optional[torch.Tensor] = None,
                   topk_weights: Optional[torch.Tensor] = None, stream=None):
     """(topk_ids int32, topk_weights fp32), [T, topk] each, of router logits fp32 or bf16 [T, E]."""
+    if _native is not None and topk_ids is None and topk_weights is None and stream is None:
+        done = _native.moe_route(_entry("mol_moe_route"), logits, topk, int(renormalize), scale)
+        if done is not None:
+            return done
     bf16 = logits.dtype == _bf16
     stride = _rows(logits, _bf16 if bf16 else _f32, "logits")
     T, E = logits.shape
@@ -265,6 +292,11 @@ def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
 
     x bf16 [T, H]; topk_ids int32 [T, topk]; w_gate_up bf16 [E, 2I, H] or W4; delta bf16
     [T * topk, 2I]: rows a LoRA gate_up stage added into zeros."""
+    if _native is not None and act is None and stream is None:
+        done = _native.moe_gate_up(_entry("mol_moe_gate_up"), x, topk_ids, *_native_weights(w_gate_up),
+                                   delta)
+        if done is not None:
+            return done
     (T, H), k = x.shape, topk_ids.shape[1]
     E, I2 = _lead(w_gate_up)
     wp, sp, group = _weights(w_gate_up, "w_gate_up", (E, I2), H)
@@ -304,6 +336,11 @@ def mol_moe_down(act: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
 
     act bf16 [T * topk, I]; w_down bf16 [E, H, I] or W4; delta bf16 [T * topk, H]: rows a LoRA down
     stage added into zeros; workspace: mol_moe_workspace_bytes of scratch."""
+    if _native is not None and out is None and workspace is None and stream is None:
+        done = _native.moe_down(_entry("mol_moe_down_split"), _entry("mol_moe_workspace_bytes"), act,
+                                topk_ids, topk_weights, *_native_weights(w_down), delta)
+        if done is not None:
+            return done
     T, k = topk_ids.shape
     E, H = _lead(w_down)
     I = act.shape[1]
@@ -327,6 +364,13 @@ def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
     x bf16 [T, H]; topk_ids int32 and topk_weights fp32 [T, topk]; weights bf16 [E, 2I, H] and
     [E, H, I], or both W4 of one group; scratch: act bf16 [T * topk, I], workspace of
     mol_moe_workspace_bytes."""
+    if (_native is not None and out is None and act is None and workspace is None
+            and stream is None):
+        done = _native.moe_forward(_entry("mol_moe_forward_split"),
+                                   _entry("mol_moe_workspace_bytes"), x, topk_ids, topk_weights,
+                                   *_native_weights(w_gate_up), *_native_weights(w_down))
+        if done is not None:
+            return done
     (T, H), k = x.shape, topk_ids.shape[1]
     E, I2 = _lead(w_gate_up)
     I = I2 // 2
@@ -351,6 +395,10 @@ def mol_w4_linear(x: torch.Tensor, w: W4, out: Optional[torch.Tensor] = None,
     """out [T, N] = x [T, K] . w^T with 4-bit weight rows [N, K]."""
     if not isinstance(w, W4):
         raise TypeError("w: expected W4")
+    if _native is not None and out is None and stream is None:
+        done = _native.w4_linear(_entry("mol_w4_linear"), x, *w)
+        if done is not None:
+            return done
     T, K = x.shape
     (N,) = _lead(w)
     wp, sp, group = _weights(w, "w", (N,), K)

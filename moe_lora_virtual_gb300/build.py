@@ -1,10 +1,16 @@
-"""Build libmol.so (the MoL LoRA CUDA library) in-tree with nvcc for sm_103a."""
+"""Build libmol.so (the MoL LoRA CUDA library) in-tree with nvcc for sm_103a.
+
+Beside it _block_native.so, the native calls of the MoE block's binding: plain C++ against
+PyTorch's headers. Without it (no compiler for them, or another PyTorch) the binding takes its
+Python path, which gives the same results."""
 
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -13,6 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libmol.so")
 # The same sources with device-side index checks (MOL_CHECKED): a diagnostic build.
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libmol_checked.so")
+NATIVE_PATH = os.path.join(PKG_DIR, "_block_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "mol_block_py.cpp")
 
 SOURCES = ["mol_abi.cu", "mol_align.cu", "mol_lora.cu", "mol_umma.cu", "mol_stage.cu",
            "mol_expand_tc.cu", "mol_block_abi.cu", "mol_block.cu", "mol_moe.cu",
@@ -32,7 +40,9 @@ def _stale(path: str) -> bool:
     if not os.path.exists(path):
         return True
     t = os.path.getmtime(path)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
+    sources = ([NATIVE_SOURCE] if path == NATIVE_PATH
+               else [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
+    deps = sources + [
         os.path.join(INCLUDE, "mol.h"), os.path.join(INCLUDE, "mol_block.h"),
         os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
@@ -46,6 +56,20 @@ def _command(out: str, checked: bool, verbose: bool) -> list:
     if verbose:
         cmd += ["-Xptxas", "-v"]
     return cmd + [os.path.join(CSRC, f) for f in SOURCES]
+
+
+def _native_command(out: str) -> list:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    dirs = [INCLUDE, os.path.join(home, "include"),
+            os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[a for d in dirs for a in ("-I", d)], NATIVE_SOURCE, "-o", out,
+            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build_library(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
@@ -67,7 +91,7 @@ def build_library(force: bool = False, verbose: bool = False, checked: bool = Fa
 
 
 def build_all(force: bool = False) -> tuple:
-    """Build the release and the checked library at the same time (two nvcc processes)."""
+    """Build the release and the checked library and the native calls at the same time."""
     jobs = []
     for checked in (False, True):
         path = CHECKED_LIB_PATH if checked else LIB_PATH
@@ -76,13 +100,20 @@ def build_all(force: bool = False) -> tuple:
             jobs.append((path, tmp, subprocess.Popen(_command(tmp, checked, False),
                                                      stdout=subprocess.PIPE,
                                                      stderr=subprocess.STDOUT, text=True)))
+    if force or _stale(NATIVE_PATH):
+        tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+        jobs.append((NATIVE_PATH, tmp, subprocess.Popen(_native_command(tmp),
+                                                        stdout=subprocess.PIPE,
+                                                        stderr=subprocess.STDOUT, text=True)))
     errors = []
     for path, tmp, proc in jobs:
         out, _ = proc.communicate()
-        if proc.returncode != 0:
-            errors.append(f"{os.path.basename(path)}:\n{out}")
-        else:
+        if proc.returncode == 0:
             os.replace(tmp, path)
+        elif path == NATIVE_PATH:
+            warnings.warn(f"{os.path.basename(path)} was not built:\n{out}")
+        else:
+            errors.append(f"{os.path.basename(path)}:\n{out}")
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     return LIB_PATH, CHECKED_LIB_PATH

@@ -252,3 +252,24 @@ def test_workspace_sizes(mol):
                   (129, 1, 4, 64, 64, 32), (20, 2, 4, 60, 64, 32)]:
         assert mol.mol_moe_workspace_bytes(*shape) == 0, shape
     assert mol.mol_moe_workspace_bytes(40, 8, 16, 64, 64, 0) == 320 * 64 * 4
+
+
+@needs_nvcc
+def test_native_calls_leave_everything_unusual_to_the_python_path(mol):
+    """Wrong kinds, counts, types, devices: None, and no exception is left behind."""
+    native = pytest.importorskip("moe_lora_virtual_gb300._block_native")
+    import torch
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    ids = torch.zeros(2, 1, dtype=torch.int32)
+    f = ctypes.cast(mol.library().mol_block_norm, ctypes.c_void_p).value
+    for name, args in [("block_norm", (f, x, x, None, None, None, 1.0, 1e-6)),
+                       ("moe_route", (f, x, 1, 1, 1.0)),
+                       ("moe_gate_up", (f, x, ids, w, None, 64, 0, None)),
+                       ("moe_down", (f, f, x, ids, x, w, None, 64, 0, None)),
+                       ("moe_forward", (f, f, x, ids, x, w, None, 64, 0, w, None, 64, 0)),
+                       ("w4_linear", (f, x, x, x, 64, 32))]:
+        call = getattr(native, name)
+        for bad in [args, args[:-1], (), (0, *args[1:]), (None, *args[1:]), (f, None, *args[2:]),
+                    (f, "x", *args[2:]), (2 ** 80, *args[1:]), tuple([x] * len(args)),
+                    (*args[:-1], 2 ** 70), (*args[:-1], "x")]:
+            assert call(*bad) is None, (name, bad)

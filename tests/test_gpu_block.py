@@ -527,3 +527,54 @@ def test_example_model_step(env, group):
     want = rms(residual, model.norm).bfloat16().double() @ dense(model.head).T
     err = ((got.double() - want).square().mean() / want.square().mean()).sqrt().item()
     assert err < 32 ** 0.5 * ROUND / 2, err
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_native_calls_equal_the_python_path(env, group, monkeypatch):
+    torch, mol = env
+    from moe_lora_virtual_gb300 import block
+    assert block._native is not None, "the native calls are not built"
+    g = torch.Generator().manual_seed(9)
+    T, E, k, H, I = 21, 6, 2, 264, 72
+    x, r, gate, w = (randn(torch, g, *s).cuda() for s in ((T, H), (T, H), (T, H), (H,)))
+    gu, _ = make_weights(torch, mol, g, (E, 2 * I), H, group)
+    dn, _ = make_weights(torch, mol, g, (E, H), I, group)
+    head, _ = make_weights(torch, mol, g, (40,), H, group or 32)
+    d = randn(torch, g, T * k, 2 * I).cuda(), randn(torch, g, T * k, H).cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    taken = []
+    real = block._native
+
+    class Count:
+        def __getattr__(self, name):
+            def call(*a):
+                out = getattr(real, name)(*a)
+                taken.append(out is not None)
+                return out
+            return call
+
+    def everything(x, r):
+        out = [*mol.mol_block_norm(x, r, w, post_weight=w, gate=gate, residual_scale=0.5, eps=1e-5),
+               mol.mol_block_norm(x, r, None, gate=w)[0]]
+        ids, tw = mol.mol_moe_route(logits, k, renormalize=False, scale=2.0)
+        act = mol.mol_moe_gate_up(x, ids, gu)
+        return out + [ids, tw, act, mol.mol_moe_gate_up(x, ids, gu, delta=d[0]),
+                      mol.mol_moe_down(act, ids, tw, dn), mol.mol_moe_down(act, ids, tw, dn, delta=d[1]),
+                      mol.mol_moe_forward(x, ids, tw, gu, dn), mol.mol_w4_linear(x, head),
+                      *mol.mol_moe_route(logits.to(torch.bfloat16), 1)]
+
+    monkeypatch.setattr(block, "_native", Count())
+    got = everything(x, r)
+    assert len(taken) == 10 and all(taken)
+    taken.clear()
+    wide = everything(strided(torch, x.cpu()), r)  # rows with a stride: not the native calls' case
+    assert taken.count(False) == 6
+    monkeypatch.setattr(block, "_native", None)
+    for a, b, c in zip(got, wide, everything(x, r)):
+        assert a.dtype == b.dtype == c.dtype and torch.equal(a, c) and torch.equal(b, c)
+    monkeypatch.setattr(block, "_native", real)
+    with pytest.raises(ValueError):
+        mol.mol_moe_forward(x, torch.zeros(T, k, dtype=torch.int32, device="cuda"),
+                            torch.zeros(T, k + 1, device="cuda"), gu, dn)
+    with pytest.raises(mol.MolError):
+        mol.mol_moe_route(logits, E + 1)
