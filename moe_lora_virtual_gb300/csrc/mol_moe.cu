@@ -42,9 +42,9 @@ int entry_tokens(int num_tokens, int pairs, int experts) {
 
 int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : xrows <= 32 ? 4 : 8; }
 
-// The ring is the lists' scratch first, 20 KB at most: sixteen stages of this size hold it, and rings
-// of fewer are larger.
-constexpr int kLeastStage = 1280;
+// down: the ring is the lists' scratch first, 36 KB at most: sixteen stages of this size hold it, and
+// rings of fewer are larger.
+constexpr int kLeastStage = 2304;
 
 // Rows of Kc inputs in a stage: as they lie in memory (one copy), or pieces of them (a copy each).
 void row_layout(StreamArgs& a, int group, int rows, int Kc) {

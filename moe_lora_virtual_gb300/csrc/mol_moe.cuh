@@ -48,9 +48,9 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kExpertsPerThread = 4;
-constexpr int kListThreads = MOL_MOE_MAX_EXPERTS / kExpertsPerThread;  // of the block's first warps
+constexpr int kListThreads = 512;  // of the block's first warps
 constexpr int kListWarps = kListThreads / 32;
+constexpr int kExpertsPerThread = MOL_MOE_MAX_EXPERTS / kListThreads;
 constexpr int kPairsPerThread = MOL_MOE_MAX_PAIRS / kListThreads;
 constexpr uint32_t kWaitPolls = 1u << 22;
 
@@ -121,7 +121,7 @@ struct Lists {
 
 // Groups the pairs by expert, in the order of their index: every block finds the same entries, so
 // blocks that hold different rows of one expert agree on which entry has which pair. An expert with
-// more than xrows pairs (a power of two) takes several entries. `scratch`: 16 E + 4 numel bytes,
+// more than xrows pairs (a power of two) takes several entries. `scratch`: 32 E + 4 numel bytes,
 // free again afterwards. The block waits for nothing but its own ids, and the code is kept short: it
 // runs once a launch, from cold instruction caches.
 MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weights) {
@@ -210,17 +210,22 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     }
   }
   __syncthreads();
-  // Counts before each warp's pairs, then (count, entries) offsets of the experts in 16 bits each.
-  int c[kExpertsPerThread], sum = 0;
+  // Counts before each warp's pairs, then (count, entries) offsets of the experts in 16 bits each. A
+  // thread's experts are neighbours, one where they suffice (all warps' counts are then loaded at
+  // once: what this step takes is the latency of its chains).
+  const int per = a.E > kListThreads ? kExpertsPerThread : 1;
+  int c[kExpertsPerThread], before_warp[kExpertsPerThread][kListWarps], sum = 0;
 #pragma unroll
   for (int j = 0; j < kExpertsPerThread; ++j) {
-    const int e = tid * kExpertsPerThread + j;  // (threads past the lists' have none)
+    const int e = tid * per + j;  // (threads past the lists' have none)
+    const bool has = j < per && e < a.E && tid < kListThreads;
     c[j] = 0;
-    if (e >= a.E) continue;
-#pragma unroll 1
-    for (int w = 0; w < used; ++w) {
-      const int n = cnt[w * a.E + e];
-      cnt[w * a.E + e] = (uint16_t)c[j];
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w) before_warp[j][w] = has && w < used ? cnt[w * a.E + e] : 0;
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w) {
+      const int n = before_warp[j][w];
+      before_warp[j][w] = c[j];
       c[j] += n;
     }
     sum += c[j] | ((c[j] + a.xrows - 1) >> xlog) << 16;
@@ -252,12 +257,13 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
   }
 #pragma unroll
   for (int j = 0; j < kExpertsPerThread; ++j) {
-    const int e = tid * kExpertsPerThread + j;
+    const int e = tid * per + j;
     if (c[j] == 0) continue;
     const int off = at & 0xFFFF;
     int idx = at >> 16;
-#pragma unroll 1
-    for (int w = 0; w < used; ++w) cnt[w * a.E + e] += (uint16_t)off;
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w)
+      if (w < used) cnt[w * a.E + e] = (uint16_t)(off + before_warp[j][w]);
 #pragma unroll 1
     for (int o = 0; o < c[j]; o += a.xrows, ++idx) {
       if (!MOL_CHECK(idx < numel, MOL_CHECK_SMEM, idx)) continue;
