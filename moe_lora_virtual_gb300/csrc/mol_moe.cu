@@ -61,14 +61,24 @@ void row_layout(StreamArgs& a, int group, int rows, int Kc) {
   a.x_pitch = align_up(Kc * 2, 128) + 64;
 }
 
-// gate_up, linear: the token slots and the teams of a block that has `room` bytes beside its rings,
-// when the blocks share `entries` entries. False when nothing fits.
+// Bytes of gate_up's and the linear's rings, token slots and sums.
+int stream_smem(const StreamArgs& a, int group) {
+  const int nt = token_tiles(a.xrows);
+  return consumer_warps(nt) * a.chunks * chunk_bytes(group) + a.xstages * a.xslot_bytes +
+         a.teams * (a.parts - 1) * nt * 512;
+}
+
+// gate_up, linear: the token slots and the teams of a block that has `room` bytes, when the blocks
+// share `entries` entries. False when nothing fits.
+// Slots: whole rows where they fit, if need be beside rings of two chunks (16 tokens of 4096 inputs and
+// 20000 rows 19.8 us; pieces beside rings of four, which read the tokens again for each group of tiles,
+// 28.2).
 // Teams: the warps of a team split the inputs of a tile, so more parts fill all warps where a block has
 // few tiles, and leave less to wait for at the end; against that each tile costs its warps half a
-// chunk's time, or two for each token tile where their sums are to be added. Taken is the
-// least of that model, with one more tile a warp for the end: measured, an output head of 49 tiles a
-// block takes 29.5 us with one part and 36 with four, a linear of one tile a block 5.5 us with one
-// and 4.1 with four.
+// chunk's time, or two for each token tile where their sums are to be added. Taken is the least of that
+// model, with one more tile a warp for the end: measured, an output head of 49 tiles a block takes
+// 29.5 us with one part and 36 with four, a linear of one tile a block 5.5 us with one and 4.1 with
+// four.
 bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
   const int inputs = group ? 256 : 64, nt = token_tiles(a.xrows);
   a.tile_rows = mode == kGateUp ? 8 : 16;
@@ -79,25 +89,25 @@ bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
   for (int parts = 1; parts <= consumer_warps(nt); ++parts) {
     a.parts = parts;
     a.teams = consumer_warps(nt) / parts;
-    const int left = room - a.teams * (parts - 1) * nt * 512;
-    auto slots = [&](int Kc, int n) {
+    auto slots = [&](int Kc, int n, int chunks) {
       a.Kc = Kc;
       a.ksteps = (a.K + Kc - 1) / Kc;
       a.x_pitch = align_up(Kc * 2, 128) + 64;
       a.xslot_bytes = align_up(a.xrows * a.x_pitch, 128);
       a.xstages = n;
-      return n * a.xslot_bytes <= left;
+      a.chunks = chunks;
+      return stream_smem(a, group) <= room;
     };
-    // whole rows; a second token slot lets the next expert's tokens come while the last one's weights
-    // are consumed. Else pieces.
-    bool fits = (entries > 1 && slots(a.K, 2)) || slots(a.K, 1);
-    for (int Kc = 2048; Kc >= 256 && !fits; Kc -= 256) fits = Kc < a.K && slots(Kc, 2);
-    fits = fits || slots(std::min(256, a.K), 1);
+    // a second token slot lets the next expert's tokens come while the last one's weights are consumed
+    bool fits = (entries > 1 && slots(a.K, 2, kChunks)) || slots(a.K, 1, kChunks);
+    fits = fits || slots(a.K, 1, 2);
+    for (int Kc = 2048; Kc >= 256 && !fits; Kc -= 256) fits = Kc < a.K && slots(Kc, 2, kChunks);
+    fits = fits || slots(std::min(256, a.K), 1, kChunks);
     if (!fits) continue;
     const int per = (std::min(a.Kc, a.K) + inputs - 1) / inputs;
-    const double one = a.ksteps * ((per + parts - 1) / parts) + (parts > 1 ? 2 * nt - 0.5 : 0.5);
+    const double one = a.ksteps * ((per + parts - 1) / parts) + (parts > 1 ? 2 * nt : 0.5);
     const double rounds = block_tiles / a.teams;
-    const double cost = (std::max(1.0, (rounds + std::ceil(rounds)) / 2) + 1) * one;
+    const double cost = (std::max(1.0, (rounds + 2 * std::ceil(rounds)) / 3) + 1) * one;
     if (best.parts && cost > least) continue;
     least = cost;
     best = a;
@@ -106,11 +116,6 @@ bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
   a = best;
   a.entry_rows = align_up(a.N, a.tile_rows * (a.ksteps > 1 ? a.teams : 1));
   return true;
-}
-
-int stream_smem(const StreamArgs& a, int group) {
-  return consumer_warps(token_tiles(a.xrows)) * kChunks * chunk_bytes(group) + a.xstages * a.xslot_bytes +
-         a.teams * (a.parts - 1) * token_tiles(a.xrows) * 512;
 }
 
 // down: the stage and the teams of a block of `rows` output rows, with `fixed` bytes of lists and
@@ -215,7 +220,7 @@ cudaError_t launch_moe_down_split(const MoeShape& s, const void* act, const int3
   a.N = s.hidden;
   a.chained = chained;
   const int entries = std::min(s.num_tokens * s.topk, s.num_experts);
-  if (!plan(a, w.group, kPairs, kSmem - list_bytes(s) - stream_smem(a, w.group), entries, g_sm_count))
+  if (!plan(a, w.group, kPairs, kSmem - list_bytes(s), entries, g_sm_count))
     return cudaErrorInvalidConfiguration;
   const size_t smem = stream_smem(a, w.group) + list_bytes(s);
   const cudaError_t e = launch_by_group(w.group, a, kPairs, g_sm_count, smem, stream);
@@ -231,7 +236,7 @@ cudaError_t launch_moe_gate_up(const MoeShape& s, const void* x, int64_t x_strid
   StreamArgs a = common_args(s, x, x_stride, topk_ids, w, delta, delta_stride, act, s.inter);
   a.N = s.inter;
   const int entries = std::min(s.num_tokens * s.topk, s.num_experts);
-  if (!plan(a, w.group, kGateUp, kSmem - list_bytes(s) - stream_smem(a, w.group), entries, g_sm_count))
+  if (!plan(a, w.group, kGateUp, kSmem - list_bytes(s), entries, g_sm_count))
     return cudaErrorInvalidConfiguration;
   const size_t smem = stream_smem(a, w.group) + list_bytes(s);
   return launch_by_group(w.group, a, kGateUp, g_sm_count, smem, stream);
@@ -301,7 +306,7 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   a.N = N;
   a.xrows = num_tokens;
   const int grid = std::min((N + 15) / 16, g_sm_count);
-  if (!plan(a, w.group, kLinear, kSmem - stream_smem(a, w.group), 1, grid))
+  if (!plan(a, w.group, kLinear, kSmem, 1, grid))
     return cudaErrorInvalidConfiguration;
   return launch_by_group(w.group, a, kLinear, grid, stream_smem(a, w.group), stream);
 }

@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
 
   // shared memory: rings | token slots | sums of a team's warps | lists
   const uint32_t rings = smem_u32(smem);
-  const uint32_t xslots = rings + consumer_warps(NT) * kChunks * kChunk;
+  const uint32_t xslots = rings + consumer_warps(NT) * a.chunks * kChunk;
   const uint32_t sums = xslots + a.xstages * a.xslot_bytes;
   Lists lists;
   lists.entry = sums + a.teams * (a.parts - 1) * NT * 512;
@@ -730,10 +730,11 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       return c.row >= a.N ? 0 : (min(a.Kc, a.K - c.ks * a.Kc) + kInputs - 1) / kInputs;
     };
 
-    // The warp's weights, chunk after chunk of its tiles, asked for kChunks - 1 ahead of their use.
+    // The warp's weights, chunk after chunk of its tiles, asked for a.chunks - 1 ahead of their use.
     // Every lane copies what it reads itself (its rows' 16 bytes of each block), so a chunk has
     // landed when the lane's own copies have; scales: a lane for each row.
-    const uint32_t ring = rings + warp * kChunks * kChunk;
+    const uint32_t ring = rings + warp * a.chunks * kChunk;
+    const int last_slot = a.chunks - 1;  // (a power of two less one)
     Cursor ahead = cur;
     int next = part, count = 0;  // chunk of ahead's step, how many it has
     const char *w0 = nullptr, *w1 = nullptr, *ws = nullptr;
@@ -797,8 +798,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       if (next < (count = chunks_of(ahead))) aim();
       else advance();
     }
-#pragma unroll
-    for (int i = 0; i < kChunks - 1; ++i) fetch(i);
+    for (int i = 0; i < last_slot; ++i) fetch(i);
 
     float acc[NT][4];
 #pragma unroll
@@ -835,11 +835,12 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       const int chunks = fault ? 0 : chunks_of(cur), len = min(a.Kc, a.K - cur.ks * a.Kc);
 #pragma unroll 1
       for (int c = part; c < chunks; c += parts) {
-        cp_async_wait_group<kChunks - 2>();
+        if (last_slot == kChunks - 1) cp_async_wait_group<kChunks - 2>();
+        else cp_async_wait_group<0>();
         __syncwarp();  // the row's scales have landed too; the chunk before has been read by all
-        fetch((slot + kChunks - 1) % kChunks);
+        fetch((slot + last_slot) & last_slot);
         const uint32_t st = ring + slot * kChunk;
-        slot = (slot + 1) % kChunks;
+        slot = (slot + 1) & last_slot;
         auto multiply = [&](auto tiles) {
           constexpr int NTC = decltype(tiles)::value;
           if constexpr (kW4) {

@@ -14,8 +14,8 @@ constexpr int kBlockWarps = 16;
 // gate_up, linear: consumer warps of a block, by its token tiles. One more brings the tokens' rows; a
 // seventeenth warp lowers the registers of a thread to 96, too few for many tokens' sums.
 __host__ __device__ constexpr int consumer_warps(int token_tiles) { return token_tiles <= 2 ? 16 : 15; }
-// gate_up, linear: a warp's ring of chunks. A chunk is 128 bytes of each of a tile's 16 weight rows, and
-// their scales.
+// gate_up, linear: a warp's ring of chunks (of 2 where tokens need the room). A chunk is 128 bytes of
+// each of a tile's 16 weight rows, and their scales.
 constexpr int kChunks = 4;
 __host__ __device__ constexpr int chunk_bytes(int group) { return 2048 + (group ? 16 * 512 / group : 0); }
 constexpr int kMaxStages = 32;  // of all teams of a block
@@ -49,6 +49,7 @@ struct StreamArgs {
   int row_pitch, scale_off, scale_pitch, stage_bytes, stages;
   // `xrows` activation rows of Kc inputs: a token slot, or at x_off of a stage (down)
   int xrows, x_pitch, xslot_bytes, xstages, x_off;
+  int chunks;              // gate_up, linear: of a warp's ring
   int teams, parts;        // teams of `parts` warps in use; the teams divide the stages
   int parts_off;           // gate_up, linear: of the partial sums inside a stage
   int acc_stride;          // down: floats between tokens of a team's sums
