@@ -31,16 +31,18 @@ cudaError_t launch_by_group(int group, const StreamArgs& a, int mode, int grid, 
 // experts need a second entry (which reads their weights again), and no more room than the tokens
 // need. From 8 on, where twice as many cost a second token tile, a tenth more than the mean suffices
 // (128 experts, 4 bits: 96 tokens 120 us at 8 and 131 at 16, 127 tokens 148 and 165; bf16: 110 tokens
-// 224 and 237, 127 tokens 273 and 243).
+// 224 and 237, 127 tokens 273 and 243). Never more than 16: the sums of 32 or 64 tokens in registers
+// cost more than a second entry's weights, which come from L2 (8 experts, 128 tokens, top 2: bf16
+// 39.3 us at 16, 39.5 at 32, 61 at 64; 4 bits 31.5, 42 and 87).
 int entry_tokens(int num_tokens, int pairs, int experts) {
   int n = num_tokens == 1 ? 1 : num_tokens == 2 ? 2 : 4;
-  while (n < 64 && n < num_tokens &&
+  while (n < 16 && n < num_tokens &&
          (n < 8 ? 2 * n * experts < 3 * pairs : 10 * n * experts < 11 * pairs))
     n *= 2;
   return n;
 }
 
-int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : xrows <= 32 ? 4 : 8; }
+int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : 4; }
 
 // down: the ring is the lists' scratch first, 36 KB at most: sixteen stages of this size hold it, and
 // rings of fewer are larger.
@@ -304,10 +306,27 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   const MoeShape s{num_tokens, 1, 1, N, w.K};
   StreamArgs a = common_args(s, x, x_stride, nullptr, w, nullptr, 0, out, out_stride);
   a.N = N;
-  a.xrows = num_tokens;
-  const int grid = std::min((N + 15) / 16, g_sm_count);
-  if (!plan(a, w.group, kLinear, kSmem, 1, grid))
-    return cudaErrorInvalidConfiguration;
+  // More tokens than 16 are entries of 16, which read the weights again, mostly from L2; up to 32 with
+  // many rows one entry (100001 rows, 2048 inputs, 32 tokens: 51 us in one, 60 in two; 2000 rows: 10.6
+  // and 7.3; 1024 inputs, 64 tokens: 60 us in four, 61 in two, 77 in one). Entries are smaller yet
+  // where their whole rows then fit (64 tokens of 8192 inputs, 20000 rows: 140 us in eight, 268 in
+  // pieces).
+  const int tiles = (N + 15) / 16;
+  int grid = 0;
+  auto fits = [&](int rows) {
+    a.xrows = rows;
+    const int entries = (num_tokens + rows - 1) / rows;
+    grid = (int)std::min<int64_t>((int64_t)tiles * entries, g_sm_count);
+    return plan(a, w.group, kLinear, kSmem, entries, grid);
+  };
+  const int most = num_tokens <= 32 && tiles >= 4 * g_sm_count ? 32 : 16;
+  bool ok = fits(std::min(num_tokens, most));
+  if (ok && a.ksteps > 1) {
+    for (int rows = most; rows >= (num_tokens < 32 ? 8 : 4) && a.ksteps > 1; rows /= 2)
+      if (rows < num_tokens) ok = fits(rows);
+    if (!ok || a.ksteps > 1) ok = fits(std::min(num_tokens, most));
+  }
+  if (!ok) return cudaErrorInvalidConfiguration;
   return launch_by_group(w.group, a, kLinear, grid, stream_smem(a, w.group), stream);
 }
 

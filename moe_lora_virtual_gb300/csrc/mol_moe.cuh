@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
   lists.entry = sums + a.teams * (a.parts - 1) * NT * 512;
   lists.order = lists.entry + (MODE == kLinear ? 0 : numel * 8);
   lists.weight = 0;
-  lists.count = 1;
+  lists.count = (a.num_tokens + a.xrows - 1) / a.xrows;  // (linear: entries of its tokens in order)
   lists.repeated = false;
 
   if (warp == consumer_warps(NT)) {
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   auto entry_of = [&](int i) {
-    if (MODE == kLinear) return Entry{0, 0, a.num_tokens};
+    if (MODE == kLinear) return Entry{0, i * a.xrows, min(a.xrows, a.num_tokens - i * a.xrows)};
     return lists.get(i);
   };
 
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
         if (lane == 0) mbar_arrive_expect_tx(&xfull[s], (uint32_t)en.n * len * 2);
         __syncwarp();
         for (int j = lane; j < en.n; j += 32) {
-          int row = j;
+          int row = en.off + j;
           if (MODE == kGateUp) row = lists.pair(en.off + j) >> 16;
           if (MODE == kPairs) row = lists.pair(en.off + j) & 0xFFFF;
           if (!MOL_CHECK(row < (MODE == kPairs ? numel : a.num_tokens), MOL_CHECK_ROW, row)) row = 0;
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
             if (g + 8 < rows) o[8] = v1;
           } else {
             if (!MOL_CHECK(cur.row + rows <= a.N, MOL_CHECK_COLUMN, cur.row)) continue;
-            bf16* o = a.out + col * a.out_stride + n;
+            bf16* o = a.out + (en.off + col) * a.out_stride + n;
             o[0] = __float2bfloat16(v0);
             if (g + 8 < rows) o[8] = __float2bfloat16(v1);
           }
@@ -1233,9 +1233,10 @@ struct StreamLaunch {
   template <int MODE>
   static cudaError_t by_tiles(const StreamArgs& a, int grid, size_t smem, cudaStream_t stream) {
     if (a.xrows <= 8) return one<MODE, 1>(a, grid, smem, stream);
-    if (a.xrows <= 16) return one<MODE, 2>(a, grid, smem, stream);
-    if (a.xrows <= 32) return one<MODE, 4>(a, grid, smem, stream);
-    return one<MODE, 8>(a, grid, smem, stream);
+    if constexpr (MODE == kLinear) {
+      if (a.xrows > 16) return one<MODE, 4>(a, grid, smem, stream);
+    }
+    return one<MODE, 2>(a, grid, smem, stream);
   }
   static cudaError_t launch(const StreamArgs& a, int mode, int grid, size_t smem,
                             cudaStream_t stream) {
@@ -1259,8 +1260,9 @@ struct StreamLaunch {
   static cudaError_t prepare_mode() {
     cudaError_t e = prepare_one<MODE, 1>();
     if (e == cudaSuccess) e = prepare_one<MODE, 2>();
-    if (e == cudaSuccess) e = prepare_one<MODE, 4>();
-    if (e == cudaSuccess) e = prepare_one<MODE, 8>();
+    if constexpr (MODE == kLinear) {
+      if (e == cudaSuccess) e = prepare_one<MODE, 4>();
+    }
     return e;
   }
   // clusters[i] (may be NULL): how many clusters of 1 << i blocks the device holds at once
