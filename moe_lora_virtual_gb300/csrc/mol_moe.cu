@@ -56,7 +56,6 @@ void row_layout(StreamArgs& a, int group, int rows, int Kc) {
   a.ksteps = (a.K + Kc - 1) / Kc;
   a.row_copies = a.ksteps > 1;
   a.row_pitch = a.row_copies ? align_up(bytes, 128) + 64 : bytes;
-  a.span = 8;
   a.span_shift = a.row_copies ? 0 : 64;  // (the pieces' pitch has the shift)
   a.scale_pitch = !group ? 0 : a.row_copies ? align_up(scale_bytes, 16) + 16 : scale_bytes;
   a.scale_off = align_up(rows * a.row_pitch + (rows + 7) / 8 * a.span_shift, 16);

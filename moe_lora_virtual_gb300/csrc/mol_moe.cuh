@@ -1,23 +1,27 @@
 // The experts of a MoE layer for a few tokens and the 4-bit linear (include/mol_block.h): the
-// streaming kernel. One translation unit per weight format instantiates it (mol_moe_*.cu).
+// streaming kernels. One translation unit per weight format instantiates them (mol_moe_*.cu).
 //
 // Mathematics. Both halves of the experts and the linear are products w . x of weight rows with a
 // few activation rows, every weight used by the tokens of its expert only (a few), so the time is
 // that of reading the taken experts' weights once: 2 bytes (or about half a byte) for 2 n
-// operations at n tokens an expert; 4-bit weights take about 120 instructions a KB to become bf16,
-// which costs more than to read them. Two streaming loops:
+// operations at n tokens an expert. 4-bit weights take about 130 instructions a KB to become bf16 and
+// be multiplied, which costs the warps more than HBM takes to bring them. Two streaming loops:
 //
-// - gate_up and linear: a block owns tiles of 16 whole weight rows (8 gate and 8 up rows) and a tile
-//   belongs to a team of warps, which split its inputs; each warp streams its share of tile after
-//   tile through a ring of its own. A lane copies (cp.async) the very 16 bytes that it will read, so
-//   nobody signals anybody: a chunk of 2 KB has landed when the lane's own copies have, and three are
-//   in flight a warp, 96 KB a block. (Stages of whole tiles, brought by bulk copies, kept shared
-//   memory full of tiles that were being multiplied: an output head took 35 us instead of 29.5.) The
-//   tokens' rows come by bulk copies into slots that all warps read, from a warp of its own, once for
-//   all the block's tiles of an expert.
-// - down: a block or cluster owns rows of every expert, and a stage holds a unit's weights and
-//   activation rows (bulk copies; rows of a tile are neighbours in memory). A team's first warp asks
-//   for the next stage as soon as the team is through with one; its warps have 16 rows each.
+// - stream_kernel: gate_up, the linear, and down's split form. A block owns tiles of 16 whole weight
+//   rows (8 gate and 8 up rows) and a tile belongs to a team of warps, which split its inputs; each
+//   warp streams its share of tile after tile through a ring of its own. A lane copies (cp.async) the
+//   very 16 bytes that it will read, so nobody signals anybody: a chunk of 2 KB has landed when the
+//   lane's own copies have, and three are in flight a warp, 96 KB a block. (Stages of whole tiles,
+//   brought by bulk copies, kept shared memory full of tiles that were being multiplied: an output
+//   head took 35 us instead of 29.5.) The tokens' rows come by bulk copies into slots that all warps
+//   read, from a warp of its own, once for all the block's tiles of an expert. Measured: 23 tokens of
+//   128 bf16 experts of 2048 x 768, top 8: both halves in 149 us, 6.3 TB/s, 0.92 of a copy's rate; a
+//   4-bit head of 120001 rows of 2048 inputs, 5 tokens: 29.6 us, 4.3 TB/s, where the schedulers issue
+//   in 63 % of the cycles and the tensor, ALU and load pipes share them.
+// - down_kernel: few pairs, or bf16. A block or cluster owns rows of every expert, and a stage holds a
+//   unit's weights and activation rows (bulk copies; rows of a tile are neighbours in memory). A team's
+//   first warp asks for the next stage as soon as the team is through with one; its warps have 16 rows
+//   each. One kernel, and no partial sums in memory.
 // - The product is mma.sync m16n8k16: weight rows are the M side, tokens the N side (8 a tile), so
 //   a single token wastes tensor work and no bandwidth. The contraction's order is free as long as
 //   both sides agree: each lane takes 8 neighbouring inputs of its row in one 16-byte shared-memory
@@ -25,15 +29,17 @@
 //   last token read that token's row again (a broadcast), their products are dropped.
 // - 4-bit words become bf16 pairs with a mask and a subtraction that are exact ((128 + q) - 136);
 //   a group's products are summed in fp32 first and multiplied by its scale after, so nothing is
-//   rounded that fp32 arithmetic would not round.
-// - Work is dealt by weight bytes: the gate_up rows of all taken experts form one list that the
-//   blocks share evenly, whatever the routing; the down rows are dealt to blocks or clusters, whose
-//   blocks split the experts. A team adds its products into sums of its own in the order of the
-//   experts; the teams' and the blocks' sums are added in a fixed order at the end, through
-//   distributed shared memory. No atomics on results.
+//   rounded that fp32 arithmetic would not round. (The subtraction left to a product of the tokens
+//   with -136 saves 32 instructions a KB and costs 8 products: 34.5 us for the head.)
+// - Work is dealt by weight bytes: the rows of all taken experts form one list that the blocks of
+//   stream_kernel share evenly, whatever the routing; the rows of down_kernel are dealt to blocks or
+//   clusters, whose blocks split the experts. There a team adds its products into sums of its own in
+//   the order of the experts; the teams' and the blocks' sums are added in a fixed order at the end,
+//   through distributed shared memory. No atomics on results.
 // - Each block groups the (token, slot) pairs by expert itself (at most 1024 of them: match masks,
-//   counts in shared memory, one scan), so the layer is two launches, and the down kernel groups
-//   the pairs and asks for its first weights while the gate_up kernel's last blocks still run.
+//   counts in shared memory, one scan; 2 us, or 1 for up to 32 pairs), so the layer is two launches,
+//   three in the split form, and the later ones group the pairs and ask for their first weights while
+//   the last blocks of the one before still run.
 #pragma once
 
 #include <type_traits>
@@ -287,11 +293,11 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
   __syncthreads();
 }
 
-// A team's place in its work, stage after stage: its tiles, each with all its k steps. The block's
-// share [lo, hi) of the list of output rows (row pairs), in which every entry takes whole tiles; the
-// team has every teams-th tile.
+// A warp's place in its work, step after step: every teams-th tile of the block's share (up to hi) of
+// the list of output rows (row pairs), in which every entry takes whole tiles; each tile with all its
+// k steps.
 struct Cursor {
-  int pos, hi;         // first position of the tile in the list, end of the share
+  int pos, hi;         // first position of the tile in the list
   int entry, row, ks;  // row: first row of the tile
   bool valid;
 
@@ -334,61 +340,56 @@ MOL_DEV uint32_t w4_pair(uint32_t v) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Products of a warp's weight rows with NTC tiles of 8 tokens over its share (every parts-th block)
-// of the stage's `len` inputs. r0, r1: the lane's rows g and g + 8 (TWO: there is a second set); x:
-// its token's row in each tile (all at the lane's 16 bytes). mma.sync has 21 cycles of latency and
-// issues every 8 a sub-partition, and a shared load takes 40: blocks are taken U at a time, loads
-// first, and one tile's two steps of a block go to two accumulators.
-template <bool TWO, int NTC, int NT>
+// Products of a warp's weight rows with NTC tiles of 8 tokens over the stage's `len` inputs. r0, r1: the
+// lane's rows g and g + 8; x: its token's row in each tile (all at the lane's 16 bytes). mma.sync has
+// 21 cycles of latency and issues every 8 a sub-partition, and a shared load takes 40: blocks are
+// taken U at a time, loads first, and a block's two steps go to two accumulators.
+template <int NTC, int NT>
 MOL_DEV void multiply_bf16(float (&acc)[NT][4], uint32_t r0, uint32_t r1, const uint32_t (&x)[NT],
-                           int len, int t, int part, int parts) {
-  constexpr int U = NTC == 1 ? 4 : NTC <= 4 ? 2 : 1;
-  constexpr bool kTwo = NTC <= 2;  // (more tiles are independent chains enough)
+                           int len, int t) {
+  constexpr int U = NTC == 1 ? 4 : 2;
   const int full = len >> 5;
-  float two[kTwo ? NTC : 1][4];
+  float two[NTC][4];
 #pragma unroll
-  for (int nt = 0; nt < (kTwo ? NTC : 1); ++nt) two[nt][0] = two[nt][1] = two[nt][2] = two[nt][3] = 0.f;
-  int b = part;
-  for (; b + (U - 1) * parts < full; b += U * parts) {
+  for (int nt = 0; nt < NTC; ++nt) two[nt][0] = two[nt][1] = two[nt][2] = two[nt][3] = 0.f;
+  int b = 0;
+  for (; b + U <= full; b += U) {
     uint4 a0[U], a1[U], v[U][NTC];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t o = (b + u * parts) * 64;
+      const uint32_t o = (b + u) * 64;
       a0[u] = ld_s16(r0 + o);
-      a1[u] = TWO ? ld_s16(r1 + o) : make_uint4(0, 0, 0, 0);
+      a1[u] = ld_s16(r1 + o);
 #pragma unroll
       for (int nt = 0; nt < NTC; ++nt) v[u][nt] = ld_s16(x[nt] + o);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int nt = 0; nt < NTC; ++nt)
+      for (int nt = 0; nt < NTC; ++nt) {
         mma_add(acc[nt], a0[u].x, a1[u].x, a0[u].y, a1[u].y, v[u][nt].x, v[u][nt].y);
-#pragma unroll
-      for (int nt = 0; nt < NTC; ++nt)
-        mma_add(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0[u].z, a1[u].z, a0[u].w, a1[u].w, v[u][nt].z, v[u][nt].w);
+        mma_add(two[nt], a0[u].z, a1[u].z, a0[u].w, a1[u].w, v[u][nt].z, v[u][nt].w);
+      }
     }
   }
-  // what is left of the share, the last, partial block with it: inputs past len are zeros
+  // what is left, the last, partial block with it: inputs past len are zeros
 #pragma unroll 1
-  for (; b * 32 < len; b += parts) {
+  for (; b * 32 < len; ++b) {
     const bool in = b * 32 + t * 8 < len;
     const uint32_t o = b * 64;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a0 = in ? ld_s16(r0 + o) : zero, a1 = TWO && in ? ld_s16(r1 + o) : zero;
+    const uint4 a0 = in ? ld_s16(r0 + o) : zero, a1 = in ? ld_s16(r1 + o) : zero;
 #pragma unroll
     for (int nt = 0; nt < NTC; ++nt) {
       const uint4 v = in ? ld_s16(x[nt] + o) : zero;
       mma_add(acc[nt], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-      mma_add(kTwo ? two[kTwo ? nt : 0] : acc[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+      mma_add(two[nt], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
     }
   }
-  if (kTwo) {
 #pragma unroll
-    for (int nt = 0; nt < NTC; ++nt)
+  for (int nt = 0; nt < NTC; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] += two[nt][i];
-  }
+    for (int i = 0; i < 4; ++i) acc[nt][i] += two[nt][i];
 }
 
 // The scales of one row for a block of 128 inputs: bf16 pairs as they lie.
@@ -486,15 +487,15 @@ MOL_DEV void block_w4(float (&acc)[NT][4], const BlockW4<G>& w, const uint32_t (
 
 template <int G, int NTC, int NT>
 MOL_DEV void multiply_w4(float (&acc)[NT][4], uint32_t r0, uint32_t r1, uint32_t s0, uint32_t s1,
-                         const uint32_t (&x)[NT], int len, int t, int part, int parts) {
+                         const uint32_t (&x)[NT], int len, int t) {
   const int full = len >> 7;
 #pragma unroll 1
-  for (int b = part; b < full; b += parts) {
+  for (int b = 0; b < full; ++b) {
     BlockW4<G> w;
     w.load(r0, r1, s0, s1, b);
     block_w4<G, NTC, NT, true>(acc, w, x, b, len, t);
   }
-  if ((len & 127) && (full & (parts - 1)) == part) {
+  if (len & 127) {
     BlockW4<G> w;
     w.load(r0, r1, s0, s1, full);
     block_w4<G, NTC, NT, false>(acc, w, x, full, len, t);
@@ -527,15 +528,15 @@ MOL_DEV void add_sums(const StreamArgs& a, const Lists& l, uint32_t sums, const 
   if (row + 8 < rows) st_sf(s + 32, fmaf(w, v1, ld_sf(s + 32)));
 }
 
-// Where row j of span q lies in a stage, and its scales. Spans of 8 rows (a half of 4 in tiles of 8)
-// are brought by a copy each, 64 bytes apart, and the lanes of odd g take the row of the odd span
-// first: the eight lanes of a shared-memory phase then read two rows that lie an odd multiple of 64
-// bytes apart (rows of a multiple of 128 bytes) and no bank twice.
+// down: where row j of span q lies in a stage, and its scales. Spans of 8 rows are brought by a copy
+// each, 64 bytes apart, and the lanes of odd g take the row of the odd span first: the eight lanes of a
+// shared-memory phase then read two rows that lie an odd multiple of 64 bytes apart (rows of a multiple
+// of 128 bytes) and no bank twice.
 MOL_DEV uint32_t row_at(const StreamArgs& a, int q, int j) {
-  return (q * a.span + j) * a.row_pitch + q * a.span_shift;
+  return (q * 8 + j) * a.row_pitch + q * a.span_shift;
 }
 MOL_DEV uint32_t scale_at(const StreamArgs& a, int q, int j) {
-  return a.scale_off + (q * a.span + j) * a.scale_pitch + q * 16;
+  return a.scale_off + (q * 8 + j) * a.scale_pitch + q * 16;
 }
 
 // The part'th of `parts` nearly equal shares of [0, all).
@@ -599,6 +600,10 @@ MOL_DEV void copy_small(uint32_t dst, const char* src) {
                  : "memory");
 }
 
+// gate_up: act[pair, n] = silu(gate) * up, gate = w[e, n] . x[token] (+ delta), up = w[e, N + n] . x[token]
+// (+ delta); kPairs: partial[pair, n] = w[e, n] . x[pair]; linear: out[t, n] = w[n] . x[t], its tokens in
+// entries of one expert. Few tokens: bound by the launch, the lists and one round trip to HBM (about
+// 4 us); many weights: bf16 by HBM, 4-bit by the warps' instructions.
 template <int G, int MODE, int NT>
 __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs a) {
@@ -1112,12 +1117,12 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
           return st + scale_at(a, i >> 3, i & 7) + ((from * spitch + k0 / GG * 2) & 15u);
         };
         if (NT > 1 && en.n <= 8)
-          multiply_w4<GG, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+          multiply_w4<GG, 1, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t);
         else
-          multiply_w4<GG, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t, 0, 1);
+          multiply_w4<GG, NT, NT>(acc, r0, r1, scales_of(i0), scales_of(i1), x, len, t);
       } else {
-        if (NT > 1 && en.n <= 8) multiply_bf16<true, 1, NT>(acc, r0, r1, x, len, t, 0, 1);
-        else multiply_bf16<true, NT, NT>(acc, r0, r1, x, len, t, 0, 1);
+        if (NT > 1 && en.n <= 8) multiply_bf16<1, NT>(acc, r0, r1, x, len, t);
+        else multiply_bf16<NT, NT>(acc, r0, r1, x, len, t);
       }
       __syncwarp();
       if (parts > 1) {

@@ -19,7 +19,6 @@ __host__ __device__ constexpr int consumer_warps(int token_tiles) { return token
 constexpr int kChunks = 4;
 __host__ __device__ constexpr int chunk_bytes(int group) { return 2048 + (group ? 16 * 512 / group : 0); }
 constexpr int kMaxStages = 32;  // of all teams of a block
-constexpr int kMaxSlots = 8;    // token slots
 constexpr int kClusterSizes = 3;  // down: clusters of 1, 2 or 4 blocks
 constexpr int kSmem = 222 * 1024;
 constexpr int kDownRows = 64;     // output rows of a block of the down kernel at most
@@ -39,19 +38,17 @@ struct StreamArgs {
   int N;                   // outputs of one expert: I, H, or the linear's N
   int chained;             // the kernel before is this call's gate_up
   int cluster;             // blocks that share output rows (down), 1 otherwise
-  // A stage: `stage_rows` (8 or 16) weight rows of Kc inputs, gate rows then up rows (gate_up);
-  // tile_rows outputs. Rows lie in spans.
-  int stage_rows, tile_rows, Kc, ksteps;
-  int entry_rows;          // gate_up, linear: N rounded up to whole tiles (to a tile for each team
-                           // where rows come in pieces)
-  int span, span_shift;    // rows of a span (8, or a half of 4), bytes between spans
+  int Kc, ksteps;          // inputs of a step (all of them, or a piece), steps of a row
+  int tile_rows;           // gate_up, linear: outputs of a tile
+  int entry_rows;          // and N rounded up to whole tiles (to a tile for each team where rows come
+                           // in pieces)
+  int span_shift;          // down: bytes between spans of 8 rows
   int row_copies;          // pieces of rows: a copy for each row; else whole rows, a copy a span
   int row_pitch, scale_off, scale_pitch, stage_bytes, stages;
   // `xrows` activation rows of Kc inputs: a token slot, or at x_off of a stage (down)
   int xrows, x_pitch, xslot_bytes, xstages, x_off;
   int chunks;              // gate_up, linear: of a warp's ring
   int teams, parts;        // teams of `parts` warps in use; the teams divide the stages
-  int parts_off;           // gate_up, linear: of the partial sums inside a stage
   int acc_stride;          // down: floats between tokens of a team's sums
 };
 
