@@ -1,5 +1,5 @@
-// Native calls of the MoE block's binding (block.py), for the common case: contiguous operands of
-// the right types and shapes, outputs to be allocated, the current stream. Each function checks that
+// Native calls of the MoE block's binding (block.py), for the common case: operands of the right types
+// and shapes (rows may have a stride), outputs to be allocated, the current stream. Each function checks that
 // case, allocates, and calls the C entry point whose address it is given; it returns None for
 // anything else, also where the entry point refuses, and the Python function then takes its own path
 // and raises what there is to raise. A call costs a third of the Python path's host time, which is
@@ -27,6 +27,16 @@ bool fits(const Tensor& t, at::ScalarType type, c10::IntArrayRef sizes) {
     return false;
   for (size_t i = 0; i < sizes.size(); ++i)
     if (sizes[i] >= 0 && t.sizes()[i] != sizes[i]) return false;
+  return true;
+}
+
+// A plain tensor of rows on the GPU, its columns neighbours; the row stride of a single row (or none)
+// does not matter.
+bool rows_fit(const Tensor& t, at::ScalarType type, int64_t rows, int64_t columns, int64_t& stride) {
+  if (t.scalar_type() != type || !t.is_cuda() || t.dim() != 2 || t.size(0) != rows ||
+      t.size(1) != columns || (t.stride(1) != 1 && columns > 1))
+    return false;
+  stride = rows > 1 ? t.stride(0) : (columns + 7) / 8 * 8;
   return true;
 }
 
@@ -117,19 +127,21 @@ PyObject* block_norm(Args a) {
   if (!a.take(f) || !a.take(y) || !a.take(residual) || !a.take_optional(pre) ||
       !a.take_optional(post) || !a.take_optional(gate) || !a.take(scale) || !a.take(eps))
     return none();
-  if (!fits(*y, at::kBFloat16, {-1, -1})) return none();
+  if (y->dim() != 2) return none();
   const int64_t T = y->size(0), H = y->size(1);
-  if (!small({T, H}) || !fits(*residual, at::kBFloat16, {T, H}) ||
-      (pre && !fits(*pre, at::kBFloat16, {H})) || (post && !fits(*post, at::kBFloat16, {H})))
+  int64_t ys, rs, gs = 0;
+  if (!small({T, H}) || !rows_fit(*y, at::kBFloat16, T, H, ys) ||
+      !rows_fit(*residual, at::kBFloat16, T, H, rs) || (pre && !fits(*pre, at::kBFloat16, {H})) ||
+      (post && !fits(*post, at::kBFloat16, {H})))
     return none();
-  const bool gate_rows = gate && gate->dim() == 2;
-  if (gate && !(gate_rows ? fits(*gate, at::kBFloat16, {T, H}) : fits(*gate, at::kBFloat16, {H})))
+  if (gate && !(gate->dim() == 2 ? rows_fit(*gate, at::kBFloat16, T, H, gs)
+                                 : fits(*gate, at::kBFloat16, {H})))
     return none();
   Tensor out = at::empty({T, H}, y->options()), normed;
   if (pre) normed = at::empty({T, H}, y->options());
   auto ptr = [](const Tensor* t) -> const void* { return t ? t->data_ptr() : nullptr; };
   const int32_t status = reinterpret_cast<decltype(&mol_block_norm)>(f)(
-      y->data_ptr(), H, residual->data_ptr(), H, ptr(post), ptr(gate), gate_rows ? H : 0,
+      y->data_ptr(), ys, residual->data_ptr(), rs, ptr(post), ptr(gate), gs,
       (float)scale, ptr(pre), (float)eps, T, (int32_t)H, out.data_ptr(), H,
       pre ? normed.data_ptr() : nullptr, pre ? H : 0, stream_of(*y));
   if (status != MOL_OK) return none();
@@ -144,13 +156,16 @@ PyObject* moe_route(Args a) {
   if (!a.take(f) || !a.take(logits) || !a.take(topk) || !a.take(renormalize) || !a.take(scale))
     return none();
   const bool bf16 = logits->scalar_type() == at::kBFloat16;
-  if (!fits(*logits, bf16 ? at::kBFloat16 : at::kFloat, {-1, -1})) return none();
+  if (logits->dim() != 2) return none();
   const int64_t T = logits->size(0), E = logits->size(1);
-  if (!small({T, E, topk})) return none();
+  int64_t stride;
+  if (!small({T, E, topk}) ||
+      !rows_fit(*logits, bf16 ? at::kBFloat16 : at::kFloat, T, E, stride))
+    return none();
   Tensor ids = at::empty({T, topk}, logits->options().dtype(at::kInt));
   Tensor weights = at::empty({T, topk}, logits->options().dtype(at::kFloat));
   const int32_t status = reinterpret_cast<decltype(&mol_moe_route)>(f)(
-      logits->data_ptr(), bf16 ? MOL_BF16 : MOL_F32, E, T, (int32_t)E, (int32_t)topk,
+      logits->data_ptr(), bf16 ? MOL_BF16 : MOL_F32, stride, T, (int32_t)E, (int32_t)topk,
       (int32_t)renormalize, (float)scale, static_cast<int32_t*>(ids.data_ptr()),
       static_cast<float*>(weights.data_ptr()), stream_of(*logits));
   return status == MOL_OK ? pair(ids, THPVariable_Wrap(weights)) : none();
@@ -164,18 +179,19 @@ PyObject* moe_gate_up(Args a) {
       w.data->dim() != 3)
     return none();
   const int64_t E = w.data->size(0), I2 = w.data->size(1);
-  if (!fits(*x, at::kBFloat16, {-1, w.K}) || !w.fits_rows(E, I2)) return none();
+  if (x->dim() != 2 || !w.fits_rows(E, I2)) return none();
   const int64_t T = x->size(0), H = w.K;
-  if (!fits(*ids, at::kInt, {T, -1})) return none();
+  int64_t xs, ds = 0;
+  if (!fits(*ids, at::kInt, {T, -1}) || !rows_fit(*x, at::kBFloat16, T, H, xs)) return none();
   const int64_t k = ids->size(1);
   if (!small({T, k, E, H, I2}) || I2 % 2 ||
-      (delta && !fits(*delta, at::kBFloat16, {T * k, I2})))
+      (delta && !rows_fit(*delta, at::kBFloat16, T * k, I2, ds)))
     return none();
   Tensor act = at::empty({T * k, I2 / 2}, x->options());
   const int32_t status = reinterpret_cast<decltype(&mol_moe_gate_up)>(f)(
-      x->data_ptr(), H, static_cast<const int32_t*>(ids->data_ptr()), T, (int32_t)k, (int32_t)E,
+      x->data_ptr(), xs, static_cast<const int32_t*>(ids->data_ptr()), T, (int32_t)k, (int32_t)E,
       (int32_t)H, (int32_t)(I2 / 2), w.data->data_ptr(), w.scale_ptr(), (int32_t)w.group,
-      delta ? delta->data_ptr() : nullptr, delta ? I2 : 0, act.data_ptr(), stream_of(*x));
+      delta ? delta->data_ptr() : nullptr, ds, act.data_ptr(), stream_of(*x));
   return status == MOL_OK ? THPVariable_Wrap(act) : none();
 }
 
@@ -193,8 +209,10 @@ PyObject* moe_down(Args a) {
   const int64_t E = w.data->size(0), H = w.data->size(1), I = w.K;
   if (!fits(*ids, at::kInt, {-1, -1}) || !w.fits_rows(E, H)) return none();
   const int64_t T = ids->size(0), k = ids->size(1);
+  int64_t ds = 0;
   if (!small({T, k, E, H, I}) || !fits(*act, at::kBFloat16, {T * k, I}) ||
-      !fits(*weights, at::kFloat, {T, k}) || (delta && !fits(*delta, at::kBFloat16, {T * k, H})))
+      !fits(*weights, at::kFloat, {T, k}) ||
+      (delta && !rows_fit(*delta, at::kBFloat16, T * k, H, ds)))
     return none();
   const size_t bytes = reinterpret_cast<decltype(&mol_moe_workspace_bytes)>(need)(
       T, (int32_t)k, (int32_t)E, (int32_t)H, (int32_t)I, (int32_t)w.group);
@@ -203,7 +221,7 @@ PyObject* moe_down(Args a) {
       act->data_ptr(), static_cast<const int32_t*>(ids->data_ptr()),
       static_cast<const float*>(weights->data_ptr()), T, (int32_t)k, (int32_t)E, (int32_t)H,
       (int32_t)I, w.data->data_ptr(), w.scale_ptr(), (int32_t)w.group,
-      delta ? delta->data_ptr() : nullptr, delta ? H : 0, bytes ? ws.data_ptr() : nullptr, bytes,
+      delta ? delta->data_ptr() : nullptr, ds, bytes ? ws.data_ptr() : nullptr, bytes,
       out.data_ptr(), H, stream_of(*act));
   return status == MOL_OK ? THPVariable_Wrap(out) : none();
 }
@@ -216,11 +234,11 @@ PyObject* moe_forward(Args a) {
       !gu.take(a) || !dn.take(a) || gu.data->dim() != 3 || dn.data->dim() != 3)
     return none();
   const int64_t E = gu.data->size(0), I = dn.K, H = gu.K;
-  if (gu.group != dn.group || !fits(*x, at::kBFloat16, {-1, H}) || !gu.fits_rows(E, 2 * I) ||
-      !dn.fits_rows(E, H))
+  if (gu.group != dn.group || x->dim() != 2 || !gu.fits_rows(E, 2 * I) || !dn.fits_rows(E, H))
     return none();
   const int64_t T = x->size(0);
-  if (!fits(*ids, at::kInt, {T, -1})) return none();
+  int64_t xs;
+  if (!fits(*ids, at::kInt, {T, -1}) || !rows_fit(*x, at::kBFloat16, T, H, xs)) return none();
   const int64_t k = ids->size(1);
   if (!small({T, k, E, H, I}) || !fits(*weights, at::kFloat, {T, k})) return none();
   const size_t bytes = reinterpret_cast<decltype(&mol_moe_workspace_bytes)>(need)(
@@ -228,7 +246,7 @@ PyObject* moe_forward(Args a) {
   Tensor out = at::empty({T, H}, x->options()), act = at::empty({T * k, I}, x->options());
   Tensor ws = scratch(*x, bytes);
   const int32_t status = reinterpret_cast<decltype(&mol_moe_forward_split)>(f)(
-      x->data_ptr(), H, static_cast<const int32_t*>(ids->data_ptr()),
+      x->data_ptr(), xs, static_cast<const int32_t*>(ids->data_ptr()),
       static_cast<const float*>(weights->data_ptr()), T, (int32_t)k, (int32_t)E, (int32_t)H,
       (int32_t)I, gu.data->data_ptr(), gu.scale_ptr(), dn.data->data_ptr(), dn.scale_ptr(),
       (int32_t)gu.group, act.data_ptr(), bytes ? ws.data_ptr() : nullptr, bytes, out.data_ptr(), H,
@@ -242,15 +260,16 @@ PyObject* w4_linear(Args a) {
   Weights w;
   if (!a.take(f) || !a.take(x) || !w.take(a) || w.data->dim() != 2 || !w.scales) return none();
   const int64_t N = w.data->size(0), K = w.K;
-  if (!fits(*x, at::kBFloat16, {-1, K}) || (w.group != 32 && w.group != 64 && w.group != 128))
+  if (x->dim() != 2 || (w.group != 32 && w.group != 64 && w.group != 128))
     return none();
   const int64_t T = x->size(0), Kp = (K + 255) / 256 * 256;
-  if (!small({T, N, K}) || !fits(*w.data, at::kByte, {N, Kp / 2}) ||
+  int64_t xs;
+  if (!small({T, N, K}) || !rows_fit(*x, at::kBFloat16, T, K, xs) || !fits(*w.data, at::kByte, {N, Kp / 2}) ||
       !fits(*w.scales, at::kBFloat16, {N, Kp / w.group}))
     return none();
   Tensor out = at::empty({T, N}, x->options());
   const int32_t status = reinterpret_cast<decltype(&mol_w4_linear)>(f)(
-      x->data_ptr(), K, T, (int32_t)K, (int32_t)N, w.data->data_ptr(), w.scale_ptr(),
+      x->data_ptr(), xs, T, (int32_t)K, (int32_t)N, w.data->data_ptr(), w.scale_ptr(),
       (int32_t)w.group, out.data_ptr(), N, stream_of(*x));
   return status == MOL_OK ? THPVariable_Wrap(out) : none();
 }
