@@ -162,40 +162,48 @@ int list_bytes(const MoeShape& s) { return s.num_tokens * s.topk * 16; }
 constexpr int kCombineThreads = 128;
 
 // The split form's second step, out[t] = sum over t's pairs of weight * partial, in the order of the
-// slots, then the deltas in that order. Four columns a thread; bound by reading the fp32 partials
-// back from L2.
+// slots, plus the same sum of the deltas. Four columns a thread; bound by reading the fp32 partials
+// back from L2, so the loads of four slots are in flight at once (an absent pair's rows are read and
+// not used).
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const StreamArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int t = blockIdx.y, n = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
   if (n >= a.N) return;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, float v0, float v1, float v2, float v3) {
-    sum.x = fmaf(w, v0, sum.x);
-    sum.y = fmaf(w, v1, sum.y);
-    sum.z = fmaf(w, v2, sum.z);
-    sum.w = fmaf(w, v3, sum.w);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f), deltas = sum;
+  auto add = [](float4& s, float w, float v0, float v1, float v2, float v3) {
+    s.x = fmaf(w, v0, s.x);
+    s.y = fmaf(w, v1, s.y);
+    s.z = fmaf(w, v2, s.z);
+    s.w = fmaf(w, v3, s.w);
   };
-#pragma unroll 4
-  for (int k = 0; k < a.topk; ++k) {
-    const int64_t pair = t * a.topk + k;
-    const int e = a.ids[pair];
-    if (e < 0 || e >= a.E) continue;
-    const float4 v = *reinterpret_cast<const float4*>(a.partial + pair * a.N + n);
-    add(a.weights[pair], v.x, v.y, v.z, v.w);
-  }
-  if (a.delta) {
-    for (int k = 0; k < a.topk; ++k) {
-      const int64_t pair = t * a.topk + k;
+  constexpr int U = 4;
+  for (int k0 = 0; k0 < a.topk; k0 += U) {
+    float4 v[U];
+    uint2 d[U];
+    float w[U];
+    bool has[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t pair = t * a.topk + min(k0 + u, a.topk - 1);
       const int e = a.ids[pair];
-      if (e < 0 || e >= a.E) continue;
-      const __nv_bfloat16* d = a.delta + pair * a.delta_stride + n;
-      add(a.weights[pair], __bfloat162float(d[0]), __bfloat162float(d[1]), __bfloat162float(d[2]),
-          __bfloat162float(d[3]));
+      has[u] = k0 + u < a.topk && e >= 0 && e < a.E;
+      w[u] = a.weights[pair];
+      v[u] = *reinterpret_cast<const float4*>(a.partial + pair * a.N + n);
+      d[u] = a.delta ? *reinterpret_cast<const uint2*>(a.delta + pair * a.delta_stride + n)
+                     : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!has[u]) continue;
+      add(sum, w[u], v[u].x, v[u].y, v[u].z, v[u].w);
+      if (a.delta)
+        add(deltas, w[u], bf16_lo(d[u].x), bf16_hi(d[u].x), bf16_lo(d[u].y), bf16_hi(d[u].y));
     }
   }
-  __nv_bfloat162 o[2] = {__floats2bfloat162_rn(sum.x, sum.y), __floats2bfloat162_rn(sum.z, sum.w)};
-  *reinterpret_cast<uint2*>(a.out + t * a.out_stride + n) = *reinterpret_cast<uint2*>(o);
+  const uint2 o = make_uint2(pack_bf16x2(sum.x + deltas.x, sum.y + deltas.y),
+                             pack_bf16x2(sum.z + deltas.z, sum.w + deltas.w));
+  *reinterpret_cast<uint2*>(a.out + t * a.out_stride + n) = o;
 }
 
 }  // namespace
@@ -204,10 +212,11 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Stre
 // and the partials' way through L2. It pays for 4-bit weights from a few pairs on, as theirs is the
 // work of the warps (128 experts of 2048 x 768, top 8, layer: 32 pairs 29.7 us against 28.8, 64 pairs
 // 44.3 against 48.9, 768 pairs 97 against 121), for bf16 where experts have many tokens (496 pairs
-// 202 us against 194, 1016 pairs 217 against 250).
+// 202 us against 194, 1016 pairs 217 against 250) or the down rows are short and their stages small
+// (102 pairs of 103 experts of 2520 x 72: 27 us against 32).
 size_t moe_split_bytes(const MoeShape& s, int group) {
   const int pairs = s.num_tokens * s.topk;
-  if (pairs <= 32 || (group == 0 && pairs < 6 * s.num_experts)) return 0;
+  if (pairs <= 32 || (group == 0 && s.inter > 192 && pairs < 6 * s.num_experts)) return 0;
   return (size_t)pairs * s.hidden * sizeof(float);
 }
 

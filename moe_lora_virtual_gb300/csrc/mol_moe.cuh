@@ -838,6 +838,28 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       }
       ++want;
       const int chunks = fault ? 0 : chunks_of(cur), len = min(a.Kc, a.K - cur.ks * a.Kc);
+      // the deltas of the tile's values, asked for before its chunks
+      const int rows = fault ? 0 : min(a.tile_rows, a.N - cur.row);
+      uint16_t delta[MODE == kGateUp ? NT : 1][2][2];
+      if constexpr (MODE == kGateUp) {
+        if (a.delta && cur.ks == a.ksteps - 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col = nt * 8 + 2 * t + h;
+              delta[nt][h][0] = delta[nt][h][1] = 0;
+              if (col >= en.n || g >= rows) continue;
+              const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
+              if (!MOL_CHECK(pair < numel, MOL_CHECK_ROW, pair)) continue;
+              const uint16_t* dl =
+                  reinterpret_cast<const uint16_t*>(a.delta) + pair * a.delta_stride + cur.row + g;
+              delta[nt][h][0] = dl[0];
+              delta[nt][h][1] = dl[a.N];
+            }
+          }
+        }
+      }
 #pragma unroll 1
       for (int c = part; c < chunks; c += parts) {
         if (last_slot == kChunks - 1) cp_async_wait_group<kChunks - 2>();
@@ -920,7 +942,6 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       }
       // the tile's values: column 2t + h of each token tile; row g of the first eight in values h, of
       // the second (gate_up: the up row) in values 2 + h
-      const int rows = fault ? 0 : min(a.tile_rows, a.N - cur.row);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -928,13 +949,12 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
           const int col = nt * 8 + 2 * t + h, n = cur.row + g;
           float v0 = acc[nt][h], v1 = acc[nt][2 + h];
           if (col >= en.n || g >= rows) continue;
-          if (MODE == kGateUp) {
+          if constexpr (MODE == kGateUp) {
             const int64_t pair = lists.pair(en.off + col) & 0xFFFF;
             if (!MOL_CHECK(pair < numel && n < a.N, MOL_CHECK_ROW, pair)) continue;
             if (a.delta) {
-              const bf16* dl = a.delta + pair * a.delta_stride + n;
-              v0 += __bfloat162float(dl[0]);
-              v1 += __bfloat162float(dl[a.N]);
+              v0 += __uint_as_float((uint32_t)delta[nt][h][0] << 16);
+              v1 += __uint_as_float((uint32_t)delta[nt][h][1] << 16);
             }
             a.out[pair * a.N + n] = __float2bfloat16(v0 / (1.f + expf(-v0)) * v1);
           } else if (MODE == kPairs) {
