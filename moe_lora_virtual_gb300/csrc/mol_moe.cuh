@@ -546,13 +546,23 @@ MOL_DEV void share(int all, int parts, int part, int& from, int& to) {
   to = from + q + (part < r);
 }
 
-// v + the deltas of token tok's pairs at output column n, in the order of the slots.
+// v + the deltas of token tok's pairs at output column n, in the order of the slots; four loads in
+// flight at once (an absent pair's delta is read and not used).
 MOL_DEV float add_deltas(const StreamArgs& a, float v, int tok, int n) {
-  for (int k = 0; k < a.topk; ++k) {
-    const int64_t pair = tok * a.topk + k;
-    const int e = a.ids[pair];
-    if (e >= 0 && e < a.E)
-      v = fmaf(a.weights[pair], __bfloat162float(a.delta[pair * a.delta_stride + n]), v);
+  constexpr int U = 4;
+  for (int k0 = 0; k0 < a.topk; k0 += U) {
+    float d[U], w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t pair = tok * a.topk + min(k0 + u, a.topk - 1);
+      const int e = a.ids[pair];
+      const bool has = k0 + u < a.topk && e >= 0 && e < a.E;
+      const float x = __bfloat162float(a.delta[pair * a.delta_stride + n]), y = a.weights[pair];
+      d[u] = has ? x : 0.f;
+      w[u] = has ? y : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) v = fmaf(w[u], d[u], v);
   }
   return v;
 }
