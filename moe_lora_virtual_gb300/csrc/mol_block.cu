@@ -194,10 +194,10 @@ MOL_DEV void sort_down(P (&c)[N]) {
 // One warp per row: lane l sorts the logits of experts l, l + 32, ... in its registers; each of the
 // topk rounds takes the largest of the lanes' first ones (one warp reduction, two for fp32), whose
 // lane moves its list up. Comparisons only, so the choice is exact, and each number is distinct, so
-// the lower index wins. The row is read once. Bound by the instructions of the sort and the rounds:
-// about 200 a row at 256 bf16 experts and topk 8 (8192 such rows: 7.3 us; a search of all
-// keys in each round took 11.0); few rows by the launch and the rounds' latency (23 rows of 128:
-// 1.6 us).
+// the lower index wins. The row is read once, its exponentials are summed in fp32. Bound by
+// instructions for many rows: about 630 a row at 256 bf16 experts and topk 8, 76 % of the issue slots
+// (8192 such rows: 6.6 us, 11.0 with a search of all keys in each round; 4 TB/s would be 1 us); few
+// rows by the launch and the rounds' latency (23 rows of 128: 1.6 us).
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     moe_route_kernel(const T* __restrict__ logits, int64_t row_stride, int64_t rows, int E,
@@ -210,31 +210,35 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   pdl_launch_dependents();
   if (row >= rows) return;
   const T* p = logits + row * row_stride;
-  P c[VPL];
+  float l[VPL];
+  P c[VPL], best = 0;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int e = lane + 32 * j;
-    pack(e < E ? load_logit(p + e) : -INFINITY, e, c[j]);
+    l[j] = e < E ? load_logit(p + e) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    pack(l[j], lane + 32 * j, c[j]);
+    best = c[j] > best ? c[j] : best;
+  }
+  best = warp_largest(best);
+  const float top = packed_value(best);
+  float all = 0.f;
+  if (!renorm) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (c[j]) all += soft(l[j], top);
   }
   sort_down(c);
-  float top = 0.f, all = 0.f;
   P mine = 0;
-  for (int r = 0; r < topk; ++r) {
-    const P best = warp_largest(c[0]);
-    if (best == 0) break;
-    if (r == 0) {
-      top = packed_value(best);
-      if (!renorm) {
-#pragma unroll
-        for (int j = 0; j < VPL; ++j)
-          if (c[j]) all += soft(packed_value(c[j]), top);
-      }
-    }
+  for (int r = 0; r < topk && best != 0; ++r) {
     if (lane == r) mine = best;
     const bool taken = c[0] == best;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
       if (taken) c[j] = j + 1 < VPL ? c[j + 1 < VPL ? j + 1 : j] : 0;
+    best = warp_largest(c[0]);
   }
   const float my_w = mine ? soft(packed_value(mine), top) : 0.f;
   float sum = renorm ? my_w : all;
