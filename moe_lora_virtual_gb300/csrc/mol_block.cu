@@ -40,17 +40,20 @@ MOL_DEV uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// One block per row, CPT chunks of 8 elements per thread, the row held in fp32
+constexpr int kNormWarps = 4;
+
+// One block per row, or a warp for short rows, CPT chunks of 8 elements per thread, the row held in fp32
 // registers between the two sums: y, the residual and the gate are read once and both
 // outputs written once, so the kernel moves what the operator cannot do without (8
 // bytes an element, 10 with a gate per token) and is bound by HBM for many rows, by the
 // launch and three dependent round trips (loads, two block sums) for a few.
 // Shared-memory halves: a second sum may start before every thread has read the first.
 template <int THREADS, int CPT>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(THREADS == 32 ? 32 * kNormWarps : THREADS) block_norm_kernel(NormArgs a) {
   __shared__ float sh[2][THREADS / 32];
   const int chunks = a.H >> 3;
-  const int64_t row = blockIdx.x;
+  const int64_t row = THREADS == 32 ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+  if (THREADS == 32 && row >= a.rows) return;
   const uint4* yr = reinterpret_cast<const uint4*>(
       static_cast<const __nv_bfloat16*>(a.y) + row * a.y_stride);
   const uint4* rr = reinterpret_cast<const uint4*>(
@@ -196,7 +199,7 @@ MOL_DEV void sort_down(P (&c)[N]) {
 // lane moves its list up. Comparisons only, so the choice is exact, and each number is distinct, so
 // the lower index wins. The row is read once, its exponentials are summed in fp32. Bound by
 // instructions for many rows: about 630 a row at 256 bf16 experts and topk 8, 76 % of the issue slots
-// (8192 such rows: 6.6 us, 11.0 with a search of all keys in each round; 4 TB/s would be 1 us); few
+// (8192 such rows: 6.6 us, 0.7 for their bytes, 11.0 with a search of all keys in each round); few
 // rows by the launch and the rounds' latency (23 rows of 128: 1.6 us).
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
@@ -271,12 +274,18 @@ cudaError_t route_by_width(const T* logits, int64_t row_stride, int64_t rows, in
 }  // namespace
 
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)a.rows);
-  auto go = [&](auto kernel, int threads) {
-    return launch_pdl(kernel, grid, dim3(threads), 0, stream, a);
-  };
+  // A warp a row, four rows a block where there are many: no sum waits for other warps, and small
+  // blocks do not use up an SM's (8000 rows of 256: 3.6 us against 8.4 with a block each). Rows of up
+  // to 512 only where there are many (8000: 5.9 us against 9.5; 23 rows: 2.2 against 1.8).
   const int chunks = a.H / 8;
+  const bool many = a.rows > 2048;
+  auto go = [&](auto kernel, int threads) {
+    const int warps = threads == 32 && many ? kNormWarps : 1;
+    return launch_pdl(kernel, dim3((unsigned)((a.rows + warps - 1) / warps)), dim3(threads, warps), 0,
+                      stream, a);
+  };
   if (chunks <= 32) return go(block_norm_kernel<32, 1>, 32);
+  if (chunks <= 64 && many) return go(block_norm_kernel<32, 2>, 32);
   if (chunks <= 128) return go(block_norm_kernel<128, 1>, 128);
   if (chunks <= 256) return go(block_norm_kernel<256, 1>, 256);
   if (chunks <= 512) return go(block_norm_kernel<256, 2>, 256);

@@ -578,3 +578,19 @@ def test_native_calls_equal_the_python_path(env, group, monkeypatch):
                             torch.zeros(T, k + 1, device="cuda"), gu, dn)
     with pytest.raises(mol.MolError):
         mol.mol_moe_route(logits, E + 1)
+
+
+@pytest.mark.parametrize("H", [8, 256, 264, 512, 520])
+def test_norm_of_many_short_rows(env, H):
+    """2051 rows: several a block, the last block's not all there."""
+    torch, mol = env
+    g = torch.Generator().manual_seed(H)
+    T = 2051
+    y, r, gate = randn(torch, g, T, H, std=3.0), randn(torch, g, T, H), randn(torch, g, T, H)
+    w = 1 + randn(torch, g, H, std=0.2)
+    ro, n = mol.mol_block_norm(strided(torch, y), strided(torch, r), w.cuda(), post_weight=w.cuda(),
+                               gate=gate.cuda(), residual_scale=0.5)
+    want, want_n = bo.block_norm(f64(y), f64(r), f64(w), f64(w), f64(gate), 0.5)
+    # one rounding each, and the fp32 sums' error as in the tests above
+    close(ro, want, ROUND * np.abs(want) + ACC, "residual")
+    close(n, want_n, ROUND * np.abs(want_n) + ACC, "normed")
