@@ -335,6 +335,18 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
     if (!ok || a.ksteps > 1) ok = fits(std::min(num_tokens, most));
   }
   if (!ok) return cudaErrorInvalidConfiguration;
+  if ((int64_t)tiles * 16 * ((num_tokens + a.xrows - 1) / a.xrows) > 1 << 30) {
+    // (the kernel counts the entries' rows in 32 bits: an entry a launch)
+    const int rows = a.xrows;
+    for (int t = 0; t < num_tokens; t += rows) {
+      const cudaError_t e = launch_w4_linear(
+          static_cast<const __nv_bfloat16*>(x) + t * x_stride, x_stride,
+          std::min(rows, num_tokens - t), N, w, static_cast<__nv_bfloat16*>(out) + t * out_stride,
+          out_stride, stream);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
   return launch_by_group(w.group, a, kLinear, grid, stream_smem(a, w.group), stream);
 }
 
