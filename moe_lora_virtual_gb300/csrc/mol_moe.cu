@@ -162,13 +162,27 @@ int list_bytes(const MoeShape& s) { return s.num_tokens * s.topk * 16; }
 constexpr int kCombineThreads = 128;
 
 // The split form's second step, out[t] = sum over t's pairs of weight * partial, in the order of the
-// slots, plus the same sum of the deltas. Four columns a thread; bound by reading the fp32 partials
-// back from L2, so the loads of four slots are in flight at once (an absent pair's rows are read and
-// not used).
+// slots, plus the same sum of the deltas. Four columns a thread; bound by the round trip of the fp32
+// partials to L2, so the loads of eight slots are in flight at once (an absent pair's rows are read and
+// not used), and the first slots' ids and weights, which the kernels before did not write, are loaded
+// before those have ended.
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const StreamArgs a) {
+  const int t = blockIdx.y, n = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
+  constexpr int U = 8;
+  float w[U];
+  bool has[U];
+  auto slots = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t pair = t * a.topk + min(k0 + u, a.topk - 1);
+      const int e = ld_cg_i32(a.ids + pair);  // (from L2: no stale L1 line)
+      has[u] = k0 + u < a.topk && e >= 0 && e < a.E;
+      w[u] = __ldcg(a.weights + pair);
+    }
+  };
+  slots(0);
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.y, n = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
   if (n >= a.N) return;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f), deltas = sum;
   auto add = [](float4& s, float w, float v0, float v1, float v2, float v3) {
@@ -177,18 +191,13 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Stre
     s.z = fmaf(w, v2, s.z);
     s.w = fmaf(w, v3, s.w);
   };
-  constexpr int U = 4;
   for (int k0 = 0; k0 < a.topk; k0 += U) {
+    if (k0 > 0) slots(k0);
     float4 v[U];
     uint2 d[U];
-    float w[U];
-    bool has[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t pair = t * a.topk + min(k0 + u, a.topk - 1);
-      const int e = a.ids[pair];
-      has[u] = k0 + u < a.topk && e >= 0 && e < a.E;
-      w[u] = a.weights[pair];
       v[u] = *reinterpret_cast<const float4*>(a.partial + pair * a.N + n);
       d[u] = a.delta ? *reinterpret_cast<const uint2*>(a.delta + pair * a.delta_stride + n)
                      : make_uint2(0, 0);
