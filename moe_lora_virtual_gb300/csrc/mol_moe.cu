@@ -222,10 +222,12 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Stre
 // work of the warps (128 experts of 2048 x 768, top 8, layer: 32 pairs 29.7 us against 28.8, 64 pairs
 // 44.3 against 48.9, 768 pairs 97 against 121), for bf16 where experts have many tokens (496 pairs
 // 202 us against 194, 1016 pairs 217 against 250) or the down rows are short and their stages small
-// (102 pairs of 103 experts of 2520 x 72: 27 us against 32).
+// (102 pairs of 103 experts of 2520 x 72: 27 us against 32; of 232 x 232 both 13.7).
 size_t moe_split_bytes(const MoeShape& s, int group) {
   const int pairs = s.num_tokens * s.topk;
-  if (pairs <= 32 || (group == 0 && s.inter > 192 && pairs < 6 * s.num_experts)) return 0;
+  if (pairs <= 32) return 0;
+  const bool short_rows = s.inter <= 192 && s.hidden >= 256;
+  if (group == 0 && !short_rows && pairs < 6 * s.num_experts) return 0;
   return (size_t)pairs * s.hidden * sizeof(float);
 }
 
