@@ -76,8 +76,9 @@ int stream_smem(const StreamArgs& a, int group) {
 // 28.2).
 // Teams: the warps of a team split the inputs of a tile, so more parts fill all warps where a block has
 // few tiles, and leave less to wait for at the end; against that each tile costs its warps half a
-// chunk's time, or two for each token tile where their sums are to be added. Taken is the least of that
-// model, with one more tile a warp for the end: measured, an output head of 49 tiles a block takes
+// chunk's time, or two for each token tile where their sums are to be added, and two more with 4-bit
+// weights, whose warps then wait for one another's products. Taken is the least of that model, with
+// one more tile a warp for the end: measured, an output head of 49 tiles a block takes
 // 29.5 us with one part and 36 with four, a linear of one tile a block 5.5 us with one and 4.1 with
 // four.
 bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
@@ -106,7 +107,7 @@ bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
     fits = fits || slots(std::min(256, a.K), 1, kChunks);
     if (!fits) continue;
     const int per = (std::min(a.Kc, a.K) + inputs - 1) / inputs;
-    const double one = a.ksteps * ((per + parts - 1) / parts) + (parts > 1 ? 2 * nt : 0.5);
+    const double one = a.ksteps * ((per + parts - 1) / parts) + (parts > 1 ? 2 * nt + (group ? 2 : 0) : 0.5);
     const double rounds = block_tiles / a.teams;
     const double cost = (std::max(1.0, (rounds + 2 * std::ceil(rounds)) / 3) + 1) * one;
     if (best.parts && cost > least) continue;
