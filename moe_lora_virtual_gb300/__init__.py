@@ -138,6 +138,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _on(stream, device):
+    """Context in which a call allocates: its own stream's, so that the memory of a tensor that the
+    call drops, or that earlier work of that stream still uses, goes to nobody who does not wait for
+    that stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = (torch.cuda.default_stream(device) if raw in (0, 1)  # (1: cudaStreamLegacy)
+                  else torch.cuda.ExternalStream(raw, device=device))
+    return torch.cuda.stream(stream)
+
+
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")

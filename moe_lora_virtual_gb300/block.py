@@ -3,8 +3,9 @@
 Norms between blocks, the router's choice, the experts for a few tokens and the
 4-bit linear. As in the package itself the functions keep the C names, marshal
 arguments and raise ``MolError`` on a status; outputs that are not passed in are
-allocated. ``w4_pack``, ``w4_quantize`` and ``w4_unpack`` lay 4-bit weights out once,
-with torch operations on the tensors' own device.
+allocated, like scratch, on the stream that the call is enqueued on: with ``stream``
+they are that stream's tensors. ``w4_pack``, ``w4_quantize`` and ``w4_unpack`` lay
+4-bit weights out once, with torch operations on the tensors' own device.
 """
 
 from __future__ import annotations
@@ -185,9 +186,17 @@ def _delta(delta: Optional[torch.Tensor], pairs: int, width: int):
     return delta.data_ptr(), stride
 
 
-def _out(out: Optional[torch.Tensor], shape, like: torch.Tensor, name: str = "out"):
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor of the call, allocated on the stream that the call is enqueued on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _mol._on(stream, like.device):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(out: Optional[torch.Tensor], shape, like: torch.Tensor, stream, name: str = "out"):
     if out is None:
-        return torch.empty(shape, dtype=_bf16, device=like.device), shape[1]
+        return _empty(shape, _bf16, like, stream), shape[1]
     stride = _rows(out, _bf16, name)
     if out.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
@@ -246,16 +255,10 @@ def mol_block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: Optional
                 raise ValueError(f"gate: expected shape {(H,)} or {tuple(y.shape)}, got "
                                  f"{tuple(gate.shape)}")
     post, pre = _vector(post_weight, "post_weight", H), _vector(pre_weight, "pre_weight", H)
-    if residual_out is None:
-        residual_out, ros = torch.empty_like(y, memory_format=torch.contiguous_format), H
-    else:
-        residual_out, ros = _out(residual_out, shape, y, "residual_out")
+    residual_out, ros = _out(residual_out, shape, y, stream, "residual_out")
     ns = 0
     if pre is not None:
-        if normed is None:
-            normed, ns = torch.empty_like(y, memory_format=torch.contiguous_format), H
-        else:
-            normed, ns = _out(normed, shape, y, "normed")
+        normed, ns = _out(normed, shape, y, stream, "normed")
     elif normed is not None:
         raise ValueError("normed: needs pre_weight")
     _call("mol_block_norm", y.data_ptr(), ys, residual.data_ptr(), rs, post, gp, gs, residual_scale,
@@ -276,9 +279,9 @@ def mol_moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True, sca
     stride = _rows(logits, _bf16 if bf16 else _f32, "logits")
     T, E = logits.shape
     if topk_ids is None:
-        topk_ids = torch.empty((T, topk), dtype=_i32, device=logits.device)
+        topk_ids = _empty((T, topk), _i32, logits, stream)
     if topk_weights is None:
-        topk_weights = torch.empty((T, topk), dtype=_f32, device=logits.device)
+        topk_weights = _empty((T, topk), _f32, logits, stream)
     _call("mol_moe_route", logits.data_ptr(), MOL_BF16 if bf16 else MOL_F32, stride, T, E, topk,
           int(renormalize), scale, _flat(topk_ids, _i32, "topk_ids", (T, topk)),
           _flat(topk_weights, _f32, "topk_weights", (T, topk)), _stream(stream, logits))
@@ -302,7 +305,7 @@ def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
     wp, sp, group = _weights(w_gate_up, "w_gate_up", (E, I2), H)
     dp, ds = _delta(delta, T * k, I2)
     if act is None:
-        act = torch.empty((T * k, I2 // 2), dtype=_bf16, device=x.device)
+        act = _empty((T * k, I2 // 2), _bf16, x, stream)
     _call("mol_moe_gate_up", x.data_ptr(), _rows(x, _bf16, "x"),
           _flat(topk_ids, _i32, "topk_ids", (T, k)), T, k, E, H, I2 // 2, wp, sp, group, dp,
           ds, _flat(act, _bf16, "act", (T * k, I2 // 2)), _stream(stream, x))
@@ -316,13 +319,13 @@ def mol_moe_workspace_bytes(num_tokens: int, topk: int, num_experts: int, hidden
                                                                  hidden, inter, group)
 
 
-def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, *shape):
+def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, *shape):
     """(pointer, bytes, tensor) of the workspace for these sizes: the one given, or a new one."""
     need = mol_moe_workspace_bytes(*shape)
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _empty(need, torch.uint8, like, stream)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace: expected a contiguous CUDA tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -346,8 +349,8 @@ def mol_moe_down(act: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
     I = act.shape[1]
     wp, sp, group = _weights(w_down, "w_down", (E, H), I)
     dp, ds = _delta(delta, T * k, H)
-    out, os = _out(out, (T, H), act)
-    ws, wsb, workspace = _workspace(workspace, act, T, k, E, H, I, group)
+    out, os = _out(out, (T, H), act, stream)
+    ws, wsb, workspace = _workspace(workspace, act, stream, T, k, E, H, I, group)
     _call("mol_moe_down_split", _flat(act, _bf16, "act", (T * k, I)),
           _flat(topk_ids, _i32, "topk_ids", (T, k)),
           _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, wp, sp, group,
@@ -379,9 +382,9 @@ def mol_moe_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
     if group != group_down:
         raise ValueError("w_gate_up, w_down: expected the same type and group")
     if act is None:
-        act = torch.empty((T * k, I), dtype=_bf16, device=x.device)
-    out, os = _out(out, (T, H), x)
-    ws, wsb, workspace = _workspace(workspace, x, T, k, E, H, I, group)
+        act = _empty((T * k, I), _bf16, x, stream)
+    out, os = _out(out, (T, H), x, stream)
+    ws, wsb, workspace = _workspace(workspace, x, stream, T, k, E, H, I, group)
     _call("mol_moe_forward_split", x.data_ptr(), _rows(x, _bf16, "x"),
           _flat(topk_ids, _i32, "topk_ids", (T, k)),
           _flat(topk_weights, _f32, "topk_weights", (T, k)), T, k, E, H, I, gp, gsp, wp,
@@ -402,7 +405,7 @@ def mol_w4_linear(x: torch.Tensor, w: W4, out: Optional[torch.Tensor] = None,
     T, K = x.shape
     (N,) = _lead(w)
     wp, sp, group = _weights(w, "w", (N,), K)
-    out, os = _out(out, (T, N), x)
+    out, os = _out(out, (T, N), x, stream)
     _call("mol_w4_linear", x.data_ptr(), _rows(x, _bf16, "x"), T, K, N, wp, sp, group,
           out.data_ptr(), os, _stream(stream, x))
     return out

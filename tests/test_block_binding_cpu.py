@@ -1,0 +1,120 @@
+"""The Python path of the MoE block's binding without a GPU: stand-ins for CUDA tensors, streams and
+the library, so that what a call allocates where, and what it hands over, can be looked at."""
+
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import moe_lora_virtual_gb300 as mol  # noqa: E402
+from moe_lora_virtual_gb300 import block  # noqa: E402
+
+bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+
+
+class Cuda(torch.Tensor):
+    """A host tensor that says that it is on the GPU."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def cuda(*shape, dtype=bf16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Cuda)
+
+
+class Stream:
+    """A stream that is only a handle (nothing is created)."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    """The calls that reach the library, and (stream, shape) of what is allocated."""
+    seen = SimpleNamespace(calls=[], made=[], at=None)
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                seen.calls.append((name, args))
+                return 4096 if name == "mol_moe_workspace_bytes" else 0
+            return call
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, seen.at = seen.at, stream
+        try:
+            yield
+        finally:
+            seen.at = before
+
+    real = torch.empty
+
+    def empty(shape, *more, dtype=None, device=None):
+        shape = (shape, *more) if isinstance(shape, int) else tuple(shape)
+        seen.made.append((seen.at, shape))
+        return real(shape, dtype=dtype).as_subclass(Cuda)
+
+    monkeypatch.setattr(block, "_native", None)
+    monkeypatch.setattr(mol, "_lib", Library())
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    return seen
+
+
+def calls(stream):
+    """Every call of the block with nothing passed in that it would allocate."""
+    T, k, E, H, I = 5, 2, 4, 64, 32
+    x, ids, w = cuda(T, H), cuda(T, k, dtype=i32), cuda(T, k, dtype=f32)
+    gu, dn = cuda(E, 2 * I, H), cuda(E, H, I)
+    head = mol.W4(cuda(7, 128, dtype=torch.uint8), cuda(7, 8), H, 32)
+    return {
+        "norm": (lambda: mol.mol_block_norm(x, x, cuda(H), stream=stream), 2),
+        "route": (lambda: mol.mol_moe_route(cuda(T, E, dtype=f32), k, stream=stream), 2),
+        "gate_up": (lambda: mol.mol_moe_gate_up(x, ids, gu, stream=stream), 1),
+        "down": (lambda: mol.mol_moe_down(cuda(T * k, I), ids, w, dn, stream=stream), 2),
+        "forward": (lambda: mol.mol_moe_forward(x, ids, w, gu, dn, stream=stream), 3),
+        "linear": (lambda: mol.mol_w4_linear(x, head, stream=stream), 1),
+    }
+
+
+NAMES = ["norm", "route", "gate_up", "down", "forward", "linear"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_and_scratch_are_the_streams_own(binding, name):
+    """Memory of the current stream would be handed out again, or still be in use there, while the
+    kernels on the call's stream write it."""
+    side = Stream(0x1230)
+    call, tensors = calls(side)[name]
+    call()
+    assert len(binding.made) == tensors
+    assert all(at is side for at, _ in binding.made), binding.made
+    assert binding.calls[-1][1][-1] == 0x1230 and binding.at is None
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_a_stream_the_current_one_is_used(binding, name, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x77)
+    call, tensors = calls(None)[name]
+    call()
+    assert [at for at, _ in binding.made] == [None] * tensors
+    assert binding.calls[-1][1][-1] == 0x77
+
+
+def test_raw_stream_handles(binding, monkeypatch):
+    """A handle as an integer: the stream itself; 0 and 1 name the default stream."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device=None: made.append(raw) or "external")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    for handle, stream in ((0, "default"), (1, "default"), (0x5550, "external")):
+        binding.made.clear()
+        calls(handle)["forward"][0]()
+        assert [at for at, _ in binding.made] == [stream] * 3
+        assert binding.calls[-1][1][-1] == handle
+    assert made == [0x5550] * 3
