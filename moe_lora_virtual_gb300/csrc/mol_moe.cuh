@@ -106,6 +106,12 @@ MOL_DEV void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* 
       : "memory");
 }
 
+// A whole warp's bounded wait. The lanes vote: where the limit passes between two lanes' polls, some
+// would see the phase complete and others not, and part ways before the warp's next barrier.
+MOL_DEV bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitPolls, limit_ns));
+}
+
 // Tokens of one expert: a tile's columns.
 struct Entry {
   int e, off, n;
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       int left = a.entry_rows - (lo - entry0 * a.entry_rows);  // pieces: rows of the entry to come
       int i = 0, s = 0, use = 0;
       for (; i < slots; ++i) {
-        if (use > 0 && !mbar_wait(&xempty[s], (use - 1) & 1, kWaitPolls, limit)) {
+        if (use > 0 && !warp_wait(&xempty[s], (use - 1) & 1, limit)) {
           fault = true;
           break;
         }
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
       // no copy may be in flight when the block leaves
       if (fault)
         for (int q = max(0, i - a.xstages); q < i; ++q)
-          (void)mbar_wait(&xfull[q % a.xstages], (q / a.xstages) & 1, kWaitPolls, limit);
+          (void)warp_wait(&xfull[q % a.xstages], (q / a.xstages) & 1, limit);
     }
   } else if (slots > 0 && warp < consumers) {
     // ---- consumers ----
@@ -829,8 +835,7 @@ __global__ void __launch_bounds__(consumer_warps(NT) * 32 + 32, 1)
         xs = 0;
         xphase ^= 1;
       }
-      if (++xi < slots)
-        fault = __any_sync(0xffffffffu, !mbar_wait(&xfull[xs], xphase, kWaitPolls, limit));
+      if (++xi < slots) fault = !warp_wait(&xfull[xs], xphase, limit);
     };
     int want = 0;  // the token slot of this step
     Entry en{0, 0, 0};
@@ -1120,7 +1125,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
     const int my_row = part * 16;
     int slot = 0, phase = 0;
     for (int unit = lo + team; unit < hi; unit += a.teams) {
-      fault = !mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+      fault = !warp_wait(&my_full[slot], phase, limit);
       if (fault) break;
       const int entry = unit / a.ksteps, ks = unit - entry * a.ksteps;
       const Entry en = lists.get(entry);
@@ -1159,7 +1164,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
         if (part > 0) {
           if (lane == 0) mbar_arrive(&my_pfull[slot]);
         } else {
-          fault = !mbar_wait(&my_pfull[slot], phase, kWaitPolls, limit);
+          fault = !warp_wait(&my_pfull[slot], phase, limit);
           if (fault) break;
         }
       }
@@ -1194,7 +1199,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
     // no copy may be in flight when the block leaves
     if (fault && part == 0)
       for (int q = 0; q < filled; ++q) {
-        (void)mbar_wait(&my_full[slot], phase, kWaitPolls, limit);
+        (void)warp_wait(&my_full[slot], phase, limit);
         if (++slot == depth) {
           slot = 0;
           phase ^= 1;
