@@ -302,6 +302,8 @@ def mol_moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, w_gate_up: Weights,
             return done
     (T, H), k = x.shape, topk_ids.shape[1]
     E, I2 = _lead(w_gate_up)
+    if I2 % 2:
+        raise ValueError(f"w_gate_up: expected as many up rows as gate rows, got {I2} in all")
     wp, sp, group = _weights(w_gate_up, "w_gate_up", (E, I2), H)
     dp, ds = _delta(delta, T * k, I2)
     if act is None:

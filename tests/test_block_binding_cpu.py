@@ -118,3 +118,18 @@ def test_raw_stream_handles(binding, monkeypatch):
         assert [at for at, _ in binding.made] == [stream] * 3
         assert binding.calls[-1][1][-1] == handle
     assert made == [0x5550] * 3
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_an_odd_number_of_gate_and_up_rows_is_refused(binding, group):
+    """17 rows are no gate and up halves: the second expert's would be read one row too early."""
+    T, k, E, H = 5, 2, 4, 64
+    gu = cuda(E, 17, H)
+    if group:
+        gu = mol.W4(cuda(E, 17, 128, dtype=torch.uint8), cuda(E, 17, 256 // group), H, group)
+    x, ids = cuda(T, H), cuda(T, k, dtype=i32)
+    with pytest.raises(ValueError):
+        mol.mol_moe_gate_up(x, ids, gu, stream=Stream(0))
+    with pytest.raises(ValueError):
+        mol.mol_moe_forward(x, ids, cuda(T, k, dtype=f32), gu, cuda(E, H, 8), stream=Stream(0))
+    assert not [c for c in binding.calls if c[0] != "mol_moe_workspace_bytes"]
