@@ -2,10 +2,11 @@
 
 Norms between blocks, the router's choice, the experts for a few tokens and the
 4-bit linear. As in the package itself the functions keep the C names, marshal
-arguments and raise ``MolError`` on a status; outputs that are not passed in are
-allocated, like scratch, on the stream that the call is enqueued on: with ``stream``
-they are that stream's tensors. ``w4_pack``, ``w4_quantize`` and ``w4_unpack`` lay
-4-bit weights out once, with torch operations on the tensors' own device.
+arguments and raise ``MolError`` on a status; operands are on the current device.
+Outputs that are not passed in are allocated, like scratch, on the stream that the
+call is enqueued on: with ``stream`` they are that stream's tensors. ``w4_pack``,
+``w4_quantize`` and ``w4_unpack`` lay 4-bit weights out once, with torch operations on
+the tensors' own device.
 """
 
 from __future__ import annotations
@@ -132,10 +133,19 @@ def w4_unpack(w: W4) -> torch.Tensor:
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 
 
+def _here(t: torch.Tensor, name: str) -> None:
+    """A call launches on the current device, so all of its operands have to be there."""
+    at = torch.cuda.current_device()
+    if t.get_device() != at:
+        raise ValueError(f"{name}: expected a tensor on the current device, cuda:{at}, got one on "
+                         f"cuda:{t.get_device()}")
+
+
 def _rows(t: torch.Tensor, dtype, name: str) -> int:
     """Row stride of a 2-D CUDA operand with unit column stride."""
     if t.dtype != dtype or not t.is_cuda:
         _mol._need(t, dtype, name)
+    _here(t, name)
     stride, shape = t.stride(), t.shape
     if len(stride) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: expected a 2-D tensor with unit column stride")
@@ -146,6 +156,7 @@ def _rows(t: torch.Tensor, dtype, name: str) -> int:
 def _flat(t: torch.Tensor, dtype, name: str, shape) -> int:
     if t.dtype != dtype or not t.is_cuda:
         _mol._need(t, dtype, name)
+    _here(t, name)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
@@ -330,6 +341,7 @@ def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, *s
         workspace = _empty(need, torch.uint8, like, stream)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace: expected a contiguous CUDA tensor")
+    _here(workspace, "workspace")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 

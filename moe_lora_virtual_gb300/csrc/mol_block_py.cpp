@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -20,9 +21,12 @@ namespace {
 
 using at::Tensor;
 
+// A tensor on the current device, which is the one that a call launches on.
+bool here(const Tensor& t) { return t.is_cuda() && t.get_device() == c10::cuda::current_device(); }
+
 // A plain tensor on the GPU, contiguous, of the type and shape; sizes of -1 match any.
 bool fits(const Tensor& t, at::ScalarType type, c10::IntArrayRef sizes) {
-  if (t.scalar_type() != type || !t.is_cuda() || t.dim() != (int64_t)sizes.size() ||
+  if (t.scalar_type() != type || !here(t) || t.dim() != (int64_t)sizes.size() ||
       !t.is_contiguous())
     return false;
   for (size_t i = 0; i < sizes.size(); ++i)
@@ -33,7 +37,7 @@ bool fits(const Tensor& t, at::ScalarType type, c10::IntArrayRef sizes) {
 // A plain tensor of rows on the GPU, its columns neighbours; the row stride of a single row (or none)
 // does not matter.
 bool rows_fit(const Tensor& t, at::ScalarType type, int64_t rows, int64_t columns, int64_t& stride) {
-  if (t.scalar_type() != type || !t.is_cuda() || t.dim() != 2 || t.size(0) != rows ||
+  if (t.scalar_type() != type || !here(t) || t.dim() != 2 || t.size(0) != rows ||
       t.size(1) != columns || (t.stride(1) != 1 && columns > 1))
     return false;
   stride = rows > 1 ? t.stride(0) : (columns + 7) / 8 * 8;

@@ -18,7 +18,7 @@ class Cuda(torch.Tensor):
     is_cuda = property(lambda self: True)
 
     def get_device(self):
-        return 0
+        return getattr(self, "on", 0)
 
 
 def cuda(*shape, dtype=bf16):
@@ -64,6 +64,7 @@ def binding(monkeypatch):
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     return seen
 
 
@@ -133,3 +134,48 @@ def test_an_odd_number_of_gate_and_up_rows_is_refused(binding, group):
     with pytest.raises(ValueError):
         mol.mol_moe_forward(x, ids, cuda(T, k, dtype=f32), gu, cuda(E, H, 8), stream=Stream(0))
     assert not [c for c in binding.calls if c[0] != "mol_moe_workspace_bytes"]
+
+
+@pytest.mark.parametrize("stream", [None, Stream(0x40)])
+def test_operands_on_another_device_are_refused(binding, stream, monkeypatch):
+    """Each operand in turn on a device that is not the current one: nothing is enqueued."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x77)
+    T, k, E, H, I = 40, 2, 4, 64, 32
+    x, y, vec, ids = cuda(T, H), cuda(T, H), cuda(H), cuda(T, k, dtype=i32)
+    w, gu, dn = cuda(T, k, dtype=f32), cuda(E, 2 * I, H), cuda(E, H, I)
+    q, s = cuda(7, 128, dtype=torch.uint8), cuda(7, 8)
+    act, dgu, ddn = cuda(T * k, I), cuda(T * k, 2 * I), cuda(T * k, H)
+    out, ws = cuda(T, H), cuda(4096, dtype=torch.uint8)
+    logits, out7 = cuda(T, E, dtype=f32), cuda(T, 7)
+
+    def norm(x, y, v, p, gate, out, normed):
+        mol.mol_block_norm(x, y, v, post_weight=p, gate=gate, residual_out=out, normed=normed,
+                           stream=stream)
+
+    def gate_up(x, ids, gu, delta, act):
+        mol.mol_moe_gate_up(x, ids, gu, act=act, delta=delta, stream=stream)
+
+    def down(act, ids, w, dn, delta, out, ws):
+        mol.mol_moe_down(act, ids, w, dn, out=out, delta=delta, workspace=ws, stream=stream)
+
+    def forward(x, ids, w, gu, dn, out, act, ws):
+        mol.mol_moe_forward(x, ids, w, gu, dn, out=out, act=act, workspace=ws, stream=stream)
+
+    def route(logits, ids, w):
+        mol.mol_moe_route(logits, k, topk_ids=ids, topk_weights=w, stream=stream)
+
+    def linear(x, q, s, out):
+        mol.mol_w4_linear(x, mol.W4(q, s, H, 32), out=out, stream=stream)
+
+    for call, operands in [(norm, (x, y, vec, cuda(H), cuda(T, H), out, cuda(T, H))),
+                           (route, (logits, ids, w)), (gate_up, (x, ids, gu, dgu, act)),
+                           (down, (act, ids, w, dn, ddn, out, ws)),
+                           (forward, (x, ids, w, gu, dn, out, act, ws)), (linear, (x, q, s, out7))]:
+        call(*operands)  # (all on the current device)
+        for t in operands:
+            binding.calls.clear()
+            t.on = 1
+            with pytest.raises(ValueError, match="current device"):
+                call(*operands)
+            del t.on
+            assert not [c for c in binding.calls if c[0] != "mol_moe_workspace_bytes"]
