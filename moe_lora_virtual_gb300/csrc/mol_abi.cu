@@ -36,6 +36,8 @@ bool valid_block_m(int32_t bm) { return bm == 16 || bm == 32 || bm == 64 || bm =
 // Read without the lock on every call; written under it once per device.
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_state[kMaxDevices] = {};
+// Per device: 1 once the experts' kernels are prepared as well.
+std::atomic<int> g_moe_state[kMaxDevices] = {};
 std::mutex g_device_mutex;
 
 }  // namespace
@@ -63,6 +65,25 @@ int32_t mol::ensure_device() {
     }
   }
   return g_device_state[dev].load(std::memory_order_relaxed) == 1 ? MOL_OK : MOL_ERR_UNSUPPORTED;
+}
+
+// ensure_device, and the kernels of the experts and the 4-bit linear prepared, which ask for nearly
+// all of an SM's shared memory: where they cannot be had, these calls alone are refused.
+int32_t mol::ensure_moe_device() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev >= 0 && dev < kMaxDevices && g_moe_state[dev].load(std::memory_order_acquire) == 1)
+    return MOL_OK;
+  const int32_t st = ensure_device();
+  if (st != MOL_OK) return st;
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  if (g_moe_state[dev].load(std::memory_order_relaxed) == 0) {
+    e = mol::prepare_moe_kernels();
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_moe_state[dev].store(1, std::memory_order_release);
+  }
+  return MOL_OK;
 }
 
 namespace {

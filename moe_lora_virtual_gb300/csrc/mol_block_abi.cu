@@ -89,7 +89,7 @@ int32_t forward(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
   const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
   bool split = false;
   if (may_split) MOL_TRY(check_workspace(s, group, workspace, workspace_bytes, split));
-  MOL_TRY(mol::ensure_device());
+  MOL_TRY(mol::ensure_moe_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mol::launch_moe_gate_up(
       s, x, x_row_stride, topk_ids, mol::WeightRows{w_gate_up, gate_up_scales, hidden, group},
@@ -175,7 +175,7 @@ int32_t mol_moe_gate_up(const void* x, int64_t x_row_stride, const int32_t* topk
   MOL_TRY(check_weights(w, w_scales, group, false));
   MOL_TRY(check_delta(delta, delta_row_stride, 2 * (int64_t)inter));
   MOL_TRY(check_rows(act, inter, inter));
-  MOL_TRY(mol::ensure_device());
+  MOL_TRY(mol::ensure_moe_device());
   const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
   return done(mol::launch_moe_gate_up(s, x, x_row_stride, topk_ids,
                                       mol::WeightRows{w, w_scales, hidden, group}, delta,
@@ -190,7 +190,7 @@ int32_t mol_moe_down(const void* act, const int32_t* topk_ids, const float* topk
   MOL_TRY(check_down(act, topk_ids, topk_weights, num_tokens, topk, num_experts, hidden, inter, w,
                      w_scales, group, delta, delta_row_stride, out, out_row_stride));
   if (num_tokens == 0) return MOL_OK;
-  MOL_TRY(mol::ensure_device());
+  MOL_TRY(mol::ensure_moe_device());
   const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
   return done(mol::launch_moe_down(s, act, topk_ids, topk_weights,
                                    mol::WeightRows{w, w_scales, inter, group}, delta,
@@ -218,7 +218,7 @@ int32_t mol_moe_down_split(const void* act, const int32_t* topk_ids, const float
   const mol::MoeShape s{(int)num_tokens, topk, num_experts, hidden, inter};
   bool split = false;
   MOL_TRY(check_workspace(s, group, workspace, workspace_bytes, split));
-  MOL_TRY(mol::ensure_device());
+  MOL_TRY(mol::ensure_moe_device());
   const mol::WeightRows rows{w, w_scales, inter, group};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(split ? mol::launch_moe_down_split(s, act, topk_ids, topk_weights, rows, delta,
@@ -261,7 +261,7 @@ int32_t mol_w4_linear(const void* x, int64_t x_row_stride, int64_t num_tokens, i
   if (reinterpret_cast<uintptr_t>(out) % 2 != 0) return MOL_ERR_UNSUPPORTED;
   MOL_TRY(check_rows(x, x_row_stride, K));
   MOL_TRY(check_weights(w, scales, group, true));
-  MOL_TRY(mol::ensure_device());
+  MOL_TRY(mol::ensure_moe_device());
   return done(mol::launch_w4_linear(x, x_row_stride, (int)num_tokens, N,
                                     mol::WeightRows{w, scales, K, group}, out, out_row_stride,
                                     static_cast<cudaStream_t>(stream)));

@@ -13,6 +13,8 @@ void count_launch();
 int32_t cuda_fail(cudaError_t e);
 // MOL_OK once the current device is a prepared sm_103 part (see mol_abi.cu).
 int32_t ensure_device();
+// The same with the kernels of the experts and the 4-bit linear prepared.
+int32_t ensure_moe_device();
 
 // Geometry of the align step for given sizes (host arithmetic).
 struct AlignPlan {

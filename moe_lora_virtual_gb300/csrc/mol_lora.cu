@@ -1076,8 +1076,6 @@ cudaError_t prepare_lora_kernels() {
   if (e != cudaSuccess) return e;
   e = prepare_expand_tc_kernels();
   if (e != cudaSuccess) return e;
-  e = prepare_moe_kernels();
-  if (e != cudaSuccess) return e;
   e = prepare_expand_st<64, true>();
   if (e != cudaSuccess) return e;
   e = prepare_expand_st<64, false>();
