@@ -1,0 +1,115 @@
+"""CPU checks of how the experts and the 4-bit linear deal out their work: the host side that plans a
+launch, compiled by itself (tests/host/moe_plan.cu), over the shapes of the GPU tests and over random
+ones of the whole contract."""
+
+import math
+import os
+import random
+import re
+import subprocess
+
+import pytest
+
+from tests import test_gpu_block, test_gpu_block_paths
+from tests.test_abi_cpu import needs_nvcc
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+GATE_UP, DOWN, LINEAR, PAIRS = 0, 1, 2, 3  # of a launch
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    """launches(lines): for each call the launches it makes, as dicts."""
+    from moe_lora_virtual_gb300.build import ARCH_FLAGS, nvcc_path
+
+    exe = str(tmp_path_factory.mktemp("plan") / "moe_plan")
+    subprocess.run([nvcc_path(), "-std=c++17", "-O1", *ARCH_FLAGS, "-I", os.path.join(ROOT, "include"),
+                    "-I", os.path.join(ROOT, "moe_lora_virtual_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "host", "moe_plan.cu"), "-o", exe], check=True)
+
+    def launches(lines):
+        out = subprocess.run([exe], input="\n".join(lines), capture_output=True, text=True, check=True)
+        out = out.stdout.splitlines()
+        assert len(out) == len(lines)
+        return [[{k: int(v) for k, v in re.findall(r"(\w+)=(-?\d+)", launch)}
+                 for launch in re.findall(r"{(.*?)}", line)] for line in out]
+
+    return launches
+
+
+def tiles(a):
+    return 1 if a["xrows"] <= 8 else 2 if a["xrows"] <= 16 else 4
+
+
+def way(a):
+    """What tells the ways through a kernel apart, of one launch."""
+    w4 = a["group"] != 0
+    if a["mode"] == DOWN:
+        return "down", w4, a["cluster"], a["ksteps"] > 1, tiles(a)
+    return ("gate_up", "", "linear", "split")[a["mode"]], w4, a["xstages"], a["chunks"], \
+        a["ksteps"] > 1, tiles(a), a["parts"] > 1
+
+
+def calls_of_the_gpu_tests():
+    shapes = list(test_gpu_block_paths.EXPERTS)
+    for T, E, k, H, I, _ in test_gpu_block.SHAPES:
+        shapes += [(group, T, k, E, H, I) for group in test_gpu_block.FORMATS]
+    lines = [f"{half} " + " ".join(map(str, s)) for s in shapes for half in ("gate_up", "down", "split")]
+    linear = list(test_gpu_block_paths.LINEAR)
+    for mark in test_gpu_block.test_linear.pytestmark:
+        if mark.name == "parametrize" and mark.args[0] == "T,K,N":
+            linear += [(group, *s) for s in mark.args[1] for group in (32, 64, 128)]
+    assert len(linear) > len(test_gpu_block_paths.LINEAR)
+    return lines + ["linear " + " ".join(map(str, s)) for s in linear]
+
+
+def random_calls(n, seed, most=math.inf):
+    rng = random.Random(seed)
+
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    lines = []
+    while len(lines) < n:
+        T = log(1, 128)
+        k, E, H, I = log(1, 1024 // T), log(1, 1024), 8 * log(1, 8192), 8 * log(1, 8192)
+        group = rng.choice([0, 32, 64, 128])
+        if 3 * E * H * I <= most and k <= (E if most < math.inf else k):
+            lines += [f"{half} {group} {T} {k} {E} {H} {I}" for half in ("gate_up", "down", "split")]
+        N = log(1, 1 << 30) if rng.random() < 0.05 else log(1, 200000)
+        if group and H * N <= most:
+            lines.append(f"linear {group} {log(1, 64)} {H} {N}")
+    return lines
+
+
+@needs_nvcc
+def test_the_gpu_tests_reach_every_way(plan):
+    """Ways of random shapes of up to 10^9 weights, each expert at most once a token."""
+    reached = {way(a) for line in plan(calls_of_the_gpu_tests()) for a in line}
+    lines = random_calls(40000, 1, most=1e9)
+    missing = {}
+    for line, launches in zip(lines, plan(lines)):
+        for a in launches:
+            if way(a) not in reached:
+                missing.setdefault(way(a), line)
+    assert not missing, missing
+
+
+@needs_nvcc
+def test_an_entry_a_launch_where_rows_pass_32_bits(plan):
+    """Each launch's tokens follow those of the one before, and none is left out."""
+    base = 1 << 40
+    lines = [f"linear {group} {T} {K} {N}" for group in (32, 64, 128) for T in (33, 50, 64)
+             for K in (8, 2048, 20000) for N in (1 << 27, (1 << 30) // 3, (1 << 30) - 15, 1 << 30)]
+    several = 0
+    for line, launches in zip(lines, plan(lines)):
+        _, _, T, K, N = line.split()
+        at = 0
+        for a in launches:
+            assert a["x"] == base + 2 * int(K) * at and a["out"] == base + 2 * int(N) * at, line
+            entries = -(-a["tokens"] // a["xrows"])
+            assert entries * a["entry_rows"] <= (1 << 30) + 4096, line
+            at += a["tokens"]
+        assert at == int(T), line
+        several += len(launches) > 1
+    assert several > len(lines) // 4
