@@ -44,9 +44,7 @@ int entry_tokens(int num_tokens, int pairs, int experts) {
 
 int token_tiles(int xrows) { return xrows <= 8 ? 1 : xrows <= 16 ? 2 : 4; }
 
-// down: the ring is the lists' scratch first, 36 KB at most: sixteen stages of this size hold it, and
-// rings of fewer are larger.
-constexpr int kLeastStage = 2304;
+constexpr int kLeastStage = 2304;  // down: stages are no smaller
 
 // Rows of Kc inputs in a stage: as they lie in memory (one copy), or pieces of them (a copy each).
 void row_layout(StreamArgs& a, int group, int rows, int Kc) {
@@ -156,6 +154,16 @@ StreamArgs common_args(const MoeShape& s, const void* x, int64_t x_stride, const
   a.cluster = 1;
   a.xrows = entry_tokens(s.num_tokens, s.num_tokens * s.topk, s.num_experts);
   return a;
+}
+
+// What grouping the pairs takes in shared memory besides the lists (build_lists: the ids, and each
+// warp's counts of each expert).
+int scratch_bytes(const MoeShape& s) {
+  const int numel = s.num_tokens * s.topk;
+  if (numel <= 32) return 0;
+  const int rounds = (numel + kListThreads - 1) / kListThreads;
+  const int warps = (numel + rounds * 32 - 1) / (rounds * 32);
+  return 4 * numel + align_up(2 * warps * s.num_experts, 4);
 }
 
 int list_bytes(const MoeShape& s) { return s.num_tokens * s.topk * 16; }
@@ -291,6 +299,8 @@ cudaError_t launch_moe_down(const MoeShape& s, const void* act, const int32_t* t
     const int fixed =
         list_bytes(s) + (cluster > 1 ? align_up(s.num_tokens, cluster) * a.acc_stride * 4 : 0);
     if (fixed + copy > kSmem / 2 || !plan_down(a, w.group, rows, Kc, fixed, copy, stages)) return;
+    // the lists' scratch lies where the ring and, behind it, the teams' sums will be
+    if (a.stages * a.stage_bytes + a.teams * copy < scratch_bytes(s)) return;
     const int64_t bytes =
         waves * ((units + cluster - 1) / cluster) * (rows * row_bytes + x_bytes) +
         (cluster > 1 ? 65536 : 0);

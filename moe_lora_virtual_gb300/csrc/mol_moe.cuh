@@ -54,7 +54,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kListThreads = 512;  // of the block's first warps
 constexpr int kListWarps = kListThreads / 32;
 constexpr int kExpertsPerThread = MOL_MOE_MAX_EXPERTS / kListThreads;
 constexpr int kPairsPerThread = MOL_MOE_MAX_PAIRS / kListThreads;
@@ -133,7 +132,7 @@ struct Lists {
 
 // Groups the pairs by expert, in the order of their index: every block finds the same entries, so
 // blocks that hold different rows of one expert agree on which entry has which pair. An expert with
-// more than xrows pairs (a power of two) takes several entries. `scratch`: 32 E + 4 numel bytes,
+// more than xrows pairs (a power of two) takes several entries. `scratch`: 32 E + 4 numel bytes at most,
 // free again afterwards. The block waits for nothing but its own ids, and the code is kept short: it
 // runs once a launch, from cold instruction caches.
 MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weights) {
@@ -1036,7 +1035,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) down_kernel(const __grid_
   const int ranks = a.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
   if (ranks > 1) cluster_arrive();  // (waited for before the first access to another block)
   build_lists(a, lists, smem, true);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scratch becomes the ring
+  // the scratch becomes the ring and the teams' sums (which are zeroed below, not before)
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   int first_row, end_row, lo, hi;
   share(a.N, gridDim.x / ranks, blockIdx.x / ranks, first_row, end_row);
   share(lists.count * a.ksteps, ranks, rank, lo, hi);

@@ -18,6 +18,7 @@ __host__ __device__ constexpr int consumer_warps(int token_tiles) { return token
 // each of a tile's 16 weight rows, and their scales.
 constexpr int kChunks = 4;
 __host__ __device__ constexpr int chunk_bytes(int group) { return 2048 + (group ? 16 * 512 / group : 0); }
+constexpr int kListThreads = 512;  // of a block's first warps group the pairs by expert
 constexpr int kMaxStages = 32;  // of all teams of a block
 constexpr int kClusterSizes = 3;  // down: clusters of 1, 2 or 4 blocks
 constexpr int kSmem = 222 * 1024;

@@ -113,3 +113,44 @@ def test_an_entry_a_launch_where_rows_pass_32_bits(plan):
         assert at == int(T), line
         several += len(launches) > 1
     assert several > len(lines) // 4
+
+
+def scratch(a):
+    """Bytes that grouping the pairs takes: ids, and counts of 16 bits of each warp and expert."""
+    numel = a["tokens"] * a["topk"]
+    if numel <= 32:
+        return 0
+    rounds = -(-numel // 512)
+    warps = -(-numel // (32 * rounds))
+    return 4 * numel + -(-2 * warps * a["E"] // 4) * 4
+
+
+@needs_nvcc
+def test_shared_memory_of_a_launch(plan):
+    """The parts of a block's shared memory lie one behind the other and fit; the scratch that groups
+    the pairs ends before the lists that it makes: in down it may reach past the ring into the teams'
+    sums, which are zeroed afterwards."""
+    room = 222 * 1024
+    lines = random_calls(60000, 2) + [f"down 0 128 8 1000 1024 {I}" for I in (32, 40, 48, 56)]
+    past_ring = 0
+    for line, launches in zip(lines, plan(lines)):
+        assert launches or line.startswith("split"), f"refused: {line}"
+        for a in launches:
+            numel, tokens = a["tokens"] * a["topk"], a["tokens"]
+            chunk = 2048 + (16 * 512 // a["group"] if a["group"] else 0)
+            if a["mode"] == DOWN:
+                ring, sums = a["stages"] * a["stage_bytes"], a["teams"] * tokens * a["acc_stride"] * 4
+                each = -(-tokens // a["cluster"])
+                lists = ring + sums + (each * a["cluster"] * a["acc_stride"] * 4 if a["cluster"] > 1 else 0)
+                end, free = lists + 16 * numel, ring + sums
+                past_ring += scratch(a) > ring
+                assert a["stages"] % a["teams"] == 0 and a["stage_bytes"] >= a["x_off"] + a["xrows"] * a["x_pitch"]
+            else:
+                warps = 15 if tiles(a) == 4 else 16
+                free = warps * a["chunks"] * chunk + a["xstages"] * a["xslot_bytes"]
+                end = free + a["teams"] * (a["parts"] - 1) * tiles(a) * 512
+                end += 0 if a["mode"] == LINEAR else 12 * numel
+                assert a["teams"] * a["parts"] <= warps and a["xslot_bytes"] >= a["xrows"] * a["x_pitch"]
+            assert end <= a["smem"] <= room, line
+            assert a["mode"] == LINEAR or scratch(a) <= free, line
+    assert past_ring >= 4
