@@ -17,11 +17,14 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 import moe_lora_virtual_gb300 as _mol
+from .build import native_current
 
-try:  # the common case of each call in one native step; None from it: the Python path below
-    from . import _block_native as _native
-except ImportError:
-    _native = None
+_native = None  # the common case of each call in one native step; None from it: the Python path below
+if native_current():  # (one that was built for another PyTorch might load, and fail later)
+    try:
+        from . import _block_native as _native
+    except ImportError:
+        pass
 
 BLOCK_EXPORTS = ("mol_block_norm", "mol_moe_route", "mol_moe_gate_up", "mol_moe_down",
                  "mol_moe_forward", "mol_moe_workspace_bytes", "mol_moe_down_split",

@@ -1,14 +1,16 @@
 """Build libmol.so (the MoL LoRA CUDA library) in-tree with nvcc for sm_103a.
 
 Beside it _block_native.so, the native calls of the MoE block's binding: plain C++ against
-PyTorch's headers. Without it (no compiler for them, or another PyTorch) the binding takes its
-Python path, which gives the same results."""
+PyTorch's headers. Without it (no compiler for them, or built for another PyTorch or Python) the
+binding takes its Python path, which gives the same results."""
 
 from __future__ import annotations
 
 import os
+import platform
 import shutil
 import subprocess
+import sys
 import sysconfig
 import warnings
 
@@ -20,6 +22,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmol.so")
 # The same sources with device-side index checks (MOL_CHECKED): a diagnostic build.
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libmol_checked.so")
 NATIVE_PATH = os.path.join(PKG_DIR, "_block_native.so")
+NATIVE_STAMP = NATIVE_PATH + ".stamp"  # what it was built for
 NATIVE_SOURCE = os.path.join(CSRC, "mol_block_py.cpp")
 
 SOURCES = ["mol_abi.cu", "mol_align.cu", "mol_lora.cu", "mol_umma.cu", "mol_stage.cu",
@@ -36,8 +39,24 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the MoL library needs the CUDA toolkit to build")
 
 
+def _built_for() -> str:
+    """What the native calls' binary interface depends on."""
+    import torch
+
+    return f"python {sys.version}\ntorch {torch.__version__}\n{platform.machine()}\n"
+
+
+def native_current() -> bool:
+    """Whether the native calls were built for this Python, PyTorch and machine."""
+    try:
+        with open(NATIVE_STAMP) as f:
+            return f.read() == _built_for()
+    except OSError:
+        return False
+
+
 def _stale(path: str) -> bool:
-    if not os.path.exists(path):
+    if not os.path.exists(path) or (path == NATIVE_PATH and not native_current()):
         return True
     t = os.path.getmtime(path)
     sources = ([NATIVE_SOURCE] if path == NATIVE_PATH
@@ -93,27 +112,37 @@ def build_library(force: bool = False, verbose: bool = False, checked: bool = Fa
 def build_all(force: bool = False) -> tuple:
     """Build the release and the checked library and the native calls at the same time."""
     jobs = []
+
+    def start(path, tmp, cmd):
+        jobs.append((path, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT, text=True)))
+
     for checked in (False, True):
         path = CHECKED_LIB_PATH if checked else LIB_PATH
         if force or _stale(path):
             tmp = path + f".tmp{os.getpid()}"
-            jobs.append((path, tmp, subprocess.Popen(_command(tmp, checked, False),
-                                                     stdout=subprocess.PIPE,
-                                                     stderr=subprocess.STDOUT, text=True)))
-    if force or _stale(NATIVE_PATH):
-        tmp = NATIVE_PATH + f".tmp{os.getpid()}"
-        jobs.append((NATIVE_PATH, tmp, subprocess.Popen(_native_command(tmp),
-                                                        stdout=subprocess.PIPE,
-                                                        stderr=subprocess.STDOUT, text=True)))
+            start(path, tmp, _command(tmp, checked, False))
+    native = os.path.basename(NATIVE_PATH)
+    try:
+        if force or _stale(NATIVE_PATH):
+            tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+            start(NATIVE_PATH, tmp, _native_command(tmp))
+    except (OSError, ImportError, AttributeError) as e:  # no g++, or no PyTorch to build against
+        warnings.warn(f"{native} was not built: {e!r}")
     errors = []
     for path, tmp, proc in jobs:
         out, _ = proc.communicate()
-        if proc.returncode == 0:
-            os.replace(tmp, path)
-        elif path == NATIVE_PATH:
-            warnings.warn(f"{os.path.basename(path)} was not built:\n{out}")
-        else:
+        if proc.returncode != 0 and path == NATIVE_PATH:
+            warnings.warn(f"{native} was not built:\n{out}")
+        elif proc.returncode != 0:
             errors.append(f"{os.path.basename(path)}:\n{out}")
+        elif path == NATIVE_PATH:
+            with open(NATIVE_STAMP, "w") as f:  # (empty while the file is another's)
+                f.flush()
+                os.replace(tmp, path)
+                f.write(_built_for())
+        else:
+            os.replace(tmp, path)
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     return LIB_PATH, CHECKED_LIB_PATH
