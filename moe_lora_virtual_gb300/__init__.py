@@ -208,11 +208,13 @@ def mol_virtual_topk(topk_ids: torch.Tensor, lora_ids: torch.Tensor, num_experts
     _need(topk_ids, torch.int32, "topk_ids")
     _need(lora_ids, torch.int32, "lora_ids")
     T, k = topk_ids.shape
-    if vtopk_ids is None:
-        vtopk_ids = torch.empty_like(topk_ids)
+    with _on(stream, topk_ids.device):
+        if vtopk_ids is None:
+            vtopk_ids = torch.empty_like(topk_ids)
+        topk_ids, lora_ids = topk_ids.contiguous(), lora_ids.contiguous()
     _check("mol_virtual_topk", library().mol_virtual_topk(
-        _ptr(topk_ids.contiguous()), _ptr(lora_ids.contiguous()), T, k, num_experts, max_loras,
-        _ptr(vtopk_ids), _stream(stream)))
+        _ptr(topk_ids), _ptr(lora_ids), T, k, num_experts, max_loras, _ptr(vtopk_ids),
+        _stream(stream)))
     return vtopk_ids
 
 
@@ -220,13 +222,14 @@ def mol_align_block_size(vtopk_ids: torch.Tensor, num_vexperts: int, block_m: in
                          routing: Optional[Routing] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> Routing:
     _need(vtopk_ids, torch.int32, "vtopk_ids")
-    v = vtopk_ids.reshape(-1)
-    numel = v.numel()
-    if routing is None:
-        routing = alloc_routing(numel, num_vexperts, block_m, v.device)
-        routing = routing._replace(vtopk_ids=v)
-    if workspace is None:
-        workspace = alloc_workspace(numel, num_vexperts, block_m, v.device)
+    with _on(stream, vtopk_ids.device):
+        v = vtopk_ids.reshape(-1)
+        numel = v.numel()
+        if routing is None:
+            routing = alloc_routing(numel, num_vexperts, block_m, v.device)
+            routing = routing._replace(vtopk_ids=v)
+        if workspace is None:
+            workspace = alloc_workspace(numel, num_vexperts, block_m, v.device)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("mol_align_block_size", library().mol_align_block_size(
         _ptr(v), numel, num_vexperts, block_m, _ptr(routing.sorted_token_ids), routing.capacity,
@@ -243,10 +246,11 @@ def mol_align_block_size_noalloc(vtopk_ids: torch.Tensor, num_vexperts: int, blo
     overlap on the GPU share the scratch and must be serialised by the caller.
     """
     _need(vtopk_ids, torch.int32, "vtopk_ids")
-    v = vtopk_ids.reshape(-1)
-    numel = v.numel()
-    if routing is None:
-        routing = alloc_routing(numel, num_vexperts, block_m, v.device)._replace(vtopk_ids=v)
+    with _on(stream, vtopk_ids.device):
+        v = vtopk_ids.reshape(-1)
+        numel = v.numel()
+        if routing is None:
+            routing = alloc_routing(numel, num_vexperts, block_m, v.device)._replace(vtopk_ids=v)
     _check("mol_align_block_size_noalloc", library().mol_align_block_size_noalloc(
         _ptr(v), numel, num_vexperts, block_m, _ptr(routing.sorted_token_ids), routing.capacity,
         _ptr(routing.expert_ids), _ptr(routing.num_tokens_post_padded), _stream(stream)))
@@ -268,7 +272,8 @@ def mol_lora_shrink(x: torch.Tensor, x_row_div: int, lora_a: torch.Tensor, num_s
     _need(lora_a, torch.bfloat16, "lora_a")
     V, R, K = lora_a.shape
     if inter is None:
-        inter = torch.empty(routing.numel, R, dtype=torch.float32, device=x.device)
+        with _on(stream, x.device):
+            inter = torch.empty(routing.numel, R, dtype=torch.float32, device=x.device)
     _need(inter, torch.float32, "inter")
     _check("mol_lora_shrink", library().mol_lora_shrink(
         _ptr(x), _row_stride(x, "x"), x_row_div, K, _ptr(lora_a), num_slices, R // num_slices,
@@ -344,7 +349,8 @@ def mol_token_lora_ids(weight_indices: torch.Tensor, seg_indptr: torch.Tensor, n
     if seg_indptr.numel() != num_reqs + 1:
         raise ValueError("seg_indptr: expected num_reqs + 1 entries")
     if lora_ids is None:
-        lora_ids = torch.empty(num_tokens, dtype=torch.int32, device=weight_indices.device)
+        with _on(stream, weight_indices.device):
+            lora_ids = torch.empty(num_tokens, dtype=torch.int32, device=weight_indices.device)
     _need(lora_ids, torch.int32, "lora_ids")
     _check("mol_token_lora_ids", library().mol_token_lora_ids(
         _ptr(weight_indices), _ptr(seg_indptr), num_reqs, num_tokens, max_loras, _ptr(lora_ranks),

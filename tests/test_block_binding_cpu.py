@@ -41,7 +41,8 @@ def binding(monkeypatch):
         def __getattr__(self, name):
             def call(*args):
                 seen.calls.append((name, args))
-                return 4096 if name == "mol_moe_workspace_bytes" else 0
+                return {"mol_moe_workspace_bytes": 4096, "mol_workspace_bytes": 4096,
+                        "mol_align_capacity": 64}.get(name, 0)
             return call
 
     @contextlib.contextmanager
@@ -179,3 +180,23 @@ def test_operands_on_another_device_are_refused(binding, stream, monkeypatch):
                 call(*operands)
             del t.on
             assert not [c for c in binding.calls if c[0] != "mol_moe_workspace_bytes"]
+
+
+def test_calls_of_the_lora_path_allocate_on_their_stream(binding, monkeypatch):
+    """The routing buffers, the align's workspace, copies that make ids contiguous: as above."""
+    side = Stream(0x1230)
+    real = torch.Tensor.contiguous
+    copies = []
+    monkeypatch.setattr(Cuda, "contiguous", lambda self: copies.append(binding.at) or real(self))
+    monkeypatch.setattr(torch, "empty_like", lambda t: torch.empty(t.shape, dtype=t.dtype))
+    ids, lora = cuda(5, 4, dtype=i32)[:, :2], cuda(5, dtype=i32)
+    vid = mol.mol_virtual_topk(ids, lora, 8, 4, stream=side)
+    assert copies == [side, side] and [at for at, _ in binding.made] == [side]
+    for align in (mol.mol_align_block_size, mol.mol_align_block_size_noalloc):
+        binding.made.clear()
+        routing = align(vid, 32, 16, stream=side)
+        assert len(binding.made) >= 3 and all(at is side for at, _ in binding.made)
+    binding.made.clear()
+    mol.mol_lora_shrink(cuda(5, 64), 2, cuda(32, 8, 64), 1, routing, stream=side)
+    mol.mol_token_lora_ids(cuda(2, dtype=i32), cuda(3, dtype=i32), 5, 4, stream=side)
+    assert [at for at, _ in binding.made] == [side, side] and binding.at is None
