@@ -89,6 +89,8 @@ def w4_pack(q: torch.Tensor, scales: torch.Tensor, group: int) -> W4:
     if scales.shape != q.shape[:-1] + (groups,):
         raise ValueError(f"scales: expected {tuple(q.shape[:-1]) + (groups,)}, "
                          f"got {tuple(scales.shape)}")
+    if q.dtype.is_floating_point or q.dtype.is_complex:
+        raise TypeError(f"q: expected integers, got {q.dtype}")
     if q.numel() and (int(q.min()) < 0 or int(q.max()) > 15):
         raise ValueError("q: expected integers 0..15")
     Kp, lead = _padded(K), q.shape[:-1]
@@ -105,8 +107,9 @@ def w4_pack(q: torch.Tensor, scales: torch.Tensor, group: int) -> W4:
 
 
 def w4_quantize(w: torch.Tensor, group: int = 128) -> W4:
-    """Rounds weight rows [..., N, K] to 4 bits: each group's largest magnitude maps to 7 (or to
-    -8 where a negative value is the largest), its scale is rounded to bf16 first."""
+    """Rounds weight rows [..., N, K] to 4 bits, to the nearest step: a group's step, its scale, is the
+    least that keeps its values within -8 and 7 steps, then rounded to bf16 (values that this leaves
+    outside are clipped to them)."""
     if group not in GROUPS:
         raise ValueError(f"group: expected one of {GROUPS}, got {group}")
     K = w.shape[-1]

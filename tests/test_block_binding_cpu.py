@@ -200,3 +200,21 @@ def test_calls_of_the_lora_path_allocate_on_their_stream(binding, monkeypatch):
     mol.mol_lora_shrink(cuda(5, 64), 2, cuda(32, 8, 64), 1, routing, stream=side)
     mol.mol_token_lora_ids(cuda(2, dtype=i32), cuda(3, dtype=i32), 5, 4, stream=side)
     assert [at for at, _ in binding.made] == [side, side] and binding.at is None
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16, torch.complex64])
+def test_pack_refuses_what_is_no_integer(dtype):
+    """3.7 would be packed as 3."""
+    with pytest.raises(TypeError):
+        mol.w4_pack(torch.full((2, 64), 3.7).to(dtype), torch.ones(2, 2), 32)
+    q = torch.full((2, 64), 3, dtype=torch.int16)
+    assert torch.equal(mol.w4_unpack(mol.w4_pack(q, torch.ones(2, 2), 32)), torch.full((2, 64), -5.0))
+
+
+@pytest.mark.parametrize("low,high,step", [(-8.0, 7.0, 1.0), (-8.5, 7.0, 1.0625), (-7.5, 7.0, 1.0), (-1.0, 14.0, 2.0)])
+def test_quantize_steps(low, high, step):
+    """The least step that keeps a group's values within -8 and 7 of them."""
+    w = torch.linspace(low, high, 64).unsqueeze(0)
+    p = mol.w4_quantize(w, 64)
+    assert p.scales[0, 0].item() == step
+    assert bool(((mol.w4_unpack(p) - w).abs() <= step / 2).all())
