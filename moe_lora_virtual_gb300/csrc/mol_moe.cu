@@ -337,10 +337,11 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   StreamArgs a = common_args(s, x, x_stride, nullptr, w, nullptr, 0, out, out_stride);
   a.N = N;
   // More tokens than 16 are entries of 16, which read the weights again, mostly from L2; up to 32 with
-  // many rows one entry (100001 rows, 2048 inputs, 32 tokens: 51 us in one, 60 in two; 2000 rows: 10.6
-  // and 7.3; 1024 inputs, 64 tokens: 60 us in four, 61 in two, 77 in one). Entries are smaller yet
-  // where their whole rows then fit (64 tokens of 8192 inputs, 20000 rows: 140 us in eight, 268 in
-  // pieces).
+  // many rows one entry (32 tokens, 2048 inputs, 100001 rows: 50 us in one, 57 in two; 2000 rows: 10.1
+  // and 7.2). Entries of 8 where 8 whole rows of tokens fit and 16 do not (24 tokens of 8192 inputs:
+  // 20000 rows 53 us against 61 in pieces, 5000 rows 20 against 33; against it, 48 tokens, 20000 rows:
+  // 107 against 85), none smaller (64 tokens of 16384 inputs, 20000 rows: 514 us in entries of 4, 267
+  // in pieces of 16).
   const int tiles = (N + 15) / 16;
   int grid = 0;
   auto fits = [&](int rows) {
@@ -352,7 +353,7 @@ cudaError_t launch_w4_linear(const void* x, int64_t x_stride, int num_tokens, in
   const int most = num_tokens <= 32 && tiles >= 4 * g_sm_count ? 32 : 16;
   bool ok = fits(std::min(num_tokens, most));
   if (ok && a.ksteps > 1) {
-    for (int rows = most; rows >= (num_tokens < 32 ? 8 : 4) && a.ksteps > 1; rows /= 2)
+    for (int rows = most; rows >= 8 && a.ksteps > 1; rows /= 2)
       if (rows < num_tokens) ok = fits(rows);
     if (!ok || a.ksteps > 1) ok = fits(std::min(num_tokens, most));
   }

@@ -154,3 +154,16 @@ def test_shared_memory_of_a_launch(plan):
             assert end <= a["smem"] <= room, line
             assert a["mode"] == LINEAR or scratch(a) <= free, line
     assert past_ring >= 4
+
+
+@needs_nvcc
+def test_the_linears_entries(plan):
+    """Long rows of many tokens: entries of 8 where their whole rows fit, else pieces of the rows of 16
+    (of up to 32 with many outputs). Entries of 4 would read the weights up to 16 times."""
+    lines = [f"linear {group} {T} {K} {N}" for group in (32, 64, 128) for T in (9, 16, 24, 33, 48, 64)
+             for K in (5000, 8192, 12000, 16384, 65536) for N in (300, 5000, 20000)]
+    for line, launches in zip(lines, plan(lines)):
+        for a in launches:
+            assert a["xrows"] >= 8, line
+            assert a["ksteps"] > 1 or a["K"] * 2 * a["xrows"] < 222 * 1024, line
+            assert a["ksteps"] == 1 or a["xrows"] >= min(16, a["tokens"]), line
