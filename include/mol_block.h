@@ -116,10 +116,12 @@ int32_t mol_moe_gate_up(const void* x, int64_t x_row_stride, const int32_t* topk
                         const void* delta, int64_t delta_row_stride, void* act, void* stream);
 
 /*
- * Second half: out[t] = sum over the slots of t, in a fixed order for given sizes, of
+ * Second half: out[t] = sum over the slots of t of
  * topk_weights[i] * (w[e] . act[i] (+ delta[i])), pairs without an expert left
  * out, in fp32, rounded to bf16 once. Every row is written (zeros for a token
- * without any expert). Deterministic.
+ * without any expert). The order of the sums, here and in mol_moe_gate_up, is fixed
+ * by the sizes and topk_ids: equal inputs give equal bits. A token's row may differ
+ * in its last bits when other tokens of the call take other experts.
  *   w        [num_experts, hidden, inter] as above (w_scales [.., hidden, Kp / group])
  *   delta    bf16 rows of `hidden` at delta + i * delta_row_stride, or NULL
  *   out      bf16 rows of `hidden` at out + t * out_row_stride
@@ -130,7 +132,10 @@ int32_t mol_moe_down(const void* act, const int32_t* topk_ids, const float* topk
                      const void* delta, int64_t delta_row_stride, void* out,
                      int64_t out_row_stride, void* stream);
 
-/* Both halves in one call; act is scratch of num_tokens * topk * inter bf16. */
+/*
+ * Both halves in one call; act is scratch of num_tokens * topk * inter bf16: the
+ * first half's values are rounded to bf16 between the halves here too.
+ */
 int32_t mol_moe_forward(const void* x, int64_t x_row_stride, const int32_t* topk_ids,
                         const float* topk_weights, int64_t num_tokens, int32_t topk,
                         int32_t num_experts, int32_t hidden, int32_t inter, const void* w_gate_up,
@@ -140,7 +145,8 @@ int32_t mol_moe_forward(const void* x, int64_t x_row_stride, const int32_t* topk
 /*
  * mol_moe_down and mol_moe_forward with a workspace, where they take one step more
  * for many pairs: the products of each pair in fp32, then their weighted sums.
- * Same contract and result (the fp32 sums are in the order of the slots then).
+ * Same contract and result (a token's pairs are added in the order of its slots
+ * then, the deltas after the products).
  *   workspace  device, >= mol_moe_workspace_bytes of the sizes, 16-byte aligned
  *              (may be NULL when that is 0); contents are scratch
  */

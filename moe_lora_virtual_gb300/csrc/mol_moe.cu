@@ -29,11 +29,15 @@ cudaError_t launch_by_group(int group, const StreamArgs& a, int mode, int grid, 
 
 // Tokens of an entry, a power of two: half as many again as the mean of an expert's pairs, so that few
 // experts need a second entry (which reads their weights again), and no more room than the tokens
-// need. From 8 on, where twice as many cost a second token tile, a tenth more than the mean suffices
-// (128 experts, 4 bits: 96 tokens 120 us at 8 and 131 at 16, 127 tokens 148 and 165; bf16: 110 tokens
-// 224 and 237, 127 tokens 273 and 243). Never more than 16: the sums of 32 or 64 tokens in registers
-// cost more than a second entry's weights, which come from L2 (8 experts, 128 tokens, top 2: bf16
-// 39.3 us at 16, 39.5 at 32, 61 at 64; 4 bits 31.5, 42 and 87).
+// need. From 8 on, where twice as many cost a second token tile, a tenth more than the mean suffices.
+// Layers of 2048 x 768 at 8 and at 16 tokens an entry, us: 128 experts, top 8, 4 bits (32): 96 tokens
+// 92 and 122, 127 tokens 113 and 126 (there 8 would be better); 4 bits (128): 110 tokens 93 and 104,
+// 127 tokens 103 and 105; bf16: 64 tokens 192 and 201, 110 tokens 205 and 199, 127 tokens 252 and 200.
+// Never more than 16: with the sums of 32 or 64 tokens in registers 8 experts, 128 tokens, top 2, took
+// 39.5 and 61 us in bf16 where 16 take 39.4 (8: 55), in 4 bits 42 and 87 where 16 take 29 (8: 32). Their
+// later entries find the weights in L2. They do not where the experts' weights are more than L2 holds,
+// as an expert's entries are dealt to different blocks: 64 bf16 experts, 128 tokens, top 8: 143 us in
+// entries of 64, 157 of 16, 146 of 8.
 int entry_tokens(int num_tokens, int pairs, int experts) {
   int n = num_tokens == 1 ? 1 : num_tokens == 2 ? 2 : 4;
   while (n < 16 && n < num_tokens &&
@@ -70,15 +74,16 @@ int stream_smem(const StreamArgs& a, int group) {
 // gate_up, linear: the token slots and the teams of a block that has `room` bytes, when the blocks
 // share `entries` entries. False when nothing fits.
 // Slots: whole rows where they fit, if need be beside rings of two chunks (16 tokens of 4096 inputs and
-// 20000 rows 19.8 us; pieces beside rings of four, which read the tokens again for each group of tiles,
-// 28.2).
+// 20000 rows 17.8 us; pieces beside rings of four, which read the tokens again for each group of tiles,
+// 27.0).
 // Teams: the warps of a team split the inputs of a tile, so more parts fill all warps where a block has
 // few tiles, and leave less to wait for at the end; against that each tile costs its warps half a
 // chunk's time, or two for each token tile where their sums are to be added, and two more with 4-bit
 // weights, whose warps then wait for one another's products. Taken is the least of that model, with
-// one more tile a warp for the end: measured, an output head of 49 tiles a block takes
-// 29.5 us with one part and 36 with four, a linear of one tile a block 5.5 us with one and 4.1 with
-// four.
+// one more tile a warp for the end: measured, an output head of 49 tiles a block takes 30.1 us with
+// one part and 37.7 with four, a linear of up to one tile a block (2048 inputs, 2432 rows) 5.8 us with
+// one, 3.9 with four, and 4.5 with the 16 that the model takes there: among equals it takes the most,
+// also more than a row has chunks.
 bool plan(StreamArgs& a, int group, int mode, int room, int entries, int grid) {
   const int inputs = group ? 256 : 64, nt = token_tiles(a.xrows);
   a.tile_rows = mode == kGateUp ? 8 : 16;
@@ -228,10 +233,11 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Stre
 
 // The split form reads each activation row once and shares all weights evenly, for a second kernel
 // and the partials' way through L2. It pays for 4-bit weights from a few pairs on, as theirs is the
-// work of the warps (128 experts of 2048 x 768, top 8, layer: 32 pairs 29.7 us against 28.8, 64 pairs
-// 44.3 against 48.9, 768 pairs 97 against 121), for bf16 where experts have many tokens (496 pairs
-// 202 us against 194, 1016 pairs 217 against 250) or the down rows are short and their stages small
-// (102 pairs of 103 experts of 2520 x 72: 27 us against 32; of 232 x 232 both 13.7).
+// work of the warps (128 experts of 2048 x 768, top 8, layer, group 128: 32 pairs 28.4 us against 27.0,
+// 64 pairs 41.0 against 46.1, 768 pairs 86 against 111), for bf16 where experts have many tokens (496
+// pairs 191 us against 190, 768 pairs 197 against 201, 1016 pairs 200 against 242) or the down rows are
+// short and their stages small (102 pairs of 103 experts of 2520 x 72: 26.6 us against 33.1; of 232 x
+// 232, which are taken in one kernel, 13.6 against 15.5).
 size_t moe_split_bytes(const MoeShape& s, int group) {
   const int pairs = s.num_tokens * s.topk;
   if (pairs <= 32) return 0;

@@ -4,7 +4,7 @@
 // Mathematics. Both halves of the experts and the linear are products w . x of weight rows with a
 // few activation rows, every weight used by the tokens of its expert only (a few), so the time is
 // that of reading the taken experts' weights once: 2 bytes (or about half a byte) for 2 n
-// operations at n tokens an expert. 4-bit weights take about 130 instructions a KB to become bf16 and
+// operations at n tokens an expert. 4-bit weights take about 170 instructions a KB to become bf16 and
 // be multiplied, which costs the warps more than HBM takes to bring them. Two streaming loops:
 //
 // - stream_kernel: gate_up, the linear, and down's split form. A block owns tiles of 16 whole weight
@@ -16,8 +16,8 @@
 //   head took 35 us instead of 29.5.) The tokens' rows come by bulk copies into slots that all warps
 //   read, from a warp of its own, once for all the block's tiles of an expert. Measured: 23 tokens of
 //   128 bf16 experts of 2048 x 768, top 8: both halves in 149 us, 6.3 TB/s, 0.92 of a copy's rate; a
-//   4-bit head of 120001 rows of 2048 inputs, 5 tokens: 29.6 us, 4.3 TB/s, where the schedulers issue
-//   in 63 % of the cycles and the tensor, ALU and load pipes share them.
+//   4-bit head of 120001 rows of 2048 inputs, 5 tokens: 30.3 us, 4.2 TB/s, where the schedulers issue
+//   in 64 % of the cycles and the tensor, ALU and load pipes share them.
 // - down_kernel: few pairs, or bf16. A block or cluster owns rows of every expert, and a stage holds a
 //   unit's weights and activation rows (bulk copies; rows of a tile are neighbours in memory). A team's
 //   first warp asks for the next stage as soon as the team is through with one; its warps have 16 rows
@@ -38,8 +38,13 @@
 //   through distributed shared memory. No atomics on results.
 // - Each block groups the (token, slot) pairs by expert itself (at most 1024 of them: match masks,
 //   counts in shared memory, one scan; 2 us, or 1 for up to 32 pairs), so the layer is two launches,
-//   three in the split form, and the later ones group the pairs and ask for their first weights while
-//   the last blocks of the one before still run.
+//   three in the split form. A block fills its SM (shared memory, registers), so one of the second
+//   launch groups the pairs and asks for its first weights as soon as the first launch's block has left
+//   its SM, while those of other SMs still run; HBM idles in between for a few microseconds.
+// - The first half's values are rounded to bf16 between the halves, in mol_moe_forward too: act is what
+//   the adapters' down stage reads, the products take bf16, and it is half the bytes. The second half
+//   sums in fp32. This rounding is the whole difference from activations in fp32: relative error 0.0023
+//   to 0.0025 instead of the 0.0017 of the output's own rounding.
 #pragma once
 
 #include <type_traits>
@@ -188,7 +193,7 @@ MOL_DEV void build_lists(const StreamArgs& a, Lists& l, char* scratch, bool weig
     return;
   }
   // Each warp ranks a contiguous run of pairs with match masks and per-warp counts; the counts are
-  // then summed over the warps, one thread to four experts.
+  // then summed over the warps, one thread to an expert (to two beyond 512 experts).
   const int rounds = (numel + kListThreads - 1) / kListThreads;
   const int used = (numel + rounds * 32 - 1) / (rounds * 32);  // warps that hold pairs
   int* ids = reinterpret_cast<int*>(scratch);
@@ -335,7 +340,9 @@ MOL_DEV void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two nibbles at bits 0 and 16 -> bf16 pair q - 8, exact: (v & mask) | 128 as one instruction (the
-// compiler makes two of the expression, and the ALU's rate is what 4-bit weights are bound by).
+// compiler makes two of the expression, and the ALU's rate is what 4-bit weights are bound by). The
+// constants follow from bf16's 7 bits of fraction: at 128 = 0x4300 their unit is 1, so an integer
+// below 128 put there makes 128 + q.
 MOL_DEV uint32_t w4_pair(uint32_t v) {
   uint32_t b;
   asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(b) : "r"(v), "r"(0x43004300u));
