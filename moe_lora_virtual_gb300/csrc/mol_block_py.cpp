@@ -21,8 +21,13 @@ namespace {
 
 using at::Tensor;
 
-// A tensor on the current device, which is the one that a call launches on.
-bool here(const Tensor& t) { return t.is_cuda() && t.get_device() == c10::cuda::current_device(); }
+// A tensor on the current device, which is the one that a call launches on; asked for once a call.
+thread_local int current = -1;
+bool here(const Tensor& t) {
+  if (!t.is_cuda()) return false;
+  if (current < 0) current = c10::cuda::current_device();
+  return t.get_device() == current;
+}
 
 // A plain tensor on the GPU, contiguous, of the type and shape; sizes of -1 match any.
 bool fits(const Tensor& t, at::ScalarType type, c10::IntArrayRef sizes) {
@@ -111,6 +116,7 @@ PyObject* pair(const Tensor& a, PyObject* second) {
 // C++ exceptions (an allocation that fails) become the Python path's to meet again.
 template <PyObject* (*F)(Args)>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  current = -1;
   try {
     return F(Args{args, n});
   } catch (const std::exception&) {
