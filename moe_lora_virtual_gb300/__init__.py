@@ -92,7 +92,7 @@ def _load(p: str) -> ctypes.CDLL:
             raise RuntimeError(f"MoL CUDA library not built ({p} missing): run "
                                "moe_lora_virtual_gb300.build.build_library() first")
         lib = ctypes.CDLL(p)
-        for name, (res, args) in (*_SIGS.items(), *BLOCK_SIGS.items()):
+        for name, (res, args) in (*_SIGS.items(), *BLOCK_SIGS.items(), *ATTN_SIGS.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -415,3 +415,8 @@ def decode_check_record(first: int, count: int) -> CheckRecord:
 from .block import (BLOCK_EXPORTS, BLOCK_SIGS, W4, mol_block_norm, mol_moe_down,  # noqa: E402
                     mol_moe_forward, mol_moe_gate_up, mol_moe_route, mol_moe_workspace_bytes,
                     mol_w4_linear, w4_pack, w4_quantize, w4_unpack)
+
+# The attention half of a layer (include/mol_attn.h).
+from .attention import (ATTN_EXPORTS, ATTN_SIGS, Rope, mol_cache_append,  # noqa: E402
+                        mol_paged_attention, mol_paged_attention_workspace_bytes, mol_rope,
+                        rope_frequencies)

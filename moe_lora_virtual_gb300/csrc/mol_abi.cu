@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "mol.h"
+#include "mol_attend.h"
 #include "mol_internal.h"
 
 
@@ -36,8 +37,9 @@ bool valid_block_m(int32_t bm) { return bm == 16 || bm == 32 || bm == 64 || bm =
 // Read without the lock on every call; written under it once per device.
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_state[kMaxDevices] = {};
-// Per device: 1 once the experts' kernels are prepared as well.
+// Per device: 1 once the experts' kernels, the attention's, are prepared as well.
 std::atomic<int> g_moe_state[kMaxDevices] = {};
+std::atomic<int> g_attn_state[kMaxDevices] = {};
 std::mutex g_device_mutex;
 
 }  // namespace
@@ -67,24 +69,25 @@ int32_t mol::ensure_device() {
   return g_device_state[dev].load(std::memory_order_relaxed) == 1 ? MOL_OK : MOL_ERR_UNSUPPORTED;
 }
 
-// ensure_device, and the kernels of the experts and the 4-bit linear prepared, which ask for nearly
-// all of an SM's shared memory: where they cannot be had, these calls alone are refused.
-int32_t mol::ensure_moe_device() {
+// ensure_device, and kernels prepared that ask for nearly all of an SM's shared memory (the experts and
+// the 4-bit linear, the attention): where they cannot be had, these calls alone are refused.
+static int32_t ensure_prepared(std::atomic<int> (&state)[kMaxDevices], cudaError_t (*prepare)()) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (dev >= 0 && dev < kMaxDevices && g_moe_state[dev].load(std::memory_order_acquire) == 1)
-    return MOL_OK;
+  if (dev >= 0 && dev < kMaxDevices && state[dev].load(std::memory_order_acquire) == 1) return MOL_OK;
   const int32_t st = ensure_device();
   if (st != MOL_OK) return st;
   std::lock_guard<std::mutex> lock(g_device_mutex);
-  if (g_moe_state[dev].load(std::memory_order_relaxed) == 0) {
-    e = mol::prepare_moe_kernels();
+  if (state[dev].load(std::memory_order_relaxed) == 0) {
+    e = prepare();
     if (e != cudaSuccess) return cuda_fail(e);
-    g_moe_state[dev].store(1, std::memory_order_release);
+    state[dev].store(1, std::memory_order_release);
   }
   return MOL_OK;
 }
+int32_t mol::ensure_moe_device() { return ensure_prepared(g_moe_state, mol::prepare_moe_kernels); }
+int32_t mol::ensure_attn_device() { return ensure_prepared(g_attn_state, mol::prepare_attn_kernels); }
 
 namespace {
 
@@ -237,11 +240,11 @@ int32_t mol_take_check_record(uint64_t* first, uint64_t* count) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
   // in the path's order: align, item shrink and expands, tcgen05 shrink, fused stage,
-  // tcgen05 expand, norm and router, experts and 4-bit linear
-  cudaError_t (*const take[7])(unsigned long long*, unsigned long long*) = {
+  // tcgen05 expand, norm and router, experts and 4-bit linear, attention
+  cudaError_t (*const take[8])(unsigned long long*, unsigned long long*) = {
       mol::take_align_checks, mol::take_lora_checks,      mol::take_tc_checks,
       mol::take_stage_checks, mol::take_expand_tc_checks, mol::take_block_checks,
-      mol::take_moe_checks};
+      mol::take_moe_checks,   mol::take_attn_checks};
   unsigned long long f = 0, n = 0;
   for (auto fn : take) {
     unsigned long long fi = 0, ni = 0;

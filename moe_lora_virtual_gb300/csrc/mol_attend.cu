@@ -1,0 +1,581 @@
+// Attention of few new tokens over the paged cache (include/mol_attn.h).
+
+#include <algorithm>
+
+#include "mol_attend.cuh"
+#include "mol_internal.h"
+
+namespace mol {
+namespace {
+
+using attn::Block;
+using attn::Parts;
+using attn::Place;
+using attn::Record;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;             // tokens a warp takes at a time
+constexpr int kTile = kWarps * kStep;
+
+MOL_DEV void ldsm4(const void* p, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p))
+               : "memory");
+}
+MOL_DEV void ldsm4_t(const void* p, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p))
+               : "memory");
+}
+// A NaN or an infinity among the two bf16 values.
+MOL_DEV bool not_finite(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+template <int D, int MT>
+struct Geo {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kStages = D == 64 ? 6 : 3;
+  static constexpr int kTileBytes = kStep * D * 2;       // keys, or values, of a step
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  // queries while a block runs, then its sums
+  static constexpr int kShared = kRows * D * 4;
+  static constexpr size_t kSmem = (size_t)kRing + kShared;
+  static constexpr int kPerSM = kSmem <= 113 * 1024 ? 2 : 1;
+  static constexpr bool kQueriesInRegisters = MT * D <= 128;
+};
+
+// The places of one warp's walk over its thread block's run of tiles.
+template <int ROWS>
+struct Walk {
+  Block k;
+  int v, h, tile;
+  int64_t left;  // tiles of the run from here on
+  MOL_DEV void start(const AttnArgs& a, const Place& p, int64_t n) {
+    v = p.v;
+    h = p.h;
+    tile = p.tile;
+    left = n;
+    k = attn::block_of(a, v, attn::block_seq(a, v, ROWS), ROWS, kTile);
+  }
+  // On to the next tile; true where that is another block's or head's.
+  MOL_DEV bool next(const AttnArgs& a, int nv) {
+    if (--left <= 0) return true;
+    if (++tile < k.tiles) return false;
+    tile = 0;
+    if (++h < a.kv_heads) return true;
+    h = 0;
+    int b = k.b;
+    do {
+      if (++v >= nv) {
+        left = 0;
+        return true;
+      }
+      while (b + 1 < a.num_seqs && attn::first_block(a, b + 1, ROWS) <= v) ++b;
+      k = attn::block_of(a, v, b, ROWS, kTile);
+    } while (k.tiles == 0);
+    return true;
+  }
+};
+
+// Few rows (new tokens x group) against long runs of keys: the cache is read once, and that is what
+// bounds it. All tiles of 64 tokens of the launch, over sequences, heads and row blocks, are one list
+// dealt in even runs to thread blocks, so sequences of any lengths fill the GPU alike; a block whose
+// tiles fall to several leaves parts that launch_join adds in order. In a tile each warp has 16
+// tokens of its own, with a cp.async ring of its own that runs on across the blocks' borders (keys and
+// values asked for two steps ahead, no barrier between warps), its own maximum, sum and fp32
+// accumulators; the warps meet where a block ends. Scores: mma.sync with the rows as the 16-row side.
+// Tokens that lie on no page, or past the sequence, are zero in shared memory, whatever memory
+// holds; where a row does not see a token that another one sees, the step's values are looked
+// through, and summed without the tensor cores should one not be finite (0 * NaN is NaN there).
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kernel(AttnArgs a) {
+  using G = Geo<D, MT>;
+  constexpr int kChunks = D / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int s_scan[kWarps + 1];
+  __shared__ Place s_place;
+  __shared__ uint32_t s_held[kWarps][G::kStages];
+  __shared__ float2 s_top[kWarps][G::kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* ring = smem + warp * (G::kStages * G::kStageBytes);
+  unsigned char* shared = smem + G::kRing;
+  float* sums = reinterpret_cast<float*>(shared);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const Parts parts = attn::parts(a.workspace, gridDim.x, G::kRows, D);
+  const int64_t total =
+      attn::count_tiles<kThreads>(a, G::kRows, kTile, s_scan) * a.kv_heads;
+  const int64_t grid = min((int64_t)gridDim.x, total);
+  const int64_t c = blockIdx.x;
+  if (c >= grid) {
+    if (tid == 0) parts.records[c].last = -1;
+    return;
+  }
+  const int64_t from = c * total / grid, to = (c + 1) * total / grid;
+  attn::find_tile<kThreads>(a, G::kRows, kTile, from, s_scan, &s_place);
+  const Place place = s_place;
+  const int nv = attn::num_blocks(a, G::kRows);
+
+  Walk<G::kRows> load, work;
+  load.start(a, place, to - from);
+  work = load;
+
+  // Asks for the step at `load` into ring stage s and moves on.
+  auto fetch = [&](int s) {
+    if (load.left > 0) {
+      const int j = (load.k.t0 + load.tile) * kTile + warp * kStep + (lane & 15);
+      int64_t at = 0;
+      bool held = j >= load.k.lo && j < load.k.hi;
+      if (held) {
+        const int p = j / a.page_size;
+        const int page = __ldg(a.page_table + load.k.b * a.table_stride + p);
+        held = page >= 0 && page < a.num_pages;
+        if (held)
+          at = page * a.page_stride + (j - p * a.page_size) * a.token_stride + load.h * a.head_stride;
+      }
+      const uint32_t mask = __ballot_sync(0xffffffffu, held);
+      if (lane == 0) s_held[warp][s] = mask;
+      unsigned char* st = ring + s * G::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kStep * kChunks / 32; ++i) {
+        const int idx = i * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
+        const int64_t from_row = __shfl_sync(0xffffffffu, at, row) + ch * 8;
+        const uint32_t n = (mask >> row) & 1 ? 16u : 0u;
+        unsigned char* d = st + row * (D * 2) + ((ch ^ (row & 7)) << 4);
+        cp_async16_zfill(d, a.k + from_row, n);
+        cp_async16_zfill(d + G::kTileBytes, a.v + from_row, n);
+      }
+      load.next(a, nv);
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int s = 0; s < G::kStages - 1; ++s) fetch(s);
+
+  const int g = lane >> 2, t4 = lane & 3;
+  int stage = 0;
+  bool begun = place.tile == 0;  // the block at hand was begun here
+  Record record = {-1, 0, 0, 0};
+  while (work.left > 0) {
+    // ------------------------------------------------------------ a block of rows and a head
+    const Block k = work.k;
+    const int h = work.h;
+    for (int i = tid; i < G::kRows * kChunks; i += kThreads) {
+      const int row = i / kChunks, ch = i % kChunks;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (row < k.nrows) {
+        const int r = k.row0 + row, token = r / a.group;
+        q = __ldg(reinterpret_cast<const uint4*>(
+            a.q + (int64_t)(k.s.start + token) * a.q_token_stride +
+            (int64_t)(h * a.group + r - token * a.group) * a.q_head_stride + ch * 8));
+      }
+      *reinterpret_cast<uint4*>(shared + row * (D * 2) + ((ch ^ (row & 7)) << 4)) = q;
+    }
+    __syncthreads();
+    auto load_q = [&](int mt, int kk, uint32_t (&r)[4]) {
+      const int row = mt * 16 + (lane & 15), ch = 2 * kk + (lane >> 4);
+      ldsm4(shared + row * (D * 2) + ((ch ^ (row & 7)) << 4), r);
+    };
+    uint32_t qf[G::kQueriesInRegisters ? MT : 1][G::kQueriesInRegisters ? D / 16 : 1][4];
+    if constexpr (G::kQueriesInRegisters) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) load_q(mt, kk, qf[mt][kk]);
+    }
+    // the positions of this lane's rows; of the block's first and last row
+    int pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        pos[mt][i] = k.s.kv - k.s.n + (k.row0 + min(mt * 16 + g + 8 * i, k.nrows - 1)) / a.group;
+    const int pos_first = k.s.kv - k.s.n + k.row0 / a.group;
+    const int pos_last = k.s.kv - k.s.n + (k.row0 + k.nrows - 1) / a.group;
+
+    float o[MT][D / 8][4];
+    float top[MT][2], sum[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      top[mt][0] = top[mt][1] = -INFINITY;
+      sum[mt][0] = sum[mt][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    }
+    bool ends;
+    int tiles_done;
+    do {
+      cp_async_wait_group<G::kStages - 2>();
+      __syncwarp();  // the step has landed, and the stage before it is free, for every lane
+      fetch(stage == 0 ? G::kStages - 1 : stage - 1);
+      const unsigned char* kt = ring + stage * G::kStageBytes;
+      const unsigned char* vt = kt + G::kTileBytes;
+      const uint32_t mask = s_held[warp][stage];
+      const int j0 = (k.t0 + work.tile) * kTile + warp * kStep;
+      if ((mask & 0xffffu) != 0) {
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t b[4];
+          const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * kk + ((lane >> 3) & 1);
+          ldsm4(kt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t q[4];
+            if constexpr (G::kQueriesInRegisters) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) q[i] = qf[mt][kk][i];
+            } else {
+              load_q(mt, kk, q);
+            }
+            mma_16816(s[mt][0], q[0], q[1], q[2], q[3], b[0], b[1]);
+            mma_16816(s[mt][1], q[0], q[1], q[2], q[3], b[2], b[3]);
+          }
+        }
+        // every row sees every token of the step, or not
+        const bool edge = (mask & 0xffffu) != 0xffffu || j0 + kStep - 1 > pos_first ||
+                          (a.window > 0 && j0 <= pos_last - a.window);
+        auto sees = [&](int j, int p) {
+          return ((mask >> (j - j0)) & 1) && j <= p && (a.window == 0 || j > p - a.window);
+        };
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[mt][n][e] *= a.scale_log2;
+              if (edge && !sees(j0 + n * 8 + 2 * t4 + (e & 1), pos[mt][e >> 1])) s[mt][n][e] = -INFINITY;
+            }
+        uint32_t p[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]),
+                            fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const float was = top[mt][i];
+            if (__any_sync(0xffffffffu, m > was)) {
+              const float now = fmaxf(was, m);
+              const float f = was == now ? 1.f : exp2f(was - now);  // (-inf before the first)
+              top[mt][i] = now;
+              sum[mt][i] *= f;
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                o[mt][n][2 * i] *= f;
+                o[mt][n][2 * i + 1] *= f;
+              }
+            }
+            // a row that has seen nothing yet keeps weights of 0: exp2(-inf)
+            const float base = top[mt][i] == -INFINITY ? 0.f : top[mt][i];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float w = exp2f(s[mt][n][2 * i + e] - base);
+                s[mt][n][2 * i + e] = w;
+                sum[mt][i] += w;
+              }
+          }
+          p[mt][0] = pack_bf16x2(s[mt][0][0], s[mt][0][1]);
+          p[mt][1] = pack_bf16x2(s[mt][0][2], s[mt][0][3]);
+          p[mt][2] = pack_bf16x2(s[mt][1][0], s[mt][1][1]);
+          p[mt][3] = pack_bf16x2(s[mt][1][2], s[mt][1][3]);
+        }
+        bool plain = false;
+        if (edge) {
+          bool bad = false;
+          for (int i = lane; i < kStep * kChunks; i += 32) {
+            const uint4 w = lds16(vt + i * 16);
+            bad |= not_finite(w.x) || not_finite(w.y) || not_finite(w.z) || not_finite(w.w);
+          }
+          plain = __any_sync(0xffffffffu, bad);
+        }
+        if (!plain) {
+#pragma unroll
+          for (int n2 = 0; n2 < D / 16; ++n2) {
+            uint32_t b[4];
+            const int row = lane & 15, ch = 2 * n2 + (lane >> 4);
+            ldsm4_t(vt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_16816(o[mt][2 * n2], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b[0], b[1]);
+              mma_16816(o[mt][2 * n2 + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kStep; ++i) {
+            const int j = j0 + i, from_lane = (lane & ~3) | ((i & 7) >> 1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              float w[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t pair = i < 8 ? p[mt][r] : p[mt][2 + r];
+                const uint32_t got = __shfl_sync(0xffffffffu, pair, from_lane);
+                w[r] = i & 1 ? bf16_hi(got) : bf16_lo(got);
+              }
+              const bool see[2] = {sees(j, pos[mt][0]), sees(j, pos[mt][1])};
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + i * (D * 2) +
+                                                                      ((n ^ (i & 7)) << 4) + 4 * t4);
+                const float v0 = bf16_lo(v), v1 = bf16_hi(v);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  if (see[r]) {
+                    o[mt][n][2 * r] += w[r] * v0;
+                    o[mt][n][2 * r + 1] += w[r] * v1;
+                  }
+              }
+            }
+          }
+        }
+      }
+      tiles_done = work.tile + 1;
+      ends = work.next(a, nv);
+      stage = stage + 1 == G::kStages ? 0 : stage + 1;
+    } while (!ends);
+
+    // ------------------------------------------------------------ the warps' sums become one
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = sum[mt][i];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (t4 == 0) s_top[warp][mt * 16 + g + 8 * i] = make_float2(top[mt][i], l);
+      }
+    __syncthreads();  // (and every warp has read its queries)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][mt * 16 + g + 8 * i].x);
+        const float f = top[mt][i] == -INFINITY ? 0.f : exp2f(top[mt][i] - m);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          // (a warp that saw nothing has sums of 0)
+          o[mt][n][2 * i] *= f;
+          o[mt][n][2 * i + 1] *= f;
+        }
+      }
+    // in each phase the warps have different quarters of the columns; a quarter's order is fixed
+#pragma unroll 1
+    for (int phase = 0; phase < kWarps; ++phase) {
+#pragma unroll
+      for (int part = 0; part < kWarps; ++part) {
+        // (a value that the compiler does not follow: it would index the registers with it)
+        int mine = (warp + phase) & (kWarps - 1);
+        asm volatile("" : "+r"(mine));
+        if (part == mine) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < D / 8 / kWarps; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int col = part * (D / 8 / kWarps) + n;
+                float2* d = reinterpret_cast<float2*>(sums + (mt * 16 + g + 8 * i) * D + col * 8 + 2 * t4);
+                float2 x = make_float2(o[mt][col][2 * i], o[mt][col][2 * i + 1]);
+                if (phase > 0) {
+                  x.x += d->x;
+                  x.y += d->y;
+                }
+                *d = x;
+              }
+        }
+      }
+      __syncthreads();
+    }
+    // ------------------------------------------------------------ the rows, or a part of them
+    const bool whole = tiles_done >= k.tiles;
+    const bool part = !begun || !whole;
+    const int slot = (int)(2 * c) + (begun ? 1 : 0);
+    if (begun && !whole && tid == 0) {
+      record.b = k.b;
+      record.row0 = k.row0;
+      record.h = h;
+      const int64_t end = to + (k.tiles - tiles_done);  // the run ends here, the block there
+      record.last = (int)((end * grid + total - 1) / total) - 1;
+    }
+    for (int i = tid; i < k.nrows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), col = i % (D / 4) * 4;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][row].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = s_top[w][row];
+        l += x.x == -INFINITY ? 0.f : x.y * exp2f(x.x - m);
+      }
+      const float4 x = *reinterpret_cast<const float4*>(sums + row * D + col);
+      if (part) {
+        *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
+        if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
+      } else {
+        const int r = k.row0 + row, token = r / a.group;
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
+                                  (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
+                                  col) =
+            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+      }
+    }
+    begun = true;
+    __syncthreads();
+  }
+  cp_async_wait_all();
+  if (tid == 0) parts.records[c] = record;
+}
+
+constexpr int kJoinWarps = 8;
+
+// A warp a share of the parts, its lanes the columns of one row; the warps' sums meet in order.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int rows, Parts p) {
+  constexpr int kPer = D / 32;  // columns a lane
+  __shared__ float s_sum[kJoinWarps][D];
+  __shared__ float s_weight[kJoinWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Record rec = p.records[c];
+  if (rec.last < 0) return;
+  const attn::Seq s = attn::sequence(a, rec.b);
+  const int nrows = min(s.n * a.group - rec.row0, rows);
+  for (int row = blockIdx.y; row < nrows; row += gridDim.y) {
+    float m = -INFINITY;
+    for (int i = c + lane; i <= rec.last; i += 32)
+      m = fmaxf(m, p.tops[(int64_t)(2 * i + (i == c)) * rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float x[kPer], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+#pragma unroll 4
+    for (int i = c + warp; i <= rec.last; i += kJoinWarps) {
+      const int64_t at = (int64_t)(2 * i + (i == c)) * rows + row;
+      const float2 t = p.tops[at];
+      const float f = t.x == -INFINITY ? 0.f : exp2f(t.x - m);
+      l += f * t.y;
+      const float* v = p.sums + at * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const float2 w = *reinterpret_cast<const float2*>(v + e);
+        x[e] += f * w.x;
+        x[e + 1] += f * w.y;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = x[e];
+    if (lane == 0) s_weight[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(&s_sum[w][threadIdx.x * 4]);
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+        l += s_weight[w];
+      }
+      const int r = rec.row0 + row, token = r / a.group;
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(a.out + (int64_t)(s.start + token) * a.out_token_stride +
+                                (int64_t)(rec.h * a.group + r - token * a.group) * a.out_head_stride +
+                                threadIdx.x * 4) =
+          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    }
+    __syncthreads();
+  }
+}
+
+int sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 152;
+    return std::min(v, 152);
+  }();
+  return n;
+}
+
+template <int D, int MT>
+cudaError_t attend_few(const AttnArgs& a, cudaStream_t stream) {
+  using G = Geo<D, MT>;
+  const int grid = sms() * G::kPerSM;
+  const cudaError_t e = launch_pdl(attend_few_kernel<D, MT>, dim3(grid), dim3(kThreads), G::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  return attn::launch_join(a, grid, G::kRows, attn::parts(a.workspace, grid, G::kRows, D), stream);
+}
+
+template <int D, int MT>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attend_few_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Geo<D, MT>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t attn::launch_join(const AttnArgs& a, int grid, int rows, const Parts& p,
+                              cudaStream_t stream) {
+  const dim3 g(grid, std::min(rows, 16)), block(kJoinWarps * 32);
+  if (a.head_dim == 64) return launch_pdl(join_kernel<64>, g, block, 0, stream, a, rows, p);
+  if (a.head_dim == 128) return launch_pdl(join_kernel<128>, g, block, 0, stream, a, rows, p);
+  return launch_pdl(join_kernel<256>, g, block, 0, stream, a, rows, p);
+}
+
+cudaError_t prepare_attn_kernels() {
+  cudaError_t e = prepare<64, 1>();
+  if (e == cudaSuccess) e = prepare<64, 2>();
+  if (e == cudaSuccess) e = prepare<128, 1>();
+  if (e == cudaSuccess) e = prepare<128, 2>();
+  if (e == cudaSuccess) e = prepare<256, 1>();
+  return e;
+}
+
+size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
+  if (num_seqs <= 0 || num_tokens <= 0) return 0;
+  return attn::parts_bytes(304, 32, head_dim);
+}
+
+cudaError_t launch_attention(const AttnArgs& args, cudaStream_t stream) {
+  AttnArgs a = args;
+  a.min_rows = 1;
+  a.max_rows = 0x7fffffff;
+  const bool wide = (a.q_starts ? (int64_t)a.num_tokens : 1) * a.group > 16;
+  if (a.head_dim == 64) return wide ? attend_few<64, 2>(a, stream) : attend_few<64, 1>(a, stream);
+  if (a.head_dim == 128) return wide ? attend_few<128, 2>(a, stream) : attend_few<128, 1>(a, stream);
+  return attend_few<256, 1>(a, stream);
+}
+
+cudaError_t take_attn_checks(unsigned long long* first, unsigned long long* count) {
+  CheckRecord r;
+  const cudaError_t e = take_check_record_here(&r);
+  *first = r.first;
+  *count = r.count;
+  return e;
+}
+
+}  // namespace mol

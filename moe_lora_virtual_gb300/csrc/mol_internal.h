@@ -15,6 +15,8 @@ int32_t cuda_fail(cudaError_t e);
 int32_t ensure_device();
 // The same with the kernels of the experts and the 4-bit linear prepared.
 int32_t ensure_moe_device();
+// The same with the attention's kernels prepared.
+int32_t ensure_attn_device();
 
 // Geometry of the align step for given sizes (host arithmetic).
 struct AlignPlan {
