@@ -205,14 +205,15 @@ int32_t mol_take_fault_flags(uint32_t* flags) {
   if (st != MOL_OK) return st;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
-  unsigned a = 0, b = 0, c = 0, d = 0, f = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
   e = mol::take_lora_faults(&a);
   if (e == cudaSuccess) e = mol::take_tc_faults(&b);
   if (e == cudaSuccess) e = mol::take_stage_faults(&c);
   if (e == cudaSuccess) e = mol::take_expand_tc_faults(&d);
   if (e == cudaSuccess) e = mol::take_moe_faults(&f);
+  if (e == cudaSuccess) e = mol::take_attn_faults(&g);
   if (e != cudaSuccess) return cuda_fail(e);
-  *flags = a | b | c | d | f;
+  *flags = a | b | c | d | f | g;
   return MOL_OK;
 }
 

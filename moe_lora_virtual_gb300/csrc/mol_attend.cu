@@ -49,39 +49,6 @@ struct Geo {
   static constexpr bool kQueriesInRegisters = MT * D <= 128;
 };
 
-// The places of one warp's walk over its thread block's run of tiles.
-template <int ROWS>
-struct Walk {
-  Block k;
-  int v, h, tile;
-  int64_t left;  // tiles of the run from here on
-  MOL_DEV void start(const AttnArgs& a, const Place& p, int64_t n) {
-    v = p.v;
-    h = p.h;
-    tile = p.tile;
-    left = n;
-    k = attn::block_of(a, v, attn::block_seq(a, v, ROWS), ROWS, kTile);
-  }
-  // On to the next tile; true where that is another block's or head's.
-  MOL_DEV bool next(const AttnArgs& a, int nv) {
-    if (--left <= 0) return true;
-    if (++tile < k.tiles) return false;
-    tile = 0;
-    if (++h < a.kv_heads) return true;
-    h = 0;
-    int b = k.b;
-    do {
-      if (++v >= nv) {
-        left = 0;
-        return true;
-      }
-      while (b + 1 < a.num_seqs && attn::first_block(a, b + 1, ROWS) <= v) ++b;
-      k = attn::block_of(a, v, b, ROWS, kTile);
-    } while (k.tiles == 0);
-    return true;
-  }
-};
-
 // Few rows (new tokens x group) against long runs of keys: the cache is read once, and that is what
 // bounds it. All tiles of 64 tokens of the launch, over sequences, heads and row blocks, are one list
 // dealt in even runs to thread blocks, so sequences of any lengths fill the GPU alike; a block whose
@@ -122,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
   const Place place = s_place;
   const int nv = attn::num_blocks(a, G::kRows);
 
-  Walk<G::kRows> load, work;
-  load.start(a, place, to - from);
+  attn::Walk<kTile> load, work;
+  load.start(a, G::kRows, place, to - from);
   work = load;
 
   // Asks for the step at `load` into ring stage s and moves on.
@@ -510,21 +477,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
   }
 }
 
-int sms() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      v = 152;
-    return std::min(v, 152);
-  }();
-  return n;
-}
-
 template <int D, int MT>
 cudaError_t attend_few(const AttnArgs& a, cudaStream_t stream) {
   using G = Geo<D, MT>;
-  const int grid = sms() * G::kPerSM;
+  const int grid = attn::sms() * G::kPerSM;
   const cudaError_t e = launch_pdl(attend_few_kernel<D, MT>, dim3(grid), dim3(kThreads), G::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   return attn::launch_join(a, grid, G::kRows, attn::parts(a.workspace, grid, G::kRows, D), stream);
@@ -537,6 +493,17 @@ cudaError_t prepare() {
 }
 
 }  // namespace
+
+int attn::sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 152;
+    return std::min(v, 152);
+  }();
+  return n;
+}
 
 cudaError_t attn::launch_join(const AttnArgs& a, int grid, int rows, const Parts& p,
                               cudaStream_t stream) {
@@ -552,22 +519,42 @@ cudaError_t prepare_attn_kernels() {
   if (e == cudaSuccess) e = prepare<128, 1>();
   if (e == cudaSuccess) e = prepare<128, 2>();
   if (e == cudaSuccess) e = prepare<256, 1>();
+  if (e == cudaSuccess) e = attn::prepare_many();
   return e;
 }
 
+// Rows that one of attend_few's blocks holds.
+constexpr int kFewRows = 32;
+
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
   if (num_seqs <= 0 || num_tokens <= 0) return 0;
-  return attn::parts_bytes(304, 32, head_dim);
+  const size_t few = attn::parts_bytes(304, kFewRows, head_dim);
+  return num_tokens * group > kFewRows ? std::max(few, attn::many_bytes(group, head_dim)) : few;
+}
+
+static cudaError_t launch_few(const AttnArgs& a, cudaStream_t stream) {
+  const bool wide = (a.q_starts ? (int64_t)a.num_tokens : 1) * a.group > 16;
+  if (a.head_dim == 64) return wide ? attend_few<64, 2>(a, stream) : attend_few<64, 1>(a, stream);
+  if (a.head_dim == 128) return wide ? attend_few<128, 2>(a, stream) : attend_few<128, 1>(a, stream);
+  return attend_few<256, 1>(a, stream);
 }
 
 cudaError_t launch_attention(const AttnArgs& args, cudaStream_t stream) {
   AttnArgs a = args;
   a.min_rows = 1;
   a.max_rows = 0x7fffffff;
-  const bool wide = (a.q_starts ? (int64_t)a.num_tokens : 1) * a.group > 16;
-  if (a.head_dim == 64) return wide ? attend_few<64, 2>(a, stream) : attend_few<64, 1>(a, stream);
-  if (a.head_dim == 128) return wide ? attend_few<128, 2>(a, stream) : attend_few<128, 1>(a, stream);
-  return attend_few<256, 1>(a, stream);
+  const int64_t rows = (int64_t)a.num_tokens * a.group;
+  const int64_t most = a.q_starts ? rows : a.group;  // of one sequence
+  if (most <= kFewRows || a.num_pages == 0 || !attn::many_fits(a.page_size, a.head_dim)) return launch_few(a, stream);
+  // The lengths are the device's: where sequences have many rows on average all take the form for
+  // many, else each the one for its own.
+  if (!a.q_starts || rows >= 128 * (int64_t)a.num_seqs) return attn::launch_many(a, stream);
+  a.max_rows = kFewRows;
+  const cudaError_t e = launch_few(a, stream);
+  if (e != cudaSuccess) return e;
+  a.min_rows = kFewRows + 1;
+  a.max_rows = 0x7fffffff;
+  return attn::launch_many(a, stream);
 }
 
 cudaError_t take_attn_checks(unsigned long long* first, unsigned long long* count) {

@@ -115,6 +115,44 @@ MOL_DEV void find_tile(const AttnArgs& a, int rows, int tile, int64_t at, int* s
   __syncthreads();
 }
 
+// A walk over a thread block's run of tiles.
+template <int TILE>
+struct Walk {
+  Block k;
+  int rows, v, h, tile;
+  int64_t left;  // tiles of the run from here on
+  MOL_DEV void start(const AttnArgs& a, int rows_, const Place& p, int64_t n) {
+    rows = rows_;
+    v = p.v;
+    h = p.h;
+    tile = p.tile;
+    left = n;
+    k = block_of(a, v, block_seq(a, v, rows), rows, TILE);
+  }
+  // On to the next tile; true where that is another block's or head's, or none.
+  MOL_DEV bool next(const AttnArgs& a, int nv) {
+    if (--left <= 0) return true;
+    if (++tile < k.tiles) return false;
+    advance(a, nv);
+    return true;
+  }
+  // On to the first tile of the next block or head.
+  MOL_DEV void advance(const AttnArgs& a, int nv) {
+    tile = 0;
+    if (++h < a.kv_heads) return;
+    h = 0;
+    int b = k.b;
+    do {
+      if (++v >= nv) {
+        left = 0;
+        return;
+      }
+      while (b + 1 < a.num_seqs && first_block(a, b + 1, rows) <= v) ++b;
+      k = block_of(a, v, b, rows, TILE);
+    } while (k.tiles == 0);
+  }
+};
+
 // Parts of blocks that several thread blocks share. Thread block c leaves the part that continues its
 // predecessor's block in slot 2c, the one that it begins and does not end in slot 2c + 1 with a
 // record of it: {last thread block of it, sequence, first row, head}, {-1} where there is none.
@@ -143,6 +181,16 @@ __host__ __device__ inline Parts parts(void* p, int grid, int rows, int D) {
 // Joins the parts of every record: out = sum_p f_p sums_p / sum_p f_p weights_p with f_p = 2^(top_p - top),
 // in an order that the timing does not change.
 cudaError_t launch_join(const AttnArgs& a, int grid, int rows, const Parts& p, cudaStream_t stream);
+
+// The device's SMs, at most 152.
+int sms();
+
+// Many rows: sequences of at least a.min_rows rows (mol_attend_tc.cu). Whether its tiles can be loaded from
+// pages of this size, for heads of this width.
+bool many_fits(int page_size, int head_dim);
+size_t many_bytes(int group, int head_dim);
+cudaError_t prepare_many();
+cudaError_t launch_many(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace mol

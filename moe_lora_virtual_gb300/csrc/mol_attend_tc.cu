@@ -1,0 +1,649 @@
+// Attention of many new tokens over the paged cache on the fifth-generation tensor cores
+// (include/mol_attn.h).
+
+#include <algorithm>
+#include <mutex>
+
+#include "mol_attend.cuh"
+#include "mol_internal.h"
+#include "mol_tc.cuh"
+
+namespace mol {
+
+__device__ unsigned int g_many_fault_flags;
+
+namespace {
+
+using attn::Block;
+using attn::Parts;
+using attn::Place;
+using attn::Record;
+
+constexpr int kM = 128;                       // rows of a query tile, tokens of a key tile
+constexpr int kThreads = 12 * 32;              // (two warps of the last four idle)
+// Registers a thread: 384 threads are launched with 168; the last four warps give theirs up to the
+// softmax warps, 256 * 208 + 128 * 72 <= 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
+constexpr uint32_t kPolls = 1u << 22;
+constexpr int kHeldRing = 8;                  // more tiles than the loader is ever ahead
+constexpr float kLazy = 8.f;                  // log2 of how far weights may pass 1
+
+template <int D>
+struct Geo {
+  static constexpr int kHalf = kM * 128;        // bytes of 64 columns of a tile
+  static constexpr int kTileBytes = kHalf * (D / 64);
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTileBytes;
+  // tensor memory: the scores of both query tiles (their weights over the first half of each), their sums
+  static constexpr uint32_t kS = 0, kO = 2 * kM;
+  static constexpr uint32_t kCols = 512;
+};
+
+MOL_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// D += A * B with A (bf16) in tensor memory.
+MOL_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Operand whose rows are the contraction (tokens) and whose 64-column atoms lie kHalf bytes apart:
+// 8-row groups 1024 bytes apart, 128-byte swizzle.
+MOL_DEV uint64_t sw128_desc_rows(uint32_t saddr, uint32_t atom) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(atom >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+MOL_DEV void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+MOL_DEV void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+MOL_DEV uint32_t tmem_ld_x1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+  return r;
+}
+MOL_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+MOL_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+MOL_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 values at a time.
+MOL_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+MOL_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+MOL_DEV bool not_finite(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// Of a tile's columns 32 w .. 32 w + 31 those that lie in (lo, hi] on a page that is held (bit p of
+// `held`: the tile's columns p * per and on).
+MOL_DEV uint32_t columns_seen(int w, int lo, int hi, uint32_t held, int per) {
+  const int first = max(lo + 1 - 32 * w, 0), last = min(hi - 32 * w, 31);
+  if (first > 31 || last < first) return 0u;
+  uint32_t sees = (0xffffffffu << first) & (0xffffffffu >> (31 - last));
+  const int log_per = 31 - __clz(per);
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (!((held >> ((32 * w + 8 * b) >> log_per)) & 1)) sees &= ~(0xffu << (8 * b));
+  return sees;
+}
+
+// M = 128, N = 128, both operands with the contraction along their rows.
+constexpr uint32_t kScores = IDesc<kM, kM>::kValue;
+// N = D, the second operand's rows are the contraction.
+template <int D>
+constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
+
+// Two query tiles of 128 rows (new tokens x the group's heads, so the group shares each key) against
+// tiles of 128 cached tokens, the whole chain in tensor memory: scores = queries . keys^T in fp32,
+// weights in bf16 written over them, sums += weights . values. tcgen05.mma bounds it: 4 * D operations a
+// score, against one exponential; while one tile's softmax runs, the tensor cores have the other
+// tile's products.
+//   warps 0-3, 4-7  softmax of query tile 0, 1: a thread a row, 128 scores in registers, maximum and sum
+//                   without a shuffle. The maximum that weights refer to moves only when one would
+//                   pass 2^8 (bf16 and fp32 lose nothing to that), so sums are hardly ever rescaled
+//   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys)
+//   warp 9          copies the queries and, page by page, keys and values (TMA, 128-byte swizzle) into a
+//                   ring of tiles
+// Tiles are dealt as in attend_few; parts of blocks join in launch_join.
+// Pages outside the cache are zeros (the copy's fill). Where a row does not see all of a tile, its
+// scores are replaced, and the tile's values looked through: those that nobody sees are zeroed if they
+// are not finite, and if another row sees such a value, the tile's products are summed without the
+// tensor cores, for which 0 * NaN is NaN.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
+  using G = Geo<D>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t q_full, q_empty, full[G::kSlots], empty[G::kSlots], s_full[2], p_full[2], o_full[2],
+      v_seen[2];
+  __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[2][2];
+  __shared__ int s_scan[kThreads / 32 + 1];
+  __shared__ Place s_place;
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* ring = smem + 2 * G::kTileBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    for (int s = 0; s < G::kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 2);  // the products' commit, and the issuing thread for what it has seen
+      mbar_init(&p_full[t], 4);  // a warp each
+      mbar_init(&o_full[t], 1);
+      mbar_init(&v_seen[t], 4);
+      s_bad[t][0] = s_bad[t][1] = 0;
+    }
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&s_tmem, G::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int tile_rows = tile_tokens * a.group, rows = 2 * tile_rows;
+  const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
+  const int64_t total = attn::count_tiles<kThreads>(a, rows, kM, s_scan) * a.kv_heads;
+  const int64_t grid = min((int64_t)gridDim.x, total);
+  const int64_t c = blockIdx.x;
+  const bool has = c < grid;
+  const int64_t from = has ? c * total / grid : 0, to = has ? (c + 1) * total / grid : 0;
+  if (has) attn::find_tile<kThreads>(a, rows, kM, from, s_scan, &s_place);
+  const Place place = has ? s_place : Place{0, 0, 0};
+  const int nv = attn::num_blocks(a, rows);
+  bool fault = false;
+  attn::Walk<kM> w;
+  w.left = 0;
+  if (has) w.start(a, rows, place, to - from);
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == 9) {
+    // ------------------------------------------------------------ copies
+    uint32_t u = 0, n = 0, seg = 0;  // ring slots used, tiles, blocks
+    const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
+    const int copies = kM / per;
+    while (w.left > 0 && !fault) {
+      const Block& k = w.k;
+      if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
+        fault = true;
+        break;
+      }
+      const bool two = k.nrows > tile_rows;
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(tile_rows * 128 * (D / 64) * (two ? 2 : 1));
+        mbar_arrive_expect_tx(&q_full, bytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
+                        k.s.start + k.row0 / a.group + t * tile_tokens, &q_full);
+      }
+      ++seg;
+      const int h = w.h;
+      const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
+      for (int i = 0; i < count && !fault; ++i, ++n) {
+        const int j0 = (k.t0 + w.tile + i) * kM;
+        // lane p: page p of the tile
+        const int j = j0 + lane * per;
+        int page = -1;
+        if (lane < copies && j + per > k.lo && j < k.hi)
+          page = __ldg(a.page_table + k.b * a.table_stride + j / a.page_size);
+        const bool held = page >= 0 && page < a.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, held);
+        if (!held) page = a.num_pages;  // past the end: zeros
+        const int offset = j % a.page_size;
+        if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
+        for (int kv = 0; kv < 2; ++kv, ++u) {
+          const int s = (int)(u % G::kSlots);
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, kPolls))) {
+            fault = true;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)G::kTileBytes);
+          __syncwarp();
+          if (lane < copies)
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
+                          x * 64, offset, h, page, &full[s]);
+        }
+      }
+      w.left -= count;
+      if (w.left > 0) w.advance(a, nv);
+    }
+    if (fault) {  // nothing of its own left in flight
+      for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; i < u; ++i)
+        mbar_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, kPolls);
+      if (seg > 0) mbar_wait(&q_full, (seg - 1) & 1, kPolls);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      uint32_t u = 0, seg = 0, np[2] = {0, 0};
+      auto wait_slot = [&](uint32_t i) {
+        if (!mbar_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, kPolls)) fault = true;
+        tc_fence_after();
+        return !fault;
+      };
+      auto scores = [&](int t, uint32_t slot) {
+        const uint32_t q = smem_u32(smem + t * G::kTileBytes);
+        const uint32_t k = smem_u32(ring + (slot % G::kSlots) * G::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * G::kHalf + (kk % 4) * 32;
+          umma_bf16(tmem + G::kS + t * kM, sw128_desc(q + off), sw128_desc(k + off), kScores, kk != 0);
+        }
+        umma_commit(&s_full[t]);
+        mbar_arrive(&s_full[t]);
+      };
+      while (w.left > 0 && !fault) {
+        const Block& k = w.k;
+        const int tiles = k.nrows > tile_rows ? 2 : 1;
+        const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
+        ++seg;
+        if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
+          fault = true;
+          break;
+        }
+        tc_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, u);
+        umma_commit(&empty[u % G::kSlots]);
+        bool begun[2] = {false, false};
+        for (int i = 0; i < count && !fault; ++i) {
+          // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
+          const bool more = i + 1 < count;
+          for (int t = 0; t < tiles && !fault; ++t) {
+            if (t == 0 && !wait_slot(u + 1)) break;
+            if (!mbar_wait(&p_full[t], np[t] & 1, kPolls)) {
+              fault = true;
+              break;
+            }
+            ++np[t];
+            tc_fence_after();
+            if (!*(volatile uint32_t*)&s_skip[t]) {
+              const uint32_t v = smem_u32(ring + ((u + 1) % G::kSlots) * G::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < kM / 16; ++kk)
+                umma_bf16_ts(tmem + G::kO + t * D, tmem + G::kS + t * kM + kk * 8,
+                             sw128_desc_rows(v + kk * 16 * 128, G::kHalf), kValues<D>,
+                             begun[t] || kk != 0);
+            }
+            begun[t] = true;
+            if (t == tiles - 1) umma_commit(&empty[(u + 1) % G::kSlots]);
+            if (more) {
+              if (t == 0 && !wait_slot(u + 2)) break;
+              scores(t, u + 2);
+              if (t == tiles - 1) umma_commit(&empty[(u + 2) % G::kSlots]);
+            } else {
+              umma_commit(&o_full[t]);
+            }
+          }
+          if (i + 1 == count && !fault) umma_commit(&q_empty);
+          u += 2;
+        }
+        w.left -= count;
+        if (w.left > 0) w.advance(a, nv);
+      }
+      // the last products are done, and their commits have arrived
+      if (fault) umma_commit(&q_empty);
+      if (seg > 0 && !mbar_wait(&q_empty, (seg - 1) & 1, kPolls)) fault = true;
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int t = warp >> 2, quarter = warp & 3;
+    const int local = quarter * 32 + lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + G::kS + t * kM, to_ = tmem + lanes + G::kO + t * D;
+    // scores waited for, tiles, ring slots, sums waited for, tiles that were looked through
+    uint32_t ns = 0, n = 0, u = 0, no = 0, edges = 0;
+    bool begun = place.tile == 0;
+    Record record = {-1, 0, 0, 0};
+    while (w.left > 0 && !fault) {
+      const Block& k = w.k;
+      const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
+      const int in_tile = min(k.nrows - t * tile_rows, tile_rows);  // rows of this query tile
+      if (in_tile > 0) {
+        const int shift = k.s.kv - k.s.n, row = k.row0 + t * tile_rows;
+        const int pos = shift + (row + min(local, in_tile - 1)) / a.group;
+        const int pos_first = shift + row / a.group, pos_last = shift + (row + in_tile - 1) / a.group;
+        float top = -INFINITY, sum = 0.f;
+        for (int i = 0; i < count; ++i) {
+          const int j0 = (k.t0 + w.tile + i) * kM;
+          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1, kPolls))) {
+            fault = true;
+            break;
+          }
+          ++ns;
+          tc_fence_after();
+          const uint32_t held = *(volatile uint32_t*)&s_held[(n + i) % kHeldRing];
+          const int per = a.page_size < kM ? a.page_size : kM;
+          const int copies = kM / per;
+          const bool all_held = copies == 32 ? held == 0xffffffffu : held == (1u << copies) - 1;
+          const bool edge = !all_held || j0 + kM - 1 > pos_first || (a.window > 0 && j0 <= pos_last - a.window);
+          bool plain = false;
+          const int hi = pos - j0, lo = a.window > 0 ? hi - a.window : -1;  // seen: lo < column <= hi
+          if (edge) {
+            // the tile's values, once they are there
+            const uint32_t slot = u + 2 * i + 1;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(&full[slot % G::kSlots], (slot / G::kSlots) & 1, kPolls))) {
+              fault = true;
+              break;
+            }
+            unsigned char* v = ring + (slot % G::kSlots) * G::kTileBytes;
+            bool bad = false;
+            for (int x = local; x < G::kTileBytes / 16; x += kM) {
+              const int j = j0 + (x % G::kHalf >> 3) % kM;
+              const uint4 q = lds16(v + x * 16);
+              if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
+                if (j < k.lo || j >= k.hi)
+                  *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+                else
+                  bad = true;
+              }
+            }
+            fence_proxy_async_smem();
+            // the warps tell one another (two words in turn: none is two such tiles ahead)
+            if (bad) *(volatile uint32_t*)&s_bad[t][edges & 1] = n + i + 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_seen[t]);
+            if (!__all_sync(0xffffffffu, mbar_wait(&v_seen[t], edges & 1, kPolls))) {
+              fault = true;
+              break;
+            }
+            plain = *(volatile uint32_t*)&s_bad[t][edges & 1] == n + i + 1;
+            ++edges;
+          }
+          uint32_t r[kM];
+#pragma unroll
+          for (int x = 0; x < kM / 32; ++x) tmem_ld_x32(ts + x * 32, r + x * 32);
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < kM / 32; ++x) {
+              const uint32_t sees = columns_seen(x, lo, hi, held, per);
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (!((sees >> y) & 1)) r[32 * x + y] = __float_as_uint(-INFINITY);
+            }
+          }
+          float m4[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) m4[x] = __uint_as_float(r[x]);
+#pragma unroll
+          for (int x = 4; x < kM; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(r[x]));
+          const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          const bool moves = m > top + kLazy || (top == -INFINITY && m > top);
+          if (__any_sync(0xffffffffu, moves)) {
+            const float f = moves ? ex2(top - m) : 1.f;
+            if (moves) top = m;
+            sum *= f;
+            if (i > 0) {  // (the scores' commit came behind the products before them)
+#pragma unroll 1
+              for (int x = 0; x < D; x += 32) {
+                uint32_t o[32];
+                tmem_ld_x32(to_ + x, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_x32(to_ + x, o);
+              }
+            }
+          }
+          const float base = top == -INFINITY ? 0.f : top;
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2), nb = make_float2(-base, -base);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t p[kM / 2];
+#pragma unroll
+          for (int x = 0; x < kM / 2; ++x) {
+            float2 e = fma2(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])), sc, nb);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            s2[x & 1] = add2(s2[x & 1], e);
+            p[x] = pack_bf16x2(e.x, e.y);
+          }
+          sum += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+          tmem_st_x32(ts, p);
+          tmem_st_x32(ts + 32, p + 32);
+          tmem_wait_st();
+          if (plain) {
+            // the row's weights come back from tensor memory two at a time
+            const uint32_t slot = u + 2 * i + 1;
+            const unsigned char* v = ring + (slot % G::kSlots) * G::kTileBytes;
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              if (i > 0) {
+                tmem_ld_x32(to_ + x, o);
+                tmem_wait_ld();
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+              }
+#pragma unroll 1
+              for (int y = 0; y < kM; ++y) {
+                const uint32_t pair = tmem_ld_x1(ts + (y >> 1));
+                tmem_wait_ld();
+                const float wt = y & 1 ? bf16_hi(pair) : bf16_lo(pair);
+                const bool sees = (columns_seen(y >> 5, lo, hi, held, per) >> (y & 31)) & 1;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  const int ch = ((x & 63) + e) >> 3;
+                  const uint4 q = lds16(v + (x >> 6) * G::kHalf + y * 128 + ((ch ^ (y & 7)) << 4));
+                  const uint32_t q4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    const float a0 = __uint_as_float(o[e + 2 * z]), a1 = __uint_as_float(o[e + 2 * z + 1]);
+                    o[e + 2 * z] = __float_as_uint(sees ? fmaf(wt, bf16_lo(q4[z]), a0) : a0);
+                    o[e + 2 * z + 1] = __float_as_uint(sees ? fmaf(wt, bf16_hi(q4[z]), a1) : a1);
+                  }
+                }
+                __syncwarp();
+              }
+              tmem_st_x32(to_ + x, o);
+            }
+            tmem_wait_st();
+          }
+          if (quarter == 0 && lane == 0) *(volatile uint32_t*)&s_skip[t] = plain;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        if (fault || !__all_sync(0xffffffffu, mbar_wait(&o_full[t], no & 1, kPolls))) {
+          fault = true;
+          break;
+        }
+        ++no;
+        tc_fence_after();
+        // ---------------------------------------------------------- the rows, or a part of them
+        const bool whole = w.tile + count >= k.tiles;
+        const bool part = !begun || !whole;
+        const int slot = (int)(2 * c) + (begun ? 1 : 0);
+        const bool mine = local < in_tile;
+        const int at = t * tile_rows + local, r = k.row0 + at, token = r / a.group;
+        const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+        uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
+                        (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;
+        float* part_dst = parts.sums + ((int64_t)slot * rows + at) * D;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(to_ + x, o);
+          tmem_wait_ld();
+          if (mine && part) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part_dst + x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t b[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                b[z] = pack_bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + x + e) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (part && mine) parts.tops[(int64_t)slot * rows + at] = make_float2(top, sum);
+        tc_fence_before();
+      }
+      if (begun && w.tile + count < k.tiles) {
+        record.b = k.b;
+        record.row0 = k.row0;
+        record.h = w.h;
+        const int64_t end = to + (k.tiles - w.tile - count);  // the run ends here, the block there
+        record.last = (int)((end * grid + total - 1) / total) - 1;
+      }
+      begun = true;
+      n += count;
+      u += 2 * count;
+      w.left -= count;
+      if (w.left > 0) w.advance(a, nv);
+    }
+    if (tid == 0) parts.records[c] = record;
+  }
+
+  if (fault) atomicOr(&g_many_fault_flags, kFaultBulkTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, G::kCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+cudaError_t g_encode_status = cudaSuccess;
+
+// A bf16 tensor of four dimensions, copied 64 values of the innermost at a time.
+bool encode(CUtensorMap* map, const void* p, const cuuint64_t (&dims)[4], const int64_t (&strides)[3],
+            const cuuint32_t (&box)[4]) {
+  cuuint64_t bytes[3];
+  // (the stride of a dimension of one means nothing, but has to be one)
+  for (int i = 0; i < 3; ++i) bytes[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : dims[0] * 2;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, bytes, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t many(const AttnArgs& a, cudaStream_t stream) {
+  const int tokens = kM / a.group, per = std::min(a.page_size, kM);
+  CUtensorMap q, k, v;
+  const cuuint64_t page_dims[4] = {(cuuint64_t)D, (cuuint64_t)a.page_size, (cuuint64_t)a.kv_heads,
+                                   (cuuint64_t)a.num_pages};
+  const int64_t page_strides[3] = {a.token_stride, a.head_stride, a.page_stride};
+  if (!encode(&q, a.q, {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_tokens},
+              {a.q_head_stride, a.q_head_stride * a.group, a.q_token_stride},
+              {64, (cuuint32_t)a.group, 1, (cuuint32_t)tokens}) ||
+      !encode(&k, a.k, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}) ||
+      !encode(&v, a.v, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}))
+    return cudaErrorInvalidValue;
+  const int grid = attn::sms(), rows = 2 * tokens * a.group;
+  const cudaError_t e = launch_pdl(attend_many_kernel<D>, dim3(grid), dim3(kThreads), Geo<D>::kSmem, stream, q,
+                                   k, v, a, tokens);
+  if (e != cudaSuccess) return e;
+  return attn::launch_join(a, grid, rows, attn::parts(a.workspace, grid, rows, D), stream);
+}
+
+}  // namespace
+
+bool attn::many_fits(int page_size, int head_dim) {
+  const bool whole = page_size % kM == 0 || (page_size >= 8 && kM % page_size == 0);
+  return whole && (head_dim == 64 || head_dim == 128);
+}
+
+size_t attn::many_bytes(int group, int head_dim) {
+  return attn::parts_bytes(152, 2 * (kM / group) * group, head_dim);
+}
+
+cudaError_t attn::prepare_many() {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    g_encode_status = cudaGetDriverEntryPointByVersion(
+        "cuTensorMapEncodeTiled", reinterpret_cast<void**>(&g_encode), 12000, cudaEnableDefault, &q);
+    if (g_encode_status == cudaSuccess && (q != cudaDriverEntryPointSuccess || !g_encode))
+      g_encode_status = cudaErrorNotSupported;
+  });
+  if (g_encode_status != cudaSuccess) return g_encode_status;
+  const cudaError_t e = cudaFuncSetAttribute(
+      attend_many_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<64>::kSmem);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(attend_many_kernel<128>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)Geo<128>::kSmem);
+}
+
+cudaError_t attn::launch_many(const AttnArgs& a, cudaStream_t stream) {
+  return a.head_dim == 64 ? many<64>(a, stream) : many<128>(a, stream);
+}
+
+cudaError_t take_attn_faults(unsigned* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_many_fault_flags, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_many_fault_flags, &zero, sizeof(unsigned));
+}
+
+}  // namespace mol
