@@ -17,6 +17,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;             // tokens a warp takes at a time
 constexpr int kTile = kWarps * kStep;
+constexpr int kExtra = 0;             // units that a block takes beside its tiles
 
 MOL_DEV void ldsm4(const void* p, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -30,11 +31,6 @@ MOL_DEV void ldsm4_t(const void* p, uint32_t (&r)[4]) {
                : "r"(smem_u32(p))
                : "memory");
 }
-// A NaN or an infinity among the two bf16 values.
-MOL_DEV bool not_finite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-
 template <int D, int MT>
 struct Geo {
   static constexpr int kRows = 16 * MT;
@@ -76,27 +72,24 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
   pdl_wait();
   pdl_launch_dependents();
   const Parts parts = attn::parts(a.workspace, gridDim.x, G::kRows, D);
-  const int64_t total =
-      attn::count_tiles<kThreads>(a, G::kRows, kTile, s_scan) * a.kv_heads;
-  const int64_t grid = min((int64_t)gridDim.x, total);
+  const attn::Run run = attn::deal<kThreads>(a, G::kRows, kTile, kExtra, s_scan, &s_place);
   const int64_t c = blockIdx.x;
-  if (c >= grid) {
+  if (c >= run.grid) {
     if (tid == 0) parts.records[c].last = -1;
     return;
   }
-  const int64_t from = c * total / grid, to = (c + 1) * total / grid;
-  attn::find_tile<kThreads>(a, G::kRows, kTile, from, s_scan, &s_place);
-  const Place place = s_place;
   const int nv = attn::num_blocks(a, G::kRows);
 
-  attn::Walk<kTile> load, work;
-  load.start(a, G::kRows, place, to - from);
+  attn::Walk<kTile, kExtra> load, work;
+  load.start(s_place, G::kRows, run.to - run.from);
+  if (load.count == 0) load.next(a, nv);
   work = load;
+  int load_tile = 0;  // of load.count
 
   // Asks for the step at `load` into ring stage s and moves on.
   auto fetch = [&](int s) {
-    if (load.left > 0) {
-      const int j = (load.k.t0 + load.tile) * kTile + warp * kStep + (lane & 15);
+    if (load.more()) {
+      const int j = (load.k.t0 + load.first + load_tile) * kTile + warp * kStep + (lane & 15);
       int64_t at = 0;
       bool held = j >= load.k.lo && j < load.k.hi;
       if (held) {
@@ -118,7 +111,10 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
         cp_async16_zfill(d, a.k + from_row, n);
         cp_async16_zfill(d + G::kTileBytes, a.v + from_row, n);
       }
-      load.next(a, nv);
+      if (++load_tile == load.count) {
+        load.next(a, nv);
+        load_tile = 0;
+      }
     }
     cp_async_commit();
   };
@@ -127,11 +123,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 
   const int g = lane >> 2, t4 = lane & 3;
   int stage = 0;
-  bool begun = place.tile == 0;  // the block at hand was begun here
-  Record record = {-1, 0, 0, 0};
-  while (work.left > 0) {
+  Record record = {};
+  record.last = -1;
+  for (; work.more(); work.next(a, nv)) {
     // ------------------------------------------------------------ a block of rows and a head
-    const Block k = work.k;
+    const Block& k = work.k;
     const int h = work.h;
     for (int i = tid; i < G::kRows * kChunks; i += kThreads) {
       const int row = i / kChunks, ch = i % kChunks;
@@ -175,16 +171,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
-    bool ends;
-    int tiles_done;
-    do {
+    for (int tile = work.first; tile < work.first + work.count; ++tile) {
       cp_async_wait_group<G::kStages - 2>();
       __syncwarp();  // the step has landed, and the stage before it is free, for every lane
       fetch(stage == 0 ? G::kStages - 1 : stage - 1);
       const unsigned char* kt = ring + stage * G::kStageBytes;
       const unsigned char* vt = kt + G::kTileBytes;
       const uint32_t mask = s_held[warp][stage];
-      const int j0 = (k.t0 + work.tile) * kTile + warp * kStep;
+      const int j0 = (k.t0 + tile) * kTile + warp * kStep;
       if ((mask & 0xffffu) != 0) {
         float s[MT][2][4];
 #pragma unroll
@@ -265,8 +259,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
         if (edge) {
           bool bad = false;
           for (int i = lane; i < kStep * kChunks; i += 32) {
-            const uint4 w = lds16(vt + i * 16);
-            bad |= not_finite(w.x) || not_finite(w.y) || not_finite(w.z) || not_finite(w.w);
+            bad |= attn::not_finite(lds16(vt + i * 16));
           }
           plain = __any_sync(0xffffffffu, bad);
         }
@@ -312,10 +305,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
           }
         }
       }
-      tiles_done = work.tile + 1;
-      ends = work.next(a, nv);
       stage = stage + 1 == G::kStages ? 0 : stage + 1;
-    } while (!ends);
+    }
 
     // ------------------------------------------------------------ the warps' sums become one
 #pragma unroll
@@ -372,16 +363,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
       __syncthreads();
     }
     // ------------------------------------------------------------ the rows, or a part of them
-    const bool whole = tiles_done >= k.tiles;
-    const bool part = !begun || !whole;
-    const int slot = (int)(2 * c) + (begun ? 1 : 0);
-    if (begun && !whole && tid == 0) {
-      record.b = k.b;
-      record.row0 = k.row0;
-      record.h = h;
-      const int64_t end = to + (k.tiles - tiles_done);  // the run ends here, the block there
-      record.last = (int)((end * grid + total - 1) / total) - 1;
-    }
+    const bool begins = work.first == 0, part = !begins || !work.ends();
+    const int slot = (int)(2 * c) + (begins ? 1 : 0);
+    if (begins && part && tid == 0) record = {work.last(run), k.s.start, k.row0, k.nrows, h, {}};
     for (int i = tid; i < k.nrows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), col = i % (D / 4) * 4;
       float m = -INFINITY, l = 0.f;
@@ -405,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
             make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
       }
     }
-    begun = true;
     __syncthreads();
   }
   cp_async_wait_all();
@@ -414,30 +397,32 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 
 constexpr int kJoinWarps = 8;
 
-// A warp a share of the parts, its lanes the columns of one row; the warps' sums meet in order.
-template <int D>
+// WAYS warps a row, its columns over their lanes: each takes every WAYS-th part, a later warp's sum is
+// added to an earlier one's. Every part is read once; a chain of four dependent loads (record,
+// maxima, parts) is what it costs.
+template <int D, int WAYS>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int rows, Parts p) {
   constexpr int kPer = D / 32;  // columns a lane
-  __shared__ float s_sum[kJoinWarps][D];
-  __shared__ float s_weight[kJoinWarps];
+  constexpr int kRows = kJoinWarps / WAYS;
+  __shared__ float s_sum[WAYS > 1 ? kRows : 1][WAYS][D];
+  __shared__ float s_weight[kRows][WAYS];
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int local = warp / WAYS, way = warp % WAYS, row = blockIdx.y * kRows + local;
   const Record rec = p.records[c];
-  if (rec.last < 0) return;
-  const attn::Seq s = attn::sequence(a, rec.b);
-  const int nrows = min(s.n * a.group - rec.row0, rows);
-  for (int row = blockIdx.y; row < nrows; row += gridDim.y) {
-    float m = -INFINITY;
+  if (rec.last < 0 || (int)blockIdx.y * kRows >= rec.nrows) return;
+  const bool has = row < rec.nrows;
+  float x[kPer], l = 0.f, m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+  if (has) {
     for (int i = c + lane; i <= rec.last; i += 32)
       m = fmaxf(m, p.tops[(int64_t)(2 * i + (i == c)) * rows + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float x[kPer], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) x[e] = 0.f;
 #pragma unroll 4
-    for (int i = c + warp; i <= rec.last; i += kJoinWarps) {
+    for (int i = c + way; i <= rec.last; i += WAYS) {
       const int64_t at = (int64_t)(2 * i + (i == c)) * rows + row;
       const float2 t = p.tops[at];
       const float f = t.x == -INFINITY ? 0.f : exp2f(t.x - m);
@@ -450,31 +435,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
         x[e + 1] += f * w.y;
       }
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = x[e];
-    if (lane == 0) s_weight[warp] = l;
-    __syncthreads();
-    if (threadIdx.x < D / 4) {
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float4 z = *reinterpret_cast<const float4*>(&s_sum[w][threadIdx.x * 4]);
-        y.x += z.x;
-        y.y += z.y;
-        y.z += z.z;
-        y.w += z.w;
-        l += s_weight[w];
-      }
-      const int r = rec.row0 + row, token = r / a.group;
-      const float inv = m == -INFINITY ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(a.out + (int64_t)(s.start + token) * a.out_token_stride +
-                                (int64_t)(rec.h * a.group + r - token * a.group) * a.out_head_stride +
-                                threadIdx.x * 4) =
-          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-    }
-    __syncthreads();
   }
+  if constexpr (WAYS > 1) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_sum[local][way][lane * kPer + e] = x[e];
+    if (lane == 0) s_weight[local][way] = l;
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int w = 1; w < WAYS; ++w) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] += s_sum[local][w][lane * kPer + e];
+      l += s_weight[local][w];
+    }
+  }
+  if (!has) return;
+  const int r = rec.row0 + row, token = r / a.group;
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t)(rec.start + token) * a.out_token_stride +
+                                              (int64_t)(rec.h * a.group + r - token * a.group) *
+                                                  a.out_head_stride) + lane * (kPer / 2);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(x[e] * inv, x[e + 1] * inv);
 }
 
 template <int D, int MT>
@@ -507,10 +489,15 @@ int attn::sms() {
 
 cudaError_t attn::launch_join(const AttnArgs& a, int grid, int rows, const Parts& p,
                               cudaStream_t stream) {
-  const dim3 g(grid, std::min(rows, 16)), block(kJoinWarps * 32);
-  if (a.head_dim == 64) return launch_pdl(join_kernel<64>, g, block, 0, stream, a, rows, p);
-  if (a.head_dim == 128) return launch_pdl(join_kernel<128>, g, block, 0, stream, a, rows, p);
-  return launch_pdl(join_kernel<256>, g, block, 0, stream, a, rows, p);
+  // Few rows come in many parts (a sequence of 128 K tokens: 38), many rows in two or three.
+  constexpr int kWays = 4;
+  const bool few = rows <= 32;
+  const int per = few ? kJoinWarps / kWays : kJoinWarps;
+  const dim3 g(grid, (rows + per - 1) / per), block(kJoinWarps * 32);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, g, block, 0, stream, a, rows, p); };
+  if (a.head_dim == 64) return few ? go(join_kernel<64, kWays>) : go(join_kernel<64, 1>);
+  if (a.head_dim == 128) return few ? go(join_kernel<128, kWays>) : go(join_kernel<128, 1>);
+  return go(join_kernel<256, kWays>);
 }
 
 cudaError_t prepare_attn_kernels() {

@@ -7,6 +7,15 @@
 namespace mol {
 namespace attn {
 
+// A NaN or an infinity among eight bf16 values: an exponent of ones carries into the sign's place.
+MOL_DEV bool not_finite(const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c |= (w[i] & 0x7F807F80u) + 0x00800080u;
+  return (c & 0x80008000u) != 0;
+}
+
 // One sequence of the call: its first row of q, its rows, its cached tokens. Whatever the caller's
 // arrays hold, rows stay within the call's and tokens within the page table.
 struct Seq {
@@ -75,89 +84,126 @@ MOL_DEV Block block_of(const AttnArgs& a, int v, int b, int rows, int tile) {
   return k;
 }
 
-// Where a part of the tiles begins: block number, head, tile of it.
-struct Place {
-  int v, h, tile;
+// What a launch does is counted in units: a block's tiles and `extra` more for what it takes to begin
+// and to end one. All units of the launch, in the order (block, head, unit), are dealt in even runs to
+// its thread blocks.
+struct Place {  // where a thread block's run begins
+  Block k;
+  int v, h, unit;
 };
+struct Run {
+  int64_t total, grid, from, to;  // units of the launch, thread blocks that get some, this one's
+};
+MOL_DEV int block_units(const Block& k, int extra) { return k.tiles > 0 ? k.tiles + extra : 0; }
 
-// All tiles of the launch, in the order (block, head, tile), are dealt in even runs. total: tiles of
-// one head. Every thread of a thread block of THREADS calls these; `sh` holds THREADS / 32 + 1 ints.
+// Every thread of a thread block of THREADS calls it; `sh` holds THREADS / 32 + 1 ints. *place is
+// written where the run is not empty.
 template <int THREADS>
-MOL_DEV int64_t count_tiles(const AttnArgs& a, int rows, int tile, int* sh) {
+MOL_DEV Run deal(const AttnArgs& a, int rows, int tile, int extra, int* sh, Place* place) {
   const int nv = num_blocks(a, rows);
-  int64_t total = 0;
+  Run run;
+  Block k = {};
+  int before = 0, sum = 0, n = 0;
+  run.total = 0;
   for (int v0 = 0; v0 < nv; v0 += THREADS) {
     const int v = v0 + threadIdx.x;
-    const int n = v < nv ? block_of(a, v, block_seq(a, v, rows), rows, tile).tiles : 0;
-    int here;
-    block_exclusive_scan<THREADS>(n, sh, here);
-    total += here;
-  }
-  return total;
-}
-template <int THREADS>
-MOL_DEV void find_tile(const AttnArgs& a, int rows, int tile, int64_t at, int* sh, Place* out) {
-  const int nv = num_blocks(a, rows);
-  int64_t passed = 0;
-  for (int v0 = 0; v0 < nv && passed * a.kv_heads <= at; v0 += THREADS) {
-    const int v = v0 + threadIdx.x;
-    const int n = v < nv ? block_of(a, v, block_seq(a, v, rows), rows, tile).tiles : 0;
-    int total;
-    const int before = block_exclusive_scan<THREADS>(n, sh, total);
-    const int64_t first = (passed + before) * a.kv_heads;
-    if (n > 0 && at >= first && at < first + (int64_t)n * a.kv_heads) {
-      out->v = v;
-      out->h = (int)((at - first) / n);
-      out->tile = (int)((at - first) % n);
+    n = 0;
+    if (v < nv) {
+      k = block_of(a, v, block_seq(a, v, rows), rows, tile);
+      n = block_units(k, extra);
     }
-    passed += total;
+    before = block_exclusive_scan<THREADS>(n, sh, sum);
+    run.total += sum;
+  }
+  run.total *= a.kv_heads;
+  run.grid = min((int64_t)gridDim.x, run.total);
+  const int64_t c = blockIdx.x;
+  run.from = run.to = 0;
+  if (c >= run.grid) return run;
+  run.from = c * run.total / run.grid;
+  run.to = (c + 1) * run.total / run.grid;
+  int64_t passed = 0;
+  for (int v0 = 0; v0 < nv && passed * a.kv_heads <= run.from; v0 += THREADS) {
+    const int v = v0 + threadIdx.x;
+    if (nv > THREADS) {  // (else as above)
+      n = 0;
+      if (v < nv) {
+        k = block_of(a, v, block_seq(a, v, rows), rows, tile);
+        n = block_units(k, extra);
+      }
+      before = block_exclusive_scan<THREADS>(n, sh, sum);
+    }
+    const int64_t first = (passed + before) * a.kv_heads, at = run.from - first;
+    if (n > 0 && at >= 0 && at < (int64_t)n * a.kv_heads) {
+      place->k = k;
+      place->v = v;
+      place->h = (int)(at / n);
+      place->unit = (int)(at % n);
+    }
+    passed += sum;
   }
   __syncthreads();
+  return run;
 }
 
-// A walk over a thread block's run of tiles.
-template <int TILE>
+// A walk over a thread block's run, a block's head at a time.
+template <int TILE, int EXTRA>
 struct Walk {
   Block k;
-  int rows, v, h, tile;
-  int64_t left;  // tiles of the run from here on
-  MOL_DEV void start(const AttnArgs& a, int rows_, const Place& p, int64_t n) {
+  int rows, v, h;
+  int first, count;  // tiles of the block in the run
+  int unit;
+  int64_t left;      // units of the run from here on
+  MOL_DEV void start(const Place& p, int rows_, int64_t n) {
+    k = p.k;
     rows = rows_;
     v = p.v;
     h = p.h;
-    tile = p.tile;
+    unit = p.unit;
     left = n;
-    k = block_of(a, v, block_seq(a, v, rows), rows, TILE);
+    cut();
   }
-  // On to the next tile; true where that is another block's or head's, or none.
-  MOL_DEV bool next(const AttnArgs& a, int nv) {
-    if (--left <= 0) return true;
-    if (++tile < k.tiles) return false;
-    advance(a, nv);
-    return true;
+  MOL_DEV void cut() {
+    const int n = (int)min((int64_t)(k.tiles + EXTRA - unit), left);
+    first = max(unit - EXTRA, 0);
+    count = max(unit + n - EXTRA, 0) - first;
   }
-  // On to the first tile of the next block or head.
-  MOL_DEV void advance(const AttnArgs& a, int nv) {
-    tile = 0;
-    if (++h < a.kv_heads) return;
-    h = 0;
-    int b = k.b;
+  MOL_DEV bool more() const { return left > 0; }
+  MOL_DEV bool ends() const { return first + count >= k.tiles; }
+  // On to the next head or block; ones that the run has no tile of are passed by.
+  MOL_DEV void next(const AttnArgs& a, int nv) {
     do {
-      if (++v >= nv) {
-        left = 0;
-        return;
+      left -= k.tiles + EXTRA - unit;
+      if (left <= 0) return;
+      unit = 0;
+      if (++h == a.kv_heads) {
+        h = 0;
+        int b = k.b;
+        do {
+          if (++v >= nv) {
+            left = 0;
+            return;
+          }
+          while (b + 1 < a.num_seqs && first_block(a, b + 1, rows) <= v) ++b;
+          k = block_of(a, v, b, rows, TILE);
+        } while (k.tiles == 0);
       }
-      while (b + 1 < a.num_seqs && first_block(a, b + 1, rows) <= v) ++b;
-      k = block_of(a, v, b, rows, TILE);
-    } while (k.tiles == 0);
+      cut();
+    } while (count == 0);
+  }
+  // The last thread block that has a tile of this block, which the run begins and does not end.
+  MOL_DEV int last(const Run& r) const {
+    const int64_t end = r.to + (k.tiles - first - count);
+    return (int)((end * r.grid + r.total - 1) / r.total) - 1;
   }
 };
 
 // Parts of blocks that several thread blocks share. Thread block c leaves the part that continues its
 // predecessor's block in slot 2c, the one that it begins and does not end in slot 2c + 1 with a
-// record of it: {last thread block of it, sequence, first row, head}, {-1} where there is none.
+// record of it: last thread block of it (-1: there is none), the sequence's first row of q, first row
+// within it, rows, head.
 struct Record {
-  int last, b, row0, h;
+  int last, start, row0, nrows, h, pad[3];
 };
 struct Parts {
   float* sums;   // [slot][rows][D], not divided

@@ -27,6 +27,7 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kHeldRing = 8;                  // more tiles than the loader is ever ahead
+constexpr int kExtra = 2;                     // units that a block takes beside its tiles
 constexpr float kLazy = 8.f;                  // log2 of how far weights may pass 1
 
 template <int D>
@@ -121,9 +122,7 @@ MOL_DEV float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-MOL_DEV bool not_finite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
+
 
 // Of a tile's columns 32 w .. 32 w + 31 those that lie in (lo, hi] on a page that is held (bit p of
 // `held`: the tile's columns p * per and on).
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
   using G = Geo<D>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full, q_empty, full[G::kSlots], empty[G::kSlots], s_full[2], p_full[2], o_full[2],
+  __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], s_full[2], p_full[2], o_full[2],
       v_seen[2];
   __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[2][2];
   __shared__ int s_scan[kThreads / 32 + 1];
@@ -178,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
+    mbar_init(&all_done, 1);
     for (int s = 0; s < G::kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -201,18 +201,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tile_rows = tile_tokens * a.group, rows = 2 * tile_rows;
   const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
-  const int64_t total = attn::count_tiles<kThreads>(a, rows, kM, s_scan) * a.kv_heads;
-  const int64_t grid = min((int64_t)gridDim.x, total);
+  const attn::Run run = attn::deal<kThreads>(a, rows, kM, kExtra, s_scan, &s_place);
   const int64_t c = blockIdx.x;
-  const bool has = c < grid;
-  const int64_t from = has ? c * total / grid : 0, to = has ? (c + 1) * total / grid : 0;
-  if (has) attn::find_tile<kThreads>(a, rows, kM, from, s_scan, &s_place);
-  const Place place = has ? s_place : Place{0, 0, 0};
   const int nv = attn::num_blocks(a, rows);
   bool fault = false;
-  attn::Walk<kM> w;
+  attn::Walk<kM, kExtra> w;
   w.left = 0;
-  if (has) w.start(a, rows, place, to - from);
+  if (c < run.grid) {
+    w.start(s_place, rows, run.to - run.from);
+    if (w.count == 0) w.next(a, nv);
+  }
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t u = 0, n = 0, seg = 0;  // ring slots used, tiles, blocks
     const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
     const int copies = kM / per;
-    while (w.left > 0 && !fault) {
+    for (; w.more() && !fault; w.next(a, nv)) {
       const Block& k = w.k;
       if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
         fault = true;
@@ -237,10 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         k.s.start + k.row0 / a.group + t * tile_tokens, &q_full);
       }
       ++seg;
-      const int h = w.h;
-      const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
-      for (int i = 0; i < count && !fault; ++i, ++n) {
-        const int j0 = (k.t0 + w.tile + i) * kM;
+      for (int i = 0; i < w.count && !fault; ++i, ++n) {
+        const int j0 = (k.t0 + w.first + i) * kM;
         // lane p: page p of the tile
         const int j = j0 + lane * per;
         int page = -1;
@@ -262,11 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < copies)
             for (int x = 0; x < D / 64; ++x)
               tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
-                          x * 64, offset, h, page, &full[s]);
+                          x * 64, offset, w.h, page, &full[s]);
         }
       }
-      w.left -= count;
-      if (w.left > 0) w.advance(a, nv);
     }
     if (fault) {  // nothing of its own left in flight
       for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; i < u; ++i)
@@ -293,10 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&s_full[t]);
         mbar_arrive(&s_full[t]);
       };
-      while (w.left > 0 && !fault) {
-        const Block& k = w.k;
-        const int tiles = k.nrows > tile_rows ? 2 : 1;
-        const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
+      for (; w.more() && !fault; w.next(a, nv)) {
+        const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
         ++seg;
         if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
           fault = true;
@@ -305,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         for (int t = 0; t < tiles; ++t) scores(t, u);
         umma_commit(&empty[u % G::kSlots]);
+        if (count == 1) umma_commit(&q_empty);  // (with the block's last scores)
         bool begun[2] = {false, false};
         for (int i = 0; i < count && !fault; ++i) {
           // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
@@ -330,20 +323,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
               if (t == 0 && !wait_slot(u + 2)) break;
               scores(t, u + 2);
-              if (t == tiles - 1) umma_commit(&empty[(u + 2) % G::kSlots]);
+              if (t == tiles - 1) {
+                umma_commit(&empty[(u + 2) % G::kSlots]);
+                if (i + 2 == count) umma_commit(&q_empty);
+              }
             } else {
               umma_commit(&o_full[t]);
             }
           }
-          if (i + 1 == count && !fault) umma_commit(&q_empty);
           u += 2;
         }
-        w.left -= count;
-        if (w.left > 0) w.advance(a, nv);
       }
-      // the last products are done, and their commits have arrived
-      if (fault) umma_commit(&q_empty);
-      if (seg > 0 && !mbar_wait(&q_empty, (seg - 1) & 1, kPolls)) fault = true;
+      // the products are done, and their commits have arrived
+      umma_commit(&all_done);
+      if (!mbar_wait(&all_done, 0, kPolls)) fault = true;
     }
   }
   } else {
@@ -355,11 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + G::kS + t * kM, to_ = tmem + lanes + G::kO + t * D;
     // scores waited for, tiles, ring slots, sums waited for, tiles that were looked through
     uint32_t ns = 0, n = 0, u = 0, no = 0, edges = 0;
-    bool begun = place.tile == 0;
-    Record record = {-1, 0, 0, 0};
-    while (w.left > 0 && !fault) {
+    Record record = {};
+    record.last = -1;
+    for (; w.more() && !fault; w.next(a, nv)) {
       const Block& k = w.k;
-      const int count = (int)min((int64_t)(k.tiles - w.tile), w.left);
+      const int count = w.count;
+      const bool begins = w.first == 0, part = !begins || !w.ends();
       const int in_tile = min(k.nrows - t * tile_rows, tile_rows);  // rows of this query tile
       if (in_tile > 0) {
         const int shift = k.s.kv - k.s.n, row = k.row0 + t * tile_rows;
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos_first = shift + row / a.group, pos_last = shift + (row + in_tile - 1) / a.group;
         float top = -INFINITY, sum = 0.f;
         for (int i = 0; i < count; ++i) {
-          const int j0 = (k.t0 + w.tile + i) * kM;
+          const int j0 = (k.t0 + w.first + i) * kM;
           if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1, kPolls))) {
             fault = true;
             break;
@@ -391,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             unsigned char* v = ring + (slot % G::kSlots) * G::kTileBytes;
             bool bad = false;
+#pragma unroll 8
             for (int x = local; x < G::kTileBytes / 16; x += kM) {
-              const int j = j0 + (x % G::kHalf >> 3) % kM;
-              const uint4 q = lds16(v + x * 16);
-              if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
+              const int j = j0 + (x >> 3) % kM;
+              if (attn::not_finite(lds16(v + x * 16))) {
                 if (j < k.lo || j >= k.hi)
                   *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
                 else
@@ -515,9 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
         // ---------------------------------------------------------- the rows, or a part of them
-        const bool whole = w.tile + count >= k.tiles;
-        const bool part = !begun || !whole;
-        const int slot = (int)(2 * c) + (begun ? 1 : 0);
+        const int slot = (int)(2 * c) + (begins ? 1 : 0);
         const bool mine = local < in_tile;
         const int at = t * tile_rows + local, r = k.row0 + at, token = r / a.group;
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
@@ -548,18 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part && mine) parts.tops[(int64_t)slot * rows + at] = make_float2(top, sum);
         tc_fence_before();
       }
-      if (begun && w.tile + count < k.tiles) {
-        record.b = k.b;
-        record.row0 = k.row0;
-        record.h = w.h;
-        const int64_t end = to + (k.tiles - w.tile - count);  // the run ends here, the block there
-        record.last = (int)((end * grid + total - 1) / total) - 1;
-      }
-      begun = true;
+      if (begins && part) record = {w.last(run), k.s.start, k.row0, k.nrows, w.h, {}};
       n += count;
       u += 2 * count;
-      w.left -= count;
-      if (w.left > 0) w.advance(a, nv);
     }
     if (tid == 0) parts.records[c] = record;
   }
