@@ -22,8 +22,8 @@ using attn::Record;
 constexpr int kM = 128;                       // rows of a query tile, tokens of a key tile
 constexpr int kThreads = 12 * 32;              // (two warps of the last four idle)
 // Registers a thread: 384 threads are launched with 168; the last four warps give theirs up to the
-// softmax warps, 256 * 208 + 128 * 72 <= 384 * 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 72;
+// softmax warps, 256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kHeldRing = 8;                  // more tiles than the loader is ever ahead
@@ -90,6 +90,24 @@ MOL_DEV void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
       "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+MOL_DEV void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+MOL_DEV void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 MOL_DEV uint32_t tmem_ld_x1(uint32_t taddr) {
@@ -170,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[2][2];
   __shared__ int s_scan[kThreads / 32 + 1];
   __shared__ Place s_place;
+  __shared__ attn::Run s_run;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* ring = smem + 2 * G::kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -200,17 +219,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   const int tile_rows = tile_tokens * a.group, rows = 2 * tile_rows;
-  const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
-  const attn::Run run = attn::deal<kThreads>(a, rows, kM, kExtra, s_scan, &s_place);
-  const int64_t c = blockIdx.x;
-  const int nv = attn::num_blocks(a, rows);
-  bool fault = false;
-  attn::Walk<kM, kExtra> w;
-  w.left = 0;
-  if (c < run.grid) {
-    w.start(s_place, rows, run.to - run.from);
-    if (w.count == 0) w.next(a, nv);
+  {
+    const attn::Run run = attn::deal<kThreads>(a, rows, kM, kExtra, s_scan, &s_place);
+    if (tid == 0) s_run = run;
+    __syncthreads();
   }
+  bool fault = false;
+  // (each role begins its own, from shared memory: nothing of it is held in registers before)
+  auto begin = [&](attn::Walk<kM, kExtra>& w) {
+    w.left = 0;
+    if (blockIdx.x < s_run.grid) {
+      w.start(s_place, rows, s_run.to - s_run.from);
+      if (w.count == 0) w.next(a, attn::num_blocks(a, rows));
+    }
+  };
+  auto next = [&](attn::Walk<kM, kExtra>& w) { w.next(a, attn::num_blocks(a, rows)); };
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -219,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t u = 0, n = 0, seg = 0;  // ring slots used, tiles, blocks
     const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
     const int copies = kM / per;
-    for (; w.more() && !fault; w.next(a, nv)) {
+    attn::Walk<kM, kExtra> w;
+    for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
         fault = true;
@@ -287,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&s_full[t]);
         mbar_arrive(&s_full[t]);
       };
-      for (; w.more() && !fault; w.next(a, nv)) {
+      attn::Walk<kM, kExtra> w;
+    for (begin(w); w.more() && !fault; next(w)) {
         const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
         ++seg;
         if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
@@ -350,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, n = 0, u = 0, no = 0, edges = 0;
     Record record = {};
     record.last = -1;
-    for (; w.more() && !fault; w.next(a, nv)) {
+    attn::Walk<kM, kExtra> w;
+    for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       const int count = w.count;
       const bool begins = w.first == 0, part = !begins || !w.ends();
@@ -433,13 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum *= f;
             if (i > 0) {  // (the scores' commit came behind the products before them)
 #pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                tmem_ld_x32(to_ + x, o);
+              for (int x = 0; x < D; x += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(to_ + x, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st_x32(to_ + x, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_x16(to_ + x, o);
               }
             }
           }
@@ -509,12 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
         // ---------------------------------------------------------- the rows, or a part of them
-        const int slot = (int)(2 * c) + (begins ? 1 : 0);
+        const int slot = 2 * (int)blockIdx.x + (begins ? 1 : 0);
         const bool mine = local < in_tile;
         const int at = t * tile_rows + local, r = k.row0 + at, token = r / a.group;
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;
+        const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
         float* part_dst = parts.sums + ((int64_t)slot * rows + at) * D;
 #pragma unroll 1
         for (int x = 0; x < D; x += 32) {
@@ -540,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part && mine) parts.tops[(int64_t)slot * rows + at] = make_float2(top, sum);
         tc_fence_before();
       }
-      if (begins && part) record = {w.last(run), k.s.start, k.row0, k.nrows, w.h, {}};
+      if (begins && part) record = {w.last(s_run), k.s.start, k.row0, k.nrows, w.h, {}};
       n += count;
       u += 2 * count;
     }
-    if (tid == 0) parts.records[c] = record;
+    if (tid == 0) attn::parts(a.workspace, gridDim.x, rows, D).records[blockIdx.x] = record;
   }
 
   if (fault) atomicOr(&g_many_fault_flags, kFaultBulkTimeout);
