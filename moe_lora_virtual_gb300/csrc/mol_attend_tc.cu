@@ -80,6 +80,22 @@ MOL_DEV void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+// The same and the largest of the 32 (NaN aside).
+MOL_DEV void tmem_ld_max_x32(uint32_t taddr, uint32_t* r, float& m) {
+  uint32_t w;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(w)
+      : "r"(taddr)
+      : "memory");
+  m = __uint_as_float(w);  // (to be read behind the wait, like the others)
+}
 MOL_DEV void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -434,23 +450,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++edges;
           }
           uint32_t r[kM];
+          float m4[kM / 32];
 #pragma unroll
-          for (int x = 0; x < kM / 32; ++x) tmem_ld_x32(ts + x * 32, r + x * 32);
+          for (int x = 0; x < kM / 32; ++x) tmem_ld_max_x32(ts + x * 32, r + x * 32, m4[x]);
           tmem_wait_ld();
           if (edge) {
 #pragma unroll
             for (int x = 0; x < kM / 32; ++x) {
               const uint32_t sees = columns_seen(x, lo, hi, held, per);
+              m4[x] = -INFINITY;
 #pragma unroll
-              for (int y = 0; y < 32; ++y)
+              for (int y = 0; y < 32; ++y) {
                 if (!((sees >> y) & 1)) r[32 * x + y] = __float_as_uint(-INFINITY);
+                m4[x] = fmaxf(m4[x], __uint_as_float(r[32 * x + y]));
+              }
             }
           }
-          float m4[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) m4[x] = __uint_as_float(r[x]);
-#pragma unroll
-          for (int x = 4; x < kM; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(r[x]));
           const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
           const bool moves = m > top + kLazy || (top == -INFINITY && m > top);
           if (__any_sync(0xffffffffu, moves)) {
