@@ -17,7 +17,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .block import _bf16, _call, _empty, _f32, _flat, _here, _i32, _stream
+from . import block as _block
+from .block import _bf16, _call, _empty, _entry, _f32, _flat, _here, _i32, _stream
 
 import moe_lora_virtual_gb300 as _mol
 
@@ -153,6 +154,10 @@ def _like(out: Optional[torch.Tensor], x: torch.Tensor, stream, name: str) -> to
 def mol_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """x bf16 [T, heads, head_dim] with positions int32 [T] turned into it; out may be `x`."""
+    if _block._native is not None and out is None and stream is None:
+        done = _block._native.rope(_entry("mol_rope"), x, positions, rope[0], int(rope[1]), rope[2])
+        if done is not None:
+            return done
     xt, xh = _heads(x, "x")
     T, H, D = x.shape
     table = _rope_table(rope)
@@ -173,6 +178,12 @@ def mol_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     int32 [T] of the cache (page * page_size + offset; outside the cache, as -1: not written), and
     returns q bf16 [T, heads, head_dim] turned likewise (None without q). q_out may be `q`; tokens
     name different slots."""
+    if _block._native is not None and q_out is None and stream is None:
+        f, interleaved, magnitude = (None, 0, 1.0) if rope is None else rope
+        done = _block._native.cache_append(_entry("mol_cache_append"), k, v, k_cache, v_cache, slots,
+                                           positions, f, int(interleaved), magnitude, q)
+        if done is not None:
+            return None if done is True else done
     kt, kh = _heads(k, "k")
     vt, vh = _heads(v, "v")
     T, H, D = k.shape
@@ -222,6 +233,13 @@ def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     rows begin (None: a row each); window > 0: the last tokens that a row sees, its own among them;
     scale: head_dim^-0.5 unless given. Rows that see nothing are 0; rows of no sequence keep what out
     held. workspace: mol_paged_attention_workspace_bytes of scratch. out may be `q`."""
+    if _block._native is not None and out is None and workspace is None and stream is None:
+        done = _block._native.paged_attention(
+            _entry("mol_paged_attention"), _entry("mol_paged_attention_workspace_bytes"), q, k_cache,
+            v_cache, page_table, kv_lens, q_starts, q.shape[-1] ** -0.5 if scale is None else scale,
+            window)
+        if done is not None:
+            return done
     qt, qh = _heads(q, "q")
     T, H, D = q.shape
     cache = _paged(k_cache, v_cache)

@@ -1,4 +1,5 @@
-// Native calls of the MoE block's binding (block.py), for the common case: operands of the right types
+// Native calls of the bindings of the MoE block and of the attention half (block.py, attention.py), for
+// the common case: operands of the right types
 // and shapes (rows may have a stride), outputs to be allocated, the current stream. Each function checks that
 // case, allocates, and calls the C entry point whose address it is given; it returns None for
 // anything else, also where the entry point refuses, and the Python function then takes its own path
@@ -15,6 +16,7 @@
 
 #include <exception>
 
+#include "mol_attn.h"
 #include "mol_block.h"
 
 namespace {
@@ -284,10 +286,144 @@ PyObject* w4_linear(Args a) {
   return status == MOL_OK ? THPVariable_Wrap(out) : none();
 }
 
+// Heads [tokens, heads, width] of bf16, a head's values next to each other. A single token or head has
+// no stride that matters.
+struct Heads {
+  const Tensor* t = nullptr;
+  int64_t tokens = 0, heads = 0, width = 0, token_stride = 0, head_stride = 0;
+  bool of(const Tensor* x) {
+    t = x;
+    if (x->scalar_type() != at::kBFloat16 || !here(*x) || x->dim() != 3 ||
+        (x->stride(2) != 1 && x->size(2) > 1))
+      return false;
+    tokens = x->size(0);
+    heads = x->size(1);
+    width = x->size(2);
+    if (!small({tokens, heads, width})) return false;
+    head_stride = heads > 1 ? x->stride(1) : (width + 7) / 8 * 8;
+    token_stride = tokens > 1 ? x->stride(0) : (heads * head_stride + 7) / 8 * 8;
+    return true;
+  }
+  void* ptr() const { return t ? t->data_ptr() : nullptr; }
+};
+
+// The operand's heads, in memory of the call's own.
+Tensor like(const Heads& h) { return at::empty({h.tokens, h.heads, h.width}, h.t->options()); }
+
+struct RopeTable {
+  const Tensor* inv_freq;
+  mol_rope_table table;
+  bool take(Args& a) {
+    int64_t interleaved;
+    double magnitude;
+    if (!a.take_optional(inv_freq) || !a.take(interleaved) || !a.take(magnitude)) return false;
+    if (!inv_freq) return true;
+    if (!fits(*inv_freq, at::kFloat, {-1}) || !small({2 * inv_freq->size(0), interleaved})) return false;
+    table = {static_cast<const float*>(inv_freq->data_ptr()), (int32_t)(2 * inv_freq->size(0)),
+             (int32_t)interleaved, (float)magnitude};
+    return true;
+  }
+  const mol_rope_table* ptr() const { return inv_freq ? &table : nullptr; }
+};
+
+// Keys and values [pages, page_size, heads, width], one shape and the same strides.
+struct Cache {
+  mol_paged_cache c;
+  bool take(Args& a) {
+    const Tensor *k, *v;
+    if (!a.take(k) || !a.take(v)) return false;
+    for (const Tensor* t : {k, v})
+      if (t->scalar_type() != at::kBFloat16 || !here(*t) || t->dim() != 4 ||
+          (t->stride(3) != 1 && t->size(3) > 1))
+        return false;
+    if (k->sizes() != v->sizes() || k->strides() != v->strides() ||
+        !small({k->size(0), k->size(1), k->size(2), k->size(3)}))
+      return false;
+    auto stride = [&](int i) { return k->size(i) > 1 ? k->stride(i) : 0; };
+    c = {k->data_ptr(), v->data_ptr(), stride(0), stride(1), stride(2), k->size(0),
+         (int32_t)k->size(1), (int32_t)k->size(2), (int32_t)k->size(3)};
+    return true;
+  }
+};
+
+const int32_t* ints(const Tensor* t) {
+  return t ? static_cast<const int32_t*>(t->data_ptr()) : nullptr;
+}
+
+PyObject* rope(Args a) {
+  void* f;
+  const Tensor *x, *positions;
+  Heads h;
+  RopeTable r;
+  if (!a.take(f) || !a.take(x) || !a.take(positions) || !r.take(a) || !r.inv_freq || !h.of(x) ||
+      !fits(*positions, at::kInt, {h.tokens}))
+    return none();
+  Tensor out = like(h);
+  const int32_t status = reinterpret_cast<decltype(&mol_rope)>(f)(
+      h.ptr(), h.token_stride, h.head_stride, ints(positions), r.ptr(), h.tokens, (int32_t)h.heads,
+      (int32_t)h.width, out.data_ptr(), h.heads * h.width, h.width, stream_of(*x));
+  return status == MOL_OK ? THPVariable_Wrap(out) : none();
+}
+
+// True where there are no queries to return.
+PyObject* cache_append(Args a) {
+  void* f;
+  const Tensor *k, *v, *slots, *positions, *q;
+  Heads kh, vh, qh;
+  Cache c;
+  RopeTable r;
+  if (!a.take(f) || !a.take(k) || !a.take(v) || !c.take(a) || !a.take(slots) ||
+      !a.take_optional(positions) || !r.take(a) || !a.take_optional(q) || !kh.of(k) || !vh.of(v) ||
+      k->sizes() != v->sizes() || kh.heads != c.c.num_heads || kh.width != c.c.head_dim ||
+      !fits(*slots, at::kInt, {kh.tokens}) || (r.inv_freq && !positions) ||
+      (positions && !fits(*positions, at::kInt, {kh.tokens})))
+    return none();
+  Tensor out;
+  if (q) {
+    if (!r.inv_freq || !qh.of(q) || qh.tokens != kh.tokens || qh.width != kh.width) return none();
+    out = like(qh);
+  }
+  const int32_t status = reinterpret_cast<decltype(&mol_cache_append)>(f)(
+      kh.ptr(), kh.token_stride, kh.head_stride, vh.ptr(), vh.token_stride, vh.head_stride, ints(slots),
+      ints(positions), r.ptr(), kh.tokens, &c.c, qh.ptr(), qh.token_stride, qh.head_stride,
+      (int32_t)qh.heads, q ? out.data_ptr() : nullptr, qh.heads * qh.width, qh.width, stream_of(*k));
+  if (status != MOL_OK) return none();
+  if (q) return THPVariable_Wrap(out);
+  Py_RETURN_TRUE;
+}
+
+PyObject* paged_attention(Args a) {
+  void *f, *need;
+  const Tensor *q, *table, *lens, *starts;
+  double scale;
+  int64_t window;
+  Heads h;
+  Cache c;
+  if (!a.take(f) || !a.take(need) || !a.take(q) || !c.take(a) || !a.take(table) || !a.take(lens) ||
+      !a.take_optional(starts) || !a.take(scale) || !a.take(window) || !h.of(q) ||
+      h.width != c.c.head_dim || table->dim() != 2 || table->scalar_type() != at::kInt ||
+      !here(*table) || (table->size(1) > 1 && table->stride(1) != 1))
+    return none();
+  const int64_t B = table->size(0), pages = table->size(1);
+  if (!small({B, pages, window}) || !fits(*lens, at::kInt, {B}) ||
+      (starts ? !fits(*starts, at::kInt, {B + 1}) : h.tokens != B))
+    return none();
+  const size_t bytes = reinterpret_cast<decltype(&mol_paged_attention_workspace_bytes)>(need)(
+      B, h.tokens, (int32_t)h.heads, c.c.num_heads, c.c.head_dim);
+  Tensor out = like(h), ws = scratch(*q, bytes);
+  const int32_t status = reinterpret_cast<decltype(&mol_paged_attention)>(f)(
+      h.ptr(), h.token_stride, h.head_stride, &c.c, ints(table), B > 1 ? table->stride(0) : pages,
+      (int32_t)pages, ints(lens), ints(starts), B, h.tokens, (int32_t)h.heads, (float)scale,
+      (int32_t)window, out.data_ptr(), h.heads * h.width, h.width, bytes ? ws.data_ptr() : nullptr,
+      bytes, stream_of(*q));
+  return status == MOL_OK ? THPVariable_Wrap(out) : none();
+}
+
 #define MOL_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MOL_METHOD(block_norm), MOL_METHOD(moe_route), MOL_METHOD(moe_gate_up),
                          MOL_METHOD(moe_down),   MOL_METHOD(moe_forward), MOL_METHOD(w4_linear),
+                         MOL_METHOD(rope),       MOL_METHOD(cache_append), MOL_METHOD(paged_attention),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_native", nullptr, -1, methods,

@@ -145,6 +145,23 @@ def test_workspace_sizes(mol):
         assert 0 < size(4, 9, 8, 2, D) < 128 << 20
 
 
+@needs_nvcc
+def test_native_calls_leave_everything_unusual_to_the_python_path(mol):
+    """Wrong kinds, counts, types, devices: None, and no exception is left behind."""
+    native = pytest.importorskip("moe_lora_virtual_gb300._block_native")
+    x, c = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16)
+    i, f = torch.zeros(2, dtype=torch.int32), torch.zeros(32)
+    e = ctypes.cast(mol.library().mol_rope, ctypes.c_void_p).value
+    for name, args in [("rope", (e, x, i, f, 0, 1.0)),
+                       ("cache_append", (e, x, x, c, c, i, i, f, 0, 1.0, x)),
+                       ("paged_attention", (e, e, x, c, c, i.view(2, 1), i, None, 0.1, 0))]:
+        call = getattr(native, name)
+        for bad in [args, args[:-1], (), (0, *args[1:]), (None, *args[1:]), (e, None, *args[2:]),
+                    (e, "x", *args[2:]), (2 ** 80, *args[1:]), tuple([x] * len(args)),
+                    (*args[:-1], 2 ** 70), (*args[:-1], "x")]:
+            assert call(*bad) is None, (name, bad)
+
+
 # ----------------------------------------------------------------------------------- frequencies
 def test_frequencies(mol):
     f = mol.rope_frequencies

@@ -256,3 +256,155 @@ def test_no_rows_no_sequences_no_pages(env):
     q = torch.ones(1, 4, 64, **bf)
     assert bool((mol.mol_paged_attention(q, kc, kc, table[:, :0], lens) == 0).all())
     assert bool((mol.mol_paged_attention(q, kc[:0], kc[:0], table, lens) == 0).all())
+
+
+# ------------------------------------------------------------------------------------ the calls
+def step(torch, mol, g, T=5, Hq=4, Hkv=2, D=64, page=8, kv=40):
+    """Tensors of one attention step of T sequences with a token each, and the calls on them."""
+    pages = T * (kv // page) + 2
+    s = dict(rows=randn(torch, g, T, Hq + 2 * Hkv, D).cuda(), rope=mol.rope_frequencies(32, device="cuda"),
+             kc=randn(torch, g, pages, page, Hkv, D).cuda(), vc=randn(torch, g, pages, page, Hkv, D).cuda(),
+             table=torch.randperm(pages, generator=g)[:T * (kv // page)].to(torch.int32).view(T, -1).cuda(),
+             lens=torch.randint(1, kv + 1, (T,), generator=g).to(torch.int32).cuda())
+    at = (s["lens"] - 1).long()
+    s["positions"] = at.to(torch.int32)
+    s["slots"] = (s["table"].gather(1, (at // page).unsqueeze(1)).view(-1) * page + at % page).to(torch.int32)
+
+    def run(**kw):
+        r = s["rows"]
+        x = mol.mol_rope(r[:, :Hq], s["positions"], s["rope"], **kw)
+        q = mol.mol_cache_append(r[:, Hq:Hq + Hkv], r[:, Hq + Hkv:], s["kc"], s["vc"], s["slots"],
+                                 s["positions"], s["rope"], q=r[:, :Hq], **kw)
+        out = mol.mol_paged_attention(q, s["kc"], s["vc"], s["table"], s["lens"], **kw)
+        return x, q, out, s["kc"], s["vc"]
+
+    return s, run
+
+
+def test_native_calls_equal_the_python_path(env, monkeypatch):
+    torch, mol = env
+    from moe_lora_virtual_gb300 import block
+    assert block._native is not None, "the native calls are not built"
+    g = torch.Generator().manual_seed(2)
+    s, run = step(torch, mol, g)
+    taken, real = [], block._native
+
+    class Count:
+        def __getattr__(self, name):
+            def call(*a):
+                out = getattr(real, name)(*a)
+                taken.append(out is not None)
+                return out
+            return call
+
+    monkeypatch.setattr(block, "_native", Count())
+    got = [t.clone() for t in run()]
+    starts = torch.tensor([0, 2, 2, 3, 5, 5], dtype=torch.int32, device="cuda")
+    more = mol.mol_paged_attention(got[1], s["kc"], s["vc"], s["table"], s["lens"], starts, scale=0.3, window=9)
+    assert mol.mol_cache_append(s["rows"][:, :2], s["rows"][:, 2:4], s["kc"], s["vc"], s["slots"]) is None
+    plain = [s["kc"].clone(), s["vc"].clone()]
+    assert len(taken) == 5 and all(taken)
+    monkeypatch.setattr(block, "_native", None)
+    mol.mol_cache_append(s["rows"][:, :2], s["rows"][:, 2:4], s["kc"], s["vc"], s["slots"])
+    assert torch.equal(plain[0], s["kc"]) and torch.equal(plain[1], s["vc"])
+    for a, b in zip(got, run()):
+        assert torch.equal(a, b)
+    assert torch.equal(more, mol.mol_paged_attention(got[1], s["kc"], s["vc"], s["table"], s["lens"], starts,
+                                                     scale=0.3, window=9))
+
+
+def test_a_layer_step_in_a_graph_and_on_a_stream(env):
+    """The three calls as a decoding step makes them: captured and replayed on new rows and lengths, and
+    on a stream of their own."""
+    torch, mol = env
+    g = torch.Generator().manual_seed(3)
+    s, run = step(torch, mol, g, T=9, D=128, kv=96)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    s["rows"].copy_(randn(torch, g, *s["rows"].shape))
+    fresh = torch.randint(1, 97, (9,), generator=g).to(torch.int32).cuda()
+    s["lens"].copy_(fresh)
+    kc, vc = s["kc"].clone(), s["vc"].clone()
+    graph.replay()
+    got = [t.clone() for t in captured]
+    s["kc"].copy_(kc), s["vc"].copy_(vc)
+    for a, b in zip(got, run()):
+        assert torch.equal(a, b)
+    s["kc"].copy_(kc), s["vc"].copy_(vc)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = run(stream=side)
+    side.synchronize()
+    for a, b in zip(got, out):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D,lens", [(64, [(1, 900), (1, 3)]), (128, [(200, 700), (1, 2000), (3, 9)]),
+                                    (256, [(5, 1500)])])
+def test_results_do_not_depend_on_timing_or_what_memory_held(env, D, lens):
+    """Bit-equal over calls, over workspaces of NaN and of ones, with the workspace of another size."""
+    torch, mol = env
+    p = au.problem(torch, D, lens, 8, 2, D, 16)
+    first = attend(env, p)
+    size = mol.mol_paged_attention_workspace_bytes(len(lens), p["q"].shape[0], 8, 2, D)
+    for byte, more in ((0xFF, 0), (1, 4096), (0x7F, 16)):
+        ws = torch.full((size + more,), byte, dtype=torch.uint8, device="cuda")
+        assert torch.equal(attend(env, p, workspace=ws), first)
+
+
+def test_out_may_be_the_queries(env):
+    torch, mol = env
+    for lens in ([(1, 70), (1, 2)], [(150, 150), (40, 700)]):
+        p = au.problem(torch, 7, lens, 8, 2, 64, 16)
+        want = attend(env, p)
+        kc, vc = au.caches(p, "cuda")
+        q = p["q"].cuda()
+        got = mol.mol_paged_attention(q, kc, vc, p["table"].cuda(), p["kv_lens"].cuda(),
+                                      None if p["starts"] is None else p["starts"].cuda(), out=q)
+        assert got is q and torch.equal(got.cpu(), want)
+
+
+def test_binding_refusals(env):
+    torch, mol = env
+    bf, i32 = (dict(dtype=d, device="cuda") for d in (torch.bfloat16, torch.int32))
+    x, pos = torch.zeros(3, 4, 64, **bf), torch.zeros(3, **i32)
+    kc, vc = torch.zeros(2, 8, 2, 64, **bf), torch.zeros(2, 8, 2, 64, **bf)
+    k, rope = x[:, :2], mol.rope_frequencies(64, device="cuda")
+    table, lens = torch.zeros(3, 2, **i32), torch.ones(3, **i32)
+    wrong = [
+        (ValueError, lambda: mol.mol_rope(x[0], pos, rope)),
+        (ValueError, lambda: mol.mol_rope(x, pos[:2], rope)),
+        (TypeError, lambda: mol.mol_rope(x, pos.long(), rope)),
+        (TypeError, lambda: mol.mol_rope(x.float(), pos, rope)),
+        (TypeError, lambda: mol.mol_rope(x.cpu(), pos, rope)),
+        (ValueError, lambda: mol.mol_rope(x.transpose(1, 2), pos, rope)),
+        (mol.MolError, lambda: mol.mol_rope(x[..., :32], pos, rope)),
+        (ValueError, lambda: mol.mol_rope(x, pos, rope, out=x[:, :2])),
+        (ValueError, lambda: mol.mol_cache_append(x, x, kc, vc, pos)),
+        (ValueError, lambda: mol.mol_cache_append(k, k[:2], kc, vc, pos)),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, vc[:1], pos)),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, vc, pos, rope=rope)),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, vc, pos, q=x)),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, vc, pos, pos, rope, q_out=x)),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, vc, pos, pos, rope, q=x[:2])),
+        (ValueError, lambda: mol.mol_cache_append(k, k, kc, torch.zeros(2, 2, 8, 64, **bf).transpose(1, 2), pos)),
+        (ValueError, lambda: mol.mol_paged_attention(x[:2], kc, vc, table, lens)),
+        (ValueError, lambda: mol.mol_paged_attention(x, kc, vc, table[0], lens)),
+        (ValueError, lambda: mol.mol_paged_attention(x, kc, vc, table, lens[:2])),
+        (ValueError, lambda: mol.mol_paged_attention(x, kc, vc, table, lens, pos)),
+        (ValueError, lambda: mol.mol_paged_attention(x[..., :32], kc, vc, table, lens)),
+        (TypeError, lambda: mol.mol_paged_attention(x, kc, vc, table.long(), lens)),
+        (ValueError, lambda: mol.mol_paged_attention(x, kc, vc, table.t(), lens[:2], pos)),
+        (mol.MolError, lambda: mol.mol_paged_attention(x[:, :3], kc, vc, table, lens)),
+        (mol.MolError, lambda: mol.mol_paged_attention(x, kc, vc, table, lens, scale=0.0)),
+        (mol.MolError, lambda: mol.mol_paged_attention(x, kc, vc, table, lens, window=-1)),
+        (mol.MolError, lambda: mol.mol_paged_attention(x, kc, vc, table, lens,
+                                                       workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))),
+    ]
+    for i, (error, call) in enumerate(wrong):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {i} was taken")
