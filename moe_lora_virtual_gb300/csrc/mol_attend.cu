@@ -15,9 +15,7 @@ using attn::Record;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;             // tokens a warp takes at a time
-constexpr int kTile = kWarps * kStep;
-constexpr int kExtra = 0;             // units that a block takes beside its tiles
+constexpr int kExtra = 1;             // units that a block takes beside its tiles
 
 MOL_DEV void ldsm4(const void* p, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -34,22 +32,25 @@ MOL_DEV void ldsm4_t(const void* p, uint32_t (&r)[4]) {
 template <int D, int MT>
 struct Geo {
   static constexpr int kRows = 16 * MT;
-  static constexpr int kStages = D == 64 ? 6 : 3;
+  static constexpr int kStep = D == 64 ? 32 : 16;        // tokens a warp takes at a time
+  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kStages = 3;
   static constexpr int kTileBytes = kStep * D * 2;       // keys, or values, of a step
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
-  // queries while a block runs, then its sums
-  static constexpr int kShared = kRows * D * 4;
-  static constexpr size_t kSmem = (size_t)kRing + kShared;
+  static constexpr size_t kSmem = (size_t)kRing + kRows * D * 2;  // and the queries
+  // Rows whose sums a warp leaves in the ring stage it has just taken, for the others to add.
+  static constexpr int kMeet = kStageBytes / (D * 4) < kRows ? kStageBytes / (D * 4) : kRows;
+  static_assert(kMeet % 16 == 0 && kRows % kMeet == 0, "sums that meet");
   static constexpr int kPerSM = kSmem <= 113 * 1024 ? 2 : 1;
   static constexpr bool kQueriesInRegisters = MT * D <= 128;
 };
 
 // Few rows (new tokens x group) against long runs of keys: the cache is read once, and that is what
-// bounds it. All tiles of 64 tokens of the launch, over sequences, heads and row blocks, are one list
+// bounds it. All tiles of 64 tokens (128 for 64 values a head) of the launch, over sequences, heads and row blocks, are one list
 // dealt in even runs to thread blocks, so sequences of any lengths fill the GPU alike; a block whose
 // tiles fall to several leaves parts that launch_join adds in order. In a tile each warp has 16
-// tokens of its own, with a cp.async ring of its own that runs on across the blocks' borders (keys and
+// (32) tokens of its own, with a cp.async ring of its own that runs on across the blocks' borders (keys and
 // values asked for two steps ahead, no barrier between warps), its own maximum, sum and fp32
 // accumulators; the warps meet where a block ends. Scores: mma.sync with the rows as the 16-row side.
 // Tokens that lie on no page, or past the sequence, are zero in shared memory, whatever memory
@@ -67,54 +68,60 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* ring = smem + warp * (G::kStages * G::kStageBytes);
   unsigned char* shared = smem + G::kRing;
-  float* sums = reinterpret_cast<float*>(shared);
 
   pdl_wait();
   pdl_launch_dependents();
   const Parts parts = attn::parts(a.workspace, gridDim.x, G::kRows, D);
-  const attn::Run run = attn::deal<kThreads>(a, G::kRows, kTile, kExtra, s_scan, &s_place);
+  const attn::Run run = attn::deal<kThreads>(a, G::kRows, G::kTile, kExtra, s_scan, &s_place);
   const int64_t c = blockIdx.x;
-  if (c >= run.grid) {
+  if (!run.any) {
     if (tid == 0) parts.records[c].last = -1;
     return;
   }
-  const int nv = attn::num_blocks(a, G::kRows);
-
-  attn::Walk<kTile, kExtra> load, work;
-  load.start(s_place, G::kRows, run.to - run.from);
-  if (load.count == 0) load.next(a, nv);
+  constexpr int kStep = G::kStep;
+  attn::Walk<G::kTile, kExtra> load, work;
+  load.start(a, s_place, G::kRows, run);
   work = load;
   int load_tile = 0;  // of load.count
 
-  // Asks for the step at `load` into ring stage s and moves on.
+  // Where this lane's token of a step lies: its page is asked for two steps before its copies are.
+  struct Token {
+    int page, offset, h;  // (page -1: no row sees the token)
+  };
+  auto look = [&]() {
+    Token t = {-1, 0, load.h};
+    if (!load.more()) return t;
+    const int j = (load.k.t0 + load.first + load_tile) * G::kTile + warp * kStep + lane % kStep;
+    if (j >= load.k.lo && j < load.k.hi) {
+      const int p = j / a.page_size;
+      t.page = __ldg(a.page_table + load.k.b * a.table_stride + p);
+      t.offset = j - p * a.page_size;
+    }
+    if (++load_tile == load.count) {
+      load.next(a);
+      load_tile = 0;
+    }
+    return t;
+  };
+  Token ahead[2] = {look(), look()};
+  // Asks for the next step into ring stage s.
   auto fetch = [&](int s) {
-    if (load.more()) {
-      const int j = (load.k.t0 + load.first + load_tile) * kTile + warp * kStep + (lane & 15);
-      int64_t at = 0;
-      bool held = j >= load.k.lo && j < load.k.hi;
-      if (held) {
-        const int p = j / a.page_size;
-        const int page = __ldg(a.page_table + load.k.b * a.table_stride + p);
-        held = page >= 0 && page < a.num_pages;
-        if (held)
-          at = page * a.page_stride + (j - p * a.page_size) * a.token_stride + load.h * a.head_stride;
-      }
-      const uint32_t mask = __ballot_sync(0xffffffffu, held);
-      if (lane == 0) s_held[warp][s] = mask;
-      unsigned char* st = ring + s * G::kStageBytes;
+    const Token t = ahead[0];
+    ahead[0] = ahead[1];
+    ahead[1] = look();
+    const bool held = t.page >= 0 && t.page < a.num_pages;
+    const int64_t at = held ? t.page * a.page_stride + t.offset * a.token_stride + t.h * a.head_stride : 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, held);
+    if (lane == 0) s_held[warp][s] = mask;
+    unsigned char* st = ring + s * G::kStageBytes;
 #pragma unroll
-      for (int i = 0; i < kStep * kChunks / 32; ++i) {
-        const int idx = i * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
-        const int64_t from_row = __shfl_sync(0xffffffffu, at, row) + ch * 8;
-        const uint32_t n = (mask >> row) & 1 ? 16u : 0u;
-        unsigned char* d = st + row * (D * 2) + ((ch ^ (row & 7)) << 4);
-        cp_async16_zfill(d, a.k + from_row, n);
-        cp_async16_zfill(d + G::kTileBytes, a.v + from_row, n);
-      }
-      if (++load_tile == load.count) {
-        load.next(a, nv);
-        load_tile = 0;
-      }
+    for (int i = 0; i < kStep * kChunks / 32; ++i) {
+      const int idx = i * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
+      const int64_t from_row = __shfl_sync(0xffffffffu, at, row) + ch * 8;
+      const uint32_t n = (mask >> row) & 1 ? 16u : 0u;
+      unsigned char* d = st + row * (D * 2) + ((ch ^ (row & 7)) << 4);
+      cp_async16_zfill(d, a.k + from_row, n);
+      cp_async16_zfill(d + G::kTileBytes, a.v + from_row, n);
     }
     cp_async_commit();
   };
@@ -123,23 +130,37 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 
   const int g = lane >> 2, t4 = lane & 3;
   int stage = 0;
-  Record record = {};
-  record.last = -1;
-  for (; work.more(); work.next(a, nv)) {
-    // ------------------------------------------------------------ a block of rows and a head
-    const Block& k = work.k;
-    const int h = work.h;
-    for (int i = tid; i < G::kRows * kChunks; i += kThreads) {
-      const int row = i / kChunks, ch = i % kChunks;
-      uint4 q = make_uint4(0, 0, 0, 0);
+  // A block's queries are asked for while the block before it ends.
+  constexpr int kQueries = G::kRows * kChunks / kThreads;
+  uint4 query[kQueries];
+  auto ask_queries = [&](const Block& k, int h) {
+#pragma unroll
+    for (int i = 0; i < kQueries; ++i) {
+      const int row = (i * kThreads + tid) / kChunks, ch = (i * kThreads + tid) % kChunks;
+      query[i] = make_uint4(0, 0, 0, 0);
       if (row < k.nrows) {
         const int r = k.row0 + row, token = r / a.group;
-        q = __ldg(reinterpret_cast<const uint4*>(
+        query[i] = __ldg(reinterpret_cast<const uint4*>(
             a.q + (int64_t)(k.s.start + token) * a.q_token_stride +
             (int64_t)(h * a.group + r - token * a.group) * a.q_head_stride + ch * 8));
       }
-      *reinterpret_cast<uint4*>(shared + row * (D * 2) + ((ch ^ (row & 7)) << 4)) = q;
     }
+  };
+  auto put_queries = [&]() {
+#pragma unroll
+    for (int i = 0; i < kQueries; ++i) {
+      const int row = (i * kThreads + tid) / kChunks, ch = (i * kThreads + tid) % kChunks;
+      *reinterpret_cast<uint4*>(shared + row * (D * 2) + ((ch ^ (row & 7)) << 4)) = query[i];
+    }
+  };
+  Record record = {};
+  record.last = -1;
+  if (work.more()) ask_queries(work.k, work.h);
+  while (work.more()) {
+    // ------------------------------------------------------------ a block of rows and a head
+    const Block& k = work.k;
+    const int h = work.h;
+    put_queries();
     __syncthreads();
     auto load_q = [&](int mt, int kk, uint32_t (&r)[4]) {
       const int row = mt * 16 + (lane & 15), ch = 2 * kk + (lane >> 4);
@@ -177,19 +198,24 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
       fetch(stage == 0 ? G::kStages - 1 : stage - 1);
       const unsigned char* kt = ring + stage * G::kStageBytes;
       const unsigned char* vt = kt + G::kTileBytes;
-      const uint32_t mask = s_held[warp][stage];
-      const int j0 = (k.t0 + tile) * kTile + warp * kStep;
-      if ((mask & 0xffffu) != 0) {
-        float s[MT][2][4];
+      constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : (1u << kStep) - 1;
+      constexpr int kNT = kStep / 8;
+      const uint32_t mask = s_held[warp][stage] & kAll;
+      const int j0 = (k.t0 + tile) * G::kTile + warp * kStep;
+      if (mask != 0) {
+        float s[MT][kNT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+          for (int n = 0; n < kNT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t b[4];
-          const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * kk + ((lane >> 3) & 1);
-          ldsm4(kt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b);
+          uint32_t b[kNT / 2][4];
+#pragma unroll
+          for (int n = 0; n < kNT / 2; ++n) {
+            const int row = n * 16 + (lane & 7) + ((lane >> 4) << 3), ch = 2 * kk + ((lane >> 3) & 1);
+            ldsm4(kt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b[n]);
+          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t q[4];
@@ -199,12 +225,13 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
             } else {
               load_q(mt, kk, q);
             }
-            mma_16816(s[mt][0], q[0], q[1], q[2], q[3], b[0], b[1]);
-            mma_16816(s[mt][1], q[0], q[1], q[2], q[3], b[2], b[3]);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              mma_16816(s[mt][n], q[0], q[1], q[2], q[3], b[n / 2][n % 2 * 2], b[n / 2][n % 2 * 2 + 1]);
           }
         }
         // every row sees every token of the step, or not
-        const bool edge = (mask & 0xffffu) != 0xffffu || j0 + kStep - 1 > pos_first ||
+        const bool edge = mask != kAll || j0 + kStep - 1 > pos_first ||
                           (a.window > 0 && j0 <= pos_last - a.window);
         auto sees = [&](int j, int p) {
           return ((mask >> (j - j0)) & 1) && j <= p && (a.window == 0 || j > p - a.window);
@@ -212,25 +239,26 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kNT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               s[mt][n][e] *= a.scale_log2;
               if (edge && !sees(j0 + n * 8 + 2 * t4 + (e & 1), pos[mt][e >> 1])) s[mt][n][e] = -INFINITY;
             }
-        uint32_t p[MT][4];
+        uint32_t p[MT][kStep / 16][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float m = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]),
-                            fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+            float m = s[mt][0][2 * i];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) m = fmaxf(m, fmaxf(s[mt][n][2 * i], s[mt][n][2 * i + 1]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const float was = top[mt][i];
             if (__any_sync(0xffffffffu, m > was)) {
               const float now = fmaxf(was, m);
-              const float f = was == now ? 1.f : exp2f(was - now);  // (-inf before the first)
+              const float f = was == now ? 1.f : attn::ex2(was - now);  // (-inf before the first)
               top[mt][i] = now;
               sum[mt][i] *= f;
 #pragma unroll
@@ -239,21 +267,22 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
                 o[mt][n][2 * i + 1] *= f;
               }
             }
-            // a row that has seen nothing yet keeps weights of 0: exp2(-inf)
+            // a row that has seen nothing yet keeps weights of 0: 2^-inf
             const float base = top[mt][i] == -INFINITY ? 0.f : top[mt][i];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kNT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float w = exp2f(s[mt][n][2 * i + e] - base);
+                const float w = attn::ex2(s[mt][n][2 * i + e] - base);
                 s[mt][n][2 * i + e] = w;
                 sum[mt][i] += w;
               }
           }
-          p[mt][0] = pack_bf16x2(s[mt][0][0], s[mt][0][1]);
-          p[mt][1] = pack_bf16x2(s[mt][0][2], s[mt][0][3]);
-          p[mt][2] = pack_bf16x2(s[mt][1][0], s[mt][1][1]);
-          p[mt][3] = pack_bf16x2(s[mt][1][2], s[mt][1][3]);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            p[mt][n / 2][n % 2 * 2] = pack_bf16x2(s[mt][n][0], s[mt][n][1]);
+            p[mt][n / 2][n % 2 * 2 + 1] = pack_bf16x2(s[mt][n][2], s[mt][n][3]);
+          }
         }
         bool plain = false;
         if (edge) {
@@ -265,50 +294,61 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
         }
         if (!plain) {
 #pragma unroll
-          for (int n2 = 0; n2 < D / 16; ++n2) {
-            uint32_t b[4];
-            const int row = lane & 15, ch = 2 * n2 + (lane >> 4);
-            ldsm4_t(vt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b);
+          for (int x = 0; x < kStep / 16; ++x)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_16816(o[mt][2 * n2], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b[0], b[1]);
-              mma_16816(o[mt][2 * n2 + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b[2], b[3]);
+            for (int n2 = 0; n2 < D / 16; ++n2) {
+              uint32_t b[4];
+              const int row = x * 16 + (lane & 15), ch = 2 * n2 + (lane >> 4);
+              ldsm4_t(vt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t(&w)[4] = p[mt][x];
+                mma_16816(o[mt][2 * n2], w[0], w[1], w[2], w[3], b[0], b[1]);
+                mma_16816(o[mt][2 * n2 + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+              }
             }
-          }
         } else {
+#pragma unroll
+          for (int x = 0; x < kStep / 16; ++x)
 #pragma unroll 1
-          for (int i = 0; i < kStep; ++i) {
-            const int j = j0 + i, from_lane = (lane & ~3) | ((i & 7) >> 1);
+            for (int i = 0; i < 16; ++i) {
+              const int at = x * 16 + i, j = j0 + at, from_lane = (lane & ~3) | ((i & 7) >> 1);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              float w[2];
+              for (int mt = 0; mt < MT; ++mt) {
+                float w[2];
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t pair = i < 8 ? p[mt][r] : p[mt][2 + r];
-                const uint32_t got = __shfl_sync(0xffffffffu, pair, from_lane);
-                w[r] = i & 1 ? bf16_hi(got) : bf16_lo(got);
-              }
-              const bool see[2] = {sees(j, pos[mt][0]), sees(j, pos[mt][1])};
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t pair = i < 8 ? p[mt][x][r] : p[mt][x][2 + r];
+                  const uint32_t got = __shfl_sync(0xffffffffu, pair, from_lane);
+                  w[r] = i & 1 ? bf16_hi(got) : bf16_lo(got);
+                }
+                const bool see[2] = {sees(j, pos[mt][0]), sees(j, pos[mt][1])};
 #pragma unroll
-              for (int n = 0; n < D / 8; ++n) {
-                const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + i * (D * 2) +
-                                                                      ((n ^ (i & 7)) << 4) + 4 * t4);
-                const float v0 = bf16_lo(v), v1 = bf16_hi(v);
+                for (int n = 0; n < D / 8; ++n) {
+                  const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + at * (D * 2) +
+                                                                        ((n ^ (at & 7)) << 4) + 4 * t4);
+                  const float v0 = bf16_lo(v), v1 = bf16_hi(v);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  if (see[r]) {
-                    o[mt][n][2 * r] += w[r] * v0;
-                    o[mt][n][2 * r + 1] += w[r] * v1;
-                  }
+                  for (int r = 0; r < 2; ++r)
+                    if (see[r]) {
+                      o[mt][n][2 * r] += w[r] * v0;
+                      o[mt][n][2 * r + 1] += w[r] * v1;
+                    }
+                }
               }
             }
-          }
         }
       }
       stage = stage + 1 == G::kStages ? 0 : stage + 1;
     }
 
     // ------------------------------------------------------------ the warps' sums become one
+    const bool begins = work.first == 0, part = !begins || !work.ends();
+    const int slot = (int)(2 * c) + (begins ? 1 : 0);
+    const int start = k.s.start, row0 = k.row0, nrows = k.nrows;
+    if (begins && part && tid == 0) record = {work.last(run), start, row0, nrows, h, {}};
+    work.next(a);
+    if (work.more()) ask_queries(work.k, work.h);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -318,78 +358,55 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (t4 == 0) s_top[warp][mt * 16 + g + 8 * i] = make_float2(top[mt][i], l);
       }
-    __syncthreads();  // (and every warp has read its queries)
+    // Each in the stage that the next copies go to; the 32-byte pieces of a row in another order for
+    // each row, so that a store's rows do not fall on the same banks.
+    const int free_stage = stage == 0 ? G::kStages - 1 : stage - 1;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int row_m = 0; row_m < G::kRows; row_m += G::kMeet) {
+      unsigned char* mine = ring + free_stage * G::kStageBytes;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float m = -INFINITY;
+      for (int mt = row_m / 16; mt < (row_m + G::kMeet) / 16; ++mt)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][mt * 16 + g + 8 * i].x);
-        const float f = top[mt][i] == -INFINITY ? 0.f : exp2f(top[mt][i] - m);
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          // (a warp that saw nothing has sums of 0)
-          o[mt][n][2 * i] *= f;
-          o[mt][n][2 * i + 1] *= f;
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(mine + (mt * 16 - row_m + g + 8 * i) * (D * 4) + ((n ^ g) << 5) +
+                                       t4 * 8) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
+      __syncthreads();
+      for (int i = tid; i < G::kMeet * (D / 4); i += kThreads) {
+        const int local = i / (D / 4), row = row_m + local, col = i % (D / 4) * 4;
+        if (row >= nrows) break;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][row].x);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {  // (in this order, whatever the timing)
+          const float2 t = s_top[w][row];
+          const float f = t.x == -INFINITY ? 0.f : attn::ex2(t.x - m);
+          const float4 y = *reinterpret_cast<const float4*>(
+              smem + (w * G::kStages + free_stage) * G::kStageBytes + local * (D * 4) +
+              (((col >> 3) ^ (local & 7)) << 5) + (col & 4) * 4);
+          l += f * t.y;
+          x.x += f * y.x;
+          x.y += f * y.y;
+          x.z += f * y.z;
+          x.w += f * y.w;
         }
-      }
-    // in each phase the warps have different quarters of the columns; a quarter's order is fixed
-#pragma unroll 1
-    for (int phase = 0; phase < kWarps; ++phase) {
-#pragma unroll
-      for (int part = 0; part < kWarps; ++part) {
-        // (a value that the compiler does not follow: it would index the registers with it)
-        int mine = (warp + phase) & (kWarps - 1);
-        asm volatile("" : "+r"(mine));
-        if (part == mine) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < D / 8 / kWarps; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int col = part * (D / 8 / kWarps) + n;
-                float2* d = reinterpret_cast<float2*>(sums + (mt * 16 + g + 8 * i) * D + col * 8 + 2 * t4);
-                float2 x = make_float2(o[mt][col][2 * i], o[mt][col][2 * i + 1]);
-                if (phase > 0) {
-                  x.x += d->x;
-                  x.y += d->y;
-                }
-                *d = x;
-              }
+        if (part) {
+          *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
+          if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
+        } else {
+          const int r = row0 + row, token = r / a.group;
+          const float inv = m == -INFINITY ? 0.f : 1.f / l;
+          *reinterpret_cast<uint2*>(a.out + (int64_t)(start + token) * a.out_token_stride +
+                                    (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
+                                    col) =
+              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
         }
       }
       __syncthreads();
     }
-    // ------------------------------------------------------------ the rows, or a part of them
-    const bool begins = work.first == 0, part = !begins || !work.ends();
-    const int slot = (int)(2 * c) + (begins ? 1 : 0);
-    if (begins && part && tid == 0) record = {work.last(run), k.s.start, k.row0, k.nrows, h, {}};
-    for (int i = tid; i < k.nrows * (D / 4); i += kThreads) {
-      const int row = i / (D / 4), col = i % (D / 4) * 4;
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][row].x);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 x = s_top[w][row];
-        l += x.x == -INFINITY ? 0.f : x.y * exp2f(x.x - m);
-      }
-      const float4 x = *reinterpret_cast<const float4*>(sums + row * D + col);
-      if (part) {
-        *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
-        if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
-      } else {
-        const int r = k.row0 + row, token = r / a.group;
-        const float inv = m == -INFINITY ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
-                                  (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
-                                  col) =
-            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-      }
-    }
-    __syncthreads();
   }
   cp_async_wait_all();
   if (tid == 0) parts.records[c] = record;
@@ -425,7 +442,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
     for (int i = c + way; i <= rec.last; i += WAYS) {
       const int64_t at = (int64_t)(2 * i + (i == c)) * rows + row;
       const float2 t = p.tops[at];
-      const float f = t.x == -INFINITY ? 0.f : exp2f(t.x - m);
+      const float f = t.x == -INFINITY ? 0.f : attn::ex2(t.x - m);
       l += f * t.y;
       const float* v = p.sums + at * D + lane * kPer;
 #pragma unroll

@@ -16,6 +16,12 @@ MOL_DEV bool not_finite(const uint4& q) {
   return (c & 0x80008000u) != 0;
 }
 
+MOL_DEV float ex2(float x) {  // 2^x, within 2^-22 of it; 0 for -infinity
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One sequence of the call: its first row of q, its rows, its cached tokens. Whatever the caller's
 // arrays hold, rows stay within the call's and tokens within the page table.
 struct Seq {
@@ -34,49 +40,28 @@ MOL_DEV Seq sequence(const AttnArgs& a, int b) {
 }
 
 // A sequence's rows (new tokens x the group's query heads, row = token * group + head) are cut into
-// blocks of `rows`. Block numbers: sequence b's begin at start * group / rows + b, which leaves each
-// sequence room for its own without a sum over those before it. Some numbers are nobody's.
-MOL_DEV int first_block(const AttnArgs& a, int b, int rows) {
-  return a.q_starts ? (int)((int64_t)seq_start(a, b) * a.group / rows) + b
-                    : b * ((a.group + rows - 1) / rows);
-}
-__host__ __device__ inline int num_blocks(const AttnArgs& a, int rows) {
-  return a.q_starts ? (int)((int64_t)a.num_tokens * a.group / rows) + a.num_seqs
-                    : a.num_seqs * ((a.group + rows - 1) / rows);
-}
-// The sequence that block number v falls to.
-MOL_DEV int block_seq(const AttnArgs& a, int v, int rows) {
-  if (!a.q_starts) return v / ((a.group + rows - 1) / rows);
-  int lo = 0, hi = a.num_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_block(a, mid, rows) <= v)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
-}
-
-// A block of rows and the tiles of `tile` cached tokens that one of its rows sees.
+// blocks of `rows`. A block and the tiles of `tile` cached tokens that one of its rows sees:
 struct Block {
-  int b;
+  int b, r;         // sequence, block of it
   Seq s;
   int row0, nrows;  // first row within the sequence, rows
   int lo, hi;       // tokens that some row sees lie in [lo, hi)
-  int t0, tiles;    // tiles of them (one, with nothing in it, where there are none); 0: nobody's
+  int t0, tiles;    // tiles of them (one, with nothing in it, where there are none)
 };
-MOL_DEV Block block_of(const AttnArgs& a, int v, int b, int rows, int tile) {
+// Blocks of a sequence; none where it is another launch's.
+MOL_DEV int num_blocks(const AttnArgs& a, const Seq& s, int rows) {
+  const int total = s.n * a.group;
+  return total < a.min_rows || total > a.max_rows ? 0 : (total + rows - 1) / rows;
+}
+MOL_DEV Block block_of(const AttnArgs& a, int b, const Seq& s, int r, int rows, int tile) {
   Block k;
   k.b = b;
-  k.s = sequence(a, b);
-  k.row0 = (v - first_block(a, b, rows)) * rows;
-  const int total = k.s.n * a.group;
-  k.nrows = min(total - k.row0, rows);
-  k.lo = k.hi = k.t0 = k.tiles = 0;
-  if (k.row0 < 0 || k.nrows <= 0 || total < a.min_rows || total > a.max_rows) return k;
+  k.r = r;
+  k.s = s;
+  k.row0 = r * rows;
+  k.nrows = min(s.n * a.group - k.row0, rows);
   const int i0 = k.row0 / a.group, i1 = (k.row0 + k.nrows - 1) / a.group;
-  const int shift = k.s.kv - k.s.n;
+  const int shift = s.kv - s.n;
   k.hi = max(shift + i1 + 1, 0);
   k.lo = a.window > 0 ? max(shift + i0 - a.window + 1, 0) : 0;
   k.t0 = k.lo / tile;
@@ -85,60 +70,77 @@ MOL_DEV Block block_of(const AttnArgs& a, int v, int b, int rows, int tile) {
 }
 
 // What a launch does is counted in units: a block's tiles and `extra` more for what it takes to begin
-// and to end one. All units of the launch, in the order (block, head, unit), are dealt in even runs to
-// its thread blocks.
+// and to end one. All units of the launch, in the order (sequence, block, head, unit), are dealt in
+// even runs to its thread blocks.
 struct Place {  // where a thread block's run begins
   Block k;
-  int v, h, unit;
+  int h, unit;
 };
 struct Run {
-  int64_t total, grid, from, to;  // units of the launch, thread blocks that get some, this one's
+  int64_t total, from, to;  // units of the launch, this thread block's
+  int64_t share, longer;    // units a thread block; the first `longer` ones have one more
+  bool any;
+  MOL_DEV int64_t begin(int64_t c) const { return c * share + min(c, longer); }
+  // The thread block that has unit u.
+  MOL_DEV int owner(int64_t u) const {
+    const int64_t split = longer * (share + 1);
+    return (int)(u < split ? u / (share + 1) : longer + (u - split) / share);
+  }
 };
-MOL_DEV int block_units(const Block& k, int extra) { return k.tiles > 0 ? k.tiles + extra : 0; }
 
 // Every thread of a thread block of THREADS calls it; `sh` holds THREADS / 32 + 1 ints. *place is
-// written where the run is not empty.
+// written where the run is not empty. A thread a sequence: one round trip for their lengths.
 template <int THREADS>
 MOL_DEV Run deal(const AttnArgs& a, int rows, int tile, int extra, int* sh, Place* place) {
-  const int nv = num_blocks(a, rows);
+  if (threadIdx.x == 0) place->k.tiles = 0;
   Run run;
-  Block k = {};
-  int before = 0, sum = 0, n = 0;
+  Seq s = {};
+  int blocks = 0, before = 0, sum = 0, n = 0;
+  auto units = [&](int b) {
+    n = blocks = 0;
+    if (b >= a.num_seqs) return;
+    s = sequence(a, b);
+    blocks = num_blocks(a, s, rows);
+    for (int r = 0; r < blocks; ++r) n += block_of(a, b, s, r, rows, tile).tiles + extra;
+  };
   run.total = 0;
-  for (int v0 = 0; v0 < nv; v0 += THREADS) {
-    const int v = v0 + threadIdx.x;
-    n = 0;
-    if (v < nv) {
-      k = block_of(a, v, block_seq(a, v, rows), rows, tile);
-      n = block_units(k, extra);
-    }
+  for (int b0 = 0; b0 < a.num_seqs; b0 += THREADS) {
+    units(b0 + threadIdx.x);
     before = block_exclusive_scan<THREADS>(n, sh, sum);
     run.total += sum;
   }
   run.total *= a.kv_heads;
-  run.grid = min((int64_t)gridDim.x, run.total);
-  const int64_t c = blockIdx.x;
-  run.from = run.to = 0;
-  if (c >= run.grid) return run;
-  run.from = c * run.total / run.grid;
-  run.to = (c + 1) * run.total / run.grid;
+  const int64_t c = blockIdx.x, grid = gridDim.x;
+  if (run.total < (int64_t)1 << 31) {  // (a division of 64 bits takes a few times as long)
+    run.share = (uint32_t)run.total / (uint32_t)grid;
+    run.longer = (uint32_t)run.total % (uint32_t)grid;
+  } else {
+    run.share = run.total / grid;
+    run.longer = run.total % grid;
+  }
+  run.from = run.begin(c);
+  run.to = run.begin(c + 1);
+  run.any = run.from < run.to;
+  if (!run.any) return run;
   int64_t passed = 0;
-  for (int v0 = 0; v0 < nv && passed * a.kv_heads <= run.from; v0 += THREADS) {
-    const int v = v0 + threadIdx.x;
-    if (nv > THREADS) {  // (else as above)
-      n = 0;
-      if (v < nv) {
-        k = block_of(a, v, block_seq(a, v, rows), rows, tile);
-        n = block_units(k, extra);
-      }
+  for (int b0 = 0; b0 < a.num_seqs && passed * a.kv_heads <= run.from; b0 += THREADS) {
+    if (a.num_seqs > THREADS) {  // (else as above)
+      units(b0 + threadIdx.x);
       before = block_exclusive_scan<THREADS>(n, sh, sum);
     }
-    const int64_t first = (passed + before) * a.kv_heads, at = run.from - first;
-    if (n > 0 && at >= 0 && at < (int64_t)n * a.kv_heads) {
-      place->k = k;
-      place->v = v;
-      place->h = (int)(at / n);
-      place->unit = (int)(at % n);
+    int64_t at = run.from - (passed + before) * a.kv_heads;
+    if (at >= 0 && at < (int64_t)n * a.kv_heads) {
+      for (int r = 0; r < blocks; ++r) {
+        const Block k = block_of(a, b0 + threadIdx.x, s, r, rows, tile);
+        const int u = k.tiles + extra;
+        if (at < (int64_t)u * a.kv_heads) {
+          place->k = k;
+          place->h = (int)(at / u);
+          place->unit = (int)(at - (int64_t)place->h * u);
+          break;
+        }
+        at -= (int64_t)u * a.kv_heads;
+      }
     }
     passed += sum;
   }
@@ -150,18 +152,19 @@ MOL_DEV Run deal(const AttnArgs& a, int rows, int tile, int extra, int* sh, Plac
 template <int TILE, int EXTRA>
 struct Walk {
   Block k;
-  int rows, v, h;
+  int rows, h;
   int first, count;  // tiles of the block in the run
   int unit;
   int64_t left;      // units of the run from here on
-  MOL_DEV void start(const Place& p, int rows_, int64_t n) {
+  MOL_DEV void start(const AttnArgs& a, const Place& p, int rows_, const Run& run) {
     k = p.k;
     rows = rows_;
-    v = p.v;
     h = p.h;
     unit = p.unit;
-    left = n;
+    left = k.tiles > 0 ? run.to - run.from : 0;  // (0: starts that decrease; sums of units may mislead)
+    if (left == 0) return;
     cut();
+    if (count == 0) next(a);
   }
   MOL_DEV void cut() {
     const int n = (int)min((int64_t)(k.tiles + EXTRA - unit), left);
@@ -171,31 +174,30 @@ struct Walk {
   MOL_DEV bool more() const { return left > 0; }
   MOL_DEV bool ends() const { return first + count >= k.tiles; }
   // On to the next head or block; ones that the run has no tile of are passed by.
-  MOL_DEV void next(const AttnArgs& a, int nv) {
+  MOL_DEV void next(const AttnArgs& a) {
     do {
       left -= k.tiles + EXTRA - unit;
       if (left <= 0) return;
       unit = 0;
       if (++h == a.kv_heads) {
         h = 0;
-        int b = k.b;
-        do {
-          if (++v >= nv) {
+        int b = k.b, r = k.r + 1;
+        Seq s = k.s;
+        while (r >= num_blocks(a, s, rows)) {
+          if (++b >= a.num_seqs) {
             left = 0;
             return;
           }
-          while (b + 1 < a.num_seqs && first_block(a, b + 1, rows) <= v) ++b;
-          k = block_of(a, v, b, rows, TILE);
-        } while (k.tiles == 0);
+          s = sequence(a, b);
+          r = 0;
+        }
+        k = block_of(a, b, s, r, rows, TILE);
       }
       cut();
     } while (count == 0);
   }
   // The last thread block that has a tile of this block, which the run begins and does not end.
-  MOL_DEV int last(const Run& r) const {
-    const int64_t end = r.to + (k.tiles - first - count);
-    return (int)((end * r.grid + r.total - 1) / r.total) - 1;
-  }
+  MOL_DEV int last(const Run& r) const { return r.owner(r.to + (k.tiles - first - count) - 1); }
 };
 
 // Parts of blocks that several thread blocks share. Thread block c leaves the part that continues its

@@ -15,6 +15,7 @@ __device__ unsigned int g_many_fault_flags;
 namespace {
 
 using attn::Block;
+using attn::ex2;
 using attn::Parts;
 using attn::Place;
 using attn::Record;
@@ -134,11 +135,6 @@ MOL_DEV uint32_t tmem_ld_x1(uint32_t taddr) {
 MOL_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 MOL_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-MOL_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two fp32 values at a time.
 MOL_DEV float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -244,12 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (each role begins its own, from shared memory: nothing of it is held in registers before)
   auto begin = [&](attn::Walk<kM, kExtra>& w) {
     w.left = 0;
-    if (blockIdx.x < s_run.grid) {
-      w.start(s_place, rows, s_run.to - s_run.from);
-      if (w.count == 0) w.next(a, attn::num_blocks(a, rows));
-    }
+    if (s_run.any) w.start(a, s_place, rows, s_run);
   };
-  auto next = [&](attn::Walk<kM, kExtra>& w) { w.next(a, attn::num_blocks(a, rows)); };
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -259,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
     const int copies = kM / per;
     attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; next(w)) {
+    for (begin(w); w.more() && !fault; w.next(a)) {
       const Block& k = w.k;
       if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
         fault = true;
@@ -328,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&s_full[t]);
       };
       attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; next(w)) {
+    for (begin(w); w.more() && !fault; w.next(a)) {
         const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
         ++seg;
         if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
@@ -392,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Record record = {};
     record.last = -1;
     attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; next(w)) {
+    for (begin(w); w.more() && !fault; w.next(a)) {
       const Block& k = w.k;
       const int count = w.count;
       const bool begins = w.first == 0, part = !begins || !w.ends();

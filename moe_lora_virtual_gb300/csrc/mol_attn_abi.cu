@@ -165,6 +165,10 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
       num_tokens * num_q_heads >= (int64_t)1 << 31 ||
       (int64_t)max_pages * cache->page_size >= (int64_t)1 << 31)
     return MOL_ERR_UNSUPPORTED;
+  // the tiles of a head are counted in 32 bits
+  const int64_t rows = num_tokens * (num_q_heads / cache->num_heads);
+  if ((rows / 16 + num_seqs) * ((int64_t)max_pages * cache->page_size / 64 + 4) >= (int64_t)1 << 31)
+    return MOL_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return MOL_OK;
   if (!kv_lens || (max_pages > 0 && !page_table)) return MOL_ERR_INVALID_ARG;
   MOL_TRY(check_heads(q, q_token_stride, q_head_stride, num_tokens, num_q_heads, d));
