@@ -57,7 +57,7 @@ struct Geo {
 // holds; where a row does not see a token that another one sees, the step's values are looked
 // through, and summed without the tensor cores should one not be finite (0 * NaN is NaN there).
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kernel(const __grid_constant__ AttnArgs a) {
   using G = Geo<D, MT>;
   constexpr int kChunks = D / 8;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     return;
   }
   constexpr int kStep = G::kStep;
-  attn::Walk<G::kTile, kExtra> load, work;
-  load.start(a, s_place, G::kRows, run);
+  attn::Walk load, work;  // over the run, of the copies and of the products
+  attn::begin(a, load, s_place, run, G::kRows, G::kTile, kExtra);
   work = load;
   int load_tile = 0;  // of load.count
 
@@ -93,22 +93,23 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     if (!load.more()) return t;
     const int j = (load.k.t0 + load.first + load_tile) * G::kTile + warp * kStep + lane % kStep;
     if (j >= load.k.lo && j < load.k.hi) {
-      const int p = j / a.page_size;
+      const int p = attn::divide(j, a.by_page);
       t.page = __ldg(a.page_table + load.k.b * a.table_stride + p);
       t.offset = j - p * a.page_size;
     }
     if (++load_tile == load.count) {
-      load.next(a);
+      attn::go_on(a, load, G::kRows, G::kTile, kExtra);
       load_tile = 0;
     }
     return t;
   };
-  Token ahead[2] = {look(), look()};
-  // Asks for the next step into ring stage s.
+  Token ahead[2];
+  // Asks for the next step into ring stage s; for a negative one only for its pages.
   auto fetch = [&](int s) {
     const Token t = ahead[0];
     ahead[0] = ahead[1];
     ahead[1] = look();
+    if (s < 0) return;
     const bool held = t.page >= 0 && t.page < a.num_pages;
     const int64_t at = held ? t.page * a.page_stride + t.offset * a.token_stride + t.h * a.head_stride : 0;
     const uint32_t mask = __ballot_sync(0xffffffffu, held);
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     cp_async_commit();
   };
 #pragma unroll 1
-  for (int s = 0; s < G::kStages - 1; ++s) fetch(s);
+  for (int s = -2; s < G::kStages - 1; ++s) fetch(s);
 
   const int g = lane >> 2, t4 = lane & 3;
   int stage = 0;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
       const int row = (i * kThreads + tid) / kChunks, ch = (i * kThreads + tid) % kChunks;
       query[i] = make_uint4(0, 0, 0, 0);
       if (row < k.nrows) {
-        const int r = k.row0 + row, token = r / a.group;
+        const int r = k.row0 + row, token = attn::divide(r, a.by_group);
         query[i] = __ldg(reinterpret_cast<const uint4*>(
             a.q + (int64_t)(k.s.start + token) * a.q_token_stride +
             (int64_t)(h * a.group + r - token * a.group) * a.q_head_stride + ch * 8));
@@ -156,10 +157,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
   Record record = {};
   record.last = -1;
   if (work.more()) ask_queries(work.k, work.h);
+#pragma unroll 1
   while (work.more()) {
     // ------------------------------------------------------------ a block of rows and a head
-    const Block& k = work.k;
-    const int h = work.h;
+    const Block k = work.k;
+    const int h = work.h, first = work.first, count = work.count;
     put_queries();
     __syncthreads();
     auto load_q = [&](int mt, int kk, uint32_t (&r)[4]) {
@@ -179,9 +181,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        pos[mt][i] = k.s.kv - k.s.n + (k.row0 + min(mt * 16 + g + 8 * i, k.nrows - 1)) / a.group;
-    const int pos_first = k.s.kv - k.s.n + k.row0 / a.group;
-    const int pos_last = k.s.kv - k.s.n + (k.row0 + k.nrows - 1) / a.group;
+        pos[mt][i] = k.s.kv - k.s.n + attn::divide(k.row0 + min(mt * 16 + g + 8 * i, k.nrows - 1), a.by_group);
+    const int pos_first = k.s.kv - k.s.n + attn::divide(k.row0, a.by_group);
+    const int pos_last = k.s.kv - k.s.n + attn::divide(k.row0 + k.nrows - 1, a.by_group);
 
     float o[MT][D / 8][4];
     float top[MT][2], sum[MT][2];
@@ -192,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
-    for (int tile = work.first; tile < work.first + work.count; ++tile) {
+#pragma unroll 1
+    for (int tile = first; tile < first + count; ++tile) {
       cp_async_wait_group<G::kStages - 2>();
       __syncwarp();  // the step has landed, and the stage before it is free, for every lane
       fetch(stage == 0 ? G::kStages - 1 : stage - 1);
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
         bool plain = false;
         if (edge) {
           bool bad = false;
+#pragma unroll 4
           for (int i = lane; i < kStep * kChunks; i += 32) {
             bad |= attn::not_finite(lds16(vt + i * 16));
           }
@@ -343,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     }
 
     // ------------------------------------------------------------ the warps' sums become one
-    const bool begins = work.first == 0, part = !begins || !work.ends();
+    const bool begins = first == 0, part = !begins || !work.ends();
     const int slot = (int)(2 * c) + (begins ? 1 : 0);
     const int start = k.s.start, row0 = k.row0, nrows = k.nrows;
     if (begins && part && tid == 0) record = {work.last(run), start, row0, nrows, h, {}};
-    work.next(a);
+    attn::go_on(a, work, G::kRows, G::kTile, kExtra);
     if (work.more()) ask_queries(work.k, work.h);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -373,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
             *reinterpret_cast<float2*>(mine + (mt * 16 - row_m + g + 8 * i) * (D * 4) + ((n ^ g) << 5) +
                                        t4 * 8) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
       __syncthreads();
+#pragma unroll 1
       for (int i = tid; i < G::kMeet * (D / 4); i += kThreads) {
         const int local = i / (D / 4), row = row_m + local, col = i % (D / 4) * 4;
         if (row >= nrows) break;
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
           *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
           if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
         } else {
-          const int r = row0 + row, token = r / a.group;
+          const int r = row0 + row, token = attn::divide(r, a.by_group);
           const float inv = m == -INFINITY ? 0.f : 1.f / l;
           *reinterpret_cast<uint2*>(a.out + (int64_t)(start + token) * a.out_token_stride +
                                     (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
@@ -467,7 +472,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
     }
   }
   if (!has) return;
-  const int r = rec.row0 + row, token = r / a.group;
+  const int r = rec.row0 + row, token = attn::divide(r, a.by_group);
   const float inv = m == -INFINITY ? 0.f : 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t)(rec.start + token) * a.out_token_stride +
                                               (int64_t)(rec.h * a.group + r - token * a.group) *
@@ -477,9 +482,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
 }
 
 template <int D, int MT>
-cudaError_t attend_few(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t attend_few(const AttnArgs& args, cudaStream_t stream) {
   using G = Geo<D, MT>;
   const int grid = attn::sms() * G::kPerSM;
+  AttnArgs a = args;
+  a.by_grid = divider(grid);
   const cudaError_t e = launch_pdl(attend_few_kernel<D, MT>, dim3(grid), dim3(kThreads), G::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   return attn::launch_join(a, grid, G::kRows, attn::parts(a.workspace, grid, G::kRows, D), stream);

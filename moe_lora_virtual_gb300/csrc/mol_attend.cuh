@@ -22,21 +22,27 @@ MOL_DEV float ex2(float x) {  // 2^x, within 2^-22 of it; 0 for -infinity
   return y;
 }
 
+MOL_DEV int divide(int n, const Divider& d) {
+  const uint32_t t = __umulhi(d.mul, (uint32_t)n);
+  return (int)((t + (((uint32_t)n - t) >> d.s1)) >> d.s2);
+}
+
 // One sequence of the call: its first row of q, its rows, its cached tokens. Whatever the caller's
 // arrays hold, rows stay within the call's and tokens within the page table.
 struct Seq {
   int start, n, kv;
 };
-MOL_DEV int seq_start(const AttnArgs& a, int b) {
-  if (!a.q_starts) return b;
-  return min(max(__ldg(a.q_starts + b), 0), a.num_tokens);
+// From its first row and what the arrays say of its end and its tokens.
+MOL_DEV Seq sequence(const AttnArgs& a, int start, int end, int kv) {
+  Seq s;
+  s.start = start;
+  s.n = a.q_starts ? max(min(max(end, 0), a.num_tokens) - start, 0) : 1;
+  s.kv = min(max(kv, 0), a.max_pages * a.page_size);
+  return s;
 }
 MOL_DEV Seq sequence(const AttnArgs& a, int b) {
-  Seq s;
-  s.start = seq_start(a, b);
-  s.n = a.q_starts ? max(seq_start(a, b + 1) - s.start, 0) : 1;
-  s.kv = min(max(__ldg(a.kv_lens + b), 0), a.max_pages * a.page_size);
-  return s;
+  const int start = a.q_starts ? min(max(__ldg(a.q_starts + b), 0), a.num_tokens) : b;
+  return sequence(a, start, a.q_starts ? __ldg(a.q_starts + b + 1) : 0, __ldg(a.kv_lens + b));
 }
 
 // A sequence's rows (new tokens x the group's query heads, row = token * group + head) are cut into
@@ -60,7 +66,7 @@ MOL_DEV Block block_of(const AttnArgs& a, int b, const Seq& s, int r, int rows, 
   k.s = s;
   k.row0 = r * rows;
   k.nrows = min(s.n * a.group - k.row0, rows);
-  const int i0 = k.row0 / a.group, i1 = (k.row0 + k.nrows - 1) / a.group;
+  const int i0 = divide(k.row0, a.by_group), i1 = divide(k.row0 + k.nrows - 1, a.by_group);
   const int shift = s.kv - s.n;
   k.hi = max(shift + i1 + 1, 0);
   k.lo = a.window > 0 ? max(shift + i0 - a.window + 1, 0) : 0;
@@ -78,127 +84,141 @@ struct Place {  // where a thread block's run begins
 };
 struct Run {
   int64_t total, from, to;  // units of the launch, this thread block's
-  int64_t share, longer;    // units a thread block; the first `longer` ones have one more
+  int64_t share;            // units a thread block; the first `longer` ones have one more
+  int longer;
   bool any;
-  MOL_DEV int64_t begin(int64_t c) const { return c * share + min(c, longer); }
-  // The thread block that has unit u.
-  MOL_DEV int owner(int64_t u) const {
-    const int64_t split = longer * (share + 1);
-    return (int)(u < split ? u / (share + 1) : longer + (u - split) / share);
+  MOL_DEV int64_t begin(int c) const { return c * share + min(c, longer); }
+  // The thread block that has the unit x behind this one's run.
+  MOL_DEV int owner(uint32_t x) const {
+    const int c = blockIdx.x + 1;
+    const uint32_t one = (uint32_t)min(share, (int64_t)0x7fffffff);  // (more than any x)
+    const int64_t span = c < longer ? (int64_t)(longer - c) * (share + 1) : 0;
+    return x < span ? c + (int)(x / (one + 1)) : max(c, longer) + (int)((x - (uint32_t)span) / one);
   }
 };
 
 // Every thread of a thread block of THREADS calls it; `sh` holds THREADS / 32 + 1 ints. *place is
-// written where the run is not empty. A thread a sequence: one round trip for their lengths.
+// written where the run is not empty. A thread a sequence: one round trip for their lengths. (The
+// kernels' code comes from memory when they start, so what is not hot is kept small.)
 template <int THREADS>
 MOL_DEV Run deal(const AttnArgs& a, int rows, int tile, int extra, int* sh, Place* place) {
   if (threadIdx.x == 0) place->k.tiles = 0;
   Run run;
   Seq s = {};
   int blocks = 0, before = 0, sum = 0, n = 0;
-  auto units = [&](int b) {
-    n = blocks = 0;
-    if (b >= a.num_seqs) return;
-    s = sequence(a, b);
-    blocks = num_blocks(a, s, rows);
-    for (int r = 0; r < blocks; ++r) n += block_of(a, b, s, r, rows, tile).tiles + extra;
-  };
-  run.total = 0;
-  for (int b0 = 0; b0 < a.num_seqs; b0 += THREADS) {
-    units(b0 + threadIdx.x);
-    before = block_exclusive_scan<THREADS>(n, sh, sum);
-    run.total += sum;
-  }
-  run.total *= a.kv_heads;
-  const int64_t c = blockIdx.x, grid = gridDim.x;
-  if (run.total < (int64_t)1 << 31) {  // (a division of 64 bits takes a few times as long)
-    run.share = (uint32_t)run.total / (uint32_t)grid;
-    run.longer = (uint32_t)run.total % (uint32_t)grid;
-  } else {
-    run.share = run.total / grid;
-    run.longer = run.total % grid;
-  }
-  run.from = run.begin(c);
-  run.to = run.begin(c + 1);
-  run.any = run.from < run.to;
-  if (!run.any) return run;
   int64_t passed = 0;
-  for (int b0 = 0; b0 < a.num_seqs && passed * a.kv_heads <= run.from; b0 += THREADS) {
-    if (a.num_seqs > THREADS) {  // (else as above)
-      units(b0 + threadIdx.x);
-      before = block_exclusive_scan<THREADS>(n, sh, sum);
-    }
-    int64_t at = run.from - (passed + before) * a.kv_heads;
-    if (at >= 0 && at < (int64_t)n * a.kv_heads) {
+  run.total = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {  // the sum of all units, then where the run begins
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.num_seqs; b0 += THREADS) {
+      const int b = b0 + threadIdx.x;
+      if (pass == 0 || a.num_seqs > THREADS) {
+        n = blocks = 0;
+        if (b < a.num_seqs) {
+          s = sequence(a, b);
+          blocks = num_blocks(a, s, rows);
+#pragma unroll 1
+          for (int r = 0; r < blocks; ++r) n += block_of(a, b, s, r, rows, tile).tiles + extra;
+        }
+        before = block_exclusive_scan<THREADS>(n, sh, sum);
+      }
+      if (pass == 0) {
+        run.total += sum;
+        continue;
+      }
+      int64_t at = run.from - (passed + before) * a.kv_heads;
+      passed += sum;
+      if (at < 0 || at >= (int64_t)n * a.kv_heads) continue;
+#pragma unroll 1
       for (int r = 0; r < blocks; ++r) {
-        const Block k = block_of(a, b0 + threadIdx.x, s, r, rows, tile);
+        const Block k = block_of(a, b, s, r, rows, tile);
         const int u = k.tiles + extra;
         if (at < (int64_t)u * a.kv_heads) {
           place->k = k;
-          place->h = (int)(at / u);
+          place->h = at >> 32 ? (int)(at / u) : (int)((uint32_t)at / (uint32_t)u);
           place->unit = (int)(at - (int64_t)place->h * u);
           break;
         }
         at -= (int64_t)u * a.kv_heads;
       }
     }
-    passed += sum;
+    if (pass == 0) {
+      run.total *= a.kv_heads;  // (below 2^47; thread blocks below 2^9)
+      const int high = divide((int)(run.total >> 20), a.by_grid);
+      const int rest = ((int)(run.total >> 20) - high * (int)gridDim.x) << 20 | (int)(run.total & 0xfffff);
+      const int low = divide(rest, a.by_grid);
+      run.share = ((int64_t)high << 20) + low;
+      run.longer = rest - low * (int)gridDim.x;
+      run.from = run.begin(blockIdx.x);
+      run.to = run.begin(blockIdx.x + 1);
+      run.any = run.from < run.to;
+      if (!run.any) return run;
+    }
   }
   __syncthreads();
   return run;
 }
 
 // A walk over a thread block's run, a block's head at a time.
-template <int TILE, int EXTRA>
 struct Walk {
   Block k;
-  int rows, h;
+  int h;
   int first, count;  // tiles of the block in the run
   int unit;
   int64_t left;      // units of the run from here on
-  MOL_DEV void start(const AttnArgs& a, const Place& p, int rows_, const Run& run) {
-    k = p.k;
-    rows = rows_;
-    h = p.h;
-    unit = p.unit;
-    left = k.tiles > 0 ? run.to - run.from : 0;  // (0: starts that decrease; sums of units may mislead)
-    if (left == 0) return;
-    cut();
-    if (count == 0) next(a);
-  }
-  MOL_DEV void cut() {
-    const int n = (int)min((int64_t)(k.tiles + EXTRA - unit), left);
-    first = max(unit - EXTRA, 0);
-    count = max(unit + n - EXTRA, 0) - first;
-  }
+  int kv1, end1;     // what the caller's arrays say of the sequence behind this one, asked for ahead
   MOL_DEV bool more() const { return left > 0; }
   MOL_DEV bool ends() const { return first + count >= k.tiles; }
-  // On to the next head or block; ones that the run has no tile of are passed by.
-  MOL_DEV void next(const AttnArgs& a) {
-    do {
-      left -= k.tiles + EXTRA - unit;
-      if (left <= 0) return;
-      unit = 0;
-      if (++h == a.kv_heads) {
-        h = 0;
-        int b = k.b, r = k.r + 1;
-        Seq s = k.s;
-        while (r >= num_blocks(a, s, rows)) {
-          if (++b >= a.num_seqs) {
-            left = 0;
-            return;
-          }
-          s = sequence(a, b);
-          r = 0;
-        }
-        k = block_of(a, b, s, r, rows, TILE);
-      }
-      cut();
-    } while (count == 0);
-  }
   // The last thread block that has a tile of this block, which the run begins and does not end.
-  MOL_DEV int last(const Run& r) const { return r.owner(r.to + (k.tiles - first - count) - 1); }
+  MOL_DEV int last(const Run& r) const { return r.owner((uint32_t)(k.tiles - first - count) - 1); }
 };
+MOL_DEV void cut(Walk& w, int extra) {
+  const int n = (int)min((int64_t)(w.k.tiles + extra - w.unit), w.left);
+  w.first = max(w.unit - extra, 0);
+  w.count = max(w.unit + n - extra, 0) - w.first;
+}
+MOL_DEV void peek(const AttnArgs& a, Walk& w) {
+  w.kv1 = w.end1 = 0;
+  if (w.k.b + 1 >= a.num_seqs) return;
+  w.kv1 = __ldg(a.kv_lens + w.k.b + 1);
+  if (a.q_starts) w.end1 = __ldg(a.q_starts + w.k.b + 2);
+}
+// On to the next head or block; ones that the run has no tile of are passed by.
+MOL_DEV void go_on(const AttnArgs& a, Walk& w, int rows, int tile, int extra) {
+#pragma unroll 1
+  do {
+    w.left -= w.k.tiles + extra - w.unit;
+    if (w.left <= 0) return;
+    w.unit = 0;
+    if (++w.h == a.kv_heads) {
+      w.h = 0;
+      int r = w.k.r + 1;
+#pragma unroll 1
+      while (r >= num_blocks(a, w.k.s, rows)) {
+        if (++w.k.b >= a.num_seqs) {
+          w.left = 0;
+          return;
+        }
+        w.k.s = sequence(a, w.k.s.start + w.k.s.n, w.end1, w.kv1);
+        peek(a, w);
+        r = 0;
+      }
+      w.k = block_of(a, w.k.b, w.k.s, r, rows, tile);
+    }
+    cut(w, extra);
+  } while (w.count == 0);
+}
+MOL_DEV void begin(const AttnArgs& a, Walk& w, const Place& p, const Run& run, int rows, int tile, int extra) {
+  w.k = p.k;
+  w.h = p.h;
+  w.unit = p.unit;
+  w.left = p.k.tiles > 0 ? run.to - run.from : 0;  // (0: starts that decrease; sums may mislead)
+  if (w.left == 0) return;
+  peek(a, w);
+  cut(w, extra);
+  if (w.count == 0) go_on(a, w, rows, tile, extra);
+}
 
 // Parts of blocks that several thread blocks share. Thread block c leaves the part that continues its
 // predecessor's block in slot 2c, the one that it begins and does not end in slot 2c + 1 with a

@@ -7,6 +7,20 @@
 
 namespace mol {
 
+// Division of a 32-bit number by one that a launch knows, with a multiplication (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994): a few instructions where the
+// compiler's take two dozen, in kernels whose code has to come from memory first.
+struct Divider {
+  uint32_t d, mul;
+  int s1, s2;
+};
+inline Divider divider(uint32_t d) {
+  int l = 0;
+  while (l < 32 && ((uint64_t)1 << l) < d) ++l;
+  const uint32_t mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
+  return {d, mul, l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+}
+
 struct HeadRows {  // heads of bf16 values: x + token * token_stride + head * head_stride
   const void* x;
   int64_t token_stride, head_stride;
@@ -38,6 +52,7 @@ struct AttnArgs {
   const uint16_t* v;
   int64_t page_stride, token_stride, head_stride;
   int num_pages, page_size, kv_heads, group, head_dim;
+  Divider by_page, by_group, by_grid;  // by_grid: the launch's thread blocks
   const int32_t* page_table;
   int64_t table_stride;
   int max_pages;

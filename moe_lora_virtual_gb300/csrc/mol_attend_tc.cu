@@ -238,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   bool fault = false;
   // (each role begins its own, from shared memory: nothing of it is held in registers before)
-  auto begin = [&](attn::Walk<kM, kExtra>& w) {
+  auto begin = [&](attn::Walk& w) {
     w.left = 0;
-    if (s_run.any) w.start(a, s_place, rows, s_run);
+    if (s_run.any) attn::begin(a, w, s_place, s_run, rows, kM, kExtra);
   };
+  auto next = [&](attn::Walk& w) { attn::go_on(a, w, rows, kM, kExtra); };
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -250,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t u = 0, n = 0, seg = 0;  // ring slots used, tiles, blocks
     const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
     const int copies = kM / per;
-    attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; w.next(a)) {
+    attn::Walk w;
+    for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
         fault = true;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < (two ? 2 : 1); ++t)
           for (int x = 0; x < D / 64; ++x)
             tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
-                        k.s.start + k.row0 / a.group + t * tile_tokens, &q_full);
+                        k.s.start + attn::divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
       }
       ++seg;
       for (int i = 0; i < w.count && !fault; ++i, ++n) {
@@ -273,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = j0 + lane * per;
         int page = -1;
         if (lane < copies && j + per > k.lo && j < k.hi)
-          page = __ldg(a.page_table + k.b * a.table_stride + j / a.page_size);
+          page = __ldg(a.page_table + k.b * a.table_stride + attn::divide(j, a.by_page));
         const bool held = page >= 0 && page < a.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, held);
         if (!held) page = a.num_pages;  // past the end: zeros
-        const int offset = j % a.page_size;
+        const int offset = j - attn::divide(j, a.by_page) * a.page_size;
         if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
         for (int kv = 0; kv < 2; ++kv, ++u) {
           const int s = (int)(u % G::kSlots);
@@ -319,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&s_full[t]);
         mbar_arrive(&s_full[t]);
       };
-      attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; w.next(a)) {
+      attn::Walk w;
+    for (begin(w); w.more() && !fault; next(w)) {
         const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
         ++seg;
         if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
@@ -383,16 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, n = 0, u = 0, no = 0, edges = 0;
     Record record = {};
     record.last = -1;
-    attn::Walk<kM, kExtra> w;
-    for (begin(w); w.more() && !fault; w.next(a)) {
+    attn::Walk w;
+    for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       const int count = w.count;
       const bool begins = w.first == 0, part = !begins || !w.ends();
       const int in_tile = min(k.nrows - t * tile_rows, tile_rows);  // rows of this query tile
       if (in_tile > 0) {
         const int shift = k.s.kv - k.s.n, row = k.row0 + t * tile_rows;
-        const int pos = shift + (row + min(local, in_tile - 1)) / a.group;
-        const int pos_first = shift + row / a.group, pos_last = shift + (row + in_tile - 1) / a.group;
+        const int pos = shift + attn::divide(row + min(local, in_tile - 1), a.by_group);
+        const int pos_first = shift + attn::divide(row, a.by_group);
+        const int pos_last = shift + attn::divide(row + in_tile - 1, a.by_group);
         float top = -INFINITY, sum = 0.f;
         for (int i = 0; i < count; ++i) {
           const int j0 = (k.t0 + w.first + i) * kM;
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- the rows, or a part of them
         const int slot = 2 * (int)blockIdx.x + (begins ? 1 : 0);
         const bool mine = local < in_tile;
-        const int at = t * tile_rows + local, r = k.row0 + at, token = r / a.group;
+        const int at = t * tile_rows + local, r = k.row0 + at, token = attn::divide(r, a.by_group);
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;
@@ -605,7 +607,7 @@ bool encode(CUtensorMap* map, const void* p, const cuuint64_t (&dims)[4], const 
 }
 
 template <int D>
-cudaError_t many(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int tokens = kM / a.group, per = std::min(a.page_size, kM);
   CUtensorMap q, k, v;
   const cuuint64_t page_dims[4] = {(cuuint64_t)D, (cuuint64_t)a.page_size, (cuuint64_t)a.kv_heads,
@@ -618,6 +620,7 @@ cudaError_t many(const AttnArgs& a, cudaStream_t stream) {
       !encode(&v, a.v, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}))
     return cudaErrorInvalidValue;
   const int grid = attn::sms(), rows = 2 * tokens * a.group;
+  a.by_grid = divider(grid);
   const cudaError_t e = launch_pdl(attend_many_kernel<D>, dim3(grid), dim3(kThreads), Geo<D>::kSmem, stream, q,
                                    k, v, a, tokens);
   if (e != cudaSuccess) return e;

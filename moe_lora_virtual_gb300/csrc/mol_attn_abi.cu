@@ -192,6 +192,8 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
   a.kv_heads = cache->num_heads;
   a.group = group;
   a.head_dim = d;
+  a.by_page = mol::divider((uint32_t)cache->page_size);
+  a.by_group = mol::divider((uint32_t)group);
   a.page_table = page_table;
   a.table_stride = table_stride;
   a.max_pages = max_pages;
