@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
   pdl_wait();
   pdl_launch_dependents();
   const Parts parts = attn::parts(a.workspace, gridDim.x, G::kRows, D);
+  attn::prefetch_table<kThreads>(a);
   const attn::Run run = attn::deal<kThreads>(a, G::kRows, G::kTile, kExtra, s_scan, &s_place);
   const int64_t c = blockIdx.x;
   if (!run.any) {
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     }
     return t;
   };
-  Token ahead[2];
+  Token ahead[2] = {{-1, 0, 0}, {-1, 0, 0}};
   // Asks for the next step into ring stage s; for a negative one only for its pages.
   auto fetch = [&](int s) {
     const Token t = ahead[0];
@@ -419,15 +420,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
 
 constexpr int kJoinWarps = 8;
 
-// WAYS warps a row, its columns over their lanes: each takes every WAYS-th part, a later warp's sum is
-// added to an earlier one's. Every part is read once; a chain of four dependent loads (record,
-// maxima, parts) is what it costs.
+// WAYS warps a row, its columns over their lanes: each takes every WAYS-th part, and the first adds what
+// they have. Every part is read once; a launch and two round trips (record, parts) are what it costs.
 template <int D, int WAYS>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int rows, Parts p) {
   constexpr int kPer = D / 32;  // columns a lane
   constexpr int kRows = kJoinWarps / WAYS;
   __shared__ float s_sum[WAYS > 1 ? kRows : 1][WAYS][D];
-  __shared__ float s_weight[kRows][WAYS];
+  __shared__ float2 s_top[kRows][WAYS];
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -439,36 +439,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
 #pragma unroll
   for (int e = 0; e < kPer; ++e) x[e] = 0.f;
   if (has) {
-    for (int i = c + lane; i <= rec.last; i += 32)
-      m = fmaxf(m, p.tops[(int64_t)(2 * i + (i == c)) * rows + row].x);
+    // (maxima and sums of four parts asked for together)
+#pragma unroll 1
+    for (int i0 = c + way; i0 <= rec.last; i0 += 4 * WAYS) {
+      float2 t[4], v[4][kPer / 2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-    for (int i = c + way; i <= rec.last; i += WAYS) {
-      const int64_t at = (int64_t)(2 * i + (i == c)) * rows + row;
-      const float2 t = p.tops[at];
-      const float f = t.x == -INFINITY ? 0.f : attn::ex2(t.x - m);
-      l += f * t.y;
-      const float* v = p.sums + at * D + lane * kPer;
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * WAYS;
+        const int64_t at = (int64_t)(2 * i + (i == c)) * rows + row;
+        t[j] = i <= rec.last ? p.tops[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 w = *reinterpret_cast<const float2*>(v + e);
-        x[e] += f * w.x;
-        x[e + 1] += f * w.y;
+        for (int e = 0; e < kPer / 2; ++e)
+          v[j][e] = i <= rec.last ? reinterpret_cast<const float2*>(p.sums + at * D + lane * kPer)[e]
+                                  : make_float2(0.f, 0.f);
+      }
+      float now = m;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) now = fmaxf(now, t[j].x);
+      const float base = now == -INFINITY ? 0.f : now, f = attn::ex2(m - base);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float fj = attn::ex2(t[j].x - base);
+        l += fj * t[j].y;
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) {
+          x[2 * e] += fj * v[j][e].x;
+          x[2 * e + 1] += fj * v[j][e].y;
+        }
       }
     }
   }
   if constexpr (WAYS > 1) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) s_sum[local][way][lane * kPer + e] = x[e];
-    if (lane == 0) s_weight[local][way] = l;
+    if (lane == 0) s_top[local][way] = make_float2(m, l);
     __syncthreads();
     if (way > 0) return;
 #pragma unroll
-    for (int w = 1; w < WAYS; ++w) {
+    for (int w = 0; w < WAYS; ++w) m = fmaxf(m, s_top[local][w].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    l = 0.f;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[e] += s_sum[local][w][lane * kPer + e];
-      l += s_weight[local][w];
+    for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) {
+      const float f = attn::ex2(s_top[local][w].x - base);
+      l += f * s_top[local][w].y;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] += f * s_sum[local][w][lane * kPer + e];
     }
   }
   if (!has) return;
@@ -534,38 +556,39 @@ cudaError_t prepare_attn_kernels() {
   return e;
 }
 
-// Rows that one of attend_few's blocks holds.
-constexpr int kFewRows = 32;
+// The form for the rows (new tokens x group) that a sequence has on average, all that the host knows: one
+// launch for all sequences, whatever each has. Measured with 8 key heads, group 1 to 8, 4 to 100 sequences
+// (us for attend_few in blocks of 16 rows | of 32 | attend_many; 16 sequences of 4000 tokens):
+//   64 values a head:  12 rows 32 | 40 | 54, 16 rows 33 | 40 | 54, 24 rows 49 | 41 | 54, 48 rows 65 | 68 | 55
+//   128 values:        12 rows 52 | 66 | 61, 16 rows 52 | 66 | 61, 24 rows 91 | 68 | 61, 48 rows 131 | 119 | 62
+// A call with both of decoding sequences and prompts pays: 200 rows of one sequence in blocks of 16 read its
+// keys 13 times (from L2). Pages that attend_many cannot copy, and 256 values a head, take blocks of 16 and 32.
+enum class Form { kFew16, kFew32, kMany };
+static Form form(int64_t num_seqs, int64_t rows, int num_pages, int page_size, int head_dim) {
+  if (rows <= 16 * num_seqs || head_dim == 256) return Form::kFew16;
+  if (num_pages == 0 || !attn::many_fits(page_size, head_dim)) return Form::kFew32;
+  return head_dim == 64 && rows <= 32 * num_seqs ? Form::kFew32 : Form::kMany;
+}
 
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
   if (num_seqs <= 0 || num_tokens <= 0) return 0;
-  const size_t few = attn::parts_bytes(304, kFewRows, head_dim);
-  return num_tokens * group > kFewRows ? std::max(few, attn::many_bytes(group, head_dim)) : few;
+  const int64_t rows = num_tokens * group;
+  if (rows <= 16 * num_seqs || head_dim == 256) return attn::parts_bytes(attn::kMaxGrid, 16, head_dim);
+  // (whatever the pages)
+  return std::max(attn::parts_bytes(attn::kMaxGrid, 32, head_dim), attn::many_bytes(group, head_dim));
 }
 
-static cudaError_t launch_few(const AttnArgs& a, cudaStream_t stream) {
-  const bool wide = (a.q_starts ? (int64_t)a.num_tokens : 1) * a.group > 16;
-  if (a.head_dim == 64) return wide ? attend_few<64, 2>(a, stream) : attend_few<64, 1>(a, stream);
-  if (a.head_dim == 128) return wide ? attend_few<128, 2>(a, stream) : attend_few<128, 1>(a, stream);
-  return attend_few<256, 1>(a, stream);
-}
-
-cudaError_t launch_attention(const AttnArgs& args, cudaStream_t stream) {
-  AttnArgs a = args;
-  a.min_rows = 1;
-  a.max_rows = 0x7fffffff;
-  const int64_t rows = (int64_t)a.num_tokens * a.group;
-  const int64_t most = a.q_starts ? rows : a.group;  // of one sequence
-  if (most <= kFewRows || a.num_pages == 0 || !attn::many_fits(a.page_size, a.head_dim)) return launch_few(a, stream);
-  // The lengths are the device's: where sequences have many rows on average all take the form for
-  // many, else each the one for its own.
-  if (!a.q_starts || rows >= 128 * (int64_t)a.num_seqs) return attn::launch_many(a, stream);
-  a.max_rows = kFewRows;
-  const cudaError_t e = launch_few(a, stream);
-  if (e != cudaSuccess) return e;
-  a.min_rows = kFewRows + 1;
-  a.max_rows = 0x7fffffff;
-  return attn::launch_many(a, stream);
+cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
+  switch (form(a.num_seqs, (int64_t)a.num_tokens * a.group, a.num_pages, a.page_size, a.head_dim)) {
+    case Form::kMany:
+      return attn::launch_many(a, stream);
+    case Form::kFew32:
+      return a.head_dim == 64 ? attend_few<64, 2>(a, stream) : attend_few<128, 2>(a, stream);
+    default:
+      return a.head_dim == 64    ? attend_few<64, 1>(a, stream)
+             : a.head_dim == 128 ? attend_few<128, 1>(a, stream)
+                                 : attend_few<256, 1>(a, stream);
+  }
 }
 
 cudaError_t take_attn_checks(unsigned long long* first, unsigned long long* count) {

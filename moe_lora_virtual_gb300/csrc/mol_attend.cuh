@@ -54,10 +54,8 @@ struct Block {
   int lo, hi;       // tokens that some row sees lie in [lo, hi)
   int t0, tiles;    // tiles of them (one, with nothing in it, where there are none)
 };
-// Blocks of a sequence; none where it is another launch's.
 MOL_DEV int num_blocks(const AttnArgs& a, const Seq& s, int rows) {
-  const int total = s.n * a.group;
-  return total < a.min_rows || total > a.max_rows ? 0 : (total + rows - 1) / rows;
+  return (s.n * a.group + rows - 1) / rows;
 }
 MOL_DEV Block block_of(const AttnArgs& a, int b, const Seq& s, int r, int rows, int tile) {
   Block k;
@@ -160,6 +158,15 @@ MOL_DEV Run deal(const AttnArgs& a, int rows, int tile, int extra, int* sh, Plac
   return run;
 }
 
+// Asks L2 for the page table, a line a thread over all thread blocks, while the runs are dealt: the first
+// copies wait for their pages, which come from memory otherwise. (Of a larger table its beginning.)
+template <int THREADS>
+MOL_DEV void prefetch_table(const AttnArgs& a) {
+  const int64_t at = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * 32;
+  const int64_t all = (int64_t)(a.num_seqs - 1) * a.table_stride + a.max_pages;
+  if (at < all) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.page_table + at));
+}
+
 // A walk over a thread block's run, a block's head at a time.
 struct Walk {
   Block k;
@@ -250,10 +257,11 @@ __host__ __device__ inline Parts parts(void* p, int grid, int rows, int D) {
 // in an order that the timing does not change.
 cudaError_t launch_join(const AttnArgs& a, int grid, int rows, const Parts& p, cudaStream_t stream);
 
-// The device's SMs, at most 152.
+// The device's SMs, at most 152, and the most thread blocks that a launch's parts are laid out for.
 int sms();
+constexpr int kMaxGrid = 2 * 152;
 
-// Many rows: sequences of at least a.min_rows rows (mol_attend_tc.cu). Whether its tiles can be loaded from
+// Many rows a sequence (mol_attend_tc.cu). Whether its tiles can be loaded from
 // pages of this size, for heads of this width.
 bool many_fits(int page_size, int head_dim);
 size_t many_bytes(int group, int head_dim);

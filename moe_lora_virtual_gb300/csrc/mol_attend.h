@@ -64,8 +64,6 @@ struct AttnArgs {
   uint16_t* out;
   int64_t out_token_stride, out_head_stride;
   void* workspace;
-  // sequences of min_rows .. max_rows (new tokens x group) are the launch's own
-  int min_rows, max_rows;
 };
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim);
 cudaError_t prepare_attn_kernels();

@@ -23,8 +23,8 @@ using attn::Record;
 constexpr int kM = 128;                       // rows of a query tile, tokens of a key tile
 constexpr int kThreads = 12 * 32;              // (two warps of the last four idle)
 // Registers a thread: 384 threads are launched with 168; the last four warps give theirs up to the
-// softmax warps, 256 * 208 + 128 * 80 <= 384 * 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+// softmax warps, 256 * 200 + 128 * 96 <= 384 * 168.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kHeldRing = 8;                  // more tiles than the loader is ever ahead
@@ -635,7 +635,7 @@ bool attn::many_fits(int page_size, int head_dim) {
 }
 
 size_t attn::many_bytes(int group, int head_dim) {
-  return attn::parts_bytes(152, 2 * (kM / group) * group, head_dim);
+  return attn::parts_bytes(kMaxGrid / 2, 2 * (kM / group) * group, head_dim);
 }
 
 cudaError_t attn::prepare_many() {
