@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     if (!load.more()) return t;
     const int j = (load.k.t0 + load.first + load_tile) * G::kTile + warp * kStep + lane % kStep;
     if (j >= load.k.lo && j < load.k.hi) {
-      const int p = attn::divide(j, a.by_page);
+      const int p = divide(j, a.by_page);
       t.page = __ldg(a.page_table + load.k.b * a.table_stride + p);
       t.offset = j - p * a.page_size;
     }
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
       const int row = (i * kThreads + tid) / kChunks, ch = (i * kThreads + tid) % kChunks;
       query[i] = make_uint4(0, 0, 0, 0);
       if (row < k.nrows) {
-        const int r = k.row0 + row, token = attn::divide(r, a.by_group);
+        const int r = k.row0 + row, token = divide(r, a.by_group);
         query[i] = __ldg(reinterpret_cast<const uint4*>(
             a.q + (int64_t)(k.s.start + token) * a.q_token_stride +
             (int64_t)(h * a.group + r - token * a.group) * a.q_head_stride + ch * 8));
@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        pos[mt][i] = k.s.kv - k.s.n + attn::divide(k.row0 + min(mt * 16 + g + 8 * i, k.nrows - 1), a.by_group);
-    const int pos_first = k.s.kv - k.s.n + attn::divide(k.row0, a.by_group);
-    const int pos_last = k.s.kv - k.s.n + attn::divide(k.row0 + k.nrows - 1, a.by_group);
+        pos[mt][i] = k.s.kv - k.s.n + divide(k.row0 + min(mt * 16 + g + 8 * i, k.nrows - 1), a.by_group);
+    const int pos_first = k.s.kv - k.s.n + divide(k.row0, a.by_group);
+    const int pos_last = k.s.kv - k.s.n + divide(k.row0 + k.nrows - 1, a.by_group);
 
     float o[MT][D / 8][4];
     float top[MT][2], sum[MT][2];
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
           *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
           if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
         } else {
-          const int r = row0 + row, token = attn::divide(r, a.by_group);
+          const int r = row0 + row, token = divide(r, a.by_group);
           const float inv = m == -INFINITY ? 0.f : 1.f / l;
           *reinterpret_cast<uint2*>(a.out + (int64_t)(start + token) * a.out_token_stride +
                                     (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
     }
   }
   if (!has) return;
-  const int r = rec.row0 + row, token = attn::divide(r, a.by_group);
+  const int r = rec.row0 + row, token = divide(r, a.by_group);
   const float inv = m == -INFINITY ? 0.f : 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t)(rec.start + token) * a.out_token_stride +
                                               (int64_t)(rec.h * a.group + r - token * a.group) *

@@ -5,6 +5,12 @@
 #include "mol_device.cuh"
 
 namespace mol {
+
+MOL_DEV int divide(int n, const Divider& d) {
+  const uint32_t t = __umulhi(d.mul, (uint32_t)n);
+  return (int)((t + (((uint32_t)n - t) >> d.s1)) >> d.s2);
+}
+
 namespace attn {
 
 // A NaN or an infinity among eight bf16 values: an exponent of ones carries into the sign's place.
@@ -20,11 +26,6 @@ MOL_DEV float ex2(float x) {  // 2^x, within 2^-22 of it; 0 for -infinity
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-MOL_DEV int divide(int n, const Divider& d) {
-  const uint32_t t = __umulhi(d.mul, (uint32_t)n);
-  return (int)((t + (((uint32_t)n - t) >> d.s1)) >> d.s2);
 }
 
 // One sequence of the call: its first row of q, its rows, its cached tokens. Whatever the caller's

@@ -41,6 +41,9 @@ struct RopeArgs {
   bool interleaved;
   float magnitude;
   int64_t num_tokens;
+  // set by launch_rope: a head's 16-byte chunks and its units; heads that a block has a thread a unit for
+  int chunks, units, step;
+  Divider by_chunks, by_units, by_page;
 };
 // in[0] into q_out; in[1] and in[2] into their slots. heads 0: not there.
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < (two ? 2 : 1); ++t)
           for (int x = 0; x < D / 64; ++x)
             tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
-                        k.s.start + attn::divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
+                        k.s.start + divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
       }
       ++seg;
       for (int i = 0; i < w.count && !fault; ++i, ++n) {
@@ -274,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = j0 + lane * per;
         int page = -1;
         if (lane < copies && j + per > k.lo && j < k.hi)
-          page = __ldg(a.page_table + k.b * a.table_stride + attn::divide(j, a.by_page));
+          page = __ldg(a.page_table + k.b * a.table_stride + divide(j, a.by_page));
         const bool held = page >= 0 && page < a.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, held);
         if (!held) page = a.num_pages;  // past the end: zeros
-        const int offset = j - attn::divide(j, a.by_page) * a.page_size;
+        const int offset = j - divide(j, a.by_page) * a.page_size;
         if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
         for (int kv = 0; kv < 2; ++kv, ++u) {
           const int s = (int)(u % G::kSlots);
@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int in_tile = min(k.nrows - t * tile_rows, tile_rows);  // rows of this query tile
       if (in_tile > 0) {
         const int shift = k.s.kv - k.s.n, row = k.row0 + t * tile_rows;
-        const int pos = shift + attn::divide(row + min(local, in_tile - 1), a.by_group);
-        const int pos_first = shift + attn::divide(row, a.by_group);
-        const int pos_last = shift + attn::divide(row + in_tile - 1, a.by_group);
+        const int pos = shift + divide(row + min(local, in_tile - 1), a.by_group);
+        const int pos_first = shift + divide(row, a.by_group);
+        const int pos_last = shift + divide(row + in_tile - 1, a.by_group);
         float top = -INFINITY, sum = 0.f;
         for (int i = 0; i < count; ++i) {
           const int j0 = (k.t0 + w.first + i) * kM;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- the rows, or a part of them
         const int slot = 2 * (int)blockIdx.x + (begins ? 1 : 0);
         const bool mine = local < in_tile;
-        const int at = t * tile_rows + local, r = k.row0 + at, token = attn::divide(r, a.by_group);
+        const int at = t * tile_rows + local, r = k.row0 + at, token = divide(r, a.by_group);
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;

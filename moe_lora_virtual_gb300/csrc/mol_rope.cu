@@ -1,13 +1,11 @@
 // Rotary positions and the append to a paged cache (include/mol_attn.h).
 
-#include "mol_attend.h"
-#include "mol_device.cuh"
+#include "mol_attend.cuh"
 #include "mol_internal.h"
 
 namespace mol {
 namespace {
 
-constexpr int kRopeThreads = 128;
 constexpr int kMaxPairs = 256;  // half of the widest head
 
 // Eight bf16 values of a 16-byte chunk.
@@ -35,87 +33,110 @@ MOL_DEV void turn_pair(float& a, float& b, float2 cs) {
   a = x;
 }
 
-// A block per token. Its angles are the same for every head: computed once, one a thread, and kept in
-// shared memory; then each thread turns 16-byte chunks (in the half layout a chunk and its partner,
-// half the turned width on) of the token's heads, queries, keys and values in one list. Bound by HBM
-// for many tokens (each value read and written once), by the launch and two dependent round trips
-// (position or slot, then values) for a few.
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+// A block per token. Its angles are the same for every head: computed once, one a thread, handed over in
+// shared memory. A head is cut into units: a 16-byte chunk or, in the half layout's turned part, a chunk
+// and its partner half the turned width on. A thread has one unit of every step-th head (queries, then
+// keys), so that its addresses move by a constant; the first one, and the values, are asked for before
+// the angles (position, frequency and 64-bit products are a chain of two round trips and some). Bound
+// by HBM for many tokens (each value read and written once), by the launch and that chain for a few.
+// What keeps HBM busy is tokens under way: with 32 registers, 16 of them on a multiprocessor, 8192 tokens
+// of 32 heads of 128, half of each turned, take 26.2 us (0.75 of a copy's rate) and 31.7 with keys and
+// values into pages (0.76); 28.1 and 34.3 with 40 registers, 33.5 and 41.7 with 64. Keeping cosines and
+// four heads in registers (72) took 26.4 and 38.3, blocks that stay for several tokens (115) 30.6 and 43.5.
+template <int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[kMaxPairs];
   const int64_t t = blockIdx.x;
-  const int chunks = a.head_dim >> 3;
-  // units of a turned head: chunk pairs and single chunks behind them, or single chunks
-  const int pairs = a.interleaved ? 0 : a.rotary_dim >> 4;
-  const int turned = a.rotary_dim >> 3;
-  const int units = chunks - pairs;
   pdl_wait();
   pdl_launch_dependents();
+  const int slot = a.slots ? a.slots[t] : -1;
+  const int h0 = divide(threadIdx.x, a.by_units), unit = threadIdx.x - h0 * a.units;
+  const int pairs = a.interleaved ? 0 : a.rotary_dim >> 4;  // units that are two chunks
+  const bool two = unit < pairs;
+  const int u = two ? unit : unit + pairs;                  // its (first) chunk
+  const int heads = a.in[0].heads + a.in[1].heads;
+  const int first = h0 < a.step ? h0 : heads;               // (threads left over have none)
+  auto from = [&](int h) {
+    const bool key = h >= a.in[0].heads;
+    const HeadRows& in = a.in[key];
+    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.x) + t * in.token_stride +
+                                          (int64_t)(key ? h - a.in[0].heads : h) * in.head_stride) + u;
+  };
+  Chunk c, d;
+  if (first < heads) {
+    c.q = from(first)[0];
+    if (two) d.q = from(first)[pairs];
+  }
   if (a.inv_freq) {
     const int p = a.positions[t];
-    for (int i = threadIdx.x; i < a.rotary_dim / 2; i += kRopeThreads)
+    for (int i = threadIdx.x; i < a.rotary_dim / 2; i += THREADS)
       cs[i] = turn(p, a.inv_freq[i], a.magnitude);
   }
-  int64_t slot = -1;
-  if (a.slots) slot = a.slots[t];
   const bool keep = slot >= 0 && slot < a.num_slots;
-  int64_t cache_at = 0;
+  const int page = keep ? divide(slot, a.by_page) : 0;
+  const int64_t cache_at = (int64_t)page * a.page_stride + (int64_t)(slot - page * a.page_size) * a.token_stride;
   if (keep) {
-    const int64_t page = slot / a.page_size;
-    cache_at = page * a.page_stride + (slot - page * a.page_size) * a.token_stride;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.in[2].heads * a.chunks; i += THREADS) {
+      const int h = divide(i, a.by_chunks), at = i - h * a.chunks;
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_cache) + cache_at + h * a.head_stride)[at] =
+          reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in[2].x) +
+                                         t * a.in[2].token_stride + h * a.in[2].head_stride)[at];
+    }
   }
   __syncthreads();
-  const int nq = a.in[0].heads * units, nk = keep ? a.in[1].heads * units : 0,
-            nv = keep ? a.in[2].heads * chunks : 0;
-  for (int i = threadIdx.x; i < nq + nk + nv; i += kRopeThreads) {
-    const int which = i < nq ? 0 : i < nq + nk ? 1 : 2;
-    const int j = which == 0 ? i : which == 1 ? i - nq : i - nq - nk;
-    const int per = which == 2 ? chunks : units;
-    const int head = j / per;
-    const int u = j - head * per;
-    const HeadRows& in = a.in[which];
-    const uint16_t* src = static_cast<const uint16_t*>(in.x) + t * in.token_stride + head * in.head_stride;
-    uint16_t* dst = which == 0 ? static_cast<uint16_t*>(a.q_out) + t * a.q_out_token_stride +
-                                     head * a.q_out_head_stride
-                               : static_cast<uint16_t*>(which == 1 ? a.k_cache : a.v_cache) + cache_at +
-                                     head * a.head_stride;
-    if (which == 2) {
-      reinterpret_cast<uint4*>(dst)[u] = reinterpret_cast<const uint4*>(src)[u];
-    } else if (a.interleaved) {
-      Chunk c;
-      c.q = reinterpret_cast<const uint4*>(src)[u];
-      if (u < turned) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = bf16_lo(c.w[e]), y = bf16_hi(c.w[e]);
-          turn_pair(x, y, cs[4 * u + e]);
-          c.w[e] = pack_bf16x2(x, y);
-        }
-      }
-      reinterpret_cast<uint4*>(dst)[u] = c.q;
-    } else if (u < pairs) {
-      Chunk c, d;
-      c.q = reinterpret_cast<const uint4*>(src)[u];
-      d.q = reinterpret_cast<const uint4*>(src)[u + pairs];
+#pragma unroll 1
+  for (int h = first; h < heads; h += a.step) {
+    if (h != first) {
+      c.q = from(h)[0];
+      if (two) d.q = from(h)[pairs];
+    }
+    if (two) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float x0 = bf16_lo(c.w[e]), x1 = bf16_hi(c.w[e]), y0 = bf16_lo(d.w[e]), y1 = bf16_hi(d.w[e]);
+        float x0 = bf16_lo(c.w[e]), x1 = bf16_hi(c.w[e]);
+        float y0 = bf16_lo(d.w[e]), y1 = bf16_hi(d.w[e]);
         turn_pair(x0, y0, cs[8 * u + 2 * e]);
         turn_pair(x1, y1, cs[8 * u + 2 * e + 1]);
         c.w[e] = pack_bf16x2(x0, x1);
         d.w[e] = pack_bf16x2(y0, y1);
       }
-      reinterpret_cast<uint4*>(dst)[u] = c.q;
-      reinterpret_cast<uint4*>(dst)[u + pairs] = d.q;
-    } else {
-      reinterpret_cast<uint4*>(dst)[u + pairs] = reinterpret_cast<const uint4*>(src)[u + pairs];
+    } else if (a.interleaved && u < a.rotary_dim >> 3) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = bf16_lo(c.w[e]), y = bf16_hi(c.w[e]);
+        turn_pair(x, y, cs[4 * u + e]);
+        c.w[e] = pack_bf16x2(x, y);
+      }
     }
+    uint16_t* dst;
+    if (h < a.in[0].heads) {
+      dst = static_cast<uint16_t*>(a.q_out) + t * a.q_out_token_stride + h * a.q_out_head_stride;
+    } else {
+      if (!keep) break;
+      dst = static_cast<uint16_t*>(a.k_cache) + cache_at + (h - a.in[0].heads) * a.head_stride;
+    }
+    reinterpret_cast<uint4*>(dst)[u] = c.q;
+    if (two) reinterpret_cast<uint4*>(dst)[u + pairs] = d.q;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
-  return launch_pdl(rope_kernel, dim3((unsigned)a.num_tokens), dim3(kRopeThreads), 0, stream, a);
+cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream) {
+  RopeArgs a = args;
+  a.chunks = a.head_dim >> 3;
+  a.units = a.chunks - (a.interleaved ? 0 : a.rotary_dim >> 4);
+  a.by_chunks = divider(a.chunks);
+  a.by_units = divider(a.units);
+  a.by_page = divider(a.page_size);
+  // Many tokens: as many as possible at a time. Few: 256 threads each, registers as they come (23 tokens of
+  // 16 heads of 128 1.9 us, 2.3 with keys and values; 2.2 and 2.8 in the form for many).
+  auto go = [&](auto kernel, int threads) {
+    a.step = threads / a.units;
+    return launch_pdl(kernel, dim3((unsigned)a.num_tokens), dim3(threads), 0, stream, a);
+  };
+  return a.num_tokens > 4 * 152 ? go(rope_kernel<128, 16>, 128) : go(rope_kernel<256, 4>, 256);
 }
 
 }  // namespace mol
