@@ -21,7 +21,7 @@ using attn::Place;
 using attn::Record;
 
 constexpr int kM = 128;                       // rows of a query tile, tokens of a key tile
-constexpr int kThreads = 12 * 32;              // (two warps of the last four idle)
+constexpr int kThreads = 12 * 32;
 // Registers a thread: 384 threads are launched with 168; the last four warps give theirs up to the
 // softmax warps, 256 * 200 + 128 * 96 <= 384 * 168.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
@@ -184,20 +184,20 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys)
 //   warp 9          copies the queries and, page by page, keys and values (TMA, 128-byte swizzle) into a
 //                   ring of tiles
-// Tiles are dealt as in attend_few; parts of blocks join in launch_join.
-// Pages outside the cache are zeros (the copy's fill). Where a row does not see all of a tile, its
-// scores are replaced, and the tile's values looked through: those that nobody sees are zeroed if they
-// are not finite, and if another row sees such a value, the tile's products are summed without the
-// tensor cores, for which 0 * NaN is NaN.
+//   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
+//                   not finite are zeroed where no row sees them; where another row does, the tile's
+//                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
+// Tiles are dealt as in attend_few; parts of blocks join in launch_join. Pages outside the cache are zeros
+// (the copy's fill); what a row does not see is replaced among its scores.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
   using G = Geo<D>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], s_full[2], p_full[2], o_full[2],
-      v_seen[2];
-  __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[2][2];
+  __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], seen[G::kSlots], s_full[2],
+      p_full[2], o_full[2];
+  __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[G::kSlots];
   __shared__ int s_scan[kThreads / 32 + 1];
   __shared__ Place s_place;
   __shared__ attn::Run s_run;
@@ -211,14 +211,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&all_done, 1);
     for (int s = 0; s < G::kSlots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 3);  // the last products' commit, and the two warps that look through values
+      mbar_init(&seen[s], 2);
+      s_bad[s] = 0;
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 2);  // the products' commit, and the issuing thread for what it has seen
       mbar_init(&p_full[t], 4);  // a warp each
       mbar_init(&o_full[t], 1);
-      mbar_init(&v_seen[t], 4);
-      s_bad[t][0] = s_bad[t][1] = 0;
     }
     fence_mbar_init();
   }
@@ -254,33 +254,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn::Walk w;
     for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
-      if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
-        fault = true;
-        break;
-      }
-      const bool two = k.nrows > tile_rows;
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)(tile_rows * 128 * (D / 64) * (two ? 2 : 1));
-        mbar_arrive_expect_tx(&q_full, bytes);
-        for (int t = 0; t < (two ? 2 : 1); ++t)
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
-                        k.s.start + divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
-      }
-      ++seg;
+      const int32_t* pages = a.page_table + k.b * a.table_stride;
+      // lane p: page p of the block's i-th tile, asked for a tile ahead
+      auto look = [&](int i) {
+        const int j = (k.t0 + w.first + i) * kM + lane * per;
+        return i < w.count && lane < copies && j + per > k.lo && j < k.hi
+                   ? __ldg(pages + divide(j, a.by_page)) : -1;
+      };
+      int page = look(0);
       for (int i = 0; i < w.count && !fault; ++i, ++n) {
-        const int j0 = (k.t0 + w.first + i) * kM;
-        // lane p: page p of the tile
-        const int j = j0 + lane * per;
-        int page = -1;
-        if (lane < copies && j + per > k.lo && j < k.hi)
-          page = __ldg(a.page_table + k.b * a.table_stride + divide(j, a.by_page));
+        const int next_page = look(i + 1);
         const bool held = page >= 0 && page < a.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, held);
         if (!held) page = a.num_pages;  // past the end: zeros
+        const int j = (k.t0 + w.first + i) * kM + lane * per;
         const int offset = j - divide(j, a.by_page) * a.page_size;
         if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
-        for (int kv = 0; kv < 2; ++kv, ++u) {
+        for (int kv = 0; kv < 2 && !fault; ++kv, ++u) {
           const int s = (int)(u % G::kSlots);
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, kPolls))) {
             fault = true;
@@ -292,13 +282,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < D / 64; ++x)
               tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
                           x * 64, offset, w.h, page, &full[s]);
+          if (i + kv == 0) {  // the queries behind the first keys, which need not wait for the block before
+            if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
+              fault = true;
+              ++u;
+              break;
+            }
+            const bool two = k.nrows > tile_rows;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full, (uint32_t)(tile_rows * 128 * (D / 64) * (two ? 2 : 1)));
+              for (int t = 0; t < (two ? 2 : 1); ++t)
+                for (int x = 0; x < D / 64; ++x)
+                  tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
+                              k.s.start + divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
+            }
+            ++seg;
+          }
         }
+        page = next_page;
       }
     }
     if (fault) {  // nothing of its own left in flight
       for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; i < u; ++i)
         mbar_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, kPolls);
       if (seg > 0) mbar_wait(&q_full, (seg - 1) & 1, kPolls);
+    }
+  } else if (warp > 9) {
+    // ------------------------------------------------------------ values that not every row sees
+    uint32_t u = 0, n = 0;
+    const int per = a.page_size < kM ? a.page_size : kM;
+    const uint32_t all = (uint32_t)(((uint64_t)1 << (kM / per)) - 1);
+    attn::Walk w;
+    for (begin(w); w.more() && !fault; next(w)) {
+      const Block& k = w.k;
+      const int shift = k.s.kv - k.s.n;
+      const int pos_first = shift + divide(k.row0, a.by_group);
+      const int pos_last = shift + divide(k.row0 + k.nrows - 1, a.by_group);
+      for (int i = 0; i < w.count && !fault; ++i, ++n)
+        for (int kv = 0; kv < 2; ++kv, ++u) {
+          const int s = (int)(u % G::kSlots);
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (u / G::kSlots) & 1, kPolls))) {
+            fault = true;
+            break;
+          }
+          const int j0 = (k.t0 + w.first + i) * kM;
+          if (kv && (*(volatile uint32_t*)&s_held[n % kHeldRing] != all || j0 + kM - 1 > pos_first ||
+                     (a.window > 0 && j0 <= pos_last - a.window))) {
+            unsigned char* v = ring + s * G::kTileBytes;
+            bool bad = false;
+#pragma unroll 4
+            for (int x = tid - 10 * 32; x < G::kTileBytes / 16; x += 64)
+              if (attn::not_finite(lds16(v + x * 16))) {
+                const int j = j0 + (x >> 3) % kM;
+                if (j < k.lo || j >= k.hi)
+                  *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+                else
+                  bad = true;
+              }
+            fence_proxy_async_smem();
+            if (bad) *(volatile uint32_t*)&s_bad[s] = u + 1;
+            __syncwarp();
+          }
+          if (lane == 0) {
+            mbar_arrive(&seen[s]);
+            mbar_arrive(&empty[s]);
+          }
+        }
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ products
@@ -380,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int local = quarter * 32 + lane;  // row of the tile
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + G::kS + t * kM, to_ = tmem + lanes + G::kO + t * D;
-    // scores waited for, tiles, ring slots, sums waited for, tiles that were looked through
-    uint32_t ns = 0, n = 0, u = 0, no = 0, edges = 0;
+    uint32_t ns = 0, n = 0, u = 0, no = 0;  // scores waited for, tiles, ring slots, sums waited for
     Record record = {};
     record.last = -1;
     attn::Walk w;
@@ -409,40 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int copies = kM / per;
           const bool all_held = copies == 32 ? held == 0xffffffffu : held == (1u << copies) - 1;
           const bool edge = !all_held || j0 + kM - 1 > pos_first || (a.window > 0 && j0 <= pos_last - a.window);
-          bool plain = false;
           const int hi = pos - j0, lo = a.window > 0 ? hi - a.window : -1;  // seen: lo < column <= hi
-          if (edge) {
-            // the tile's values, once they are there
-            const uint32_t slot = u + 2 * i + 1;
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(&full[slot % G::kSlots], (slot / G::kSlots) & 1, kPolls))) {
-              fault = true;
-              break;
-            }
-            unsigned char* v = ring + (slot % G::kSlots) * G::kTileBytes;
-            bool bad = false;
-#pragma unroll 8
-            for (int x = local; x < G::kTileBytes / 16; x += kM) {
-              const int j = j0 + (x >> 3) % kM;
-              if (attn::not_finite(lds16(v + x * 16))) {
-                if (j < k.lo || j >= k.hi)
-                  *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
-                else
-                  bad = true;
-              }
-            }
-            fence_proxy_async_smem();
-            // the warps tell one another (two words in turn: none is two such tiles ahead)
-            if (bad) *(volatile uint32_t*)&s_bad[t][edges & 1] = n + i + 1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_seen[t]);
-            if (!__all_sync(0xffffffffu, mbar_wait(&v_seen[t], edges & 1, kPolls))) {
-              fault = true;
-              break;
-            }
-            plain = *(volatile uint32_t*)&s_bad[t][edges & 1] == n + i + 1;
-            ++edges;
-          }
           uint32_t r[kM];
           float m4[kM / 32];
 #pragma unroll
@@ -494,9 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_x32(ts, p);
           tmem_st_x32(ts + 32, p + 32);
           tmem_wait_st();
+          const uint32_t slot = u + 2 * i + 1;  // of the tile's values
+          bool plain = false;
+          if (edge) {  // they have been looked through
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(&seen[slot % G::kSlots], (slot / G::kSlots) & 1, kPolls))) {
+              fault = true;
+              break;
+            }
+            plain = *(volatile uint32_t*)&s_bad[slot % G::kSlots] == slot + 1;
+          }
           if (plain) {
             // the row's weights come back from tensor memory two at a time
-            const uint32_t slot = u + 2 * i + 1;
             const unsigned char* v = ring + (slot % G::kSlots) * G::kTileBytes;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
