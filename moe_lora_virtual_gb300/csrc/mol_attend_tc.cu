@@ -49,24 +49,38 @@ MOL_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// D += A * B with A (bf16) in tensor memory.
-MOL_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                          uint32_t accumulate) {
+// Shared-memory operands: low word of their descriptor (address and, for rows that are the contraction, the
+// distance of their 64-column atoms in the upper half) and the high word that all have: 8-row groups
+// 1024 bytes apart, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+MOL_DEV uint32_t desc_low(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+// D += A * B by one lane of the converged warp: A and B with the contraction along their rows.
+MOL_DEV void umma_ss(uint32_t leader, uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
+                     uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_low | 1u << 16), "r"(b_low | 1u << 16), "r"(idesc), "r"(accumulate), "r"(leader), "r"(kDescHigh)
       : "memory");
 }
-// Operand whose rows are the contraction (tokens) and whose 64-column atoms lie kHalf bytes apart:
-// 8-row groups 1024 bytes apart, 128-byte swizzle.
-MOL_DEV uint64_t sw128_desc_rows(uint32_t saddr, uint32_t atom) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(atom >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// The same with A (bf16) in tensor memory and B's rows the contraction, its atoms `atom` 16-byte units apart.
+MOL_DEV void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t atom,
+                     uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low | atom << 16), "r"(idesc), "r"(accumulate), "r"(leader), "r"(kDescHigh)
+      : "memory");
+}
+MOL_DEV void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
 }
 MOL_DEV void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -351,76 +365,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      uint32_t u = 0, seg = 0, np[2] = {0, 0};
-      auto wait_slot = [&](uint32_t i) {
-        if (!mbar_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, kPolls)) fault = true;
-        tc_fence_after();
-        return !fault;
-      };
-      auto scores = [&](int t, uint32_t slot) {
-        const uint32_t q = smem_u32(smem + t * G::kTileBytes);
-        const uint32_t k = smem_u32(ring + (slot % G::kSlots) * G::kTileBytes);
+    // The whole warp goes through it, so that what the products take lies in registers that the warp shares;
+    // one lane issues them.
+    uint32_t u = 0, seg = 0, np[2] = {0, 0};
+    const uint32_t leader = lane == 0;
+    const uint32_t q_at = desc_low(smem_u32(smem)), ring_at = desc_low(smem_u32(ring));
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls))) fault = true;
+      tc_fence_after();
+      return !fault;
+    };
+    auto wait_slot = [&](uint32_t i) { return wait(&full[i % G::kSlots], (i / G::kSlots) & 1); };
+    auto scores = [&](int t, uint32_t slot) {
+      const uint32_t q = q_at + t * (G::kTileBytes >> 4);
+      const uint32_t k = ring_at + (slot % G::kSlots) * (G::kTileBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * G::kHalf + (kk % 4) * 32;
-          umma_bf16(tmem + G::kS + t * kM, sw128_desc(q + off), sw128_desc(k + off), kScores, kk != 0);
-        }
-        umma_commit(&s_full[t]);
-        mbar_arrive(&s_full[t]);
-      };
-      attn::Walk w;
-    for (begin(w); w.more() && !fault; next(w)) {
-        const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
-        ++seg;
-        if (!mbar_wait(&q_full, (seg - 1) & 1, kPolls) || !wait_slot(u)) {
-          fault = true;
-          break;
-        }
-        tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, u);
-        umma_commit(&empty[u % G::kSlots]);
-        if (count == 1) umma_commit(&q_empty);  // (with the block's last scores)
-        bool begun[2] = {false, false};
-        for (int i = 0; i < count && !fault; ++i) {
-          // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
-          const bool more = i + 1 < count;
-          for (int t = 0; t < tiles && !fault; ++t) {
-            if (t == 0 && !wait_slot(u + 1)) break;
-            if (!mbar_wait(&p_full[t], np[t] & 1, kPolls)) {
-              fault = true;
-              break;
-            }
-            ++np[t];
-            tc_fence_after();
-            if (!*(volatile uint32_t*)&s_skip[t]) {
-              const uint32_t v = smem_u32(ring + ((u + 1) % G::kSlots) * G::kTileBytes);
-#pragma unroll
-              for (int kk = 0; kk < kM / 16; ++kk)
-                umma_bf16_ts(tmem + G::kO + t * D, tmem + G::kS + t * kM + kk * 8,
-                             sw128_desc_rows(v + kk * 16 * 128, G::kHalf), kValues<D>,
-                             begun[t] || kk != 0);
-            }
-            begun[t] = true;
-            if (t == tiles - 1) umma_commit(&empty[(u + 1) % G::kSlots]);
-            if (more) {
-              if (t == 0 && !wait_slot(u + 2)) break;
-              scores(t, u + 2);
-              if (t == tiles - 1) {
-                umma_commit(&empty[(u + 2) % G::kSlots]);
-                if (i + 2 == count) umma_commit(&q_empty);
-              }
-            } else {
-              umma_commit(&o_full[t]);
-            }
-          }
-          u += 2;
-        }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * G::kHalf + (kk % 4) * 32) >> 4;
+        umma_ss(leader, tmem + G::kS + t * kM, q + off, k + off, kScores, kk != 0);
       }
-      // the products are done, and their commits have arrived
-      umma_commit(&all_done);
-      if (!mbar_wait(&all_done, 0, kPolls)) fault = true;
+      commit(leader, &s_full[t]);
+      if (leader) mbar_arrive(&s_full[t]);
+    };
+    attn::Walk w;
+    for (begin(w); w.more() && !fault; next(w)) {
+      const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
+      ++seg;
+      if (!wait(&q_full, (seg - 1) & 1) || !wait_slot(u)) break;
+      scores(0, u);
+      if (tiles == 2) scores(1, u);
+      commit(leader, &empty[u % G::kSlots]);
+      if (count == 1) commit(leader, &q_empty);  // (with the block's last scores)
+      bool begun[2] = {false, false};
+      for (int i = 0; i < count && !fault; ++i) {
+        // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
+        const bool more = i + 1 < count;
+        if (!wait_slot(u + 1)) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == tiles || !wait(&p_full[t], np[t] & 1)) break;
+          ++np[t];
+          if (!*(volatile uint32_t*)&s_skip[t]) {
+            const uint32_t v = ring_at + ((u + 1) % G::kSlots) * (G::kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kM / 16; ++kk)
+              umma_ts(leader, tmem + G::kO + t * D, tmem + G::kS + t * kM + kk * 8, v + (kk * 16 * 128 >> 4),
+                      G::kHalf >> 4, kValues<D>, begun[t] || kk != 0);
+          }
+          begun[t] = true;
+          if (t == tiles - 1) commit(leader, &empty[(u + 1) % G::kSlots]);
+          if (more) {
+            if (t == 0 && !wait_slot(u + 2)) break;
+            scores(t, u + 2);
+            if (t == tiles - 1) {
+              commit(leader, &empty[(u + 2) % G::kSlots]);
+              if (i + 2 == count) commit(leader, &q_empty);
+            }
+          } else {
+            commit(leader, &o_full[t]);
+          }
+        }
+        u += 2;
+      }
     }
+    // the products are done, and their commits have arrived
+    commit(leader, &all_done);
+    if (!__all_sync(0xffffffffu, mbar_wait(&all_done, 0, kPolls))) fault = true;
   }
   } else {
     // ------------------------------------------------------------ softmax
