@@ -372,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_at = desc_low(smem_u32(smem)), ring_at = desc_low(smem_u32(ring));
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls))) fault = true;
-      tc_fence_after();
       return !fault;
     };
     auto wait_slot = [&](uint32_t i) { return wait(&full[i % G::kSlots], (i / G::kSlots) & 1); };
@@ -400,10 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < count && !fault; ++i) {
         // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
         const bool more = i + 1 < count;
-        if (!wait_slot(u + 1)) break;
+        if (!wait_slot(u + 1) || (more && !wait_slot(u + 2))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t == tiles || !wait(&p_full[t], np[t] & 1)) break;
+          tc_fence_after();
           ++np[t];
           if (!*(volatile uint32_t*)&s_skip[t]) {
             const uint32_t v = ring_at + ((u + 1) % G::kSlots) * (G::kTileBytes >> 4);
@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           begun[t] = true;
           if (t == tiles - 1) commit(leader, &empty[(u + 1) % G::kSlots]);
           if (more) {
-            if (t == 0 && !wait_slot(u + 2)) break;
             scores(t, u + 2);
             if (t == tiles - 1) {
               commit(leader, &empty[(u + 2) % G::kSlots]);
