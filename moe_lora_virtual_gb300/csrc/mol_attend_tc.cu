@@ -37,8 +37,10 @@ struct Geo {
   static constexpr int kTileBytes = kHalf * (D / 64);
   static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTileBytes;
-  // tensor memory: the scores of both query tiles (their weights over the first half of each), their sums
-  static constexpr uint32_t kS = 0, kO = 2 * kM;
+  // Tensor memory: the scores of both query tiles, their sums, and the weights: in columns of their own
+  // where there are any left (64 values a head), else over the first half of the scores.
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kS = 0, kO = 2 * kM, kP = kApart ? kO + 2 * D : kS, kPStep = kApart ? kM / 2 : kM;
   static constexpr uint32_t kCols = 512;
 };
 
@@ -195,7 +197,8 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //   warps 0-3, 4-7  softmax of query tile 0, 1: a thread a row, 128 scores in registers, maximum and sum
 //                   without a shuffle. The maximum that weights refer to moves only when one would
 //                   pass 2^8 (bf16 and fp32 lose nothing to that), so sums are hardly ever rescaled
-//   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys)
+//   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys); Q0 K', Q1 K', P0 V, P1 V
+//                   for 64 values a head, whose weights need not wait for the scores' place
 //   warp 9          copies the queries and, page by page, keys and values (TMA, 128-byte swizzle) into a
 //                   ring of tiles
 //   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using G = Geo<D>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], seen[G::kSlots], s_full[2],
-      p_full[2], o_full[2];
+      p_full[2], o_full[2], s_read[2];
   __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[G::kSlots];
   __shared__ int s_scan[kThreads / 32 + 1];
   __shared__ Place s_place;
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[t], 2);  // the products' commit, and the issuing thread for what it has seen
       mbar_init(&p_full[t], 4);  // a warp each
       mbar_init(&o_full[t], 1);
+      mbar_init(&s_read[t], 4);
     }
     fence_mbar_init();
   }
@@ -400,6 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
         const bool more = i + 1 < count;
         if (!wait_slot(u + 1) || (more && !wait_slot(u + 2))) break;
+        // the next tile's scores as soon as these have been read, where the weights lie apart
+        if (G::kApart && more) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == tiles || !wait(&s_read[t], np[t] & 1)) break;
+            tc_fence_after();
+            scores(t, u + 2);
+          }
+          if (fault) break;
+          commit(leader, &empty[(u + 2) % G::kSlots]);
+          if (i + 2 == count) commit(leader, &q_empty);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t == tiles || !wait(&p_full[t], np[t] & 1)) break;
@@ -409,19 +425,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v = ring_at + ((u + 1) % G::kSlots) * (G::kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < kM / 16; ++kk)
-              umma_ts(leader, tmem + G::kO + t * D, tmem + G::kS + t * kM + kk * 8, v + (kk * 16 * 128 >> 4),
-                      G::kHalf >> 4, kValues<D>, begun[t] || kk != 0);
+              umma_ts(leader, tmem + G::kO + t * D, tmem + G::kP + t * G::kPStep + kk * 8,
+                      v + (kk * 16 * 128 >> 4), G::kHalf >> 4, kValues<D>, begun[t] || kk != 0);
           }
           begun[t] = true;
           if (t == tiles - 1) commit(leader, &empty[(u + 1) % G::kSlots]);
-          if (more) {
+          if (G::kApart || !more) commit(leader, &o_full[t]);
+          if (!G::kApart && more) {
             scores(t, u + 2);
             if (t == tiles - 1) {
               commit(leader, &empty[(u + 2) % G::kSlots]);
               if (i + 2 == count) commit(leader, &q_empty);
             }
-          } else {
-            commit(leader, &o_full[t]);
           }
         }
         u += 2;
@@ -438,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int local = quarter * 32 + lane;  // row of the tile
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + G::kS + t * kM, to_ = tmem + lanes + G::kO + t * D;
+    const uint32_t tp = tmem + lanes + G::kP + t * G::kPStep;
     uint32_t ns = 0, n = 0, u = 0, no = 0;  // scores waited for, tiles, ring slots, sums waited for
     Record record = {};
     record.last = -1;
@@ -472,6 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < kM / 32; ++x) tmem_ld_max_x32(ts + x * 32, r + x * 32, m4[x]);
           tmem_wait_ld();
+          if (G::kApart) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_read[t]);
+          }
           if (edge) {
 #pragma unroll
             for (int x = 0; x < kM / 32; ++x) {
@@ -485,12 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          // the products before these weights are done (where these lie over scores, those came behind them)
+          if (G::kApart && ns > 1) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&o_full[t], ns & 1, kPolls))) {
+              fault = true;
+              break;
+            }
+            tc_fence_after();
+          }
           const bool moves = m > top + kLazy || (top == -INFINITY && m > top);
           if (__any_sync(0xffffffffu, moves)) {
             const float f = moves ? ex2(top - m) : 1.f;
             if (moves) top = m;
             sum *= f;
-            if (i > 0) {  // (the scores' commit came behind the products before them)
+            if (i > 0) {
 #pragma unroll 1
               for (int x = 0; x < D; x += 16) {
                 uint32_t o[16];
@@ -515,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[x] = pack_bf16x2(e.x, e.y);
           }
           sum += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-          tmem_st_x32(ts, p);
-          tmem_st_x32(ts + 32, p + 32);
+          tmem_st_x32(tp, p);
+          tmem_st_x32(tp + 32, p + 32);
           tmem_wait_st();
           const uint32_t slot = u + 2 * i + 1;  // of the tile's values
           bool plain = false;
@@ -543,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
 #pragma unroll 1
               for (int y = 0; y < kM; ++y) {
-                const uint32_t pair = tmem_ld_x1(ts + (y >> 1));
+                const uint32_t pair = tmem_ld_x1(tp + (y >> 1));
                 tmem_wait_ld();
                 const float wt = y & 1 ? bf16_hi(pair) : bf16_lo(pair);
                 const bool sees = (columns_seen(y >> 5, lo, hi, held, per) >> (y & 31)) & 1;
@@ -570,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[t]);
         }
-        if (fault || !__all_sync(0xffffffffu, mbar_wait(&o_full[t], no & 1, kPolls))) {
+        if (fault || !__all_sync(0xffffffffu, mbar_wait(&o_full[t], (G::kApart ? ns - 1 : no) & 1, kPolls))) {
           fault = true;
           break;
         }
