@@ -408,3 +408,98 @@ def test_binding_refusals(env):
         with pytest.raises(error):
             call()
             pytest.fail(f"call {i} was taken")
+
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decode_layers.py")
+    spec = importlib.util.spec_from_file_location("decode_layers", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_example_attention_half(env):
+    """The example's attention over a prompt and the tokens behind it against the same in float64, with
+    bf16 where the layer holds bf16: the norm, the projection, the cache's keys and the queries, the
+    weights, the attention and the output are seven roundings in a row of 2^-8 each, taken in the mean
+    square over the rows."""
+    torch, mol = env
+    module = example()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    H, heads, kv, D = 256, 8, 2, 64
+    batch = module.Batch(3, 200, 16)
+    half = module.Attention(g, H, heads, kv, D, batch, 64)
+    x = torch.randn(64, H, generator=g, device="cuda").to(torch.bfloat16)
+    zero = torch.zeros_like(x)
+    chunks = [[30, 0, 14], [1, 20, 3], None, [0, 2, 1], None]
+    rows, seen, want, got = 0, [[], [], []], [], []
+    qkv, proj = mol.w4_unpack(half.qkv).double(), mol.w4_unpack(half.out).double()
+    for counts in chunks:
+        n = 3 if counts is None else sum(counts)
+        here = x[rows:rows + n] if rows + n <= len(x) else x[:n]
+        place = batch.place(counts)
+        y, _ = half(zero[:n], here, batch, place)
+        got.append(y.clone())
+        r = here.double()
+        normed = r * torch.rsqrt((r * r).mean(-1, keepdim=True) + 1e-6)
+        p = (normed @ qkv.T).view(n, -1, D).cpu().numpy()
+        freq = f64(half.rope.inv_freq)
+        at = f64(place[0])
+        q, k = ao.rope(p[:, :heads], at, freq), ao.rope(p[:, heads:heads + kv], at, freq)
+        row = 0
+        for b, m in enumerate([1, 1, 1] if counts is None else counts):
+            for _ in range(m):
+                assert at[row] == len(seen[b])
+                seen[b].append((k[row], p[row, heads + kv:]))
+                ks, vs = (np.stack([t[i] for t in seen[b]]) for i in (0, 1))
+                s = np.einsum("hd,jhd->hj", q[row], np.repeat(ks, heads // kv, 1)) * D ** -0.5
+                w = np.exp(s - s.max(1, keepdims=True))
+                o = np.einsum("hj,jhd->hd", w / w.sum(1, keepdims=True), np.repeat(vs, heads // kv, 1))
+                want.append(o.reshape(-1) @ proj.cpu().numpy().T)
+                row += 1
+        rows = (rows + n) % 40
+    got, want = f64(torch.cat(got)), np.stack(want)
+    err = np.sqrt(((got - want) ** 2).mean() / (want ** 2).mean())
+    assert err < 7 ** 0.5 * ROUND, err
+
+
+def test_example_model_with_attention_in_a_graph(env):
+    """Steps of the whole model, a prompt first: the replayed graph gives what the calls give."""
+    torch, mol = env
+    module = example()
+    T = 5
+    kw = dict(tokens=T, layers=2, group=0, seed=3, heads=4, kv_heads=2, head_dim=64, context=64, page=8)
+    g = torch.Generator().manual_seed(4)
+    prompt = torch.randint(0, 5000, (17,), generator=g).cuda()
+    tokens = torch.randint(0, 5000, (3, T), generator=g).cuda()
+    lora = torch.randint(-1, 4, (17,), generator=g).to(torch.int32).cuda()
+    # (as many pairs as the model's buffers hold: five tokens at a time)
+    parts = [[2, 1, 0, 1, 1], [0, 3, 1, 0, 1], [5, 0, 0, 0, 0]]
+
+    def begin():
+        torch.manual_seed(7)  # the pages' order
+        model, at = module.Model(**kw), 0
+        for counts in parts:
+            model(prompt[at:at + sum(counts)], lora[at:at + sum(counts)], counts)
+            at += sum(counts)
+        return model
+
+    model = begin()
+    want = [model(t, lora[:T]).clone() for t in tokens]
+    assert model.batch.lens.tolist() == [10, 7, 4, 4, 5]
+    model = begin()
+    first = model(tokens[0], lora[:T])  # (before the capture, on the same cache)
+    assert torch.equal(first, want[0])
+    step = tokens[1].clone()
+    graph = torch.cuda.CUDAGraph()
+    lens = model.batch.lens.clone()
+    with torch.cuda.graph(graph):
+        logits = model(step, lora[:T])
+    assert torch.equal(model.batch.lens, lens)
+    for i in (1, 2):
+        step.copy_(tokens[i])
+        graph.replay()
+        assert torch.equal(logits, want[i])
