@@ -224,6 +224,7 @@ int32_t mol_debug_wait_test(uint32_t stall_producer, uint64_t wait_limit_ns) {
   const unsigned long long lim = wait_limit_ns == 0 ? 1000000000ull : wait_limit_ns;
   cudaError_t e = mol::set_wait_test(stall_producer, lim);
   if (e == cudaSuccess) e = mol::set_moe_wait_test(stall_producer, lim);
+  if (e == cudaSuccess) e = mol::set_attn_wait_test(stall_producer, lim);
   return e == cudaSuccess ? MOL_OK : cuda_fail(e);
 }
 
@@ -241,11 +242,12 @@ int32_t mol_take_check_record(uint64_t* first, uint64_t* count) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
   // in the path's order: align, item shrink and expands, tcgen05 shrink, fused stage,
-  // tcgen05 expand, norm and router, experts and 4-bit linear, attention
-  cudaError_t (*const take[8])(unsigned long long*, unsigned long long*) = {
+  // tcgen05 expand, norm and router, experts and 4-bit linear, rotation, attention
+  cudaError_t (*const take[10])(unsigned long long*, unsigned long long*) = {
       mol::take_align_checks, mol::take_lora_checks,      mol::take_tc_checks,
       mol::take_stage_checks, mol::take_expand_tc_checks, mol::take_block_checks,
-      mol::take_moe_checks,   mol::take_attn_checks};
+      mol::take_moe_checks,   mol::take_rope_checks,      mol::take_attn_checks,
+      mol::take_many_checks};
   unsigned long long f = 0, n = 0;
   for (auto fn : take) {
     unsigned long long fi = 0, ni = 0;

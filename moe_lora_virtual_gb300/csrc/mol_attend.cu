@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     const int j = (load.k.t0 + load.first + load_tile) * G::kTile + warp * kStep + lane % kStep;
     if (j >= load.k.lo && j < load.k.hi) {
       const int p = divide(j, a.by_page);
-      t.page = __ldg(a.page_table + load.k.b * a.table_stride + p);
+      if (MOL_CHECK(p >= 0 && p < a.max_pages, MOL_CHECK_COLUMN, p))
+        t.page = __ldg(a.page_table + load.k.b * a.table_stride + p);
       t.offset = j - p * a.page_size;
     }
     if (++load_tile == load.count) {
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
       query[i] = make_uint4(0, 0, 0, 0);
       if (row < k.nrows) {
         const int r = k.row0 + row, token = divide(r, a.by_group);
-        query[i] = __ldg(reinterpret_cast<const uint4*>(
+        if (MOL_CHECK(k.s.start + token < a.num_tokens, MOL_CHECK_ROW, k.s.start + token))
+          query[i] = __ldg(reinterpret_cast<const uint4*>(
             a.q + (int64_t)(k.s.start + token) * a.q_token_stride +
             (int64_t)(h * a.group + r - token * a.group) * a.q_head_stride + ch * 8));
       }
@@ -399,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
           x.z += f * y.z;
           x.w += f * y.w;
         }
+        if (kChecked && !MOL_CHECK(start + divide(row0 + row, a.by_group) < a.num_tokens, MOL_CHECK_ROW,
+                                   start + divide(row0 + row, a.by_group)))
+          continue;
         if (part) {
           *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
           if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
@@ -433,6 +438,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(AttnArgs a, int r
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int local = warp / WAYS, way = warp % WAYS, row = blockIdx.y * kRows + local;
   const Record rec = p.records[c];
+  if (rec.last >= 0)
+    (void)MOL_CHECK(rec.last > c && rec.last < (int)gridDim.x, MOL_CHECK_ROW, rec.last);
   if (rec.last < 0 || (int)blockIdx.y * kRows >= rec.nrows) return;
   const bool has = row < rec.nrows;
   float x[kPer], l = 0.f, m = -INFINITY;

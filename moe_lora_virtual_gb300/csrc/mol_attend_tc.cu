@@ -11,6 +11,9 @@
 namespace mol {
 
 __device__ unsigned int g_many_fault_flags;
+// Test controls of the bounded waits, set only through mol_debug_wait_test.
+__device__ unsigned int g_many_test_stall;
+__device__ unsigned long long g_many_wait_limit_ns = kWaitLimitNs;
 
 namespace {
 
@@ -43,6 +46,11 @@ struct Geo {
   static constexpr uint32_t kS = 0, kO = 2 * kM, kP = kApart ? kO + 2 * D : kS, kPStep = kApart ? kM / 2 : kM;
   static constexpr uint32_t kCols = 512;
 };
+
+// A whole warp's bounded wait, whose lanes agree on its outcome.
+MOL_DEV bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls, limit_ns));
+}
 
 MOL_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
   asm volatile(
@@ -255,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   bool fault = false;
+  const unsigned long long limit = g_many_wait_limit_ns;
   // (each role begins its own, from shared memory: nothing of it is held in registers before)
   auto begin = [&](attn::Walk& w) {
     w.left = 0;
@@ -270,14 +279,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
     const int copies = kM / per;
     attn::Walk w;
-    for (begin(w); w.more() && !fault; next(w)) {
+    for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
       const Block& k = w.k;
       const int32_t* pages = a.page_table + k.b * a.table_stride;
       // lane p: page p of the block's i-th tile, asked for a tile ahead
       auto look = [&](int i) {
         const int j = (k.t0 + w.first + i) * kM + lane * per;
-        return i < w.count && lane < copies && j + per > k.lo && j < k.hi
-                   ? __ldg(pages + divide(j, a.by_page)) : -1;
+        if (i >= w.count || lane >= copies || j + per <= k.lo || j >= k.hi) return -1;
+        const int p = divide(j, a.by_page);
+        return MOL_CHECK(p >= 0 && p < a.max_pages, MOL_CHECK_COLUMN, p) ? __ldg(pages + p) : -1;
       };
       int page = look(0);
       for (int i = 0; i < w.count && !fault; ++i, ++n) {
@@ -287,10 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!held) page = a.num_pages;  // past the end: zeros
         const int j = (k.t0 + w.first + i) * kM + lane * per;
         const int offset = j - divide(j, a.by_page) * a.page_size;
+        (void)MOL_CHECK(lane >= copies || (offset >= 0 && offset + per <= a.page_size), MOL_CHECK_TMA_COORD,
+                        offset);
         if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
         for (int kv = 0; kv < 2 && !fault; ++kv, ++u) {
           const int s = (int)(u % G::kSlots);
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, kPolls))) {
+          if (!warp_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, limit)) {
             fault = true;
             break;
           }
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
                           x * 64, offset, w.h, page, &full[s]);
           if (i + kv == 0) {  // the queries behind the first keys, which need not wait for the block before
-            if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty, (seg - 1) & 1, kPolls))) {
+            if (seg > 0 && !warp_wait(&q_empty, (seg - 1) & 1, limit)) {
               fault = true;
               ++u;
               break;
@@ -322,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (fault) {  // nothing of its own left in flight
       for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; i < u; ++i)
-        mbar_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, kPolls);
-      if (seg > 0) mbar_wait(&q_full, (seg - 1) & 1, kPolls);
+        (void)warp_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, limit);
+      if (seg > 0) (void)warp_wait(&q_full, (seg - 1) & 1, limit);
     }
   } else if (warp > 9) {
     // ------------------------------------------------------------ values that not every row sees
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < w.count && !fault; ++i, ++n)
         for (int kv = 0; kv < 2; ++kv, ++u) {
           const int s = (int)(u % G::kSlots);
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (u / G::kSlots) & 1, kPolls))) {
+          if (!warp_wait(&full[s], (u / G::kSlots) & 1, limit)) {
             fault = true;
             break;
           }
@@ -375,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader = lane == 0;
     const uint32_t q_at = desc_low(smem_u32(smem)), ring_at = desc_low(smem_u32(ring));
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls))) fault = true;
+      if (!warp_wait(bar, parity, limit)) fault = true;
       return !fault;
     };
     auto wait_slot = [&](uint32_t i) { return wait(&full[i % G::kSlots], (i / G::kSlots) & 1); };
@@ -444,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the products are done, and their commits have arrived
     commit(leader, &all_done);
-    if (!__all_sync(0xffffffffu, mbar_wait(&all_done, 0, kPolls))) fault = true;
+    if (!warp_wait(&all_done, 0, limit)) fault = true;
   }
   } else {
     // ------------------------------------------------------------ softmax
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = -INFINITY, sum = 0.f;
         for (int i = 0; i < count; ++i) {
           const int j0 = (k.t0 + w.first + i) * kM;
-          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1, kPolls))) {
+          if (!warp_wait(&s_full[t], ns & 1, limit)) {
             fault = true;
             break;
           }
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
           // the products before these weights are done (where these lie over scores, those came behind them)
           if (G::kApart && ns > 1) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&o_full[t], ns & 1, kPolls))) {
+            if (!warp_wait(&o_full[t], ns & 1, limit)) {
               fault = true;
               break;
             }
@@ -550,8 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = u + 2 * i + 1;  // of the tile's values
           bool plain = false;
           if (edge) {  // they have been looked through
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(&seen[slot % G::kSlots], (slot / G::kSlots) & 1, kPolls))) {
+            if (!warp_wait(&seen[slot % G::kSlots], (slot / G::kSlots) & 1, limit)) {
               fault = true;
               break;
             }
@@ -599,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[t]);
         }
-        if (fault || !__all_sync(0xffffffffu, mbar_wait(&o_full[t], (G::kApart ? ns - 1 : no) & 1, kPolls))) {
+        if (fault || !warp_wait(&o_full[t], (G::kApart ? ns - 1 : no) & 1, limit)) {
           fault = true;
           break;
         }
@@ -607,8 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // ---------------------------------------------------------- the rows, or a part of them
         const int slot = 2 * (int)blockIdx.x + (begins ? 1 : 0);
-        const bool mine = local < in_tile;
         const int at = t * tile_rows + local, r = k.row0 + at, token = divide(r, a.by_group);
+        const bool mine = local < in_tile && MOL_CHECK(k.s.start + token < a.num_tokens, MOL_CHECK_ROW,
+                                                       k.s.start + token);
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;
@@ -726,6 +738,19 @@ cudaError_t take_attn_faults(unsigned* out) {
   if (e != cudaSuccess) return e;
   const unsigned zero = 0;
   return cudaMemcpyToSymbol(g_many_fault_flags, &zero, sizeof(unsigned));
+}
+
+cudaError_t set_attn_wait_test(unsigned stall, unsigned long long limit_ns) {
+  const cudaError_t e = cudaMemcpyToSymbol(g_many_test_stall, &stall, sizeof(unsigned));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_many_wait_limit_ns, &limit_ns, sizeof(limit_ns));
+}
+
+cudaError_t take_many_checks(unsigned long long* first, unsigned long long* count) {
+  CheckRecord r;
+  const cudaError_t e = take_check_record_here(&r);
+  *first = r.first;
+  *count = r.count;
+  return e;
 }
 
 }  // namespace mol

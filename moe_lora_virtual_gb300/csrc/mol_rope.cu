@@ -72,8 +72,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_cons
     for (int i = threadIdx.x; i < a.rotary_dim / 2; i += THREADS)
       cs[i] = turn(p, a.inv_freq[i], a.magnitude);
   }
-  const bool keep = slot >= 0 && slot < a.num_slots;
-  const int page = keep ? divide(slot, a.by_page) : 0;
+  const bool in = slot >= 0 && slot < a.num_slots;
+  const int page = in ? divide(slot, a.by_page) : 0;
+  const bool keep = in && MOL_CHECK(slot - page * a.page_size >= 0 && slot - page * a.page_size < a.page_size,
+                                    MOL_CHECK_ROW, slot);
   const int64_t cache_at = (int64_t)page * a.page_stride + (int64_t)(slot - page * a.page_size) * a.token_stride;
   if (keep) {
 #pragma unroll 1
@@ -137,6 +139,14 @@ cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream) {
     return launch_pdl(kernel, dim3((unsigned)a.num_tokens), dim3(threads), 0, stream, a);
   };
   return a.num_tokens > 4 * 152 ? go(rope_kernel<128, 16>, 128) : go(rope_kernel<256, 4>, 256);
+}
+
+cudaError_t take_rope_checks(unsigned long long* first, unsigned long long* count) {
+  CheckRecord r;
+  const cudaError_t e = take_check_record_here(&r);
+  *first = r.first;
+  *count = r.count;
+  return e;
 }
 
 }  // namespace mol
