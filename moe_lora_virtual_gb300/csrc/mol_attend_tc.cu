@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kM / 32; ++x) {
               const uint32_t sees = columns_seen(x, lo, hi, held, per);
+              if (__all_sync(0xffffffffu, sees == 0xffffffffu)) continue;  // (its maximum stands)
               m4[x] = -INFINITY;
 #pragma unroll
               for (int y = 0; y < 32; ++y) {
