@@ -84,6 +84,13 @@ MOL_DEV void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t
       "r"(a_tmem), "r"(b_low | atom << 16), "r"(idesc), "r"(accumulate), "r"(leader), "r"(kDescHigh)
       : "memory");
 }
+MOL_DEV void arrive(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
 MOL_DEV void commit(uint32_t leader, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
@@ -391,6 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       return !fault;
     };
     auto wait_slot = [&](uint32_t i) { return wait(&full[i % G::kSlots], (i / G::kSlots) & 1); };
+    // Two barriers with one vote where both have completed (a wait is some 100 cycles without a product).
+    auto wait_two = [&](uint64_t* a0, uint32_t p0, uint64_t* a1, uint32_t p1) {
+      const bool one = mbar_try_wait(a0, p0), other = mbar_try_wait(a1, p1);
+      return __all_sync(0xffffffffu, one && other) || (wait(a0, p0) && wait(a1, p1));
+    };
     auto scores = [&](int t, uint32_t slot) {
       const uint32_t q = q_at + t * (G::kTileBytes >> 4);
       const uint32_t k = ring_at + (slot % G::kSlots) * (G::kTileBytes >> 4);
@@ -400,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_ss(leader, tmem + G::kS + t * kM, q + off, k + off, kScores, kk != 0);
       }
       commit(leader, &s_full[t]);
-      if (leader) mbar_arrive(&s_full[t]);
+      arrive(leader, &s_full[t]);
     };
     attn::Walk w;
     for (begin(w); w.more() && !fault; next(w)) {
@@ -415,16 +427,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < count && !fault; ++i) {
         // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
         const bool more = i + 1 < count;
-        if (!wait_slot(u + 1) || (more && !wait_slot(u + 2))) break;
+        const uint32_t k1 = more ? u + 2 : u + 1;
+        if (!wait_two(&full[(u + 1) % G::kSlots], ((u + 1) / G::kSlots) & 1, &full[k1 % G::kSlots],
+                      (k1 / G::kSlots) & 1))
+          break;
         // the next tile's scores as soon as these have been read, where the weights lie apart
         if (G::kApart && more) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t == tiles || !wait(&s_read[t], np[t] & 1)) break;
-            tc_fence_after();
-            scores(t, u + 2);
-          }
-          if (fault) break;
+          const bool both = tiles == 2;
+          if (!wait_two(&s_read[0], np[0] & 1, &s_read[both], (both ? np[1] : np[0]) & 1)) break;
+          tc_fence_after();
+          scores(0, u + 2);
+          if (both) scores(1, u + 2);
           commit(leader, &empty[(u + 2) % G::kSlots]);
           if (i + 2 == count) commit(leader, &q_empty);
         }

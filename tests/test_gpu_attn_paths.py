@@ -106,6 +106,20 @@ def test_long(env, lens, Hq, Hkv, D, page, window):
     near(torch, attend(env, p, window), p, D ** -0.5, window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("most", [3, 6, 90])
+def test_many_blocks_of_unlike_sizes(env, D, window, most):
+    """A thread block goes through several blocks of rows, of one query tile and of two, of one tile of
+    keys and of several, and through parts of some."""
+    torch, _ = env
+    rng = np.random.default_rng(D + window + most)
+    lens = [(int(rng.integers(1, most + 1)), int(rng.integers(1, 1200))) for _ in range(150)]
+    lens = [(min(n, kv), kv) for n, kv in lens]
+    p = au.problem(torch, most, lens, 8, 4, D, 16)
+    near(torch, attend(env, p, window), p, D ** -0.5, window)
+
+
 @pytest.mark.parametrize("scale", [1e-4, 3.0])
 @pytest.mark.parametrize("lens", [[(1, 3000)], [(200, 3000)]])
 def test_flat_and_sharp_weights(env, scale, lens):
