@@ -557,7 +557,6 @@ cudaError_t prepare_attn_kernels() {
   cudaError_t e = prepare<64, 1>();
   if (e == cudaSuccess) e = prepare<64, 2>();
   if (e == cudaSuccess) e = prepare<128, 1>();
-  if (e == cudaSuccess) e = prepare<128, 2>();
   if (e == cudaSuccess) e = prepare<256, 1>();
   if (e == cudaSuccess) e = attn::prepare_many();
   return e;
@@ -569,28 +568,26 @@ cudaError_t prepare_attn_kernels() {
 //   64 values a head:  12 rows 32 | 40 | 54, 16 rows 33 | 40 | 54, 24 rows 49 | 41 | 54, 48 rows 65 | 68 | 55
 //   128 values:        12 rows 52 | 66 | 61, 16 rows 52 | 66 | 61, 24 rows 91 | 68 | 61, 48 rows 131 | 119 | 62
 // A call with both of decoding sequences and prompts pays: 200 rows of one sequence in blocks of 16 read its
-// keys 13 times (from L2). Pages that attend_many cannot copy, and 256 values a head, take blocks of 16 and 32.
+// keys 13 times (from L2). 256 values a head take blocks of 16 whatever the rows.
 enum class Form { kFew16, kFew32, kMany };
-static Form form(int64_t num_seqs, int64_t rows, int num_pages, int page_size, int head_dim) {
+static Form form(int64_t num_seqs, int64_t rows, int head_dim) {
   if (rows <= 16 * num_seqs || head_dim == 256) return Form::kFew16;
-  if (num_pages == 0 || !attn::many_fits(page_size, head_dim)) return Form::kFew32;
   return head_dim == 64 && rows <= 32 * num_seqs ? Form::kFew32 : Form::kMany;
 }
 
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
   if (num_seqs <= 0 || num_tokens <= 0) return 0;
-  const int64_t rows = num_tokens * group;
-  if (rows <= 16 * num_seqs || head_dim == 256) return attn::parts_bytes(attn::kMaxGrid, 16, head_dim);
-  // (whatever the pages)
-  return std::max(attn::parts_bytes(attn::kMaxGrid, 32, head_dim), attn::many_bytes(group, head_dim));
+  const Form f = form(num_seqs, num_tokens * group, head_dim);
+  return f == Form::kMany ? attn::many_bytes(group, head_dim)
+                          : attn::parts_bytes(attn::kMaxGrid, f == Form::kFew32 ? 32 : 16, head_dim);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
-  switch (form(a.num_seqs, (int64_t)a.num_tokens * a.group, a.num_pages, a.page_size, a.head_dim)) {
+  switch (form(a.num_seqs, (int64_t)a.num_tokens * a.group, a.head_dim)) {
     case Form::kMany:
       return attn::launch_many(a, stream);
     case Form::kFew32:
-      return a.head_dim == 64 ? attend_few<64, 2>(a, stream) : attend_few<128, 2>(a, stream);
+      return attend_few<64, 2>(a, stream);
     default:
       return a.head_dim == 64    ? attend_few<64, 1>(a, stream)
              : a.head_dim == 128 ? attend_few<128, 1>(a, stream)

@@ -262,9 +262,7 @@ cudaError_t launch_join(const AttnArgs& a, int grid, int rows, const Parts& p, c
 int sms();
 constexpr int kMaxGrid = 2 * 152;
 
-// Many rows a sequence (mol_attend_tc.cu). Whether its tiles can be loaded from
-// pages of this size, for heads of this width.
-bool many_fits(int page_size, int head_dim);
+// Many rows a sequence (mol_attend_tc.cu): 64 or 128 values a head.
 size_t many_bytes(int group, int head_dim);
 cudaError_t prepare_many();
 cudaError_t launch_many(const AttnArgs& a, cudaStream_t stream);

@@ -185,19 +185,36 @@ MOL_DEV float2 add2(float2 a, float2 b) {
 }
 
 
-// Of a tile's columns 32 w .. 32 w + 31 those that lie in (lo, hi] on a page that is held (bit p of
-// `held`: the tile's columns p * per and on).
-MOL_DEV uint32_t columns_seen(int w, int lo, int hi, uint32_t held, int per) {
+// Which of a tile's tokens lie in the cache: bit p for those of page p of the tile, or a bit a token and
+// whether all do. (Copied page by page, 64 values a head are faster with the second, mixed batch 98 us
+// against 104, and 128 with the first, chunk of 509 tokens 182 against 200.)
+template <bool TOKENS>
+struct Held {
+  uint32_t pages;
+  MOL_DEV bool all(int per) const { return pages == (uint32_t)(((uint64_t)1 << (kM / per)) - 1); }
+  MOL_DEV uint32_t columns(int w, int per) const {  // 32 w .. 32 w + 31
+    uint32_t c = 0xffffffffu;
+    const int log_per = 31 - __clz(per);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (!((pages >> ((32 * w + 8 * b) >> log_per)) & 1)) c &= ~(0xffu << (8 * b));
+    return c;
+  }
+};
+template <>
+struct Held<true> {
+  uint32_t tokens[4];
+  uint32_t whole;
+  MOL_DEV bool all(int) const { return whole != 0; }
+  MOL_DEV uint32_t columns(int w, int) const { return tokens[w]; }
+};
+// Of a tile's columns 32 w .. 32 w + 31 those that lie in (lo, hi] and whose token is held.
+template <typename H>
+MOL_DEV uint32_t columns_seen(int w, int lo, int hi, const H& held, int per) {
   const int first = max(lo + 1 - 32 * w, 0), last = min(hi - 32 * w, 31);
   if (first > 31 || last < first) return 0u;
-  uint32_t sees = (0xffffffffu << first) & (0xffffffffu >> (31 - last));
-  const int log_per = 31 - __clz(per);
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    if (!((held >> ((32 * w + 8 * b) >> log_per)) & 1)) sees &= ~(0xffu << (8 * b));
-  return sees;
+  return (0xffffffffu << first) & (0xffffffffu >> (31 - last)) & held.columns(w, per);
 }
-
 // M = 128, N = 128, both operands with the contraction along their rows.
 constexpr uint32_t kScores = IDesc<kM, kM>::kValue;
 // N = D, the second operand's rows are the contraction.
@@ -215,21 +232,25 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys); Q0 K', Q1 K', P0 V, P1 V
 //                   for 64 values a head, whose weights need not wait for the scores' place
 //   warp 9          copies the queries and, page by page, keys and values (TMA, 128-byte swizzle) into a
-//                   ring of tiles
+//                   ring of tiles; token by token (cp.async) from pages whose tokens make no such copies
 //   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
 //                   not finite are zeroed where no row sees them; where another row does, the tile's
 //                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
 // Tiles are dealt as in attend_few; parts of blocks join in launch_join. Pages outside the cache are zeros
 // (the copy's fill); what a row does not see is replaced among its scores.
-template <int D>
+template <int D, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
   using G = Geo<D>;
+  constexpr bool kTokens = GATHER || D == 64;
+  // tokens that are gathered take two warps, keys and values, and leave one to look through these
+  constexpr int kLookers = GATHER ? 1 : 2;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], seen[G::kSlots], s_full[2],
       p_full[2], o_full[2], s_read[2];
-  __shared__ uint32_t s_tmem, s_held[kHeldRing], s_skip[2], s_bad[G::kSlots];
+  __shared__ Held<kTokens> s_held[kHeldRing];
+  __shared__ uint32_t s_tmem, s_skip[2], s_bad[G::kSlots];
   __shared__ int s_scan[kThreads / 32 + 1];
   __shared__ Place s_place;
   __shared__ attn::Run s_run;
@@ -242,9 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&q_empty, 1);
     mbar_init(&all_done, 1);
     for (int s = 0; s < G::kSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 3);  // the last products' commit, and the two warps that look through values
-      mbar_init(&seen[s], 2);
+      mbar_init(&full[s], GATHER ? 32 : 1);
+      mbar_init(&empty[s], 1 + kLookers);  // the last products' commit, and the warps that look through values
+      mbar_init(&seen[s], kLookers);
       s_bad[s] = 0;
     }
     for (int t = 0; t < 2; ++t) {
@@ -269,6 +290,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) s_run = run;
     __syncthreads();
   }
+  auto held_at = [&](uint32_t n) {
+    Held<kTokens> h;
+    const volatile Held<kTokens>* at = &s_held[n % kHeldRing];
+    if constexpr (kTokens) {
+      for (int x = 0; x < 4; ++x) h.tokens[x] = at->tokens[x];
+      h.whole = at->whole;
+    } else {
+      h.pages = at->pages;
+    }
+    return h;
+  };
   bool fault = false;
   const unsigned long long limit = g_many_wait_limit_ns;
   // (each role begins its own, from shared memory: nothing of it is held in registers before)
@@ -280,49 +312,133 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 9) {
+  if (warp == 9 || (GATHER && warp == 10)) {
     // ------------------------------------------------------------ copies
     uint32_t u = 0, n = 0, seg = 0;  // ring slots used, tiles, blocks
-    const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
-    const int copies = kM / per;
-    attn::Walk w;
-    for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
-      const Block& k = w.k;
-      const int32_t* pages = a.page_table + k.b * a.table_stride;
-      // lane p: page p of the block's i-th tile, asked for a tile ahead
-      auto look = [&](int i) {
-        const int j = (k.t0 + w.first + i) * kM + lane * per;
-        if (i >= w.count || lane >= copies || j + per <= k.lo || j >= k.hi) return -1;
-        const int p = divide(j, a.by_page);
-        return MOL_CHECK(p >= 0 && p < a.max_pages, MOL_CHECK_COLUMN, p) ? __ldg(pages + p) : -1;
-      };
-      int page = look(0);
-      for (int i = 0; i < w.count && !fault; ++i, ++n) {
-        const int next_page = look(i + 1);
-        const bool held = page >= 0 && page < a.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, held);
-        if (!held) page = a.num_pages;  // past the end: zeros
-        const int j = (k.t0 + w.first + i) * kM + lane * per;
-        const int offset = j - divide(j, a.by_page) * a.page_size;
-        (void)MOL_CHECK(lane >= copies || (offset >= 0 && offset + per <= a.page_size), MOL_CHECK_TMA_COORD,
-                        offset);
-        if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing] = mask;
-        for (int kv = 0; kv < 2 && !fault; ++kv, ++u) {
+    if constexpr (!GATHER) {
+      const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
+      const int copies = kM / per;
+      attn::Walk w;
+      for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
+        const Block& k = w.k;
+        const int32_t* pages = a.page_table + k.b * a.table_stride;
+        // lane p: page p of the block's i-th tile, asked for a tile ahead
+        auto look = [&](int i) {
+          const int j = (k.t0 + w.first + i) * kM + lane * per;
+          if (i >= w.count || lane >= copies || j + per <= k.lo || j >= k.hi) return -1;
+          const int p = divide(j, a.by_page);
+          return MOL_CHECK(p >= 0 && p < a.max_pages, MOL_CHECK_COLUMN, p) ? __ldg(pages + p) : -1;
+        };
+        int page = look(0);
+        for (int i = 0; i < w.count && !fault; ++i, ++n) {
+          const int next_page = look(i + 1);
+          const bool held = page >= 0 && page < a.num_pages;
+          const uint32_t mask = __ballot_sync(0xffffffffu, held);
+          if (!held) page = a.num_pages;  // past the end: zeros
+          const int j = (k.t0 + w.first + i) * kM + lane * per;
+          const int offset = j - divide(j, a.by_page) * a.page_size;
+          (void)MOL_CHECK(lane >= copies || (offset >= 0 && offset + per <= a.page_size), MOL_CHECK_TMA_COORD,
+                          offset);
+          if constexpr (kTokens) {
+            const Held<false> by_page{mask};
+            if (lane < 4) *(volatile uint32_t*)&s_held[n % kHeldRing].tokens[lane] = by_page.columns(lane, per);
+            if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing].whole = by_page.all(per);
+            __syncwarp();
+          } else {
+            if (lane == 0) *(volatile uint32_t*)&s_held[n % kHeldRing].pages = mask;
+          }
+          for (int kv = 0; kv < 2 && !fault; ++kv, ++u) {
+            const int s = (int)(u % G::kSlots);
+            if (!warp_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, limit)) {
+              fault = true;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)G::kTileBytes);
+            __syncwarp();
+            if (lane < copies)
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
+                            x * 64, offset, w.h, page, &full[s]);
+            if (i + kv == 0) {  // the queries behind the first keys, which need not wait for the block before
+              if (seg > 0 && !warp_wait(&q_empty, (seg - 1) & 1, limit)) {
+                fault = true;
+                ++u;
+                break;
+              }
+              const bool two = k.nrows > tile_rows;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full, (uint32_t)(tile_rows * 128 * (D / 64) * (two ? 2 : 1)));
+                for (int t = 0; t < (two ? 2 : 1); ++t)
+                  for (int x = 0; x < D / 64; ++x)
+                    tma_load_4d(smem + t * G::kTileBytes + x * G::kHalf, &map_q, x * 64, 0, w.h,
+                                k.s.start + divide(k.row0, a.by_group) + t * tile_tokens, &q_full);
+              }
+              ++seg;
+            }
+          }
+          page = next_page;
+        }
+      }
+    } else {
+      // token by token, 16 bytes a lane: keys by one warp, values by the other
+      constexpr int kChunks = D / 8;
+      const int kv = warp - 9;
+      const uint16_t* src = kv ? a.v : a.k;
+      u = kv;
+      attn::Walk w;
+      for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
+        const Block& k = w.k;
+        const int32_t* pages = a.page_table + k.b * a.table_stride;
+        // lane l: the pages of tokens l, 32 + l, 64 + l, 96 + l of the block's i-th tile
+        int page[4], next_page[4];
+        auto look = [&](int i, int (&to)[4]) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int j = (k.t0 + w.first + i) * kM + 32 * x + lane;
+            const int p = divide(max(j, 0), a.by_page);
+            to[x] = i < w.count && j >= k.lo && j < k.hi && MOL_CHECK(p < a.max_pages, MOL_CHECK_COLUMN, p)
+                        ? __ldg(pages + p) : -1;
+          }
+        };
+        look(0, page);
+        for (int i = 0; i < w.count && !fault; ++i, ++n, u += 2) {
+          look(i + 1, next_page);
+          int64_t at[4];
+          uint32_t held[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int j = (k.t0 + w.first + i) * kM + 32 * x + lane;
+            const bool in = page[x] >= 0 && page[x] < a.num_pages;
+            at[x] = in ? page[x] * a.page_stride + (j - divide(j, a.by_page) * a.page_size) * a.token_stride +
+                             w.h * a.head_stride : 0;
+            held[x] = __ballot_sync(0xffffffffu, in);
+            page[x] = next_page[x];
+          }
+          if (kv == 0 && lane == 0) {
+            volatile Held<kTokens>* to = &s_held[n % kHeldRing];
+            for (int x = 0; x < 4; ++x) to->tokens[x] = held[x];
+            to->whole = (held[0] & held[1] & held[2] & held[3]) == 0xffffffffu;
+          }
+          __syncwarp();
           const int s = (int)(u % G::kSlots);
           if (!warp_wait(&empty[s], ((u / G::kSlots) & 1) ^ 1, limit)) {
             fault = true;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)G::kTileBytes);
-          __syncwarp();
-          if (lane < copies)
-            for (int x = 0; x < D / 64; ++x)
-              tma_load_4d(ring + s * G::kTileBytes + x * G::kHalf + lane * per * 128, kv ? &map_v : &map_k,
-                          x * 64, offset, w.h, page, &full[s]);
-          if (i + kv == 0) {  // the queries behind the first keys, which need not wait for the block before
+          unsigned char* tile = ring + s * G::kTileBytes;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll 8
+            for (int y = 0; y < kChunks; ++y) {
+              const int row = (y * 32 + lane) / kChunks, ch = (y * 32 + lane) % kChunks;
+              cp_async16_zfill(tile + (ch >> 3) * G::kHalf + (32 * x + row) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                               src + __shfl_sync(0xffffffffu, at[x], row) + ch * 8,
+                               (held[x] >> row) & 1 ? 16u : 0u);
+            }
+          cp_async_arrive_noinc(&full[s]);
+          if (i == 0 && kv == 0) {
             if (seg > 0 && !warp_wait(&q_empty, (seg - 1) & 1, limit)) {
               fault = true;
-              ++u;
               break;
             }
             const bool two = k.nrows > tile_rows;
@@ -336,11 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++seg;
           }
         }
-        page = next_page;
       }
+      cp_async_wait_all();
     }
-    if (fault) {  // nothing of its own left in flight
-      for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; i < u; ++i)
+    if (fault) {  // nothing left in flight (gathered tokens are not, by now)
+      for (uint32_t i = u > (uint32_t)G::kSlots ? u - G::kSlots : 0; !GATHER && i < u; ++i)
         (void)warp_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, limit);
       if (seg > 0) (void)warp_wait(&q_full, (seg - 1) & 1, limit);
     }
@@ -348,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ values that not every row sees
     uint32_t u = 0, n = 0;
     const int per = a.page_size < kM ? a.page_size : kM;
-    const uint32_t all = (uint32_t)(((uint64_t)1 << (kM / per)) - 1);
     attn::Walk w;
     for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
@@ -363,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const int j0 = (k.t0 + w.first + i) * kM;
-          if (kv && (*(volatile uint32_t*)&s_held[n % kHeldRing] != all || j0 + kM - 1 > pos_first ||
+          if (kv && (!held_at(n).all(per) || j0 + kM - 1 > pos_first ||
                      (a.window > 0 && j0 <= pos_last - a.window))) {
             unsigned char* v = ring + s * G::kTileBytes;
             bool bad = false;
 #pragma unroll 4
-            for (int x = tid - 10 * 32; x < G::kTileBytes / 16; x += 64)
+            for (int x = tid - (12 - kLookers) * 32; x < G::kTileBytes / 16; x += kLookers * 32)
               if (attn::not_finite(lds16(v + x * 16))) {
                 const int j = j0 + (x >> 3) % kM;
                 if (j < k.lo || j >= k.hi)
@@ -397,7 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(bar, parity, limit)) fault = true;
       return !fault;
     };
-    auto wait_slot = [&](uint32_t i) { return wait(&full[i % G::kSlots], (i / G::kSlots) & 1); };
+    // (what came token by token is the generic proxy's; the products read through the async one)
+    auto wait_slot = [&](uint32_t i) {
+      const bool ok = wait(&full[i % G::kSlots], (i / G::kSlots) & 1);
+      if (GATHER) fence_proxy_async_smem();
+      return ok;
+    };
     // Two barriers with one vote where both have completed (a wait is some 100 cycles without a product).
     auto wait_two = [&](uint64_t* a0, uint32_t p0, uint64_t* a1, uint32_t p1) {
       const bool one = mbar_try_wait(a0, p0), other = mbar_try_wait(a1, p1);
@@ -431,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_two(&full[(u + 1) % G::kSlots], ((u + 1) / G::kSlots) & 1, &full[k1 % G::kSlots],
                       (k1 / G::kSlots) & 1))
           break;
+        if (GATHER) fence_proxy_async_smem();
         // the next tile's scores as soon as these have been read, where the weights lie apart
         if (G::kApart && more) {
           const bool both = tiles == 2;
@@ -502,11 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++ns;
           tc_fence_after();
-          const uint32_t held = *(volatile uint32_t*)&s_held[(n + i) % kHeldRing];
+          const Held<kTokens> held = held_at(n + i);
           const int per = a.page_size < kM ? a.page_size : kM;
-          const int copies = kM / per;
-          const bool all_held = copies == 32 ? held == 0xffffffffu : held == (1u << copies) - 1;
-          const bool edge = !all_held || j0 + kM - 1 > pos_first || (a.window > 0 && j0 <= pos_last - a.window);
+          const bool edge = !held.all(per) || j0 + kM - 1 > pos_first ||
+                            (a.window > 0 && j0 <= pos_last - a.window);
           const int hi = pos - j0, lo = a.window > 0 ? hi - a.window : -1;  // seen: lo < column <= hi
           uint32_t r[kM];
           float m4[kM / 32];
@@ -600,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t pair = tmem_ld_x1(tp + (y >> 1));
                 tmem_wait_ld();
                 const float wt = y & 1 ? bf16_hi(pair) : bf16_lo(pair);
-                const bool sees = (columns_seen(y >> 5, lo, hi, held, per) >> (y & 31)) & 1;
+                const bool sees = (columns_seen(y >> 5, lo, hi, held_at(n + i), per) >> (y & 31)) & 1;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                   const int ch = ((x & 63) + e) >> 3;
@@ -694,7 +814,12 @@ bool encode(CUtensorMap* map, const void* p, const cuuint64_t (&dims)[4], const 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+// Pages that tensor copies can take a tile from: parts of 8 tokens (a swizzle's rows) or more, or whole tiles.
+bool in_copies(const AttnArgs& a) {
+  return a.num_pages > 0 && (a.page_size % kM == 0 || (a.page_size >= 8 && kM % a.page_size == 0));
+}
+
+template <int D, bool GATHER>
 cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int tokens = kM / a.group, per = std::min(a.page_size, kM);
   CUtensorMap q, k, v;
@@ -703,24 +828,27 @@ cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int64_t page_strides[3] = {a.token_stride, a.head_stride, a.page_stride};
   if (!encode(&q, a.q, {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_tokens},
               {a.q_head_stride, a.q_head_stride * a.group, a.q_token_stride},
-              {64, (cuuint32_t)a.group, 1, (cuuint32_t)tokens}) ||
-      !encode(&k, a.k, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}) ||
-      !encode(&v, a.v, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}))
+              {64, (cuuint32_t)a.group, 1, (cuuint32_t)tokens}))
+    return cudaErrorInvalidValue;
+  k = v = q;  // (not read where tokens are gathered)
+  if (!GATHER && (!encode(&k, a.k, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1}) ||
+                  !encode(&v, a.v, page_dims, page_strides, {64, (cuuint32_t)per, 1, 1})))
     return cudaErrorInvalidValue;
   const int grid = attn::sms(), rows = 2 * tokens * a.group;
   a.by_grid = divider(grid);
-  const cudaError_t e = launch_pdl(attend_many_kernel<D>, dim3(grid), dim3(kThreads), Geo<D>::kSmem, stream, q,
-                                   k, v, a, tokens);
+  const cudaError_t e = launch_pdl(attend_many_kernel<D, GATHER>, dim3(grid), dim3(kThreads), Geo<D>::kSmem,
+                                   stream, q, k, v, a, tokens);
   if (e != cudaSuccess) return e;
   return attn::launch_join(a, grid, rows, attn::parts(a.workspace, grid, rows, D), stream);
 }
 
-}  // namespace
-
-bool attn::many_fits(int page_size, int head_dim) {
-  const bool whole = page_size % kM == 0 || (page_size >= 8 && kM % page_size == 0);
-  return whole && (head_dim == 64 || head_dim == 128);
+template <int D, bool GATHER>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attend_many_kernel<D, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Geo<D>::kSmem);
 }
+
+}  // namespace
 
 size_t attn::many_bytes(int group, int head_dim) {
   return attn::parts_bytes(kMaxGrid / 2, 2 * (kM / group) * group, head_dim);
@@ -735,16 +863,16 @@ cudaError_t attn::prepare_many() {
       g_encode_status = cudaErrorNotSupported;
   });
   if (g_encode_status != cudaSuccess) return g_encode_status;
-  const cudaError_t e = cudaFuncSetAttribute(
-      attend_many_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<64>::kSmem);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(attend_many_kernel<128>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)Geo<128>::kSmem);
+  cudaError_t e = prepare<64, false>();
+  if (e == cudaSuccess) e = prepare<64, true>();
+  if (e == cudaSuccess) e = prepare<128, false>();
+  if (e == cudaSuccess) e = prepare<128, true>();
+  return e;
 }
 
 cudaError_t attn::launch_many(const AttnArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? many<64>(a, stream) : many<128>(a, stream);
+  if (in_copies(a)) return a.head_dim == 64 ? many<64, false>(a, stream) : many<128, false>(a, stream);
+  return a.head_dim == 64 ? many<64, true>(a, stream) : many<128, true>(a, stream);
 }
 
 cudaError_t take_attn_faults(unsigned* out) {

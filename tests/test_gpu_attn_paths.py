@@ -201,12 +201,13 @@ def test_past_32_bit_offsets(env, D, Hkv, page):
         assert torch.equal(got.cpu(), attend(env, dict(small, starts=starts.cpu())))
 
 
+@pytest.mark.parametrize("page", [16, 5])
 @pytest.mark.parametrize("D", [64, 128])
-def test_wait_runs_out_sets_flag_then_device_recovers(env, D):
+def test_wait_runs_out_sets_flag_then_device_recovers(env, D, page):
     """With nothing copied every wait of the form for many rows gives up: the call returns, bit 0 is
     reported, nothing was written; the same call right after is right, with no bit set."""
     torch, mol = env
-    p = au.problem(torch, D, [(100, 300), (20, 700)], 4, 2, D, 16)
+    p = au.problem(torch, D, [(100, 300), (20, 700)], 4, 2, D, page)
     want = attend(env, p)
     assert mol.mol_take_fault_flags() == 0
     try:
