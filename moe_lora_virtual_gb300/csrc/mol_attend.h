@@ -67,6 +67,7 @@ struct AttnArgs {
   uint16_t* out;
   int64_t out_token_stride, out_head_stride;
   void* workspace;
+  bool whole;  // blocks of rows are not dealt out in parts (set by the launches)
 };
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim);
 cudaError_t prepare_attn_kernels();
