@@ -28,7 +28,8 @@ NATIVE_SOURCE = os.path.join(CSRC, "mol_block_py.cpp")
 SOURCES = ["mol_abi.cu", "mol_align.cu", "mol_lora.cu", "mol_umma.cu", "mol_stage.cu",
            "mol_expand_tc.cu", "mol_block_abi.cu", "mol_block.cu", "mol_moe.cu",
            "mol_moe_bf16.cu", "mol_moe_w4_32.cu", "mol_moe_w4_64.cu", "mol_moe_w4_128.cu",
-           "mol_attn_abi.cu", "mol_rope.cu", "mol_attend.cu", "mol_attend_tc.cu"]
+           "mol_attn_abi.cu", "mol_rope.cu", "mol_attend.cu", "mol_attend_tc.cu",
+           "mol_attend_wide.cu"]
 HEADERS = ["mol_device.cuh", "mol_internal.h", "mol_tc.cuh", "mol_moe.h", "mol_moe.cuh",
            "mol_attend.h", "mol_attend.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -243,11 +243,11 @@ int32_t mol_take_check_record(uint64_t* first, uint64_t* count) {
   if (e != cudaSuccess) return cuda_fail(e);
   // in the path's order: align, item shrink and expands, tcgen05 shrink, fused stage,
   // tcgen05 expand, norm and router, experts and 4-bit linear, rotation, attention
-  cudaError_t (*const take[10])(unsigned long long*, unsigned long long*) = {
+  cudaError_t (*const take[11])(unsigned long long*, unsigned long long*) = {
       mol::take_align_checks, mol::take_lora_checks,      mol::take_tc_checks,
       mol::take_stage_checks, mol::take_expand_tc_checks, mol::take_block_checks,
       mol::take_moe_checks,   mol::take_rope_checks,      mol::take_attn_checks,
-      mol::take_many_checks};
+      mol::take_many_checks,  mol::take_wide_checks};
   unsigned long long f = 0, n = 0;
   for (auto fn : take) {
     unsigned long long fi = 0, ni = 0;

@@ -17,18 +17,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kExtra = 1;             // units that a block takes beside its tiles
 
-MOL_DEV void ldsm4(const void* p, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_u32(p))
-               : "memory");
-}
-MOL_DEV void ldsm4_t(const void* p, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_u32(p))
-               : "memory");
-}
+using attn::ldsm4;
+using attn::ldsm4_t;
+
 template <int D, int MT>
 struct Geo {
   static constexpr int kRows = 16 * MT;
@@ -39,16 +30,15 @@ struct Geo {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr size_t kSmem = (size_t)kRing + kRows * D * 2;  // and the queries
-  // Rows whose sums a warp leaves in the ring stage it has just taken, for the others to add.
-  static constexpr int kMeet = kStageBytes / (D * 4) < kRows ? kStageBytes / (D * 4) : kRows;
-  static_assert(kMeet % 16 == 0 && kRows % kMeet == 0, "sums that meet");
+  // A warp's sums go to the ring stage it has just taken, for the others to add.
+  static_assert(kRows * D * 4 <= kStageBytes, "sums that meet");
   static constexpr int kPerSM = kSmem <= 113 * 1024 ? 2 : 1;
   static constexpr bool kQueriesInRegisters = MT * D <= 128;
 };
 
 // Few rows (new tokens x group) against long runs of keys: the cache is read once, and that is what
-// bounds it. All tiles of 64 tokens (128 for 64 values a head) of the launch, over sequences, heads and row blocks, are one list
-// dealt in even runs to thread blocks, so sequences of any lengths fill the GPU alike; a block whose
+// bounds it. All tiles of 64 tokens (128 for 64 values a head) of the launch, over sequences, heads and row
+// blocks, are one list dealt in even runs to thread blocks, so sequences of any lengths fill the GPU alike; a block whose
 // tiles fall to several leaves parts that launch_join adds in order. In a tile each warp has 16
 // (32) tokens of its own, with a cp.async ring of its own that runs on across the blocks' borders (keys and
 // values asked for two steps ahead, no barrier between warps), its own maximum, sum and fp32
@@ -57,7 +47,8 @@ struct Geo {
 // holds; where a row does not see a token that another one sees, the step's values are looked
 // through, and summed without the tensor cores should one not be finite (0 * NaN is NaN there).
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
+    attend_few_kernel(const __grid_constant__ AttnArgs a) {
   using G = Geo<D, MT>;
   constexpr int kChunks = D / 8;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -365,56 +356,53 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM) attend_few_kerne
     // Each in the stage that the next copies go to; the 32-byte pieces of a row in another order for
     // each row, so that a store's rows do not fall on the same banks.
     const int free_stage = stage == 0 ? G::kStages - 1 : stage - 1;
+    unsigned char* mine = ring + free_stage * G::kStageBytes;
 #pragma unroll
-    for (int row_m = 0; row_m < G::kRows; row_m += G::kMeet) {
-      unsigned char* mine = ring + free_stage * G::kStageBytes;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int mt = row_m / 16; mt < (row_m + G::kMeet) / 16; ++mt)
+      for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(mine + (mt * 16 - row_m + g + 8 * i) * (D * 4) + ((n ^ g) << 5) +
-                                       t4 * 8) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
-      __syncthreads();
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float2*>(mine + (mt * 16 + g + 8 * i) * (D * 4) + ((n ^ g) << 5) +
+                                     t4 * 8) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
+    __syncthreads();
 #pragma unroll 1
-      for (int i = tid; i < G::kMeet * (D / 4); i += kThreads) {
-        const int local = i / (D / 4), row = row_m + local, col = i % (D / 4) * 4;
-        if (row >= nrows) break;
-        float m = -INFINITY, l = 0.f;
+    for (int i = tid; i < G::kRows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), col = i % (D / 4) * 4;
+      if (row >= nrows) break;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][row].x);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_top[w][row].x);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {  // (in this order, whatever the timing)
-          const float2 t = s_top[w][row];
-          const float f = t.x == -INFINITY ? 0.f : attn::ex2(t.x - m);
-          const float4 y = *reinterpret_cast<const float4*>(
-              smem + (w * G::kStages + free_stage) * G::kStageBytes + local * (D * 4) +
-              (((col >> 3) ^ (local & 7)) << 5) + (col & 4) * 4);
-          l += f * t.y;
-          x.x += f * y.x;
-          x.y += f * y.y;
-          x.z += f * y.z;
-          x.w += f * y.w;
-        }
-        if (kChecked && !MOL_CHECK(start + divide(row0 + row, a.by_group) < a.num_tokens, MOL_CHECK_ROW,
-                                   start + divide(row0 + row, a.by_group)))
-          continue;
-        if (part) {
-          *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
-          if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
-        } else {
-          const int r = row0 + row, token = divide(r, a.by_group);
-          const float inv = m == -INFINITY ? 0.f : 1.f / l;
-          *reinterpret_cast<uint2*>(a.out + (int64_t)(start + token) * a.out_token_stride +
-                                    (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
-                                    col) =
-              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-        }
+      for (int w = 0; w < kWarps; ++w) {  // (in this order, whatever the timing)
+        const float2 t = s_top[w][row];
+        const float f = t.x == -INFINITY ? 0.f : attn::ex2(t.x - m);
+        const float4 y = *reinterpret_cast<const float4*>(
+            smem + (w * G::kStages + free_stage) * G::kStageBytes + row * (D * 4) +
+            (((col >> 3) ^ (row & 7)) << 5) + (col & 4) * 4);
+        l += f * t.y;
+        x.x += f * y.x;
+        x.y += f * y.y;
+        x.z += f * y.z;
+        x.w += f * y.w;
       }
-      __syncthreads();
+      if (kChecked && !MOL_CHECK(start + divide(row0 + row, a.by_group) < a.num_tokens, MOL_CHECK_ROW,
+                                 start + divide(row0 + row, a.by_group)))
+        continue;
+      if (part) {
+        *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
+        if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
+      } else {
+        const int r = row0 + row, token = divide(r, a.by_group);
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(start + token) * a.out_token_stride +
+                                  (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride +
+                                  col) =
+            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+      }
     }
+    __syncthreads();
   }
   cp_async_wait_all();
   if (tid == 0) parts.records[c] = record;
@@ -557,7 +545,7 @@ cudaError_t attn::launch_join(const AttnArgs& a, int grid, int rows, const Parts
   auto go = [&](auto kernel) { return launch_pdl(kernel, g, block, 0, stream, a, rows, p); };
   if (a.head_dim == 64) return few ? go(join_kernel<64, kWays>) : go(join_kernel<64, 1>);
   if (a.head_dim == 128) return few ? go(join_kernel<128, kWays>) : go(join_kernel<128, 1>);
-  return go(join_kernel<256, kWays>);
+  return few ? go(join_kernel<256, kWays>) : go(join_kernel<256, 1>);
 }
 
 cudaError_t prepare_attn_kernels() {
@@ -566,6 +554,7 @@ cudaError_t prepare_attn_kernels() {
   if (e == cudaSuccess) e = prepare<128, 1>();
   if (e == cudaSuccess) e = prepare<256, 1>();
   if (e == cudaSuccess) e = attn::prepare_many();
+  if (e == cudaSuccess) e = attn::prepare_wide();
   return e;
 }
 
@@ -575,17 +564,21 @@ cudaError_t prepare_attn_kernels() {
 //   64 values a head:  12 rows 32 | 40 | 54, 16 rows 33 | 40 | 54, 24 rows 49 | 41 | 54, 48 rows 65 | 68 | 55
 //   128 values:        12 rows 52 | 66 | 61, 16 rows 52 | 66 | 61, 24 rows 91 | 68 | 61, 48 rows 131 | 119 | 62
 // A call with both of decoding sequences and prompts pays: 200 rows of one sequence in blocks of 16 read its
-// keys 13 times (from L2). 256 values a head take blocks of 16 whatever the rows.
-enum class Form { kFew16, kFew32, kMany };
+// keys 13 times (from L2). 256 values a head, 2 key heads (us for attend_few | attend_wide): one sequence of
+// 2000 tokens, 32 rows 15 | 22, 128 rows 20 | 32; 8 of them, 32 rows each 25 | 29, 64 rows 37 | 34, 128 rows
+// 60 | 45; 200 new of 300 tokens, 1600 rows 31 | 24; 2048 tokens 590 | 202.
+enum class Form { kFew16, kFew32, kMany, kWide };
 static Form form(int64_t num_seqs, int64_t rows, int head_dim) {
-  if (rows <= 16 * num_seqs || head_dim == 256) return Form::kFew16;
+  if (rows <= 16 * num_seqs) return Form::kFew16;
+  if (head_dim == 256) return rows <= std::max<int64_t>(64 * num_seqs, 256) ? Form::kFew16 : Form::kWide;
   return head_dim == 64 && rows <= 32 * num_seqs ? Form::kFew32 : Form::kMany;
 }
 
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
   if (num_seqs <= 0 || num_tokens <= 0) return 0;
   const Form f = form(num_seqs, num_tokens * group, head_dim);
-  return f == Form::kMany ? attn::many_bytes(group, head_dim)
+  return f == Form::kMany   ? attn::many_bytes(group, head_dim)
+         : f == Form::kWide ? attn::wide_bytes()
                           : attn::parts_bytes(attn::kMaxGrid, f == Form::kFew32 ? 32 : 16, head_dim);
 }
 
@@ -593,6 +586,8 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   switch (form(a.num_seqs, (int64_t)a.num_tokens * a.group, a.head_dim)) {
     case Form::kMany:
       return attn::launch_many(a, stream);
+    case Form::kWide:
+      return attn::launch_wide(a, stream);
     case Form::kFew32:
       return attend_few<64, 2>(a, stream);
     default:

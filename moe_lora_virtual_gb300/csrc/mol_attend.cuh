@@ -22,6 +22,18 @@ MOL_DEV bool not_finite(const uint4& q) {
   return (c & 0x80008000u) != 0;
 }
 
+MOL_DEV void ldsm4(const void* p, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p))
+               : "memory");
+}
+MOL_DEV void ldsm4_t(const void* p, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p))
+               : "memory");
+}
 MOL_DEV float ex2(float x) {  // 2^x, within 2^-22 of it; 0 for -infinity
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -325,6 +337,10 @@ constexpr int kMaxGrid = 2 * 152;
 size_t many_bytes(int group, int head_dim);
 cudaError_t prepare_many();
 cudaError_t launch_many(const AttnArgs& a, cudaStream_t stream);
+// Many rows a sequence of 256 values a head (mol_attend_wide.cu).
+size_t wide_bytes();
+cudaError_t prepare_wide();
+cudaError_t launch_wide(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace mol

@@ -74,6 +74,7 @@ cudaError_t prepare_attn_kernels();
 cudaError_t take_rope_checks(unsigned long long* first, unsigned long long* count);
 cudaError_t take_attn_checks(unsigned long long* first, unsigned long long* count);
 cudaError_t take_many_checks(unsigned long long* first, unsigned long long* count);
+cudaError_t take_wide_checks(unsigned long long* first, unsigned long long* count);
 cudaError_t set_attn_wait_test(unsigned stall, unsigned long long limit_ns);
 cudaError_t take_attn_faults(unsigned* out);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);

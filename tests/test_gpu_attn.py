@@ -343,7 +343,7 @@ def test_a_layer_step_in_a_graph_and_on_a_stream(env):
 
 
 @pytest.mark.parametrize("D,lens", [(64, [(1, 900), (1, 3)]), (128, [(200, 700), (1, 2000), (3, 9)]),
-                                    (256, [(5, 1500)])])
+                                    (256, [(5, 1500)]), (256, [(200, 700), (1, 2000)])])
 def test_results_do_not_depend_on_timing_or_what_memory_held(env, D, lens):
     """Bit-equal over calls, over workspaces of NaN and of ones, with the workspace of another size."""
     torch, mol = env

@@ -99,7 +99,8 @@ def near(torch, got, p, scale, window=0):
     ([(1, 16000), (1, 1), (1, 9000)], 4, 2, 64, 32, 0), ([(1, 12000)], 2, 1, 256, 64, 0),
     ([(40, 30000)], 8, 1, 128, 16, 0), ([(33, 16000), (200, 9000)], 8, 2, 64, 64, 3000),
     ([(2048, 2048)], 4, 2, 128, 64, 0), ([(1000, 5000), (1, 7000), (37, 37)], 8, 4, 64, 16, 1024),
-    ([(700, 3000)], 1, 1, 128, 128, 0)])
+    ([(700, 3000)], 1, 1, 128, 128, 0), ([(300, 9000), (1, 77)], 4, 2, 256, 16, 0),
+    ([(130, 5000), (700, 1400)], 3, 1, 256, 64, 900)])
 def test_long(env, lens, Hq, Hkv, D, page, window):
     torch, _ = env
     p = au.problem(torch, D, lens, Hq, Hkv, D, page)
@@ -125,7 +126,7 @@ def test_many_blocks_of_unlike_sizes(env, D, window, most):
 def test_flat_and_sharp_weights(env, scale, lens):
     """Scores near 0, and hundreds of powers of two apart, the largest anywhere in the sequence."""
     torch, _ = env
-    for D in (64, 128):
+    for D in (64, 128, 256):
         p = au.problem(torch, D, lens, 4, 2, D, 16, std=3.0)
         near(torch, attend(env, p, scale=scale), p, scale)
 
@@ -133,7 +134,8 @@ def test_flat_and_sharp_weights(env, scale, lens):
 def test_scores_that_rise_and_fall(env):
     """Maxima that grow from tile to tile (sums rescaled each time), and that only the first tile has."""
     torch, mol = env
-    for D, lens in ((64, [(1, 1000)]), (128, [(150, 1000)]), (64, [(150, 1000)])):
+    for D, lens in ((64, [(1, 1000)]), (128, [(150, 1000)]), (64, [(150, 1000)]),
+                    (256, [(1, 1000)]), (256, [(150, 1000)])):
         p = au.problem(torch, D, lens, 4, 2, D, 16)
         k, _ = au.caches(p, "cpu")
         p["q"][..., 0] = 8.0
