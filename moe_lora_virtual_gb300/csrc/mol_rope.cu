@@ -39,13 +39,17 @@ MOL_DEV void turn_pair(float& a, float& b, float2 cs) {
 // keys), so that its addresses move by a constant; the first one, and the values, are asked for before
 // the angles (position, frequency and 64-bit products are a chain of two round trips and some). Bound
 // by HBM for many tokens (each value read and written once), by the launch and that chain for a few.
-// What keeps HBM busy is tokens under way: with 32 registers, 16 of them on a multiprocessor, 8192 tokens
-// of 32 heads of 128, half of each turned, take 26.2 us (0.75 of a copy's rate) and 31.7 with keys and
-// values into pages (0.76); 28.1 and 34.3 with 40 registers, 33.5 and 41.7 with 64. Keeping cosines and
-// four heads in registers (72) took 26.4 and 38.3, blocks that stay for several tokens (115) 30.6 and 43.5.
-template <int THREADS, int BLOCKS>
+// What keeps HBM busy is bytes under way, so for many tokens a thread's later units are prefetched into L2,
+// 14 tokens on a multiprocessor: 8192 tokens of 32 heads of 128, half of each turned, take 24.6 us (0.80 of a
+// copy's rate) and 29.0 with keys and values into pages (0.83). Without the prefetch 26.4 and 31.8 with 16
+// tokens (32 registers), 28.1 and 34.3 with 12, 33.5 and 41.7 with 64 registers; with it 24.9 and 29.1 with 16,
+// 25.5 and 30.4 with 12, 26.3 and 30.9 with 28 blocks of 64 threads. Before it, cosines and four heads in
+// registers (72) took 26.4 and 38.3, blocks that stay for several tokens (115) 30.6 and 43.5.
+template <int THREADS, int BLOCKS, bool MANY>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 cs[kMaxPairs];
+  // Pairs 2 e and 2 e + 1 of unit u at [e * turned + u], so that neighbouring lanes read neighbouring
+  // 16 bytes (in the pairs' own order four units share their banks).
+  __shared__ float4 cs[kMaxPairs / 2];
   const int64_t t = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
@@ -54,6 +58,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_cons
   const int pairs = a.interleaved ? 0 : a.rotary_dim >> 4;  // units that are two chunks
   const bool two = unit < pairs;
   const int u = two ? unit : unit + pairs;                  // its (first) chunk
+  const int shift = a.interleaved ? 2 : 3, turned = a.rotary_dim / 2 >> shift;  // pairs of a unit; units
   const int heads = a.in[0].heads + a.in[1].heads;
   const int first = h0 < a.step ? h0 : heads;               // (threads left over have none)
   auto from = [&](int h) {
@@ -67,10 +72,28 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_cons
     c.q = from(first)[0];
     if (two) d.q = from(first)[pairs];
   }
+  auto value = [&](int i, int h) {
+    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in[2].x) + t * a.in[2].token_stride +
+                                          h * a.in[2].head_stride) + i - h * a.chunks;
+  };
+  if constexpr (MANY) {
+    // What the thread asks for later is on its way to L2 at once, which takes no registers.
+    auto soon = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+#pragma unroll 1
+    for (int h = first + a.step; h < heads; h += a.step) {
+      soon(from(h));
+      if (two) soon(from(h) + pairs);
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.in[2].heads * a.chunks; i += THREADS) soon(value(i, divide(i, a.by_chunks)));
+  }
   if (a.inv_freq) {
     const int p = a.positions[t];
-    for (int i = threadIdx.x; i < a.rotary_dim / 2; i += THREADS)
-      cs[i] = turn(p, a.inv_freq[i], a.magnitude);
+    for (int i = threadIdx.x; i < a.rotary_dim / 2; i += THREADS) {
+      const int in_unit = i & ((1 << shift) - 1);
+      reinterpret_cast<float2*>(cs + (in_unit >> 1) * turned + (i >> shift))[in_unit & 1] =
+          turn(p, a.inv_freq[i], a.magnitude);
+    }
   }
   const bool in = slot >= 0 && slot < a.num_slots;
   const int page = in ? divide(slot, a.by_page) : 0;
@@ -80,10 +103,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_cons
   if (keep) {
 #pragma unroll 1
     for (int i = threadIdx.x; i < a.in[2].heads * a.chunks; i += THREADS) {
-      const int h = divide(i, a.by_chunks), at = i - h * a.chunks;
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_cache) + cache_at + h * a.head_stride)[at] =
-          reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in[2].x) +
-                                         t * a.in[2].token_stride + h * a.in[2].head_stride)[at];
+      const int h = divide(i, a.by_chunks);
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_cache) + cache_at + h * a.head_stride)[i - h * a.chunks] =
+          *value(i, h);
     }
   }
   __syncthreads();
@@ -98,17 +120,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_kernel(const __grid_cons
       for (int e = 0; e < 4; ++e) {
         float x0 = bf16_lo(c.w[e]), x1 = bf16_hi(c.w[e]);
         float y0 = bf16_lo(d.w[e]), y1 = bf16_hi(d.w[e]);
-        turn_pair(x0, y0, cs[8 * u + 2 * e]);
-        turn_pair(x1, y1, cs[8 * u + 2 * e + 1]);
+        const float4 f = cs[e * turned + u];
+        turn_pair(x0, y0, make_float2(f.x, f.y));
+        turn_pair(x1, y1, make_float2(f.z, f.w));
         c.w[e] = pack_bf16x2(x0, x1);
         d.w[e] = pack_bf16x2(y0, y1);
       }
-    } else if (a.interleaved && u < a.rotary_dim >> 3) {
+    } else if (a.interleaved && u < turned) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = bf16_lo(c.w[e]), y = bf16_hi(c.w[e]);
-        turn_pair(x, y, cs[4 * u + e]);
-        c.w[e] = pack_bf16x2(x, y);
+      for (int e = 0; e < 2; ++e) {
+        const float4 f = cs[e * turned + u];
+        float x0 = bf16_lo(c.w[2 * e]), y0 = bf16_hi(c.w[2 * e]);
+        float x1 = bf16_lo(c.w[2 * e + 1]), y1 = bf16_hi(c.w[2 * e + 1]);
+        turn_pair(x0, y0, make_float2(f.x, f.y));
+        turn_pair(x1, y1, make_float2(f.z, f.w));
+        c.w[2 * e] = pack_bf16x2(x0, y0);
+        c.w[2 * e + 1] = pack_bf16x2(x1, y1);
       }
     }
     uint16_t* dst;
@@ -133,12 +160,12 @@ cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream) {
   a.by_units = divider(a.units);
   a.by_page = divider(a.page_size);
   // Many tokens: as many as possible at a time. Few: 256 threads each, registers as they come (23 tokens of
-  // 16 heads of 128 1.9 us, 2.3 with keys and values; 2.2 and 2.8 in the form for many).
+  // 16 heads of 128 1.9 us, 2.1 with keys and values; 2.1 and 2.8 in the form for many).
   auto go = [&](auto kernel, int threads) {
     a.step = threads / a.units;
     return launch_pdl(kernel, dim3((unsigned)a.num_tokens), dim3(threads), 0, stream, a);
   };
-  return a.num_tokens > 4 * 152 ? go(rope_kernel<128, 16>, 128) : go(rope_kernel<256, 4>, 256);
+  return a.num_tokens > 4 * 152 ? go(rope_kernel<128, 14, true>, 128) : go(rope_kernel<256, 4, false>, 256);
 }
 
 cudaError_t take_rope_checks(unsigned long long* first, unsigned long long* count) {
