@@ -329,7 +329,8 @@ int32_t mol_take_fault_flags(uint32_t* flags);
  * issues any copy, and so does the weight producer of the tensor-core expand
  * (full routed blocks of rank 64), so the other roles' waits run out with
  * nothing in flight and record bit 0 of mol_take_fault_flags; 0 restores
- * normal operation. wait_limit_ns bounds every wait of those two kernels (0 =
+ * normal operation. mol_paged_attention's tcgen05 kernel heeds both arguments too
+ * (its copying warp stays away). wait_limit_ns bounds every wait of those kernels (0 =
  * the default, one second). Synchronizes the device; for tests only, never while another
  * thread uses the library. Returns MOL_ERR_INVALID_ARG for stall_producer > 1.
  */
@@ -380,7 +381,7 @@ int32_t mol_checked_build(void);
  * checks since the last call (0 in the release build), *first = (site << 48)
  * | (value & 0xFFFFFFFFFFFF) of the first one recorded by the earliest kernel
  * file in the path's order (align, shrink/expand, tcgen05 shrink, fused
- * stage), 0 if none. Synchronizes the device. Either pointer may be NULL.
+ * stage, tcgen05 expand, the block's kernels, the attention's), 0 if none. Synchronizes the device. Either pointer may be NULL.
  */
 int32_t mol_take_check_record(uint64_t* first, uint64_t* count);
 

@@ -111,8 +111,8 @@ MOL_DEV Block block_of(const AttnArgs& a, int b, const Seq& s, int r, int rows, 
 }
 
 // What a launch does is counted in units: a block's tiles and `extra` more for what it takes to begin
-// and to end one; or blocks, where these go undivided. All units of the launch, in the order (sequence, block, head, unit), are dealt in
-// even runs to its thread blocks.
+// and to end one; or blocks, where these go undivided. All units of the launch, in the order (sequence,
+// block, head, unit), are dealt in even runs to its thread blocks.
 MOL_DEV int units_of(const AttnArgs& a, const Block& k, int extra) { return a.whole ? 1 : k.tiles + extra; }
 
 struct Place {  // where a thread block's run begins
