@@ -111,10 +111,11 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  *               calls that may run at the same time need one each
  * out may be q itself (same strides).
  * Contract: head_dim 64, 128 or 256; num_q_heads a multiple of cache->num_heads,
- * at most MOL_ATTN_MAX_GROUP times it; scale > 0 and finite; window >= 0;
- * max_pages * page_size < 2^31; num_tokens * num_q_heads < 2^31; with g query
- * heads to a key head, (num_tokens * g / 16 + num_seqs) * (max_pages *
- * page_size / 64 + 4) < 2^31 (32 K rows of group 8 over tables of 8 M tokens).
+ * at most MOL_ATTN_MAX_GROUP times it; scale > 0, it and its product with
+ * log2(e) finite; window >= 0; num_tokens * num_q_heads < 2^31; num_tokens +
+ * max_pages * page_size <= 2^31 - 1024; with g query heads to a key head,
+ * (num_tokens * g / 16 + num_seqs) * (max_pages * page_size / 64 + 4) < 2^31
+ * (32 K rows of group 8 over tables of 8 M tokens).
  */
 int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                             const mol_paged_cache* cache, const int32_t* page_table,

@@ -227,7 +227,7 @@ MOL_DEV Run wait_and_deal(const AttnArgs& a, int rows, int tile, int extra, int*
 template <int THREADS>
 MOL_DEV void prefetch_table(const AttnArgs& a) {
   const int64_t at = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * 32;
-  const int64_t all = (int64_t)(a.num_seqs - 1) * a.table_stride + a.max_pages;
+  const int64_t all = a.max_pages > 0 ? (int64_t)(a.num_seqs - 1) * a.table_stride + a.max_pages : 0;
   if (at < all) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.page_table + at));
 }
 

@@ -155,19 +155,22 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
                             int64_t out_token_stride, int64_t out_head_stride, void* workspace,
                             size_t workspace_bytes, void* stream) {
   MOL_TRY(check_cache(cache));
+  const float scale_log2 = scale * 1.4426950408889634f;
   if (num_seqs < 0 || num_tokens < 0 || num_q_heads < 1 || max_pages < 0 || window < 0 ||
-      !(scale > 0.f) || !std::isfinite(scale) || (!q_starts && num_tokens != num_seqs) ||
+      !(scale > 0.f) || !std::isfinite(scale_log2) || (!q_starts && num_tokens != num_seqs) ||
       num_q_heads % cache->num_heads != 0 || (num_seqs > 1 && table_stride < max_pages))
     return MOL_ERR_INVALID_ARG;
   const int d = cache->head_dim;
   if ((d != 64 && d != 128 && d != 256) || num_q_heads / cache->num_heads > MOL_ATTN_MAX_GROUP ||
       num_q_heads > 65536 || num_seqs >= (int64_t)1 << 24 || num_tokens >= (int64_t)1 << 31 ||
-      num_tokens * num_q_heads >= (int64_t)1 << 31 ||
-      (int64_t)max_pages * cache->page_size >= (int64_t)1 << 31)
+      num_tokens * num_q_heads >= (int64_t)1 << 31)
     return MOL_ERR_UNSUPPORTED;
+  // positions, a window before the first and a tile behind the last are 32-bit numbers
+  const int64_t cached = (int64_t)max_pages * cache->page_size;
+  if (num_tokens + cached > ((int64_t)1 << 31) - 1024) return MOL_ERR_UNSUPPORTED;
   // the tiles of a head are counted in 32 bits
   const int64_t rows = num_tokens * (num_q_heads / cache->num_heads);
-  if ((rows / 16 + num_seqs) * ((int64_t)max_pages * cache->page_size / 64 + 4) >= (int64_t)1 << 31)
+  if ((rows / 16 + num_seqs) * (cached / 64 + 4) >= (int64_t)1 << 31)
     return MOL_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return MOL_OK;
   if (!kv_lens || (max_pages > 0 && !page_table)) return MOL_ERR_INVALID_ARG;
@@ -201,8 +204,8 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
   a.q_starts = q_starts;
   a.num_seqs = (int)num_seqs;
   a.num_tokens = (int)num_tokens;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
+  a.scale_log2 = scale_log2;
+  a.window = window < cached ? window : 0;  // (0: all)
   a.out = static_cast<uint16_t*>(out);
   a.out_token_stride = out_token_stride;
   a.out_head_stride = out_head_stride;

@@ -121,10 +121,11 @@ def test_append_refusals(mol, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(H=3), INVALID),
     (dict(H=2 * 65), UNSUPPORTED), (dict(mp=-1), INVALID), (dict(win=-1), INVALID), (dict(scale=0.0), INVALID),
-    (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(scale=3e38), INVALID),
     (dict(starts=None), INVALID), (dict(st=3), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID),
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(qt=56), INVALID), (dict(oh=68), UNSUPPORTED),
     (dict(q=P(8)), UNSUPPORTED), (dict(mp=1 << 28, st=1 << 28), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED),
+    (dict(mp=(1 << 28) - 64, st=1 << 28), UNSUPPORTED),  # (a tile's end past 2^31)
     (dict(T=1 << 29), UNSUPPORTED), (dict(B=1 << 24), UNSUPPORTED), (dict(ws=None), CAPACITY),
     (dict(wsb=64), CAPACITY), (dict(ws=P(8)), UNSUPPORTED), (dict(T=0), OK), (dict(B=0), OK),
     (dict(cache=dict(D=96, hs=96, ts=192, ps=1536)), UNSUPPORTED), (dict(cache=dict(D=32)), UNSUPPORTED),

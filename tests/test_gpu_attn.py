@@ -228,6 +228,17 @@ def test_what_a_row_does_not_see_does_not_reach_it(env, D, Hq, Hkv, bad, window)
                 assert not bool(torch.isfinite(got[:n][torch.from_numpy(sees)][..., 3]).any())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 1, 70, (1 << 31) - 1])
+@pytest.mark.parametrize("lens", [[(5, 3), (4, 0), (1, 40)], [(400, 90), (300, 0), (5, 3), (70, 69)]])
+def test_more_rows_than_cached_tokens(env, D, window, lens):
+    """Rows before position 0 see nothing, whatever the window; those behind them what is there."""
+    torch, _ = env
+    got = run(env, au.problem(torch, D + window % 1000, lens, 8, 4, D, 16), window)
+    for (n, kv), at in zip(lens, np.cumsum([0] + [n for n, _ in lens])):
+        assert bool((got[at:at + max(n - kv, 0)] == 0).all())
+
+
 def test_table_and_lengths_past_their_ends(env):
     """Lengths past the table are its width; starts past the rows are their end; none below 0."""
     torch, mol = env
