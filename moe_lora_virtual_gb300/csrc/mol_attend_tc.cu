@@ -232,7 +232,8 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //                   without a shuffle. The maximum that weights refer to moves only when one would
 //                   pass 2^8 (bf16 and fp32 lose nothing to that), so sums are hardly ever rescaled
 //   warp 8          issues the products: P0 V, Q0 K', P1 V, Q1 K' (K' the next keys); Q0 K', Q1 K', P0 V, P1 V
-//                   for 64 values a head, whose weights need not wait for the scores' place
+//                   for 64 values a head, whose weights need not wait for the scores' place. TWO: the
+//                   scores' products alone, those of the weights are issued by warp 10
 //   warp 9          copies the queries and, page by page, keys and values (TMA, 128-byte swizzle) into a
 //                   ring of tiles; token by token (cp.async) from pages whose tokens make no such copies
 //   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
@@ -240,14 +241,15 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
 // Tiles are dealt as in attend_few; parts of blocks join in launch_join. Pages outside the cache are zeros
 // (the copy's fill); what a row does not see is replaced among its scores.
-template <int D, bool GATHER>
+template <int D, bool GATHER, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
   using G = Geo<D>;
   constexpr bool kTokens = GATHER || D == 64;
-  // tokens that are gathered take two warps, keys and values, and leave one to look through these
-  constexpr int kLookers = GATHER ? 1 : 2;
+  static_assert(!TWO || (G::kApart && !GATHER), "a free warp, and weights apart from the scores");
+  // tokens that are gathered, or a second issuing warp, leave one to look through values
+  constexpr int kLookers = GATHER || TWO ? 1 : 2;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t q_full, q_empty, all_done, full[G::kSlots], empty[G::kSlots], seen[G::kSlots], s_full[2],
       p_full[2], o_full[2], s_read[2];
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
-    mbar_init(&all_done, 1);
+    mbar_init(&all_done, TWO ? 2 : 1);
     for (int s = 0; s < G::kSlots; ++s) {
       mbar_init(&full[s], GATHER ? 32 : 1);
       mbar_init(&empty[s], 1 + kLookers);  // the last products' commit, and the warps that look through values
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[t], 2);  // the products' commit, and the issuing thread for what it has seen
       mbar_init(&p_full[t], 4);  // a warp each
       mbar_init(&o_full[t], 1);
-      mbar_init(&s_read[t], 4);
+      mbar_init(&s_read[t], TWO ? 5 : 4);  // and the values' issuing warp, for the products of before
     }
     fence_mbar_init();
   }
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         (void)warp_wait(&full[i % G::kSlots], (i / G::kSlots) & 1, limit);
       if (seg > 0) (void)warp_wait(&q_full, (seg - 1) & 1, limit);
     }
-  } else if (warp > 9) {
+  } else if (warp >= 12 - kLookers) {
     // ------------------------------------------------------------ values that not every row sees
     uint32_t u = 0, n = 0;
     const int per = a.page_size < kM ? a.page_size : kM;
@@ -481,16 +483,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kv && (!held_at(n).all(per) || j0 + kM - 1 > pos_first ||
                      (a.window > 0 && j0 <= pos_last - a.window))) {
             unsigned char* v = ring + s * G::kTileBytes;
+            // 0 times a value is NaN where it is not finite, and stays so in the sum
+            uint32_t zeros = 0;
+#pragma unroll 8
+            for (int x = tid - (12 - kLookers) * 32; x < G::kTileBytes / 16; x += kLookers * 32) {
+              const uint4 q = lds16(v + x * 16);
+              for (uint32_t two : {q.x, q.y, q.z, q.w})
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zeros) : "r"(two), "r"(0u));
+            }
             bool bad = false;
-#pragma unroll 4
-            for (int x = tid - (12 - kLookers) * 32; x < G::kTileBytes / 16; x += kLookers * 32)
-              if (attn::not_finite(lds16(v + x * 16))) {
-                const int j = j0 + (x >> 3) % kM;
-                if (j < k.lo || j >= k.hi)
-                  *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
-                else
-                  bad = true;
-              }
+            if (zeros & 0x7fff7fffu) {
+#pragma unroll 1
+              for (int x = tid - (12 - kLookers) * 32; x < G::kTileBytes / 16; x += kLookers * 32)
+                if (attn::not_finite(lds16(v + x * 16))) {
+                  const int j = j0 + (x >> 3) % kM;
+                  if (j < k.lo || j >= k.hi)
+                    *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+                  else
+                    bad = true;
+                }
+            }
             fence_proxy_async_smem();
             if (bad) *(volatile uint32_t*)&s_bad[s] = u + 1;
             __syncwarp();
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
     }
-  } else if (warp == 8) {
+  } else {
     // ------------------------------------------------------------ products
     // The whole warp goes through it, so that what the products take lies in registers that the warp shares;
     // one lane issues them.
@@ -534,58 +546,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(leader, &s_full[t]);
       arrive(leader, &s_full[t]);
     };
+    // false where the weights do not come
+    auto sums = [&](int t, uint32_t slot, bool begun) {
+      if (!wait(&p_full[t], np[t] & 1)) return false;
+      tc_fence_after();
+      ++np[t];
+      if (!*(volatile uint32_t*)&s_skip[t]) {
+        const uint32_t v = ring_at + (slot % G::kSlots) * (G::kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kM / 16; ++kk)
+          umma_ts(leader, tmem + G::kO + t * D, tmem + G::kP + t * G::kPStep + kk * 8, v + (kk * 16 * 128 >> 4),
+                  G::kHalf >> 4, kValues<D>, begun || kk != 0);
+      }
+      return true;
+    };
     attn::Walk w;
-    for (begin(w); w.more() && !fault; next(w)) {
-      const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
-      ++seg;
-      if (!wait(&q_full, (seg - 1) & 1) || !wait_slot(u)) break;
-      scores(0, u);
-      if (tiles == 2) scores(1, u);
-      commit(leader, &empty[u % G::kSlots]);
-      if (count == 1) commit(leader, &q_empty);  // (with the block's last scores)
-      bool begun[2] = {false, false};
-      for (int i = 0; i < count && !fault; ++i) {
-        // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
-        const bool more = i + 1 < count;
-        const uint32_t k1 = more ? u + 2 : u + 1;
-        if (!wait_two(&full[(u + 1) % G::kSlots], ((u + 1) / G::kSlots) & 1, &full[k1 % G::kSlots],
-                      (k1 / G::kSlots) & 1))
-          break;
-        if (GATHER) fence_proxy_async_smem();
-        // the next tile's scores as soon as these have been read, where the weights lie apart
-        if (G::kApart && more) {
-          const bool both = tiles == 2;
-          if (!wait_two(&s_read[0], np[0] & 1, &s_read[both], (both ? np[1] : np[0]) & 1)) break;
-          tc_fence_after();
-          scores(0, u + 2);
-          if (both) scores(1, u + 2);
-          commit(leader, &empty[(u + 2) % G::kSlots]);
-          if (i + 2 == count) commit(leader, &q_empty);
-        }
+    if constexpr (TWO) {
+      // One warp's waits while the other's products run; the scores go on into the next block. A tile's next
+      // scores are issued behind the products of the weights before, which their softmax waits for first.
+      if (warp == 10) {
+        arrive(leader, &s_read[0]);
+        arrive(leader, &s_read[1]);
+      }
+      for (begin(w); w.more() && !fault; next(w)) {
+        const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
+        ++seg;
+        if (warp == 8 && !wait(&q_full, (seg - 1) & 1)) break;
+        for (int i = 0; i < count && !fault; ++i, u += 2) {
+          const uint32_t slot = warp == 8 ? u : u + 1;
+          if (!wait_slot(slot)) break;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == tiles || !wait(&p_full[t], np[t] & 1)) break;
-          tc_fence_after();
-          ++np[t];
-          if (!*(volatile uint32_t*)&s_skip[t]) {
-            const uint32_t v = ring_at + ((u + 1) % G::kSlots) * (G::kTileBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kM / 16; ++kk)
-              umma_ts(leader, tmem + G::kO + t * D, tmem + G::kP + t * G::kPStep + kk * 8,
-                      v + (kk * 16 * 128 >> 4), G::kHalf >> 4, kValues<D>, begun[t] || kk != 0);
-          }
-          begun[t] = true;
-          if (t == tiles - 1) commit(leader, &empty[(u + 1) % G::kSlots]);
-          if (G::kApart || !more) commit(leader, &o_full[t]);
-          if (!G::kApart && more) {
-            scores(t, u + 2);
-            if (t == tiles - 1) {
-              commit(leader, &empty[(u + 2) % G::kSlots]);
-              if (i + 2 == count) commit(leader, &q_empty);
+          for (int t = 0; t < 2; ++t) {
+            if (t == tiles) break;
+            if (warp == 8) {  // as soon as the scores before these have been read
+              if (np[t] > 0 && !wait(&s_read[t], (np[t] - 1) & 1)) break;
+              tc_fence_after();
+              ++np[t];
+              scores(t, slot);
+            } else {
+              if (!sums(t, slot, i > 0)) break;
+              commit(leader, &o_full[t]);
+              arrive(leader, &s_read[t]);
             }
           }
+          commit(leader, &empty[slot % G::kSlots]);
+          if (warp == 8 && i + 1 == count) commit(leader, &q_empty);
         }
-        u += 2;
+      }
+    } else {
+      for (begin(w); w.more() && !fault; next(w)) {
+        const int tiles = w.k.nrows > tile_rows ? 2 : 1, count = w.count;
+        ++seg;
+        if (!wait(&q_full, (seg - 1) & 1) || !wait_slot(u)) break;
+        scores(0, u);
+        if (tiles == 2) scores(1, u);
+        commit(leader, &empty[u % G::kSlots]);
+        if (count == 1) commit(leader, &q_empty);  // (with the block's last scores)
+        bool begun[2] = {false, false};
+        for (int i = 0; i < count && !fault; ++i) {
+          // slot u: the tile's keys (done with), u + 1: its values, u + 2: the next tile's keys
+          const bool more = i + 1 < count;
+          const uint32_t k1 = more ? u + 2 : u + 1;
+          if (!wait_two(&full[(u + 1) % G::kSlots], ((u + 1) / G::kSlots) & 1, &full[k1 % G::kSlots],
+                        (k1 / G::kSlots) & 1))
+            break;
+          if (GATHER) fence_proxy_async_smem();
+          // the next tile's scores as soon as these have been read, where the weights lie apart
+          if (G::kApart && more) {
+            const bool both = tiles == 2;
+            if (!wait_two(&s_read[0], np[0] & 1, &s_read[both], (both ? np[1] : np[0]) & 1)) break;
+            tc_fence_after();
+            scores(0, u + 2);
+            if (both) scores(1, u + 2);
+            commit(leader, &empty[(u + 2) % G::kSlots]);
+            if (i + 2 == count) commit(leader, &q_empty);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == tiles || !sums(t, u + 1, begun[t])) break;
+            begun[t] = true;
+            if (t == tiles - 1) commit(leader, &empty[(u + 1) % G::kSlots]);
+            if (G::kApart || !more) commit(leader, &o_full[t]);
+            if (!G::kApart && more) {
+              scores(t, u + 2);
+              if (t == tiles - 1) {
+                commit(leader, &empty[(u + 2) % G::kSlots]);
+                if (i + 2 == count) commit(leader, &q_empty);
+              }
+            }
+          }
+          u += 2;
+        }
       }
     }
     // the products are done, and their commits have arrived
@@ -819,7 +870,7 @@ bool in_copies(const AttnArgs& a) {
   return a.num_pages > 0 && (a.page_size % kM == 0 || (a.page_size >= 8 && kM % a.page_size == 0));
 }
 
-template <int D, bool GATHER>
+template <int D, bool GATHER, bool TWO>
 cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int tokens = kM / a.group, per = std::min(a.page_size, kM);
   CUtensorMap q, k, v;
@@ -837,15 +888,15 @@ cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int grid = attn::sms(), rows = 2 * tokens * a.group;
   a.by_grid = divider(grid);
   a.whole = attn::undivided(a, rows, kM, kWhole);
-  const cudaError_t e = launch_pdl(attend_many_kernel<D, GATHER>, dim3(grid), dim3(kThreads), Geo<D>::kSmem,
+  const cudaError_t e = launch_pdl(attend_many_kernel<D, GATHER, TWO>, dim3(grid), dim3(kThreads), Geo<D>::kSmem,
                                    stream, q, k, v, a, tokens);
   if (e != cudaSuccess || a.whole) return e;
   return attn::launch_join(a, grid, rows, attn::parts(a.workspace, grid, rows, D), stream);
 }
 
-template <int D, bool GATHER>
+template <int D, bool GATHER, bool TWO>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attend_many_kernel<D, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attend_many_kernel<D, GATHER, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)Geo<D>::kSmem);
 }
 
@@ -864,16 +915,26 @@ cudaError_t attn::prepare_many() {
       g_encode_status = cudaErrorNotSupported;
   });
   if (g_encode_status != cudaSuccess) return g_encode_status;
-  cudaError_t e = prepare<64, false>();
-  if (e == cudaSuccess) e = prepare<64, true>();
-  if (e == cudaSuccess) e = prepare<128, false>();
-  if (e == cudaSuccess) e = prepare<128, true>();
+  cudaError_t e = prepare<64, false, false>();
+  if (e == cudaSuccess) e = prepare<64, false, true>();
+  if (e == cudaSuccess) e = prepare<64, true, false>();
+  if (e == cudaSuccess) e = prepare<128, false, false>();
+  if (e == cudaSuccess) e = prepare<128, true, false>();
   return e;
 }
 
+// 64 values a head are bound by the issue of products, 24 small ones a pair of tiles with the waits before
+// them. Two issuing warps hide those, where both query tiles have rows and few tiles are cut by a mask
+// (us with one | two, 32 heads on 8: 512 tokens over 30000 170 | 146, a prompt of 8192 384 | 353, 16 times 64
+// tokens over 3000 55 | 52; but one query tile, 16 times 20 tokens over 3000, 39.6 | 40.6, and with a window of
+// 1024 the prompt 140 | 143, a batch of prompts and single tokens 99 | 101, for which one warp then looks
+// through the values).
 cudaError_t attn::launch_many(const AttnArgs& a, cudaStream_t stream) {
-  if (in_copies(a)) return a.head_dim == 64 ? many<64, false>(a, stream) : many<128, false>(a, stream);
-  return a.head_dim == 64 ? many<64, true>(a, stream) : many<128, true>(a, stream);
+  const bool copies = in_copies(a);
+  if (a.head_dim == 128) return copies ? many<128, false, false>(a, stream) : many<128, true, false>(a, stream);
+  if (!copies) return many<64, true, false>(a, stream);
+  const bool two = a.window == 0 && (int64_t)a.num_tokens * a.group > (int64_t)kM * a.num_seqs;
+  return two ? many<64, false, true>(a, stream) : many<64, false, false>(a, stream);
 }
 
 cudaError_t take_attn_faults(unsigned* out) {

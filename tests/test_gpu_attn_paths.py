@@ -109,7 +109,7 @@ def test_long(env, lens, Hq, Hkv, D, page, window):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("window", [0, 150])
-@pytest.mark.parametrize("most", [3, 6, 90])
+@pytest.mark.parametrize("most", [3, 6, 90, 300])
 def test_many_blocks_of_unlike_sizes(env, D, window, most):
     """A thread block goes through several blocks of rows, of one query tile and of two, of one tile of
     keys and of several, and through parts of some."""
@@ -208,11 +208,12 @@ def test_past_32_bit_offsets(env, D, Hkv, page):
 
 @pytest.mark.parametrize("page", [16, 5])
 @pytest.mark.parametrize("D", [64, 128])
-def test_wait_runs_out_sets_flag_then_device_recovers(env, D, page):
+@pytest.mark.parametrize("lens", [[(100, 300), (20, 700)], [(300, 300), (20, 700)]])
+def test_wait_runs_out_sets_flag_then_device_recovers(env, D, page, lens):
     """With nothing copied every wait of the form for many rows gives up: the call returns, bit 0 is
     reported, nothing was written; the same call right after is right, with no bit set."""
     torch, mol = env
-    p = au.problem(torch, D, [(100, 300), (20, 700)], 4, 2, D, page)
+    p = au.problem(torch, D, lens, 4, 2, D, page)
     want = attend(env, p)
     assert mol.mol_take_fault_flags() == 0
     try:
