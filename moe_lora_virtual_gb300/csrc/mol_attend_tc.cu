@@ -241,6 +241,9 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
 // Tiles are dealt as in attend_few; parts of blocks join in launch_join. Pages outside the cache are zeros
 // (the copy's fill); what a row does not see is replaced among its scores.
+// 509 tokens over 30001, 32 heads of 128 on 4: 183 us, 1360 TFLOP/s (0.71 of the measured rate), a prompt of
+// 8192 426 us, 1290. A pair of tiles takes 3200 cycles: a query tile's own products 1340, its softmax 1525,
+// hand-overs 380, against 2680 of both tiles' products.
 template <int D, bool GATHER, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
