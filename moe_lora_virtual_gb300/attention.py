@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -100,6 +101,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, interleaved: boo
                 1.0 if magnitude is None else magnitude)
 
 
+def _number(x) -> int:
+    """x as an int32 argument takes it: one past its ends becomes the nearer end (ctypes would keep its
+    low 32 bits, which may be any number)."""
+    return min(max(operator.index(x), -(1 << 31)), (1 << 31) - 1)
+
+
 def _heads(t: torch.Tensor, name: str):
     """(token stride, head stride) of a CUDA operand [tokens, heads, head_dim]."""
     if t.dtype != _bf16 or not t.is_cuda:
@@ -123,8 +130,8 @@ def _rope_table(rope: Rope) -> _RopeTable:
     f = rope.inv_freq
     if f.dim() != 1:
         raise ValueError("inv_freq: expected one dimension")
-    return _RopeTable(_flat(f, _f32, "inv_freq", f.shape), 2 * f.shape[0], int(rope.interleaved),
-                      rope.magnitude)
+    return _RopeTable(_flat(f, _f32, "inv_freq", f.shape), _number(2 * f.shape[0]),
+                      _number(int(rope.interleaved)), rope.magnitude)
 
 
 def _paged(k: torch.Tensor, v: torch.Tensor) -> _PagedCache:
@@ -141,7 +148,7 @@ def _paged(k: torch.Tensor, v: torch.Tensor) -> _PagedCache:
     s, n = k.stride(), k.shape
     # a single page, token or head has no stride that matters
     return _PagedCache(k.data_ptr(), v.data_ptr(), s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0,
-                       s[2] if n[2] > 1 else 0, n[0], n[1], n[2], n[3])
+                       s[2] if n[2] > 1 else 0, n[0], *(_number(x) for x in n[1:]))
 
 
 def _like(out: Optional[torch.Tensor], x: torch.Tensor, stream, name: str) -> torch.Tensor:
@@ -218,7 +225,7 @@ def mol_paged_attention_workspace_bytes(num_seqs: int, num_tokens: int, num_q_he
                                         num_kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace mol_paged_attention uses for these sizes."""
     return (_mol._lib or _mol.library()).mol_paged_attention_workspace_bytes(
-        num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim)
+        num_seqs, num_tokens, _number(num_q_heads), _number(num_kv_heads), _number(head_dim))
 
 
 def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -230,9 +237,10 @@ def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
 
     page_table int32 [B, pages] (entries outside the cache, as -1: tokens that no row sees); kv_lens
     int32 [B]: cached tokens, the new ones among them; q_starts int32 [B + 1]: where each sequence's
-    rows begin (None: a row each); window > 0: the last tokens that a row sees, its own among them;
-    scale: head_dim^-0.5 unless given. Rows that see nothing are 0; rows of no sequence keep what out
-    held. workspace: mol_paged_attention_workspace_bytes of scratch. out may be `q`."""
+    rows begin (None: a row each); window > 0: the last tokens that a row sees, its own among them
+    (2^31 - 1 and more: all of them); scale: head_dim^-0.5 unless given. Rows that see nothing are 0;
+    rows of no sequence keep what out held. workspace: mol_paged_attention_workspace_bytes of scratch.
+    out may be `q`."""
     if _block._native is not None and out is None and workspace is None and stream is None:
         done = _block._native.paged_attention(
             _entry("mol_paged_attention"), _entry("mol_paged_attention_workspace_bytes"), q, k_cache,
@@ -267,6 +275,6 @@ def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         _here(workspace, "workspace")
     _call("mol_paged_attention", q.data_ptr(), qt, qh, cache, page_table.data_ptr(),
           page_table.stride(0) if B > 1 else pages, pages, lens, starts, B, T, H,
-          D ** -0.5 if scale is None else scale, window, out.data_ptr(), ot, oh,
+          D ** -0.5 if scale is None else scale, _number(window), out.data_ptr(), ot, oh,
           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, q))
     return out
