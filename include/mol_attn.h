@@ -114,6 +114,7 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * at most MOL_ATTN_MAX_GROUP times it; scale > 0, it and its product with
  * log2(e) finite; window >= 0; num_tokens * num_q_heads < 2^31; num_tokens +
  * max_pages * page_size <= 2^31 - 1024; with g query heads to a key head,
+ * num_tokens * g <= 2^31 - 1024 and
  * (num_tokens * g / 16 + num_seqs) * (max_pages * page_size / 64 + 4) < 2^31
  * (32 K rows of group 8 over tables of 8 M tokens).
  */

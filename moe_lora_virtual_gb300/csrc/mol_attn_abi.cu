@@ -168,8 +168,9 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
   // positions, a window before the first and a tile behind the last are 32-bit numbers
   const int64_t cached = (int64_t)max_pages * cache->page_size;
   if (num_tokens + cached > ((int64_t)1 << 31) - 1024) return MOL_ERR_UNSUPPORTED;
-  // the tiles of a head are counted in 32 bits
+  // the rows of a key head, with a block's more, and the tiles of a head are counted in 32 bits
   const int64_t rows = num_tokens * (num_q_heads / cache->num_heads);
+  if (rows > ((int64_t)1 << 31) - 1024) return MOL_ERR_UNSUPPORTED;
   if ((rows / 16 + num_seqs) * (cached / 64 + 4) >= (int64_t)1 << 31)
     return MOL_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return MOL_OK;
