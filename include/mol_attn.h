@@ -116,7 +116,7 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * max_pages * page_size <= 2^31 - 1024; with g query heads to a key head,
  * num_tokens * g <= 2^31 - 1024 and
  * (num_tokens * g / 16 + num_seqs) * (max_pages * page_size / 64 + 4) < 2^31
- * (32 K rows of group 8 over tables of 8 M tokens).
+ * (16 K tokens of group 8 over tables of 8 M).
  */
 int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                             const mol_paged_cache* cache, const int32_t* page_table,

@@ -1,10 +1,12 @@
 """CPU checks of the sizes at which paged attention's 32-bit numbers end: the last ones that are taken and
 the first ones that are not. A call without scratch is refused behind the sizes, so none reaches a kernel."""
 
+import re
+
 import pytest
 
 from tests.test_abi_cpu import mol, needs_nvcc  # noqa: F401  (fixture)
-from tests.test_attn_cpu import CAPACITY, P, UNSUPPORTED, cache
+from tests.test_attn_cpu import CAPACITY, P, UNSUPPORTED, cache, header
 
 pytestmark = needs_nvcc
 
@@ -27,3 +29,17 @@ def test_rows_of_a_key_head(mol, group):  # noqa: F811
         assert attend(mol, T, group, **one) == UNSUPPORTED
     # (with more key heads the rows of each are fewer)
     assert attend(mol, ((1 << 31) - 1) // (2 * group), 2 * group, heads=2) == CAPACITY
+
+
+def test_tiles_of_a_head(mol):  # noqa: F811
+    """8 M cached tokens in pages of 8, group 8: the product of the header's bound passes 2^31 between 32765
+    tokens and 32766."""
+    for T, status in ((32765, CAPACITY), (32766, UNSUPPORTED), (32768, UNSUPPORTED)):
+        assert attend(mol, T, 16, pages=1 << 20) == status
+        assert ((T * 8 // 16 + 1) * ((8 << 20) // 64 + 4) < 1 << 31) == (status == CAPACITY)
+
+
+def test_the_size_that_the_header_offers_is_taken(mol):  # noqa: F811
+    offered = re.search(r"\((\d+) K (?:rows|tokens) of group (\d+) over\s+(?:\*\s+)?tables of (\d+) M", header())
+    T, group, cached = (int(x) for x in offered.groups())
+    assert attend(mol, T << 10, 2 * group, pages=cached << 17) == CAPACITY
