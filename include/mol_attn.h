@@ -107,8 +107,9 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * row does not see does not reach it, whatever it holds (NaN, infinities).
  * A kv_lens[b] past the table's width is taken as that width; q_starts outside
  * [0, num_tokens] as the nearer end (they do not decrease).
- *   workspace   mol_paged_attention_workspace_bytes of scratch, 16-byte aligned;
- *               calls that may run at the same time need one each
+ *   workspace   mol_paged_attention_workspace_bytes of scratch, of these sizes or
+ *               larger ones, 16-byte aligned; calls that may run at the same
+ *               time need one each
  * out may be q itself (same strides).
  * Contract: head_dim 64, 128 or 256; num_q_heads a multiple of cache->num_heads,
  * at most MOL_ATTN_MAX_GROUP times it; scale > 0, it and its product with
@@ -126,7 +127,12 @@ int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_hea
                             int64_t out_token_stride, int64_t out_head_stride, void* workspace,
                             size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace mol_paged_attention takes for these sizes (host arithmetic). */
+/*
+ * Bytes of workspace with which every mol_paged_attention call of at most
+ * num_seqs sequences and num_tokens tokens of these heads is served (host
+ * arithmetic): a buffer of the largest sizes serves all calls. 0 for sizes that
+ * the call refuses.
+ */
 size_t mol_paged_attention_workspace_bytes(int64_t num_seqs, int64_t num_tokens,
                                            int32_t num_q_heads, int32_t num_kv_heads,
                                            int32_t head_dim);

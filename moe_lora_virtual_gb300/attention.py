@@ -223,7 +223,8 @@ def mol_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
 
 def mol_paged_attention_workspace_bytes(num_seqs: int, num_tokens: int, num_q_heads: int,
                                         num_kv_heads: int, head_dim: int) -> int:
-    """Bytes of workspace mol_paged_attention uses for these sizes."""
+    """Bytes of workspace that serve every mol_paged_attention of at most num_seqs sequences and
+    num_tokens tokens of these heads (of a long-lived buffer: of the largest sizes)."""
     return (_mol._lib or _mol.library()).mol_paged_attention_workspace_bytes(
         num_seqs, num_tokens, _number(num_q_heads), _number(num_kv_heads), _number(head_dim))
 
@@ -239,8 +240,8 @@ def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     int32 [B]: cached tokens, the new ones among them; q_starts int32 [B + 1]: where each sequence's
     rows begin (None: a row each); window > 0: the last tokens that a row sees, its own among them
     (2^31 - 1 and more: all of them); scale: head_dim^-0.5 unless given. Rows that see nothing are 0;
-    rows of no sequence keep what out held. workspace: mol_paged_attention_workspace_bytes of scratch.
-    out may be `q`."""
+    rows of no sequence keep what out held. workspace: mol_paged_attention_workspace_bytes of scratch,
+    of these sizes or larger ones. out may be `q`."""
     if _block._native is not None and out is None and workspace is None and stream is None:
         done = _block._native.paged_attention(
             _entry("mol_paged_attention"), _entry("mol_paged_attention_workspace_bytes"), q, k_cache,

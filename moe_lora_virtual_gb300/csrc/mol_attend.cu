@@ -577,12 +577,20 @@ static Form form(int64_t num_seqs, int64_t rows, int head_dim) {
   return head_dim == 64 && rows <= 32 * num_seqs ? Form::kFew32 : Form::kMany;
 }
 
-size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
-  if (num_seqs <= 0 || num_tokens <= 0) return 0;
-  const Form f = form(num_seqs, num_tokens * group, head_dim);
+static size_t bytes_of(Form f, int group, int head_dim) {
   return f == Form::kMany   ? attn::many_bytes(group, head_dim)
          : f == Form::kWide ? attn::wide_bytes()
                           : attn::parts_bytes(attn::kMaxGrid, f == Form::kFew32 ? 32 : 16, head_dim);
+}
+size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim) {
+  if (num_seqs <= 0 || num_tokens <= 0) return 0;
+  return bytes_of(form(num_seqs, num_tokens * group, head_dim), group, head_dim);
+}
+// A form for more rows takes more scratch, and of at most so many sequences and tokens it is one sequence
+// with all the tokens that has the most rows.
+size_t attn_workspace_most(int64_t num_tokens, int group, int head_dim) {
+  if (num_tokens <= 0) return 0;
+  return bytes_of(form(1, num_tokens * group, head_dim), group, head_dim);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {

@@ -69,7 +69,9 @@ struct AttnArgs {
   void* workspace;
   bool whole;  // blocks of rows are not dealt out in parts (set by the launches)
 };
+// Scratch of a call of these sizes, and the most that one of up to num_tokens takes.
 size_t attn_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int group, int head_dim);
+size_t attn_workspace_most(int64_t num_tokens, int group, int head_dim);
 cudaError_t prepare_attn_kernels();
 cudaError_t take_rope_checks(unsigned long long* first, unsigned long long* count);
 cudaError_t take_attn_checks(unsigned long long* first, unsigned long long* count);

@@ -142,9 +142,10 @@ size_t mol_paged_attention_workspace_bytes(int64_t num_seqs, int64_t num_tokens,
                                            int32_t num_q_heads, int32_t num_kv_heads,
                                            int32_t head_dim) {
   if (num_seqs <= 0 || num_tokens <= 0 || num_kv_heads < 1 || num_q_heads < num_kv_heads ||
-      num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > MOL_ATTN_MAX_GROUP ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  return mol::attn_workspace_bytes(num_seqs, num_tokens, num_q_heads / num_kv_heads, head_dim);
+  return mol::attn_workspace_most(num_tokens, num_q_heads / num_kv_heads, head_dim);
 }
 
 int32_t mol_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
