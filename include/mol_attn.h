@@ -106,7 +106,8 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * before they meet the values, their sum is not; out is rounded once. What a
  * row does not see does not reach it, whatever it holds (NaN, infinities).
  * A kv_lens[b] past the table's width is taken as that width; q_starts outside
- * [0, num_tokens] as the nearer end (they do not decrease).
+ * [0, num_tokens] as the nearer end. They do not decrease: a call in which one
+ * does leaves all of out as it was.
  *   workspace   mol_paged_attention_workspace_bytes of scratch, of these sizes or
  *               larger ones, 16-byte aligned; calls that may run at the same
  *               time need one each

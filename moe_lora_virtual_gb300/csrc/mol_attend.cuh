@@ -70,11 +70,12 @@ MOL_DEV Given given(const AttnArgs& a, int b) {
   }
   return g;
 }
-// From its first row and what the arrays say of its end and its tokens.
+// From its first row and what the arrays say of its end and its tokens. (Fewer than no rows: it ends before it
+// begins, and has no blocks.)
 MOL_DEV Seq sequence(const AttnArgs& a, int start, int end, int kv) {
   Seq s;
   s.start = start;
-  s.n = a.q_starts ? max(min(max(end, 0), a.num_tokens) - start, 0) : 1;
+  s.n = a.q_starts ? min(max(end, 0), a.num_tokens) - start : 1;
   s.kv = min(max(kv, 0), a.max_pages * a.page_size);
   return s;
 }
@@ -145,6 +146,7 @@ MOL_DEV Run deal(const AttnArgs& a, const Given& mine, int rows, int tile, int e
   Seq s = {};
   int blocks = 0, before = 0, sum = 0, n = 0;
   int64_t passed = 0;
+  bool falls = false;
   run.total = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {  // the sum of all units, then where the run begins
@@ -155,6 +157,7 @@ MOL_DEV Run deal(const AttnArgs& a, const Given& mine, int rows, int tile, int e
         n = blocks = 0;
         if (b < a.num_seqs) {
           s = sequence(a, a.num_seqs > THREADS ? given(a, b) : mine);
+          falls |= s.n < 0;
           blocks = num_blocks(a, s, rows);
 #pragma unroll 1
           for (int r = 0; r < blocks; ++r) n += units_of(a, block_of(a, b, s, r, rows, tile), extra);
@@ -182,6 +185,9 @@ MOL_DEV Run deal(const AttnArgs& a, const Given& mine, int rows, int tile, int e
       }
     }
     if (pass == 0) {
+      // Starts that decrease: sequences overlap here and not in the walk, which goes on from where the last
+      // one ended, so parts would be left to thread blocks past the last. Such a call has no units.
+      if (a.q_starts && __syncthreads_or(falls)) run.total = 0;
       run.total *= a.kv_heads;  // (below 2^47; thread blocks below 2^9)
       const int high = divide((int)(run.total >> 20), a.by_grid);
       const int rest = ((int)(run.total >> 20) - high * (int)gridDim.x) << 20 | (int)(run.total & 0xfffff);
@@ -289,7 +295,7 @@ MOL_DEV void begin(const AttnArgs& a, Walk& w, const Place& p, const Run& run, i
   w.k = p.k;
   w.h = p.h;
   w.unit = p.unit;
-  w.left = p.k.tiles > 0 ? run.to - run.from : 0;  // (0: starts that decrease; sums may mislead)
+  w.left = p.k.tiles > 0 ? run.to - run.from : 0;  // (0: lengths that changed under the call)
   if (w.left == 0) return;
   peek(a, w);
   cut(a, w, extra);
