@@ -45,11 +45,12 @@ struct Geo {
 // accumulators; the warps meet where a block ends. Scores: mma.sync with the rows as the 16-row side.
 // Tokens that lie on no page, or past the sequence, are zero in shared memory, whatever memory
 // holds; where a row does not see a token that another one sees, the step's values are looked
-// through, and summed without the tensor cores should one not be finite (0 * NaN is NaN there).
+// through, and summed without the tensor cores should one not be finite (0 * NaN is NaN there). LONG: blocks
+// that may see more than kStretch tokens, their stretches added up in the slot of the block's part.
 // 4 sequences of 131072, one new token each, 64 heads of 128 on 8: 322 us, 6.67 TB/s (0.98 of a copy's rate);
 // 24 of up to 8191, 16 heads on 2: 19.7 us, 3.3 TB/s. What a call takes beside its stream: the deal 1.7 us,
 // pages and first copies 1.2, their data 1.3, a step 0.7, the warps' sums 0.8, the join 2.3.
-template <int D, int MT>
+template <int D, int MT, bool LONG>
 __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
     attend_few_kernel(const __grid_constant__ AttnArgs a) {
   using G = Geo<D, MT>;
@@ -59,6 +60,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
   __shared__ Place s_place;
   __shared__ uint32_t s_held[kWarps][G::kStages];
   __shared__ float2 s_top[kWarps][G::kRows];
+  __shared__ float2 s_met[LONG ? 2 : 1][G::kRows];  // maxima and sums of a block's stretches so far, of even and odd ones
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* ring = smem + warp * (G::kStages * G::kStageBytes);
   unsigned char* shared = smem + G::kRing;
@@ -72,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
     return;
   }
   constexpr int kStep = G::kStep;
-  attn::Walk load, work;  // over the run, of the copies and of the products
+  attn::Walk<LONG> load, work;  // over the run, of the copies and of the products
   attn::begin(a, load, s_place, run, G::kRows, G::kTile, kExtra);
   work = load;
   int load_tile = 0;  // of load.count
@@ -341,10 +343,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
     }
 
     // ------------------------------------------------------------ the warps' sums become one
-    const bool begins = first == 0, part = !begins || !work.ends();
+    const bool begins = work.begins(), joins = work.joins(), stays = work.stays(kExtra);
+    const bool part = stays || !begins || !work.ends();
     const int slot = (int)(2 * c) + (begins ? 1 : 0);
+    const int odd = LONG ? (first - work.from) / (attn::kStretch / G::kTile) & 1 : 0;
     const int start = k.s.start, row0 = k.row0, nrows = k.nrows;
-    if (begins && part && tid == 0) record = {work.last(run), start, row0, nrows, h, {}};
+    if (begins && part && !stays && tid == 0) record = {work.last(run), start, row0, nrows, h, {}};
     attn::go_on(a, work, G::kRows, G::kTile, kExtra);
     if (work.more()) ask_queries(work.k, work.h);
 #pragma unroll
@@ -390,12 +394,22 @@ __global__ void __launch_bounds__(kThreads, Geo<D, MT>::kPerSM)
         x.z += f * y.z;
         x.w += f * y.w;
       }
+      float4* const met = reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col);
+      if (joins) {  // (the thread's own values of the stretch before)
+        const float2 t = s_met[odd ^ 1][row];
+        const float4 y = *met;
+        const float most = fmaxf(m, t.x), base = most == -INFINITY ? 0.f : most;
+        const float f = attn::ex2(t.x - base), own = attn::ex2(m - base);
+        m = most;
+        l = f * t.y + own * l;
+        x = make_float4(f * y.x + own * x.x, f * y.y + own * x.y, f * y.z + own * x.z, f * y.w + own * x.w);
+      }
       if (kChecked && !MOL_CHECK(start + divide(row0 + row, a.by_group) < a.num_tokens, MOL_CHECK_ROW,
                                  start + divide(row0 + row, a.by_group)))
         continue;
       if (part) {
-        *reinterpret_cast<float4*>(parts.sums + ((int64_t)slot * G::kRows + row) * D + col) = x;
-        if (col == 0) parts.tops[slot * G::kRows + row] = make_float2(m, l);
+        *met = x;
+        if (col == 0) (stays ? s_met[odd][row] : parts.tops[slot * G::kRows + row]) = make_float2(m, l);
       } else {
         const int r = row0 + row, token = divide(r, a.by_group);
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
@@ -507,15 +521,20 @@ cudaError_t attend_few(const AttnArgs& args, cudaStream_t stream) {
   // Up to four tiles (two of wide heads) one after the other take no longer than parts and their join: one
   // request of 120 tokens, 128 values a head, 7.1 us against 9.5, of 250 8.8 against 9.7.
   a.whole = attn::undivided(a, G::kRows, G::kTile, D == 256 ? 2 : 4);
-  const cudaError_t e = launch_pdl(attend_few_kernel<D, MT>, dim3(grid), dim3(kThreads), G::kSmem, stream, a);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kThreads), G::kSmem, stream, a); };
+  const cudaError_t e = attn::beyond_a_stretch(a, G::kRows, G::kTile) ? go(attend_few_kernel<D, MT, true>)
+                                                                     : go(attend_few_kernel<D, MT, false>);
   if (e != cudaSuccess || a.whole) return e;
   return attn::launch_join(a, grid, G::kRows, attn::parts(a.workspace, grid, G::kRows, D), stream);
 }
 
 template <int D, int MT>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attend_few_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Geo<D, MT>::kSmem);
+  auto set = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<D, MT>::kSmem);
+  };
+  const cudaError_t e = set(attend_few_kernel<D, MT, false>);
+  return e != cudaSuccess ? e : set(attend_few_kernel<D, MT, true>);
 }
 
 }  // namespace
@@ -531,11 +550,17 @@ int attn::sms() {
   return n;
 }
 
+// Cached tokens that a block's rows see together, at most.
+static int64_t most_tokens(const AttnArgs& a, int rows, int tile) {
+  const int64_t tokens = (int64_t)a.max_pages * a.page_size;
+  // (a window's rows see so many, and a tile's beginning is theirs by chance)
+  return a.window > 0 ? std::min<int64_t>(tokens, (int64_t)a.window + rows / a.group + tile) : tokens;
+}
 bool attn::undivided(const AttnArgs& a, int rows, int tile, int tiles) {
-  int64_t tokens = (int64_t)a.max_pages * a.page_size;
-  // (a window's rows see so many tokens together, and a tile's beginning is theirs by chance)
-  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + rows / a.group + tile);
-  return tokens <= (int64_t)tiles * tile;
+  return most_tokens(a, rows, tile) <= (int64_t)tiles * tile;
+}
+bool attn::beyond_a_stretch(const AttnArgs& a, int rows, int tile) {
+  return most_tokens(a, rows, tile) > kStretch;
 }
 
 cudaError_t attn::launch_join(const AttnArgs& a, int grid, int rows, const Parts& p,

@@ -237,20 +237,35 @@ MOL_DEV void prefetch_table(const AttnArgs& a) {
   if (at < all) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.page_table + at));
 }
 
-// A walk over a thread block's run, a block's head at a time.
+// Cached tokens whose products one sum takes. A matrix instruction cuts what does not fit its fp32 sum, so a
+// sum of like signs falls short by 2^-24 or so an instruction of 16 tokens: 2^-8.5 a million, more than half of
+// a bf16 step. Behind 2^16 (2^-12.5) the sum goes to memory and a fresh one is begun, to be added in fp32.
+constexpr int kStretch = 1 << 16;
+// Whether a block may see more, for which the kernels have a form of their own: with what it takes to go on
+// and to add, the others would be slower (a prompt of 8192 434 us against 425, mixed batches 104 against 99).
+bool beyond_a_stretch(const AttnArgs& a, int rows, int tile);
+
+// A walk over a thread block's run, a block's head at a time, with LONG of a long block a stretch at a time.
+template <bool LONG>
 struct Walk {
   Block k;
   int h;
-  int first, count;  // tiles of the block in the run
+  int first, count;  // tiles of the block, or of a stretch of it
+  int from;          // the block's first tile in the run (LONG)
   int unit;
   int64_t left;      // units of the run from here on
   int kv1, end1;     // what the caller's arrays say of the sequence behind this one, asked for ahead
   MOL_DEV bool more() const { return left > 0; }
+  MOL_DEV bool begins() const { return (LONG ? from : first) == 0; }
   MOL_DEV bool ends() const { return first + count >= k.tiles; }
+  MOL_DEV bool joins() const { return LONG && first > from; }  // a stretch behind another one
+  MOL_DEV int taken(int extra) const { return first + count + extra - unit; }  // units of the stretch
+  MOL_DEV bool stays(int extra) const { return LONG && !ends() && left > taken(extra); }  // another one behind it
   // The last thread block that has a tile of this block, which the run begins and does not end.
   MOL_DEV int last(const Run& r) const { return r.owner((uint32_t)(k.tiles - first - count) - 1); }
 };
-MOL_DEV void cut(const AttnArgs& a, Walk& w, int extra) {
+template <bool LONG>
+MOL_DEV void cut(const AttnArgs& a, Walk<LONG>& w, int tile, int extra) {
   if (a.whole) {
     w.first = 0;
     w.count = w.k.tiles;
@@ -259,15 +274,26 @@ MOL_DEV void cut(const AttnArgs& a, Walk& w, int extra) {
   const int n = (int)min((int64_t)(w.k.tiles + extra - w.unit), w.left);
   w.first = max(w.unit - extra, 0);
   w.count = max(w.unit + n - extra, 0) - w.first;
+  if (LONG) w.count = min(w.count, kStretch / tile);
 }
-MOL_DEV void peek(const AttnArgs& a, Walk& w) {
+template <bool LONG>
+MOL_DEV void peek(const AttnArgs& a, Walk<LONG>& w) {
   w.kv1 = w.end1 = 0;
   if (w.k.b + 1 >= a.num_seqs) return;
   w.kv1 = load_int(a.kv_lens + w.k.b + 1);
   if (a.q_starts) w.end1 = load_int(a.q_starts + w.k.b + 2);
 }
-// On to the next head or block; ones that the run has no tile of are passed by.
-MOL_DEV void go_on(const AttnArgs& a, Walk& w, int rows, int tile, int extra) {
+// On to the next stretch, head or block; ones that the run has no tile of are passed by.
+template <bool LONG>
+MOL_DEV void go_on(const AttnArgs& a, Walk<LONG>& w, int rows, int tile, int extra) {
+  if (w.stays(extra)) {
+    const int n = w.taken(extra);
+    w.left -= n;
+    w.unit += n;
+    cut(a, w, tile, extra);
+    return;
+  }
+  w.from = 0;
 #pragma unroll 1
   do {
     w.left -= units_of(a, w.k, extra) - w.unit;
@@ -288,23 +314,26 @@ MOL_DEV void go_on(const AttnArgs& a, Walk& w, int rows, int tile, int extra) {
       }
       w.k = block_of(a, w.k.b, w.k.s, r, rows, tile);
     }
-    cut(a, w, extra);
+    cut(a, w, tile, extra);
   } while (w.count == 0);
 }
-MOL_DEV void begin(const AttnArgs& a, Walk& w, const Place& p, const Run& run, int rows, int tile, int extra) {
+template <bool LONG>
+MOL_DEV void begin(const AttnArgs& a, Walk<LONG>& w, const Place& p, const Run& run, int rows, int tile,
+                   int extra) {
   w.k = p.k;
   w.h = p.h;
   w.unit = p.unit;
   w.left = p.k.tiles > 0 ? run.to - run.from : 0;  // (0: lengths that changed under the call)
   if (w.left == 0) return;
   peek(a, w);
-  cut(a, w, extra);
+  cut(a, w, tile, extra);
+  w.from = w.first;
   if (w.count == 0) go_on(a, w, rows, tile, extra);
 }
 
 // Parts of blocks that several thread blocks share. Thread block c leaves the part that continues its
-// predecessor's block in slot 2c, the one that it begins and does not end in slot 2c + 1 with a
-// record of it: last thread block of it (-1: there is none), the sequence's first row of q, first row
+// predecessor's block in slot 2c, the one that it begins and does not end in slot 2c + 1 (its last one, so until
+// then the stretches of others that it begins meet there) with a record of it: last thread block of it (-1: there is none), the sequence's first row of q, first row
 // within it, rows, head.
 struct Record {
   int last, start, row0, nrows, h, pad[3];

@@ -239,12 +239,12 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
 //                   not finite are zeroed where no row sees them; where another row does, the tile's
 //                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
-// Tiles are dealt as in attend_few; parts of blocks join in launch_join. Pages outside the cache are zeros
+// Tiles are dealt as in attend_few, long blocks summed by stretches (LONG); parts of blocks join in launch_join. Pages outside the cache are zeros
 // (the copy's fill); what a row does not see is replaced among its scores.
 // 509 tokens over 30001, 32 heads of 128 on 4: 183 us, 1360 TFLOP/s (0.71 of the measured rate), a prompt of
 // 8192 426 us, 1290. A pair of tiles takes 3200 cycles: a query tile's own products 1340, its softmax 1525,
 // hand-overs 380, against 2680 of both tiles' products.
-template <int D, bool GATHER, bool TWO>
+template <int D, bool GATHER, bool TWO, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, AttnArgs a, int tile_tokens) {
@@ -309,11 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool fault = false;
   const unsigned long long limit = g_many_wait_limit_ns;
   // (each role begins its own, from shared memory: nothing of it is held in registers before)
-  auto begin = [&](attn::Walk& w) {
+  using Walk = attn::Walk<LONG>;
+  auto begin = [&](Walk& w) {
     w.left = 0;
     if (s_run.any) attn::begin(a, w, s_place, s_run, rows, kM, kExtra);
   };
-  auto next = [&](attn::Walk& w) { attn::go_on(a, w, rows, kM, kExtra); };
+  auto next = [&](Walk& w) { attn::go_on(a, w, rows, kM, kExtra); };
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!GATHER) {
       const int per = a.page_size < kM ? a.page_size : kM;  // tokens a copy
       const int copies = kM / per;
-      attn::Walk w;
+      Walk w;
       for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
         const Block& k = w.k;
         const int32_t* pages = a.page_table + k.b * a.table_stride;
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kv = warp - 9;
       const uint16_t* src = kv ? a.v : a.k;
       u = kv;
-      attn::Walk w;
+      Walk w;
       for (begin(w); w.more() && !fault && !(g_many_test_stall & 1); next(w)) {
         const Block& k = w.k;
         const int32_t* pages = a.page_table + k.b * a.table_stride;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ values that not every row sees
     uint32_t u = 0, n = 0;
     const int per = a.page_size < kM ? a.page_size : kM;
-    attn::Walk w;
+    Walk w;
     for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       const int shift = k.s.kv - k.s.n;
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    attn::Walk w;
+    Walk w;
     if constexpr (TWO) {
       // One warp's waits while the other's products run; the scores go on into the next block. A tile's next
       // scores are issued behind the products of the weights before, which their softmax waits for first.
@@ -657,11 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, n = 0, u = 0, no = 0;  // scores waited for, tiles, ring slots, sums waited for
     Record record = {};
     record.last = -1;
-    attn::Walk w;
+    Walk w;
     for (begin(w); w.more() && !fault; next(w)) {
       const Block& k = w.k;
       const int count = w.count;
-      const bool begins = w.first == 0, part = !begins || !w.ends();
+      const bool begins = w.begins(), stays = w.stays(kExtra), part = stays || !begins || !w.ends();
       const int in_tile = min(k.nrows - t * tile_rows, tile_rows);  // rows of this query tile
       if (in_tile > 0) {
         const int shift = k.s.kv - k.s.n, row = k.row0 + t * tile_rows;
@@ -809,16 +810,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = t * tile_rows + local, r = k.row0 + at, token = divide(r, a.by_group);
         const bool mine = local < in_tile && MOL_CHECK(k.s.start + token < a.num_tokens, MOL_CHECK_ROW,
                                                        k.s.start + token);
+        const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
+        float* part_dst = parts.sums + ((int64_t)slot * rows + at) * D;
+        float was = 0.f, own = 1.f;  // factors of the stretches before and of this one
+        if (w.joins() && mine) {
+          const float2 met = parts.tops[(int64_t)slot * rows + at];
+          const float most = fmaxf(top, met.x), base = most == -INFINITY ? 0.f : most;
+          was = ex2(met.x - base);
+          own = ex2(top - base);
+          top = most;
+          sum = was * met.y + own * sum;
+        }
         const float inv = top == -INFINITY ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(w.h * a.group + r - token * a.group) * a.out_head_stride;
-        const Parts parts = attn::parts(a.workspace, gridDim.x, rows, D);
-        float* part_dst = parts.sums + ((int64_t)slot * rows + at) * D;
 #pragma unroll 1
         for (int x = 0; x < D; x += 32) {
           uint32_t o[32];
           tmem_ld_x32(to_ + x, o);
           tmem_wait_ld();
+          if (w.joins() && mine) {  // (what the thread itself left there)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(part_dst + x + e);
+              o[e] = __float_as_uint(was * y.x + own * __uint_as_float(o[e]));
+              o[e + 1] = __float_as_uint(was * y.y + own * __uint_as_float(o[e + 1]));
+              o[e + 2] = __float_as_uint(was * y.z + own * __uint_as_float(o[e + 2]));
+              o[e + 3] = __float_as_uint(was * y.w + own * __uint_as_float(o[e + 3]));
+            }
+          }
           if (mine && part) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -838,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part && mine) parts.tops[(int64_t)slot * rows + at] = make_float2(top, sum);
         tc_fence_before();
       }
-      if (begins && part) record = {w.last(s_run), k.s.start, k.row0, k.nrows, w.h, {}};
+      if (begins && part && !stays) record = {w.last(s_run), k.s.start, k.row0, k.nrows, w.h, {}};
       n += count;
       u += 2 * count;
     }
@@ -891,16 +911,22 @@ cudaError_t many(AttnArgs a, cudaStream_t stream) {
   const int grid = attn::sms(), rows = 2 * tokens * a.group;
   a.by_grid = divider(grid);
   a.whole = attn::undivided(a, rows, kM, kWhole);
-  const cudaError_t e = launch_pdl(attend_many_kernel<D, GATHER, TWO>, dim3(grid), dim3(kThreads), Geo<D>::kSmem,
-                                   stream, q, k, v, a, tokens);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), Geo<D>::kSmem, stream, q, k, v, a, tokens);
+  };
+  const cudaError_t e = attn::beyond_a_stretch(a, rows, kM) ? go(attend_many_kernel<D, GATHER, TWO, true>)
+                                                           : go(attend_many_kernel<D, GATHER, TWO, false>);
   if (e != cudaSuccess || a.whole) return e;
   return attn::launch_join(a, grid, rows, attn::parts(a.workspace, grid, rows, D), stream);
 }
 
 template <int D, bool GATHER, bool TWO>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attend_many_kernel<D, GATHER, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Geo<D>::kSmem);
+  auto set = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<D>::kSmem);
+  };
+  const cudaError_t e = set(attend_many_kernel<D, GATHER, TWO, false>);
+  return e != cudaSuccess ? e : set(attend_many_kernel<D, GATHER, TWO, true>);
 }
 
 }  // namespace

@@ -33,7 +33,9 @@ constexpr int kWhole = 8;                     // most tiles of blocks that go un
 // queries (8 KB, no registers are left for them) and the tile (32 KB) for 2 x 16 x 32 x 256 products, which
 // at 128 bytes a cycle allows 470 TFLOP/s; 16 query heads of 2 key heads reach 233 on 8 prompts of 8192
 // tokens and 195 on 8 of 2048 (attend_few: 74), the rest waits, as two warps a scheduler hide little.
-// Tiles are dealt, and what a row does not see is treated, as in attend_few.
+// Tiles are dealt, what a row does not see is treated, and long blocks are summed by stretches (LONG), as in
+// attend_few.
+template <bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_scan[kWarps + 1];
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     if (tid == 0) parts.records[c].last = -1;
     return;
   }
-  attn::Walk load, work;  // over the run, of the copies and of the products
+  attn::Walk<LONG> load, work;  // over the run, of the copies and of the products
   attn::begin(a, load, s_place, run, kRows, kTile, kExtra);
   work = load;
   int load_tile = 0;  // of load.count
@@ -260,31 +262,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     }
 
     // ------------------------------------------------------------ the rows, or a part of them
-    const bool begins = first == 0, part = !begins || !work.ends();
+    const bool begins = work.begins(), stays = work.stays(kExtra), joins = work.joins();
+    const bool part = stays || !begins || !work.ends();
     const int slot = (int)(2 * c) + (begins ? 1 : 0);
-    if (begins && part && tid == 0) record = {work.last(run), k.s.start, k.row0, k.nrows, h, {}};
+    if (begins && part && !stays && tid == 0) record = {work.last(run), k.s.start, k.row0, k.nrows, h, {}};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float l = sum[i];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       const int row = row_w + g + 8 * i;
+      float was = 0.f, own = 1.f;  // factors of the stretches before and of this one
+      if (joins) {
+        float2 met = t4 == 0 ? parts.tops[(int64_t)slot * kRows + row] : make_float2(0.f, 0.f);
+        met.x = __shfl_sync(0xffffffffu, met.x, lane & ~3);
+        met.y = __shfl_sync(0xffffffffu, met.y, lane & ~3);
+        const float most = fmaxf(top[i], met.x), base = most == -INFINITY ? 0.f : most;
+        was = attn::ex2(met.x - base);
+        own = attn::ex2(top[i] - base);
+        top[i] = most;
+        l = was * met.y + own * l;
+      }
       if (row >= k.nrows) continue;
       const int r = k.row0 + row, token = divide(r, a.by_group);
       if (!MOL_CHECK(k.s.start + token < a.num_tokens, MOL_CHECK_ROW, k.s.start + token)) continue;
-      if (part) {
-        float* dst = parts.sums + ((int64_t)slot * kRows + row) * kD + 2 * t4;
+      float2* sums = reinterpret_cast<float2*>(parts.sums + ((int64_t)slot * kRows + row) * kD + 2 * t4);
+      if (joins) {  // (with what the lane itself left there)
 #pragma unroll
-        for (int n = 0; n < kD / 8; ++n)
-          *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+        for (int n = 0; n < kD / 8; ++n) {
+          const float2 y = sums[n * 4];
+          sums[n * 4] = make_float2(was * y.x + own * o[n][2 * i], was * y.y + own * o[n][2 * i + 1]);
+        }
+      } else if (part) {
+#pragma unroll
+        for (int n = 0; n < kD / 8; ++n) sums[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+      }
+      if (part) {
         if (t4 == 0) parts.tops[(int64_t)slot * kRows + row] = make_float2(top[i], l);
       } else {
         const float inv = top[i] == -INFINITY ? 0.f : 1.f / l;
         uint16_t* dst = a.out + (int64_t)(k.s.start + token) * a.out_token_stride +
                         (int64_t)(h * a.group + r - token * a.group) * a.out_head_stride + 2 * t4;
+        if (joins) {
+#pragma unroll 4
+          for (int n = 0; n < kD / 8; ++n)
+            *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16x2(sums[n * 4].x * inv, sums[n * 4].y * inv);
+        } else {
 #pragma unroll
-        for (int n = 0; n < kD / 8; ++n)
-          *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+          for (int n = 0; n < kD / 8; ++n)
+            *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+        }
       }
     }
     attn::go_on(a, work, kRows, kTile, kExtra);
@@ -299,7 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 size_t attn::wide_bytes() { return attn::parts_bytes(kMaxGrid / 2, kRows, kD); }
 
 cudaError_t attn::prepare_wide() {
-  return cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  auto set = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  };
+  const cudaError_t e = set(attend_wide_kernel<false>);
+  return e != cudaSuccess ? e : set(attend_wide_kernel<true>);
 }
 
 cudaError_t attn::launch_wide(const AttnArgs& args, cudaStream_t stream) {
@@ -307,7 +338,9 @@ cudaError_t attn::launch_wide(const AttnArgs& args, cudaStream_t stream) {
   AttnArgs a = args;
   a.by_grid = divider(grid);
   a.whole = attn::undivided(a, kRows, kTile, kWhole);
-  const cudaError_t e = launch_pdl(attend_wide_kernel, dim3(grid), dim3(kThreads), kSmem, stream, a);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmem, stream, a); };
+  const cudaError_t e = attn::beyond_a_stretch(a, kRows, kTile) ? go(attend_wide_kernel<true>)
+                                                               : go(attend_wide_kernel<false>);
   if (e != cudaSuccess || a.whole) return e;
   return attn::launch_join(a, grid, kRows, attn::parts(a.workspace, grid, kRows, kD), stream);
 }
