@@ -101,7 +101,8 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * the cache (-1: given back) is seen by no row. Query head h reads key head
  * h / (num_q_heads / cache->num_heads):
  *   out[row, h] = sum_j w_j v[j],  w = softmax over the seen j of scale * q[row, h] . k[j]
- * A row that sees no token is 0. Rows of q that belong to no sequence leave out
+ * A row that sees no token, or whose every score is -infinity, is 0; one with a
+ * score of +infinity or NaN is NaN. Rows of q that belong to no sequence leave out
  * as it was. Products of bf16 with fp32 sums; the weights are rounded to bf16
  * before they meet the values, their sum is not; out is rounded once. What a
  * row does not see does not reach it, whatever it holds (NaN, infinities).

@@ -240,8 +240,9 @@ def mol_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     int32 [B]: cached tokens, the new ones among them; q_starts int32 [B + 1]: where each sequence's
     rows begin (None: a row each), not decreasing (else no row is written); window > 0: the last
     tokens that a row sees, its own among them (2^31 - 1 and more: all of them); scale:
-    head_dim^-0.5 unless given. Rows that see nothing are 0; rows of no sequence keep what out held.
-    workspace: mol_paged_attention_workspace_bytes of scratch, of these sizes or larger ones. out may be `q`."""
+    head_dim^-0.5 unless given. Rows that see nothing, or whose every score is -infinity, are 0; rows
+    of no sequence keep what out held. workspace: mol_paged_attention_workspace_bytes of scratch, of
+    these sizes or larger ones. out may be `q`."""
     if _block._native is not None and out is None and workspace is None and stream is None:
         done = _block._native.paged_attention(
             _entry("mol_paged_attention"), _entry("mol_paged_attention_workspace_bytes"), q, k_cache,
