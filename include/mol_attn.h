@@ -65,7 +65,7 @@ typedef struct mol_paged_cache {
  * out[t, h] = x[t, h] with positions[t] (int32, any sign) turned into it.
  * out may be x itself (same strides); any other overlap is outside the contract.
  * Contract: head_dim a multiple of 8 up to MOL_ROPE_MAX_HEAD_DIM, strides
- * multiples of 8, num_tokens < 2^31.
+ * multiples of 8, num_tokens < 2^31, num_heads <= 65536.
  */
 int32_t mol_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride,
                  const int32_t* positions, const mol_rope_table* rope, int64_t num_tokens,
@@ -78,7 +78,7 @@ int32_t mol_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride,
  * cache (-1: a padding row) writes nothing there. With q, its num_q_heads heads
  * of head_dim are turned into q_out by the same launch, padding rows too; q_out
  * may be q itself (same strides). Tokens name different slots: of two that name
- * one, either's values, or some of each, remain.
+ * one, either's values, or some of each, remain. k, v and q lie outside the cache.
  *   rope        NULL: keys are copied (positions is not read then; q NULL)
  * Contract: as mol_rope for the heads, cache->head_dim their width.
  */
@@ -115,9 +115,10 @@ int32_t mol_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * out may be q itself (same strides).
  * Contract: head_dim 64, 128 or 256; num_q_heads a multiple of cache->num_heads,
  * at most MOL_ATTN_MAX_GROUP times it; scale > 0, it and its product with
- * log2(e) finite; window >= 0; num_tokens * num_q_heads < 2^31; num_tokens +
- * max_pages * page_size <= 2^31 - 1024; with g query heads to a key head,
- * num_tokens * g <= 2^31 - 1024 and
+ * log2(e) finite; window >= 0; num_q_heads <= 65536; num_seqs < 2^24;
+ * num_tokens * num_q_heads < 2^31;
+ * num_tokens + max_pages * page_size <= 2^31 - 1024; with g query heads to a key
+ * head, num_tokens * g <= 2^31 - 1024 and
  * (num_tokens * g / 16 + num_seqs) * (max_pages * page_size / 64 + 4) < 2^31
  * (16 K tokens of group 8 over tables of 8 M).
  */

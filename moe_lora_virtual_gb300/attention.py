@@ -4,9 +4,10 @@ Rotary positions, appending to a paged cache of keys and values, attention of th
 tokens over it. As in the package itself the functions keep the C names, marshal
 arguments and raise ``MolError`` on a status; operands are on the current device.
 Outputs and scratch that are not passed in are allocated on the stream that the call is
-enqueued on. A cache is a pair of bf16 tensors [pages, page_size, heads, head_dim] of one
-shape and the same strides, the heads' values next to each other; a buffer laid out
-[pages, heads, page_size, head_dim] is passed as its ``transpose(1, 2)``.
+enqueued on. Nothing records gradients: operands that require them give outputs that do
+not. A cache is a pair of bf16 tensors [pages, page_size, heads, head_dim] of one shape and
+the same strides, the heads' values next to each other; a buffer laid out [pages, heads,
+page_size, head_dim] is passed as its ``transpose(1, 2)``.
 """
 
 from __future__ import annotations

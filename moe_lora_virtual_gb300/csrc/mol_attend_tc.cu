@@ -31,7 +31,7 @@ constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kHeldRing = 8;                  // more tiles than the loader is ever ahead
-// Most tiles of blocks that go undivided: 200 tokens over 500, 16 heads of 128, 17.1 us against 21.2 in parts.
+// Most tiles of blocks that go undivided: 200 tokens over 500, 16 heads of 128 on 2, 14.6 us against 19.9 in parts.
 constexpr int kWhole = 4;
 constexpr int kExtra = 2;                     // units that a block takes beside its tiles
 constexpr float kLazy = 8.f;                  // log2 of how far weights may pass 1
@@ -239,8 +239,9 @@ constexpr uint32_t kValues = IDesc<kM, D>::kValue | (1u << 16);
 //   warps 10, 11    look through the values of tiles that some row does not see all of: values that are
 //                   not finite are zeroed where no row sees them; where another row does, the tile's
 //                   softmax warps sum its products without the tensor cores, for which 0 * NaN is NaN
-// Tiles are dealt as in attend_few, long blocks summed by stretches (LONG); parts of blocks join in launch_join. Pages outside the cache are zeros
-// (the copy's fill); what a row does not see is replaced among its scores.
+// Tiles are dealt as in attend_few, long blocks summed by stretches (LONG); parts of blocks join in
+// launch_join. Pages outside the cache are zeros (the copy's fill); what a row does not see is replaced among
+// its scores.
 // 509 tokens over 30001, 32 heads of 128 on 4: 183 us, 1360 TFLOP/s (0.71 of the measured rate), a prompt of
 // 8192 426 us, 1290. A pair of tiles takes 3200 cycles: a query tile's own products 1340, its softmax 1525,
 // hand-overs 380, against 2680 of both tiles' products.
@@ -954,8 +955,8 @@ cudaError_t attn::prepare_many() {
 
 // 64 values a head are bound by the issue of products, 24 small ones a pair of tiles with the waits before
 // them. Two issuing warps hide those, where both query tiles have rows and few tiles are cut by a mask
-// (us with one | two, 32 heads on 8: 512 tokens over 30000 170 | 146, a prompt of 8192 384 | 353, 16 times 64
-// tokens over 3000 55 | 52; but one query tile, 16 times 20 tokens over 3000, 39.6 | 40.6, and with a window of
+// (us with one | two, 32 heads on 8: 512 tokens over 30000 169 | 144, a prompt of 8192 384 | 351, 16 times 64
+// tokens over 3000 54.5 | 51.7; but one query tile, 16 times 20 tokens over 3000, 39.6 | 40.6, and with a window of
 // 1024 the prompt 140 | 143, a batch of prompts and single tokens 99 | 101, for which one warp then looks
 // through the values).
 cudaError_t attn::launch_many(const AttnArgs& a, cudaStream_t stream) {

@@ -26,10 +26,10 @@ constexpr size_t kSmem = kRing + kRows * kD * 2;  // and the queries
 constexpr int kExtra = 4;                     // units that a block takes beside its tiles
 constexpr int kWhole = 8;                     // most tiles of blocks that go undivided
 
-// Sums of 256 columns leave tensor memory no room for a second tile of queries, and with one tile the
-// softmax and the products would take turns; so this is mma.sync: 128 rows a thread block, 16 a warp,
-// which all read one ring of 32-token tiles (cp.async, three stages, a barrier a tile). A row's scores,
-// maximum, sum and 256 columns of sums stay with four lanes. Bound by shared memory: a warp reads its
+// The simple form, on mma.sync (on tcgen05 one tile's sums would take half of tensor memory and two tiles of
+// scores the other half, so that the softmax of one overlaps the products of the next; that form is not
+// built): 128 rows a thread block, 16 a warp, which all read one ring of 32-token tiles (cp.async, three
+// stages, a barrier a tile). A row's scores, maximum, sum and 256 columns of sums stay with four lanes. Bound by shared memory: a warp reads its
 // queries (8 KB, no registers are left for them) and the tile (32 KB) for 2 x 16 x 32 x 256 products, which
 // at 128 bytes a cycle allows 470 TFLOP/s; 16 query heads of 2 key heads reach 233 on 8 prompts of 8192
 // tokens and 195 on 8 of 2048 (attend_few: 74), the rest waits, as two warps a scheduler hide little.
